@@ -16,8 +16,9 @@
  *    without copy-engine transfers. No call allocates or frees memory. mx_create allocates the handle's device memory
  *    once: a status word, the per-tile counters of the persistent chain kernel
  *    (64 KiB), the activation scratch of wo_a_grouped's two-launch form
- *    (8.25 MiB) and the block sums of squares of mx_gemm_chain_norm's
- *    three-launch form (64 KiB); mx_gemm_chain_noalloc also uses a fixed
+ *    (8.25 MiB), the block sums of squares of mx_gemm_chain_norm's
+ *    three-launch form (64 KiB) and mx_route's row counts (1 MiB);
+ *    mx_gemm_chain_noalloc also uses a fixed
  *    array inside the library.
  *  - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *    NULL is the legacy default stream) and must be made with the handle's
@@ -320,6 +321,109 @@ size_t mx_warmup_bytes(const mx_weight* w, int nw, const int* rows, int nrows);
  * so what it readies are the plans, the tensor maps and the first launch. */
 int mx_warmup(mx_handle* h, const mx_weight* w, int nw, const int* rows, int nrows,
               void* scratch, size_t scratch_bytes, void* stream);
+
+/* ------------------------------------------------ MXFP4 and expert layers
+ * MXFP4 here means: E2M1 values, two to a byte (element 2i in the low four bits),
+ * with one UE8M0 scale per 32 consecutive elements along K: the scales, their
+ * 128x4 layout and mx_scale_bytes are those of MXFP8.
+ *
+ * The five entry points below are the parts of an expert layer whose weights are
+ * in MXFP4: route the tokens, quantize them, multiply each expert's rows, sum
+ * each token's rows (examples/expert_layer.py runs them together). */
+
+/* Element types of the inputs that may have several. */
+#define MX_TYPE_BF16 0
+#define MX_TYPE_F16 1
+#define MX_TYPE_F32 2
+
+/* Rows -> MXFP4. x [M, K] of x_type, row stride ldx elements (ldx >= K,
+ * ldx % 8 == 0), 16-byte aligned.
+ *   q       out [M, K/2] packed E2M1 codes, 16-byte aligned
+ *   scales  out, as for mx_quantize_rows: mx_scale_bytes(M, K) bytes in the 128x4
+ *           layout with zero padding (swizzled != 0), else plain [M, K/32]; 4-byte
+ *           aligned
+ *   y       out [M, K] bf16, the values that the codes stand for (exact), or null
+ * Per 32-block: e = floor(log2 amax) - 2 clamped below at -127; codes = E2M1
+ * round-to-nearest-even of x * 2^-e, saturating at +-6; scale byte e + 127. A zero
+ * block has scale byte 0; the sign of zeros is kept. A block with an Inf or NaN has
+ * scale byte 0xFF (NaN), zero codes and NaN values.
+ * Constraints: M >= 1, K % 32 == 0; M * K < 2^34, else MX_ERR_UNSUPPORTED. */
+int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, int x_type, void* q,
+                         void* scales, int swizzled, void* y, void* stream);
+
+/* out[M, N] bf16 = dequant(a) x dequant(w)^T with MXFP4 weights, float32 accumulation.
+ *   a, a_scales  activations [M, K]: MXFP8 (a_fp4 = 0: E4M3 codes, K bytes a row) or
+ *                MXFP4 (a_fp4 = 1: packed, K/2 bytes a row); scales in the 128x4
+ *                layout; both 16-byte aligned
+ *   w, w_scales  MXFP4 weights [N, K] packed, scales in the 128x4 layout; both
+ *                32-byte aligned
+ *   flags        MX_FLAG_PDL or 0, as for mx_gemm
+ * Constraints: 1 <= M <= 2^24, N % 128 == 0, K % 128 == 0, else MX_ERR_UNSUPPORTED. */
+int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_scales, int a_fp4,
+                const void* w, const void* w_scales, void* out, unsigned flags, void* stream);
+
+/* The products of E experts' rows: for expert e and row r, offsets[e] <= r <
+ * offsets[e + 1], out[r] = dequant(a[tokens[r]]) x dequant(w[e])^T.
+ *   R            rows of out
+ *   a, a_scales  activations [a_rows, K], MXFP8 or MXFP4 as in mx_gemm_fp4, but with
+ *                plain [a_rows, K/32] scales (rows are gathered one by one)
+ *   w, w_scales  [E, N, K] packed MXFP4, and each expert's scales in the 128x4 layout,
+ *                one expert after another
+ *   offsets      [E + 1] int32 on the device, non-decreasing; values outside [0, R]
+ *                are taken as the nearest of the two. Rows of out that no expert
+ *                has are not written
+ *   tokens       [R] int32 on the device: the row of a behind each row of out; null: row
+ *                r of a (a_rows >= R). A value outside [0, a_rows) reads as a zero row
+ *                and is reported by mx_device_status as MX_ERR_INVALID_ARG
+ *   gated        0: out is [R, N]. Otherwise weight rows 2i and 2i + 1 are gate i and
+ *                up i, and out is [R, N/2]: silu(gate) * up, from the float32 products
+ * Constraints: N % 128 == 0, K % 128 == 0, E <= 512, R and a_rows <= 2^24,
+ * E * N < 2^31, else MX_ERR_UNSUPPORTED. */
+int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a, int a_rows,
+                        const void* a_scales, int a_fp4, const void* w, const void* w_scales,
+                        const int* offsets, const int* tokens, int gated, void* out, void* stream);
+
+#define MX_SCORE_SOFTMAX 0
+#define MX_SCORE_SIGMOID 1
+
+/* Routes T tokens to top_k of E experts.
+ *   logits   [T, E] float32 or bf16 (logits_type), row stride ldl >= E elements
+ *   bias     [E] float32 added to the scores for the selection only, or null
+ * A token's scores are the softmax over all E logits or 1 / (1 + exp(-x)); its keys
+ * are score + bias (without a bias the logits order the experts). With n_groups > 1
+ * the experts form n_groups equal groups of neighbours, ranked by their largest key
+ * (with a bias: the sum of their two largest), and only the first topk_groups
+ * groups' experts can be chosen. The top_k largest keys are chosen, the largest first,
+ * ties to the lowest index; which they are is decided as in exact arithmetic on the
+ * given float32 / bf16 numbers (float64 where float32 cannot tell).
+ *   weights  out [T, top_k] float32: the chosen scores, divided by their sum if
+ *            renormalize (0 where the sum is 0), times scale
+ *   experts  out [T, top_k] int32
+ *   offsets  out [E + 1] int32: first row of each expert when the T * top_k (token,
+ *            choice) pairs are ordered by expert, then token and choice
+ *   tokens   out [T * top_k] int32: the token of each row in that order
+ *   slots    out [T, top_k] int32: the row of each pair
+ * -inf and NaN logits (masked experts) and experts of -inf or NaN bias come after all
+ * others; a masked logit's weight is 0. +inf counts as the largest float32.
+ * Scratch: a fixed part of the handle (calls on one handle whose work overlaps on the
+ * GPU race on it: give each stream its own handle).
+ * Constraints: E % n_groups == 0, top_k <= topk_groups * (E / n_groups); E <= 512,
+ * top_k <= 32, n_groups <= 32, T * top_k <= 2^24, else MX_ERR_UNSUPPORTED. */
+int mx_route(mx_handle* h, int T, int E, int top_k, const void* logits, long ldl, int logits_type,
+             const float* bias, int scoring, int n_groups, int topk_groups, int renormalize, float scale,
+             float* weights, int* experts, int* offsets, int* tokens, int* slots, void* stream);
+
+/* out[t] = sum over j of weights[t, j] * y[slots[t, j]] (+ residual[t]), float32 sums in
+ * the order of j, residual last, bf16 out.
+ *   y         [R, N] bf16, row stride ldy elements, 16-byte aligned
+ *   slots     [T, top_k] int32, weights [T, top_k] float32 (as mx_route writes them);
+ *             a slot outside [0, R) adds nothing and is reported by mx_device_status
+ *             as MX_ERR_INVALID_ARG
+ *   residual  [T, N] bf16 or null; out [T, N] bf16 (may be residual itself); 16-byte aligned
+ * Constraints: N % 8 == 0, ldy % 8 == 0; top_k <= 32, T <= 2^24, N <= 2^20, else
+ * MX_ERR_UNSUPPORTED. */
+int mx_combine(mx_handle* h, int T, int top_k, int N, const void* y, int R, long ldy, const int* slots,
+               const float* weights, const void* residual, void* out, void* stream);
 
 /* ------------------------------------------------------------ plan queries
  * Host-only (no device, no handle): the launch plans the entry points make,

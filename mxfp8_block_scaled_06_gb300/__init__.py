@@ -9,7 +9,9 @@ layout and residency on the handle's GPU (TypeError / ValueError, nothing
 launched).
 
 Names and argument order follow the C entry points: mx_create, mx_scale_bytes,
-mx_quantize_rows, mx_gemm, mx_gemm_chain, wo_a_grouped, mx_device_status.
+mx_quantize_rows, mx_gemm, mx_gemm_chain, wo_a_grouped, mx_device_status; for expert
+layers with MXFP4 weights mx_quantize_rows_fp4, mx_gemm_fp4, mx_route,
+mx_gemm_fp4_grouped, mx_combine.
 """
 from __future__ import annotations
 
@@ -26,7 +28,8 @@ EXPORTS = ["mx_create", "mx_destroy", "mx_scale_bytes", "mx_quantize_rows",
            "mx_rmsnorm_quantize_rows", "mx_gemm", "mx_gemm_bf16", "mx_gemm_chain",
            "mx_gemm_chain_norm", "mx_gemm_chain_noalloc", "wo_a_grouped", "wo_a_grouped_unfused",
            "mx_warmup_bytes", "mx_warmup", "mx_plan_gemm", "mx_plan_chain_push", "mx_device_status",
-           "mx_wait_selftest", "mx_status_string"]
+           "mx_wait_selftest", "mx_status_string", "mx_quantize_rows_fp4", "mx_gemm_fp4", "mx_gemm_fp4_grouped",
+           "mx_route", "mx_combine"]
 
 _vp, _i, _l, _u = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_uint
 
@@ -38,6 +41,9 @@ class MxWeight(ctypes.Structure):
 # reduction forms and push receive areas of the plan queries (include/mx.h)
 MX_REDUCE_ITEMS, MX_REDUCE_ROWS, MX_REDUCE_PUSH, MX_REDUCE_PUSH_COMPACT = range(4)
 MX_PUSH_NONE, MX_PUSH_COMPACT, MX_PUSH_FULL = range(3)
+# element types and router scorings (include/mx.h)
+MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32 = range(3)
+MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = range(2)
 
 
 class MxPlanInfo(ctypes.Structure):
@@ -87,6 +93,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                  _vp, _vp, _vp, _vp, _vp, _i, _vp]
     lib.wo_a_grouped_unfused.argtypes = [_vp, _i, _vp, _l, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i,
                                          _i, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.mx_quantize_rows_fp4.argtypes = [_vp, _i, _i, _vp, _l, _i, _vp, _vp, _i, _vp, _vp]
+    lib.mx_gemm_fp4.argtypes = [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _u, _vp]
+    lib.mx_gemm_fp4_grouped.argtypes = [_vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp]
+    lib.mx_route.argtypes = [_vp, _i, _i, _i, _vp, _l, _i, _vp, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp,
+                             _vp, _vp, _vp]
+    lib.mx_combine.argtypes = [_vp, _i, _i, _i, _vp, _i, _l, _vp, _vp, _vp, _vp, _vp]
     lib.mx_device_status.argtypes = [_vp, ctypes.POINTER(_i)]
     lib.mx_wait_selftest.argtypes = [_vp, _vp]
     lib.mx_status_string.argtypes = [_i]
@@ -500,6 +512,174 @@ def wo_a_grouped_unfused(h: Handle, x, positions, cos_sin, w, w_scales, n_groups
                                                _ptr(zt), _ptr(q), _ptr(q_scales), _stream(stream)),
            "wo_a_grouped_unfused")
     return dict(q=q, q_scales=q_scales, z=zt, xq=xq, xq_scales=xq_scales)
+
+
+def _type_code(name: str, t, allowed):
+    """MX_TYPE_* of a tensor, which has to be one of allowed."""
+    import torch
+    codes = {torch.bfloat16: MX_TYPE_BF16, torch.float16: MX_TYPE_F16, torch.float32: MX_TYPE_F32}
+    code = codes.get(t.dtype)
+    if code is None or code not in allowed:
+        raise TypeError(f"{name}: dtype {t.dtype} not supported")
+    return code
+
+
+def mx_quantize_rows_fp4(h: Handle, x, q=None, scales=None, swizzled: bool = True, y: bool = False,
+                         stream=None):
+    """bf16, fp16 or fp32 [M, K] (row stride x.stride(0)) -> (packed E2M1 codes uint8
+    [M, K/2], scale bytes, y): y = the codes' values in bf16 [M, K] when asked, else None."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x: a 2-D [M, K] tensor is required")
+    m, k = x.shape
+    code = _type_code("x", x, (MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32))
+    _matrix("x", x, (x.dtype,), m, k, row_stride=True)
+    if k % 32:
+        raise ValueError(f"x: {k} columns, a multiple of 32 is required")
+    sbytes = _sbytes(m, k) if swizzled else m * (k // 32)
+    if q is not None:
+        _matrix("q", q, (torch.uint8,), m, k // 2)
+    if scales is not None:
+        _flat("scales", scales, _scale_types(), sbytes)
+    _resident(h, x=x, q=q, scales=scales)
+    q = _empty_u8((m, k // 2), x.device) if q is None else q
+    scales = _empty_u8((sbytes,) if swizzled else (m, k // 32), x.device) if scales is None else scales
+    yt = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
+    _check(load_library().mx_quantize_rows_fp4(h.ptr, m, k, _ptr(x), x.stride(0), code, _ptr(q), _ptr(scales),
+                                               int(swizzled), _ptr(yt), _stream(stream)),
+           "mx_quantize_rows_fp4")
+    return q, scales, yt
+
+
+def _fp4_activations(a, m: int, k: int):
+    """1 if a holds m rows of packed MXFP4, 0 if of MXFP8: told by its columns."""
+    import torch
+    if a is None or a.dim() != 2 or a.shape[1] not in (k, k // 2):
+        raise ValueError(f"a: expected [>= {m}, {k}] MXFP8 codes or [>= {m}, {k // 2}] packed MXFP4 codes")
+    fp4 = a.shape[1] == k // 2
+    _matrix("a", a, (torch.uint8,) if fp4 else _codes_types(), m, a.shape[1])
+    return int(fp4)
+
+
+def mx_gemm_fp4(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = None, pdl: bool = False,
+                stream=None):
+    """out[M, N] bf16 = dequant(a) x dequant(w)^T with MXFP4 weights w: packed codes uint8
+    [N, K/2] and swizzled scales. a: MXFP8 codes [M, K] or packed MXFP4 codes [M, K/2],
+    with swizzled scales (M = a's rows unless m is given)."""
+    import torch
+    if w is None or w.dim() != 2:
+        raise ValueError("w: a 2-D [N, K/2] tensor is required")
+    n, k = w.shape[0], 2 * w.shape[1]
+    _matrix("w", w, (torch.uint8,), n, k // 2)
+    _flat("w_scales", w_scales, _scale_types(), _sbytes(n, k))
+    m = a.shape[0] if m is None else m
+    fp4 = _fp4_activations(a, m, k)
+    _flat("a_scales", a_scales, _scale_types(), _sbytes(m, k))
+    if out is not None:
+        _matrix("out", out, (torch.bfloat16,), m, n)
+    _resident(h, a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out)
+    out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device) if out is None else out
+    _check(load_library().mx_gemm_fp4(h.ptr, m, n, k, _ptr(a), _ptr(a_scales), fp4, _ptr(w), _ptr(w_scales),
+                                      _ptr(out), MX_FLAG_PDL if pdl else 0, _stream(stream)), "mx_gemm_fp4")
+    return out
+
+
+def mx_gemm_fp4_grouped(h: Handle, a, a_scales, w, w_scales, offsets, tokens=None, gated: bool = False,
+                        out=None, stream=None):
+    """The experts' products: out[r] = dequant(a[tokens[r]]) x dequant(w[e])^T for rows
+    offsets[e] <= r < offsets[e + 1] (tokens None: row r of a). a: MXFP8 codes [rows, K] or
+    packed MXFP4 codes [rows, K/2] with plain [rows, K/32] scales; w: packed codes uint8
+    [E, N, K/2], w_scales each expert's swizzled scales; offsets int32 [E + 1], tokens
+    int32 [R]. gated: weight rows 2i, 2i + 1 are gate i, up i and out is [R, N/2],
+    silu(gate) * up. Rows that no expert has are left as they are."""
+    import torch
+    if w is None or w.dim() != 3:
+        raise ValueError("w: a 3-D [E, N, K/2] tensor is required")
+    e, n, k = w.shape[0], w.shape[1], 2 * w.shape[2]
+    _flat("w", w, (torch.uint8,), e * n * k // 2)
+    if n % 128:
+        raise ValueError(f"w: {n} rows per expert, a multiple of 128 is required")
+    _flat("w_scales", w_scales, _scale_types(), e * _sbytes(n, k))
+    fp4 = _fp4_activations(a, 1, k)
+    rows = a.shape[0]
+    _flat("a_scales", a_scales, _scale_types(), rows * (k // 32))
+    _flat("offsets", offsets, (torch.int32,), e + 1)
+    if tokens is not None:
+        _flat("tokens", tokens, (torch.int32,), 1)
+    r = rows if tokens is None else tokens.numel()
+    cols = n // 2 if gated else n
+    if out is not None:
+        _matrix("out", out, (torch.bfloat16,), r, cols)
+    _resident(h, a=a, a_scales=a_scales, w=w, w_scales=w_scales, offsets=offsets, tokens=tokens, out=out)
+    out = torch.empty((r, cols), dtype=torch.bfloat16, device=w.device) if out is None else out
+    _check(load_library().mx_gemm_fp4_grouped(h.ptr, e, r, n, k, _ptr(a), rows, _ptr(a_scales), fp4, _ptr(w),
+                                              _ptr(w_scales), _ptr(offsets), _ptr(tokens), int(gated), _ptr(out),
+                                              _stream(stream)), "mx_gemm_fp4_grouped")
+    return out
+
+
+def mx_route(h: Handle, logits, top_k: int, bias=None, scoring: str = "softmax", n_groups: int = 1,
+             topk_groups: int = 1, renormalize: bool = True, scale: float = 1.0, weights=None, experts=None,
+             offsets=None, tokens=None, slots=None, stream=None) -> dict:
+    """Routes tokens to experts: logits fp32 or bf16 [T, E] (row stride logits.stride(0)),
+    bias fp32 [E] for the selection only, scoring "softmax" or "sigmoid". Returns weights
+    fp32 and experts int32 [T, top_k], and the rows in expert order: offsets int32 [E + 1],
+    tokens int32 [T * top_k] (the token of each row), slots int32 [T, top_k] (the row of
+    each choice)."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits: a 2-D [T, E] tensor is required")
+    t, e = logits.shape
+    code = _type_code("logits", logits, (MX_TYPE_BF16, MX_TYPE_F32))
+    _matrix("logits", logits, (logits.dtype,), t, e, row_stride=True)
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError(f"scoring: {scoring!r}, expected 'softmax' or 'sigmoid'")
+    top_k = int(top_k)
+    if top_k < 1:
+        raise ValueError(f"top_k: {top_k}, at least 1 is required")
+    if bias is not None:
+        _flat("bias", bias, (torch.float32,), e)
+    given = dict(weights=weights, experts=experts, offsets=offsets, tokens=tokens, slots=slots)
+    for name, x in given.items():
+        if x is not None:
+            _flat(name, x, (torch.float32 if name == "weights" else torch.int32,),
+                  e + 1 if name == "offsets" else t * top_k)
+    _resident(h, logits=logits, bias=bias, **given)
+    dev = logits.device
+    out = dict(
+        weights=torch.empty((t, top_k), dtype=torch.float32, device=dev) if weights is None else weights,
+        experts=torch.empty((t, top_k), dtype=torch.int32, device=dev) if experts is None else experts,
+        offsets=torch.empty((e + 1,), dtype=torch.int32, device=dev) if offsets is None else offsets,
+        tokens=torch.empty((t * top_k,), dtype=torch.int32, device=dev) if tokens is None else tokens,
+        slots=torch.empty((t, top_k), dtype=torch.int32, device=dev) if slots is None else slots)
+    _check(load_library().mx_route(h.ptr, t, e, top_k, _ptr(logits), logits.stride(0), code, _ptr(bias),
+                                   MX_SCORE_SIGMOID if scoring == "sigmoid" else MX_SCORE_SOFTMAX, n_groups,
+                                   topk_groups, int(renormalize), float(scale), _ptr(out["weights"]),
+                                   _ptr(out["experts"]), _ptr(out["offsets"]), _ptr(out["tokens"]),
+                                   _ptr(out["slots"]), _stream(stream)), "mx_route")
+    return out
+
+
+def mx_combine(h: Handle, y, slots, weights, residual=None, out=None, stream=None):
+    """out[t] = sum over j of weights[t, j] * y[slots[t, j]] (+ residual[t]): y bf16 [R, N]
+    (row stride y.stride(0)), slots int32 and weights fp32 [T, top_k], bf16 [T, N] out."""
+    import torch
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("y [R, N] and slots [T, top_k]: 2-D tensors are required")
+    r, n = y.shape
+    t, k = slots.shape
+    _matrix("y", y, (torch.bfloat16,), r, n, row_stride=True)
+    _matrix("slots", slots, (torch.int32,), t, k)
+    _matrix("weights", weights, (torch.float32,), t, k)
+    if residual is not None:
+        _matrix("residual", residual, (torch.bfloat16,), t, n)
+    if out is not None:
+        _matrix("out", out, (torch.bfloat16,), t, n)
+    _resident(h, y=y, slots=slots, weights=weights, residual=residual, out=out)
+    out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device) if out is None else out
+    _check(load_library().mx_combine(h.ptr, t, k, n, _ptr(y), r, y.stride(0), _ptr(slots), _ptr(weights),
+                                     _ptr(residual), _ptr(out), _stream(stream)), "mx_combine")
+    return out
 
 
 def mx_warmup(h: Handle, weights, rows, stream=None) -> list:

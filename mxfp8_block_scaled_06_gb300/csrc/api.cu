@@ -21,6 +21,7 @@ struct TmapEntry {
   int rows;
   long k;
   int box_rows;
+  bool fp4;
   CUtensorMap map;
 };
 constexpr int kTmapCache = 32;
@@ -50,6 +51,7 @@ struct mx_handle {
   int chain_clusters;  // clusters of 8 CTAs it may use (0: the three-launch path only)
   uint8_t* d_woa;      // wo_a_grouped's two-launch activation (kWoaScratchBytes)
   float* d_ssq;        // mx_gemm_chain_norm's block sums of squares (kSsqBytes)
+  int* d_route;        // mx_route's rows per (expert, chunk of tokens) (kRouteWorkspace)
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   TmapEntry tmaps[kTmapCache];
   int tmap_count;
@@ -80,6 +82,9 @@ constexpr int kWoaFusedMaxTokens = 8;
 constexpr int kNormFusedMaxRows = 16;
 // the block sums of squares G1 hands to G2 there: [M, g1_cols / 32] floats
 constexpr size_t kSsqBytes = size_t{64} << 10;
+// rows of the MXFP4 products, and (token, choice) rows of the router: tile and row
+// numbers are 32-bit
+constexpr int kMaxFp4Rows = 1 << 24;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -178,27 +183,29 @@ bool chain_norm_fused(int M, int g1_cols, size_t fused_g2_smem) {
 }
 
 // 2-D uint8 tensor map over a row-major [rows, k] matrix, box {128 bytes, box_rows}
-// with the 128-byte swizzle; out-of-range rows of a box read as zero.
-int make_tmap(mx_handle* h, CUtensorMap* tm, const void* ptr, int rows, long k, int box_rows) {
+// with the 128-byte swizzle; out-of-range rows of a box read as zero. fp4: k is the
+// elements of a row of packed E2M1 (k / 2 bytes), and a box of 128 elements lands
+// unpacked, 16 elements in the low 8 of 16 bytes.
+int make_tmap(mx_handle* h, CUtensorMap* tm, const void* ptr, int rows, long k, int box_rows, bool fp4 = false) {
   for (int i = 0; i < h->tmap_count; ++i) {
     const TmapEntry& e = h->tmaps[i];
-    if (e.ptr == ptr && e.rows == rows && e.k == k && e.box_rows == box_rows) {
+    if (e.ptr == ptr && e.rows == rows && e.k == k && e.box_rows == box_rows && e.fp4 == fp4) {
       *tm = e.map;
       return MX_OK;
     }
   }
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(fp4 ? k / 2 : k)};
   cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = h->encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims,
+  CUresult r = h->encode(tm, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return MX_ERR_CUDA;
   const int slot = h->tmap_count < kTmapCache ? h->tmap_count++ : h->tmap_next;
   if (h->tmap_count == kTmapCache) h->tmap_next = (slot + 1) % kTmapCache;
-  h->tmaps[slot] = TmapEntry{ptr, rows, k, box_rows, *tm};
+  h->tmaps[slot] = TmapEntry{ptr, rows, k, box_rows, fp4, *tm};
   return MX_OK;
 }
 
@@ -387,13 +394,14 @@ int mx_create(mx_handle** out, int device) {
     } else {
       h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
       if (mx::set_gemm_attributes() != cudaSuccess || mx::set_wo_a_attributes() != cudaSuccess ||
-          mx::set_chain_attributes() != cudaSuccess ||
+          mx::set_chain_attributes() != cudaSuccess || mx::set_gemm_fp4_attributes() != cudaSuccess ||
           cudaMalloc(&h->d_status, 16) != cudaSuccess ||
           cudaMemset(h->d_status, 0, 16) != cudaSuccess ||
           cudaMalloc(&h->d_chain, mx::kChainCounters * sizeof(unsigned)) != cudaSuccess ||
           cudaMemset(h->d_chain, 0, mx::kChainCounters * sizeof(unsigned)) != cudaSuccess ||
           cudaMalloc(&h->d_woa, kWoaScratchBytes) != cudaSuccess ||
           cudaMalloc(&h->d_ssq, kSsqBytes) != cudaSuccess ||
+          cudaMalloc(&h->d_route, mx::kRouteWorkspace) != cudaSuccess ||
 #ifdef MX_TIMELINE
           cudaMalloc(&h->d_tl, kTimelineBytes) != cudaSuccess ||
           cudaMemset(h->d_tl, 0, kTimelineBytes) != cudaSuccess ||
@@ -410,6 +418,7 @@ int mx_create(mx_handle** out, int device) {
     if (h->d_chain) cudaFree(h->d_chain);
     if (h->d_woa) cudaFree(h->d_woa);
     if (h->d_ssq) cudaFree(h->d_ssq);
+    if (h->d_route) cudaFree(h->d_route);
     delete h;
     h = nullptr;
   }
@@ -427,6 +436,7 @@ int mx_destroy(mx_handle* h) {
   cudaFree(h->d_chain);
   cudaFree(h->d_woa);
   cudaFree(h->d_ssq);
+  cudaFree(h->d_route);
 #ifdef MX_TIMELINE
   cudaFree(h->d_tl);
 #endif
@@ -798,6 +808,166 @@ int wo_a_grouped_unfused(mx_handle* h, int T, const void* x, long ldx, const int
     return MX_ERR_INVALID_ARG;
   return woa_two_launch(h, T, x, ldx, positions, cos_sin, max_pos, w, w_scales, G, H, d_nope, d_rope,
                         R, xq, xq_scales, z, q, q_scales, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------ MXFP4 and experts
+static_assert(MX_TYPE_BF16 == mx::kTypeBf16 && MX_TYPE_F16 == mx::kTypeF16 && MX_TYPE_F32 == mx::kTypeF32,
+              "mx.h element types");
+static_assert(MX_SCORE_SOFTMAX == mx::kScoreSoftmax && MX_SCORE_SIGMOID == mx::kScoreSigmoid, "mx.h scorings");
+
+int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, int x_type, void* q, void* scales,
+                         int swizzled, void* y, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (M < 1 || K < 32 || K % 32 != 0 || ldx < K || ldx % 8 != 0) return MX_ERR_INVALID_ARG;
+  if (x_type != MX_TYPE_BF16 && x_type != MX_TYPE_F16 && x_type != MX_TYPE_F32) return MX_ERR_INVALID_ARG;
+  if (x == nullptr || q == nullptr || scales == nullptr) return MX_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 4) || !aligned(y, 16)) return MX_ERR_INVALID_ARG;
+  if (static_cast<long>(M) * K >= (1L << 34)) return MX_ERR_UNSUPPORTED;
+  return cuda_status(mx::launch_quantize_rows_fp4(x, ldx, x_type, M, K, q, scales, swizzled, y,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// The tensor maps and the launch shared by the two entry points below; the
+// arguments are validated by the callers.
+int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp4, const void* w, bool gather,
+                    cudaStream_t stream) {
+  const mx::GemmFp4Plan plan = mx::plan_gemm_fp4(args.E, args.R, args.N, args.K, a_fp4 != 0, h->sm_count);
+  if (plan.stages < 2) return MX_ERR_UNSUPPORTED;
+  args.nt = plan.nt;
+  args.stages = plan.stages;
+  args.tmem_cols = plan.tmem_cols;
+  args.status = h->d_status;
+  CUtensorMap tm_w, tm_a;
+  const int w_rows = args.E * args.N;
+  int rc = a_fp4 ? make_tmap(h, &tm_w, w, w_rows, args.K / 2, 128) : make_tmap(h, &tm_w, w, w_rows, args.K, 128, true);
+  if (rc == MX_OK) rc = make_tmap(h, &tm_a, a, args.a_rows, a_fp4 ? args.K / 2 : args.K, gather ? 1 : plan.nt);
+  if (rc != MX_OK) return rc;
+  return cuda_status(mx::launch_gemm_fp4(tm_w, tm_a, args, plan, a_fp4 != 0, gather, stream));
+}
+
+}  // namespace
+
+int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_scales, int a_fp4, const void* w,
+                const void* w_scales, void* out, unsigned flags, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (M < 1 || N < 1 || K < 1 || K % 32 != 0 || (flags & ~MX_FLAG_PDL)) return MX_ERR_INVALID_ARG;
+  if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr)
+    return MX_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(w, 32) || !aligned(w_scales, 32) || !aligned(out, 16))
+    return MX_ERR_INVALID_ARG;
+  if (N % 128 != 0 || K % 128 != 0 || M > kMaxFp4Rows) return MX_ERR_UNSUPPORTED;
+  mx::GemmFp4Args args = {};
+  args.E = 1;
+  args.N = N;
+  args.K = K;
+  args.R = args.a_rows = M;
+  args.a_scales = static_cast<const uint8_t*>(a_scales);
+  args.a_swizzled = 1;
+  args.w_scales = static_cast<const uint8_t*>(w_scales);
+  args.out = static_cast<__nv_bfloat16*>(out);
+  return gemm_fp4_launch(h, args, a, a_fp4, w, false, static_cast<cudaStream_t>(stream));
+}
+
+int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a, int a_rows, const void* a_scales,
+                        int a_fp4, const void* w, const void* w_scales, const int* offsets, const int* tokens,
+                        int gated, void* out, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (E < 1 || R < 1 || N < 1 || K < 1 || a_rows < 1 || K % 32 != 0) return MX_ERR_INVALID_ARG;
+  if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr || offsets == nullptr ||
+      out == nullptr)
+    return MX_ERR_INVALID_ARG;
+  if (tokens == nullptr && a_rows < R) return MX_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(w, 32) || !aligned(w_scales, 32) || !aligned(out, 16) ||
+      !aligned(offsets, 4) || !aligned(tokens, 4))
+    return MX_ERR_INVALID_ARG;
+  if (N % 128 != 0 || K % 128 != 0 || E > mx::kRouteMaxExperts || R > kMaxFp4Rows || a_rows > kMaxFp4Rows ||
+      static_cast<long>(E) * N >= (1L << 31))
+    return MX_ERR_UNSUPPORTED;
+  mx::GemmFp4Args args = {};
+  args.E = E;
+  args.N = N;
+  args.K = K;
+  args.R = R;
+  args.a_rows = a_rows;
+  args.a_scales = static_cast<const uint8_t*>(a_scales);
+  args.w_scales = static_cast<const uint8_t*>(w_scales);
+  args.offsets = offsets;
+  args.tokens = tokens;
+  args.gated = gated != 0;
+  args.out = static_cast<__nv_bfloat16*>(out);
+  return gemm_fp4_launch(h, args, a, a_fp4, w, true, static_cast<cudaStream_t>(stream));
+}
+
+int mx_route(mx_handle* h, int T, int E, int top_k, const void* logits, long ldl, int logits_type, const float* bias,
+             int scoring, int n_groups, int topk_groups, int renormalize, float scale, float* weights, int* experts,
+             int* offsets, int* tokens, int* slots, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (T < 1 || E < 1 || top_k < 1 || n_groups < 1 || topk_groups < 1 || topk_groups > n_groups || ldl < E ||
+      E % n_groups != 0 || top_k > topk_groups * (E / n_groups))
+    return MX_ERR_INVALID_ARG;
+  if (scoring != MX_SCORE_SOFTMAX && scoring != MX_SCORE_SIGMOID) return MX_ERR_INVALID_ARG;
+  if (logits_type != MX_TYPE_F32 && logits_type != MX_TYPE_BF16) return MX_ERR_INVALID_ARG;
+  if (logits == nullptr || weights == nullptr || experts == nullptr || offsets == nullptr || tokens == nullptr ||
+      slots == nullptr)
+    return MX_ERR_INVALID_ARG;
+  if (!aligned(logits, logits_type == MX_TYPE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(weights, 4) ||
+      !aligned(experts, 4) || !aligned(offsets, 4) || !aligned(tokens, 4) || !aligned(slots, 4))
+    return MX_ERR_INVALID_ARG;
+  if (E > mx::kRouteMaxExperts || top_k > mx::kRouteMaxTopK || n_groups > 32 ||
+      static_cast<long>(T) * top_k > kMaxFp4Rows)
+    return MX_ERR_UNSUPPORTED;
+  mx::RouteArgs args = {};
+  args.T = T;
+  args.E = E;
+  args.top_k = top_k;
+  args.logits = logits;
+  args.ldl = ldl;
+  args.bf16 = logits_type == MX_TYPE_BF16;
+  args.bias = bias;
+  args.scoring = scoring;
+  args.n_groups = n_groups;
+  args.topk_groups = topk_groups;
+  args.renormalize = renormalize;
+  args.scale = scale;
+  args.weights = weights;
+  args.experts = experts;
+  args.offsets = offsets;
+  args.tokens = tokens;
+  args.slots = slots;
+  args.counts = h->d_route;
+  args.totals = h->d_route + static_cast<size_t>(mx::kRouteMaxExperts) * mx::kRouteChunks;
+  return cuda_status(mx::launch_route(args, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_combine(mx_handle* h, int T, int top_k, int N, const void* y, int R, long ldy, const int* slots,
+               const float* weights, const void* residual, void* out, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (T < 1 || top_k < 1 || N < 1 || R < 1 || ldy < N) return MX_ERR_INVALID_ARG;
+  if (y == nullptr || slots == nullptr || weights == nullptr || out == nullptr) return MX_ERR_INVALID_ARG;
+  if (N % 8 != 0 || ldy % 8 != 0) return MX_ERR_INVALID_ARG;
+  if (!aligned(y, 16) || !aligned(out, 16) || !aligned(residual, 16) || !aligned(slots, 4) || !aligned(weights, 4))
+    return MX_ERR_INVALID_ARG;
+  if (top_k > mx::kRouteMaxTopK || T > kMaxFp4Rows || N > (1 << 20)) return MX_ERR_UNSUPPORTED;
+  mx::CombineArgs args = {};
+  args.T = T;
+  args.top_k = top_k;
+  args.N = N;
+  args.R = R;
+  args.y = static_cast<const __nv_bfloat16*>(y);
+  args.ldy = ldy;
+  args.slots = slots;
+  args.weights = weights;
+  args.residual = static_cast<const __nv_bfloat16*>(residual);
+  args.out = static_cast<__nv_bfloat16*>(out);
+  args.status = h->d_status;
+  return cuda_status(mx::launch_combine(args, static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------ chain without allocation

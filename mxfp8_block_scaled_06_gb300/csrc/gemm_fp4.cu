@@ -1,0 +1,464 @@
+// gemm_fp4.cu - products with MXFP4 weights on tcgen05 (sm_103a): the experts'
+// grouped product, and the plain product as its one-expert case.
+//
+// out[r, n] = sum over k of dequant(a)[row(r), k] dequant(w[e(r)])[n, k], fp32
+// accumulate, bf16 out; optionally silu(column 2i) * column 2i + 1.
+//
+// Swap-AB as in gemm.cu: 128 weight rows are the MMA's M, a tile of up to nt
+// tokens its N, so a few rows per expert cost a narrow MMA and the weights are read
+// once. Persistent CTAs walk the tiles (expert, 128 weight rows, token tile) and the
+// ring of operand stages runs on across tiles. Warps:
+//   0     weight boxes (TMA) and their scale tiles (bulk copies)
+//   1     tcgen05.cp of the scales and tcgen05.mma, by an elected lane
+//   2     activation rows: a TMA box, or gathered by row index (tile::gather4)
+//   3     activation scales: gathered with plain loads into 128x4 scale tiles
+//   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half
+// A stage holds 128 bytes of K per operand row in the 128-byte swizzle: 128
+// elements against MXFP8 activations (.kind::mxf8f6f4 wants E2M1 unpacked to a
+// byte each, which the tensor map does on the way: HBM sees 4 bits), 256 elements
+// with both operands packed (.kind::mxf4). Either way four MMAs of 32 bytes.
+// Every mbarrier wait is bounded; on expiry the kernel records MX_ERR_TIMEOUT,
+// stops, waits for its copies and frees its tensor memory.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
+// bytes that an unpacking copy of it completes on its barrier: the packed ones
+constexpr uint32_t kWBytesUnpacked = 128 * 64;
+constexpr uint32_t kSfTile = 512;  // one 128x4 scale tile: 128 rows x 128 elements of K
+constexpr int kMaxNt = 224;        // two accumulators of 224 columns leave 64 columns of TMEM for scales
+constexpr int kMaxE = kRouteMaxExperts;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+// Shared memory of one CTA, from its 1024-aligned base.
+struct Layout {
+  uint32_t a_bytes, stage_bytes, sfw_stage, sfa_stage, sfw, sfa, bars, table, end;
+  __host__ __device__ Layout(int nt, int stages, int tiles_per_chunk, int E) {
+    a_bytes = static_cast<uint32_t>(nt) * 128u;
+    stage_bytes = kWBytes + a_bytes;
+    sfw_stage = tiles_per_chunk * kSfTile;
+    sfa_stage = tiles_per_chunk * ((nt + 127) / 128) * kSfTile;
+    sfw = stages * stage_bytes;
+    sfa = sfw + stages * sfw_stage;
+    bars = sfa + stages * sfa_stage;
+    table = bars + 8u * (2 * stages + 4) + 16u;
+    end = table + 8u * (E + 1);
+  }
+  __host__ __device__ size_t total() const { return 1024 + end; }
+};
+
+struct Tile {
+  int w_row;  // first weight row, of all experts
+  int n0;     // first output column
+  int row0, rows;
+  int n;  // MMA N: rows rounded up to 16 (an expert's token tiles are balanced)
+};
+
+// The CTA's table of the experts: tile numbers before each one, first rows.
+struct Table {
+  const int* cum;
+  const int* off;
+  int E, nt;
+  __device__ Tile at(int idx, int N) const {
+    int e = 0;
+    for (int step = kMaxE; step > 0; step >>= 1)
+      if (e + step < E && cum[e + step] <= idx) e += step;
+    const int count = off[e + 1] - off[e];
+    const int tt = (count + nt - 1) / nt;
+    const int local = idx - cum[e];
+    const int ni = local / tt, ti = local - ni * tt;
+    const int per = ((count + tt - 1) / tt + 15) & ~15;
+    Tile t;
+    t.w_row = e * N + ni * 128;
+    t.n0 = ni * 128;
+    t.row0 = off[e] + ti * per;
+    t.rows = min(per, count - ti * per);
+    t.n = (t.rows + 15) & ~15;
+    return t;
+  }
+};
+
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+
+template <bool kA4, bool kGather>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                    const __grid_constant__ GemmFp4Args p) {
+  constexpr int kTiles = kA4 ? 2 : 1;  // scale tiles (128 elements of K) per stage
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
+  const Layout L(p.nt, stages, kTiles, p.E);
+  const int units = p.K >> 7;                        // scale tiles along K
+  const int chunks = (units + kTiles - 1) / kTiles;  // stages along K
+  const uint32_t bars = base + L.bars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (stages + s); };
+  const uint32_t acc_full = bars + 16u * stages, acc_empty = acc_full + 16u;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L.bars + 8 * (2 * stages + 4));
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* const cum = reinterpret_cast<int*>(base_ptr + L.table);
+  int* const off = cum + p.E + 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full(s), 3);  // weights, activations, activation scales
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, 4);  // the epilogue's warps
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_a);
+  }
+  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+  if (warp == 1) {
+    // the experts' rows, clamped to the output, and the tiles before each expert
+    const int ntiles = p.N >> 7;
+    int run = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, hi = p.R;
+      if (p.offsets != nullptr && e < p.E) {
+        lo = min(max(p.offsets[e], 0), p.R);
+        hi = min(max(p.offsets[e + 1], lo), p.R);
+      }
+      const int own = e < p.E ? (hi - lo + p.nt - 1) / p.nt * ntiles : 0;
+      int s = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFull, s, o);
+        if (lane >= o) s += up;
+      }
+      if (e < p.E) {
+        cum[e] = run + s - own;
+        off[e] = lo;
+        if (e == p.E - 1) off[p.E] = hi;
+      }
+      run += __shfl_sync(kFull, s, 31);
+    }
+    if (lane == 0) cum[p.E] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Table table{cum, off, p.E, p.nt};
+  const int total = cum[p.E];
+  // one wait for the whole warp; false (for all lanes) once it has expired anywhere
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) {
+    const bool ok = mbar_wait_or(bar, parity, abort_flag);
+    if (__all_sync(kFull, ok)) return true;
+    if (lane == 0) {
+      atomicOr(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    return false;
+  };
+
+  if (warp == 0) {
+    // ---------------- weights and their scales
+    const uint64_t pol = policy_evict_normal();
+    int s = 0, issuer = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
+      const Tile t = table.at(idx, p.N);
+      const uint8_t* const sf = p.w_scales + static_cast<size_t>(t.w_row >> 7) * units * kSfTile;
+      for (int i = 0; i < chunks; ++i) {
+        if (!(ok = warp_wait(empty(s), ph))) break;
+        if (lane == issuer) {
+          const uint32_t sf_bytes = min(kTiles, units - i * kTiles) * kSfTile;
+          mbar_expect_tx(full(s), (kA4 ? kWBytes : kWBytesUnpacked) + sf_bytes);
+          tma_load_2d(base + s * L.stage_bytes, &tm_w, full(s), i * 128, t.w_row, pol);
+          bulk_load(base + L.sfw + s * L.sfw_stage, sf + static_cast<size_t>(i) * kTiles * kSfTile, sf_bytes, full(s),
+                    pol);
+        }
+        __syncwarp();
+        issuer = (issuer + 1) & 31;
+        if (++s == stages) s = 0, ph ^= 1u;
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------- activation rows
+    const uint64_t pol = policy_evict_last();
+    int s = 0, issuer = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
+      const Tile t = table.at(idx, p.N);
+      int4 r[2];
+      if constexpr (kGather) {
+        // lane l gathers rows 4l .. 4l + 3 and 128 + 4l ..; rows past the tile (and
+        // tokens outside a) are out of the tensor and read as zero
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          int v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = b * 128 + lane * 4 + q;
+            v[q] = i < t.rows ? (p.tokens != nullptr ? p.tokens[t.row0 + i] : t.row0 + i) : p.a_rows;
+            if (v[q] < 0 || v[q] > p.a_rows) v[q] = p.a_rows;
+          }
+          r[b] = make_int4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      for (int i = 0; i < chunks; ++i) {
+        if (!(ok = warp_wait(empty(s), ph))) break;
+        const uint32_t dst = base + s * L.stage_bytes + kWBytes;
+        if constexpr (kGather) {
+          if (lane == 0) mbar_expect_tx(full(s), static_cast<uint32_t>(t.n) * 128u);
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (b * 128 + lane * 4 < t.n)
+              tma_gather4(dst + (b * 128 + lane * 4) * 128, &tm_a, full(s), i * 128, r[b], pol);
+        } else if (lane == issuer) {
+          mbar_expect_tx(full(s), L.a_bytes);
+          tma_load_2d(dst, &tm_a, full(s), i * 128, t.row0, pol);
+        }
+        __syncwarp();
+        issuer = (issuer + 1) & 31;
+        if (++s == stages) s = 0, ph ^= 1u;
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
+    // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows
+    constexpr int kRows = (kMaxNt + 31) / 32, kBatch = 4;  // rows per lane; scale tiles loaded at once
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    const int sfa_tiles = (p.nt + 127) >> 7;
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
+      const Tile t = table.at(idx, p.N);
+      const uint8_t* src[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int i = lane + 32 * j;
+        src[j] = nullptr;
+        if (i < t.rows) {
+          const int r = kGather && p.tokens != nullptr ? p.tokens[t.row0 + i] : t.row0 + i;
+          if (r < 0 || r >= p.a_rows) {
+            atomicOr(p.status, kStatusBadInput);  // reads as zero
+          } else if (p.a_swizzled) {
+            src[j] = p.a_scales + static_cast<size_t>(r >> 7) * units * kSfTile + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+          } else {
+            src[j] = p.a_scales + static_cast<size_t>(r) * units * 4;
+          }
+        }
+      }
+      const int step = p.a_swizzled ? kSfTile : 4;
+      uint32_t v[kBatch][kRows], next[kBatch][kRows];
+      auto load = [&](int u0, uint32_t (&w)[kBatch][kRows]) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int j = 0; j < kRows; ++j)
+            w[b][j] = src[j] != nullptr && u0 + b < units
+                          ? __ldg(reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step))
+                          : 0u;
+      };
+      load(0, next);
+      for (int u0 = 0; ok && u0 < units; u0 += kBatch) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) v[b][j] = next[b][j];
+        load(u0 + kBatch, next);
+#pragma unroll
+        for (int c = 0; c < kBatch / kTiles; ++c) {
+          if (u0 + c * kTiles >= units) break;
+          if (!(ok = warp_wait(empty(s), ph))) break;
+          uint8_t* const dst = base_ptr + L.sfa + s * L.sfa_stage + lane * 16;
+#pragma unroll
+          for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+              const int b = c * kTiles + h;
+              if (rt * 128 < t.n)
+                *reinterpret_cast<uint4*>(dst + (h * sfa_tiles + rt) * kSfTile) =
+                    make_uint4(v[b][4 * rt], v[b][4 * rt + 1], v[b][4 * rt + 2],
+                               4 * rt + 3 < kRows ? v[b][min(4 * rt + 3, kRows - 1)] : 0u);
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(s));
+          if (++s == stages) s = 0, ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- scales into TMEM, and the MMAs
+    const uint64_t wd = sdesc_k_sw128(base), fd = sdesc_sf(base + L.sfw), gd = sdesc_sf(base + L.sfa);
+    const uint32_t op_hi = static_cast<uint32_t>(wd >> 32), sf_hi = static_cast<uint32_t>(fd >> 32);
+    const uint32_t w_lo0 = static_cast<uint32_t>(wd), f_lo0 = static_cast<uint32_t>(fd);
+    const uint32_t g_lo0 = static_cast<uint32_t>(gd);
+    const int sfa_tiles = (p.nt + 127) >> 7;
+    // tcgen05.cp and tcgen05.mma of one thread run in order, so two sets of scale
+    // columns are enough
+    const uint32_t sf_col = tmem + 2 * p.nt, sf_cols = 4 * kTiles * (1 + sfa_tiles);
+    constexpr uint32_t kSf = (1u << 4) | (1u << 29);  // the next scale byte, in both fields of the descriptor
+    int s = 0, it = 0;
+    uint32_t ph = 0, odd = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x, ++it) {
+      const Tile t = table.at(idx, p.N);
+      const int buf = it & 1;
+      if (!(ok = warp_wait(acc_empty + 8 * buf, ((it >> 1) & 1) ^ 1))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * p.nt;
+      const uint32_t id0 = idesc_w4<kA4>(t.n, 0);
+      for (int i = 0; i < chunks; ++i) {
+        if (!(ok = warp_wait(full(s), ph))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t ta = sf_col + odd * sf_cols, tb = ta + 4 * kTiles;
+          const uint32_t f_lo = f_lo0 + s * (L.sfw_stage >> 4), g_lo = g_lo0 + s * (L.sfa_stage >> 4);
+          const int have = min(kTiles, units - i * kTiles);
+#pragma unroll
+          for (int h = 0; h < kTiles; ++h) {
+            if (h < have) {
+              tmem_cp_32x128b_x4_lh(ta + 4 * h, f_lo + h * (kSfTile >> 4), sf_hi);
+              for (int rt = 0; rt * 128 < t.n; ++rt)
+                tmem_cp_32x128b_x4_lh(tb + 4 * (h * sfa_tiles + rt), g_lo + (h * sfa_tiles + rt) * (kSfTile >> 4),
+                                      sf_hi);
+            }
+          }
+          const uint32_t w_lo = w_lo0 + s * (L.stage_bytes >> 4), a_lo = w_lo + (kWBytes >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // .mxf8f6f4: scale byte j of the stage's one tile; .mxf4: bytes 2 (j % 2) and the next of tile j / 2
+            const int h = kA4 ? j >> 1 : 0;
+            if (h < have)
+              mma_w4_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id0 + (kA4 ? 2 * (j & 1) : j) * kSf,
+                             ta + 4 * h, tb + 4 * h * sfa_tiles, i != 0 || j != 0);
+          }
+          tc_commit(empty(s));
+          if (i == chunks - 1) tc_commit(acc_full + 8 * buf);
+        }
+        __syncwarp();
+        odd ^= 1u;
+        if (++s == stages) s = 0, ph ^= 1u;
+      }
+    }
+  } else {
+    // ---------------- epilogue: lane l of quarter q holds output column n0 + 32q + l
+    const int q = warp & 3;
+    const bool odd = lane & 1;
+    int it = 0;
+    bool ok = true;
+    const size_t ldo = p.gated ? p.N >> 1 : p.N;
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x, ++it) {
+      const Tile t = table.at(idx, p.N);
+      const int buf = it & 1;
+      if (!(ok = warp_wait(acc_full + 8 * buf, (it >> 1) & 1))) break;
+      tc_fence_after();
+      const int col = t.n0 + q * 32 + (lane & ~1);
+      __nv_bfloat16* const out = p.out + static_cast<size_t>(t.row0) * ldo + (p.gated ? col >> 1 : col);
+      for (int c0 = 0; c0 < t.n; c0 += 16) {
+        float v[16];
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * p.nt + c0, v);
+        // neighbouring lanes trade, so that the even one has both columns of token
+        // c0 + 2i and the odd one both of c0 + 2i + 1
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float got = __shfl_xor_sync(kFull, odd ? v[2 * i] : v[2 * i + 1], 1);
+          const float a = odd ? got : v[2 * i], b = odd ? v[2 * i + 1] : got;
+          const int tok = c0 + 2 * i + odd;
+          if (tok < t.rows) {
+            if (p.gated)
+              out[tok * ldo] = __float2bfloat16_rn(silu(a) * b);
+            else
+              *reinterpret_cast<__nv_bfloat162*>(out + tok * ldo) = __floats2bfloat162_rn(a, b);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag != 0 && threadIdx.x == 0) {
+    // copies still in flight land within this time, whether or not their stage's
+    // barrier completes (its other arrivals may be missing)
+    for (int s = 0; s < stages; ++s) {
+      mbar_wait(full(s), 0, 2000000);
+      mbar_wait(full(s), 1, 2000000);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+}  // namespace
+
+GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) {
+  GemmFp4Plan pl{};
+  const int kt = a_fp4 ? 2 : 1;
+  // token tile: the rows of an expert in as few tiles of at most kMaxNt as they
+  // take, balanced; with several experts, room for twice the mean
+  const long want = E == 1 ? R : std::min<long>(R, 2L * ((R + E - 1) / E));
+  const long tt = (want + kMaxNt - 1) / kMaxNt;
+  pl.nt = std::min(kMaxNt, static_cast<int>((want + tt - 1) / tt + 15) & ~15);
+  pl.ctas_per_sm = 1;
+  const int cols = 2 * pl.nt + 2 * 4 * kt * (1 + (pl.nt + 127) / 128);
+  pl.tmem_cols = 32;
+  while (pl.tmem_cols < cols) pl.tmem_cols <<= 1;
+  const size_t fixed = Layout(pl.nt, 0, kt, E).total();
+  const size_t per = Layout(pl.nt, 1, kt, E).total() - fixed;
+  pl.stages = static_cast<int>(std::min<size_t>((kMaxDynamicSmem - fixed) / per, 12));
+  // CTAs that share an SM share its tensor memory: take the shared memory that
+  // keeps any more than fit from being resident
+  pl.smem = std::max(Layout(pl.nt, pl.stages, kt, E).total(),
+                     static_cast<size_t>(233472 / (pl.ctas_per_sm + 1) + 1));
+  const long tiles = static_cast<long>(N / 128) * std::min<long>((R + pl.nt - 1L) / pl.nt + E - 1, R);
+  pl.grid = static_cast<int>(std::min<long>(tiles, static_cast<long>(sm_count) * pl.ctas_per_sm));
+  return pl;
+}
+
+cudaError_t set_gemm_fp4_attributes() {
+  for (const void* k : {reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false>),
+                        reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true>),
+                        reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false>),
+                        reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true>)}) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxDynamicSmem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
+                            const GemmFp4Plan& plan, bool a_fp4, bool gather, cudaStream_t stream) {
+  if (plan.smem > kMaxDynamicSmem || plan.stages < 2) return cudaErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    kernel<<<plan.grid, kThreads, plan.smem, stream>>>(tm_w, tm_a, args);
+    return cudaGetLastError();
+  };
+  if (a_fp4) return gather ? go(gemm_fp4_kernel<true, true>) : go(gemm_fp4_kernel<true, false>);
+  return gather ? go(gemm_fp4_kernel<false, true>) : go(gemm_fp4_kernel<false, false>);
+}
+
+}  // namespace mx

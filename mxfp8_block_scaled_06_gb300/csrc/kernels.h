@@ -3,6 +3,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace mx {
@@ -216,5 +217,90 @@ WoaPlan plan_wo_a(int T, int G, int H, int R, int sm_count, const PlanEnv& env);
 cudaError_t set_wo_a_attributes();
 cudaError_t launch_wo_a(const CUtensorMap& tm_w, const WoaArgs& args, const WoaPlan& plan,
                         cudaStream_t stream);
+
+// ------------------------------------------------------------ MXFP4 quantizer
+// Element types of the inputs that may have several (MX_TYPE_* of mx.h).
+enum ElementType : int { kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2 };
+
+// Division of 32-bit numbers by a fixed one (quantize_fp4.cu).
+struct FastDiv {
+  uint32_t mul;
+  int shift;  // -1: the divisor is 1
+};
+FastDiv fast_div(uint32_t d);
+
+// M * K / 8 < 2^31; y (the codes' values in bf16 [M, K]) may be null.
+cudaError_t launch_quantize_rows_fp4(const void* x, long ldx, int x_type, int M, int K, void* q, void* scales,
+                                     int swizzled, void* y, cudaStream_t stream);
+
+// ------------------------------------------------------------ MXFP4 products
+// out = dequant(a) x dequant(w)^T for the rows of E experts (route.cu orders them;
+// a plain product is one expert of M rows). Row r of expert e, offsets[e] <= r <
+// offsets[e + 1], is row tokens[r] of a (r itself where tokens is null).
+struct GemmFp4Args {
+  int E, N, K;
+  int R;                    // output rows
+  int a_rows;               // rows of a
+  int nt;                   // largest token tile (MMA N), a multiple of 16
+  int stages, tmem_cols;
+  const uint8_t* a_scales;  // plain [a_rows, K / 32], or (a_swizzled) the 128x4 layout
+  int a_swizzled;
+  const uint8_t* w_scales;  // 128x4 layout of each expert's [N, K], one after another
+  const int* offsets;       // device, [E + 1]; null: one expert of R rows
+  const int* tokens;        // device, [R], or null
+  int gated;                // out [R, N / 2] = silu(column 2i) * column 2i + 1
+  __nv_bfloat16* out;
+  int* status;
+};
+struct GemmFp4Plan {
+  int nt, stages, tmem_cols, ctas_per_sm, grid;
+  size_t smem;
+};
+GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count);
+cudaError_t set_gemm_fp4_attributes();
+// tm_w: [E N, K] weights, tm_a: the activations (box one row high where gather is set).
+cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
+                            const GemmFp4Plan& plan, bool a_fp4, bool gather, cudaStream_t stream);
+
+// ------------------------------------------------------------ routing to experts
+enum Scoring : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+constexpr int kRouteMaxExperts = 512;
+constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteChunks = 512;   // chunks of tokens whose rows are counted apart
+constexpr int kRouteMinChunk = 32;  // tokens of a chunk, at least
+// the handle's workspace: rows per (expert, chunk), rows per expert
+constexpr size_t kRouteWorkspace = sizeof(int) * (static_cast<size_t>(kRouteMaxExperts) * kRouteChunks + kRouteMaxExperts);
+
+struct RouteArgs {
+  int T, E, top_k;
+  const void* logits;  // float32 or bf16 [T, E], row stride ldl
+  long ldl;
+  int bf16;
+  const float* bias;  // [E] or null
+  int scoring, n_groups, topk_groups, renormalize;
+  float scale;
+  float* weights;  // [T, top_k]
+  int* experts;    // [T, top_k]
+  int* offsets;    // [E + 1]
+  int* tokens;     // [T top_k]: token of each row in expert order
+  int* slots;      // [T, top_k]: the row of each (token, choice)
+  int* counts;     // workspace [E][chunks]
+  int* totals;     // workspace [E]
+  // set by launch_route
+  int chunk, chunks, group_parts, shared_keys;
+};
+cudaError_t launch_route(RouteArgs args, cudaStream_t stream);
+
+struct CombineArgs {
+  int T, top_k, N, R;
+  const __nv_bfloat16* y;  // [R, N], row stride ldy
+  long ldy;
+  const int* slots;
+  const float* weights;
+  const __nv_bfloat16* residual;  // [T, N] or null
+  __nv_bfloat16* out;             // [T, N]
+  int* status;
+};
+cudaError_t launch_combine(const CombineArgs& args, cudaStream_t stream);
 
 }  // namespace mx

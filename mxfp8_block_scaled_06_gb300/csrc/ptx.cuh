@@ -72,6 +72,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// As mbar_wait, giving up early once *abort (shared memory) is set.
+__device__ __forceinline__ bool mbar_wait_or(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort != 0 || globaltimer() - t0 > kWaitLimitNs)) return false;
+  }
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
@@ -83,6 +96,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, 
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+// Four rows (row coordinates r.x..r.w, a box one row high) of a 2-D tensor from
+// element column x into four consecutive box rows; a row coordinate outside the
+// tensor reads as zero.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int4 r,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "l"(policy)
       : "memory");
 }
 // Untiled bulk copy global -> shared; bytes % 16 == 0, both addresses 16-byte aligned.
@@ -97,6 +121,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 __device__ __forceinline__ uint64_t policy_evict_last() {
@@ -340,6 +369,33 @@ __device__ __forceinline__ void mma_mxf8_lh(uint32_t d_tmem, uint32_t a_lo, uint
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accumulate), "r"(idesc), "r"(sfa_tmem),
       "r"(sfb_tmem)
       : "memory");
+}
+// Instruction descriptor of tcgen05.mma .block_scale with E2M1 weights (A):
+// .kind::mxf8f6f4 against E4M3 activations (K = 32; format codes 5 and 0 there),
+// or .kind::mxf4 with E2M1 activations (K = 64; format code 1). sf_id is the
+// scale byte, or the first of the two scale bytes, of the 32-bit scale word.
+template <bool kA4>
+__device__ __forceinline__ uint32_t idesc_w4(uint32_t n, uint32_t sf_id) {
+  return (sf_id << 4) | ((kA4 ? 1u : 5u) << 7) | ((kA4 ? 1u : 0u) << 10) | ((n >> 3) << 17) | (1u << 23) |
+         ((128u >> 4) << 24) | (sf_id << 29);
+}
+// D[tmem] (+)= A[smem] x B[smem]^T, A MXFP4, as mma_mxf8_lh. .kind::mxf8f6f4 reads
+// E2M1 elements unpacked (16 elements in the low 8 of 16 bytes), .kind::mxf4 packed.
+template <bool kA4>
+__device__ __forceinline__ void mma_w4_lh(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                          uint32_t accumulate) {
+  if constexpr (kA4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %6, [%7], "
+        "[%8], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accumulate), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+  else
+    mma_mxf8_lh(d_tmem, a_lo, a_hi, b_lo, b_hi, idesc, sfa_tmem, sfb_tmem, accumulate);
 }
 // Copy a 32x128-bit smem tile into TMEM lanes 0-31, replicated into all four
 // 32-lane quarters (4 columns); the descriptor as its two 32-bit halves.
