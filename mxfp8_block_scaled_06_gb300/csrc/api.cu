@@ -832,10 +832,11 @@ namespace {
 
 // The tensor maps and the launch shared by the two entry points below; the
 // arguments are validated by the callers.
-int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp4, const void* w, bool gather,
+int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp4, const void* w,
                     cudaStream_t stream) {
   const mx::GemmFp4Plan plan = mx::plan_gemm_fp4(args.E, args.R, args.N, args.K, a_fp4 != 0, h->sm_count);
-  if (plan.stages < 2) return MX_ERR_UNSUPPORTED;
+  if (plan.stages < 3) return MX_ERR_UNSUPPORTED;
+  args.a = static_cast<const uint8_t*>(a);
   args.nt = plan.nt;
   args.stages = plan.stages;
   args.tmem_cols = plan.tmem_cols;
@@ -843,9 +844,9 @@ int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp
   CUtensorMap tm_w, tm_a;
   const int w_rows = args.E * args.N;
   int rc = a_fp4 ? make_tmap(h, &tm_w, w, w_rows, args.K / 2, 128) : make_tmap(h, &tm_w, w, w_rows, args.K, 128, true);
-  if (rc == MX_OK) rc = make_tmap(h, &tm_a, a, args.a_rows, a_fp4 ? args.K / 2 : args.K, gather ? 1 : plan.nt);
+  if (rc == MX_OK) rc = make_tmap(h, &tm_a, a, args.a_rows, a_fp4 ? args.K / 2 : args.K, plan.nt);
   if (rc != MX_OK) return rc;
-  return cuda_status(mx::launch_gemm_fp4(tm_w, tm_a, args, plan, a_fp4 != 0, gather, stream));
+  return cuda_status(mx::launch_gemm_fp4(tm_w, tm_a, args, plan, a_fp4 != 0, stream));
 }
 
 }  // namespace
@@ -869,7 +870,7 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
   args.a_swizzled = 1;
   args.w_scales = static_cast<const uint8_t*>(w_scales);
   args.out = static_cast<__nv_bfloat16*>(out);
-  return gemm_fp4_launch(h, args, a, a_fp4, w, false, static_cast<cudaStream_t>(stream));
+  return gemm_fp4_launch(h, args, a, a_fp4, w, static_cast<cudaStream_t>(stream));
 }
 
 int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a, int a_rows, const void* a_scales,
@@ -900,7 +901,7 @@ int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a,
   args.tokens = tokens;
   args.gated = gated != 0;
   args.out = static_cast<__nv_bfloat16*>(out);
-  return gemm_fp4_launch(h, args, a, a_fp4, w, true, static_cast<cudaStream_t>(stream));
+  return gemm_fp4_launch(h, args, a, a_fp4, w, static_cast<cudaStream_t>(stream));
 }
 
 int mx_route(mx_handle* h, int T, int E, int top_k, const void* logits, long ldl, int logits_type, const float* bias,

@@ -10,9 +10,12 @@
 // ring of operand stages runs on across tiles. Warps:
 //   0     weight boxes (TMA) and their scale tiles (bulk copies)
 //   1     tcgen05.cp of the scales and tcgen05.mma, by an elected lane
-//   2     activation rows: a TMA box, or gathered by row index (tile::gather4)
+//   2     activation rows, where they are neighbours: a TMA box
 //   3     activation scales: gathered with plain loads into 128x4 scale tiles
 //   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half
+//   8-11  activation rows gathered by index: 16-byte cp.async into the swizzled
+//         tile (tile::gather4 copies, four rows each, came at 34 ns apiece: 1.9 us
+//         for a stage of 224 rows, against 0.4 us that the MMAs of a stage take)
 // A stage holds 128 bytes of K per operand row in the 128-byte swizzle: 128
 // elements against MXFP8 activations (.kind::mxf8f6f4 wants E2M1 unpacked to a
 // byte each, which the tensor map does on the way: HBM sees 4 bits), 256 elements
@@ -29,7 +32,7 @@
 namespace mx {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kGatherThreads = 128;  // the latter on top, where rows are gathered
 constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
 // bytes that an unpacking copy of it completes on its barrier: the packed ones
 constexpr uint32_t kWBytesUnpacked = 128 * 64;
@@ -89,7 +92,7 @@ struct Table {
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 template <bool kA4, bool kGather>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ GemmFp4Args p) {
   constexpr int kTiles = kA4 ? 2 : 1;  // scale tiles (128 elements of K) per stage
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full(s), 3);  // weights, activations, activation scales
+      mbar_init(full(s), 2 + (kGather ? kGatherThreads / 32 : 1));  // weights, activation scales, activations
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -193,49 +196,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++s == stages) s = 0, ph ^= 1u;
       }
     }
-  } else if (warp == 2) {
-    // ---------------- activation rows
+  } else if (!kGather && warp == 2) {
+    // ---------------- activation rows from row0 on: rows past the tile belong to
+    // other tiles and end in columns that are not stored; past the tensor: zeros
     const uint64_t pol = policy_evict_last();
     int s = 0, issuer = 0;
     uint32_t ph = 1;
     bool ok = true;
     for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
       const Tile t = table.at(idx, p.N);
-      int4 r[2];
-      if constexpr (kGather) {
-        // lane l gathers rows 4l .. 4l + 3 and 128 + 4l ..; rows past the tile (and
-        // tokens outside a) are out of the tensor and read as zero
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          int v[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int i = b * 128 + lane * 4 + q;
-            v[q] = i < t.rows ? (p.tokens != nullptr ? p.tokens[t.row0 + i] : t.row0 + i) : p.a_rows;
-            if (v[q] < 0 || v[q] > p.a_rows) v[q] = p.a_rows;
-          }
-          r[b] = make_int4(v[0], v[1], v[2], v[3]);
-        }
-      }
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(empty(s), ph))) break;
-        const uint32_t dst = base + s * L.stage_bytes + kWBytes;
-        if constexpr (kGather) {
-          if (lane == 0) mbar_expect_tx(full(s), static_cast<uint32_t>(t.n) * 128u);
-          __syncwarp();
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            if (b * 128 + lane * 4 < t.n)
-              tma_gather4(dst + (b * 128 + lane * 4) * 128, &tm_a, full(s), i * 128, r[b], pol);
-        } else if (lane == issuer) {
+        if (lane == issuer) {
           mbar_expect_tx(full(s), L.a_bytes);
-          tma_load_2d(dst, &tm_a, full(s), i * 128, t.row0, pol);
+          tma_load_2d(base + s * L.stage_bytes + kWBytes, &tm_a, full(s), i * 128, t.row0, pol);
         }
         __syncwarp();
         issuer = (issuer + 1) & 31;
         if (++s == stages) s = 0, ph ^= 1u;
       }
     }
+  } else if (kGather && warp >= kThreads / 32) {
+    // ---------------- gathered activation rows: eight threads a row, 16 bytes each
+    constexpr int kRows = (kMaxNt + 15) / 16;  // rows per thread, 16 apart
+    constexpr int kLag = 2;                    // stages copied ahead of the one handed over
+    const int gt = threadIdx.x - kThreads, c = gt & 7, r0 = gt >> 3;
+    const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
+    // rows r0, r0 + 16, ... have the same r % 8: one swizzle for all
+    const uint32_t dst0 = base + kWBytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+    int s = 0, handed = 0, pending = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    auto hand_over = [&]() {
+      fence_proxy_async_smem();  // written by the threads, read by the tensor cores
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(handed));
+      if (++handed == stages) handed = 0;
+      --pending;
+    };
+    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
+      const Tile t = table.at(idx, p.N);
+      // byte offsets in a; rows past the tile and tokens outside a read as zero
+      const uint8_t* src[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const int i = r0 + 16 * j;
+        src[j] = nullptr;
+        if (i < t.rows) {
+          const int r = p.tokens[t.row0 + i];
+          if (r >= 0 && r < p.a_rows) src[j] = p.a + static_cast<size_t>(r) * row_bytes + c * 16;
+        }
+      }
+      for (int i = 0; i < chunks; ++i) {
+        if (!(ok = warp_wait(empty(s), ph))) break;
+        const uint32_t dst = dst0 + s * L.stage_bytes;
+        const bool in_row = static_cast<uint32_t>(i) * 128u + c * 16u < row_bytes;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (16 * j < t.n)
+            cp_async_16(dst + j * 2048, src[j] != nullptr ? src[j] + static_cast<size_t>(i) * 128 : p.a,
+                        src[j] != nullptr && in_row ? 16u : 0u);
+        cp_async_commit();
+        if (++pending > kLag) {
+          cp_async_wait<kLag>();
+          hand_over();
+        }
+        if (++s == stages) s = 0, ph ^= 1u;
+      }
+    }
+    cp_async_wait<0>();
+    while (pending > 0) hand_over();
   } else if (warp == 3) {
     // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
     // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows
@@ -252,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = lane + 32 * j;
         src[j] = nullptr;
         if (i < t.rows) {
-          const int r = kGather && p.tokens != nullptr ? p.tokens[t.row0 + i] : t.row0 + i;
+          const int r = kGather ? p.tokens[t.row0 + i] : t.row0 + i;
           if (r < 0 || r >= p.a_rows) {
             atomicOr(p.status, kStatusBadInput);  // reads as zero
           } else if (p.a_swizzled) {
@@ -356,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++s == stages) s = 0, ph ^= 1u;
       }
     }
-  } else {
+  } else if (warp >= 4 && warp < 8) {
     // ---------------- epilogue: lane l of quarter q holds output column n0 + 32q + l
     const int q = warp & 3;
     const bool odd = lane & 1;
@@ -451,10 +481,11 @@ cudaError_t set_gemm_fp4_attributes() {
 }
 
 cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
-                            const GemmFp4Plan& plan, bool a_fp4, bool gather, cudaStream_t stream) {
-  if (plan.smem > kMaxDynamicSmem || plan.stages < 2) return cudaErrorInvalidValue;
+                            const GemmFp4Plan& plan, bool a_fp4, cudaStream_t stream) {
+  const bool gather = args.tokens != nullptr;
+  if (plan.smem > kMaxDynamicSmem || plan.stages < 3) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
-    kernel<<<plan.grid, kThreads, plan.smem, stream>>>(tm_w, tm_a, args);
+    kernel<<<plan.grid, kThreads + (gather ? kGatherThreads : 0), plan.smem, stream>>>(tm_w, tm_a, args);
     return cudaGetLastError();
   };
   if (a_fp4) return gather ? go(gemm_fp4_kernel<true, true>) : go(gemm_fp4_kernel<true, false>);

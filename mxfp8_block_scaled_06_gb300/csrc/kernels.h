@@ -241,6 +241,7 @@ struct GemmFp4Args {
   int E, N, K;
   int R;                    // output rows
   int a_rows;               // rows of a
+  const uint8_t* a;         // the activations, read directly where tokens is set
   int nt;                   // largest token tile (MMA N), a multiple of 16
   int stages, tmem_cols;
   const uint8_t* a_scales;  // plain [a_rows, K / 32], or (a_swizzled) the 128x4 layout
@@ -258,9 +259,9 @@ struct GemmFp4Plan {
 };
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count);
 cudaError_t set_gemm_fp4_attributes();
-// tm_w: [E N, K] weights, tm_a: the activations (box one row high where gather is set).
+// tm_w: [E N, K] weights, tm_a: the activations (box nt rows high; unused where tokens is set).
 cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
-                            const GemmFp4Plan& plan, bool a_fp4, bool gather, cudaStream_t stream);
+                            const GemmFp4Plan& plan, bool a_fp4, cudaStream_t stream);
 
 // ------------------------------------------------------------ routing to experts
 enum Scoring : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
