@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -38,6 +39,10 @@ constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
 constexpr uint32_t kWBytesUnpacked = 128 * 64;
 constexpr uint32_t kSfTile = 512;  // one 128x4 scale tile: 128 rows x 128 elements of K
 constexpr int kMaxNt = 224;        // two accumulators of 224 columns leave 64 columns of TMEM for scales
+// Token tiles up to kSmallNt run two CTAs to an SM. A narrow MMA of a block-scaled
+// kind takes about 140 cycles whatever its width, one issuing thread is bound by
+// that, and two CTAs issue side by side.
+constexpr int kSmallNt = 64;
 constexpr int kMaxE = kRouteMaxExperts;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -91,11 +96,12 @@ struct Table {
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
-template <bool kA4, bool kGather>
-__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), 1)
+template <bool kA4, bool kGather, bool kSmall>
+__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSmall ? 2 : 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ GemmFp4Args p) {
   constexpr int kTiles = kA4 ? 2 : 1;  // scale tiles (128 elements of K) per stage
+  constexpr int kNt = kSmall ? kSmallNt : kMaxNt;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -218,8 +224,8 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), 1)
     }
   } else if (kGather && warp >= kThreads / 32) {
     // ---------------- gathered activation rows: eight threads a row, 16 bytes each
-    constexpr int kRows = (kMaxNt + 15) / 16;  // rows per thread, 16 apart
-    constexpr int kLag = 2;                    // stages copied ahead of the one handed over
+    constexpr int kRows = (kNt + 15) / 16;  // rows per thread, 16 apart
+    constexpr int kLag = 2;                 // stages copied ahead of the one handed over
     const int gt = threadIdx.x - kThreads, c = gt & 7, r0 = gt >> 3;
     const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
     // rows r0, r0 + 16, ... have the same r % 8: one swizzle for all
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), 1)
   } else if (warp == 3) {
     // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
     // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows
-    constexpr int kRows = (kMaxNt + 31) / 32, kBatch = 4;  // rows per lane; scale tiles loaded at once
+    constexpr int kRows = (kNt + 31) / 32, kBatch = 4;  // rows per lane; scale tiles loaded at once
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
@@ -318,12 +324,13 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), 1)
 #pragma unroll
           for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) {
+            for (int rt = 0; rt < (kNt + 127) / 128; ++rt) {
               const int b = c * kTiles + h;
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = 4 * rt + j < kRows ? v[b][min(4 * rt + j, kRows - 1)] : 0u;
               if (rt * 128 < t.n)
-                *reinterpret_cast<uint4*>(dst + (h * sfa_tiles + rt) * kSfTile) =
-                    make_uint4(v[b][4 * rt], v[b][4 * rt + 1], v[b][4 * rt + 2],
-                               4 * rt + 3 < kRows ? v[b][min(4 * rt + 3, kRows - 1)] : 0u);
+                *reinterpret_cast<uint4*>(dst + (h * sfa_tiles + rt) * kSfTile) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           fence_proxy_async_smem();
           __syncwarp();
@@ -451,13 +458,14 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
   const long want = E == 1 ? R : std::min<long>(R, 2L * ((R + E - 1) / E));
   const long tt = (want + kMaxNt - 1) / kMaxNt;
   pl.nt = std::min(kMaxNt, static_cast<int>((want + tt - 1) / tt + 15) & ~15);
-  pl.ctas_per_sm = 1;
+  pl.ctas_per_sm = pl.nt <= kSmallNt ? 2 : 1;
   const int cols = 2 * pl.nt + 2 * 4 * kt * (1 + (pl.nt + 127) / 128);
   pl.tmem_cols = 32;
   while (pl.tmem_cols < cols) pl.tmem_cols <<= 1;
   const size_t fixed = Layout(pl.nt, 0, kt, E).total();
   const size_t per = Layout(pl.nt, 1, kt, E).total() - fixed;
-  pl.stages = static_cast<int>(std::min<size_t>((kMaxDynamicSmem - fixed) / per, 12));
+  const size_t room = pl.ctas_per_sm == 1 ? kMaxDynamicSmem : 233472 / 2 - 1024;  // 1 KB of each CTA's is reserved
+  pl.stages = static_cast<int>(std::min<size_t>((room - fixed) / per, 12));
   // CTAs that share an SM share its tensor memory: take the shared memory that
   // keeps any more than fit from being resident
   pl.smem = std::max(Layout(pl.nt, pl.stages, kt, E).total(),
@@ -468,10 +476,16 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
 }
 
 cudaError_t set_gemm_fp4_attributes() {
-  for (const void* k : {reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false>),
-                        reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true>),
-                        reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false>),
-                        reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true>)}) {
+  const void* const kernels[] = {
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, false>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, false>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, false>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, false>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, true>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, true>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, true>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, true>)};
+  for (const void* k : kernels) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxDynamicSmem));
@@ -488,8 +502,12 @@ cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, co
     kernel<<<plan.grid, kThreads + (gather ? kGatherThreads : 0), plan.smem, stream>>>(tm_w, tm_a, args);
     return cudaGetLastError();
   };
-  if (a_fp4) return gather ? go(gemm_fp4_kernel<true, true>) : go(gemm_fp4_kernel<true, false>);
-  return gather ? go(gemm_fp4_kernel<false, true>) : go(gemm_fp4_kernel<false, false>);
+  auto pick = [&](auto small) {
+    constexpr bool S = decltype(small)::value;
+    if (a_fp4) return gather ? go(gemm_fp4_kernel<true, true, S>) : go(gemm_fp4_kernel<true, false, S>);
+    return gather ? go(gemm_fp4_kernel<false, true, S>) : go(gemm_fp4_kernel<false, false, S>);
+  };
+  return plan.nt <= kSmallNt ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace mx
