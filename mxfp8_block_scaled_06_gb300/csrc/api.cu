@@ -32,6 +32,7 @@ struct PlanEntry {
   bool fused, norm;
   int push_mode;
   bool table_depth;
+  int w_fmt;
   mx::GemmPlan plan;
 };
 constexpr int kPlanCache = 64;
@@ -85,6 +86,16 @@ constexpr size_t kSsqBytes = size_t{64} << 10;
 // rows of the MXFP4 products, and (token, choice) rows of the router: tile and row
 // numbers are 32-bit
 constexpr int kMaxFp4Rows = 1 << 24;
+// Whether mx_gemm_fp4 splits K over a cluster (gemm.cu, up to 256 rows) instead of
+// walking whole-K tiles (gemm_fp4.cu): S splits save (1 - 1 / S) of a tile's chain of
+// K / 128 chunks, about 0.25 us each, and add about 0.02 us a row to exchange the
+// partial sums. Measured on GB300, split / whole us: N = 2048, K = 5120 5.9 / 14.2 at one
+// row and 12.6 / 17.0 at 256; N = 8192, K = 1536 7.2 / 7.7 at 64 rows, 9.0 / 9.2 at 128,
+// 12.6 / 9.8 at 256; N = K = 512 4.5 / 4.8 at 32 rows, 5.4 / 5.1 at 64; N = 16384 (one
+// split) 13.5 / 12.8 at 8 rows, 24.1 / 18.1 at 201.
+bool fp4_split_k(int M, int K, const mx::GemmPlan& plan) {
+  return plan.smem <= mx::kMaxDynamicSmem && static_cast<long>(M) * plan.splits < 12L * (K / 128) * (plan.splits - 1);
+}
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -109,17 +120,17 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MX_OK : MX_ERR_CUDA; 
 // The GEMM plan of a problem, computed once per handle (mx_warmup computes those
 // of the registered shapes ahead of the first call).
 mx::GemmPlan get_plan(mx_handle* h, int M, int N, int K, bool fused = false, bool norm = false,
-                      int push_mode = mx::kPushFull, bool table_depth = true) {
+                      int push_mode = mx::kPushFull, bool table_depth = true, int w_fmt = 0) {
   for (int i = 0; i < h->plan_count; ++i) {
     const PlanEntry& e = h->plans[i];
     if (e.M == M && e.N == N && e.K == K && e.fused == fused && e.norm == norm && e.push_mode == push_mode &&
-        e.table_depth == table_depth)
+        e.table_depth == table_depth && e.w_fmt == w_fmt)
       return e.plan;
   }
-  const mx::GemmPlan plan = mx::plan_gemm(M, N, K, h->sm_count, h->env, fused, norm, push_mode, table_depth);
+  const mx::GemmPlan plan = mx::plan_gemm(M, N, K, h->sm_count, h->env, fused, norm, push_mode, table_depth, w_fmt);
   const int slot = h->plan_count < kPlanCache ? h->plan_count++ : h->plan_next;
   if (h->plan_count == kPlanCache) h->plan_next = (slot + 1) % kPlanCache;
-  h->plans[slot] = PlanEntry{M, N, K, fused, norm, push_mode, table_depth, plan};
+  h->plans[slot] = PlanEntry{M, N, K, fused, norm, push_mode, table_depth, w_fmt, plan};
   return plan;
 }
 
@@ -238,11 +249,14 @@ int gemm_prepare(mx_handle* h, GemmLaunch* L, int M, int N, int K, const void* a
                  const void* a_scales, const void* w, const void* w_scales, void* out, uint8_t* q,
                  uint8_t* q_scales, int q_cols, const void* x = nullptr, long ldx = 0,
                  int groups = 1, const mx::GemmNorm* norm = nullptr, int push_mode = mx::kPushFull,
-                 bool table_depth = true) {
-  L->plan = get_plan(h, M, N, K, x != nullptr, norm != nullptr, push_mode, table_depth);
-  int rc = make_tmap(h, &L->tm_w, w, N, K, 128);
+                 bool table_depth = true, int w_fmt = 0) {
+  L->plan = get_plan(h, M, N, K, x != nullptr, norm != nullptr, push_mode, table_depth, w_fmt);
+  int rc = make_tmap(h, &L->tm_w, w, N, w_fmt == 2 ? K / 2 : K, 128, w_fmt == 1);
   if (rc != MX_OK) return rc;
-  if (x != nullptr) {
+  if (w_fmt == 2) {
+    rc = make_tmap(h, &L->tm_a, a, M, K / 2, L->plan.mtile);
+    if (rc != MX_OK) return rc;
+  } else if (x != nullptr) {
     L->tm_a = L->tm_w;  // not read by the fused kernel
   } else {
     rc = make_tmap(h, &L->tm_a, a, M, static_cast<long>(K) * groups, L->plan.mtile);
@@ -253,9 +267,10 @@ int gemm_prepare(mx_handle* h, GemmLaunch* L, int M, int N, int K, const void* a
   args.M = M;
   args.N = N;
   args.K = K;
+  args.w_fmt = w_fmt;
   args.mtile = L->plan.mtile;
   args.stages = L->plan.stages;
-  args.nchunks = K / 128;
+  args.nchunks = w_fmt == 2 ? (K / 128 + 1) / 2 : K / 128;
   args.tmem_cols = L->plan.tmem_cols;
   args.a_scales = static_cast<const uint8_t*>(a_scales);
   args.w_scales = static_cast<const uint8_t*>(w_scales);
@@ -861,6 +876,13 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
   if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(w, 32) || !aligned(w_scales, 32) || !aligned(out, 16))
     return MX_ERR_INVALID_ARG;
   if (N % 128 != 0 || K % 128 != 0 || M > kMaxFp4Rows) return MX_ERR_UNSUPPORTED;
+  const int fmt = a_fp4 ? 2 : 1;
+  if (M <= 256 && fp4_split_k(M, K, get_plan(h, M, N, K, false, false, mx::kPushFull, true, fmt))) {
+    GemmLaunch L;
+    rc = gemm_prepare(h, &L, M, N, K, a, a_scales, w, w_scales, out, nullptr, nullptr, 0, nullptr, 0, 1, nullptr,
+                      mx::kPushFull, true, fmt);
+    return rc != MX_OK ? rc : gemm_run(h, &L, (flags & MX_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
+  }
   mx::GemmFp4Args args = {};
   args.E = 1;
   args.N = N;
@@ -870,6 +892,7 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
   args.a_swizzled = 1;
   args.w_scales = static_cast<const uint8_t*>(w_scales);
   args.out = static_cast<__nv_bfloat16*>(out);
+  args.early_weights = (flags & MX_FLAG_PDL) != 0;
   return gemm_fp4_launch(h, args, a, a_fp4, w, static_cast<cudaStream_t>(stream));
 }
 

@@ -34,8 +34,11 @@
 //    activation) takes its 32 values as one block; a relaxed cluster barrier
 //    keeps every CTA alive until its peers are done with its shared memory.
 // Variants: bf16 activations quantized in the prologue into resident operand
-// tiles (kFusedA), and grouped activations (weight tile t contracts the K-slice
-// of its group of a wider activation).
+// tiles (kFusedA), grouped activations (weight tile t contracts the K-slice
+// of its group of a wider activation), and MXFP4 weights (kFmt) against MXFP8 or
+// MXFP4 activations: a chunk stays 128 bytes of shared memory per row, which is 128
+// elements of K unpacked to a byte each by the tensor map (.kind::mxf8f6f4), or
+// 256 packed elements with two scale tiles (.kind::mxf4).
 // Every mbarrier wait is bounded; on expiry the kernel records MX_ERR_TIMEOUT,
 // skips the remaining work, drains its outstanding copies and frees TMEM.
 #include <cuda_bf16.h>
@@ -81,6 +84,11 @@ __device__ __forceinline__ unsigned long long tl_smid() {
 #endif
 constexpr uint32_t kWTileBytes = 128 * 128;  // one weight box: 128 rows x 128 K-bytes
 constexpr uint32_t kSfTileBytes = 512;       // one 128x4 scale tile
+// Weight formats: MXFP8, MXFP4 against MXFP8 activations, MXFP4 against MXFP4.
+enum Format : int { kFmtMx8 = 0, kFmtW4A8 = 1, kFmtW4A4 = 2 };
+__host__ __device__ constexpr int sf_tiles(int fmt) { return fmt == kFmtW4A4 ? 2 : 1; }  // scale tiles of a chunk
+// bytes that a weight box completes on its barrier: an unpacking copy counts the packed ones
+__host__ __device__ constexpr uint32_t w_tx_bytes(int fmt) { return fmt == kFmtW4A8 ? kWTileBytes / 2 : kWTileBytes; }
 
 // Shared-memory carve-up of one CTA: a ring of `stages` (weight box, activation
 // box) pairs, then the weight and activation scale tiles of the CTA's whole
@@ -98,17 +106,19 @@ constexpr int kRedRows = 4;  // rows a warp reduces at once in the several-rows 
 struct Layout {
   uint32_t a_bytes, stage_bytes, ring_bytes, sfa_bytes, sfb_bytes, act, xraw, gam, ssq, inv, bars;
   uint32_t red_bar, red, red_bytes;
-  int stages, nsfb, nmax;
+  int stages, nsfb, nmax, tiles;
+  // tiles_: scale tiles of a chunk
   __host__ __device__ Layout(int mtile, int stages_, int nmax_, bool fused = false, int xrows = 0,
-                             int norm_blocks = 0, uint32_t red_bytes_ = 0) {
+                             int norm_blocks = 0, uint32_t red_bytes_ = 0, int tiles_ = 1) {
     stages = stages_;
     nmax = nmax_;
+    tiles = tiles_;
     nsfb = (mtile + 127) / 128;
     a_bytes = static_cast<uint32_t>(mtile) * 128u;
     stage_bytes = fused ? kWTileBytes : (kWTileBytes + a_bytes + 1023u) & ~1023u;
     ring_bytes = static_cast<uint32_t>(stages) * stage_bytes;
-    sfa_bytes = static_cast<uint32_t>(nmax) * kSfTileBytes;
-    sfb_bytes = static_cast<uint32_t>(nmax * nsfb) * kSfTileBytes;
+    sfa_bytes = static_cast<uint32_t>(nmax * tiles) * kSfTileBytes;
+    sfb_bytes = static_cast<uint32_t>(nmax * tiles * nsfb) * kSfTileBytes;
     act = (ring_bytes + sfa_bytes + sfb_bytes + 1023u) & ~1023u;
     xraw = act + (fused ? static_cast<uint32_t>(nmax) * a_bytes : 0u);
     gam = xraw + (fused ? static_cast<uint32_t>(xrows * nmax) * 256u : 0u);
@@ -122,9 +132,9 @@ struct Layout {
   }
   __host__ __device__ uint32_t w_off(int s) const { return s * stage_bytes; }
   __host__ __device__ uint32_t a_off(int s) const { return s * stage_bytes + kWTileBytes; }
-  __host__ __device__ uint32_t sfa_off(int i) const { return ring_bytes + i * kSfTileBytes; }
+  __host__ __device__ uint32_t sfa_off(int i) const { return ring_bytes + i * tiles * kSfTileBytes; }
   __host__ __device__ uint32_t sfb_off(int rt, int i) const {
-    return ring_bytes + sfa_bytes + (rt * nmax + i) * kSfTileBytes;
+    return ring_bytes + sfa_bytes + (rt * nmax + i) * tiles * kSfTileBytes;
   }
   // full[stages], empty[stages], sfa, sfb, accum, x; then TMEM slot and abort
   // flag; then the push reduction's receive barrier
@@ -175,7 +185,7 @@ __device__ __forceinline__ void load_block64(const uint8_t* src, int rot, uint32
 }
 
 // kRed: how the K-splits' partials are summed (Reduction).
-template <bool kRequant, bool kFusedA, int kRed>
+template <bool kRequant, bool kFusedA, int kRed, int kFmt = kFmtMx8>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                 const GemmArgs p) {
@@ -200,7 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PushGeometry pgeo(p.M, kPush ? S : 1, kPush ? split : 0);
   const uint32_t slot = pgeo.slot;
   const Layout L(p.mtile, stages, (p.nchunks + S - 1) / S, kFusedA, min(p.M, kRowBatch),
-                 norm ? p.K / 32 : 0, kPush ? push_area_bytes(p.M, S, compact) : 0u);
+                 norm ? p.K / 32 : 0, kPush ? push_area_bytes(p.M, S, compact) : 0u, sf_tiles(kFmt));
+  // scale tiles along K, of all and of this CTA's chunks (MXFP4 activations: the last chunk may be half a one)
+  const int units = kFmt == kFmtMx8 ? p.nchunks : p.K >> 7;
+  const int n_units = kFmt == kFmtMx8 ? n : min(n * sf_tiles(kFmt), units - c_begin * sf_tiles(kFmt));
   const int nsfb = L.nsfb;
   // Whether anything consumes the output columns of the tile's 32-column block
   // q: a block nobody consumes (no bf16 output, outside the requantized and the
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPush) cluster_arrive_release();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sfa_col = tmem_sfa_col(p.mtile);
-  const uint32_t sfb_col = sfa_col + 4 * stages;
+  const uint32_t sfb_col = sfa_col + 4 * sf_tiles(kFmt) * stages;
   if (threadIdx.x == 0) MX_TL(1, globaltimer());
 
   auto fail = [&]() {
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int last = -1;      // last chunk this lane loaded (weight or activation warps)
   int issued_n = 0;   // chunks its warp has loaded so far (warp-uniform)
   auto issue_w = [&](int i, int s) {
-    mbar_expect_tx(full(s), kWTileBytes);
+    mbar_expect_tx(full(s), w_tx_bytes(kFmt));
     tma_load_2d(base + L.w_off(s), &tm_w, full(s), (c_begin + i) * 128, tile * 128, pol_w);
     last = i;
   };
@@ -286,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) issued_n = min(n, stages);
   if (warp == 0 && lane == 0) MX_TL(2, globaltimer());
   if (warp == 2 && lane == 0) {
-    mbar_expect_tx(sfa_bar, static_cast<uint32_t>(n) * kSfTileBytes);
+    mbar_expect_tx(sfa_bar, static_cast<uint32_t>(n_units) * kSfTileBytes);
     bulk_load(base + L.sfa_off(0),
-              p.w_scales + (static_cast<size_t>(tile) * p.nchunks + c_begin) * kSfTileBytes,
-              static_cast<uint32_t>(n) * kSfTileBytes, sfa_bar, pol_w);
+              p.w_scales + (static_cast<size_t>(tile) * units + c_begin * sf_tiles(kFmt)) * kSfTileBytes,
+              static_cast<uint32_t>(n_units) * kSfTileBytes, sfa_bar, pol_w);
   }
   pdl_launch_dependents();
 #ifdef MX_TIMELINE
@@ -350,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a_lane && lane < n) issue_a(lane, lane);
     if (warp == 3) issued_n = min(n, stages);
     if (warp == 2 && lane == 1) {
-      mbar_expect_tx(sfb_bar, static_cast<uint32_t>(n * nsfb) * kSfTileBytes);
+      mbar_expect_tx(sfb_bar, static_cast<uint32_t>(n_units * nsfb) * kSfTileBytes);
       for (int rt = 0; rt < nsfb; ++rt)
         bulk_load(base + L.sfb_off(rt, 0),
-                  p.a_scales + (static_cast<size_t>(rt) * p.a_sf_chunks + a_k0 / 128 + c_begin) *
-                                   kSfTileBytes,
-                  static_cast<uint32_t>(n) * kSfTileBytes, sfb_bar, pol_a);
+                  p.a_scales + (static_cast<size_t>(rt) * p.a_sf_chunks + a_k0 / 128 +
+                                c_begin * sf_tiles(kFmt)) * kSfTileBytes,
+                  static_cast<uint32_t>(n_units) * kSfTileBytes, sfb_bar, pol_a);
     }
   } else {
     // bf16 rows of the CTA's K-range -> MXFP8 codes in the 128-byte-swizzled
@@ -625,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t gd = sdesc_sf(base + L.sfb_off(0, 0));
     const uint32_t op_hi = static_cast<uint32_t>(wd >> 32), sf_hi = static_cast<uint32_t>(fd >> 32);
     const uint32_t stage_units = L.stage_bytes >> 4;
-    const uint32_t rt_units = (static_cast<uint32_t>(L.nmax) * kSfTileBytes) >> 4;
+    const uint32_t rt_units = (static_cast<uint32_t>(L.nmax * sf_tiles(kFmt)) * kSfTileBytes) >> 4;
     const uint32_t id0 = idesc_mxf8(p.mtile, 0), id1 = idesc_mxf8(p.mtile, 1);
     const uint32_t id2 = idesc_mxf8(p.mtile, 2), id3 = idesc_mxf8(p.mtile, 3);
     // every wait below is taken by all lanes and decided by a warp vote, so the
@@ -650,7 +663,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 1 && lane == 0) MX_TL(18, globaltimer());
         if (i == n - 1 && lane == 0) MX_TL(15, globaltimer());
         tc_fence_after();
-        if (elect_one()) {
+        if (kFmt != kFmtMx8 && elect_one()) {
+          const uint32_t w4_id = idesc_w4<kFmt == kFmtW4A4>(p.mtile, 0);
+          const int have = min(sf_tiles(kFmt), n_units - i * sf_tiles(kFmt));
+#pragma unroll
+          for (int u = 0; u < sf_tiles(kFmt); ++u) {
+            if (u < have) {
+              tmem_cp_32x128b_x4_lh(ta + 4 * u, f_lo + u * (kSfTileBytes >> 4), sf_hi);
+              tmem_cp_32x128b_x4_lh(tb + 4 * u * nsfb, g_lo + u * (kSfTileBytes >> 4), sf_hi);
+              if (nsfb > 1)
+                tmem_cp_32x128b_x4_lh(tb + 4 * u * nsfb + 4, g_lo + rt_units + u * (kSfTileBytes >> 4), sf_hi);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // .mxf8f6f4: scale byte j of the chunk's one tile; .mxf4: bytes 2 (j % 2) and the next of tile j / 2
+            const int u = kFmt == kFmtW4A4 ? j >> 1 : 0, byte = kFmt == kFmtW4A4 ? 2 * (j & 1) : j;
+            if (u < have)
+              mma_w4_lh<kFmt == kFmtW4A4>(tmem, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi,
+                                          w4_id + byte * ((1u << 4) | (1u << 29)), ta + 4 * u, tb + 4 * u * nsfb,
+                                          i != 0 || j != 0);
+          }
+          if (i + stages < n) tc_commit(empty_s);  // only stages that will be refilled
+        }
+        if (kFmt == kFmtMx8 && elect_one()) {
           tmem_cp_32x128b_x4_lh(ta, f_lo, sf_hi);
           tmem_cp_32x128b_x4_lh(tb, g_lo, sf_hi);
           if (nsfb > 1) tmem_cp_32x128b_x4_lh(tb + 4, g_lo + rt_units, sf_hi);
@@ -661,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i + stages < n) tc_commit(empty_s);  // only stages that will be refilled
         }
         __syncwarp();
-        f_lo += kSfTileBytes >> 4;
-        g_lo += kSfTileBytes >> 4;
+        f_lo += sf_tiles(kFmt) * kSfTileBytes >> 4;
+        g_lo += sf_tiles(kFmt) * kSfTileBytes >> 4;
         if (kFusedA) a_lo += L.a_bytes >> 4;  // resident tiles: one per chunk
         if (++s == stages) {
           s = 0;
@@ -676,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           w_lo += stage_units;
           if (!kFusedA) a_lo += stage_units;
-          ta += 4;
-          tb += 4 * nsfb;
+          ta += 4 * sf_tiles(kFmt);
+          tb += 4 * sf_tiles(kFmt) * nsfb;
           full_s += 8;
           empty_s += 8;
         }
@@ -1009,18 +1045,19 @@ PlanEnv read_plan_env() {
 }
 
 GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool fused_a, bool norm,
-                   int push_mode, bool table_depth) {
+                   int push_mode, bool table_depth, int w_fmt) {
   int force_splits, force_stages;
   plan_override(env.plan_at, N, K, &force_splits, &force_stages);
   const int mtile = (M + 15) & ~15;
   const int tiles = N / 128;
-  const int nchunks = K / 128;
+  const int sft = sf_tiles(w_fmt);
+  const int nchunks = (K / 128 + sft - 1) / sft;
   const int nsfb = (mtile + 127) / 128;
   const int xrows = std::min(M, kRowBatch);
   const int push_rows = env.push_rows >= 0 ? env.push_rows : kPushMaxRows;
   // the scale tiles of a CTA's K-range stay resident: at most 48 KB of them
   auto scale_bytes = [&](int sp) {
-    return static_cast<size_t>((nchunks + sp - 1) / sp) * kSfTileBytes * (1 + nsfb);
+    return static_cast<size_t>((nchunks + sp - 1) / sp) * sft * kSfTileBytes * (1 + nsfb);
   };
   // the plan for a given number of K splits
   auto plan_for = [&](int splits) {
@@ -1029,7 +1066,7 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     while (splits < std::min(8, nchunks) && scale_bytes(splits) > 48 * 1024) ++splits;
     pl.splits = splits;
     const int per_cta = (nchunks + splits - 1) / splits;
-    const Layout L1(mtile, 1, per_cta, fused_a, xrows, norm ? K / 32 : 0);
+    const Layout L1(mtile, 1, per_cta, fused_a, xrows, norm ? K / 32 : 0, 0, sft);
     // resident per CTA besides the ring: scale tiles (and, fused, the activation
     // tiles and the bf16 staging rows)
     const size_t scales = L1.bars - L1.ring_bytes;
@@ -1048,16 +1085,16 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     while (static_cast<size_t>(stages) * L1.stage_bytes + scales < static_cast<size_t>(mtile) * 512)
       ++stages;
     pl.stages = stages;
-    pl.tmem_cols = pow2_at_least(tmem_sfa_col(mtile) + 4 * stages * (1 + nsfb));
+    pl.tmem_cols = pow2_at_least(tmem_sfa_col(mtile) + 4 * sft * stages * (1 + nsfb));
     // the push reduction (where asked for and its receive area fits)
     const uint32_t area = push_area_bytes(M, splits, push_mode == kPushCompact);
     const bool push = push_mode != kPushNone && M <= push_rows &&
-                      Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area).total() <=
+                      Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area, sft).total() <=
                           kMaxDynamicSmem;
     pl.reduction = !push                         ? (row_reduction(M, splits) ? kReduceRows : kReduceItems)
                    : push_mode == kPushCompact ? kReducePushCompact
                                                : kReducePush;
-    const Layout L(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, push ? area : 0u);
+    const Layout L(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, push ? area : 0u, sft);
     // CTAs that can share an SM must fit their TMEM together: ask for enough
     // shared memory that at most 512 / tmem_cols of them are resident.
     const int max_res = 512 / pl.tmem_cols;
@@ -1067,10 +1104,15 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
   };
   int splits = std::max(1, sm_count / std::max(tiles, 1));
   // the table was measured with 152 SMs; other parts keep the SM-count rule
-  const SplitEntry* te = sm_count == 152 ? table_entry(M, N, K) : nullptr;
+  const SplitEntry* te = sm_count == 152 && w_fmt == kFmtMx8 ? table_entry(M, N, K) : nullptr;
   if (te != nullptr) splits = te->splits;
   if (te != nullptr && force_stages == 0 && table_depth) force_stages = te->stages;
   splits = std::min(splits, std::min(8, nchunks));
+  // MXFP4 weights halve the stream that more splits would shorten: six at most, and
+  // from 65 rows four (whole-row reduction). Measured on GB300, N = 2048, K = 5120, us
+  // with 4 / 6 / 8 splits: 6.7 / 5.9 / 6.7 at one row, 8.4 / 8.0 / 8.2 at 64, 9.8 /
+  // 10.5 / 10.1 at 128, 12.6 / 14.5 / 23.4 at 256.
+  if (w_fmt != kFmtMx8) splits = std::min(splits, M > 64 ? 4 : 6);
   bool forced = false;
   if (env.splits > 0) {
     splits = std::min(env.splits, nchunks);
@@ -1091,7 +1133,13 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
 }
 
 cudaError_t set_gemm_attributes() {
-  const void* ks[16] = {
+  const void* ks[22] = {
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems, kFmtW4A8>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A8>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReducePush, kFmtW4A8>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems, kFmtW4A4>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A4>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReducePush, kFmtW4A4>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems>),
       reinterpret_cast<const void*>(&gemm_kernel<true, false, kReduceItems>),
       reinterpret_cast<const void*>(&gemm_kernel<false, true, kReduceItems>),
@@ -1149,6 +1197,10 @@ cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const 
   auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, args); };
   auto pick = [&](auto red) {
     constexpr int R = decltype(red)::value;
+    if constexpr (R != kReducePushCompact) {
+      if (args.w_fmt == kFmtW4A8) return go(gemm_kernel<false, false, R, kFmtW4A8>);
+      if (args.w_fmt == kFmtW4A4) return go(gemm_kernel<false, false, R, kFmtW4A4>);
+    }
     if (fx) return rq ? go(gemm_kernel<true, true, R>) : go(gemm_kernel<false, true, R>);
     return rq ? go(gemm_kernel<true, false, R>) : go(gemm_kernel<false, false, R>);
   };

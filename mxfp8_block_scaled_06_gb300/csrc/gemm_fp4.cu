@@ -135,7 +135,9 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     prefetch_tmap(&tm_a);
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+  pdl_launch_dependents();
   if (warp == 1) {
+    if (p.offsets != nullptr) pdl_wait();
     // the experts' rows, clamped to the output, and the tiles before each expert
     const int ntiles = p.N >> 7;
     int run = 0;
@@ -165,6 +167,9 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // nothing that an earlier kernel may have written is read, and nothing written,
+  // before the wait; with early_weights warp 0 starts on the weights without it
+  if (warp != 0 || !p.early_weights) pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const Table table{cum, off, p.E, p.nt};
   const int total = cum[p.E];
@@ -499,8 +504,17 @@ cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, co
   const bool gather = args.tokens != nullptr;
   if (plan.smem > kMaxDynamicSmem || plan.stages < 3) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
-    kernel<<<plan.grid, kThreads + (gather ? kGatherThreads : 0), plan.smem, stream>>>(tm_w, tm_a, args);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.grid);
+    cfg.blockDim = dim3(kThreads + (gather ? kGatherThreads : 0));
+    cfg.dynamicSmemBytes = plan.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, args);
   };
   auto pick = [&](auto small) {
     constexpr bool S = decltype(small)::value;

@@ -88,6 +88,7 @@ struct GemmNorm {
 
 struct GemmArgs {
   int M, N, K;
+  int w_fmt;  // 0: MXFP8 weights, 1: MXFP4 weights and MXFP8 activations, 2: both MXFP4
   int mtile, stages, nchunks, tmem_cols;
   const uint8_t* a_scales;  // MXFP8 activations' swizzled scales (unused when x is set)
   const uint8_t* w_scales;
@@ -125,9 +126,10 @@ constexpr int kTimelineCtas = 512;
 
 // fused_a: bf16 activations quantized in the kernel; norm: with the RMS norm;
 // push_mode: whether the push reduction may be chosen, and its receive area;
-// table_depth: the ring depth of the split table's row (false: as planned).
+// table_depth: the ring depth of the split table's row (false: as planned);
+// w_fmt as in GemmArgs (MXFP4 weights: neither fused_a nor a compact push area).
 GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool fused_a = false,
-                   bool norm = false, int push_mode = kPushFull, bool table_depth = true);
+                   bool norm = false, int push_mode = kPushFull, bool table_depth = true, int w_fmt = 0);
 cudaError_t set_gemm_attributes();
 cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmArgs& args,
                         const GemmPlan& plan, bool pdl, cudaStream_t stream);
@@ -250,6 +252,7 @@ struct GemmFp4Args {
   const int* offsets;       // device, [E + 1]; null: one expert of R rows
   const int* tokens;        // device, [R], or null
   int gated;                // out [R, N / 2] = silu(column 2i) * column 2i + 1
+  int early_weights;        // weights are read before the previous kernel has ended (offsets null)
   __nv_bfloat16* out;
   int* status;
 };
