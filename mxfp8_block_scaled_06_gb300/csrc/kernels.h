@@ -271,7 +271,7 @@ enum Scoring : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 constexpr int kRouteMaxExperts = 512;
 constexpr int kRouteMaxTopK = 32;
 constexpr int kRouteChunks = 512;   // chunks of tokens whose rows are counted apart
-constexpr int kRouteMinChunk = 32;  // tokens of a chunk, at least
+constexpr int kRouteOneBlock = 16;  // tokens that one block routes and orders
 // the handle's workspace: rows per (expert, chunk), rows per expert
 constexpr size_t kRouteWorkspace = sizeof(int) * (static_cast<size_t>(kRouteMaxExperts) * kRouteChunks + kRouteMaxExperts);
 
@@ -292,6 +292,7 @@ struct RouteArgs {
   int* totals;     // workspace [E]
   // set by launch_route
   int chunk, chunks, group_parts, shared_keys;
+  FastDiv per_group;
 };
 cudaError_t launch_route(RouteArgs args, cudaStream_t stream);
 

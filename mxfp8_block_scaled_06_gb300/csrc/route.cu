@@ -14,16 +14,16 @@
 // order is the logits' order and the logits themselves are compared. With a bias
 // the keys are float32 sums with a known error; whenever two neighbours of the
 // selection, the last one taken and one left out, or the last chosen and the
-// first rejected group are closer than their errors, the token is done again in
-// float64. With 256 experts that is a few tokens in a thousand.
+// first rejected group are closer than their errors, the keys in question are
+// computed again in float64. With 256 experts that is a few tokens in a thousand.
 //
 // Masked logits: -inf and NaN logits have score 0 and are chosen last; +inf
 // counts as the largest float. When every chosen score is 0 so are the weights.
 //
 // Row order: the tokens are cut into at most kRouteChunks chunks; each chunk
-// counts its rows per expert, one warp per expert turns the chunks' counts into
-// starts, and each chunk places its rows in (token, choice) order, so the order is
-// the stable one whatever the launch (integer sums only).
+// counts its rows per expert and numbers them in (token, choice) order, one warp per
+// expert turns the chunks' counts into starts, and a third kernel adds the two, so
+// the order is the stable one whatever the launch (integer sums only).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -58,6 +58,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// n / d for the d that f was made for (fast_div).
+__device__ __forceinline__ uint32_t div_u32(uint32_t n, FastDiv f) {
+  const uint32_t t = __umulhi(f.mul, n);
+  return f.shift < 0 ? n : (t + ((n - t) >> 1)) >> f.shift;
+}
+
 // Keeps the two largest of (a1 >= a2) and (b1 >= b2) in a1, a2.
 template <typename F>
 __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
@@ -84,66 +90,55 @@ __device__ __forceinline__ float key_error(const RouteArgs& p, const Token& t, f
   return (s > 0.f ? s * d * 1.2e-7f : 0.f) + fabsf(key) * 1.2e-7f + 1e-37f;
 }
 
-// Groups in the order of their best keys: a bit mask of the topk_groups first.
-// keys: the warp's E keys in shared memory. best = the largest key of a group, or
-// with a bias the sum of its two largest. Sets *close when the last group in and
-// the first one out differ by no more than err.
-template <typename F>
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, const volatile F* keys, F err, bool* close) {
-  const int lane = threadIdx.x & 31;
-  const int parts = p.group_parts;  // lanes per group, a power of two
-  const int g = lane / parts, part = lane & (parts - 1);
-  const int size = p.E / p.n_groups;
-  F a1 = -CUDART_INF_F, a2 = -CUDART_INF_F;
-  if (g < p.n_groups)
-    for (int e = part; e < size; e += parts) merge_top2<F>(a1, a2, keys[g * size + e], -CUDART_INF_F);
-  for (int o = 1; o < parts; o <<= 1) {
-    const F b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-    merge_top2<F>(a1, a2, b1, b2);
-  }
-  const F best = p.bias == nullptr || size == 1 ? a1 : a1 + a2;
-  int rank = 0;
-  for (int j = 0; j < p.n_groups; ++j) {
-    const F b = __shfl_sync(kFull, best, j * parts);
-    rank += b > best || (b == best && j < g);
-  }
-  const bool mine = g < p.n_groups && part == 0;
-  const uint32_t in = __ballot_sync(kFull, mine && rank < p.topk_groups);
-  const uint32_t last = __ballot_sync(kFull, mine && rank == p.topk_groups - 1);
-  const uint32_t next = __ballot_sync(kFull, mine && rank == p.topk_groups);
-  if (next != 0) {
-    const F x = __shfl_sync(kFull, best, __ffs(last) - 1), y = __shfl_sync(kFull, best, __ffs(next) - 1);
-    if (y > -CUDART_INF_F && !(x - y > err)) *close = true;
-  }
-  uint32_t mask = 0;
-  for (int j = 0; j < p.n_groups; ++j) mask |= (in >> (j * parts) & 1u) << j;
-  return mask;
+// The parts of a token's selection in float64, for keys that float32 cannot tell
+// apart; out of line, as few tokens come here. float64 is slow on this GPU (a warp
+// instruction takes about 16 cycles), so only the keys in question are computed,
+// one to a lane.
+
+// Sum of exp(x - top) over the token's experts in float64 (softmax; 1 otherwise).
+__device__ __noinline__ double sum64(const RouteArgs& p, size_t base, float top) {
+  if (p.scoring == kScoreSigmoid) return 1.0;
+  double sum = 0;
+  for (int e = threadIdx.x & 31; e < p.E; e += 32)
+    sum += exp(static_cast<double>(load_logit(p.logits, base + e, p.bf16)) - top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  return sum;
 }
 
-// The token's selection in float64, for keys too close for float32: lane j < top_k
-// returns the j-th expert. keys: the warp's shared memory.
-__device__ __noinline__ int select64(const RouteArgs& p, size_t token, volatile double* keys) {
+__device__ __forceinline__ double key64(const RouteArgs& p, size_t base, int e, float top, double sum) {
+  const double x = load_logit(p.logits, base + e, p.bf16);
+  const float b = p.bias[e];
+  if (x == -CUDART_INF || isnan(b)) return -CUDART_INF;
+  return (p.scoring == kScoreSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum) + static_cast<double>(b);
+}
+
+// Lane i < n holds one of n candidates (expert e): the candidate of rank lane by
+// (key, then lowest index) to every lane < n.
+__device__ __noinline__ int order64(const RouteArgs& p, size_t base, int e, int n, float top, volatile int* list) {
   const int lane = threadIdx.x & 31;
-  const size_t base = token * static_cast<size_t>(p.ldl);
-  double top = -CUDART_INF, sum = 0;
-  for (int e = lane; e < p.E; e += 32) top = fmax(top, static_cast<double>(load_logit(p.logits, base + e, p.bf16)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
-  if (p.scoring == kScoreSoftmax && top > -CUDART_INF) {
-    for (int e = lane; e < p.E; e += 32) sum += exp(static_cast<double>(load_logit(p.logits, base + e, p.bf16)) - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  const double sum = sum64(p, base, top);
+  const double k = lane < n ? key64(p, base, e, top, sum) : 0.0;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double kj = __shfl_sync(kFull, k, j);
+    const int ej = __shfl_sync(kFull, e, j);
+    rank += kj > k || (kj == k && ej < e);
   }
   __syncwarp();
-  for (int e = lane; e < p.E; e += 32) {
-    const double x = load_logit(p.logits, base + e, p.bf16);
-    const double s = p.scoring == kScoreSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
-    keys[e] = x == -CUDART_INF || isnan(p.bias[e]) ? -CUDART_INF : s + static_cast<double>(p.bias[e]);
-  }
+  if (lane < n) list[rank] = e;
   __syncwarp();
-  uint32_t open = kFull;
-  bool close = false;
-  if (p.n_groups > 1) open = choose_groups<double>(p, keys, 0.0, &close);
+  return list[lane < n ? lane : 0];
+}
+
+// The whole token in float64, where more than 32 keys are in question: lane j <
+// top_k returns the j-th expert of the open groups. keys: the warp's shared memory.
+__device__ __noinline__ int select64(const RouteArgs& p, size_t base, float top, uint32_t open, volatile double* keys) {
+  const int lane = threadIdx.x & 31;
+  const double sum = sum64(p, base, top);
+  __syncwarp();
+  for (int e = lane; e < p.E; e += 32) keys[e] = key64(p, base, e, top, sum);
+  __syncwarp();
   const int size = p.E / p.n_groups;
   int mine = 0;
   // each round takes the largest (key, then lowest index) after the last one taken
@@ -154,7 +149,7 @@ __device__ __noinline__ int select64(const RouteArgs& p, size_t token, volatile 
     int at = p.E;
     for (int e = lane; e < p.E; e += 32) {
       const double v = keys[e];
-      if (p.n_groups > 1 && !(open >> (e / size) & 1u)) continue;
+      if (!(open >> (e / size) & 1u)) continue;
       if (v > last || (v == last && e <= last_e)) continue;
       if (at == p.E || v > k) k = v, at = e;
     }
@@ -171,19 +166,101 @@ __device__ __noinline__ int select64(const RouteArgs& p, size_t token, volatile 
   return mine;
 }
 
+// The chosen groups when the float32 sums of `contended` groups (a bit mask) are too
+// close: `in` of the groups outside it are chosen already. With each contended
+// group's keys that may be among its two largest (at least `floor`, float32) in
+// float64, its exact sum; the largest sums fill the places left.
+__device__ __noinline__ uint32_t groups64(const RouteArgs& p, size_t base, float top, uint32_t in, uint32_t contended,
+                                          const volatile float* keys32, float far) {
+  const int lane = threadIdx.x & 31;
+  const int size = p.E / p.n_groups;
+  const double sum = sum64(p, base, top);
+  double best = -CUDART_INF;  // lane g: the sum of contended group g
+  for (uint32_t left = contended; left != 0; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    float a1 = -CUDART_INF_F, a2 = -CUDART_INF_F;
+    for (int e = lane; e < size; e += 32) merge_top2<float>(a1, a2, keys32[g * size + e], -CUDART_INF_F);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+      merge_top2<float>(a1, a2, b1, b2);
+    }
+    const float floor = (size == 1 ? a1 : a2) - 2.f * far;
+    double d1 = -CUDART_INF, d2 = -CUDART_INF;
+    for (int e = lane; e < size; e += 32)
+      if (!(keys32[g * size + e] < floor))
+        merge_top2<double>(d1, d2, key64(p, base, g * size + e, top, sum), -CUDART_INF);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double b1 = __shfl_xor_sync(kFull, d1, o), b2 = __shfl_xor_sync(kFull, d2, o);
+      merge_top2<double>(d1, d2, b1, b2);
+    }
+    if (lane == g) best = size == 1 ? d1 : d1 + d2;
+  }
+  int rank = 0;
+  for (uint32_t left = contended; left != 0; left &= left - 1) {
+    const int j = __ffs(left) - 1;
+    const double b = __shfl_sync(kFull, best, j);
+    rank += b > best || (b == best && j < lane);
+  }
+  return in | __ballot_sync(kFull, (contended >> lane & 1u) && rank < p.topk_groups - __popc(in));
+}
+
+// The topk_groups groups of the largest key, or with a bias the largest sum of two
+// keys, as a bit mask. keys: the warp's E keys in shared memory, each off by `far`
+// at most.
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t base, float top,
+                                                  const volatile float* keys, float far) {
+  const int lane = threadIdx.x & 31;
+  const int parts = p.group_parts;  // lanes per group, a power of two
+  const int g = lane / parts, part = lane & (parts - 1);
+  const int size = p.E / p.n_groups;
+  float a1 = -CUDART_INF_F, a2 = -CUDART_INF_F;
+  if (g < p.n_groups)
+    for (int e = part; e < size; e += parts) merge_top2<float>(a1, a2, keys[g * size + e], -CUDART_INF_F);
+  for (int o = 1; o < parts; o <<= 1) {
+    const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+    merge_top2<float>(a1, a2, b1, b2);
+  }
+  // lane j: group j's best
+  const float whole = p.bias == nullptr || size == 1 ? a1 : a1 + a2;
+  const float best = lane < p.n_groups ? __shfl_sync(kFull, whole, lane * parts) : __shfl_sync(kFull, whole, 0);
+  int rank = 0;
+  for (int j = 0; j < p.n_groups; ++j) {
+    const float b = __shfl_sync(kFull, best, j);
+    rank += b > best || (b == best && j < lane);
+  }
+  const bool mine = lane < p.n_groups;
+  const uint32_t in = __ballot_sync(kFull, mine && rank < p.topk_groups);
+  const uint32_t next = __ballot_sync(kFull, mine && rank == p.topk_groups);
+  if (p.bias == nullptr || next == 0) return in;
+  // the last one in and the first one out, and whatever is within reach of either:
+  // two sums are off by 2 far each and round once
+  const uint32_t last = __ballot_sync(kFull, mine && rank == p.topk_groups - 1);
+  const float x = __shfl_sync(kFull, best, __ffs(last) - 1), y = __shfl_sync(kFull, best, __ffs(next) - 1);
+  const float err = 6.f * far;
+  if (!(y > -CUDART_INF_F) || x - y > err) return in;
+  const uint32_t contended = __ballot_sync(kFull, mine && !(best - x > err) && !(y - best > err));
+  return groups64(p, base, top, in & ~contended, contended, keys, far);
+}
+
 // The selection of one token: lane j < top_k returns the j-th expert and its weight.
+// shared: the warp's shared memory (route_shared_bytes).
 template <int V>  // keys per lane
-__device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, const float (&bias)[V],
-                                            const int (&group)[V], double* shared, int* expert, float* weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, const float (&bias)[V], double* shared,
+                                            int* expert, float* weight) {
   const int lane = threadIdx.x & 31;
   const size_t base = token * static_cast<size_t>(p.ldl);
   float x[V];
+  if (p.bf16) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    x[i] = e < p.E ? load_logit(p.logits, base + e, p.bf16) : -CUDART_INF_F;
+    for (int i = 0; i < V; ++i) x[i] = lane + 32 * i < p.E ? load_logit(p.logits, base + lane + 32 * i, 1) : -CUDART_INF_F;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = lane + 32 * i < p.E ? load_logit(p.logits, base + lane + 32 * i, 0) : -CUDART_INF_F;
   }
   Token t{0.f, 1.f};
+  float s[V];  // scores (needed for the keys with a bias only)
   if (p.scoring == kScoreSoftmax) {
     float top = x[0];
 #pragma unroll
@@ -193,24 +270,32 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     float sum = 0.f;
     if (t.top > -CUDART_INF_F) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += expf(x[i] - t.top);
+      for (int i = 0; i < V; ++i) {
+        s[i] = expf(x[i] - t.top);
+        sum += s[i];
+      }
     }
     t.sum = warp_sum(sum);
   }
   uint32_t key[V];
   float far = 0.f;  // the largest error of the token's keys
+  if (p.bias == nullptr) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float k = x[i];
-    if (p.bias != nullptr && k > -CUDART_INF_F) {
-      const float s = score32(p, t, x[i]);
-      k = isnan(bias[i]) ? -CUDART_INF_F : s + bias[i];
-      if (k > -CUDART_INF_F) far = fmaxf(far, key_error(p, t, x[i], s, k));
+    for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < p.E ? ord32(x[i] + 0.f) : 0u;  // + 0: -0 and 0 are the same key
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float k = x[i];
+      if (k > -CUDART_INF_F) {
+        const float sc = p.scoring == kScoreSigmoid ? 1.f / (1.f + expf(-x[i])) : s[i] / t.sum;
+        k = isnan(bias[i]) ? -CUDART_INF_F : sc + bias[i];
+        if (k > -CUDART_INF_F) far = fmaxf(far, key_error(p, t, x[i], sc, k));
+      }
+      key[i] = lane + 32 * i < p.E ? ord32(k + 0.f) : 0u;
     }
-    key[i] = lane + 32 * i < p.E ? ord32(k + 0.f) : 0u;  // + 0: -0 and 0 are the same key
+    far = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(far)));
   }
-  far = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(far)));
-  bool close = false;
+  uint32_t open = kFull;
   if (p.n_groups > 1) {
     volatile float* const keys = reinterpret_cast<volatile float*>(shared);
     __syncwarp();
@@ -218,46 +303,66 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     for (int i = 0; i < V; ++i)
       if (lane + 32 * i < p.E) keys[lane + 32 * i] = unord32(key[i]);
     __syncwarp();
-    // a group's sum has at most twice the largest error, and rounds once more;
-    // without a bias the keys are exact
-    const uint32_t open = choose_groups<float>(p, keys, p.bias == nullptr ? -1.f : 6.f * far, &close);
+    open = choose_groups(p, base, t.top, keys, far);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (!(open >> group[i] & 1u)) key[i] = 0u;  // no round takes a closed expert
+      if (!(open >> div_u32(lane + 32 * i, p.per_group) & 1u)) key[i] = 0u;  // no round takes a closed expert
   }
   int mine = 0;
   uint32_t last = 0;  // the previous round's key; its expert
   int last_e = 0;
-  for (int j = 0; j < p.top_k && !close; ++j) {
+  bool close = false;
+  for (int j = 0; j < p.top_k; ++j) {
     uint32_t k = key[0];
-    int at = lane;
+    int at = 0;
 #pragma unroll
     for (int i = 1; i < V; ++i)
-      if (key[i] > k) k = key[i], at = lane + 32 * i;
+      if (key[i] > k) k = key[i], at = i;
     const uint32_t best = __reduce_max_sync(kFull, k);
-    const int e = static_cast<int>(__reduce_min_sync(kFull, k == best ? static_cast<uint32_t>(at) : 0xFFFFu));
+    const uint32_t e = __reduce_min_sync(kFull, k == best ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFu);
     // neighbours of the selection that float32 cannot tell apart, unless they are a
     // true tie (the same logit and bias), which the lowest index has won
     if (p.bias != nullptr && j > 0 && best > ord32(-CUDART_INF_F) && !(unord32(last) - unord32(best) > 2.f * far))
-      close = load_logit(p.logits, base + last_e, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
-              p.bias[last_e] != p.bias[e];
+      close |= load_logit(p.logits, base + last_e, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
+               p.bias[last_e] != p.bias[e];
     if (lane == j) mine = e;
+    const int own = (e & 31) == lane ? static_cast<int>(e >> 5) : -1;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i == e) key[i] = 0u;
+      if (i == own) key[i] = 0u;
     last = best;
     last_e = e;
   }
-  if (p.bias != nullptr && last > ord32(-CUDART_INF_F)) {
+  if (p.bias != nullptr) {
     // and whatever was left out that may belong before the last one taken
-    const float least = unord32(last) - 2.f * far;
+    const bool masked = last <= ord32(-CUDART_INF_F);
+    const uint32_t least = masked ? 0xFFFFFFFFu : ord32(unord32(last) - 2.f * far);
     const float xl = load_logit(p.logits, base + last_e, p.bf16), bl = p.bias[last_e];
     bool near = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) near |= key[i] != 0u && !(unord32(key[i]) < least) && (x[i] != xl || bias[i] != bl);
-    close |= __any_sync(kFull, near) != 0;
+    for (int i = 0; i < V; ++i) near |= key[i] >= least && (x[i] != xl || bias[i] != bl);
+    if (__any_sync(kFull, near || close)) {
+      // the candidates: the ones taken, and these
+      volatile int* const list = reinterpret_cast<volatile int*>(shared);
+      __syncwarp();
+      if (lane < p.top_k) list[lane] = mine;
+      int n = p.top_k;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t m = __ballot_sync(kFull, key[i] >= least);
+        const int at = n + __popc(m & ((1u << lane) - 1));
+        if ((m >> lane & 1u) && at < 32) list[at] = lane + 32 * i;
+        n += __popc(m);
+      }
+      __syncwarp();
+      if (n <= 32) {
+        const int c = list[lane < n ? lane : 0];
+        mine = order64(p, base, c, n, t.top, list);
+      } else {
+        mine = select64(p, base, t.top, open, shared);
+      }
+    }
   }
-  if (close) mine = select64(p, token, shared);
   float w = 0.f;
   if (lane < p.top_k) {
     const float xm = load_logit(p.logits, base + mine, p.bf16);
@@ -271,70 +376,77 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
   *weight = w * p.scale;
 }
 
-// v[0..n) become the sums of the values before each, by one warp; returns the sum of all.
+// v[0..n) become the sums of the values before each, by one warp; returns the sum of
+// all. n <= 512; the loads are issued together.
 __device__ __forceinline__ int exclusive_scan(int* v, int n) {
   const int lane = threadIdx.x & 31;
+  int own[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) own[i] = 32 * i + lane < n ? v[32 * i + lane] : 0;
   int run = 0;
-  for (int e0 = 0; e0 < n; e0 += 32) {
-    const int own = e0 + lane < n ? v[e0 + lane] : 0;
-    int s = own;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (32 * i >= n) break;
+    int s = own[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(kFull, s, o);
       if (lane >= o) s += up;
     }
-    if (e0 + lane < n) v[e0 + lane] = run + s - own;
+    if (32 * i + lane < n) v[32 * i + lane] = run + s - own[i];
     run += __shfl_sync(kFull, s, 31);
   }
   __syncwarp();
   return run;
 }
 
-// Places the rows [r0, r1) in (token, choice) order, by one warp; base[e] (shared
-// memory) is the next free row of expert e.
-__device__ __forceinline__ void place_rows(const RouteArgs& p, int r0, int r1, int* base) {
+// The places of the rows [r0, r1) in (token, choice) order, by one warp: slots[r] =
+// base[its expert]++ (base in shared memory); with tokens also the token behind each place.
+__device__ __forceinline__ void place_rows(const RouteArgs& p, int r0, int r1, int* base, bool tokens) {
   const int lane = threadIdx.x & 31;
-  for (int r = r0; r < r1; r += 32) {
-    const bool in = r + lane < r1;
-    const int e = in ? p.experts[r + lane] : -1;
-    const uint32_t peers = __match_any_sync(kFull, e);
-    const int before = __popc(peers & ((1u << lane) - 1));
-    const int at = in ? base[e] + before : 0;
-    __syncwarp();
-    if (in && before == 0) base[e] = at + __popc(peers);
-    __syncwarp();
-    if (in) {
-      p.slots[r + lane] = at;
-      p.tokens[at] = (r + lane) / p.top_k;
+  constexpr int kAhead = 8;
+  for (int b = r0; b < r1; b += 32 * kAhead) {
+    int expert[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) expert[i] = b + 32 * i + lane < r1 ? p.experts[b + 32 * i + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = b + 32 * i + lane, e = expert[i];
+      if (b + 32 * i >= r1) break;
+      const uint32_t peers = __match_any_sync(kFull, e);
+      const int before = __popc(peers & ((1u << lane) - 1));
+      const int at = e >= 0 ? base[e] + before : 0;
+      __syncwarp();
+      if (e >= 0 && before == 0) base[e] = at + __popc(peers);
+      __syncwarp();
+      if (e >= 0) {
+        p.slots[r] = at;
+        if (tokens) p.tokens[at] = r / p.top_k;
+      }
     }
   }
 }
 
-// One block per chunk of tokens: the selection, and the chunk's rows per expert
-// (counts[e][chunk]). With a single chunk the block also orders the rows.
+// One block per chunk of tokens: the selection, the chunk's rows per expert
+// (counts[e][chunk]) and each row's place among the chunk's rows of its expert
+// (slots). With a single chunk that place is the row's.
 template <int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_constant__ RouteArgs p) {
+__global__ void __launch_bounds__(kRouteWarps * 32, 4) route_kernel(const __grid_constant__ RouteArgs p) {
   extern __shared__ double route_smem[];
-  int* const hist = reinterpret_cast<int*>(route_smem + (p.shared_keys ? kRouteWarps * p.E : 0));
+  int* const hist = reinterpret_cast<int*>(route_smem + kRouteWarps * p.shared_keys);
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  double* const keys = route_smem + (p.shared_keys ? warp * p.E : 0);
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
   pdl_wait();
   float bias[V];
-  int group[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
-    group[i] = p.n_groups > 1 && e < p.E ? e / (p.E / p.n_groups) : 0;
-  }
+  for (int i = 0; i < V; ++i) bias[i] = p.bias != nullptr && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.f;
   __syncthreads();
-  const int t1 = min(p.T, static_cast<int>(blockIdx.x + 1) * p.chunk);
-  for (int t = blockIdx.x * p.chunk + warp; t < t1; t += kRouteWarps) {
+  const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  for (int t = t0 + warp; t < t1; t += kRouteWarps) {
     int e;
     float w;
-    route_token<V>(p, t, bias, group, keys, &e, &w);
+    route_token<V>(p, t, bias, route_smem + warp * p.shared_keys, &e, &w);
     if (lane < p.top_k) {
       const size_t r = static_cast<size_t>(t) * p.top_k + lane;
       p.experts[r] = e;
@@ -344,15 +456,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const __grid_co
   }
   __syncthreads();
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.counts[e * p.chunks + blockIdx.x] = hist[e];
-    return;
-  }
-  if (warp == 0) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      p.counts[e * p.chunks + blockIdx.x] = hist[e];
+      hist[e] = 0;
+    }
+    __syncthreads();
+    if (warp == 0) place_rows(p, t0 * p.top_k, t1 * p.top_k, hist, false);
+  } else if (warp == 0) {
     const int rows = exclusive_scan(hist, p.E);
     for (int e = lane; e < p.E; e += 32) p.offsets[e] = hist[e];
     if (lane == 0) p.offsets[p.E] = rows;
     __syncwarp();
-    place_rows(p, 0, rows, hist);
+    place_rows(p, 0, rows, hist, true);
   }
 }
 
@@ -367,25 +482,31 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_scan_kernel(const __gr
   if ((threadIdx.x & 31) == 0) p.totals[e] = total;
 }
 
-// One warp per chunk: its rows into expert order.
-__global__ void __launch_bounds__(32) route_place_kernel(const __grid_constant__ RouteArgs p) {
+// One block per chunk: its rows' places among all rows.
+__global__ void __launch_bounds__(kRouteWarps * 32) route_place_kernel(const __grid_constant__ RouteArgs p) {
   extern __shared__ double route_smem[];
   int* const base = reinterpret_cast<int*>(route_smem);
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x;
-  for (int e = lane; e < p.E; e += 32) base[e] = p.totals[e];
-  __syncwarp();
-  const int rows = exclusive_scan(base, p.E);
-  if (blockIdx.x == 0) {
-    for (int e = lane; e < p.E; e += 32) p.offsets[e] = base[e];
-    if (lane == 0) p.offsets[p.E] = rows;
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) base[e] = p.totals[e];
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int rows = exclusive_scan(base, p.E);
+    if (blockIdx.x == 0) {
+      for (int e = threadIdx.x; e < p.E; e += 32) p.offsets[e] = base[e];
+      if (threadIdx.x == 0) p.offsets[p.E] = rows;
+    }
   }
-  __syncwarp();
-  for (int e = lane; e < p.E; e += 32) base[e] += p.counts[static_cast<size_t>(e) * p.chunks + blockIdx.x];
-  __syncwarp();
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
+    base[e] += p.counts[static_cast<size_t>(e) * p.chunks + blockIdx.x];
+  __syncthreads();
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  place_rows(p, t0 * p.top_k, t1 * p.top_k, base);
+  for (int r = t0 * p.top_k + threadIdx.x; r < t1 * p.top_k; r += blockDim.x) {
+    const int at = base[p.experts[r]] + p.slots[r];
+    p.slots[r] = at;
+    p.tokens[at] = r / p.top_k;
+  }
 }
 
 // out[t] = sum over j of weights[t][j] y[slots[t][j]] (+ residual[t]) in float32,
@@ -458,14 +579,16 @@ cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, int threads, size_t smem
 }  // namespace
 
 cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
-  // tokens per chunk: at least kRouteMinChunk (one block then does everything up
-  // to that many tokens), at most kRouteChunks chunks
-  p.chunk = std::max(kRouteMinChunk, (p.T + kRouteChunks - 1) / kRouteChunks);
+  // tokens per chunk: one block does everything up to kRouteOneBlock tokens; beyond,
+  // a token to a warp, and at most kRouteChunks chunks
+  p.chunk = p.T <= kRouteOneBlock ? p.T : std::max(kRouteWarps, (p.T + kRouteChunks - 1) / kRouteChunks);
   p.chunks = (p.T + p.chunk - 1) / p.chunk;
   p.group_parts = 32;
   while (p.group_parts * p.n_groups > 32) p.group_parts >>= 1;
-  p.shared_keys = p.n_groups > 1 || p.bias != nullptr;
-  const size_t smem = (p.shared_keys ? sizeof(double) * kRouteWarps * p.E : 0) + sizeof(int) * p.E;
+  p.per_group = fast_div(p.E / p.n_groups);
+  // per warp: its keys, or two lists of 32 candidates
+  p.shared_keys = p.n_groups > 1 || p.bias != nullptr ? std::max(p.E, 32) : 0;
+  const size_t smem = sizeof(double) * kRouteWarps * p.shared_keys + sizeof(int) * p.E;
   const dim3 grid(p.chunks);
   const int threads = kRouteWarps * 32;
   cudaError_t e;
@@ -477,7 +600,7 @@ cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
   if (e != cudaSuccess || p.chunks == 1) return e;
   e = launch_pdl(route_scan_kernel, dim3((p.E + kRouteWarps - 1) / kRouteWarps), threads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(route_place_kernel, grid, 32, sizeof(int) * p.E, stream, p);
+  return launch_pdl(route_place_kernel, grid, threads, sizeof(int) * p.E, stream, p);
 }
 
 cudaError_t launch_combine(const CombineArgs& p, cudaStream_t stream) {
