@@ -5,10 +5,13 @@
 // to the lowest index), weights s_j / sum s_j * scale, and the order of all
 // (token, choice) rows by expert for a grouped product.
 //
-// One warp per token; lane l holds experts l, l + 32, ... in registers. A key is
-// compared as an order-preserving 32-bit pattern, so one round of the selection
-// is a scan over the lane's keys and two warp reductions (the largest key, then
-// the lowest index that has it).
+// One warp per token; lane l holds experts l, l + 32, ... in registers, their keys as
+// order-preserving 32-bit patterns. The top_k-th largest of the lanes' largest keys
+// bounds the selection from below; the few keys at or above it (with a bias: or
+// within the keys' error of it) are gathered one to a lane and ranked by counting.
+// Rounds of a scan over each lane's keys and two warp reductions, one round for
+// each choice, took twice the instructions (1945 against about 1000 a token with 256
+// experts, eight groups and a bias; 60 % of the issue slots were busy).
 //
 // The selection is the one that exact scores give. Without a bias the scores'
 // order is the logits' order and the logits themselves are compared. With a bias
@@ -81,13 +84,18 @@ __device__ __forceinline__ float score32(const RouteArgs& p, const Token& t, flo
   return t.sum > 0.f ? expf(x - t.top) / t.sum : 0.f;
 }
 
-// Bound of |computed key - exact key| of score32(x) + bias in float32: expf is
-// within 2 units in the last place, x - top is rounded once (an error that exp
-// multiplies by the score), the sum of E <= 512 terms and the division add a few
-// more, and the addition rounds the key once.
-__device__ __forceinline__ float key_error(const RouteArgs& p, const Token& t, float x, float s, float key) {
-  const float d = p.scoring == kScoreSigmoid ? 8.f : 24.f + (t.top - x);
-  return (s > 0.f ? s * d * 1.2e-7f : 0.f) + fabsf(key) * 1.2e-7f + 1e-37f;
+// The keys' score: approximate exp and reciprocal, a few units in the last place.
+__device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Bound of |computed key - exact key| of the token's keys. Units are 2^-23. A score's
+// exp has an argument error of 1.2 units a unit of its argument u and 3 units more,
+// the sum of E <= 512 such terms and the reciprocal or division at most 20 more, so s
+// is off by s (26 + 1.2 u) units at most; with s <= s_top exp(-u) (softmax) or
+// s <= min(1, exp(-u)) (sigmoid, u = max(-x, 0)) that is below 27 s_top. Adding the
+// bias rounds once.
+__device__ __forceinline__ float keys_error(const RouteArgs& p, const Token& t, float largest_bias) {
+  const float top = p.scoring == kScoreSigmoid ? 1.f : t.sum > 0.f ? 1.f / t.sum : 0.f;
+  return (28.f * top + largest_bias) * 1.2e-7f + 1e-37f;
 }
 
 // The parts of a token's selection in float64, for keys that float32 cannot tell
@@ -162,6 +170,24 @@ __device__ __noinline__ int select64(const RouteArgs& p, size_t base, float top,
     if (lane == j) mine = at;
     last = k;
     last_e = at;
+  }
+  return mine;
+}
+
+// The selection by rounds where more than 32 keys are at or above the bound (many
+// equal ones) and the float32 keys are exact. keys: the warp's shared memory; a key
+// of 0 is not taken.
+__device__ __noinline__ int select32(const RouteArgs& p, volatile uint32_t* keys) {
+  const int lane = threadIdx.x & 31;
+  int mine = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t k = 0u, at = 0xFFFFu;
+    for (int e = lane; e < p.E; e += 32)
+      if (keys[e] > k) k = keys[e], at = e;
+    const uint32_t best = __reduce_max_sync(kFull, k);
+    const uint32_t e = __reduce_min_sync(kFull, k == best ? at : 0xFFFFu);
+    if (static_cast<uint32_t>(lane) == (e & 31)) keys[e] = 0u;
+    if (lane == j) mine = e;
   }
   return mine;
 }
@@ -245,10 +271,11 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t bas
 }
 
 // The selection of one token: lane j < top_k returns the j-th expert and its weight.
-// shared: the warp's shared memory (route_shared_bytes).
+// groups: the lane's keys' groups, five bits each. shared: the warp's shared memory.
 template <int V>  // keys per lane
-__device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, const float (&bias)[V], double* shared,
-                                            int* expert, float* weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, const float (&bias)[V],
+                                            float largest_bias, const uint32_t (&groups)[(V + 5) / 6],
+                                            double* shared, int* expert, float* weight) {
   const int lane = threadIdx.x & 31;
   const size_t base = token * static_cast<size_t>(p.ldl);
   float x[V];
@@ -260,7 +287,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     for (int i = 0; i < V; ++i) x[i] = lane + 32 * i < p.E ? load_logit(p.logits, base + lane + 32 * i, 0) : -CUDART_INF_F;
   }
   Token t{0.f, 1.f};
-  float s[V];  // scores (needed for the keys with a bias only)
+  uint32_t key[V];
+  float far = 0.f;  // the keys' error
   if (p.scoring == kScoreSoftmax) {
     float top = x[0];
 #pragma unroll
@@ -270,98 +298,96 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     float sum = 0.f;
     if (t.top > -CUDART_INF_F) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s[i] = expf(x[i] - t.top);
-        sum += s[i];
-      }
+      for (int i = 0; i < V; ++i) sum += __expf(x[i] - t.top);
     }
     t.sum = warp_sum(sum);
   }
-  uint32_t key[V];
-  float far = 0.f;  // the largest error of the token's keys
-  if (p.bias == nullptr) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < p.E ? ord32(x[i] + 0.f) : 0u;  // + 0: -0 and 0 are the same key
-  } else {
+  if (p.bias != nullptr) {
+    far = keys_error(p, t, largest_bias);
+    const float inv = p.scoring == kScoreSoftmax && t.sum > 0.f ? 1.f / t.sum : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float k = x[i];
-      if (k > -CUDART_INF_F) {
-        const float sc = p.scoring == kScoreSigmoid ? 1.f / (1.f + expf(-x[i])) : s[i] / t.sum;
-        k = isnan(bias[i]) ? -CUDART_INF_F : sc + bias[i];
-        if (k > -CUDART_INF_F) far = fmaxf(far, key_error(p, t, x[i], sc, k));
-      }
-      key[i] = lane + 32 * i < p.E ? ord32(k + 0.f) : 0u;
+      const float s = p.scoring == kScoreSigmoid ? quick_sigmoid(x[i]) : __expf(x[i] - t.top) * inv;
+      if (x[i] > -CUDART_INF_F) x[i] = s + bias[i];  // a bias of NaN is -inf here
     }
-    far = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(far)));
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < p.E ? ord32(x[i] + 0.f) : 0u;  // + 0: -0 and 0 are the same key
   uint32_t open = kFull;
   if (p.n_groups > 1) {
     volatile float* const keys = reinterpret_cast<volatile float*>(shared);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < p.E) keys[lane + 32 * i] = unord32(key[i]);
+      if (lane + 32 * i < p.E) keys[lane + 32 * i] = x[i];
     __syncwarp();
     open = choose_groups(p, base, t.top, keys, far);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (!(open >> div_u32(lane + 32 * i, p.per_group) & 1u)) key[i] = 0u;  // no round takes a closed expert
+      if (!(open >> (groups[i / 6] >> (5 * (i % 6)) & 31u) & 1u)) key[i] = 0u;  // no closed expert is taken
   }
-  int mine = 0;
-  uint32_t last = 0;  // the previous round's key; its expert
-  int last_e = 0;
-  bool close = false;
-  for (int j = 0; j < p.top_k; ++j) {
-    uint32_t k = key[0];
-    int at = 0;
+  // at least top_k keys are at or above the top_k-th largest of the lanes' largest
+  uint32_t most = key[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > k) k = key[i], at = i;
-    const uint32_t best = __reduce_max_sync(kFull, k);
-    const uint32_t e = __reduce_min_sync(kFull, k == best ? static_cast<uint32_t>(lane + 32 * at) : 0xFFFFu);
-    // neighbours of the selection that float32 cannot tell apart, unless they are a
-    // true tie (the same logit and bias), which the lowest index has won
-    if (p.bias != nullptr && j > 0 && best > ord32(-CUDART_INF_F) && !(unord32(last) - unord32(best) > 2.f * far))
-      close |= load_logit(p.logits, base + last_e, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
-               p.bias[last_e] != p.bias[e];
-    if (lane == j) mine = e;
-    const int own = (e & 31) == lane ? static_cast<int>(e >> 5) : -1;
+  for (int i = 1; i < V; ++i) most = max(most, key[i]);
+  uint32_t least = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    least = __reduce_max_sync(kFull, most);
+    if (most == least) most = 0;
+  }
+  if (p.bias != nullptr && least != 0) least = ord32(unord32(least) - 2.f * far);
+  least = max(least, 1u);
+  // gathered in the order of their indices
+  volatile uint2* const list = reinterpret_cast<volatile uint2*>(shared);
+  int n = 0;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t m = __ballot_sync(kFull, key[i] >= least);
+    const int at = n + __popc(m & ((1u << lane) - 1));
+    if (key[i] >= least && at < 32) {
+      list[at].x = key[i];
+      list[at].y = lane + 32 * i;
+    }
+    n += __popc(m);
+  }
+  __syncwarp();
+  int mine;
+  if (n <= 32) {
+    uint32_t k = lane < n ? list[lane].x : 0u, e = lane < n ? list[lane].y : 0u;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t kj = __shfl_sync(kFull, k, j);
+      rank += kj > k || (kj == k && j < lane);
+    }
+    __syncwarp();
+    if (lane < n) {
+      list[rank].x = k;
+      list[rank].y = e;
+    }
+    __syncwarp();
+    if (lane < n) k = list[lane].x, e = list[lane].y;
+    mine = e;
+    if (p.bias != nullptr) {
+      // neighbours of the selection, or the last one taken and one left out, that
+      // float32 cannot tell apart, unless they are a true tie (the same logit and bias)
+      const int other = lane < p.top_k ? max(lane - 1, 0) : p.top_k - 1;
+      const uint32_t ko = __shfl_sync(kFull, k, other), eo = __shfl_sync(kFull, e, other);
+      bool close = false;
+      if (lane > 0 && lane < n && k > ord32(-CUDART_INF_F) && !(unord32(ko) - unord32(k) > 2.f * far))
+        close = load_logit(p.logits, base + eo, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
+                p.bias[eo] != p.bias[e];
+      if (__any_sync(kFull, close)) mine = order64(p, base, e, n, t.top, reinterpret_cast<volatile int*>(shared));
+    }
+  } else if (p.bias != nullptr) {
+    mine = select64(p, base, t.top, open, shared);
+  } else {
+    volatile uint32_t* const keys = reinterpret_cast<volatile uint32_t*>(shared);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i == own) key[i] = 0u;
-    last = best;
-    last_e = e;
-  }
-  if (p.bias != nullptr) {
-    // and whatever was left out that may belong before the last one taken
-    const bool masked = last <= ord32(-CUDART_INF_F);
-    const uint32_t least = masked ? 0xFFFFFFFFu : ord32(unord32(last) - 2.f * far);
-    const float xl = load_logit(p.logits, base + last_e, p.bf16), bl = p.bias[last_e];
-    bool near = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) near |= key[i] >= least && (x[i] != xl || bias[i] != bl);
-    if (__any_sync(kFull, near || close)) {
-      // the candidates: the ones taken, and these
-      volatile int* const list = reinterpret_cast<volatile int*>(shared);
-      __syncwarp();
-      if (lane < p.top_k) list[lane] = mine;
-      int n = p.top_k;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t m = __ballot_sync(kFull, key[i] >= least);
-        const int at = n + __popc(m & ((1u << lane) - 1));
-        if ((m >> lane & 1u) && at < 32) list[at] = lane + 32 * i;
-        n += __popc(m);
-      }
-      __syncwarp();
-      if (n <= 32) {
-        const int c = list[lane < n ? lane : 0];
-        mine = order64(p, base, c, n, t.top, list);
-      } else {
-        mine = select64(p, base, t.top, open, shared);
-      }
-    }
+      if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
+    __syncwarp();
+    mine = select32(p, keys);
   }
   float w = 0.f;
   if (lane < p.top_k) {
@@ -438,15 +464,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 4) route_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
   pdl_wait();
-  float bias[V];
+  float bias[V], largest_bias = 0.f;
+  uint32_t groups[(V + 5) / 6] = {};
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = p.bias != nullptr && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.f;
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
+    if (isnan(bias[i])) bias[i] = -CUDART_INF_F;
+    if (bias[i] > -CUDART_INF_F) largest_bias = fmaxf(largest_bias, fabsf(bias[i]));
+    if (e < p.E) groups[i / 6] |= div_u32(e, p.per_group) << (5 * (i % 6));
+  }
+  largest_bias = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(largest_bias)));
   __syncthreads();
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   for (int t = t0 + warp; t < t1; t += kRouteWarps) {
     int e;
     float w;
-    route_token<V>(p, t, bias, route_smem + warp * p.shared_keys, &e, &w);
+    route_token<V>(p, t, bias, largest_bias, groups, route_smem + warp * p.shared_keys, &e, &w);
     if (lane < p.top_k) {
       const size_t r = static_cast<size_t>(t) * p.top_k + lane;
       p.experts[r] = e;
@@ -586,8 +620,7 @@ cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
   p.group_parts = 32;
   while (p.group_parts * p.n_groups > 32) p.group_parts >>= 1;
   p.per_group = fast_div(p.E / p.n_groups);
-  // per warp: its keys, or two lists of 32 candidates
-  p.shared_keys = p.n_groups > 1 || p.bias != nullptr ? std::max(p.E, 32) : 0;
+  p.shared_keys = std::max(p.E, 32);  // per warp: its keys, or 32 candidates
   const size_t smem = sizeof(double) * kRouteWarps * p.shared_keys + sizeof(int) * p.E;
   const dim3 grid(p.chunks);
   const int threads = kRouteWarps * 32;
