@@ -859,7 +859,7 @@ int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp
   CUtensorMap tm_w, tm_a;
   const int w_rows = args.E * args.N;
   int rc = a_fp4 ? make_tmap(h, &tm_w, w, w_rows, args.K / 2, 128) : make_tmap(h, &tm_w, w, w_rows, args.K, 128, true);
-  if (rc == MX_OK) rc = make_tmap(h, &tm_a, a, args.a_rows, a_fp4 ? args.K / 2 : args.K, plan.nt);
+  if (rc == MX_OK) rc = make_tmap(h, &tm_a, a, args.a_rows, a_fp4 ? args.K / 2 : args.K, plan.a_rows);
   if (rc != MX_OK) return rc;
   return cuda_status(mx::launch_gemm_fp4(tm_w, tm_a, args, plan, a_fp4 != 0, stream));
 }

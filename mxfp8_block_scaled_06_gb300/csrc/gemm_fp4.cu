@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kernels.h"
@@ -43,21 +44,28 @@ constexpr int kMaxNt = 224;        // two accumulators of 224 columns leave 64 c
 // kind takes about 140 cycles whatever its width, one issuing thread is bound by
 // that, and two CTAs issue side by side.
 constexpr int kSmallNt = 64;
+enum Mode : int {
+  kOne = 0,    // a CTA to an SM
+  kSmall = 1,  // two CTAs to an SM, token tiles up to kSmallNt
+  kPair = 2,   // two SMs share a tile of 256 weight rows: half the activation rows each
+};
+__host__ __device__ constexpr int rows_round(int mode) { return mode == kPair ? 32 : 16; }  // MMA N's granule
 constexpr int kMaxE = kRouteMaxExperts;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // Shared memory of one CTA, from its 1024-aligned base.
 struct Layout {
   uint32_t a_bytes, stage_bytes, sfw_stage, sfa_stage, sfw, sfa, bars, table, end;
-  __host__ __device__ Layout(int nt, int stages, int tiles_per_chunk, int E) {
-    a_bytes = static_cast<uint32_t>(nt) * 128u;
+  // a_rows: activation rows of a stage (nt, or half of it for a pair)
+  __host__ __device__ Layout(int nt, int a_rows, int stages, int tiles_per_chunk, int E) {
+    a_bytes = static_cast<uint32_t>(a_rows) * 128u;
     stage_bytes = kWBytes + a_bytes;
     sfw_stage = tiles_per_chunk * kSfTile;
     sfa_stage = tiles_per_chunk * ((nt + 127) / 128) * kSfTile;
     sfw = stages * stage_bytes;
     sfa = sfw + stages * sfw_stage;
     bars = sfa + stages * sfa_stage;
-    table = bars + 8u * (2 * stages + 4) + 16u;
+    table = bars + 8u * (3 * stages + 4) + 16u;
     end = table + 8u * (E + 1);
   }
   __host__ __device__ size_t total() const { return 1024 + end; }
@@ -67,15 +75,17 @@ struct Tile {
   int w_row;  // first weight row, of all experts
   int n0;     // first output column
   int row0, rows;
-  int n;  // MMA N: rows rounded up to 16 (an expert's token tiles are balanced)
+  int n;  // MMA N: rows rounded up (an expert's token tiles are balanced)
 };
 
 // The CTA's table of the experts: tile numbers before each one, first rows.
+template <int kMode>
 struct Table {
   const int* cum;
   const int* off;
   int E, nt;
-  __device__ Tile at(int idx, int N) const {
+  __device__ Tile at(int idx, int N, int rank) const {
+    constexpr int kRound = rows_round(kMode) - 1;
     int e = 0;
     for (int step = kMaxE; step > 0; step >>= 1)
       if (e + step < E && cum[e + step] <= idx) e += step;
@@ -83,39 +93,45 @@ struct Table {
     const int tt = (count + nt - 1) / nt;
     const int local = idx - cum[e];
     const int ni = local / tt, ti = local - ni * tt;
-    const int per = ((count + tt - 1) / tt + 15) & ~15;
+    const int per = ((count + tt - 1) / tt + kRound) & ~kRound;
     Tile t;
-    t.w_row = e * N + ni * 128;
-    t.n0 = ni * 128;
+    t.n0 = kMode == kPair ? ni * 256 + rank * 128 : ni * 128;
+    t.w_row = e * N + t.n0;
     t.row0 = off[e] + ti * per;
     t.rows = min(per, count - ti * per);
-    t.n = (t.rows + 15) & ~15;
+    t.n = (t.rows + kRound) & ~kRound;
     return t;
   }
 };
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
-template <bool kA4, bool kGather, bool kSmall>
-__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSmall ? 2 : 1)
+template <bool kA4, bool kGather, int kMode>
+__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMode == kSmall ? 2 : 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ GemmFp4Args p) {
   constexpr int kTiles = kA4 ? 2 : 1;  // scale tiles (128 elements of K) per stage
-  constexpr int kNt = kSmall ? kSmallNt : kMaxNt;
+  constexpr int kNt = kMode == kSmall ? kSmallNt : kMaxNt;
+  constexpr bool kTwo = kMode == kPair;
+  constexpr int kStageRows = kTwo ? kNt / 2 : kNt;  // activation rows of a stage, at most
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw_addr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
-  const Layout L(p.nt, stages, kTiles, p.E);
+  const int rank = kTwo ? static_cast<int>(cluster_rank()) : 0;
+  const int first = kTwo ? blockIdx.x >> 1 : blockIdx.x, stride = kTwo ? gridDim.x >> 1 : gridDim.x;
+  const Layout L(p.nt, kTwo ? p.nt / 2 : p.nt, stages, kTiles, p.E);
   const int units = p.K >> 7;                        // scale tiles along K
   const int chunks = (units + kTiles - 1) / kTiles;  // stages along K
   const uint32_t bars = base + L.bars;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (stages + s); };
-  const uint32_t acc_full = bars + 16u * stages, acc_empty = acc_full + 16u;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L.bars + 8 * (2 * stages + 4));
+  // the first CTA of a pair: the second one's stage is full
+  auto peer_full = [&](int s) { return bars + 8u * (2 * stages + s); };
+  const uint32_t acc_full = bars + 24u * stages, acc_empty = acc_full + 16u;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L.bars + 8 * (3 * stages + 4));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* const cum = reinterpret_cast<int*>(base_ptr + L.table);
   int* const off = cum + p.E + 1;
@@ -124,22 +140,28 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     for (int s = 0; s < stages; ++s) {
       mbar_init(full(s), 2 + (kGather ? kGatherThreads / 32 : 1));  // weights, activation scales, activations
       mbar_init(empty(s), 1);
+      mbar_init(peer_full(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, 4);  // the epilogue's warps
+      mbar_init(acc_empty + 8 * b, kTwo ? 8 : 4);  // the epilogues' warps
     }
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_a);
   }
-  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+  if (warp == 0) {
+    if constexpr (kTwo)
+      tmem_alloc_pair(smem_u32(tmem_slot), p.tmem_cols);
+    else
+      tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+  }
   pdl_launch_dependents();
   if (warp == 1) {
     if (p.offsets != nullptr) pdl_wait();
     // the experts' rows, clamped to the output, and the tiles before each expert
-    const int ntiles = p.N >> 7;
+    const int ntiles = kTwo ? p.N >> 8 : p.N >> 7;
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -164,14 +186,18 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     }
     if (lane == 0) cum[p.E] = run;
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kTwo)
+    cluster_sync();  // the pair's barriers and tensor memory are ready
+  else
+    __syncthreads();
   tc_fence_after();
   // nothing that an earlier kernel may have written is read, and nothing written,
   // before the wait; with early_weights warp 0 starts on the weights without it
   if (warp != 0 || !p.early_weights) pdl_wait();
   const uint32_t tmem = *tmem_slot;
-  const Table table{cum, off, p.E, p.nt};
+  const Table<kMode> table{cum, off, p.E, p.nt};
   const int total = cum[p.E];
   // one wait for the whole warp; false (for all lanes) once it has expired anywhere
   auto warp_wait = [&](uint32_t bar, uint32_t parity) {
@@ -190,8 +216,8 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     int s = 0, issuer = 0;
     uint32_t ph = 1;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
-      const Tile t = table.at(idx, p.N);
+    for (int idx = first; ok && idx < total; idx += stride) {
+      const Tile t = table.at(idx, p.N, rank);
       const uint8_t* const sf = p.w_scales + static_cast<size_t>(t.w_row >> 7) * units * kSfTile;
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(empty(s), ph))) break;
@@ -214,13 +240,13 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     int s = 0, issuer = 0;
     uint32_t ph = 1;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
-      const Tile t = table.at(idx, p.N);
+    for (int idx = first; ok && idx < total; idx += stride) {
+      const Tile t = table.at(idx, p.N, rank);
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(empty(s), ph))) break;
         if (lane == issuer) {
           mbar_expect_tx(full(s), L.a_bytes);
-          tma_load_2d(base + s * L.stage_bytes + kWBytes, &tm_a, full(s), i * 128, t.row0, pol);
+          tma_load_2d(base + s * L.stage_bytes + kWBytes, &tm_a, full(s), i * 128, t.row0 + rank * (t.n >> 1), pol);
         }
         __syncwarp();
         issuer = (issuer + 1) & 31;
@@ -229,8 +255,8 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     }
   } else if (kGather && warp >= kThreads / 32) {
     // ---------------- gathered activation rows: eight threads a row, 16 bytes each
-    constexpr int kRows = (kNt + 15) / 16;  // rows per thread, 16 apart
-    constexpr int kLag = 2;                 // stages copied ahead of the one handed over
+    constexpr int kRows = (kStageRows + 15) / 16;  // rows per thread, 16 apart
+    constexpr int kLag = kTwo ? 4 : 2;             // stages copied ahead of the one handed over
     const int gt = threadIdx.x - kThreads, c = gt & 7, r0 = gt >> 3;
     const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
     // rows r0, r0 + 16, ... have the same r % 8: one swizzle for all
@@ -245,15 +271,16 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
       if (++handed == stages) handed = 0;
       --pending;
     };
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
-      const Tile t = table.at(idx, p.N);
-      // byte offsets in a; rows past the tile and tokens outside a read as zero
+    for (int idx = first; ok && idx < total; idx += stride) {
+      const Tile t = table.at(idx, p.N, rank);
+      // rows past the tile and tokens outside a read as zero
+      const int mine = kTwo ? t.n >> 1 : t.n;  // rows of the tile in this CTA
       const uint8_t* src[kRows];
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
-        const int i = r0 + 16 * j;
+        const int i = r0 + 16 * j + rank * mine;
         src[j] = nullptr;
-        if (i < t.rows) {
+        if (r0 + 16 * j < mine && i < t.rows) {
           const int r = p.tokens[t.row0 + i];
           if (r >= 0 && r < p.a_rows) src[j] = p.a + static_cast<size_t>(r) * row_bytes + c * 16;
         }
@@ -264,7 +291,7 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
         const bool in_row = static_cast<uint32_t>(i) * 128u + c * 16u < row_bytes;
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
-          if (16 * j < t.n)
+          if (16 * j < mine)
             cp_async_16(dst + j * 2048, src[j] != nullptr ? src[j] + static_cast<size_t>(i) * 128 : p.a,
                         src[j] != nullptr && in_row ? 16u : 0u);
         cp_async_commit();
@@ -285,8 +312,8 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     uint32_t ph = 1;
     bool ok = true;
     const int sfa_tiles = (p.nt + 127) >> 7;
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x) {
-      const Tile t = table.at(idx, p.N);
+    for (int idx = first; ok && idx < total; idx += stride) {
+      const Tile t = table.at(idx, p.N, rank);
       const uint8_t* src[kRows];
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
@@ -344,6 +371,20 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
         }
       }
     }
+  } else if (kTwo && warp == 1 && rank != 0) {
+    // ---------------- the second CTA of a pair: its stages' arrivals, passed on to
+    // the first one, which issues the pair's MMAs
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int idx = first; ok && idx < total; idx += stride) {
+      for (int i = 0; i < chunks; ++i) {
+        if (!(ok = warp_wait(full(s), ph))) break;
+        if (lane == 0) mbar_arrive_remote(map_shared_rank(peer_full(s), 0));
+        __syncwarp();
+        if (++s == stages) s = 0, ph ^= 1u;
+      }
+    }
   } else if (warp == 1) {
     // ---------------- scales into TMEM, and the MMAs
     const uint64_t wd = sdesc_k_sw128(base), fd = sdesc_sf(base + L.sfw), gd = sdesc_sf(base + L.sfa);
@@ -355,18 +396,31 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     // columns are enough
     const uint32_t sf_col = tmem + 2 * p.nt, sf_cols = 4 * kTiles * (1 + sfa_tiles);
     constexpr uint32_t kSf = (1u << 4) | (1u << 29);  // the next scale byte, in both fields of the descriptor
+    auto copy_scales = [&](uint32_t taddr, uint32_t lo) {
+      if constexpr (kTwo)
+        tmem_cp_32x128b_x4_pair_lh(taddr, lo, sf_hi);
+      else
+        tmem_cp_32x128b_x4_lh(taddr, lo, sf_hi);
+    };
+    auto commit = [&](uint32_t bar) {
+      if constexpr (kTwo)
+        tc_commit_pair(bar);
+      else
+        tc_commit(bar);
+    };
     int s = 0, it = 0;
     uint32_t ph = 0, odd = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x, ++it) {
-      const Tile t = table.at(idx, p.N);
+    for (int idx = first; ok && idx < total; idx += stride, ++it) {
+      const Tile t = table.at(idx, p.N, rank);
       const int buf = it & 1;
       if (!(ok = warp_wait(acc_empty + 8 * buf, ((it >> 1) & 1) ^ 1))) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * p.nt;
-      const uint32_t id0 = idesc_w4<kA4>(t.n, 0);
+      const uint32_t id0 = idesc_w4<kA4>(t.n, 0, kTwo ? 256 : 128);
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(full(s), ph))) break;
+        if (kTwo && !(ok = warp_wait(peer_full(s), ph))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t ta = sf_col + odd * sf_cols, tb = ta + 4 * kTiles;
@@ -375,10 +429,9 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
 #pragma unroll
           for (int h = 0; h < kTiles; ++h) {
             if (h < have) {
-              tmem_cp_32x128b_x4_lh(ta + 4 * h, f_lo + h * (kSfTile >> 4), sf_hi);
+              copy_scales(ta + 4 * h, f_lo + h * (kSfTile >> 4));
               for (int rt = 0; rt * 128 < t.n; ++rt)
-                tmem_cp_32x128b_x4_lh(tb + 4 * (h * sfa_tiles + rt), g_lo + (h * sfa_tiles + rt) * (kSfTile >> 4),
-                                      sf_hi);
+                copy_scales(tb + 4 * (h * sfa_tiles + rt), g_lo + (h * sfa_tiles + rt) * (kSfTile >> 4));
             }
           }
           const uint32_t w_lo = w_lo0 + s * (L.stage_bytes >> 4), a_lo = w_lo + (kWBytes >> 4);
@@ -386,12 +439,15 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
           for (int j = 0; j < 4; ++j) {
             // .mxf8f6f4: scale byte j of the stage's one tile; .mxf4: bytes 2 (j % 2) and the next of tile j / 2
             const int h = kA4 ? j >> 1 : 0;
-            if (h < have)
-              mma_w4_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id0 + (kA4 ? 2 * (j & 1) : j) * kSf,
-                             ta + 4 * h, tb + 4 * h * sfa_tiles, i != 0 || j != 0);
+            const uint32_t id = id0 + (kA4 ? 2 * (j & 1) : j) * kSf, sfw = ta + 4 * h, sfa = tb + 4 * h * sfa_tiles;
+            if (h >= have) continue;
+            if constexpr (kTwo)
+              mma_w4_pair_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, i != 0 || j != 0);
+            else
+              mma_w4_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, i != 0 || j != 0);
           }
-          tc_commit(empty(s));
-          if (i == chunks - 1) tc_commit(acc_full + 8 * buf);
+          commit(empty(s));
+          if (i == chunks - 1) commit(acc_full + 8 * buf);
         }
         __syncwarp();
         odd ^= 1u;
@@ -405,8 +461,8 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
     int it = 0;
     bool ok = true;
     const size_t ldo = p.gated ? p.N >> 1 : p.N;
-    for (int idx = blockIdx.x; ok && idx < total; idx += gridDim.x, ++it) {
-      const Tile t = table.at(idx, p.N);
+    for (int idx = first; ok && idx < total; idx += stride, ++it) {
+      const Tile t = table.at(idx, p.N, rank);
       const int buf = it & 1;
       if (!(ok = warp_wait(acc_full + 8 * buf, (it >> 1) & 1))) break;
       tc_fence_after();
@@ -432,7 +488,12 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + 8 * buf);
+      if (lane == 0) {
+        if constexpr (kTwo)
+          mbar_arrive_remote(map_shared_rank(acc_empty + 8 * buf, 0));
+        else
+          mbar_arrive(acc_empty + 8 * buf);
+      }
     }
   }
   __syncwarp();
@@ -446,11 +507,20 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kSm
       mbar_wait(full(s), 1, 2000000);
     }
   }
-  __syncthreads();
+  __syncwarp();
+  if constexpr (kTwo)
+    cluster_sync();  // no CTA frees its tensor memory, or leaves, while its peer may still use the pair's
+  else
+    __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem_cols);
+    if constexpr (kTwo)
+      tmem_dealloc_pair(tmem, p.tmem_cols);
+    else
+      tmem_dealloc(tmem, p.tmem_cols);
   }
+  __syncwarp();
+  if constexpr (kTwo) cluster_sync();
 }
 
 }  // namespace
@@ -462,34 +532,42 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
   // take, balanced; with several experts, room for twice the mean
   const long want = E == 1 ? R : std::min<long>(R, 2L * ((R + E - 1) / E));
   const long tt = (want + kMaxNt - 1) / kMaxNt;
-  pl.nt = std::min(kMaxNt, static_cast<int>((want + tt - 1) / tt + 15) & ~15);
-  pl.ctas_per_sm = pl.nt <= kSmallNt ? 2 : 1;
+  const int nt = static_cast<int>((want + tt - 1) / tt);
+  pl.mode = nt <= kSmallNt ? kSmall : N % 256 == 0 && getenv("MX_TMP_NOPAIR") == nullptr ? kPair : kOne;
+  pl.nt = std::min(kMaxNt, (nt + rows_round(pl.mode) - 1) & -rows_round(pl.mode));
+  pl.a_rows = pl.mode == kPair ? pl.nt / 2 : pl.nt;
+  pl.ctas_per_sm = pl.mode == kSmall ? 2 : 1;
   const int cols = 2 * pl.nt + 2 * 4 * kt * (1 + (pl.nt + 127) / 128);
   pl.tmem_cols = 32;
   while (pl.tmem_cols < cols) pl.tmem_cols <<= 1;
-  const size_t fixed = Layout(pl.nt, 0, kt, E).total();
-  const size_t per = Layout(pl.nt, 1, kt, E).total() - fixed;
+  const size_t fixed = Layout(pl.nt, pl.a_rows, 0, kt, E).total();
+  const size_t per = Layout(pl.nt, pl.a_rows, 1, kt, E).total() - fixed;
   const size_t room = pl.ctas_per_sm == 1 ? kMaxDynamicSmem : 233472 / 2 - 1024;  // 1 KB of each CTA's is reserved
   pl.stages = static_cast<int>(std::min<size_t>((room - fixed) / per, 12));
   // CTAs that share an SM share its tensor memory: take the shared memory that
   // keeps any more than fit from being resident
-  pl.smem = std::max(Layout(pl.nt, pl.stages, kt, E).total(),
+  pl.smem = std::max(Layout(pl.nt, pl.a_rows, pl.stages, kt, E).total(),
                      static_cast<size_t>(233472 / (pl.ctas_per_sm + 1) + 1));
-  const long tiles = static_cast<long>(N / 128) * std::min<long>((R + pl.nt - 1L) / pl.nt + E - 1, R);
-  pl.grid = static_cast<int>(std::min<long>(tiles, static_cast<long>(sm_count) * pl.ctas_per_sm));
+  const int ctas = pl.mode == kPair ? 2 : 1;  // of a tile
+  const long tiles = static_cast<long>(N / (128 * ctas)) * std::min<long>((R + pl.nt - 1L) / pl.nt + E - 1, R);
+  pl.grid = static_cast<int>(std::min<long>(tiles, static_cast<long>(sm_count) * pl.ctas_per_sm / ctas)) * ctas;
   return pl;
 }
 
 cudaError_t set_gemm_fp4_attributes() {
   const void* const kernels[] = {
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, false>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, false>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, false>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, false>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, true>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, true>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, true>),
-      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, true>)};
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, kOne>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, kOne>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, kOne>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, kOne>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, kSmall>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, kSmall>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, kSmall>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, kSmall>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, false, kPair>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<false, true, kPair>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, false, kPair>),
+      reinterpret_cast<const void*>(&gemm_fp4_kernel<true, true, kPair>)};
   for (const void* k : kernels) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
@@ -509,19 +587,24 @@ cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, co
     cfg.blockDim = dim3(kThreads + (gather ? kGatherThreads : 0));
     cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = 2;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = plan.mode == kPair ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, args);
   };
-  auto pick = [&](auto small) {
-    constexpr bool S = decltype(small)::value;
+  auto pick = [&](auto mode) {
+    constexpr int S = decltype(mode)::value;
     if (a_fp4) return gather ? go(gemm_fp4_kernel<true, true, S>) : go(gemm_fp4_kernel<true, false, S>);
     return gather ? go(gemm_fp4_kernel<false, true, S>) : go(gemm_fp4_kernel<false, false, S>);
   };
-  return plan.nt <= kSmallNt ? pick(std::true_type{}) : pick(std::false_type{});
+  if (plan.mode == kPair) return pick(std::integral_constant<int, kPair>{});
+  if (plan.mode == kSmall) return pick(std::integral_constant<int, kSmall>{});
+  return pick(std::integral_constant<int, kOne>{});
 }
 
 }  // namespace mx

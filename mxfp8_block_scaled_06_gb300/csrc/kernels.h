@@ -257,6 +257,8 @@ struct GemmFp4Args {
   int* status;
 };
 struct GemmFp4Plan {
+  int mode;    // how CTAs share SMs and tiles (gemm_fp4.cu)
+  int a_rows;  // activation rows of a stage: the tensor map's box
   int nt, stages, tmem_cols, ctas_per_sm, grid;
   size_t smem;
 };

@@ -81,6 +81,13 @@ __device__ __forceinline__ bool mbar_wait_or(uint32_t bar, uint32_t parity, cons
     if ((i & 63u) == 0 && (*abort != 0 || globaltimer() - t0 > kWaitLimitNs)) return false;
   }
 }
+// Arrive on the barrier of another CTA of the cluster (an address from
+// map_shared_rank). The arrival follows what this thread has seen and done in its own
+// CTA's shared memory; a release at cluster scope would also wait for the thread's
+// earlier arrivals to reach the other SM, about 0.9 us each.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -285,6 +292,12 @@ __device__ __forceinline__ void cluster_sum_batch(const uint32_t (&addr)[kSumBat
   }
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
 // ------------------------------------------------------------------ warp
 // True in exactly one active lane of a converged warp (elect.sync); code around
 // it stays warp-uniform, so its values can live in uniform registers.
@@ -310,6 +323,15 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
+// The same for a pair of CTAs (ranks 2i and 2i + 1 of the cluster), one warp of each.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -321,6 +343,14 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
                : "memory");
+}
+
+// As tc_commit for a pair: arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Shared-memory matrix descriptor: K-major operand in the 128-byte swizzle
@@ -374,10 +404,11 @@ __device__ __forceinline__ void mma_mxf8_lh(uint32_t d_tmem, uint32_t a_lo, uint
 // .kind::mxf8f6f4 against E4M3 activations (K = 32; format codes 5 and 0 there),
 // or .kind::mxf4 with E2M1 activations (K = 64; format code 1). sf_id is the
 // scale byte, or the first of the two scale bytes, of the 32-bit scale word.
+// m: 128, or 256 for a pair of CTAs.
 template <bool kA4>
-__device__ __forceinline__ uint32_t idesc_w4(uint32_t n, uint32_t sf_id) {
+__device__ __forceinline__ uint32_t idesc_w4(uint32_t n, uint32_t sf_id, uint32_t m = 128) {
   return (sf_id << 4) | ((kA4 ? 1u : 5u) << 7) | ((kA4 ? 1u : 0u) << 10) | ((n >> 3) << 17) | (1u << 23) |
-         ((128u >> 4) << 24) | (sf_id << 29);
+         ((m >> 4) << 24) | (sf_id << 29);
 }
 // D[tmem] (+)= A[smem] x B[smem]^T, A MXFP4, as mma_mxf8_lh. .kind::mxf8f6f4 reads
 // E2M1 elements unpacked (16 elements in the low 8 of 16 bytes), .kind::mxf4 packed.
@@ -396,6 +427,39 @@ __device__ __forceinline__ void mma_w4_lh(uint32_t d_tmem, uint32_t a_lo, uint32
         : "memory");
   else
     mma_mxf8_lh(d_tmem, a_lo, a_hi, b_lo, b_hi, idesc, sfa_tmem, sfb_tmem, accumulate);
+}
+// The same for a pair of CTAs, issued by the first: each CTA has its 128 of the 256
+// rows of A, half the rows of B, A's scales for its rows and B's for all, at the
+// same offsets; D's 256 rows end 128 in each CTA's tensor memory.
+template <bool kA4>
+__device__ __forceinline__ void mma_w4_pair_lh(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                               uint32_t b_hi, uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                               uint32_t accumulate) {
+  if constexpr (kA4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %6, [%7], "
+        "[%8], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accumulate), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %6, [%7], "
+        "[%8], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(accumulate), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+// As tmem_cp_32x128b_x4_lh in both CTAs of a pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_32x128b_x4_pair_lh(uint32_t taddr, uint32_t lo, uint32_t hi) {
+  asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+               "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+               "r"(lo), "r"(hi)
+               : "memory");
 }
 // Copy a 32x128-bit smem tile into TMEM lanes 0-31, replicated into all four
 // 32-lane quarters (4 columns); the descriptor as its two 32-bit halves.
