@@ -65,7 +65,7 @@ struct Layout {
     sfw = stages * stage_bytes;
     sfa = sfw + stages * sfw_stage;
     bars = sfa + stages * sfa_stage;
-    table = bars + 8u * (3 * stages + 4) + 16u;
+    table = bars + 8u * (2 * stages + 4) + 16u;
     end = table + 8u * (E + 1);
   }
   __host__ __device__ size_t total() const { return 1024 + end; }
@@ -118,7 +118,10 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw_addr);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the shuffle tells the compiler that the warp's number is uniform: the MMA warp's
+  // loop then runs on uniform registers (an MMA and a scale copy every 50 to 70 cycles
+  // of its one issuing thread, which bounds the loop; without it 20 % more)
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int stages = p.stages;
   const int rank = kTwo ? static_cast<int>(cluster_rank()) : 0;
   const int first = kTwo ? blockIdx.x >> 1 : blockIdx.x, stride = kTwo ? gridDim.x >> 1 : gridDim.x;
@@ -128,19 +131,17 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
   const uint32_t bars = base + L.bars;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (stages + s); };
-  // the first CTA of a pair: the second one's stage is full
-  auto peer_full = [&](int s) { return bars + 8u * (2 * stages + s); };
-  const uint32_t acc_full = bars + 24u * stages, acc_empty = acc_full + 16u;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L.bars + 8 * (3 * stages + 4));
+  const uint32_t acc_full = bars + 16u * stages, acc_empty = acc_full + 16u;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + L.bars + 8 * (2 * stages + 4));
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* const cum = reinterpret_cast<int*>(base_ptr + L.table);
   int* const off = cum + p.E + 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full(s), 2 + (kGather ? kGatherThreads / 32 : 1));  // weights, activation scales, activations
+      // weights, activation scales, activations; the first CTA of a pair: the second one's
+      mbar_init(full(s), 2 + (kGather ? kGatherThreads / 32 : 1) + (kTwo && rank == 0));
       mbar_init(empty(s), 1);
-      mbar_init(peer_full(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + 8 * b, 1);
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
     for (int idx = first; ok && idx < total; idx += stride) {
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(full(s), ph))) break;
-        if (lane == 0) mbar_arrive_remote(map_shared_rank(peer_full(s), 0));
+        if (lane == 0) mbar_arrive_remote(map_shared_rank(full(s), 0));
         __syncwarp();
         if (++s == stages) s = 0, ph ^= 1u;
       }
@@ -420,7 +421,6 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
       const uint32_t id0 = idesc_w4<kA4>(t.n, 0, kTwo ? 256 : 128);
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(full(s), ph))) break;
-        if (kTwo && !(ok = warp_wait(peer_full(s), ph))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t ta = sf_col + odd * sf_cols, tb = ta + 4 * kTiles;
