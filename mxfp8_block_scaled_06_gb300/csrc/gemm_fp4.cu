@@ -410,8 +410,35 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
         tc_commit(bar);
     };
     int s = 0, it = 0;
-    uint32_t ph = 0, odd = 0;
-    bool ok = true;
+    uint32_t ph = 0;
+    uint32_t w_lo = w_lo0, f_lo = f_lo0, g_lo = g_lo0, ta = sf_col;
+    bool ok = true, landed = false;
+    // one stage: its scales, its MMAs (kHave scale tiles of K, the second one's two
+    // MMAs left out where K ends inside the stage) and the commits
+    auto issue = [&](auto have_c, const uint32_t d, const uint32_t id0, const bool wide, const bool begins,
+                     const bool ends, const int buf) {
+      constexpr int kHave = decltype(have_c)::value;
+      const uint32_t tb = ta + 4 * kTiles;
+#pragma unroll
+      for (int h = 0; h < kHave; ++h) {
+        copy_scales(ta + 4 * h, f_lo + h * (kSfTile >> 4));
+        copy_scales(tb + 4 * h * sfa_tiles, g_lo + h * sfa_tiles * (kSfTile >> 4));
+        if (wide) copy_scales(tb + 4 * (h * sfa_tiles + 1), g_lo + (h * sfa_tiles + 1) * (kSfTile >> 4));
+      }
+      const uint32_t a_lo = w_lo + (kWBytes >> 4);
+#pragma unroll
+      for (int j = 0; j < (kA4 ? 2 * kHave : 4); ++j) {
+        // .mxf8f6f4: scale byte j of the stage's one tile; .mxf4: bytes 2 (j % 2) and the next of tile j / 2
+        const int h = kA4 ? j >> 1 : 0;
+        const uint32_t id = id0 + (kA4 ? 2 * (j & 1) : j) * kSf, sfw = ta + 4 * h, sfa = tb + 4 * h * sfa_tiles;
+        if constexpr (kTwo)
+          mma_w4_pair_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, j != 0 || !begins);
+        else
+          mma_w4_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, j != 0 || !begins);
+      }
+      commit(empty(s));
+      if (ends) commit(acc_full + 8 * buf);
+    };
     for (int idx = first; ok && idx < total; idx += stride, ++it) {
       const Tile t = table.at(idx, p.N, rank);
       const int buf = it & 1;
@@ -419,39 +446,31 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
       tc_fence_after();
       const uint32_t d = tmem + buf * p.nt;
       const uint32_t id0 = idesc_w4<kA4>(t.n, 0, kTwo ? 256 : 128);
+      const bool wide = t.n > 128;
       for (int i = 0; i < chunks; ++i) {
-        if (!(ok = warp_wait(full(s), ph))) break;
+        if (!__all_sync(kFull, landed) && !(ok = warp_wait(full(s), ph))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t ta = sf_col + odd * sf_cols, tb = ta + 4 * kTiles;
-          const uint32_t f_lo = f_lo0 + s * (L.sfw_stage >> 4), g_lo = g_lo0 + s * (L.sfa_stage >> 4);
-          const int have = min(kTiles, units - i * kTiles);
-#pragma unroll
-          for (int h = 0; h < kTiles; ++h) {
-            if (h < have) {
-              copy_scales(ta + 4 * h, f_lo + h * (kSfTile >> 4));
-              for (int rt = 0; rt * 128 < t.n; ++rt)
-                copy_scales(tb + 4 * (h * sfa_tiles + rt), g_lo + (h * sfa_tiles + rt) * (kSfTile >> 4));
-            }
-          }
-          const uint32_t w_lo = w_lo0 + s * (L.stage_bytes >> 4), a_lo = w_lo + (kWBytes >> 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // .mxf8f6f4: scale byte j of the stage's one tile; .mxf4: bytes 2 (j % 2) and the next of tile j / 2
-            const int h = kA4 ? j >> 1 : 0;
-            const uint32_t id = id0 + (kA4 ? 2 * (j & 1) : j) * kSf, sfw = ta + 4 * h, sfa = tb + 4 * h * sfa_tiles;
-            if (h >= have) continue;
-            if constexpr (kTwo)
-              mma_w4_pair_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, i != 0 || j != 0);
-            else
-              mma_w4_lh<kA4>(d, w_lo + 2 * j, op_hi, a_lo + 2 * j, op_hi, id, sfw, sfa, i != 0 || j != 0);
-          }
-          commit(empty(s));
-          if (i == chunks - 1) commit(acc_full + 8 * buf);
+          const bool ends = i == chunks - 1;
+          if (kTiles == 1 || (units & 1) == 0 || !ends)
+            issue(std::integral_constant<int, kTiles>{}, d, id0, wide, i == 0, ends, buf);
+          else
+            issue(std::integral_constant<int, 1>{}, d, id0, wide, i == 0, ends, buf);
         }
         __syncwarp();
-        odd ^= 1u;
-        if (++s == stages) s = 0, ph ^= 1u;
+        ta = ta == sf_col ? sf_col + sf_cols : sf_col;
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+          w_lo = w_lo0;
+          f_lo = f_lo0;
+          g_lo = g_lo0;
+        } else {
+          w_lo += L.stage_bytes >> 4;
+          f_lo += L.sfw_stage >> 4;
+          g_lo += L.sfa_stage >> 4;
+        }
+        landed = mbar_test_wait(full(s), ph);  // the next stage, while the MMAs run
       }
     }
   } else if (warp >= 4 && warp < 8) {
