@@ -11,7 +11,8 @@
 //   0     weight boxes (TMA) and their scale tiles (bulk copies)
 //   1     tcgen05.cp of the scales and tcgen05.mma, by an elected lane
 //   2     activation rows, where they are neighbours: a TMA box
-//   3     activation scales: gathered with plain loads into 128x4 scale tiles
+//   3     activation scales: gathered with plain loads into 128x4 scale tiles (wide
+//         tiles: with the block's last warp)
 //   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half
 //   8-11  activation rows gathered by index: 16-byte cp.async into the swizzled
 //         tile (tile::gather4 copies, four rows each, came at 34 ns apiece: 1.9 us
@@ -35,6 +36,13 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256, kGatherThreads = 128;  // the latter on top, where rows are gathered
+// warps that load the activation scales: a second one, the block's last, where token
+// tiles are wide (one alone held an MXFP4 stage of 224 rows at 0.4 us; 8192 x 8192 x
+// 5120 took 130 us, without its loads 96)
+__host__ __device__ constexpr int scale_warps(int mode) { return mode == 1 ? 1 : 2; }
+__host__ __device__ constexpr int threads(int mode, bool gather) {
+  return kThreads + (gather ? kGatherThreads : 0) + (scale_warps(mode) - 1) * 32;
+}
 constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
 // bytes that an unpacking copy of it completes on its barrier: the packed ones
 constexpr uint32_t kWBytesUnpacked = 128 * 64;
@@ -107,12 +115,14 @@ struct Table {
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 template <bool kA4, bool kGather, int kMode>
-__global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMode == kSmall ? 2 : 1)
+__global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 : 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                     const __grid_constant__ GemmFp4Args p) {
   constexpr int kTiles = kA4 ? 2 : 1;  // scale tiles (128 elements of K) per stage
   constexpr int kNt = kMode == kSmall ? kSmallNt : kMaxNt;
   constexpr bool kTwo = kMode == kPair;
+  constexpr int kScaleWarps = scale_warps(kMode);
+  constexpr int kExtraWarp = (kThreads + (kGather ? kGatherThreads : 0)) / 32;  // the second of them
   constexpr int kStageRows = kTwo ? kNt / 2 : kNt;  // activation rows of a stage, at most
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
         if (++s == stages) s = 0, ph ^= 1u;
       }
     }
-  } else if (kGather && warp >= kThreads / 32) {
+  } else if (kGather && warp >= kThreads / 32 && warp < (kThreads + kGatherThreads) / 32) {
     // ---------------- gathered activation rows: eight threads a row, 16 bytes each
     constexpr int kRows = (kStageRows + 15) / 16;  // rows per thread, 16 apart
     constexpr int kLag = kTwo ? 4 : 2;             // stages copied ahead of the one handed over
@@ -305,14 +315,27 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
     }
     cp_async_wait<0>();
     while (pending > 0) hand_over();
-  } else if (warp == 3) {
+  } else if (warp == 3 || (kScaleWarps == 2 && warp == kExtraWarp)) {
     // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
-    // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows
-    constexpr int kRows = (kNt + 31) / 32, kBatch = 4;  // rows per lane; scale tiles loaded at once
+    // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows. A batch of
+    // kBatch scale tiles is loaded at once, the next one while it is stored; with two
+    // warps they take the batches in turn.
+    constexpr int kRows = (kNt + 31) / 32, kBatch = 4;  // rows per lane
+    constexpr int kBatchStages = kBatch / kTiles;
+    const int which = warp == 3 ? 0 : 1;
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
+    auto advance = [&](int n) {
+      s += n;
+      while (s >= stages) s -= stages, ph ^= 1u;
+    };
     const int sfa_tiles = (p.nt + 127) >> 7;
+    // plain scales of four tiles are 16 bytes of a row: one load, where rows start at
+    // multiples of 16
+    const bool vec = !p.a_swizzled && (units & 3) == 0;
+    const int step = p.a_swizzled ? kSfTile : 4;
+    int batch = 0;  // over all tiles
     for (int idx = first; ok && idx < total; idx += stride) {
       const Tile t = table.at(idx, p.N, rank);
       const uint8_t* src[kRows];
@@ -331,9 +354,20 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
           }
         }
       }
-      const int step = p.a_swizzled ? kSfTile : 4;
       uint32_t v[kBatch][kRows], next[kBatch][kRows];
       auto load = [&](int u0, uint32_t (&w)[kBatch][kRows]) {
+        if (vec) {
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) {
+            const uint4 q = src[j] != nullptr && u0 < units ? __ldg(reinterpret_cast<const uint4*>(src[j] + u0 * 4))
+                                                            : make_uint4(0, 0, 0, 0);
+            w[0][j] = q.x;
+            w[1][j] = q.y;
+            w[2][j] = q.z;
+            w[3][j] = q.w;
+          }
+          return;
+        }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
 #pragma unroll
@@ -342,15 +376,20 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
                           ? __ldg(reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step))
                           : 0u;
       };
-      load(0, next);
-      for (int u0 = 0; ok && u0 < units; u0 += kBatch) {
+      int u0 = 0;
+      if (kScaleWarps == 2 && (batch & 1) != which) {  // this tile's first batch is the other warp's
+        u0 = kBatch;
+        advance(min(kBatchStages, chunks));
+      }
+      if (u0 < units) load(u0, next);
+      for (; ok && u0 < units; u0 += kBatch * kScaleWarps) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
 #pragma unroll
           for (int j = 0; j < kRows; ++j) v[b][j] = next[b][j];
-        load(u0 + kBatch, next);
+        load(u0 + kBatch * kScaleWarps, next);
 #pragma unroll
-        for (int c = 0; c < kBatch / kTiles; ++c) {
+        for (int c = 0; c < kBatchStages; ++c) {
           if (u0 + c * kTiles >= units) break;
           if (!(ok = warp_wait(empty(s), ph))) break;
           uint8_t* const dst = base_ptr + L.sfa + s * L.sfa_stage + lane * 16;
@@ -368,9 +407,12 @@ __global__ void __launch_bounds__(kThreads + (kGather ? kGatherThreads : 0), kMo
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(full(s));
-          if (++s == stages) s = 0, ph ^= 1u;
+          advance(1);
         }
+        // the other warp's batch
+        if (kScaleWarps == 2) advance(max(0, min(kBatchStages, chunks - (u0 + kBatch) / kTiles)));
       }
+      batch += (units + kBatch - 1) / kBatch;
     }
   } else if (kTwo && warp == 1 && rank != 0) {
     // ---------------- the second CTA of a pair: its stages' arrivals, passed on to
@@ -603,7 +645,7 @@ cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, co
   auto go = [&](auto kernel) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(kThreads + (gather ? kGatherThreads : 0));
+    cfg.blockDim = dim3(threads(plan.mode, gather));
     cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
