@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       // weights, activation scales, activations; the first CTA of a pair: the second one's
-      mbar_init(full(s), 2 + (kGather ? kGatherThreads / 32 : 1) + (kTwo && rank == 0));
+      mbar_init(full(s), 3 + (kTwo && rank == 0));
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -265,56 +265,69 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       }
     }
   } else if (kGather && warp >= kThreads / 32 && warp < (kThreads + kGatherThreads) / 32) {
-    // ---------------- gathered activation rows: eight threads a row, 16 bytes each
-    constexpr int kRows = (kStageRows + 15) / 16;  // rows per thread, 16 apart
-    constexpr int kLag = kTwo ? 4 : 2;             // stages copied ahead of the one handed over
-    const int gt = threadIdx.x - kThreads, c = gt & 7, r0 = gt >> 3;
+    // ---------------- gathered activation rows: the warps take the stages in turn,
+    // eight threads a row, 16 bytes each. A warp hands a stage over once it has
+    // issued its next one, or when that one is not free yet.
+    constexpr int kRows = kStageRows / 4;  // rows per thread, 4 apart
+    constexpr int kWarps = kGatherThreads / 32;
+    const int c = lane & 7, r0 = lane >> 3;
     const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
-    // rows r0, r0 + 16, ... have the same r % 8: one swizzle for all
-    const uint32_t dst0 = base + kWBytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
-    int s = 0, handed = 0, pending = 0;
+    const uint32_t dst0 = base + kWBytes + r0 * 128;
+    // rows r0, r0 + 4, ... have two values of r % 8: two swizzles in turn
+    const uint32_t swz[2] = {static_cast<uint32_t>(c ^ r0) << 4, static_cast<uint32_t>(c ^ (r0 + 4)) << 4};
+    int s = warp - kThreads / 32;  // stages: at least kWarps - 1 (the plan)
     uint32_t ph = 1;
+    if (s >= stages) s -= stages, ph ^= 1u;
+    int pending = -1;  // the stage to hand over
     bool ok = true;
     auto hand_over = [&]() {
       fence_proxy_async_smem();  // written by the threads, read by the tensor cores
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(handed));
-      if (++handed == stages) handed = 0;
-      --pending;
+      if (lane == 0) mbar_arrive(full(pending));
+      pending = -1;
     };
+    int chunk = warp - kThreads / 32;  // of the tile
     for (int idx = first; ok && idx < total; idx += stride) {
-      const Tile t = table.at(idx, p.N, rank);
-      // rows past the tile and tokens outside a read as zero
-      const int mine = kTwo ? t.n >> 1 : t.n;  // rows of the tile in this CTA
-      const uint8_t* src[kRows];
+      if (chunk < chunks) {
+        const Tile t = table.at(idx, p.N, rank);
+        // rows past the tile and tokens outside a read as zero
+        const int mine = kTwo ? t.n >> 1 : t.n;  // rows of the tile in this CTA
+        int row[kRows];
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int i = r0 + 16 * j + rank * mine;
-        src[j] = nullptr;
-        if (r0 + 16 * j < mine && i < t.rows) {
-          const int r = p.tokens[t.row0 + i];
-          if (r >= 0 && r < p.a_rows) src[j] = p.a + static_cast<size_t>(r) * row_bytes + c * 16;
+        for (int j = 0; j < kRows; ++j) {
+          const int i = r0 + 4 * j + rank * mine;
+          row[j] = r0 + 4 * j < mine && i < t.rows ? __ldg(p.tokens + t.row0 + i) : -1;
+          if (row[j] >= p.a_rows) row[j] = -1;
+        }
+        for (; chunk < chunks; chunk += kWarps) {
+          if (pending >= 0 && !__all_sync(kFull, mbar_test_wait(empty(s), ph))) {
+            cp_async_wait<0>();
+            hand_over();
+          }
+          if (!(ok = warp_wait(empty(s), ph))) break;
+          const uint32_t dst = dst0 + s * L.stage_bytes;
+          const uint32_t at = static_cast<uint32_t>(chunk) * 128u + c * 16u;
+          const bool in_row = at < row_bytes;
+          const uint8_t* const col = p.a + (in_row ? at : 0u);
+#pragma unroll
+          for (int j = 0; j < kRows; ++j)
+            if (4 * j < mine)
+              cp_async_16(dst + j * 512 + swz[j & 1], col + static_cast<size_t>(max(row[j], 0)) * row_bytes,
+                          row[j] >= 0 && in_row ? 16u : 0u);
+          cp_async_commit();
+          if (pending >= 0) {
+            cp_async_wait<1>();
+            hand_over();
+          }
+          pending = s;
+          s += kWarps;
+          while (s >= stages) s -= stages, ph ^= 1u;
         }
       }
-      for (int i = 0; i < chunks; ++i) {
-        if (!(ok = warp_wait(empty(s), ph))) break;
-        const uint32_t dst = dst0 + s * L.stage_bytes;
-        const bool in_row = static_cast<uint32_t>(i) * 128u + c * 16u < row_bytes;
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
-          if (16 * j < mine)
-            cp_async_16(dst + j * 2048, src[j] != nullptr ? src[j] + static_cast<size_t>(i) * 128 : p.a,
-                        src[j] != nullptr && in_row ? 16u : 0u);
-        cp_async_commit();
-        if (++pending > kLag) {
-          cp_async_wait<kLag>();
-          hand_over();
-        }
-        if (++s == stages) s = 0, ph ^= 1u;
-      }
+      chunk -= chunks;
     }
     cp_async_wait<0>();
-    while (pending > 0) hand_over();
+    if (pending >= 0) hand_over();
   } else if (warp == 3 || (kScaleWarps == 2 && warp == kExtraWarp)) {
     // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
     // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows. A batch of
