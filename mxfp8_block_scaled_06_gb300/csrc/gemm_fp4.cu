@@ -26,7 +26,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kernels.h"
@@ -540,24 +539,47 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       const int buf = it & 1;
       if (!(ok = warp_wait(acc_full + 8 * buf, (it >> 1) & 1))) break;
       tc_fence_after();
-      const int col = t.n0 + q * 32 + (lane & ~1);
-      __nv_bfloat16* const out = p.out + static_cast<size_t>(t.row0) * ldo + (p.gated ? col >> 1 : col);
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * p.nt;
+      // Plain: a lane stores its column, 64 bytes of a token to a warp; trading
+      // columns for wider stores first was no faster (100 us against 101 with two
+      // columns of a token to a lane, 118 with four; 8192 x 8192 x 5120).
+      // Gated: four neighbouring lanes trade the four tokens c0 + 4i .. + 3, first in
+      // pairs, the even lane taking gate and up of tokens 0 and 2, the odd one of 1
+      // and 3; then, the products in bf16, between the pairs, the first one taking
+      // tokens 0 and 1. A lane stores two columns of one token.
+      const int tok0 = (lane & 2) + odd;
+      const int col = t.n0 + q * 32 + (p.gated ? lane & ~3 : lane);
+      __nv_bfloat16* out = p.gated ? p.out + (static_cast<size_t>(t.row0) + tok0) * ldo + (col >> 1)
+                                   : p.out + static_cast<size_t>(t.row0) * ldo + col;
       for (int c0 = 0; c0 < t.n; c0 += 16) {
         float v[16];
-        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * p.nt + c0, v);
-        // neighbouring lanes trade, so that the even one has both columns of token
-        // c0 + 2i and the odd one both of c0 + 2i + 1
+        tmem_ld_32x32b_x16(acc + c0, v);
+        if (!p.gated) {
+          if (c0 + 16 <= t.rows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float got = __shfl_xor_sync(kFull, odd ? v[2 * i] : v[2 * i + 1], 1);
-          const float a = odd ? got : v[2 * i], b = odd ? v[2 * i + 1] : got;
-          const int tok = c0 + 2 * i + odd;
-          if (tok < t.rows) {
-            if (p.gated)
-              out[tok * ldo] = __float2bfloat16_rn(silu(a) * b);
-            else
-              *reinterpret_cast<__nv_bfloat162*>(out + tok * ldo) = __floats2bfloat162_rn(a, b);
+            for (int i = 0; i < 16; ++i) out[i * ldo] = __float2bfloat16_rn(v[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < t.rows) out[i * ldo] = __float2bfloat16_rn(v[i]);
           }
+          out += 16 * ldo;
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float two[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float even = v[4 * i + 2 * j], other = v[4 * i + 2 * j + 1];
+            const float got = __shfl_xor_sync(kFull, odd ? even : other, 1);
+            two[j] = silu(odd ? got : even) * (odd ? other : got);
+          }
+          const float got = __shfl_xor_sync(kFull, lane & 2 ? two[0] : two[1], 2);
+          if (c0 + 4 * i + tok0 < t.rows)
+            *reinterpret_cast<__nv_bfloat162*>(out) =
+                __floats2bfloat162_rn(lane & 2 ? got : two[0], lane & 2 ? two[1] : got);
+          out += 4 * ldo;
         }
       }
       tc_fence_before();
@@ -602,12 +624,22 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) {
   GemmFp4Plan pl{};
   const int kt = a_fp4 ? 2 : 1;
-  // token tile: the rows of an expert in as few tiles of at most kMaxNt as they
-  // take, balanced; with several experts, room for twice the mean
+  // Token tile: the rows of an expert in as few tiles of at most kMaxNt as they
+  // take, balanced; with several experts, room for twice the mean. A plain product
+  // takes more and narrower tiles where that saves time in its last wave: a tile
+  // costs about its rows and 100 more.
   const long want = E == 1 ? R : std::min<long>(R, 2L * ((R + E - 1) / E));
-  const long tt = (want + kMaxNt - 1) / kMaxNt;
+  long tt = (want + kMaxNt - 1) / kMaxNt;
+  if (E == 1 && want > kMaxNt / 2) {
+    const int at_once = N % 256 == 0 ? sm_count / 2 : sm_count;
+    const long w_tiles = N % 256 == 0 ? N / 256 : N / 128;
+    auto cost = [&](long k) { return (w_tiles * k + at_once - 1) / at_once * ((want + k - 1) / k + 100); };
+    const long most = 3 * tt;
+    for (long k = tt + 1; k <= most && (want + k - 1) / k > kSmallNt; ++k)
+      if (cost(k) < cost(tt)) tt = k;
+  }
   const int nt = static_cast<int>((want + tt - 1) / tt);
-  pl.mode = nt <= kSmallNt ? kSmall : N % 256 == 0 && getenv("MX_TMP_NOPAIR") == nullptr ? kPair : kOne;
+  pl.mode = nt <= kSmallNt ? kSmall : N % 256 == 0 ? kPair : kOne;
   pl.nt = std::min(kMaxNt, (nt + rows_round(pl.mode) - 1) & -rows_round(pl.mode));
   pl.a_rows = pl.mode == kPair ? pl.nt / 2 : pl.nt;
   pl.ctas_per_sm = pl.mode == kSmall ? 2 : 1;
