@@ -194,7 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw_addr);
 
-  const int warp = threadIdx.x >> 5;
+  // the shuffle tells the compiler that the warp's number is uniform, so that the MMA
+  // warp's loop runs on uniform registers (the one issuing thread bounds it): one
+  // row, N = 2048, K = 5120 3.95 -> 3.62 us under PDL, N = 5120, K = 8192 6.70 -> 6.17
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int tile = blockIdx.x;
   const int S = gridDim.y;
