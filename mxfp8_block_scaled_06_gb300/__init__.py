@@ -514,11 +514,51 @@ def wo_a_grouped_unfused(h: Handle, x, positions, cos_sin, w, w_scales, n_groups
     return dict(q=q, q_scales=q_scales, z=zt, xq=xq, xq_scales=xq_scales)
 
 
+# The five calls below run in a few microseconds of GPU time for a decode step, so
+# their host path is kept short: element types resolved once, residency by device
+# number, and the current stream's raw handle (2.8 us through torch.cuda.current_stream).
+_TYPE_CODES = _U8 = _I32 = _F32 = _RAW_STREAM = None
+
+
+def _setup():
+    """Resolves what the calls below need of torch, once."""
+    global _TYPE_CODES, _U8, _I32, _F32, _RAW_STREAM
+    import torch
+    _types()
+    _U8, _I32, _F32 = (torch.uint8,), (torch.int32,), (torch.float32,)
+    _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _TYPE_CODES = {torch.bfloat16: MX_TYPE_BF16, torch.float16: MX_TYPE_F16, torch.float32: MX_TYPE_F32}
+    return torch
+
+
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        _torch = _setup()
+    return _torch
+
+
+def _here(h: Handle, *named) -> None:
+    """As _resident, of (name, tensor or None) pairs."""
+    device = h.device
+    for name, t in named:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: on {t.device}, the handle's device is cuda:{device}")
+
+
+def _stream_of(h: Handle, stream):
+    """Raw handle of the given stream, or of the handle's device's current one."""
+    if stream is None and _RAW_STREAM is not None:
+        return _RAW_STREAM(h.device)
+    return _stream(stream)
+
+
 def _type_code(name: str, t, allowed):
     """MX_TYPE_* of a tensor, which has to be one of allowed."""
-    import torch
-    codes = {torch.bfloat16: MX_TYPE_BF16, torch.float16: MX_TYPE_F16, torch.float32: MX_TYPE_F32}
-    code = codes.get(t.dtype)
+    code = _TYPE_CODES.get(t.dtype)
     if code is None or code not in allowed:
         raise TypeError(f"{name}: dtype {t.dtype} not supported")
     return code
@@ -528,7 +568,7 @@ def mx_quantize_rows_fp4(h: Handle, x, q=None, scales=None, swizzled: bool = Tru
                          stream=None):
     """bf16, fp16 or fp32 [M, K] (row stride x.stride(0)) -> (packed E2M1 codes uint8
     [M, K/2], scale bytes, y): y = the codes' values in bf16 [M, K] when asked, else None."""
-    import torch
+    torch = _t()
     if x.dim() != 2:
         raise ValueError("x: a 2-D [M, K] tensor is required")
     m, k = x.shape
@@ -538,26 +578,27 @@ def mx_quantize_rows_fp4(h: Handle, x, q=None, scales=None, swizzled: bool = Tru
         raise ValueError(f"x: {k} columns, a multiple of 32 is required")
     sbytes = _sbytes(m, k) if swizzled else m * (k // 32)
     if q is not None:
-        _matrix("q", q, (torch.uint8,), m, k // 2)
+        _matrix("q", q, _U8, m, k // 2)
     if scales is not None:
         _flat("scales", scales, _scale_types(), sbytes)
-    _resident(h, x=x, q=q, scales=scales)
-    q = _empty_u8((m, k // 2), x.device) if q is None else q
-    scales = _empty_u8((sbytes,) if swizzled else (m, k // 32), x.device) if scales is None else scales
+    _here(h, ("x", x), ("q", q), ("scales", scales))
+    if q is None:
+        q = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((sbytes,) if swizzled else (m, k // 32), dtype=torch.uint8, device=x.device)
     yt = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
-    _check(load_library().mx_quantize_rows_fp4(h.ptr, m, k, _ptr(x), x.stride(0), code, _ptr(q), _ptr(scales),
-                                               int(swizzled), _ptr(yt), _stream(stream)),
+    _check(load_library().mx_quantize_rows_fp4(h.ptr, m, k, x.data_ptr(), x.stride(0), code, q.data_ptr(),
+                                               scales.data_ptr(), int(swizzled), _ptr(yt), _stream_of(h, stream)),
            "mx_quantize_rows_fp4")
     return q, scales, yt
 
 
 def _fp4_activations(a, m: int, k: int):
     """1 if a holds m rows of packed MXFP4, 0 if of MXFP8: told by its columns."""
-    import torch
     if a is None or a.dim() != 2 or a.shape[1] not in (k, k // 2):
         raise ValueError(f"a: expected [>= {m}, {k}] MXFP8 codes or [>= {m}, {k // 2}] packed MXFP4 codes")
     fp4 = a.shape[1] == k // 2
-    _matrix("a", a, (torch.uint8,) if fp4 else _codes_types(), m, a.shape[1])
+    _matrix("a", a, _U8 if fp4 else _codes_types(), m, a.shape[1])
     return int(fp4)
 
 
@@ -566,21 +607,23 @@ def mx_gemm_fp4(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = N
     """out[M, N] bf16 = dequant(a) x dequant(w)^T with MXFP4 weights w: packed codes uint8
     [N, K/2] and swizzled scales. a: MXFP8 codes [M, K] or packed MXFP4 codes [M, K/2],
     with swizzled scales (M = a's rows unless m is given)."""
-    import torch
+    torch = _t()
     if w is None or w.dim() != 2:
         raise ValueError("w: a 2-D [N, K/2] tensor is required")
     n, k = w.shape[0], 2 * w.shape[1]
-    _matrix("w", w, (torch.uint8,), n, k // 2)
+    _matrix("w", w, _U8, n, k // 2)
     _flat("w_scales", w_scales, _scale_types(), _sbytes(n, k))
     m = a.shape[0] if m is None else m
     fp4 = _fp4_activations(a, m, k)
     _flat("a_scales", a_scales, _scale_types(), _sbytes(m, k))
     if out is not None:
-        _matrix("out", out, (torch.bfloat16,), m, n)
-    _resident(h, a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out)
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device) if out is None else out
-    _check(load_library().mx_gemm_fp4(h.ptr, m, n, k, _ptr(a), _ptr(a_scales), fp4, _ptr(w), _ptr(w_scales),
-                                      _ptr(out), MX_FLAG_PDL if pdl else 0, _stream(stream)), "mx_gemm_fp4")
+        _matrix("out", out, _BF16, m, n)
+    _here(h, ("a", a), ("a_scales", a_scales), ("w", w), ("w_scales", w_scales), ("out", out))
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device)
+    _check(load_library().mx_gemm_fp4(h.ptr, m, n, k, a.data_ptr(), a_scales.data_ptr(), fp4, w.data_ptr(),
+                                      w_scales.data_ptr(), out.data_ptr(), MX_FLAG_PDL if pdl else 0,
+                                      _stream_of(h, stream)), "mx_gemm_fp4")
     return out
 
 
@@ -592,29 +635,32 @@ def mx_gemm_fp4_grouped(h: Handle, a, a_scales, w, w_scales, offsets, tokens=Non
     [E, N, K/2], w_scales each expert's swizzled scales; offsets int32 [E + 1], tokens
     int32 [R]. gated: weight rows 2i, 2i + 1 are gate i, up i and out is [R, N/2],
     silu(gate) * up. Rows that no expert has are left as they are."""
-    import torch
+    torch = _t()
     if w is None or w.dim() != 3:
         raise ValueError("w: a 3-D [E, N, K/2] tensor is required")
     e, n, k = w.shape[0], w.shape[1], 2 * w.shape[2]
-    _flat("w", w, (torch.uint8,), e * n * k // 2)
+    _flat("w", w, _U8, e * n * k // 2)
     if n % 128:
         raise ValueError(f"w: {n} rows per expert, a multiple of 128 is required")
     _flat("w_scales", w_scales, _scale_types(), e * _sbytes(n, k))
     fp4 = _fp4_activations(a, 1, k)
     rows = a.shape[0]
     _flat("a_scales", a_scales, _scale_types(), rows * (k // 32))
-    _flat("offsets", offsets, (torch.int32,), e + 1)
+    _flat("offsets", offsets, _I32, e + 1)
     if tokens is not None:
-        _flat("tokens", tokens, (torch.int32,), 1)
+        _flat("tokens", tokens, _I32, 1)
     r = rows if tokens is None else tokens.numel()
     cols = n // 2 if gated else n
     if out is not None:
-        _matrix("out", out, (torch.bfloat16,), r, cols)
-    _resident(h, a=a, a_scales=a_scales, w=w, w_scales=w_scales, offsets=offsets, tokens=tokens, out=out)
-    out = torch.empty((r, cols), dtype=torch.bfloat16, device=w.device) if out is None else out
-    _check(load_library().mx_gemm_fp4_grouped(h.ptr, e, r, n, k, _ptr(a), rows, _ptr(a_scales), fp4, _ptr(w),
-                                              _ptr(w_scales), _ptr(offsets), _ptr(tokens), int(gated), _ptr(out),
-                                              _stream(stream)), "mx_gemm_fp4_grouped")
+        _matrix("out", out, _BF16, r, cols)
+    _here(h, ("a", a), ("a_scales", a_scales), ("w", w), ("w_scales", w_scales), ("offsets", offsets),
+          ("tokens", tokens), ("out", out))
+    if out is None:
+        out = torch.empty((r, cols), dtype=torch.bfloat16, device=w.device)
+    _check(load_library().mx_gemm_fp4_grouped(h.ptr, e, r, n, k, a.data_ptr(), rows, a_scales.data_ptr(), fp4,
+                                              w.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), _ptr(tokens),
+                                              int(gated), out.data_ptr(), _stream_of(h, stream)),
+           "mx_gemm_fp4_grouped")
     return out
 
 
@@ -626,7 +672,7 @@ def mx_route(h: Handle, logits, top_k: int, bias=None, scoring: str = "softmax",
     fp32 and experts int32 [T, top_k], and the rows in expert order: offsets int32 [E + 1],
     tokens int32 [T * top_k] (the token of each row), slots int32 [T, top_k] (the row of
     each choice)."""
-    import torch
+    torch = _t()
     if logits.dim() != 2:
         raise ValueError("logits: a 2-D [T, E] tensor is required")
     t, e = logits.shape
@@ -638,47 +684,55 @@ def mx_route(h: Handle, logits, top_k: int, bias=None, scoring: str = "softmax",
     if top_k < 1:
         raise ValueError(f"top_k: {top_k}, at least 1 is required")
     if bias is not None:
-        _flat("bias", bias, (torch.float32,), e)
-    given = dict(weights=weights, experts=experts, offsets=offsets, tokens=tokens, slots=slots)
-    for name, x in given.items():
+        _flat("bias", bias, _F32, e)
+    if weights is not None:
+        _flat("weights", weights, _F32, t * top_k)
+    for name, x, count in (("experts", experts, t * top_k), ("offsets", offsets, e + 1),
+                           ("tokens", tokens, t * top_k), ("slots", slots, t * top_k)):
         if x is not None:
-            _flat(name, x, (torch.float32 if name == "weights" else torch.int32,),
-                  e + 1 if name == "offsets" else t * top_k)
-    _resident(h, logits=logits, bias=bias, **given)
-    dev = logits.device
-    out = dict(
-        weights=torch.empty((t, top_k), dtype=torch.float32, device=dev) if weights is None else weights,
-        experts=torch.empty((t, top_k), dtype=torch.int32, device=dev) if experts is None else experts,
-        offsets=torch.empty((e + 1,), dtype=torch.int32, device=dev) if offsets is None else offsets,
-        tokens=torch.empty((t * top_k,), dtype=torch.int32, device=dev) if tokens is None else tokens,
-        slots=torch.empty((t, top_k), dtype=torch.int32, device=dev) if slots is None else slots)
-    _check(load_library().mx_route(h.ptr, t, e, top_k, _ptr(logits), logits.stride(0), code, _ptr(bias),
+            _flat(name, x, _I32, count)
+    _here(h, ("logits", logits), ("bias", bias), ("weights", weights), ("experts", experts), ("offsets", offsets),
+          ("tokens", tokens), ("slots", slots))
+    dev, i32 = logits.device, torch.int32
+    if weights is None:
+        weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+    if experts is None:
+        experts = torch.empty((t, top_k), dtype=i32, device=dev)
+    if offsets is None:
+        offsets = torch.empty((e + 1,), dtype=i32, device=dev)
+    if tokens is None:
+        tokens = torch.empty((t * top_k,), dtype=i32, device=dev)
+    if slots is None:
+        slots = torch.empty((t, top_k), dtype=i32, device=dev)
+    _check(load_library().mx_route(h.ptr, t, e, top_k, logits.data_ptr(), logits.stride(0), code, _ptr(bias),
                                    MX_SCORE_SIGMOID if scoring == "sigmoid" else MX_SCORE_SOFTMAX, n_groups,
-                                   topk_groups, int(renormalize), float(scale), _ptr(out["weights"]),
-                                   _ptr(out["experts"]), _ptr(out["offsets"]), _ptr(out["tokens"]),
-                                   _ptr(out["slots"]), _stream(stream)), "mx_route")
-    return out
+                                   topk_groups, int(renormalize), scale, weights.data_ptr(), experts.data_ptr(),
+                                   offsets.data_ptr(), tokens.data_ptr(), slots.data_ptr(), _stream_of(h, stream)),
+           "mx_route")
+    return dict(weights=weights, experts=experts, offsets=offsets, tokens=tokens, slots=slots)
 
 
 def mx_combine(h: Handle, y, slots, weights, residual=None, out=None, stream=None):
     """out[t] = sum over j of weights[t, j] * y[slots[t, j]] (+ residual[t]): y bf16 [R, N]
     (row stride y.stride(0)), slots int32 and weights fp32 [T, top_k], bf16 [T, N] out."""
-    import torch
+    torch = _t()
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y [R, N] and slots [T, top_k]: 2-D tensors are required")
     r, n = y.shape
     t, k = slots.shape
-    _matrix("y", y, (torch.bfloat16,), r, n, row_stride=True)
-    _matrix("slots", slots, (torch.int32,), t, k)
-    _matrix("weights", weights, (torch.float32,), t, k)
+    _matrix("y", y, _BF16, r, n, row_stride=True)
+    _matrix("slots", slots, _I32, t, k)
+    _matrix("weights", weights, _F32, t, k)
     if residual is not None:
-        _matrix("residual", residual, (torch.bfloat16,), t, n)
+        _matrix("residual", residual, _BF16, t, n)
     if out is not None:
-        _matrix("out", out, (torch.bfloat16,), t, n)
-    _resident(h, y=y, slots=slots, weights=weights, residual=residual, out=out)
-    out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device) if out is None else out
-    _check(load_library().mx_combine(h.ptr, t, k, n, _ptr(y), r, y.stride(0), _ptr(slots), _ptr(weights),
-                                     _ptr(residual), _ptr(out), _stream(stream)), "mx_combine")
+        _matrix("out", out, _BF16, t, n)
+    _here(h, ("y", y), ("slots", slots), ("weights", weights), ("residual", residual), ("out", out))
+    if out is None:
+        out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device)
+    _check(load_library().mx_combine(h.ptr, t, k, n, y.data_ptr(), r, y.stride(0), slots.data_ptr(),
+                                     weights.data_ptr(), _ptr(residual), out.data_ptr(), _stream_of(h, stream)),
+           "mx_combine")
     return out
 
 
