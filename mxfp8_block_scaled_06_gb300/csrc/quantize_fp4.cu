@@ -10,7 +10,8 @@
 // The value c 2^e has one mantissa bit, so bf16 holds it exactly (its smallest,
 // 2^-128, is a bf16 subnormal).
 //
-// Four threads share a block, eight elements each: one 16-byte load (32 bytes
+// Bound by memory: 2 (4) bytes in, 0.53 out, and 2 more for the values. Four threads
+// share a block, eight elements each: one 16-byte load (32 bytes
 // for fp32), two xor-shuffles for the block's amax, one 4-byte store of codes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +25,11 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
+// From this many units on (8 Mi elements) a thread takes four, whose loads are in
+// flight together: 16381 x 8192 bf16 70.7 -> 55.2 us, with y 103 -> 89 us (6.8 TB/s, a
+// plain copy's rate); below, more blocks serve better. Streaming loads and stores
+// (.cs) were slower: 62 and 95 us.
+constexpr uint32_t kManyUnits = 1u << 20;
 
 // n / d for the d that (mul, shift) was made for (host: fast_div).
 __device__ __forceinline__ uint32_t div_u32(uint32_t n, FastDiv f) {
@@ -76,33 +82,58 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   }
 }
 
-template <typename T>
+// kUnits 8-element units per thread, kThreads apart: their loads are in flight together.
+template <typename T, int kUnits>
 __global__ void __launch_bounds__(kThreads)
     quantize_rows_fp4_kernel(const T* __restrict__ x, long ldx, int M, int K, uint32_t* __restrict__ q,
                              uint8_t* __restrict__ scales, int swizzled, uint4* __restrict__ y, uint32_t units,
-                             FastDiv per_row) {
+                             FastDiv per_row, uint32_t unit_blocks) {
   pdl_launch_dependents();
-  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;  // 8-element unit, row-major
+  if (blockIdx.x >= unit_blocks) {
+    // rows [M, ceil128(M)) of the swizzled scales: zero, four to a thread
+    const uint32_t words = ((static_cast<uint32_t>(K) >> 5) + 3) >> 2;  // of a row
+    const uint32_t i = (blockIdx.x - unit_blocks) * kThreads + threadIdx.x;
+    pdl_wait();
+    if (i < (-M & 127) * words)
+      *reinterpret_cast<uint32_t*>(scales + swz_offset(M + i / words, i % words * 4, words * 4)) = 0u;
+    return;
+  }
+  const uint32_t u0 = blockIdx.x * (kThreads * kUnits) + threadIdx.x;  // 8-element unit, row-major
   const uint32_t upr = static_cast<uint32_t>(K) >> 3;
-  const uint32_t row = div_u32(u, per_row);
-  const uint32_t col = u - row * upr;
-  const uint32_t nblk = static_cast<uint32_t>(K) >> 5, blk = col >> 2;
+  const uint32_t nblk = static_cast<uint32_t>(K) >> 5;
   const uint32_t cpad4 = (nblk + 3) & ~3u;
-  pdl_wait();
-  // units % 4 == 0 and a block's four threads are neighbours: they are in range together
-  const bool valid = u < units;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (valid) load8(x + static_cast<size_t>(row) * ldx + col * 8, v);
-  // max |v| as bits: at or above Inf's bits when any value is Inf or NaN
-  uint32_t amax = 0;
+  uint32_t row[kUnits], col[kUnits];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-  const bool finite = amax < 0x7F800000u;
-  const uint32_t s = finite ? static_cast<uint32_t>(max(static_cast<int>(amax >> 23) - 2, 0)) : 0xFFu;
-  const uint32_t codes = finite ? cvt_e2m1x8(v, mx_inv_scale(s)) : 0u;
-  if (valid) {
+  for (int i = 0; i < kUnits; ++i) {
+    row[i] = div_u32(u0 + i * kThreads, per_row);
+    col[i] = u0 + i * kThreads - row[i] * upr;
+  }
+  pdl_wait();
+  float v[kUnits][8];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (u0 + i * kThreads < units) {
+      load8(x + static_cast<size_t>(row[i]) * ldx + col[i] * 8, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    // units % 4 == 0 and a block's four threads are neighbours: they are in range together
+    const bool valid = u < units;
+    // max |v| as bits: at or above Inf's bits when any value is Inf or NaN
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const bool finite = amax < 0x7F800000u;
+    const uint32_t s = finite ? static_cast<uint32_t>(max(static_cast<int>(amax >> 23) - 2, 0)) : 0xFFu;
+    const uint32_t codes = finite ? cvt_e2m1x8(v[i], mx_inv_scale(s)) : 0u;
+    if (!valid) continue;
     q[u] = codes;
     if (y != nullptr) {
       // 2^(s - 127): s = 0 is the subnormal 2^-127, 0xFF is NaN
@@ -111,26 +142,18 @@ __global__ void __launch_bounds__(kThreads)
                                : __uint_as_float(0x7FC00000u);
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = e2m1_value(codes >> (8 * i)) * f, b = e2m1_value(codes >> (8 * i + 4)) * f;
-        w[i] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);  // exact: the low halves are zero
+      for (int e = 0; e < 4; ++e) {
+        const float a = e2m1_value(codes >> (8 * e)) * f, b = e2m1_value(codes >> (8 * e + 4)) * f;
+        w[e] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);  // exact: the low halves are zero
       }
       y[u] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if ((col & 3) == 0)
-      scales[swizzled ? swz_offset(row, blk, cpad4) : row * static_cast<size_t>(nblk) + blk] = static_cast<uint8_t>(s);
-  }
-  if (swizzled) {
-    // the layout's padding, zero: columns [nblk, cpad4) of every row, rows [M, ceil128(M))
-    const uint32_t rows = (static_cast<uint32_t>(M) + 127) & ~127u;
-    const uint32_t threads = gridDim.x * kThreads;
-    if (cpad4 != nblk)
-      for (uint32_t r = u; r < static_cast<uint32_t>(M); r += threads)
-        for (uint32_t c = nblk; c < cpad4; ++c) scales[swz_offset(r, c, cpad4)] = 0;
-    // four scales of a padding row at a time
-    const uint32_t words = (rows - M) * (cpad4 >> 2);
-    for (uint32_t i = u; i < words; i += threads)
-      *reinterpret_cast<uint32_t*>(scales + swz_offset(M + i / (cpad4 >> 2), i % (cpad4 >> 2) * 4, cpad4)) = 0u;
+    if ((col[i] & 3) != 0) continue;
+    const uint32_t blk = col[i] >> 2;
+    scales[swizzled ? swz_offset(row[i], blk, cpad4) : row[i] * static_cast<size_t>(nblk) + blk] =
+        static_cast<uint8_t>(s);
+    if (swizzled && blk == nblk - 1)
+      for (uint32_t c = nblk; c < cpad4; ++c) scales[swz_offset(row[i], c, cpad4)] = 0;  // padding columns
   }
 }
 
@@ -148,8 +171,12 @@ FastDiv fast_div(uint32_t d) {
 cudaError_t launch_quantize_rows_fp4(const void* x, long ldx, int x_type, int M, int K, void* q, void* scales,
                                      int swizzled, void* y, cudaStream_t stream) {
   const uint32_t units = static_cast<uint32_t>(static_cast<long>(M) * K / 8);
+  const bool many = units >= kManyUnits;
+  const uint32_t per_block = kThreads * (many ? 4 : 1);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((units + kThreads - 1) / kThreads);
+  const uint32_t unit_blocks = (units + per_block - 1) / per_block;
+  const uint32_t pad_words = swizzled ? (-M & 127) * ((K / 32 + 3) / 4) : 0;
+  cfg.gridDim = dim3(unit_blocks + (pad_words + kThreads - 1) / kThreads);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -160,11 +187,15 @@ cudaError_t launch_quantize_rows_fp4(const void* x, long ldx, int x_type, int M,
   const FastDiv per_row = fast_div(static_cast<uint32_t>(K / 8));
   auto go = [&](auto kernel, auto* p) {
     return cudaLaunchKernelEx(&cfg, kernel, p, ldx, M, K, static_cast<uint32_t*>(q), static_cast<uint8_t*>(scales),
-                              swizzled, static_cast<uint4*>(y), units, per_row);
+                              swizzled, static_cast<uint4*>(y), units, per_row, unit_blocks);
   };
-  if (x_type == kTypeF32) return go(quantize_rows_fp4_kernel<float>, static_cast<const float*>(x));
-  if (x_type == kTypeF16) return go(quantize_rows_fp4_kernel<__half>, static_cast<const __half*>(x));
-  return go(quantize_rows_fp4_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(x));
+  auto pick = [&](auto* p) {
+    using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+    return many ? go(quantize_rows_fp4_kernel<T, 4>, p) : go(quantize_rows_fp4_kernel<T, 1>, p);
+  };
+  if (x_type == kTypeF32) return pick(static_cast<const float*>(x));
+  if (x_type == kTypeF16) return pick(static_cast<const __half*>(x));
+  return pick(static_cast<const __nv_bfloat16*>(x));
 }
 
 }  // namespace mx
