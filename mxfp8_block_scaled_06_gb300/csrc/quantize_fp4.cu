@@ -60,13 +60,26 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
   return __uint_as_float(__float_as_uint(m) | ((c & 8u) << 28));
 }
 
+// Eight elements as loaded, their values, and the bits of the largest magnitude as a
+// float: at or above Inf's bits when any element is Inf or NaN.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p);
+struct Unit {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
+  // magnitudes of either 16-bit type order as unsigned numbers, NaN last: two at a time
+  __device__ __forceinline__ uint32_t amax() const {
+    constexpr uint32_t kMag = 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(raw.x & kMag, raw.y & kMag), __vmaxu2(raw.z & kMag, raw.w & kMag));
+    return max(m & 0xFFFFu, m >> 16);
+  }
+  static __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
+    if constexpr (std::is_same<T, __half>::value)
+      return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    else
+      return m << 16;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -80,7 +93,28 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
       }
     }
   }
-}
+};
+template <>
+struct Unit<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t amax() const {
+    float v[8];
+    values(v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t amax_bits(uint32_t m) { return m; }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 
 // kUnits 8-element units per thread, kThreads apart: their loads are in flight together.
 template <typename T, int kUnits>
@@ -109,30 +143,28 @@ __global__ void __launch_bounds__(kThreads)
     col[i] = u0 + i * kThreads - row[i] * upr;
   }
   pdl_wait();
-  float v[kUnits][8];
+  Unit<T> in[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    if (u0 + i * kThreads < units) {
-      load8(x + static_cast<size_t>(row[i]) * ldx + col[i] * 8, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
+    if (u0 + i * kThreads < units)
+      in[i].load(x + static_cast<size_t>(row[i]) * ldx + col[i] * 8);
+    else
+      in[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const uint32_t u = u0 + i * kThreads;
     // units % 4 == 0 and a block's four threads are neighbours: they are in range together
     const bool valid = u < units;
-    // max |v| as bits: at or above Inf's bits when any value is Inf or NaN
-    uint32_t amax = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    uint32_t amax = in[i].amax();
     amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    amax = Unit<T>::amax_bits(amax);
     const bool finite = amax < 0x7F800000u;
     const uint32_t s = finite ? static_cast<uint32_t>(max(static_cast<int>(amax >> 23) - 2, 0)) : 0xFFu;
-    const uint32_t codes = finite ? cvt_e2m1x8(v[i], mx_inv_scale(s)) : 0u;
+    float v[8];
+    in[i].values(v);
+    const uint32_t codes = finite ? cvt_e2m1x8(v, mx_inv_scale(s)) : 0u;
     if (!valid) continue;
     q[u] = codes;
     if (y != nullptr) {
