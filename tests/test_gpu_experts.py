@@ -104,6 +104,45 @@ def test_route_many_tokens(mx, t):
     check_route(mx, logits, 2, bias=(0.1 * rng.standard_normal(16)).astype(np.float32), scoring="softmax")
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("t,e,k,groups,top", [(1100, 256, 8, 8, 4), (1024, 64, 6, 1, 1), (1031, 96, 16, 3, 2),
+                                              (1500, 128, 1, 8, 1), (1200, 240, 5, 5, 5), (1025, 256, 17, 2, 1),
+                                              (1333, 16, 4, 1, 1), (1027, 256, 4, 16, 3), (1026, 200, 4, 1, 1)])
+def test_route_over_a_thousand_tokens(mx, t, e, k, groups, top, bias, scoring):
+    rng = np.random.default_rng(t * e)
+    x = 2 * rng.standard_normal((t, e))
+    x[rng.random((t, e)) < 0.02] = -np.inf
+    x[::97] = -np.inf
+    x[5::131, 1:] = -np.inf
+    x[3, 0], x[4, 1] = np.nan, np.inf
+    b = (0.2 * rng.standard_normal(e)).astype(np.float32) if bias else None
+    logits = on_gpu(x.astype(np.float32))
+    check_route(mx, logits, k, bias=b, scoring=scoring, n_groups=groups, topk_groups=top, scale=2.5)
+    check_route(mx, logits.bfloat16(), k, bias=b, scoring=scoring, n_groups=groups, topk_groups=top, renormalize=False)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_close_keys_over_a_thousand_tokens(mx, scoring):
+    """As the tests of ties and of neighbours, in many blocks."""
+    rng = np.random.default_rng(15)
+    grid = on_gpu((rng.integers(-4, 5, (1100, 128)) / 2).astype(np.float32))
+    tiny = (rng.integers(0, 3, 128) * 2.0**-26).astype(np.float32)
+    for b in (None, tiny):
+        for groups, top in ((1, 1), (8, 3)):
+            check_route(mx, grid.bfloat16(), 7, bias=b, scoring=scoring, n_groups=groups, topk_groups=top)
+    x = rng.standard_normal(64)
+    b = (0.5 - 1 / (1 + np.exp(-x))).astype(np.float32)
+    near = on_gpu((x + rng.integers(-2, 3, (1060, 64)) * 2.0**-24).astype(np.float32))
+    check_route(mx, near, 8, bias=b, scoring=scoring)
+    check_route(mx, near, 4, bias=b, scoring=scoring, n_groups=4, topk_groups=2)
+    # equal logits: more candidates than there are lanes; odd strides
+    check_route(mx, torch.zeros((1100, 256), device=dev()), 8, bias=np.zeros(256, np.float32), scoring=scoring)
+    check_route(mx, torch.zeros((1100, 64), device=dev()), 3, scoring=scoring)
+    wide = on_gpu(rng.standard_normal((1100, 131)).astype(np.float32))
+    check_route(mx, wide[:, 3:131], 6, bias=np.zeros(128, np.float32), scoring=scoring)
+
+
 def test_route_strides_types_and_guards(mx):
     rng = np.random.default_rng(14)
     wide = on_gpu(rng.standard_normal((70, 101)).astype(np.float32))
