@@ -273,7 +273,8 @@ enum Scoring : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 constexpr int kRouteMaxExperts = 512;
 constexpr int kRouteMaxTopK = 32;
 constexpr int kRouteChunks = 512;   // chunks of tokens whose rows are counted apart
-constexpr int kRouteOneBlock = 16;  // tokens that one block routes and orders
+constexpr int kRouteOneBlock = 8;       // tokens that one block routes and orders
+constexpr int kRouteDirectChunks = 16;  // chunks whose counts every block of the last kernel adds up itself
 // the handle's workspace: rows per (expert, chunk), rows per expert
 constexpr size_t kRouteWorkspace = sizeof(int) * (static_cast<size_t>(kRouteMaxExperts) * kRouteChunks + kRouteMaxExperts);
 
@@ -293,7 +294,7 @@ struct RouteArgs {
   int* counts;     // workspace [E][chunks]
   int* totals;     // workspace [E]
   // set by launch_route
-  int chunk, chunks, group_parts, shared_keys;
+  int chunk, chunks, group_parts, shared_keys, direct;
   FastDiv per_group;
 };
 cudaError_t launch_route(RouteArgs args, cudaStream_t stream);

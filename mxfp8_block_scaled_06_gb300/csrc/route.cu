@@ -87,15 +87,18 @@ __device__ __forceinline__ float score32(const RouteArgs& p, const Token& t, flo
 // The keys' score: approximate exp and reciprocal, a few units in the last place.
 __device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// Bound of |computed key - exact key| of the token's keys. Units are 2^-23. A score's
-// exp has an argument error of 1.2 units a unit of its argument u and 3 units more,
-// the sum of E <= 512 such terms and the reciprocal or division at most 20 more, so s
-// is off by s (26 + 1.2 u) units at most; with s <= s_top exp(-u) (softmax) or
-// s <= min(1, exp(-u)) (sigmoid, u = max(-x, 0)) that is below 27 s_top. Adding the
-// bias rounds once.
+// Bound of |computed key - exact key| of the token's keys, in units of 2^-23.
+// __expf(y) is within 2 + 1.18 |y| units (2 ulp and its argument's rounding),
+// __fdividef within 2, an addition or division within 0.5.
+//   sigmoid: s = 1 / D, D = 1 + exp(-x): relative (1 - s)(2 + 1.18 |x|) + 0.5 + 2, so
+//            absolute at most 0.61 + 2.5 (s (1 - s)(2 + 1.18 |x|) peaks at 0.61).
+//   softmax: u = top - x is rounded once: a term is off by 2 + 1.68 u, the sum of E <=
+//            512 terms (a softmax's mean u is at most ln E) by 12.6 + 21 roundings, the
+//            quotient by 1 more: s is off by s (26.1 + 1.68 u) <= 26.2 s_top.
+// The key adds 0.5 |s + bias|.
 __device__ __forceinline__ float keys_error(const RouteArgs& p, const Token& t, float largest_bias) {
-  const float top = p.scoring == kScoreSigmoid ? 1.f : t.sum > 0.f ? 1.f / t.sum : 0.f;
-  return (28.f * top + largest_bias) * 1.2e-7f + 1e-37f;
+  const float s = p.scoring == kScoreSigmoid ? 3.2f : t.sum > 0.f ? 26.2f / t.sum : 0.f;
+  return (s + 0.5f * (1.f + largest_bias)) * 1.2e-7f + 1e-37f;
 }
 
 // The parts of a token's selection in float64, for keys that float32 cannot tell
@@ -260,11 +263,11 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t bas
   const uint32_t in = __ballot_sync(kFull, mine && rank < p.topk_groups);
   const uint32_t next = __ballot_sync(kFull, mine && rank == p.topk_groups);
   if (p.bias == nullptr || next == 0) return in;
-  // the last one in and the first one out, and whatever is within reach of either:
-  // two sums are off by 2 far each and round once
+  // the last one in and the first one out, and whatever is within reach of either: two
+  // sums are off by 2 far each, and round by (1 + |bias|) units each, at most 2 far
   const uint32_t last = __ballot_sync(kFull, mine && rank == p.topk_groups - 1);
   const float x = __shfl_sync(kFull, best, __ffs(last) - 1), y = __shfl_sync(kFull, best, __ffs(next) - 1);
-  const float err = 6.f * far;
+  const float err = 8.f * far;
   if (!(y > -CUDART_INF_F) || x - y > err) return in;
   const uint32_t contended = __ballot_sync(kFull, mine && !(best - x > err) && !(y - best > err));
   return groups64(p, base, top, in & ~contended, contended, keys, far);
@@ -516,13 +519,34 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_scan_kernel(const __gr
   if ((threadIdx.x & 31) == 0) p.totals[e] = total;
 }
 
-// One block per chunk: its rows' places among all rows.
+// One block per chunk: its rows' places among all rows. With few chunks (p.direct) each
+// block adds up the chunks' counts itself and no scan kernel runs before it.
 __global__ void __launch_bounds__(kRouteWarps * 32) route_place_kernel(const __grid_constant__ RouteArgs p) {
   extern __shared__ double route_smem[];
   int* const base = reinterpret_cast<int*>(route_smem);
   pdl_launch_dependents();
   pdl_wait();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) base[e] = p.totals[e];
+  int before[kRouteMaxExperts / (kRouteWarps * 32)];  // rows of this thread's experts in earlier chunks
+#pragma unroll
+  for (int i = 0; i < kRouteMaxExperts / (kRouteWarps * 32); ++i) {
+    const int e = threadIdx.x + i * kRouteWarps * 32;
+    before[i] = 0;
+    if (e >= p.E) continue;
+    const int* const counts = p.counts + static_cast<size_t>(e) * p.chunks;
+    if (p.direct) {
+      int total = 0;
+#pragma unroll 8
+      for (int c = 0; c < p.chunks; ++c) {
+        const int n = counts[c];
+        total += n;
+        before[i] += c < static_cast<int>(blockIdx.x) ? n : 0;
+      }
+      base[e] = total;
+    } else {
+      base[e] = p.totals[e];
+      before[i] = counts[blockIdx.x];
+    }
+  }
   __syncthreads();
   if (threadIdx.x < 32) {
     const int rows = exclusive_scan(base, p.E);
@@ -532,8 +556,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_place_kernel(const __g
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-    base[e] += p.counts[static_cast<size_t>(e) * p.chunks + blockIdx.x];
+#pragma unroll
+  for (int i = 0; i < kRouteMaxExperts / (kRouteWarps * 32); ++i) {
+    const int e = threadIdx.x + i * kRouteWarps * 32;
+    if (e < p.E) base[e] += before[i];
+  }
   __syncthreads();
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   for (int r = t0 * p.top_k + threadIdx.x; r < t1 * p.top_k; r += blockDim.x) {
@@ -617,6 +644,7 @@ cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
   // a token to a warp, and at most kRouteChunks chunks
   p.chunk = p.T <= kRouteOneBlock ? p.T : std::max(kRouteWarps, (p.T + kRouteChunks - 1) / kRouteChunks);
   p.chunks = (p.T + p.chunk - 1) / p.chunk;
+  p.direct = p.chunks <= kRouteDirectChunks;
   p.group_parts = 32;
   while (p.group_parts * p.n_groups > 32) p.group_parts >>= 1;
   p.per_group = fast_div(p.E / p.n_groups);
@@ -631,8 +659,10 @@ cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
   else if (p.E <= 256) e = launch_pdl(route_kernel<8>, grid, threads, smem, stream, p);
   else e = launch_pdl(route_kernel<16>, grid, threads, smem, stream, p);
   if (e != cudaSuccess || p.chunks == 1) return e;
-  e = launch_pdl(route_scan_kernel, dim3((p.E + kRouteWarps - 1) / kRouteWarps), threads, 0, stream, p);
-  if (e != cudaSuccess) return e;
+  if (!p.direct) {
+    e = launch_pdl(route_scan_kernel, dim3((p.E + kRouteWarps - 1) / kRouteWarps), threads, 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(route_place_kernel, grid, threads, sizeof(int) * p.E, stream, p);
 }
 
