@@ -294,7 +294,7 @@ struct RouteArgs {
   int* counts;     // workspace [E][chunks]
   int* totals;     // workspace [E]
   // set by launch_route
-  int chunk, chunks, group_parts, shared_keys, direct;
+  int chunk, chunks, group_parts, group_regs, shared_keys, direct;
   FastDiv per_group;
 };
 cudaError_t launch_route(RouteArgs args, cudaStream_t stream);

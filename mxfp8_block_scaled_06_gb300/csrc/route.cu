@@ -44,7 +44,7 @@ constexpr int kRouteWarps = 8;
 // Order-preserving bits: a < b as floats <=> ord(a) < ord(b); never 0 for a number.
 __device__ __forceinline__ uint32_t ord32(float f) {
   const uint32_t b = __float_as_uint(f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unord32(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
@@ -235,11 +235,33 @@ __device__ __noinline__ uint32_t groups64(const RouteArgs& p, size_t base, float
   return in | __ballot_sync(kFull, (contended >> lane & 1u) && rank < p.topk_groups - __popc(in));
 }
 
-// The topk_groups groups of the largest key, or with a bias the largest sum of two
-// keys, as a bit mask. keys: the warp's E keys in shared memory, each off by `far`
-// at most.
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t base, float top,
-                                                  const volatile float* keys, float far) {
+// Each group's largest key, or with a bias the sum of its two largest, in lane g; for
+// groups of whole registers of the warp (32, 64, ... experts): two warp reductions a
+// group, where the keys in shared memory took 387 instructions a token in all.
+template <int V>
+__device__ __forceinline__ float best_of_registers(const RouteArgs& p, const uint32_t (&key)[V]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k1 = 0, k2 = 0, best1 = 0, best2 = 0;
+  int g = 0, left = p.group_regs;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    k2 = max(k2, min(k1, key[i]));
+    k1 = max(k1, key[i]);
+    if (--left == 0) {
+      const uint32_t w1 = __reduce_max_sync(kFull, k1);
+      const uint32_t owner = __ffs(__ballot_sync(kFull, k1 == w1)) - 1;
+      const uint32_t w2 = __reduce_max_sync(kFull, static_cast<uint32_t>(lane) == owner ? k2 : k1);
+      if (lane == g) best1 = w1, best2 = w2;
+      k1 = k2 = 0;
+      left = p.group_regs;
+      ++g;
+    }
+  }
+  return p.bias == nullptr ? unord32(best1) : unord32(best1) + unord32(best2);
+}
+
+// The same for any groups, from the warp's E keys in shared memory.
+__device__ __forceinline__ float best_of_shared(const RouteArgs& p, const volatile float* keys) {
   const int lane = threadIdx.x & 31;
   const int parts = p.group_parts;  // lanes per group, a power of two
   const int g = lane / parts, part = lane & (parts - 1);
@@ -251,9 +273,15 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t bas
     const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
     merge_top2<float>(a1, a2, b1, b2);
   }
-  // lane j: group j's best
   const float whole = p.bias == nullptr || size == 1 ? a1 : a1 + a2;
-  const float best = lane < p.n_groups ? __shfl_sync(kFull, whole, lane * parts) : __shfl_sync(kFull, whole, 0);
+  return __shfl_sync(kFull, whole, lane < p.n_groups ? lane * parts : 0);
+}
+
+// The topk_groups groups of the largest `best` (lane g: group g's), as a bit mask.
+// *contended: the groups whose sums float32 cannot rank where it matters, of which
+// none is in the mask; 0 if there are none.
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, float best, float far, uint32_t* contended) {
+  const int lane = threadIdx.x & 31;
   int rank = 0;
   for (int j = 0; j < p.n_groups; ++j) {
     const float b = __shfl_sync(kFull, best, j);
@@ -262,6 +290,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t bas
   const bool mine = lane < p.n_groups;
   const uint32_t in = __ballot_sync(kFull, mine && rank < p.topk_groups);
   const uint32_t next = __ballot_sync(kFull, mine && rank == p.topk_groups);
+  *contended = 0;
   if (p.bias == nullptr || next == 0) return in;
   // the last one in and the first one out, and whatever is within reach of either: two
   // sums are off by 2 far each, and round by (1 + |bias|) units each, at most 2 far
@@ -269,8 +298,8 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, size_t bas
   const float x = __shfl_sync(kFull, best, __ffs(last) - 1), y = __shfl_sync(kFull, best, __ffs(next) - 1);
   const float err = 8.f * far;
   if (!(y > -CUDART_INF_F) || x - y > err) return in;
-  const uint32_t contended = __ballot_sync(kFull, mine && !(best - x > err) && !(y - best > err));
-  return groups64(p, base, top, in & ~contended, contended, keys, far);
+  *contended = __ballot_sync(kFull, mine && !(best - x > err) && !(y - best > err));
+  return in & ~*contended;
 }
 
 // The selection of one token: lane j < top_k returns the j-th expert and its weight.
@@ -319,12 +348,26 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
   uint32_t open = kFull;
   if (p.n_groups > 1) {
     volatile float* const keys = reinterpret_cast<volatile float*>(shared);
-    __syncwarp();
+    auto share_keys = [&]() {
+      __syncwarp();
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < p.E) keys[lane + 32 * i] = x[i];
-    __syncwarp();
-    open = choose_groups(p, base, t.top, keys, far);
+      for (int i = 0; i < V; ++i)
+        if (lane + 32 * i < p.E) keys[lane + 32 * i] = x[i];
+      __syncwarp();
+    };
+    float best;
+    if (p.group_regs > 0) {
+      best = best_of_registers<V>(p, key);
+    } else {
+      share_keys();
+      best = best_of_shared(p, keys);
+    }
+    uint32_t contended;
+    open = choose_groups(p, best, far, &contended);
+    if (contended != 0) {
+      share_keys();
+      open = groups64(p, base, t.top, open, contended, keys, far);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (!(open >> (groups[i / 6] >> (5 * (i % 6)) & 31u) & 1u)) key[i] = 0u;  // no closed expert is taken
@@ -648,6 +691,7 @@ cudaError_t launch_route(RouteArgs p, cudaStream_t stream) {
   p.group_parts = 32;
   while (p.group_parts * p.n_groups > 32) p.group_parts >>= 1;
   p.per_group = fast_div(p.E / p.n_groups);
+  p.group_regs = p.E / p.n_groups % 32 == 0 ? p.E / p.n_groups / 32 : 0;
   p.shared_keys = std::max(p.E, 32);  // per warp: its keys, or 32 candidates
   const size_t smem = sizeof(double) * kRouteWarps * p.shared_keys + sizeof(int) * p.E;
   const dim3 grid(p.chunks);
