@@ -624,11 +624,13 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) {
   GemmFp4Plan pl{};
   const int kt = a_fp4 ? 2 : 1;
-  // Token tile: the rows of an expert in as few tiles of at most kMaxNt as they
-  // take, balanced; with several experts, room for twice the mean. A plain product
-  // takes more and narrower tiles where that saves time in its last wave: a tile
-  // costs about its rows and 100 more.
-  const long want = E == 1 ? R : std::min<long>(R, 2L * ((R + E - 1) / E));
+  // Token tile. A plain product takes its rows in as few tiles of at most kMaxNt as
+  // they take, balanced, or more and narrower ones where that saves time in its last
+  // wave: a tile costs about its rows and 100 more. Several experts: a third more
+  // than the mean (an expert with more rows takes several balanced tiles). With 64
+  // experts of 4096 x 2048, gated, us with twice the mean / with this: 512 tokens to 6
+  // each 68 / 55 (MXFP4 rows 60 / 50), 1024 76 / 73 (74 / 61).
+  const long want = E == 1 ? R : std::min<long>({R, 4L * ((R + E - 1) / E) / 3, kMaxNt});
   long tt = (want + kMaxNt - 1) / kMaxNt;
   if (E == 1 && want > kMaxNt / 2) {
     const int at_once = N % 256 == 0 ? sm_count / 2 : sm_count;
