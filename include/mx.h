@@ -358,7 +358,10 @@ int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, in
  *   w, w_scales  MXFP4 weights [N, K] packed, scales in the 128x4 layout; both
  *                32-byte aligned
  *   flags        MX_FLAG_PDL or 0, as for mx_gemm
- * Constraints: 1 <= M <= 2^24, N % 128 == 0, K % 128 == 0, else MX_ERR_UNSUPPORTED. */
+ * Up to 256 rows the call takes mx_gemm's kernel (K split over a cluster) where that is
+ * the faster one, otherwise a kernel of whole-K tiles.
+ * Constraints: 1 <= M <= 2^24, N % 128 == 0, K % 128 == 0, (N / 128) (M / 16 + 1) < 2^31,
+ * else MX_ERR_UNSUPPORTED. */
 int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_scales, int a_fp4,
                 const void* w, const void* w_scales, void* out, unsigned flags, void* stream);
 
@@ -378,7 +381,7 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
  *   gated        0: out is [R, N]. Otherwise weight rows 2i and 2i + 1 are gate i and
  *                up i, and out is [R, N/2]: silu(gate) * up, from the float32 products
  * Constraints: N % 128 == 0, K % 128 == 0, E <= 512, R and a_rows <= 2^24,
- * E * N < 2^31, else MX_ERR_UNSUPPORTED. */
+ * E * N < 2^31, (N / 128) (R / 16 + E) < 2^31, else MX_ERR_UNSUPPORTED. */
 int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a, int a_rows,
                         const void* a_scales, int a_fp4, const void* w, const void* w_scales,
                         const int* offsets, const int* tokens, int gated, void* out, void* stream);

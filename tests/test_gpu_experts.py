@@ -176,13 +176,7 @@ def experts_case(rng, counts, rows_a, k, n, fp4, gather):
     return args, ref, k * 2.0**-22 * size
 
 
-@pytest.mark.parametrize("gated", [False, True])
-@pytest.mark.parametrize("fp4", [False, True])
-@pytest.mark.parametrize("counts,rows_a,k,n,gather", [
-    ([1], 1, 128, 128, True), ([0, 3, 0, 0, 1, 0], 4, 384, 256, True), ([1] * 40, 8, 512, 128, True),
-    ([5, 16, 17, 0, 33, 2], 30, 640, 256, True), ([130, 0, 1, 300], 200, 256, 128, True),
-    ([224, 225, 448, 7], 500, 128, 128, True), ([3, 0, 50], 0, 896, 384, False), ([700, 13], 0, 256, 128, False)])
-def test_grouped_product(mx, counts, rows_a, k, n, gather, fp4, gated):
+def check_grouped(mx, counts, rows_a, k, n, gather, fp4, gated):
     rng = np.random.default_rng(sum(counts) + k)
     args, y, err = experts_case(rng, counts, rows_a, k, n, fp4, gather)
     r, cols = len(y), n // 2 if gated else n
@@ -200,6 +194,26 @@ def test_grouped_product(mx, counts, rows_a, k, n, gather, fp4, gated):
     d = np.abs(out.float().cpu().numpy().astype(np.float64) - ref)
     assert (d <= tol).all(), (d / tol).max()
     assert intact(ob, r * cols * 2)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,k,n", [([200, 90, 0, 431], 640, 256), ([100, 160], 128, 512), ([70, 224, 225], 256, 256),
+                                        ([97], 1408, 768), ([0, 0, 500, 0], 896, 256), ([97, 31], 384, 384)])
+def test_grouped_product_of_wide_tiles(mx, counts, k, n, gather, fp4, gated):
+    """Pairs of SMs (256 weight rows at a time) and single ones (384), K of one stage and more."""
+    check_grouped(mx, counts, 150, k, n, gather, fp4, gated)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("counts,rows_a,k,n,gather", [
+    ([1], 1, 128, 128, True), ([0, 3, 0, 0, 1, 0], 4, 384, 256, True), ([1] * 40, 8, 512, 128, True),
+    ([5, 16, 17, 0, 33, 2], 30, 640, 256, True), ([130, 0, 1, 300], 200, 256, 128, True),
+    ([224, 225, 448, 7], 500, 128, 128, True), ([3, 0, 50], 0, 896, 384, False), ([700, 13], 0, 256, 128, False)])
+def test_grouped_product(mx, counts, rows_a, k, n, gather, fp4, gated):
+    check_grouped(mx, counts, rows_a, k, n, gather, fp4, gated)
 
 
 def test_grouped_rows_outside(mx):
@@ -242,6 +256,38 @@ def test_combine(mx, t, k, n, residual, pad):
         assert torch.equal(res, out)
 
 
+def test_grouped_product_past_32_bit_offsets(mx):
+    """Five gigabytes of weights: rows of the first and of the last experts."""
+    rng = np.random.default_rng(21)
+    e, n, k, r = 40, 8192, 32768, 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randint(0, 256, (e, n, k // 2), generator=g, device=dev(), dtype=torch.uint8)
+    s = torch.randint(120, 124, (e, n * k // 32), generator=g, device=dev(), dtype=torch.uint8)
+    aq, as_, av = operand(rng, r, k, True, 0)
+    counts = np.zeros(e, np.int64)
+    counts[[0, e - 2, e - 1]] = 1, 2, 2
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    out = mx.mx_gemm_fp4_grouped(handle(), on_gpu(aq), on_gpu(as_), w, s, on_gpu(offsets)).double().cpu().numpy()
+    assert mx.mx_device_status(handle()) == mx.MX_OK
+    which = np.repeat(np.arange(e), counts)
+    for i, c in enumerate(which):
+        rows = rng.integers(0, n, 64)
+        q = w[c][on_gpu(rows)].cpu().numpy()
+        plain = s[c].view(n // 128, k // 128, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(n, k // 32)
+        wv = ox.decode_fp4(q, plain[on_gpu(rows)].cpu().numpy())
+        ref, size = wv @ av[i], np.abs(wv) @ np.abs(av[i])
+        assert (np.abs(out[i, rows] - ref) <= 2.0**-8 * np.abs(ref) + k * 2.0**-22 * size).all()
+
+
+def test_combine_past_32_bit_offsets(mx):
+    r, n = 300_000, 8192
+    y = torch.zeros((r, n), dtype=torch.bfloat16, device=dev())
+    slots = torch.tensor([[r - 1, 0], [r - 2, 262_144]], dtype=torch.int32, device=dev())
+    y[slots.long().reshape(-1)] = torch.arange(1, 5, device=dev()).bfloat16()[:, None].expand(4, n)
+    out = mx.mx_combine(handle(), y, slots, torch.ones((2, 2), device=dev()))
+    assert out[0].eq(3).all() and out[1].eq(7).all()
+
+
 def test_combine_slots_outside(mx):
     y = torch.ones((4, 64), dtype=torch.bfloat16, device=dev())
     slots = on_gpu(np.array([[0, 4], [-1, 3]], np.int32))
@@ -274,7 +320,8 @@ def test_c_entry_refusals(mx):
     for kw in (dict(e=0), dict(r=0), dict(rows=0), dict(k=100), dict(a=None), dict(off=None), dict(tok=None, rows=3),
                dict(a=p + 8), dict(w=p + 16), dict(out=o + 8), dict(off=p + 2), dict(tok=p + 1)):
         assert grouped(**kw) == bad, kw
-    for kw in (dict(n=64), dict(k=160), dict(e=513), dict(r=(1 << 24) + 1), dict(e=512, n=1 << 22)):
+    for kw in (dict(n=64), dict(k=160), dict(e=513), dict(r=(1 << 24) + 1), dict(e=512, n=1 << 22),
+               dict(e=1, r=1 << 24, n=1 << 18, rows=1 << 24)):
         assert grouped(**kw) == no, kw
 
     def combine(t=2, k=2, n=64, y=p, r=4, ldy=64, s=p, w=p, res=None, out=o):

@@ -108,7 +108,8 @@ def bound(a, w, ref):
 @pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("m,n,k", [(1, 128, 128), (1, 2048, 5120), (3, 256, 384), (8, 8192, 1536), (16, 128, 4096),
                                    (17, 384, 640), (33, 128, 128), (129, 256, 896), (201, 640, 1024), (256, 128, 256),
-                                   (257, 256, 512), (300, 128, 1152), (449, 384, 2176), (1000, 1280, 384)])
+                                   (257, 256, 512), (300, 128, 1152), (449, 384, 2176), (1000, 1280, 384),
+                                   (230, 512, 128), (700, 256, 256), (90, 16384, 128), (40, 16384, 384)])
 def test_product(mx, m, n, k, fp4):
     rng = np.random.default_rng(m + n + k)
     aq, as_, av = operand(rng, m, k, fp4)
