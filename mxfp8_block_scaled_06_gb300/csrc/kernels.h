@@ -273,8 +273,12 @@ enum Scoring : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 constexpr int kRouteMaxExperts = 512;
 constexpr int kRouteMaxTopK = 32;
 constexpr int kRouteChunks = 512;   // chunks of tokens whose rows are counted apart
-constexpr int kRouteOneBlock = 8;       // tokens that one block routes and orders
-constexpr int kRouteDirectChunks = 16;  // chunks whose counts every block of the last kernel adds up itself
+// Tokens that one block routes and orders in one launch, and chunks whose counts every
+// block of the last kernel adds up itself, without a scan kernel. Measured with 8 of
+// 256 experts, us: 8 tokens 6.8 in one launch; 16 tokens 10.9 in one launch, 8.0 in two,
+// 9.7 in three; 128 tokens (16 chunks) 9.5 in two, 9.9 in three; 256 tokens 13.2 and 10.2.
+constexpr int kRouteOneBlock = 8;
+constexpr int kRouteDirectChunks = 16;
 // the handle's workspace: rows per (expert, chunk), rows per expert
 constexpr size_t kRouteWorkspace = sizeof(int) * (static_cast<size_t>(kRouteMaxExperts) * kRouteChunks + kRouteMaxExperts);
 

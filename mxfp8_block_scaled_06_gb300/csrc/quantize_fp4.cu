@@ -26,9 +26,10 @@ namespace {
 
 constexpr int kThreads = 256;
 // From this many units on (8 Mi elements) a thread takes four, whose loads are in
-// flight together: 16381 x 8192 bf16 70.7 -> 55.2 us, with y 103 -> 89 us (6.8 TB/s, a
-// plain copy's rate); below, more blocks serve better. Streaming loads and stores
-// (.cs) were slower: 62 and 95 us.
+// flight together: 16381 x 8192 bf16 70.7 -> 57.5 us, with y 103 -> 90 us (6.7 TB/s, a
+// plain copy's rate), 1024 x 8192 4.9 -> 4.2 us; 512 x 8192 takes 3.7 us either way and
+// smaller calls need the blocks. Streaming loads and stores (.cs) were slower: 62 and
+// 95 us.
 constexpr uint32_t kManyUnits = 1u << 20;
 
 // n / d for the d that (mul, shift) was made for (host: fast_div).
