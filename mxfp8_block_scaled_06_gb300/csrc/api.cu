@@ -86,18 +86,6 @@ constexpr size_t kSsqBytes = size_t{64} << 10;
 // rows of the MXFP4 products, and (token, choice) rows of the router: tile and row
 // numbers are 32-bit
 constexpr int kMaxFp4Rows = 1 << 24;
-// Whether mx_gemm_fp4 splits K over a cluster (gemm.cu, up to 256 rows) instead of
-// walking whole-K tiles (gemm_fp4.cu). S splits save (1 - 1 / S) of a tile's way through
-// K, about 0.18 us (MXFP4 rows 0.11 us) for 128 elements, and cost about 1 us and
-// 0.016 us a row to exchange the partial sums. Measured on GB300, split / whole us with
-// MXFP8 rows (MXFP4 rows): N = 2048, K = 5120 5.3 / 10.3 (4.8 / 6.8) at one row, 8.4 /
-// 10.9 (7.6 / 8.5) at 128, 10.6 / 10.8 (9.3 / 8.4) at 201; N = 4096, K = 4096 8.9 / 9.7
-// (7.7 / 8.0) at 128, 10.8 / 10.6 (9.8 / 8.7) at 201; N = 8192, K = 1536 4.9 / 5.4 (4.4 /
-// 4.2) at one row, 7.2 / 7.1 (6.7 / 6.4) at 96; N = K = 512 3.6 / 3.3 at one row.
-bool fp4_split_k(int M, int K, int a_fp4, const mx::GemmPlan& plan) {
-  const long saved_ns = (a_fp4 ? 110L : 180L) * (K / 128) * (plan.splits - 1) / plan.splits;
-  return plan.smem <= mx::kMaxDynamicSmem && saved_ns > 1000 + 16L * M;
-}
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -271,6 +259,7 @@ int gemm_prepare(mx_handle* h, GemmLaunch* L, int M, int N, int K, const void* a
   args.K = K;
   args.w_fmt = w_fmt;
   args.mtile = L->plan.mtile;
+  args.slice = L->plan.slice;
   args.stages = L->plan.stages;
   args.nchunks = w_fmt == 2 ? (K / 128 + 1) / 2 : K / 128;
   args.tmem_cols = L->plan.tmem_cols;
@@ -428,6 +417,7 @@ int mx_create(mx_handle** out, int device) {
       // every CTA of the chain kernel must be resident at once: the largest
       // number of its clusters that fit (16 at most are used)
       if (rc == MX_OK) h->chain_clusters = std::min(16, mx::chain_max_clusters());
+      for (int s = 2; rc == MX_OK && s <= 8; ++s) h->env.clusters[s] = mx::gemm_max_clusters(s);
     }
   }
   if (rc != MX_OK && h != nullptr) {
@@ -881,10 +871,13 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
     return MX_ERR_INVALID_ARG;
   if (N % 128 != 0 || K % 128 != 0 || M > kMaxFp4Rows) return MX_ERR_UNSUPPORTED;
   const int fmt = a_fp4 ? 2 : 1;
-  if (M <= 256 && fp4_split_k(M, K, a_fp4, get_plan(h, M, N, K, false, false, mx::kPushFull, true, fmt))) {
+  // behind a kernel that it overlaps the push exchange is the faster (gemm.cu)
+  const int push = flags & MX_FLAG_PDL ? mx::kPushFull : mx::kPushNone;
+  const mx::GemmPlan plan = get_plan(h, M, N, K, false, false, push, true, fmt);
+  if (plan.splits > 1 && plan.smem <= mx::kMaxDynamicSmem) {
     GemmLaunch L;
     rc = gemm_prepare(h, &L, M, N, K, a, a_scales, w, w_scales, out, nullptr, nullptr, 0, nullptr, 0, 1, nullptr,
-                      mx::kPushFull, true, fmt);
+                      push, true, fmt);
     return rc != MX_OK ? rc : gemm_run(h, &L, (flags & MX_FLAG_PDL) != 0, static_cast<cudaStream_t>(stream));
   }
   mx::GemmFp4Args args = {};

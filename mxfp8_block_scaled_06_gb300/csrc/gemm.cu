@@ -202,6 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile = blockIdx.x;
   const int S = gridDim.y;
   const int split = blockIdx.y;
+  // MXFP4 weights: blockIdx.z takes its slice of the rows
+  const int m_first = kFmt == kFmtMx8 ? 0 : static_cast<int>(blockIdx.z) * p.slice;
+  const int M = kFmt == kFmtMx8 ? p.M : min(p.slice, p.M - m_first);
   const int c_begin = split * p.nchunks / S;
   const int n = (split + 1) * p.nchunks / S - c_begin;
   const int stages = p.stages;
@@ -210,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool norm = kFusedA && p.norm.gamma != nullptr;
   constexpr bool kPush = kRed == kReducePush || kRed == kReducePushCompact;
   constexpr bool compact = kRed == kReducePushCompact;
-  const PushGeometry pgeo(p.M, kPush ? S : 1, kPush ? split : 0);
+  const PushGeometry pgeo(M, kPush ? S : 1, kPush ? split : 0);
   const uint32_t slot = pgeo.slot;
-  const Layout L(p.mtile, stages, (p.nchunks + S - 1) / S, kFusedA, min(p.M, kRowBatch),
-                 norm ? p.K / 32 : 0, kPush ? push_area_bytes(p.M, S, compact) : 0u, sf_tiles(kFmt));
+  const Layout L(p.mtile, stages, (p.nchunks + S - 1) / S, kFusedA, min(M, kRowBatch),
+                 norm ? p.K / 32 : 0, kPush ? push_area_bytes(M, S, compact) : 0u, sf_tiles(kFmt));
   // scale tiles along K, of all and of this CTA's chunks (MXFP4 activations: the last chunk may be half a one)
   const int units = kFmt == kFmtMx8 ? p.nchunks : p.K >> 7;
   const int n_units = kFmt == kFmtMx8 ? n : min(n * sf_tiles(kFmt), units - c_begin * sf_tiles(kFmt));
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto issue_a = [&](int i, int s) {
     mbar_expect_tx(full(s), L.a_bytes);
-    tma_load_2d(base + L.a_off(s), &tm_a, full(s), a_k0 + (c_begin + i) * 128, 0, pol_a);
+    tma_load_2d(base + L.a_off(s), &tm_a, full(s), a_k0 + (c_begin + i) * 128, m_first, pol_a);
     last = i;
   };
 
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int q_tpb = 1, q_row0 = 0, q_blk0 = 0, q_drow = 0, q_dblk = 0;
   if constexpr (kFusedA) {
     const int bpr = n * 4;
-    const int total0 = min(p.M, kRowBatch) * bpr;
+    const int total0 = min(M, kRowBatch) * bpr;
     q_tpb = total0 * 8 <= kThreads ? 8 : total0 * 4 <= kThreads ? 4 : total0 * 2 <= kThreads ? 2 : 1;
     const int w = static_cast<int>(threadIdx.x) / q_tpb, dw = kThreads / q_tpb;
     q_row0 = w / bpr;
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kFusedA) {
     // shared memory only, so before the wait: zero rows [M, mtile) of every
     // activation chunk tile, and the activation scale tiles
-    for (int idx = threadIdx.x; idx < n * (p.mtile - p.M) * 8; idx += kThreads) {
-      const int i = idx / ((p.mtile - p.M) * 8), rem = idx % ((p.mtile - p.M) * 8);
-      const int m = p.M + rem / 8;
+    for (int idx = threadIdx.x; idx < n * (p.mtile - M) * 8; idx += kThreads) {
+      const int i = idx / ((p.mtile - M) * 8), rem = idx % ((p.mtile - M) * 8);
+      const int m = M + rem / 8;
       *reinterpret_cast<uint4*>(base_ptr + L.act + i * L.a_bytes + m * 128 + (rem % 8) * 16) =
           make_uint4(0, 0, 0, 0);
     }
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_expect_tx(sfb_bar, static_cast<uint32_t>(n_units * nsfb) * kSfTileBytes);
       for (int rt = 0; rt < nsfb; ++rt)
         bulk_load(base + L.sfb_off(rt, 0),
-                  p.a_scales + (static_cast<size_t>(rt) * p.a_sf_chunks + a_k0 / 128 +
+                  p.a_scales + (static_cast<size_t>(m_first / 128 + rt) * p.a_sf_chunks + a_k0 / 128 +
                                 c_begin * sf_tiles(kFmt)) * kSfTileBytes,
                   static_cast<uint32_t>(n_units) * kSfTileBytes, sfb_bar, pol_a);
     }
@@ -382,11 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool norm_out = norm && tile == 0;  // tile 0 writes y and the activation
     const int nblk = p.K >> 5;                // 32-blocks of a whole row (the norm's sum)
     const int blocks_per_row = n * 4;         // 32-blocks in the K-range
-    for (int r0 = 0, batch = 0; r0 < p.M; r0 += kRowBatch, ++batch) {
+    for (int r0 = 0, batch = 0; r0 < M; r0 += kRowBatch, ++batch) {
       // every thread reads the flag after the previous batch's barrier: once a
       // wait has expired no further row batch is requested
       if (*abort_flag != 0) break;
-      const int rb = min(kRowBatch, p.M - r0);
+      const int rb = min(kRowBatch, M - r0);
       const bool gam = norm && batch == 0;  // the norm weight's K-range comes with batch 0
       if (warp == 3) {
         // one lane per row: each row's K-range is contiguous; with the norm, lane
@@ -410,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (gam && norm_out && p.norm.a_q_scales != nullptr) {
         // padding rows [M, ceil128(M)) of the K-range's scale columns
-        const int mpad = (p.M + 127) & ~127;
-        for (int idx = threadIdx.x; idx < (mpad - p.M) * n * 4; idx += kThreads)
-          p.norm.a_q_scales[swz_offset(p.M + idx / (n * 4), c_begin * 4 + idx % (n * 4), nblk)] = 0;
+        const int mpad = (M + 127) & ~127;
+        for (int idx = threadIdx.x; idx < (mpad - M) * n * 4; idx += kThreads)
+          p.norm.a_q_scales[swz_offset(M + idx / (n * 4), c_begin * 4 + idx % (n * 4), nblk)] = 0;
       }
       if (!mbar_wait(x_bar, batch & 1)) fail();
       if (batch == 0 && threadIdx.x == 0) MX_TL(14, globaltimer());
@@ -770,11 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------- cluster reduction + bf16 (+ MXFP8) store
   if (ok) {
     const uint32_t red_addr = smem_u32(red);
-    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out);
+    __nv_bfloat16* const out =
+        p.out != nullptr ? static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(m_first) * p.N : nullptr;
     // Item = 32 columns of one row. An item nobody consumes is not reduced: a
     // peer's shared memory is read only for a value that is then used, so no
     // read is in flight when the peers exit.
-    auto wanted = [&](int item) { return item < p.M * 4 && want_q(item & 3); };
+    auto wanted = [&](int item) { return item < M * 4 && want_q(item & 3); };
     auto item_addr = [&](int item) {
       return red_addr + static_cast<uint32_t>((item >> 2) * 128 + (item & 3) * 32 + lane) * 4u;
     };
@@ -811,15 +815,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if constexpr (kPush) {
       push_sum<compact>(pgeo, warp, kThreads / 32, lane, push, own, want_q, emit);
-    } else if (p.M <= S) {
+    } else if (M <= S) {
       // at most one item per warp
-      for (int item = split + S * warp; item < p.M * 4; item += 4 * S)
+      for (int item = split + S * warp; item < M * 4; item += 4 * S)
         if (wanted(item)) emit(item, cluster_sum(item_addr(item), S));
     } else if (kRed == kReduceItems) {
       // several items per warp: four items' peer loads in flight at once (the
       // warp is alone on its scheduler, so one item at a time would be
       // latency-bound), each still summed in rank order
-      for (int i0 = split + S * warp; i0 < p.M * 4; i0 += 4 * S * kSumBatch) {
+      for (int i0 = split + S * warp; i0 < M * 4; i0 += 4 * S * kSumBatch) {
         uint32_t offs[kSumBatch];
         bool use[kSumBatch];
         float sums[kSumBatch];
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int r = 0; r < 8; ++r) rank_base[r] = r < S ? map_shared_rank(red_addr, r) : 0u;
       const int col0 = tile * 128 + lane * 4;  // the lane's first output column
-      for (int m0 = split + S * warp; row_wanted && m0 < p.M; m0 += 4 * S * kRedRows) {
+      for (int m0 = split + S * warp; row_wanted && m0 < M; m0 += 4 * S * kRedRows) {
         float4 acc[kRedRows];
 #pragma unroll
         for (int b = 0; b < kRedRows; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -858,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int m = m0 + b * 4 * S;
-              v[b][r] = m < p.M && r0 + r < S
+              v[b][r] = m < M && r0 + r < S
                             ? ld_shared_cluster_v4(rank_base[r0 + r] + static_cast<uint32_t>(m * 512 + lane * 16))
                             : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -876,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < kRedRows; ++b) {
           const int m = m0 + b * 4 * S;
-          if (m >= p.M) break;  // warp-uniform
+          if (m >= M) break;  // warp-uniform
           const float a4[4] = {acc[b].x, acc[b].y, acc[b].z, acc[b].w};
           uint32_t hb[4];
           float v4[4];
@@ -928,9 +932,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kRequant && split == 0 && tile * 128 < p.q_cols) {
       // padding rows of this tile's four scale columns
-      const int mpad = (p.M + 127) & ~127;
-      for (int idx = threadIdx.x; idx < (mpad - p.M) * 4; idx += kThreads) {
-        const int m = p.M + (idx >> 2);
+      const int mpad = (M + 127) & ~127;
+      for (int idx = threadIdx.x; idx < (mpad - M) * 4; idx += kThreads) {
+        const int m = M + (idx >> 2);
         p.q_scales[swz_offset(m, tile * 4 + (idx & 3), p.q_cols >> 5)] = 0;
       }
     }
@@ -1047,12 +1051,63 @@ PlanEnv read_plan_env() {
   return env;
 }
 
+// K-splits of a product with MXFP4 weights, and the rows that a cluster takes: those
+// with the least time on top of what any launch costs, in ns. A tile's way through K
+// takes 180 (MXFP4 rows 110) for 128 elements, a third more with over 128 rows, and the
+// splits' exchange 1300 and 12 a row (22 with more than four splits). More clusters than
+// the device holds at once with one CTA to an SM (of 152 SMs 76 of two CTAs, 46, 36, 28,
+// 23, 15 and 15 of eight) run two to an SM where both fit: a quarter more for the way, and
+// 4 a row (with more than four splits 250 and 14 a row). One split: no gain, whole-K
+// tiles (gemm_fp4.cu, 800 more from 65 rows on) are the faster.
+// Measured on GB300, us with MXFP8 rows and 2 / 3 / 4 / 6 / 8 splits: N = 1024, K = 10368
+// 11.8 / 9.1 / 7.9 / 6.7 / 6.1 at one row, 14.9 / 11.9 / 10.6 / 10.2 / 9.8 at 128; N = 2048,
+// K = 5120 7.7 / 6.6 / 5.9 / 5.1 / 5.5 (two to an SM) at one row, 9.2 / 8.0 / 7.2 / 6.9 / 7.6
+// at 64, whole K 10.3 and 11.1; two to an SM: N = 8192, K = 8192, four splits 8.1 at one
+// row, whole K 10.1; N = 6144, K = 5120 6.5, two splits with one CTA to an SM 7.8. Slices
+// of 128 rows / one of all: N = 1024, K = 10368, 256 rows 10.7 / 14.4; N = 5120, K = 8192,
+// 201 rows, three splits 15.3 / 14.4. N = 256, K = 16000, 344 rows 10.7, whole K 24.4.
+struct W4Split {
+  int slice, splits;
+};
+W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4) {
+  const int sft = a_fp4 ? 2 : 1, chunks = (K / 128 + sft - 1) / sft;
+  const long walk = (a_fp4 ? 110L : 180L) * (K / 128);
+  W4Split best{std::min(M, 128), 1};
+  long least = walk + (M > 64 ? 800 : 0);
+  for (int slice : {std::min(M, 128), std::min(M, 256)}) {
+    const long clusters = static_cast<long>(N / 128) * ((M + slice - 1) / slice);
+    for (int s = 2; s <= std::min(slice > 128 ? 4 : 8, chunks); ++s) {
+      const bool two = clusters > env.clusters[s];  // CTAs to an SM
+      if (two && (slice > 64 || clusters > 2 * env.clusters[s])) continue;
+      // a CTA's scale tiles stay in shared memory (plan_for)
+      if (static_cast<long>((chunks + s - 1) / s) * sft * kSfTileBytes * (slice > 128 ? 3 : 2) > 48 * 1024) continue;
+      const long way = walk * (slice > 128 ? 16 : two ? 15 : 12) / (12 * s);
+      const long exchange = s > 4 ? (two ? 1550 + 36L * slice : 1300 + 22L * slice) : 1300 + (two ? 16L : 12L) * slice;
+      if (way + exchange < least) {
+        least = way + exchange;
+        best = {slice, s};
+      }
+    }
+  }
+  return best;
+}
+
 GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool fused_a, bool norm,
                    int push_mode, bool table_depth, int w_fmt) {
   int force_splits, force_stages;
   plan_override(env.plan_at, N, K, &force_splits, &force_stages);
+  const W4Split w4 = w_fmt != kFmtMx8 ? w4_split(M, N, K, env, w_fmt == kFmtW4A4) : W4Split{M, 1};
+  const int slices = (M + w4.slice - 1) / w4.slice;
+  if (w_fmt != kFmtMx8 && slices > 2) force_splits = 0;  // overrides are for the decode shapes
+  const int env_splits = w_fmt != kFmtMx8 && slices > 2 ? 0 : env.splits;
+  if (w_fmt != kFmtMx8 && (env_splits | force_splits) <= 1 && w4.splits == 1) {
+    GemmPlan whole{};
+    whole.splits = 1;
+    return whole;
+  }
+  M = w4.slice;  // rows of a cluster
   const int mtile = (M + 15) & ~15;
-  const int tiles = N / 128;
+  const int tiles = N / 128 * slices;
   const int sft = sf_tiles(w_fmt);
   const int nchunks = (K / 128 + sft - 1) / sft;
   const int nsfb = (mtile + 127) / 128;
@@ -1066,6 +1121,8 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
   auto plan_for = [&](int splits) {
     GemmPlan pl{};
     pl.mtile = mtile;
+    pl.slice = M;
+    pl.slices = slices;
     while (splits < std::min(8, nchunks) && scale_bytes(splits) > 48 * 1024) ++splits;
     pl.splits = splits;
     const int per_cta = (nchunks + splits - 1) / splits;
@@ -1076,7 +1133,8 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     // Short K-ranges (all chunks in flight at once): about 100 KB per CTA, so
     // the next kernel's CTAs fit beside this one. Long ones: as deep a ring as
     // lets the whole grid be resident in one wave (CTAs per SM x shared memory).
-    const int per_sm = (tiles * splits + sm_count - 1) / std::max(sm_count, 1);
+    const int per_sm = std::max((tiles * splits + sm_count - 1) / std::max(sm_count, 1),
+                                w_fmt != kFmtMx8 && tiles > env.clusters[splits] ? 2 : 1);
     const size_t wave = per_sm <= 1 ? 180 * 1024 : 227 * 1024 / static_cast<size_t>(per_sm) - 4 * 1024;
     const size_t budget = per_cta <= 8 ? std::min<size_t>(100 * 1024, wave) : wave;
     int stages = budget > scales ? static_cast<int>((budget - scales) / L1.stage_bytes) : 0;
@@ -1092,9 +1150,10 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     // the push reduction (where asked for and its receive area fits)
     const uint32_t area = push_area_bytes(M, splits, push_mode == kPushCompact);
     const bool push = push_mode != kPushNone && M <= push_rows &&
+                      (w_fmt == kFmtMx8 || tiles <= env.clusters[splits]) &&
                       Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area, sft).total() <=
                           kMaxDynamicSmem;
-    pl.reduction = !push                         ? (row_reduction(M, splits) ? kReduceRows : kReduceItems)
+    pl.reduction = !push                         ? (w_fmt != kFmtMx8 || row_reduction(M, splits) ? kReduceRows : kReduceItems)
                    : push_mode == kPushCompact ? kReducePushCompact
                                                : kReducePush;
     const Layout L(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, push ? area : 0u, sft);
@@ -1111,14 +1170,10 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
   if (te != nullptr) splits = te->splits;
   if (te != nullptr && force_stages == 0 && table_depth) force_stages = te->stages;
   splits = std::min(splits, std::min(8, nchunks));
-  // MXFP4 weights halve the stream that more splits would shorten: six at most, and
-  // from 65 rows four (whole-row reduction). Measured on GB300, N = 2048, K = 5120, us
-  // with 4 / 6 / 8 splits: 6.7 / 5.9 / 6.7 at one row, 8.4 / 8.0 / 8.2 at 64, 9.8 /
-  // 10.5 / 10.1 at 128, 12.6 / 14.5 / 23.4 at 256.
-  if (w_fmt != kFmtMx8) splits = std::min(splits, M > 64 ? 4 : 6);
+  if (w_fmt != kFmtMx8) splits = w4.splits;
   bool forced = false;
-  if (env.splits > 0) {
-    splits = std::min(env.splits, nchunks);
+  if (env_splits > 0) {
+    splits = std::min(env_splits, nchunks);
     forced = true;
   }
   if (force_splits > 0) {
@@ -1130,17 +1185,15 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
   // room for one CTA per SM: a grid beyond one CTA per SM would run in two
   // waves (M = 256, N = 5120, K = 8192: 240 CTAs, 36 us against 19 us at 192
   // rows), so such plans take at most one CTA per SM.
-  if (!forced && pl.tmem_cols > 256 && tiles * pl.splits > sm_count)
+  if (!forced && w_fmt == kFmtMx8 && pl.tmem_cols > 256 && tiles * pl.splits > sm_count)
     pl = plan_for(std::max(1, std::min(pl.splits, sm_count / std::max(tiles, 1))));
   return pl;
 }
 
 cudaError_t set_gemm_attributes() {
-  const void* ks[22] = {
-      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems, kFmtW4A8>),
+  const void* ks[20] = {
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A8>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReducePush, kFmtW4A8>),
-      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems, kFmtW4A4>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A4>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReducePush, kFmtW4A4>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceItems>),
@@ -1174,11 +1227,27 @@ cudaError_t set_gemm_attributes() {
   return cudaSuccess;
 }
 
+int gemm_max_clusters(int size) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.y = size;
+  cfg.gridDim = dim3(256, size, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = 180 * 1024;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel<false, false, kReduceRows, kFmtW4A8>, &cfg);
+  return e == cudaSuccess ? n : 0;
+}
+
 cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmArgs& args,
                         const GemmPlan& plan, bool pdl, cudaStream_t stream) {
   if (plan.smem > kMaxDynamicSmem) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(args.N / 128, plan.splits, 1);
+  cfg.gridDim = dim3(args.N / 128, plan.splits, plan.slices);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = plan.smem;
   cfg.stream = stream;
@@ -1200,7 +1269,7 @@ cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const 
   auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, args); };
   auto pick = [&](auto red) {
     constexpr int R = decltype(red)::value;
-    if constexpr (R != kReducePushCompact) {
+    if constexpr (R == kReducePush || R == kReduceRows) {
       if (args.w_fmt == kFmtW4A8) return go(gemm_kernel<false, false, R, kFmtW4A8>);
       if (args.w_fmt == kFmtW4A4) return go(gemm_kernel<false, false, R, kFmtW4A4>);
     }

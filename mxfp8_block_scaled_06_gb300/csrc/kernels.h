@@ -47,6 +47,8 @@ struct PlanEnv {
   int woa_splits;
   int push_rows;  // the push reduction up to this many rows (0: the default)
   char plan_at[256];
+  // clusters of 2..8 CTAs, one CTA to an SM, that the device holds at once (0: not known)
+  int clusters[9];
 };
 PlanEnv read_plan_env();
 
@@ -66,6 +68,7 @@ struct GemmPlan {
   int stages;
   int tmem_cols;
   int reduction;  // Reduction
+  int slice, slices;  // rows of a cluster (MXFP4 weights: multiples of 128), and how many take all
   size_t smem;
 };
 
@@ -90,6 +93,7 @@ struct GemmArgs {
   int M, N, K;
   int w_fmt;  // 0: MXFP8 weights, 1: MXFP4 weights and MXFP8 activations, 2: both MXFP4
   int mtile, stages, nchunks, tmem_cols;
+  int slice;  // rows of a cluster (MXFP4 weights)
   const uint8_t* a_scales;  // MXFP8 activations' swizzled scales (unused when x is set)
   const uint8_t* w_scales;
   // bf16 activations [M, K] (row stride ldx elements) quantized inside the
@@ -131,6 +135,8 @@ constexpr int kTimelineCtas = 512;
 GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool fused_a = false,
                    bool norm = false, int push_mode = kPushFull, bool table_depth = true, int w_fmt = 0);
 cudaError_t set_gemm_attributes();
+// how many clusters of `size` CTAs of the GEMM, one CTA to an SM, the device holds at once
+int gemm_max_clusters(int size);
 cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmArgs& args,
                         const GemmPlan& plan, bool pdl, cudaStream_t stream);
 

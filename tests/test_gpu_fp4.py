@@ -126,6 +126,29 @@ def test_product(mx, m, n, k, fp4):
 
 
 @pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("pdl", [False, True])
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 2688), (1, 8192, 3840), (7, 256, 6016), (16, 128, 4096), (17, 6144, 2560),
+                                   (64, 640, 3968), (128, 384, 5760), (129, 128, 5248), (201, 3840, 4096),
+                                   (255, 512, 3200), (344, 256, 4224), (513, 128, 8064), (1300, 128, 4736)])
+def test_product_split_along_k(mx, m, n, k, pdl, fp4):
+    """Clusters along K: of 2 to 8, several row slices, two to an SM, behind an earlier kernel or not."""
+    rng = np.random.default_rng(m + n + k)
+    aq, as_, av = operand(rng, m, k, fp4)
+    wq, ws, wv = operand(rng, n, k, True)
+    ob, o = guarded(m * n * 2)
+    out = o.view(torch.bfloat16).view(m, n)
+    args = [on_gpu(aq), on_gpu(oracle.swizzle_scales(as_)), on_gpu(wq), on_gpu(oracle.swizzle_scales(ws))]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        mx.mx_gemm_fp4(handle(), *args, out=out, pdl=pdl)
+    assert mx.mx_device_status(handle()) == mx.MX_OK
+    ref = av @ wv.T
+    err = np.abs(out.float().cpu().numpy().astype(np.float64) - ref)
+    assert (err <= bound(av, wv, ref)).all(), (err / bound(av, wv, ref)).max()
+    assert intact(ob, m * n * 2)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("m", [2, 40, 500])
 def test_product_of_exact_values(mx, m, fp4):
     """E2M1 values under scales of one: every sum is exact in float32."""
