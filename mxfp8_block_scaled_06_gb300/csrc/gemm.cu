@@ -215,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool compact = kRed == kReducePushCompact;
   const PushGeometry pgeo(M, kPush ? S : 1, kPush ? split : 0);
   const uint32_t slot = pgeo.slot;
+  // bulk reduction: rank r sums rows [r * rank_rows, (r + 1) * rank_rows) of the tile
+  constexpr bool kBulk = kRed == kReduceBulk;
+  const int rank_rows = (M + S - 1) / S;
+  const int own_row0 = split * rank_rows, own_rows = max(0, min(rank_rows, M - own_row0));
   const Layout L(p.mtile, stages, (p.nchunks + S - 1) / S, kFusedA, min(M, kRowBatch),
                  norm ? p.K / 32 : 0, kPush ? push_area_bytes(M, S, compact) : 0u, sf_tiles(kFmt));
   // scale tiles along K, of all and of this CTA's chunks (MXFP4 activations: the last chunk may be half a one)
@@ -257,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // wanted units (the peers start storing after the cluster barrier below)
       mbar_expect_tx(base + L.red_bar, push_expect_bytes(pgeo, want_q));
     }
+    if constexpr (kBulk) mbar_expect_tx(base + L.red_bar, static_cast<uint32_t>((S - 1) * own_rows) * 512u);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_w);
@@ -756,6 +761,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every store into this CTA has landed: its part of the exit barrier (an
     // arrival waits for the thread's own stores to peers, by now delivered)
     cluster_arrive_relaxed();
+  } else if constexpr (kBulk) {
+    // The peers' blocks land over the ring, behind this CTA's own partials: first every
+    // CTA of the cluster has to be done with its ring. Then one block of rows after the
+    // other goes out as it is staged, this rank's own last.
+    cluster_arrive_release();
+    const uint32_t recv = base + static_cast<uint32_t>(p.mtile) * 512u;
+    for (int i = 1; i <= S; ++i) {
+      const int r = split + i < S ? split + i : split + i - S;
+      const int row0 = r * rank_rows, row1 = min(M, row0 + rank_rows);
+      for (int c0 = row0; c0 < row1; c0 += 32) {
+        uint32_t v[2][16];
+        tmem_ld_32x32b_x16_nowait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0, v[0]);
+        if (c0 + 16 < row1) tmem_ld_32x32b_x16_nowait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c0 + 16, v[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j < row1) red[(c0 + j) * 128 + warp * 32 + lane] = __uint_as_float(v[j >> 4][j & 15]);
+      }
+      fence_proxy_async_smem();
+      if (i == 1) cluster_wait_acquire();
+      __syncthreads();
+      if (threadIdx.x == 0 && r != split && row1 > row0 && ok) {
+        const uint32_t to = recv + static_cast<uint32_t>((split < r ? split : split - 1) * rank_rows) * 512u;
+        bulk_copy_to_peer(map_shared_rank(to, r), base + static_cast<uint32_t>(row0) * 512u,
+                          static_cast<uint32_t>(row1 - row0) * 512u, map_shared_rank(base + L.red_bar, r));
+      }
+      __syncwarp();
+    }
+    if (threadIdx.x == 0) bulk_commit();
+    tc_fence_before();
+    if (!mbar_wait(base + L.red_bar, 0)) fail();
+    if (threadIdx.x == 0) MX_TL(7, globaltimer());
+    if (threadIdx.x == 0) bulk_wait();  // this CTA's copies have arrived too, so its part of the exit barrier
+    __syncwarp();
+    cluster_arrive_relaxed();
   } else {
     if (ok) {
       for (int c0 = 0; c0 < p.mtile; c0 += 16) {
@@ -813,7 +853,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) p.q_scales[swz_offset(m, col >> 5, p.q_cols >> 5)] = static_cast<uint8_t>(sbyte);
       }
     };
-    if constexpr (kPush) {
+    if constexpr (kBulk) {
+      // a warp sums whole rows, lane l columns 4l .. 4l + 3, in rank order
+      const uint32_t recv = base + static_cast<uint32_t>(p.mtile) * 512u + lane * 16;
+      const uint32_t mine = base + static_cast<uint32_t>(own_row0) * 512u + lane * 16;
+      const int col0 = tile * 128 + lane * 4;
+      for (int m0 = warp * kRedRows; m0 < own_rows; m0 += kThreads / 32 * kRedRows) {
+        float4 acc[kRedRows];
+#pragma unroll
+        for (int b = 0; b < kRedRows; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r0 = 0; r0 < 8; r0 += 4) {  // S <= 8
+          if (r0 >= S) break;
+          float4 v[kRedRows][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int from = min(r0 + r, S - 1), slot = from < split ? from : from - 1;
+            const uint32_t at = from == split ? mine : recv + static_cast<uint32_t>(slot * rank_rows) * 512u;
+#pragma unroll
+            for (int b = 0; b < kRedRows; ++b)
+              v[b][r] = ld_shared_v4(at + static_cast<uint32_t>(min(m0 + b, own_rows - 1)) * 512u);
+          }
+#pragma unroll
+          for (int b = 0; b < kRedRows; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r0 + r < S) {
+                acc[b].x += v[b][r].x;
+                acc[b].y += v[b][r].y;
+                acc[b].z += v[b][r].z;
+                acc[b].w += v[b][r].w;
+              }
+        }
+#pragma unroll
+        for (int b = 0; b < kRedRows; ++b)
+          if (m0 + b < own_rows) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[b].x, acc[b].y);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[b].z, acc[b].w);
+            *reinterpret_cast<uint2*>(out + static_cast<size_t>(own_row0 + m0 + b) * p.N + col0) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          }
+      }
+    } else if constexpr (kPush) {
       push_sum<compact>(pgeo, warp, kThreads / 32, lane, push, own, want_q, emit);
     } else if (M <= S) {
       // at most one item per warp
@@ -943,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the peers' reads of this CTA's partials have completed (their values were
   // consumed), so ordering the exits needs no memory release; with the push
   // reduction every CTA has arrived once all stores into it landed
-  if constexpr (kPush)
+  if constexpr (kPush || kBulk)
     cluster_wait();
   else
     cluster_sync_relaxed();
@@ -1051,21 +1132,29 @@ PlanEnv read_plan_env() {
   return env;
 }
 
+// A product with MXFP4 weights reduces whole rows up to this many of them and by bulk
+// copies beyond: N = 2048, K = 5120, MXFP8 rows, six splits, rows / bulk us 5.2 / 5.6 at
+// one row, 6.0 / 6.4 at 32, 6.9 / 6.6 at 64, 8.6 / 7.4 at 128 (the push 5.3, 6.7, 7.9 and
+// 11.1); behind a kernel that it overlaps the push up to kPushMaxRows, 3.8 against 4.2.
+constexpr int kRowsMax = 48;
 // K-splits of a product with MXFP4 weights, and the rows that a cluster takes: those
 // with the least time on top of what any launch costs, in ns. A tile's way through K
-// takes 180 (MXFP4 rows 110) for 128 elements, a third more with over 128 rows, and the
-// splits' exchange 1300 and 12 a row (22 with more than four splits). More clusters than
-// the device holds at once with one CTA to an SM (of 152 SMs 76 of two CTAs, 46, 36, 28,
-// 23, 15 and 15 of eight) run two to an SM where both fit: a quarter more for the way, and
-// 4 a row (with more than four splits 250 and 14 a row). One split: no gain, whole-K
-// tiles (gemm_fp4.cu, 800 more from 65 rows on) are the faster.
+// takes 180 (MXFP4 rows 110) for 128 elements, a twelfth more with over 64 rows and a
+// third with over 128; the splits' exchange 1300 and 12 a row (22 with more than four
+// splits), by bulk copies 1300 and 14 a row (2300 and 7). More clusters than the device
+// holds at once with one CTA to an SM (of 152 SMs 76 of two CTAs, 46, 36, 28, 23, 15 and 15
+// of eight) run two to an SM where both fit: a quarter more for the way, and more for the
+// exchange. One split stands for whole-K tiles (gemm_fp4.cu), which take 14 a row more, from
+// 65 rows on 1500 (MXFP4 rows 1900) more; 33 to 64 MXFP8 rows against over 76 weight tiles
+// 2500 on top (N = 12288, K = 5120 11.5 us at 32 rows, 13.9 at 48).
 // Measured on GB300, us with MXFP8 rows and 2 / 3 / 4 / 6 / 8 splits: N = 1024, K = 10368
-// 11.8 / 9.1 / 7.9 / 6.7 / 6.1 at one row, 14.9 / 11.9 / 10.6 / 10.2 / 9.8 at 128; N = 2048,
-// K = 5120 7.7 / 6.6 / 5.9 / 5.1 / 5.5 (two to an SM) at one row, 9.2 / 8.0 / 7.2 / 6.9 / 7.6
+// 11.8 / 9.1 / 7.9 / 6.7 / 6.1 at one row, 14.3 / 11.5 / 10.1 / 8.8 / 8.3 at 128; N = 2048,
+// K = 5120 7.7 / 6.6 / 5.9 / 5.1 / 5.3 (two to an SM) at one row, 8.9 / 7.8 / 7.0 / 6.6 / 7.9
 // at 64, whole K 10.3 and 11.1; two to an SM: N = 8192, K = 8192, four splits 8.1 at one
 // row, whole K 10.1; N = 6144, K = 5120 6.5, two splits with one CTA to an SM 7.8. Slices
 // of 128 rows / one of all: N = 1024, K = 10368, 256 rows 10.7 / 14.4; N = 5120, K = 8192,
-// 201 rows, three splits 15.3 / 14.4. N = 256, K = 16000, 344 rows 10.7, whole K 24.4.
+// 201 rows, three splits 15.3 / 14.4 (rows; bulk 12.9). N = 256, K = 16000, 344 rows
+// 9.1, whole K 24.4.
 struct W4Split {
   int slice, splits;
 };
@@ -1073,7 +1162,7 @@ W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4) {
   const int sft = a_fp4 ? 2 : 1, chunks = (K / 128 + sft - 1) / sft;
   const long walk = (a_fp4 ? 110L : 180L) * (K / 128);
   W4Split best{std::min(M, 128), 1};
-  long least = walk + (M > 64 ? 800 : 0);
+  long least = walk + (M > 64 ? (a_fp4 ? 1900 : 1500) : 14 * M + (!a_fp4 && M > 32 && N / 128 > 76 ? 2500 : 0));
   for (int slice : {std::min(M, 128), std::min(M, 256)}) {
     const long clusters = static_cast<long>(N / 128) * ((M + slice - 1) / slice);
     for (int s = 2; s <= std::min(slice > 128 ? 4 : 8, chunks); ++s) {
@@ -1081,8 +1170,11 @@ W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4) {
       if (two && (slice > 64 || clusters > 2 * env.clusters[s])) continue;
       // a CTA's scale tiles stay in shared memory (plan_for)
       if (static_cast<long>((chunks + s - 1) / s) * sft * kSfTileBytes * (slice > 128 ? 3 : 2) > 48 * 1024) continue;
-      const long way = walk * (slice > 128 ? 16 : two ? 15 : 12) / (12 * s);
-      const long exchange = s > 4 ? (two ? 1550 + 36L * slice : 1300 + 22L * slice) : 1300 + (two ? 16L : 12L) * slice;
+      const long way = walk * (slice > 128 ? 16 : two ? 15 : slice > 64 ? 13 : 12) / (12 * s);
+      const long exchange = slice <= kRowsMax ? (s > 4 ? (two ? 1550 + 36L * slice : 1300 + 22L * slice)
+                                                       : 1300 + (two ? 16L : 12L) * slice)
+                            : s > 4           ? 2300 + (two ? 22L : 7L) * slice
+                                              : 1300 + (two ? 30L : 14L) * slice;
       if (way + exchange < least) {
         least = way + exchange;
         best = {slice, s};
@@ -1143,7 +1235,10 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     if (force_stages > 0) stages = force_stages;
     stages = std::min(stages, per_cta);
     // the epilogue stages the fp32 partials [mtile][128] over the ring and what follows it
-    while (static_cast<size_t>(stages) * L1.stage_bytes + scales < static_cast<size_t>(mtile) * 512)
+    // (bulk reduction: and what the peers send)
+    const size_t staged = static_cast<size_t>(mtile) * 512 +
+                          (w_fmt != kFmtMx8 ? static_cast<size_t>(splits - 1) * ((M + splits - 1) / splits) * 512 : 0);
+    while (static_cast<size_t>(stages) * L1.stage_bytes + scales < staged)
       ++stages;
     pl.stages = stages;
     pl.tmem_cols = pow2_at_least(tmem_sfa_col(mtile) + 4 * sft * stages * (1 + nsfb));
@@ -1153,7 +1248,9 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
                       (w_fmt == kFmtMx8 || tiles <= env.clusters[splits]) &&
                       Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area, sft).total() <=
                           kMaxDynamicSmem;
-    pl.reduction = !push                         ? (w_fmt != kFmtMx8 || row_reduction(M, splits) ? kReduceRows : kReduceItems)
+    pl.reduction = !push                         ? w_fmt != kFmtMx8          ? M <= kRowsMax ? kReduceRows : kReduceBulk
+                                                   : row_reduction(M, splits) ? kReduceRows
+                                                                              : kReduceItems
                    : push_mode == kPushCompact ? kReducePushCompact
                                                : kReducePush;
     const Layout L(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, push ? area : 0u, sft);
@@ -1191,7 +1288,9 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
 }
 
 cudaError_t set_gemm_attributes() {
-  const void* ks[20] = {
+  const void* ks[22] = {
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceBulk, kFmtW4A8>),
+      reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceBulk, kFmtW4A4>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A8>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReducePush, kFmtW4A8>),
       reinterpret_cast<const void*>(&gemm_kernel<false, false, kReduceRows, kFmtW4A4>),
@@ -1269,15 +1368,20 @@ cudaError_t launch_gemm(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const 
   auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_a, args); };
   auto pick = [&](auto red) {
     constexpr int R = decltype(red)::value;
-    if constexpr (R == kReducePush || R == kReduceRows) {
+    if constexpr (R == kReducePush || R == kReduceBulk || R == kReduceRows) {
       if (args.w_fmt == kFmtW4A8) return go(gemm_kernel<false, false, R, kFmtW4A8>);
       if (args.w_fmt == kFmtW4A4) return go(gemm_kernel<false, false, R, kFmtW4A4>);
     }
-    if (fx) return rq ? go(gemm_kernel<true, true, R>) : go(gemm_kernel<false, true, R>);
-    return rq ? go(gemm_kernel<true, false, R>) : go(gemm_kernel<false, false, R>);
+    if constexpr (R == kReduceBulk) {
+      return cudaErrorInvalidValue;  // MXFP4 weights only
+    } else {
+      if (fx) return rq ? go(gemm_kernel<true, true, R>) : go(gemm_kernel<false, true, R>);
+      return rq ? go(gemm_kernel<true, false, R>) : go(gemm_kernel<false, false, R>);
+    }
   };
   if (plan.reduction == kReducePush) return pick(std::integral_constant<int, kReducePush>{});
   if (plan.reduction == kReducePushCompact) return pick(std::integral_constant<int, kReducePushCompact>{});
+  if (plan.reduction == kReduceBulk) return pick(std::integral_constant<int, kReduceBulk>{});
   if (plan.reduction == kReduceRows) return pick(std::integral_constant<int, kReduceRows>{});
   return pick(std::integral_constant<int, kReduceItems>{});
 }

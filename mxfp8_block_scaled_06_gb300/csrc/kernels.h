@@ -57,8 +57,9 @@ PlanEnv read_plan_env();
 // warp sums whole rows with 16-byte peer loads; push = every CTA stores the
 // partials of the units another rank owns straight into that rank's shared
 // memory (st.async, counted on its mbarrier) and sums its own units locally,
-// with a receive slot per rank, or (compact) per peer.
-enum Reduction : int { kReduceItems = 0, kReduceRows = 1, kReducePush = 2, kReducePushCompact = 3 };
+// with a receive slot per rank, or (compact) per peer; bulk (MXFP4 weights) = every
+// CTA copies the rows that another rank owns, as one block, into that rank's shared memory.
+enum Reduction : int { kReduceItems = 0, kReduceRows = 1, kReducePush = 2, kReducePushCompact = 3, kReduceBulk = 4 };
 // Whether a plan may take the push reduction, and with which receive area.
 enum PushMode : int { kPushNone = 0, kPushCompact = 1, kPushFull = 2 };
 
