@@ -40,6 +40,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kRouteWarps = 8;
+constexpr uint32_t kMasked = 0x007FFFFFu;  // ord32(-inf)
 
 // Order-preserving bits: a < b as floats <=> ord(a) < ord(b); never 0 for a number.
 __device__ __forceinline__ uint32_t ord32(float f) {
@@ -373,15 +374,27 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       if (!(open >> (groups[i / 6] >> (5 * (i % 6)) & 31u) & 1u)) key[i] = 0u;  // no closed expert is taken
   }
   // at least top_k keys are at or above the top_k-th largest of the lanes' largest
-  uint32_t most = key[0];
+  auto bound = [&]() {
+    uint32_t most = key[0], least = 0;
 #pragma unroll
-  for (int i = 1; i < V; ++i) most = max(most, key[i]);
-  uint32_t least = 0;
-  for (int j = 0; j < p.top_k; ++j) {
-    least = __reduce_max_sync(kFull, most);
-    if (most == least) most = 0;
+    for (int i = 1; i < V; ++i) most = max(most, key[i]);
+    for (int j = 0; j < p.top_k; ++j) {
+      least = __reduce_max_sync(kFull, most);
+      if (most == least) most = 0;
+    }
+    return least;
+  };
+  uint32_t least = bound();
+  if (least <= kMasked) {
+    // Masked experts may have to be taken, the lowest index first: below the key of -inf
+    // there are no other keys, so theirs can say that order. (Left equal, more than 32
+    // of them went by rounds; a few padding tokens then took 17 of 29 us.)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] == kMasked) key[i] -= lane + 32 * i;
+    least = bound();
   }
-  if (p.bias != nullptr && least != 0) least = ord32(unord32(least) - 2.f * far);
+  if (p.bias != nullptr && least > kMasked) least = ord32(unord32(least) - 2.f * far);
   least = max(least, 1u);
   // gathered in the order of their indices
   volatile uint2* const list = reinterpret_cast<volatile uint2*>(shared);
@@ -420,7 +433,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       const int other = lane < p.top_k ? max(lane - 1, 0) : p.top_k - 1;
       const uint32_t ko = __shfl_sync(kFull, k, other), eo = __shfl_sync(kFull, e, other);
       bool close = false;
-      if (lane > 0 && lane < n && k > ord32(-CUDART_INF_F) && !(unord32(ko) - unord32(k) > 2.f * far))
+      if (lane > 0 && lane < n && k > kMasked && !(unord32(ko) - unord32(k) > 2.f * far))
         close = load_logit(p.logits, base + eo, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
                 p.bias[eo] != p.bias[e];
       if (__any_sync(kFull, close)) mine = order64(p, base, e, n, t.top, reinterpret_cast<volatile int*>(shared));

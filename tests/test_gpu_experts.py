@@ -97,6 +97,23 @@ def test_route_masks_and_extremes(mx, bias, scoring):
     check_route(mx, on_gpu(x), 6, bias=b, scoring=scoring, renormalize=False, scale=0.25)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [None, "numbers", "some -inf"])
+@pytest.mark.parametrize("e,k,groups,top", [(512, 16, 1, 1), (512, 16, 8, 2), (96, 32, 1, 1), (160, 5, 5, 1), (70, 9, 7, 3)])
+def test_route_fewer_experts_than_choices(mx, e, k, groups, top, bias, scoring):
+    """Rows with 0 to k + 2 experts that are not masked, anywhere, or in the first or last places."""
+    rng = np.random.default_rng(e + k)
+    x = np.full((4 * (k + 3), e), -np.inf)
+    for r in range(len(x)):
+        n = r // 4
+        at = (rng.permutation(e)[:n], np.arange(n), np.arange(e - n, e), 32 * np.arange(n) % e)[r % 4]
+        x[r, at] = 2 * rng.standard_normal(n)
+    b = None if bias is None else (0.2 * rng.standard_normal(e)).astype(np.float32)
+    if bias == "some -inf":
+        b[rng.random(e) < 0.7] = -np.inf
+    check_route(mx, on_gpu(x.astype(np.float32)), k, bias=b, scoring=scoring, n_groups=groups, topk_groups=top)
+
+
 @pytest.mark.parametrize("t", [16384, 20011])
 def test_route_many_tokens(mx, t):
     rng = np.random.default_rng(t)
