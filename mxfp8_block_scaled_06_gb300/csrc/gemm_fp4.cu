@@ -13,7 +13,8 @@
 //   2     activation rows, where they are neighbours: a TMA box
 //   3     activation scales: gathered with plain loads into 128x4 scale tiles (wide
 //         tiles: with the block's last warp)
-//   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half
+//   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half (wide
+//         tiles: with four more warps)
 //   8-11  activation rows gathered by index: 16-byte cp.async into the swizzled
 //         tile (tile::gather4 copies, four rows each, came at 34 ns apiece: 1.9 us
 //         for a stage of 224 rows, against 0.4 us that the MMAs of a stage take)
@@ -39,8 +40,13 @@ constexpr int kThreads = 256, kGatherThreads = 128;  // the latter on top, where
 // tiles are wide (one alone held an MXFP4 stage of 224 rows at 0.4 us; 8192 x 8192 x
 // 5120 took 130 us, without its loads 96)
 __host__ __device__ constexpr int scale_warps(int mode) { return mode == 1 ? 1 : 2; }
+// Epilogue warps: a second set of four, before that one, where token tiles are wide. With
+// few elements along K, or a gate, four could not keep up. Measured with eight / four: 64
+// experts of 4096 x 4096, 32744 MXFP4 rows, gated 259 / 324 us; 14 of 5888 x 512, 20818
+// rows, gated 82 / 96; 4096 x 4096 x 512 14.4 / 16.4; 8192 x 8192 x 5120 100 / 100.
+__host__ __device__ constexpr int epilogue_warps(int mode) { return mode == 1 ? 4 : 8; }
 __host__ __device__ constexpr int threads(int mode, bool gather) {
-  return kThreads + (gather ? kGatherThreads : 0) + (scale_warps(mode) - 1) * 32;
+  return kThreads + (gather ? kGatherThreads : 0) + (epilogue_warps(mode) - 4 + scale_warps(mode) - 1) * 32;
 }
 constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
 // bytes that an unpacking copy of it completes on its barrier: the packed ones
@@ -123,7 +129,9 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   constexpr int kNt = kMode == kSmall ? kSmallNt : kMaxNt;
   constexpr bool kTwo = kMode == kPair;
   constexpr int kScaleWarps = scale_warps(kMode);
-  constexpr int kExtraWarp = (kThreads + (kGather ? kGatherThreads : 0)) / 32;  // the second of them
+  constexpr int kEpilogue = epilogue_warps(kMode);
+  constexpr int kEpilogue2 = (kThreads + (kGather ? kGatherThreads : 0)) / 32;  // the first of the second four
+  constexpr int kExtraWarp = kEpilogue2 + kEpilogue - 4;  // the second scale warp
   constexpr int kStageRows = kTwo ? kNt / 2 : kNt;  // activation rows of a stage, at most
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -156,7 +164,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, kTwo ? 8 : 4);  // the epilogues' warps
+      mbar_init(acc_empty + 8 * b, (kTwo ? 2 : 1) * kEpilogue);  // the epilogues' warps
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
         landed = mbar_test_wait(full(s), ph);  // the next stage, while the MMAs run
       }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if ((warp >= 4 && warp < 8) || (kEpilogue == 8 && warp >= kEpilogue2 && warp < kEpilogue2 + 4)) {
     // ---------------- epilogue: lane l of quarter q holds output column n0 + 32q + l
     const int q = warp & 3;
     const bool odd = lane & 1;
@@ -553,7 +561,10 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       const int col = t.n0 + q * 32 + (p.gated ? lane & ~3 : lane);
       __nv_bfloat16* out = p.gated ? p.out + (static_cast<size_t>(t.row0) + tok0) * ldo + (col >> 1)
                                    : p.out + static_cast<size_t>(t.row0) * ldo + col;
-      for (int c0 = 0; c0 < t.n; c0 += 16) {
+      constexpr int kStep = 16 * kEpilogue / 4;  // of eight warps, four take every other 16 tokens
+      const int c_first = kEpilogue == 8 && warp >= 8 ? 16 : 0;
+      out += c_first * ldo;
+      for (int c0 = c_first; c0 < t.n; c0 += kStep) {
         float v[16];
         tmem_ld_32x32b_x16(acc + c0, v);
         if (!p.gated) {
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
             for (int i = 0; i < 16; ++i)
               if (c0 + i < t.rows) out[i * ldo] = __float2bfloat16_rn(v[i]);
           }
-          out += 16 * ldo;
+          out += kStep * ldo;
           continue;
         }
 #pragma unroll
@@ -583,6 +594,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
                 __floats2bfloat162_rn(lane & 2 ? got : two[0], lane & 2 ? two[1] : got);
           out += 4 * ldo;
         }
+        out += (kStep - 16) * ldo;
       }
       tc_fence_before();
       __syncwarp();
