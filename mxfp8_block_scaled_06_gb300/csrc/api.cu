@@ -844,7 +844,7 @@ int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp
   // tile numbers are 32-bit; a token tile has 16 rows at least
   if (static_cast<long>(args.N / 128) * (args.R / 16 + args.E) >= (1L << 31)) return MX_ERR_UNSUPPORTED;
   const mx::GemmFp4Plan plan = mx::plan_gemm_fp4(args.E, args.R, args.N, args.K, a_fp4 != 0, h->sm_count);
-  if (plan.stages < 3) return MX_ERR_UNSUPPORTED;
+  if (plan.stages < plan.min_stages) return MX_ERR_UNSUPPORTED;
   args.a = static_cast<const uint8_t*>(a);
   args.nt = plan.nt;
   args.stages = plan.stages;

@@ -40,6 +40,15 @@ constexpr int kThreads = 256, kGatherThreads = 128;  // the latter on top, where
 // tiles are wide (one alone held an MXFP4 stage of 224 rows at 0.4 us; 8192 x 8192 x
 // 5120 took 130 us, without its loads 96)
 __host__ __device__ constexpr int scale_warps(int mode) { return mode == 1 ? 1 : 2; }
+constexpr int kScaleBatch = 4;  // scale tiles that such a warp loads at once, and two take in turn
+// Stages that the ring needs. A warp that leaves n stages to others (a scale warp the other
+// one's batch, a gathering warp those of the other three) waits for the stage behind them
+// by its parity, which says whether the slot's last use is over only if the use before it is
+// known to be: what the warp knows is that the stage a ring before its last own one is over,
+// so the ring has to be n + 1 stages long. (With four, scale warps overran each other.)
+__host__ __device__ constexpr int min_stages(int mode, bool a_fp4) {
+  return scale_warps(mode) == 2 && !a_fp4 ? kScaleBatch + 1 : 4;
+}
 // Epilogue warps: a second set of four, before that one, where token tiles are wide. With
 // few elements along K, or a gate, four could not keep up. Measured with eight / four: 64
 // experts of 4096 x 4096, 32744 MXFP4 rows, gated 259 / 324 us; 14 of 5888 x 512, 20818
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     const uint32_t dst0 = base + kWBytes + r0 * 128;
     // rows r0, r0 + 4, ... have two values of r % 8: two swizzles in turn
     const uint32_t swz[2] = {static_cast<uint32_t>(c ^ r0) << 4, static_cast<uint32_t>(c ^ (r0 + 4)) << 4};
-    int s = warp - kThreads / 32;  // stages: at least kWarps - 1 (the plan)
+    int s = warp - kThreads / 32;  // stages: at least kWarps (min_stages)
     uint32_t ph = 1;
     if (s >= stages) s -= stages, ph ^= 1u;
     int pending = -1;  // the stage to hand over
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows. A batch of
     // kBatch scale tiles is loaded at once, the next one while it is stored; with two
     // warps they take the batches in turn.
-    constexpr int kRows = (kNt + 31) / 32, kBatch = 4;  // rows per lane
+    constexpr int kRows = (kNt + 31) / 32, kBatch = kScaleBatch;  // rows per lane
     constexpr int kBatchStages = kBatch / kTiles;
     const int which = warp == 3 ? 0 : 1;
     int s = 0;
@@ -644,9 +653,11 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
   // than the mean (an expert with more rows takes several balanced tiles). With 64
   // experts of 4096 x 2048, gated, us with twice the mean / with this: 512 tokens to 6
   // each 68 / 55 (MXFP4 rows 60 / 50), 1024 76 / 73 (74 / 61).
-  const long want = E == 1 ? R : std::min<long>({R, 4L * ((R + E - 1) / E) / 3, kMaxNt});
-  long tt = (want + kMaxNt - 1) / kMaxNt;
-  if (E == 1 && want > kMaxNt / 2) {
+  // One CTA to an SM, MXFP8 rows: 208 rows at most, which leave room for five stages (min_stages).
+  const int most_nt = N % 256 == 0 || a_fp4 ? kMaxNt : 208;
+  const long want = E == 1 ? R : std::min<long>({R, 4L * ((R + E - 1) / E) / 3, most_nt});
+  long tt = (want + most_nt - 1) / most_nt;
+  if (E == 1 && want > most_nt / 2) {
     const int at_once = N % 256 == 0 ? sm_count / 2 : sm_count;
     const long w_tiles = N % 256 == 0 ? N / 256 : N / 128;
     auto cost = [&](long k) { return (w_tiles * k + at_once - 1) / at_once * ((want + k - 1) / k + 100); };
@@ -656,9 +667,10 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
   }
   const int nt = static_cast<int>((want + tt - 1) / tt);
   pl.mode = nt <= kSmallNt ? kSmall : N % 256 == 0 ? kPair : kOne;
-  pl.nt = std::min(kMaxNt, (nt + rows_round(pl.mode) - 1) & -rows_round(pl.mode));
+  pl.nt = std::min(most_nt, (nt + rows_round(pl.mode) - 1) & -rows_round(pl.mode));
   pl.a_rows = pl.mode == kPair ? pl.nt / 2 : pl.nt;
   pl.ctas_per_sm = pl.mode == kSmall ? 2 : 1;
+  pl.min_stages = min_stages(pl.mode, a_fp4);
   const int cols = 2 * pl.nt + 2 * 4 * kt * (1 + (pl.nt + 127) / 128);
   pl.tmem_cols = 32;
   while (pl.tmem_cols < cols) pl.tmem_cols <<= 1;
@@ -702,7 +714,7 @@ cudaError_t set_gemm_fp4_attributes() {
 cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
                             const GemmFp4Plan& plan, bool a_fp4, cudaStream_t stream) {
   const bool gather = args.tokens != nullptr;
-  if (plan.smem > kMaxDynamicSmem || plan.stages < 3) return cudaErrorInvalidValue;
+  if (plan.smem > kMaxDynamicSmem || plan.stages < plan.min_stages) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.grid);

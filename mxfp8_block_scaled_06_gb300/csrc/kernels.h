@@ -266,7 +266,7 @@ struct GemmFp4Args {
 struct GemmFp4Plan {
   int mode;    // how CTAs share SMs and tiles (gemm_fp4.cu)
   int a_rows;  // activation rows of a stage: the tensor map's box
-  int nt, stages, tmem_cols, ctas_per_sm, grid;
+  int nt, stages, min_stages, tmem_cols, ctas_per_sm, grid;
   size_t smem;
 };
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count);

@@ -223,6 +223,14 @@ def test_grouped_product_of_wide_tiles(mx, counts, k, n, gather, fp4, gated):
     check_grouped(mx, counts, 150, k, n, gather, fp4, gated)
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,k,n", [([430, 0, 215, 900, 417], 1024, 640), ([3000], 2048, 128), ([1700, 5, 224], 640, 1920)])
+def test_grouped_product_of_the_widest_tiles(mx, counts, k, n, gather, fp4):
+    """Tiles of 200 rows and more with one CTA to an SM: the shortest rings, over many stages."""
+    check_grouped(mx, counts, 800, k, n, gather, fp4, False)
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("counts,rows_a,k,n,gather", [

@@ -126,6 +126,13 @@ def test_product(mx, m, n, k, fp4):
 
 
 @pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("m,n,k", [(2230, 384, 1152), (4300, 128, 2048), (3360, 640, 1536), (8400, 384, 640)])
+def test_product_of_the_widest_tiles(mx, m, n, k, fp4):
+    """Tiles of 200 rows and more with one CTA to an SM: the shortest rings, over many stages."""
+    test_product(mx, m, n, k, fp4)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("pdl", [False, True])
 @pytest.mark.parametrize("m,n,k", [(1, 1024, 2688), (1, 8192, 3840), (7, 256, 6016), (16, 128, 4096), (17, 6144, 2560),
                                    (64, 640, 3968), (128, 384, 5760), (129, 128, 5248), (201, 3840, 4096),
