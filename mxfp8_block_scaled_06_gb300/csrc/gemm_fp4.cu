@@ -12,7 +12,7 @@
 //   1     tcgen05.cp of the scales and tcgen05.mma, by an elected lane
 //   2     activation rows, where they are neighbours: a TMA box
 //   3     activation scales: gathered with plain loads into 128x4 scale tiles (wide
-//         tiles: with the block's last warp)
+//         tiles: with a second warp, 2 where that has no rows to load, else the last)
 //   4-7   epilogue: TMEM -> bf16, while the next tile accumulates in the other half (wide
 //         tiles: with four more warps)
 //   8-11  activation rows gathered by index: 16-byte cp.async into the swizzled
@@ -36,18 +36,18 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256, kGatherThreads = 128;  // the latter on top, where rows are gathered
-// warps that load the activation scales: a second one, the block's last, where token
+// warps that load the activation scales: a second one where token
 // tiles are wide (one alone held an MXFP4 stage of 224 rows at 0.4 us; 8192 x 8192 x
 // 5120 took 130 us, without its loads 96)
 __host__ __device__ constexpr int scale_warps(int mode) { return mode == 1 ? 1 : 2; }
 constexpr int kScaleBatch = 4;  // scale tiles that such a warp loads at once, and two take in turn
 // Stages that the ring needs. A warp that leaves n stages to others (a scale warp the other
-// one's batch, a gathering warp those of the other three) waits for the stage behind them
+// one's batch, a gathering warp every other stage) waits for the stage behind them
 // by its parity, which says whether the slot's last use is over only if the use before it is
 // known to be: what the warp knows is that the stage a ring before its last own one is over,
 // so the ring has to be n + 1 stages long. (With four, scale warps overran each other.)
 __host__ __device__ constexpr int min_stages(int mode, bool a_fp4) {
-  return scale_warps(mode) == 2 && !a_fp4 ? kScaleBatch + 1 : 4;
+  return scale_warps(mode) == 2 ? kScaleBatch / (a_fp4 ? 2 : 1) + 1 : 3;
 }
 // Epilogue warps: a second set of four, before that one, where token tiles are wide. With
 // few elements along K, or a gate, four could not keep up. Measured with eight / four: 64
@@ -55,7 +55,7 @@ __host__ __device__ constexpr int min_stages(int mode, bool a_fp4) {
 // rows, gated 82 / 96; 4096 x 4096 x 512 14.4 / 16.4; 8192 x 8192 x 5120 100 / 100.
 __host__ __device__ constexpr int epilogue_warps(int mode) { return mode == 1 ? 4 : 8; }
 __host__ __device__ constexpr int threads(int mode, bool gather) {
-  return kThreads + (gather ? kGatherThreads : 0) + (epilogue_warps(mode) - 4 + scale_warps(mode) - 1) * 32;
+  return kThreads + (epilogue_warps(mode) - 4) * 32 + (gather ? kGatherThreads : (scale_warps(mode) - 1) * 32);
 }
 constexpr uint32_t kWBytes = 128 * 128;  // weight box in shared memory
 // bytes that an unpacking copy of it completes on its barrier: the packed ones
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   constexpr int kScaleWarps = scale_warps(kMode);
   constexpr int kEpilogue = epilogue_warps(kMode);
   constexpr int kEpilogue2 = (kThreads + (kGather ? kGatherThreads : 0)) / 32;  // the first of the second four
-  constexpr int kExtraWarp = kEpilogue2 + kEpilogue - 4;  // the second scale warp
+  constexpr int kScale2 = kGather ? 2 : kEpilogue2 + kEpilogue - 4;  // the second scale warp
   constexpr int kStageRows = kTwo ? kNt / 2 : kNt;  // activation rows of a stage, at most
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -156,6 +156,10 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   const Layout L(p.nt, kTwo ? p.nt / 2 : p.nt, stages, kTiles, p.E);
   const int units = p.K >> 7;                        // scale tiles along K
   const int chunks = (units + kTiles - 1) / kTiles;  // stages along K
+  // Warps that share a gathered stage: two where K is long, as every thread's arrival takes
+  // its time (6144 rows, K = 2048 65 us, with four 70), four where it is short (20818 rows, K
+  // = 512 91 us, with two 98) or the tiles narrow.
+  const int per = kMode == kSmall || chunks <= 6 ? 4 : 2;
   const uint32_t bars = base + L.bars;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (stages + s); };
@@ -167,8 +171,9 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
-      // weights, activation scales, activations; the first CTA of a pair: the second one's
-      mbar_init(full(s), 3 + (kTwo && rank == 0));
+      // weights, activation scales, activations (gathered: every thread's copies); the
+      // first CTA of a pair: the second one's
+      mbar_init(full(s), 2 + (kGather ? per * 32 : 1) + (kTwo && rank == 0));
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -283,70 +288,80 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       }
     }
   } else if (kGather && warp >= kThreads / 32 && warp < (kThreads + kGatherThreads) / 32) {
-    // ---------------- gathered activation rows: the warps take the stages in turn,
-    // eight threads a row, 16 bytes each. A warp hands a stage over once it has
-    // issued its next one, or when that one is not free yet.
-    constexpr int kRows = kStageRows / 4;  // rows per thread, 4 apart
-    constexpr int kWarps = kGatherThreads / 32;
-    const int c = lane & 7, r0 = lane >> 3;
-    const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
-    const uint32_t dst0 = base + kWBytes + r0 * 128;
-    // rows r0, r0 + 4, ... have two values of r % 8: two swizzles in turn
-    const uint32_t swz[2] = {static_cast<uint32_t>(c ^ r0) << 4, static_cast<uint32_t>(c ^ (r0 + 4)) << 4};
-    int s = warp - kThreads / 32;  // stages: at least kWarps (min_stages)
-    uint32_t ph = 1;
-    if (s >= stages) s -= stages, ph ^= 1u;
-    int pending = -1;  // the stage to hand over
-    bool ok = true;
-    auto hand_over = [&]() {
-      fence_proxy_async_smem();  // written by the threads, read by the tensor cores
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(pending));
-      pending = -1;
-    };
-    int chunk = warp - kThreads / 32;  // of the tile
-    for (int idx = first; ok && idx < total; idx += stride) {
-      if (chunk < chunks) {
-        const Tile t = table.at(idx, p.N, rank);
-        // rows past the tile and tokens outside a read as zero
-        const int mine = kTwo ? t.n >> 1 : t.n;  // rows of the tile in this CTA
-        int row[kRows];
+    // ---------------- gathered activation rows: eight threads a row, 16 bytes each.
+    // `per` warps share a stage, the groups of them take the stages in turn. A stage's
+    // copies report to its barrier as they land, and the MMA warp fences them, so these
+    // warps wait for free stages only. Measured with the warps waiting for their copies
+    // and fencing them (a stage a warp, handed over after the next one's issue) / with
+    // this, us: 14 experts of 5888 rows, 20818 MXFP8 rows, K = 512 122 / 91, K = 2048 190 /
+    // 175; 64 of 4096 x 2048, 6144 rows 73 / 65; 16 of 1920 x 1024, 8000 rows 122 / 26; 64
+    // of 4096 x 4096, 32744 rows 415 / 395 (MXFP4 rows 264 / 250; rows that need no
+    // gathering 350 and 206).
+    auto gather = [&](auto per_c) {
+      constexpr int kPer = decltype(per_c)::value, groups = 4 / kPer, apart = 4 * kPer;
+      constexpr int kRows = kStageRows / apart;  // rows per thread, so far apart
+      const int gw = warp - kThreads / 32;
+      const int c = lane & 7, r0 = (gw & (kPer - 1)) * 4 + (lane >> 3);
+      const uint32_t row_bytes = kA4 ? p.K >> 1 : p.K;
+      // apart is 8 or 16: one swizzle for all of a thread's rows
+      const uint32_t dst0 = base + kWBytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+      int s = gw / kPer;  // stages: at least as many as groups (the plan)
+      uint32_t ph = 1;
+      // the next stage's tile and place along K, and the same of the group's next tile
+      int idx = first, chunk = s;
+      auto find = [&](int& tile, int& place) {
+        while (place >= chunks && tile < total) place -= chunks, tile += stride;
+      };
+      // row numbers are read a tile ahead; rows past the tile and tokens outside read as zero
+      int row[kRows], ahead[kRows], mine = 0, mine_ahead = 0;
+      auto fetch_rows = [&](int tile) {
+        const Tile t = table.at(tile, p.N, rank);
+        mine_ahead = kTwo ? t.n >> 1 : t.n;  // rows of the tile in this CTA
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          const int i = r0 + 4 * j + rank * mine;
-          row[j] = r0 + 4 * j < mine && i < t.rows ? __ldg(p.tokens + t.row0 + i) : -1;
-          if (row[j] >= p.a_rows) row[j] = -1;
+          const int r = r0 + apart * j, i = r + rank * mine_ahead;
+          ahead[j] = r < mine_ahead && i < t.rows ? __ldg(p.tokens + t.row0 + i) : -1;
         }
-        for (; chunk < chunks; chunk += kWarps) {
-          if (pending >= 0 && !__all_sync(kFull, mbar_test_wait(empty(s), ph))) {
-            cp_async_wait<0>();
-            hand_over();
-          }
+      };
+      find(idx, chunk);
+      if (idx < total) fetch_rows(idx);
+      bool ok = true;
+      while (ok && idx < total) {
+        mine = mine_ahead;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) row[j] = ahead[j];
+        int next = idx, next_chunk = chunk + (chunks - chunk + groups - 1) / groups * groups;
+        find(next, next_chunk);
+        bool fetch = next < total;
+        for (; chunk < chunks; chunk += groups) {
           if (!(ok = warp_wait(empty(s), ph))) break;
           const uint32_t dst = dst0 + s * L.stage_bytes;
           const uint32_t at = static_cast<uint32_t>(chunk) * 128u + c * 16u;
           const bool in_row = at < row_bytes;
           const uint8_t* const col = p.a + (in_row ? at : 0u);
 #pragma unroll
-          for (int j = 0; j < kRows; ++j)
-            if (4 * j < mine)
-              cp_async_16(dst + j * 512 + swz[j & 1], col + static_cast<size_t>(max(row[j], 0)) * row_bytes,
-                          row[j] >= 0 && in_row ? 16u : 0u);
-          cp_async_commit();
-          if (pending >= 0) {
-            cp_async_wait<1>();
-            hand_over();
+          for (int j = 0; j < kRows; ++j) {
+            const bool real = static_cast<uint32_t>(row[j]) < static_cast<uint32_t>(p.a_rows);
+            if (apart * j < mine)
+              cp_async_16(dst + apart * j * 128, col + static_cast<size_t>(real ? row[j] : 0) * row_bytes,
+                          real && in_row ? 16u : 0u);
           }
-          pending = s;
-          s += kWarps;
+          cp_async_arrive(full(s));
+          s += groups;
           while (s >= stages) s -= stages, ph ^= 1u;
+          if (fetch) fetch_rows(next);
+          fetch = false;
         }
+        idx = next;
+        chunk = next_chunk;
       }
-      chunk -= chunks;
-    }
-    cp_async_wait<0>();
-    if (pending >= 0) hand_over();
-  } else if (warp == 3 || (kScaleWarps == 2 && warp == kExtraWarp)) {
+    };
+    if (kMode == kSmall || per == 4)
+      gather(std::integral_constant<int, 4>{});
+    else
+      gather(std::integral_constant<int, kMode == kSmall ? 4 : 2>{});
+    cp_async_wait_all();
+  } else if (warp == 3 || (kScaleWarps == 2 && warp == kScale2)) {
     // ---------------- activation scales: lane l serves rows l, l + 32, ... of the
     // tile, whose words (4 scale bytes) are one 16-byte store per 128 rows. A batch of
     // kBatch scale tiles is loaded at once, the next one while it is stored; with two
@@ -454,6 +469,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     for (int idx = first; ok && idx < total; idx += stride) {
       for (int i = 0; i < chunks; ++i) {
         if (!(ok = warp_wait(full(s), ph))) break;
+        if (kGather) fence_proxy_async_smem();
         if (lane == 0) mbar_arrive_remote(map_shared_rank(full(s), 0));
         __syncwarp();
         if (++s == stages) s = 0, ph ^= 1u;
@@ -522,6 +538,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       const bool wide = t.n > 128;
       for (int i = 0; i < chunks; ++i) {
         if (!__all_sync(kFull, landed) && !(ok = warp_wait(full(s), ph))) break;
+        if (kGather) fence_proxy_async_smem();  // the gathered rows came by the generic proxy
         tc_fence_after();
         if (elect_one()) {
           const bool ends = i == chunks - 1;
