@@ -847,6 +847,7 @@ int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp
   if (plan.stages < plan.min_stages) return MX_ERR_UNSUPPORTED;
   args.a = static_cast<const uint8_t*>(a);
   args.nt = plan.nt;
+  args.band = plan.band;
   args.stages = plan.stages;
   args.tmem_cols = plan.tmem_cols;
   args.status = h->d_status;

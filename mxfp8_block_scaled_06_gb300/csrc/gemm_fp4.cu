@@ -75,6 +75,11 @@ enum Mode : int {
 };
 __host__ __device__ constexpr int rows_round(int mode) { return mode == kPair ? 32 : 16; }  // MMA N's granule
 constexpr int kMaxE = kRouteMaxExperts;
+// Activations of more bytes than this go over the weights in bands of as many, so that a
+// band stays in L2 however many rows there are. Measured, us without bands / of 64 / 32 / 16
+// MB: 32744 x 4096 x 4096 423 / 364 / 348 / 348 (MXFP4 rows 208 / 209 / 191 / 187), 16384 x
+// 1280 x 16384 255 / 230 / 225 / 222, 60000 x 1024 x 2048 109 / 101 / 96 / 95.
+constexpr long kBandBytes = 16L << 20;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // Shared memory of one CTA, from its 1024-aligned base.
@@ -107,7 +112,7 @@ template <int kMode>
 struct Table {
   const int* cum;
   const int* off;
-  int E, nt;
+  int E, nt, band;
   __device__ Tile at(int idx, int N, int rank) const {
     constexpr int kRound = rows_round(kMode) - 1;
     int e = 0;
@@ -116,7 +121,16 @@ struct Table {
     const int count = off[e + 1] - off[e];
     const int tt = (count + nt - 1) / nt;
     const int local = idx - cum[e];
-    const int ni = local / tt, ti = local - ni * tt;
+    // an expert's tiles: all token tiles of a band with one weight tile after the other
+    int width = tt, r = local, ti = 0;
+    if (tt > band) {
+      const int whole = band * (N >> (kMode == kPair ? 8 : 7)), b = local / whole;
+      r = local - b * whole;
+      ti = b * band;
+      width = min(band, tt - ti);
+    }
+    const int ni = r / width;
+    ti += r - ni * width;
     const int per = ((count + tt - 1) / tt + kRound) & ~kRound;
     Tile t;
     t.n0 = kMode == kPair ? ni * 256 + rank * 128 : ni * 128;
@@ -231,7 +245,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   // before the wait; with early_weights warp 0 starts on the weights without it
   if (warp != 0 || !p.early_weights) pdl_wait();
   const uint32_t tmem = *tmem_slot;
-  const Table<kMode> table{cum, off, p.E, p.nt};
+  const Table<kMode> table{cum, off, p.E, p.nt, p.band};
   const int total = cum[p.E];
   // one wait for the whole warp; false (for all lanes) once it has expired anywhere
   auto warp_wait = [&](uint32_t bar, uint32_t parity) {
@@ -699,6 +713,7 @@ GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count) 
   // keeps any more than fit from being resident
   pl.smem = std::max(Layout(pl.nt, pl.a_rows, pl.stages, kt, E).total(),
                      static_cast<size_t>(233472 / (pl.ctas_per_sm + 1) + 1));
+  pl.band = static_cast<int>(std::clamp(kBandBytes / (static_cast<long>(pl.nt) * (a_fp4 ? K / 2 : K)), 1L, 1L << 24));
   const int ctas = pl.mode == kPair ? 2 : 1;  // of a tile
   const long tiles = static_cast<long>(N / (128 * ctas)) * std::min<long>((R + pl.nt - 1L) / pl.nt + E - 1, R);
   pl.grid = static_cast<int>(std::min<long>(tiles, static_cast<long>(sm_count) * pl.ctas_per_sm / ctas)) * ctas;

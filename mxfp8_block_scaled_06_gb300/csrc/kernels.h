@@ -252,6 +252,7 @@ struct GemmFp4Args {
   int a_rows;               // rows of a
   const uint8_t* a;         // the activations, read directly where tokens is set
   int nt;                   // largest token tile (MMA N), a multiple of 16
+  int band;                 // token tiles that go over all weight tiles together
   int stages, tmem_cols;
   const uint8_t* a_scales;  // plain [a_rows, K / 32], or (a_swizzled) the 128x4 layout
   int a_swizzled;
@@ -266,7 +267,7 @@ struct GemmFp4Args {
 struct GemmFp4Plan {
   int mode;    // how CTAs share SMs and tiles (gemm_fp4.cu)
   int a_rows;  // activation rows of a stage: the tensor map's box
-  int nt, stages, min_stages, tmem_cols, ctas_per_sm, grid;
+  int nt, band, stages, min_stages, tmem_cols, ctas_per_sm, grid;
   size_t smem;
 };
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count);

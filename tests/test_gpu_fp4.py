@@ -132,6 +132,12 @@ def test_product_of_the_widest_tiles(mx, m, n, k, fp4):
     test_product(mx, m, n, k, fp4)
 
 
+@pytest.mark.parametrize("m,n,k,fp4", [(26500, 512, 640, False), (30011, 384, 1152, True), (33000, 384, 512, False)])
+def test_product_of_more_rows_than_a_band(mx, m, n, k, fp4):
+    """Activations of over 16 MB go over the weights in bands of rows."""
+    test_product(mx, m, n, k, fp4)
+
+
 @pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("pdl", [False, True])
 @pytest.mark.parametrize("m,n,k", [(1, 1024, 2688), (1, 8192, 3840), (7, 256, 6016), (16, 128, 4096), (17, 6144, 2560),
