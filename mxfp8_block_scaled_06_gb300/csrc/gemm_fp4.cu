@@ -590,17 +590,18 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       if (!(ok = warp_wait(acc_full + 8 * buf, (it >> 1) & 1))) break;
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * p.nt;
-      // Plain: a lane stores its column, 64 bytes of a token to a warp; trading
-      // columns for wider stores first was no faster (100 us against 101 with two
-      // columns of a token to a lane, 118 with four; 8192 x 8192 x 5120).
+      // Plain: two neighbouring lanes trade two tokens, so that a lane stores two columns of
+      // one; in narrow tiles four lanes four tokens. Measured, us, a column a lane / two /
+      // four: 20818 rows of 14 experts, N = 5888, K = 512 96 / 92 / 97; 32744 of 64, N = 4096,
+      // K = 1408 132 / 132 / 137; 7182 x 8192 x 768 51.5 / 50.6 / 52.3; narrow: 128 x 8192 x
+      // 512 7.3 / 7.1 / 6.5, 8 x 8192 x 1536 5.1 / 5.0 / 4.6.
       // Gated: four neighbouring lanes trade the four tokens c0 + 4i .. + 3, first in
       // pairs, the even lane taking gate and up of tokens 0 and 2, the odd one of 1
       // and 3; then, the products in bf16, between the pairs, the first one taking
       // tokens 0 and 1. A lane stores two columns of one token.
-      const int tok0 = (lane & 2) + odd;
-      const int col = t.n0 + q * 32 + (p.gated ? lane & ~3 : lane);
-      __nv_bfloat16* out = p.gated ? p.out + (static_cast<size_t>(t.row0) + tok0) * ldo + (col >> 1)
-                                   : p.out + static_cast<size_t>(t.row0) * ldo + col;
+      const int tok0 = p.gated || kMode == kSmall ? (lane & 2) + odd : odd;
+      const int col = t.n0 + q * 32 + (p.gated || kMode == kSmall ? lane & ~3 : lane & ~1);
+      __nv_bfloat16* out = p.out + (static_cast<size_t>(t.row0) + tok0) * ldo + (p.gated ? col >> 1 : col);
       constexpr int kStep = 16 * kEpilogue / 4;  // of eight warps, four take every other 16 tokens
       const int c_first = kEpilogue == 8 && warp >= 8 ? 16 : 0;
       out += c_first * ldo;
@@ -608,13 +609,27 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
         float v[16];
         tmem_ld_32x32b_x16(acc + c0, v);
         if (!p.gated) {
-          if (c0 + 16 <= t.rows) {
+          const bool all = c0 + 16 <= t.rows;
+          uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) out[i * ldo] = __float2bfloat16_rn(v[i]);
+          for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            const uint32_t own = *reinterpret_cast<const uint32_t*>(&two);
+            const uint32_t got = __shfl_xor_sync(kFull, own, 1);
+            w[i] = odd ? __byte_perm(got, own, 0x7632) : __byte_perm(own, got, 0x5410);
+          }
+          if constexpr (kMode == kSmall) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t got = __shfl_xor_sync(kFull, lane & 2 ? w[2 * i] : w[2 * i + 1], 2);
+              if (all || c0 + 4 * i + tok0 < t.rows)
+                *reinterpret_cast<uint2*>(out + 4 * i * ldo) =
+                    lane & 2 ? make_uint2(got, w[2 * i + 1]) : make_uint2(w[2 * i], got);
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < t.rows) out[i * ldo] = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 8; ++i)
+              if (all || c0 + 2 * i + tok0 < t.rows) *reinterpret_cast<uint32_t*>(out + 2 * i * ldo) = w[i];
           }
           out += kStep * ldo;
           continue;
