@@ -358,8 +358,8 @@ int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, in
  *   w, w_scales  MXFP4 weights [N, K] packed, scales in the 128x4 layout; both
  *                32-byte aligned
  *   flags        MX_FLAG_PDL or 0, as for mx_gemm
- * Up to 256 rows the call takes mx_gemm's kernel (K split over a cluster) where that is
- * the faster one, otherwise a kernel of whole-K tiles.
+ * The call takes mx_gemm's kernel (K split over a cluster) where that is the faster one
+ * (few rows or few columns), otherwise a kernel of whole-K tiles.
  * Constraints: 1 <= M <= 2^24, N % 128 == 0, K % 128 == 0, (N / 128) (M / 16 + 1) < 2^31,
  * else MX_ERR_UNSUPPORTED. */
 int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_scales, int a_fp4,
