@@ -462,15 +462,16 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
 }
 
 // v[0..n) become the sums of the values before each, by one warp; returns the sum of
-// all. n <= 512; the loads are issued together.
+// all. n <= 608; the loads are issued together.
 __device__ __forceinline__ int exclusive_scan(int* v, int n) {
   const int lane = threadIdx.x & 31;
-  int own[16];
+  constexpr int kOwn = std::max(kRouteChunks, kRouteMaxExperts) / 32;
+  int own[kOwn];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) own[i] = 32 * i + lane < n ? v[32 * i + lane] : 0;
+  for (int i = 0; i < kOwn; ++i) own[i] = 32 * i + lane < n ? v[32 * i + lane] : 0;
   int run = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kOwn; ++i) {
     if (32 * i >= n) break;
     int s = own[i];
 #pragma unroll
