@@ -465,6 +465,28 @@ typedef struct mx_plan_info {
 int mx_plan_gemm(int M, int N, int K, int sm_count, int fused, int norm, int push,
                  mx_plan_info* out);
 
+/* As mx_plan_info, for a product with MXFP4 weights. */
+#define MX_REDUCE_BULK 4 /* each CTA copies the rows another rank owns, as one block */
+typedef struct mx_plan_fp4_info {
+  int splits;      /* K-splits: the CTAs of one cluster; 1: tiles of the whole K */
+  int rows;        /* rows of a cluster (slices of all rows), or at most of a token tile */
+  int mtile;       /* rows as the MMA's N: a multiple of 16 */
+  int slices;      /* clusters that take all rows, for each 128 weight rows; 0: whole K */
+  int scale_tiles; /* the launch reads the first so many 128-row tiles of a_scales */
+  int stages;      /* ring depth, and the least that the form may have */
+  int min_stages;
+  int tmem_cols;   /* tensor-memory columns per CTA */
+  int reduction;   /* MX_REDUCE_*, of K-splits */
+  size_t smem;     /* dynamic shared memory per CTA, bytes */
+} mx_plan_fp4_info;
+
+/* The plan that mx_gemm_fp4 (E = 0, R = M rows) or mx_gemm_fp4_grouped (E experts, R rows) makes
+ * on a device with sm_count SMs that holds clusters[s - 2] clusters of s = 2..8 CTAs at
+ * once, one CTA to an SM. flags as for mx_gemm_fp4. Returns MX_ERR_INVALID_ARG where the
+ * entry point would refuse the sizes, and for sm_count < 1 or a null pointer. */
+int mx_plan_gemm_fp4(int E, int R, int N, int K, int a_fp4, unsigned flags, int sm_count, const int clusters[7],
+                     mx_plan_fp4_info* out);
+
 /* The push receive area (MX_PUSH_*) each of the three projections w[0..2] of
  * mx_gemm_chain (norm = 0) or mx_gemm_chain_norm (norm = 1) takes at M rows on
  * a device with sm_count SMs, smem_per_sm bytes of shared memory per SM and

@@ -27,7 +27,8 @@ MX_FLAG_PDL = 1
 EXPORTS = ["mx_create", "mx_destroy", "mx_scale_bytes", "mx_quantize_rows",
            "mx_rmsnorm_quantize_rows", "mx_gemm", "mx_gemm_bf16", "mx_gemm_chain",
            "mx_gemm_chain_norm", "mx_gemm_chain_noalloc", "wo_a_grouped", "wo_a_grouped_unfused",
-           "mx_warmup_bytes", "mx_warmup", "mx_plan_gemm", "mx_plan_chain_push", "mx_device_status",
+           "mx_warmup_bytes", "mx_warmup", "mx_plan_gemm", "mx_plan_gemm_fp4", "mx_plan_chain_push",
+           "mx_device_status",
            "mx_wait_selftest", "mx_status_string", "mx_quantize_rows_fp4", "mx_gemm_fp4", "mx_gemm_fp4_grouped",
            "mx_route", "mx_combine"]
 
@@ -39,7 +40,7 @@ class MxWeight(ctypes.Structure):
 
 
 # reduction forms and push receive areas of the plan queries (include/mx.h)
-MX_REDUCE_ITEMS, MX_REDUCE_ROWS, MX_REDUCE_PUSH, MX_REDUCE_PUSH_COMPACT = range(4)
+MX_REDUCE_ITEMS, MX_REDUCE_ROWS, MX_REDUCE_PUSH, MX_REDUCE_PUSH_COMPACT, MX_REDUCE_BULK = range(5)
 MX_PUSH_NONE, MX_PUSH_COMPACT, MX_PUSH_FULL = range(3)
 # element types and router scorings (include/mx.h)
 MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32 = range(3)
@@ -49,6 +50,11 @@ MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = range(2)
 class MxPlanInfo(ctypes.Structure):
     _fields_ = [("splits", _i), ("stages", _i), ("mtile", _i), ("tmem_cols", _i), ("reduction", _i),
                 ("smem", ctypes.c_size_t)]
+
+
+class MxPlanFp4Info(ctypes.Structure):
+    _fields_ = [(f, _i) for f in ("splits", "rows", "mtile", "slices", "scale_tiles", "stages", "min_stages",
+                                  "tmem_cols", "reduction")] + [("smem", ctypes.c_size_t)]
 
 
 class MxError(RuntimeError):
@@ -85,6 +91,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mx_warmup_bytes.argtypes = [ctypes.POINTER(MxWeight), _i, ctypes.POINTER(_i), _i]
     lib.mx_warmup_bytes.restype = ctypes.c_size_t
     lib.mx_plan_gemm.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(MxPlanInfo)]
+    lib.mx_plan_gemm_fp4.argtypes = [_i, _i, _i, _i, _i, _u, _i, ctypes.POINTER(_i), ctypes.POINTER(MxPlanFp4Info)]
     lib.mx_plan_chain_push.argtypes = [_i, ctypes.POINTER(MxWeight), _i, _i, ctypes.c_size_t, ctypes.c_size_t,
                                        ctypes.POINTER(_i)]
     lib.mx_warmup.argtypes = [_vp, ctypes.POINTER(MxWeight), _i, ctypes.POINTER(_i), _i, _vp,
@@ -777,6 +784,16 @@ def mx_plan_gemm(m: int, n: int, k: int, sm_count: int = 152, fused: bool = Fals
     _check(load_library().mx_plan_gemm(m, n, k, sm_count, int(fused), int(norm), push, ctypes.byref(info)),
            "mx_plan_gemm")
     return {f: getattr(info, f) for f, _ in MxPlanInfo._fields_}
+
+
+def mx_plan_gemm_fp4(m: int, n: int, k: int, experts: int = 0, fp4_activations: bool = False, pdl: bool = False,
+                     sm_count: int = 152, clusters=(76, 46, 36, 28, 23, 15, 15)) -> dict:
+    """The plan of mx_gemm_fp4 for m rows, or (experts > 0) of mx_gemm_fp4_grouped, on a device
+    with sm_count SMs that holds so many clusters of 2..8 CTAs at once. Host only."""
+    info = MxPlanFp4Info()
+    _check(load_library().mx_plan_gemm_fp4(experts, m, n, k, int(fp4_activations), MX_FLAG_PDL if pdl else 0, sm_count,
+                                           (_i * 7)(*clusters), ctypes.byref(info)), "mx_plan_gemm_fp4")
+    return {f: getattr(info, f) for f, _ in MxPlanFp4Info._fields_}
 
 
 def mx_plan_chain_push(m: int, shapes, norm: bool = False, sm_count: int = 152, smem_per_sm: int = 233472,

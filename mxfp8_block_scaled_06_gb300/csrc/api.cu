@@ -837,12 +837,21 @@ int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, in
 
 namespace {
 
+// mx_gemm_fp4's plan of K split over a cluster, or whether whole-K tiles take the product.
+int fp4_push_mode(unsigned flags) {
+  // behind a kernel that it overlaps the push exchange is the faster (gemm.cu)
+  return flags & MX_FLAG_PDL ? mx::kPushFull : mx::kPushNone;
+}
+bool fp4_splits_k(const mx::GemmPlan& plan) { return plan.splits > 1 && plan.smem <= mx::kMaxDynamicSmem; }
+
+// tile numbers of the whole-K products are 32-bit; a token tile has 16 rows at least
+bool fp4_tiles_fit(int E, int R, int N) { return static_cast<long>(N / 128) * (R / 16 + E) < (1L << 31); }
+
 // The tensor maps and the launch shared by the two entry points below; the
 // arguments are validated by the callers.
 int gemm_fp4_launch(mx_handle* h, mx::GemmFp4Args& args, const void* a, int a_fp4, const void* w,
                     cudaStream_t stream) {
-  // tile numbers are 32-bit; a token tile has 16 rows at least
-  if (static_cast<long>(args.N / 128) * (args.R / 16 + args.E) >= (1L << 31)) return MX_ERR_UNSUPPORTED;
+  if (!fp4_tiles_fit(args.E, args.R, args.N)) return MX_ERR_UNSUPPORTED;
   const mx::GemmFp4Plan plan = mx::plan_gemm_fp4(args.E, args.R, args.N, args.K, a_fp4 != 0, h->sm_count);
   if (plan.stages < plan.min_stages) return MX_ERR_UNSUPPORTED;
   args.a = static_cast<const uint8_t*>(a);
@@ -872,10 +881,8 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
     return MX_ERR_INVALID_ARG;
   if (N % 128 != 0 || K % 128 != 0 || M > kMaxFp4Rows) return MX_ERR_UNSUPPORTED;
   const int fmt = a_fp4 ? 2 : 1;
-  // behind a kernel that it overlaps the push exchange is the faster (gemm.cu)
-  const int push = flags & MX_FLAG_PDL ? mx::kPushFull : mx::kPushNone;
-  const mx::GemmPlan plan = get_plan(h, M, N, K, false, false, push, true, fmt);
-  if (plan.splits > 1 && plan.smem <= mx::kMaxDynamicSmem) {
+  const int push = fp4_push_mode(flags);
+  if (fp4_splits_k(get_plan(h, M, N, K, false, false, push, true, fmt))) {
     GemmLaunch L;
     rc = gemm_prepare(h, &L, M, N, K, a, a_scales, w, w_scales, out, nullptr, nullptr, 0, nullptr, 0, 1, nullptr,
                       push, true, fmt);
@@ -1054,6 +1061,31 @@ int mx_plan_gemm(int M, int N, int K, int sm_count, int fused, int norm, int pus
     return MX_ERR_INVALID_ARG;
   const mx::GemmPlan pl = mx::plan_gemm(M, N, K, sm_count, mx::read_plan_env(), fused != 0, norm != 0, push);
   *out = mx_plan_info{pl.splits, pl.stages, pl.mtile, pl.tmem_cols, pl.reduction, pl.smem};
+  return MX_OK;
+}
+
+static_assert(MX_REDUCE_BULK == mx::kReduceBulk, "mx.h reduction codes");
+
+int mx_plan_gemm_fp4(int E, int R, int N, int K, int a_fp4, unsigned flags, int sm_count, const int clusters[7],
+                     mx_plan_fp4_info* out) {
+  if (out == nullptr || clusters == nullptr || E < 0 || E > mx::kRouteMaxExperts || R < 1 || R > kMaxFp4Rows ||
+      N < 128 || N % 128 != 0 || K < 128 || K % 128 != 0 || sm_count < 1 || (flags & ~MX_FLAG_PDL) ||
+      !fp4_tiles_fit(std::max(E, 1), R, N))
+    return MX_ERR_INVALID_ARG;
+  if (E == 0) {
+    mx::PlanEnv env = mx::read_plan_env();
+    for (int s = 2; s <= 8; ++s) env.clusters[s] = clusters[s - 2];
+    const mx::GemmPlan pl = mx::plan_gemm(R, N, K, sm_count, env, false, false, fp4_push_mode(flags), true,
+                                          a_fp4 ? 2 : 1);
+    if (fp4_splits_k(pl)) {
+      const int before = (pl.slices - 1) * pl.slice;  // rows before the last slice
+      *out = mx_plan_fp4_info{pl.splits, pl.slice, pl.mtile, pl.slices, before / 128 + mx::scale_row_tiles(R - before),
+                              pl.stages, 1, pl.tmem_cols, pl.reduction, pl.smem};
+      return MX_OK;
+    }
+  }
+  const mx::GemmFp4Plan pl = mx::plan_gemm_fp4(std::max(E, 1), R, N, K, a_fp4 != 0, sm_count);
+  *out = mx_plan_fp4_info{1, pl.nt, pl.nt, 0, mx::scale_row_tiles(R), pl.stages, pl.min_stages, pl.tmem_cols, 0, pl.smem};
   return MX_OK;
 }
 

@@ -225,6 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int units = kFmt == kFmtMx8 ? p.nchunks : p.K >> 7;
   const int n_units = kFmt == kFmtMx8 ? n : min(n * sf_tiles(kFmt), units - c_begin * sf_tiles(kFmt));
   const int nsfb = L.nsfb;
+  // row tiles of activation scales behind this CTA's rows: the last slice may have fewer
+  // than the tile, and the scales end with the rows
+  const int have_sfb = scale_row_tiles(M);
   // Whether anything consumes the output columns of the tile's 32-column block
   // q: a block nobody consumes (no bf16 output, outside the requantized and the
   // summed-square columns) is not reduced.
@@ -374,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a_lane && lane < n) issue_a(lane, lane);
     if (warp == 3) issued_n = min(n, stages);
     if (warp == 2 && lane == 1) {
-      mbar_expect_tx(sfb_bar, static_cast<uint32_t>(n_units * nsfb) * kSfTileBytes);
-      for (int rt = 0; rt < nsfb; ++rt)
+      mbar_expect_tx(sfb_bar, static_cast<uint32_t>(n_units * have_sfb) * kSfTileBytes);
+      for (int rt = 0; rt < have_sfb; ++rt)
         bulk_load(base + L.sfb_off(rt, 0),
                   p.a_scales + (static_cast<size_t>(m_first / 128 + rt) * p.a_sf_chunks + a_k0 / 128 +
                                 c_begin * sf_tiles(kFmt)) * kSfTileBytes,
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u < have) {
               tmem_cp_32x128b_x4_lh(ta + 4 * u, f_lo + u * (kSfTileBytes >> 4), sf_hi);
               tmem_cp_32x128b_x4_lh(tb + 4 * u * nsfb, g_lo + u * (kSfTileBytes >> 4), sf_hi);
-              if (nsfb > 1)
+              if (have_sfb > 1)  // otherwise the columns that they scale are not stored
                 tmem_cp_32x128b_x4_lh(tb + 4 * u * nsfb + 4, g_lo + rt_units + u * (kSfTileBytes >> 4), sf_hi);
             }
           }

@@ -63,13 +63,16 @@ enum Reduction : int { kReduceItems = 0, kReduceRows = 1, kReducePush = 2, kRedu
 // Whether a plan may take the push reduction, and with which receive area.
 enum PushMode : int { kPushNone = 0, kPushCompact = 1, kPushFull = 2 };
 
+// 128-row tiles of block scales behind `rows` rows.
+__host__ __device__ constexpr int scale_row_tiles(int rows) { return (rows + 127) / 128; }
+
 struct GemmPlan {
   int mtile;
   int splits;
   int stages;
   int tmem_cols;
   int reduction;  // Reduction
-  int slice, slices;  // rows of a cluster (MXFP4 weights: multiples of 128), and how many take all
+  int slice, slices;  // rows of a cluster, and how many take all (MXFP4 weights: slices of 128 or 256)
   size_t smem;
 };
 

@@ -1,0 +1,48 @@
+"""Plan queries of the products with MXFP4 weights (host only, no GPU), over rows, shapes and
+both kinds of activations: what a launch reads and holds, as invariants of the plans."""
+import itertools
+
+import pytest
+
+import mxfp8_block_scaled_06_gb300 as mx
+
+MAX_SMEM = 232448
+NS = [128, 256, 640, 1024, 2048, 2560, 4096, 5120, 8192]
+KS = [128, 384, 1536, 2048, 5120, 8192, 10368, 16384]
+ROWS = [1, 2, 15, 16, 17, 48, 49, 64, 65, 100, 128, 129, 200, 240, 256, 257, 300, 344, 384, 385, 500, 512, 513, 600, 640,
+        641, 1000, 2048]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+
+
+def plans(rows=ROWS):
+    for m, n, k, fp4, pdl in itertools.product(rows, NS, KS, (False, True), (False, True)):
+        yield (m, n, k, fp4, pdl), mx.mx_plan_gemm_fp4(m, n, k, fp4_activations=fp4, pdl=pdl)
+
+
+def test_scale_tiles_read_are_those_of_the_rows():
+    """The scales end with the last row's 128-row tile, however the rows are sliced."""
+    wide = 0
+    for case, p in plans():
+        assert p["scale_tiles"] == (case[0] + 127) // 128, (case, p)
+        wide += p["slices"] > 1 and p["rows"] == 256 and (case[0] - 1) % 256 < 128
+    assert wide > 0  # slices of 256 rows of which the last has one tile only
+
+
+def test_slices_take_all_rows():
+    for case, p in plans():
+        assert p["splits"] == 1 or p["slices"] * p["rows"] >= case[0] > (p["slices"] - 1) * p["rows"], (case, p)
+
+
+def test_rejects_bad_arguments():
+    for args in ((0, 256, 256), (1 << 25, 256, 256), (1, 200, 256), (1, 256, 200), (1, 0, 256)):
+        with pytest.raises(mx.MxError):
+            mx.mx_plan_gemm_fp4(*args)
+    for kw in (dict(experts=-1), dict(experts=513), dict(sm_count=0)):
+        with pytest.raises(mx.MxError):
+            mx.mx_plan_gemm_fp4(1, 256, 256, **kw)
