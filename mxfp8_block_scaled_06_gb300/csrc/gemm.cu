@@ -1158,10 +1158,14 @@ constexpr int kRowsMax = 48;
 // of 128 rows / one of all: N = 1024, K = 10368, 256 rows 10.7 / 14.4; N = 5120, K = 8192,
 // 201 rows, three splits 15.3 / 14.4 (rows; bulk 12.9). N = 256, K = 16000, 344 rows
 // 9.1, whole K 24.4.
+// Only splits whose plan fits in shared memory (`fits`) are taken: four splits of 240 rows and
+// more mostly do not (the staged partials and the peers' blocks: 224 KB), and 256 rows, N =
+// 4096, K = 8192 then go as two slices of two splits instead of whole K.
 struct W4Split {
   int slice, splits;
 };
-W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4) {
+template <typename Fits>
+W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4, const Fits& fits) {
   const int sft = a_fp4 ? 2 : 1, chunks = (K / 128 + sft - 1) / sft;
   const long walk = (a_fp4 ? 110L : 180L) * (K / 128);
   W4Split best{std::min(M, 128), 1};
@@ -1178,7 +1182,7 @@ W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4) {
                                                        : 1300 + (two ? 16L : 12L) * slice)
                             : s > 4           ? 2300 + (two ? 22L : 7L) * slice
                                               : 1300 + (two ? 30L : 14L) * slice;
-      if (way + exchange < least) {
+      if (way + exchange < least && fits(slice, s)) {
         least = way + exchange;
         best = {slice, s};
       }
@@ -1191,32 +1195,21 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
                    int push_mode, bool table_depth, int w_fmt) {
   int force_splits, force_stages;
   plan_override(env.plan_at, N, K, &force_splits, &force_stages);
-  const W4Split w4 = w_fmt != kFmtMx8 ? w4_split(M, N, K, env, w_fmt == kFmtW4A4) : W4Split{M, 1};
-  const int slices = (M + w4.slice - 1) / w4.slice;
-  if (w_fmt != kFmtMx8 && slices > 2) force_splits = 0;  // overrides are for the decode shapes
-  const int env_splits = w_fmt != kFmtMx8 && slices > 2 ? 0 : env.splits;
-  if (w_fmt != kFmtMx8 && (env_splits | force_splits) <= 1 && w4.splits == 1) {
-    GemmPlan whole{};
-    whole.splits = 1;
-    return whole;
-  }
-  M = w4.slice;  // rows of a cluster
-  const int mtile = (M + 15) & ~15;
-  const int tiles = N / 128 * slices;
   const int sft = sf_tiles(w_fmt);
   const int nchunks = (K / 128 + sft - 1) / sft;
-  const int nsfb = (mtile + 127) / 128;
-  const int xrows = std::min(M, kRowBatch);
   const int push_rows = env.push_rows >= 0 ? env.push_rows : kPushMaxRows;
-  // the scale tiles of a CTA's K-range stay resident: at most 48 KB of them
-  auto scale_bytes = [&](int sp) {
-    return static_cast<size_t>((nchunks + sp - 1) / sp) * sft * kSfTileBytes * (1 + nsfb);
-  };
-  // the plan for a given number of K splits
-  auto plan_for = [&](int splits) {
+  // the plan for a given number of rows of a cluster and of K splits
+  auto plan_of = [&](int rows, int splits) {
     GemmPlan pl{};
+    const int mtile = (rows + 15) & ~15, slices = (M + rows - 1) / rows, tiles = N / 128 * slices;
+    const int nsfb = (mtile + 127) / 128;
+    const int xrows = std::min(rows, kRowBatch);
+    // the scale tiles of a CTA's K-range stay resident: at most 48 KB of them
+    auto scale_bytes = [&](int sp) {
+      return static_cast<size_t>((nchunks + sp - 1) / sp) * sft * kSfTileBytes * (1 + nsfb);
+    };
     pl.mtile = mtile;
-    pl.slice = M;
+    pl.slice = rows;
     pl.slices = slices;
     while (splits < std::min(8, nchunks) && scale_bytes(splits) > 48 * 1024) ++splits;
     pl.splits = splits;
@@ -1240,19 +1233,19 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     // the epilogue stages the fp32 partials [mtile][128] over the ring and what follows it
     // (bulk reduction: and what the peers send)
     const size_t staged = static_cast<size_t>(mtile) * 512 +
-                          (w_fmt != kFmtMx8 ? static_cast<size_t>(splits - 1) * ((M + splits - 1) / splits) * 512 : 0);
+                          (w_fmt != kFmtMx8 ? static_cast<size_t>(splits - 1) * ((rows + splits - 1) / splits) * 512 : 0);
     while (static_cast<size_t>(stages) * L1.stage_bytes + scales < staged)
       ++stages;
     pl.stages = stages;
     pl.tmem_cols = pow2_at_least(tmem_sfa_col(mtile) + 4 * sft * stages * (1 + nsfb));
     // the push reduction (where asked for and its receive area fits)
-    const uint32_t area = push_area_bytes(M, splits, push_mode == kPushCompact);
-    const bool push = push_mode != kPushNone && M <= push_rows &&
+    const uint32_t area = push_area_bytes(rows, splits, push_mode == kPushCompact);
+    const bool push = push_mode != kPushNone && rows <= push_rows &&
                       (w_fmt == kFmtMx8 || tiles <= env.clusters[splits]) &&
                       Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area, sft).total() <=
                           kMaxDynamicSmem;
-    pl.reduction = !push                         ? w_fmt != kFmtMx8          ? M <= kRowsMax ? kReduceRows : kReduceBulk
-                                                   : row_reduction(M, splits) ? kReduceRows
+    pl.reduction = !push                         ? w_fmt != kFmtMx8          ? rows <= kRowsMax ? kReduceRows : kReduceBulk
+                                                   : row_reduction(rows, splits) ? kReduceRows
                                                                               : kReduceItems
                    : push_mode == kPushCompact ? kReducePushCompact
                                                : kReducePush;
@@ -1264,6 +1257,23 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
     pl.smem = std::max(L.total(), min_smem);
     return pl;
   };
+  // the rows of a cluster with MXFP4 weights, and their K splits; otherwise all rows
+  W4Split w4{M, 1};
+  if (w_fmt != kFmtMx8)
+    w4 = w4_split(M, N, K, env, w_fmt == kFmtW4A4, [&](int rows, int splits) {
+      const GemmPlan pl = plan_of(rows, splits);
+      return pl.splits == splits && pl.smem <= kMaxDynamicSmem;
+    });
+  const int slices = (M + w4.slice - 1) / w4.slice;
+  if (w_fmt != kFmtMx8 && slices > 2) force_splits = 0;  // overrides are for the decode shapes
+  const int env_splits = w_fmt != kFmtMx8 && slices > 2 ? 0 : env.splits;
+  if (w_fmt != kFmtMx8 && (env_splits | force_splits) <= 1 && w4.splits == 1) {
+    GemmPlan whole{};
+    whole.splits = 1;
+    return whole;
+  }
+  const int tiles = N / 128 * slices;
+  auto plan_for = [&](int splits) { return plan_of(w4.slice, splits); };
   int splits = std::max(1, sm_count / std::max(tiles, 1));
   // the table was measured with 152 SMs; other parts keep the SM-count rule
   const SplitEntry* te = sm_count == 152 && w_fmt == kFmtMx8 ? table_entry(M, N, K) : nullptr;

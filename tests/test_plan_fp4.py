@@ -46,3 +46,17 @@ def test_rejects_bad_arguments():
     for kw in (dict(experts=-1), dict(experts=513), dict(sm_count=0)):
         with pytest.raises(mx.MxError):
             mx.mx_plan_gemm_fp4(1, 256, 256, **kw)
+
+
+def test_every_plan_fits():
+    for case, p in plans():
+        assert p["smem"] <= MAX_SMEM and p["tmem_cols"] <= 512 and p["stages"] >= p["min_stages"], (case, p)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_slices_of_128_rows_are_open_to_more_rows(fp4):
+    """j slices of 128 rows cost what one costs against j times the columns (the same clusters):
+    where that splits K, so does the product of 128 j rows."""
+    for j, n, k in itertools.product((2, 3, 4, 5, 8), NS, KS):
+        if mx.mx_plan_gemm_fp4(128, j * n, k, fp4_activations=fp4)["splits"] > 1:
+            assert mx.mx_plan_gemm_fp4(128 * j, n, k, fp4_activations=fp4)["splits"] > 1, (j, n, k)
