@@ -407,7 +407,8 @@ int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a,
  *   tokens   out [T * top_k] int32: the token of each row in that order
  *   slots    out [T, top_k] int32: the row of each pair
  * -inf and NaN logits (masked experts) and experts of -inf or NaN bias come after all
- * others; a masked logit's weight is 0. +inf counts as the largest float32.
+ * others; a masked logit's weight is 0. +inf, as a logit or a bias, counts as the largest
+ * float32.
  * Scratch: a fixed part of the handle (calls on one handle whose work overlaps on the
  * GPU race on it: give each stream its own handle).
  * Constraints: E % n_groups == 0, top_k <= topk_groups * (E / n_groups); E <= 512,

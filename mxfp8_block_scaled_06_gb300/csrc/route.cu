@@ -21,7 +21,8 @@
 // computed again in float64. With 256 experts that is a few tokens in a thousand.
 //
 // Masked logits: -inf and NaN logits have score 0 and are chosen last; +inf
-// counts as the largest float. When every chosen score is 0 so are the weights.
+// counts as the largest float, and so does a bias of +inf (keys and their errors stay
+// finite). When every chosen score is 0 so are the weights.
 //
 // Row order: the tokens are cut into at most kRouteChunks chunks; each chunk
 // counts its rows per expert and numbers them in (token, choice) order, one warp per
@@ -54,6 +55,12 @@ __device__ __forceinline__ float unord32(uint32_t o) {
 __device__ __forceinline__ float load_logit(const void* p, size_t i, int bf16) {
   const float f = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
   return isnan(f) ? -CUDART_INF_F : fminf(f, CUDART_MAX_NORMAL_F);
+}
+
+// An expert's bias: NaN counts as -inf, +inf as the largest float.
+__device__ __forceinline__ float load_bias(const float* p, int e) {
+  const float b = p[e];
+  return isnan(b) ? -CUDART_INF_F : fminf(b, CUDART_MAX_NORMAL_F);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -120,8 +127,8 @@ __device__ __noinline__ double sum64(const RouteArgs& p, size_t base, float top)
 
 __device__ __forceinline__ double key64(const RouteArgs& p, size_t base, int e, float top, double sum) {
   const double x = load_logit(p.logits, base + e, p.bf16);
-  const float b = p.bias[e];
-  if (x == -CUDART_INF || isnan(b)) return -CUDART_INF;
+  const float b = load_bias(p.bias, e);
+  if (x == -CUDART_INF) return -CUDART_INF;
   return (p.scoring == kScoreSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum) + static_cast<double>(b);
 }
 
@@ -341,7 +348,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float s = p.scoring == kScoreSigmoid ? quick_sigmoid(x[i]) : __expf(x[i] - t.top) * inv;
-      if (x[i] > -CUDART_INF_F) x[i] = s + bias[i];  // a bias of NaN is -inf here
+      if (x[i] > -CUDART_INF_F) x[i] = s + bias[i];
     }
   }
 #pragma unroll
@@ -435,7 +442,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       bool close = false;
       if (lane > 0 && lane < n && k > kMasked && !(unord32(ko) - unord32(k) > 2.f * far))
         close = load_logit(p.logits, base + eo, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
-                p.bias[eo] != p.bias[e];
+                load_bias(p.bias, eo) != load_bias(p.bias, e);
       if (__any_sync(kFull, close)) mine = order64(p, base, e, n, t.top, reinterpret_cast<volatile int*>(shared));
     }
   } else if (p.bias != nullptr) {
@@ -529,8 +536,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 4) route_kernel(const __grid
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
-    bias[i] = p.bias != nullptr && e < p.E ? p.bias[e] : 0.f;
-    if (isnan(bias[i])) bias[i] = -CUDART_INF_F;
+    bias[i] = p.bias != nullptr && e < p.E ? load_bias(p.bias, e) : 0.f;
     if (bias[i] > -CUDART_INF_F) largest_bias = fmaxf(largest_bias, fabsf(bias[i]));
     if (e < p.E) groups[i / 6] |= div_u32(e, p.per_group) << (5 * (i % 6));
   }

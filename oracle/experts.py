@@ -84,7 +84,7 @@ def route(logits, top_k, bias=None, scoring="softmax", n_groups=1, topk_groups=1
             s /= s.sum()
         key = row.copy()
         if bias is not None:
-            b = np.asarray(bias, dtype=np.float64)
+            b = np.minimum(np.asarray(bias, dtype=np.float64), np.finfo(np.float32).max)  # NaN stays
             key = np.where(np.isneginf(row) | np.isnan(b), -np.inf, s + b)
         allowed = range(e)
         if n_groups > 1:

@@ -95,3 +95,11 @@ def test_silu_gate(g, u):
 def test_fp8_decode_shares_the_scale_rule():
     q, s = oracle.mx_quantize(np.linspace(-3, 3, 64)[None])
     assert np.abs(ox.decode_fp8(q, s) - np.linspace(-3, 3, 64)).max() < 3 * 2.0**-4
+
+
+def test_route_bias_of_plus_infinity():
+    """+inf counts as the largest float32: such experts come first, the lowest index first."""
+    x = np.zeros((1, 6))
+    bias = np.array([0.1, np.inf, 0.3, np.inf, np.nan, np.finfo(np.float32).max])
+    _, e = ox.route(x, 6, bias=bias, scoring="sigmoid")
+    assert e.tolist() == [[1, 3, 5, 2, 0, 4]]
