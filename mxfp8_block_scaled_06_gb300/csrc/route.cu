@@ -58,8 +58,7 @@ __device__ __forceinline__ float load_logit(const void* p, size_t i, int bf16) {
 }
 
 // An expert's bias: NaN counts as -inf, +inf as the largest float.
-__device__ __forceinline__ float load_bias(const float* p, int e) {
-  const float b = p[e];
+__device__ __forceinline__ float bias_value(float b) {
   return isnan(b) ? -CUDART_INF_F : fminf(b, CUDART_MAX_NORMAL_F);
 }
 
@@ -95,19 +94,25 @@ __device__ __forceinline__ float score32(const RouteArgs& p, const Token& t, flo
 // The keys' score: approximate exp and reciprocal, a few units in the last place.
 __device__ __forceinline__ float quick_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// Bound of |computed key - exact key| of the token's keys, in units of 2^-23.
+// Bound of |computed score - exact score| of the token's keys, in units of 2^-23.
 // __expf(y) is within 2 + 1.18 |y| units (2 ulp and its argument's rounding),
 // __fdividef within 2, an addition or division within 0.5.
 //   sigmoid: s = 1 / D, D = 1 + exp(-x): relative (1 - s)(2 + 1.18 |x|) + 0.5 + 2, so
-//            absolute at most 0.61 + 2.5 (s (1 - s)(2 + 1.18 |x|) peaks at 0.61).
+//            absolute at most 0.63 + 2.5 (s (1 - s)(2 + 1.18 |x|) peaks at 0.627).
 //   softmax: u = top - x is rounded once: a term is off by 2 + 1.68 u, the sum of E <=
 //            512 terms (a softmax's mean u is at most ln E) by 12.6 + 21 roundings, the
 //            quotient by 1 more: s is off by s (26.1 + 1.68 u) <= 26.2 s_top.
-// The key adds 0.5 |s + bias|.
-__device__ __forceinline__ float keys_error(const RouteArgs& p, const Token& t, float largest_bias) {
+__device__ __forceinline__ float scores_error(const RouteArgs& p, const Token& t) {
   const float s = p.scoring == kScoreSigmoid ? 3.2f : t.sum > 0.f ? 26.2f / t.sum : 0.f;
-  return (s + 0.5f * (1.f + largest_bias)) * 1.2e-7f + 1e-37f;
+  return s * 1.2e-7f + 1e-37f;
 }
+
+// Bound of |computed key - exact key|: the score's, and half a unit of the sum with the bias,
+// taken twice to leave room for the roundings of what is computed with it. It is the
+// key's own, so a large bias elsewhere (-1e9 for a masked expert) brings no other key
+// into question. k + key_error and k - key_error grow with k, so keys sorted by k that
+// are further apart than their errors from neighbour to neighbour are so altogether.
+__device__ __forceinline__ float key_error(float score_error, float k) { return score_error + 1.2e-7f * fabsf(k); }
 
 // The parts of a token's selection in float64, for keys that float32 cannot tell
 // apart; out of line, as few tokens come here. float64 is slow on this GPU (a warp
@@ -127,7 +132,7 @@ __device__ __noinline__ double sum64(const RouteArgs& p, size_t base, float top)
 
 __device__ __forceinline__ double key64(const RouteArgs& p, size_t base, int e, float top, double sum) {
   const double x = load_logit(p.logits, base + e, p.bf16);
-  const float b = load_bias(p.bias, e);
+  const float b = bias_value(p.bias[e]);
   if (x == -CUDART_INF) return -CUDART_INF;
   return (p.scoring == kScoreSigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum) + static_cast<double>(b);
 }
@@ -208,7 +213,7 @@ __device__ __noinline__ int select32(const RouteArgs& p, volatile uint32_t* keys
 // group's keys that may be among its two largest (at least `floor`, float32) in
 // float64, its exact sum; the largest sums fill the places left.
 __device__ __noinline__ uint32_t groups64(const RouteArgs& p, size_t base, float top, uint32_t in, uint32_t contended,
-                                          const volatile float* keys32, float far) {
+                                          const volatile float* keys32, float score_error) {
   const int lane = threadIdx.x & 31;
   const int size = p.E / p.n_groups;
   const double sum = sum64(p, base, top);
@@ -222,7 +227,7 @@ __device__ __noinline__ uint32_t groups64(const RouteArgs& p, size_t base, float
       const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
       merge_top2<float>(a1, a2, b1, b2);
     }
-    const float floor = (size == 1 ? a1 : a2) - 2.f * far;
+    const float second = size == 1 ? a1 : a2, floor = second - 2.f * key_error(score_error, second);
     double d1 = -CUDART_INF, d2 = -CUDART_INF;
     for (int e = lane; e < size; e += 32)
       if (!(keys32[g * size + e] < floor))
@@ -243,11 +248,21 @@ __device__ __noinline__ uint32_t groups64(const RouteArgs& p, size_t base, float
   return in | __ballot_sync(kFull, (contended >> lane & 1u) && rank < p.topk_groups - __popc(in));
 }
 
-// Each group's largest key, or with a bias the sum of its two largest, in lane g; for
-// groups of whole registers of the warp (32, 64, ... experts): two warp reductions a
+// A group's two largest keys (without a bias and in groups of one expert the second is 0).
+struct Best {
+  float k1, k2;
+};
+// What ranks the groups: their largest keys, or with a bias the sum of their two largest; beyond
+// float's range its end, -inf where the second is masked.
+__device__ __forceinline__ float group_sum(Best b) {
+  const float sum = fmaxf(fminf(b.k1 + b.k2, CUDART_MAX_NORMAL_F), -CUDART_MAX_NORMAL_F);
+  return fminf(b.k1, b.k2) > -CUDART_INF_F ? sum : -CUDART_INF_F;
+}
+
+// Each group's two largest keys, in lane g; for groups of whole registers of the warp (32, 64, ... experts): two warp reductions a
 // group, where the keys in shared memory took 387 instructions a token in all.
 template <int V>
-__device__ __forceinline__ float best_of_registers(const RouteArgs& p, const uint32_t (&key)[V]) {
+__device__ __forceinline__ Best best_of_registers(const RouteArgs& p, const uint32_t (&key)[V]) {
   const int lane = threadIdx.x & 31;
   uint32_t k1 = 0, k2 = 0, best1 = 0, best2 = 0;
   int g = 0, left = p.group_regs;
@@ -265,11 +280,11 @@ __device__ __forceinline__ float best_of_registers(const RouteArgs& p, const uin
       ++g;
     }
   }
-  return p.bias == nullptr ? unord32(best1) : unord32(best1) + unord32(best2);
+  return {unord32(best1), p.bias == nullptr ? 0.f : unord32(best2)};
 }
 
 // The same for any groups, from the warp's E keys in shared memory.
-__device__ __forceinline__ float best_of_shared(const RouteArgs& p, const volatile float* keys) {
+__device__ __forceinline__ Best best_of_shared(const RouteArgs& p, const volatile float* keys) {
   const int lane = threadIdx.x & 31;
   const int parts = p.group_parts;  // lanes per group, a power of two
   const int g = lane / parts, part = lane & (parts - 1);
@@ -281,32 +296,51 @@ __device__ __forceinline__ float best_of_shared(const RouteArgs& p, const volati
     const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
     merge_top2<float>(a1, a2, b1, b2);
   }
-  const float whole = p.bias == nullptr || size == 1 ? a1 : a1 + a2;
-  return __shfl_sync(kFull, whole, lane < p.n_groups ? lane * parts : 0);
+  const int from = lane < p.n_groups ? lane * parts : 0;
+  a2 = p.bias == nullptr || size == 1 ? 0.f : a2;
+  return {__shfl_sync(kFull, a1, from), __shfl_sync(kFull, a2, from)};
 }
 
-// The topk_groups groups of the largest `best` (lane g: group g's), as a bit mask.
-// *contended: the groups whose sums float32 cannot rank where it matters, of which
-// none is in the mask; 0 if there are none.
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, float best, float far, uint32_t* contended) {
+// The groups (a bit mask) that float32 cannot rank where it matters, each by its own error: a
+// wide one may belong to any group, those of a sum far below among them.
+__device__ __noinline__ uint32_t groups_in_question(Best best, float score_error, bool chosen, bool left) {
+  const float sum = group_sum(best);
+  const float err = sum > -CUDART_INF_F ? fminf(key_error(score_error, best.k1) + key_error(score_error, best.k2) +
+                                                    1.2e-7f * fabsf(best.k1 + best.k2),
+                                                CUDART_MAX_NORMAL_F)
+                                        : 0.f;
+  // how low the chosen ones may be, and how high the ones left out
+  const float low = sum - err, high = sum + err;
+  const float least = unord32(__reduce_min_sync(kFull, chosen ? ord32(low) : ord32(CUDART_INF_F)));
+  const float most = unord32(__reduce_max_sync(kFull, left ? ord32(high) : kMasked));
+  if (least > most) return 0u;
+  return __ballot_sync(kFull, (chosen && !(low > most)) || (left && !(high < least)));
+}
+
+// The topk_groups groups of the largest sums (lane g: group g's), as a bit mask.
+// *contended: the groups that float32 cannot rank where it matters, of which none is in
+// the mask; 0 if there are none.
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, Best best, float score_error,
+                                                  uint32_t* contended) {
   const int lane = threadIdx.x & 31;
+  const float sum = group_sum(best);
   int rank = 0;
   for (int j = 0; j < p.n_groups; ++j) {
-    const float b = __shfl_sync(kFull, best, j);
-    rank += b > best || (b == best && j < lane);
+    const float b = __shfl_sync(kFull, sum, j);
+    rank += b > sum || (b == sum && j < lane);
   }
   const bool mine = lane < p.n_groups;
   const uint32_t in = __ballot_sync(kFull, mine && rank < p.topk_groups);
   const uint32_t next = __ballot_sync(kFull, mine && rank == p.topk_groups);
   *contended = 0;
   if (p.bias == nullptr || next == 0) return in;
-  // the last one in and the first one out, and whatever is within reach of either: two
-  // sums are off by 2 far each, and round by (1 + |bias|) units each, at most 2 far
+  // the last one in and the first one out, further apart than twice the error of any sum
   const uint32_t last = __ballot_sync(kFull, mine && rank == p.topk_groups - 1);
-  const float x = __shfl_sync(kFull, best, __ffs(last) - 1), y = __shfl_sync(kFull, best, __ffs(next) - 1);
-  const float err = 8.f * far;
-  if (!(y > -CUDART_INF_F) || x - y > err) return in;
-  *contended = __ballot_sync(kFull, mine && !(best - x > err) && !(y - best > err));
+  const float x = __shfl_sync(kFull, sum, __ffs(last) - 1), y = __shfl_sync(kFull, sum, __ffs(next) - 1);
+  const float size = mine && sum > -CUDART_INF_F ? fmaxf(fabsf(best.k1), fabsf(best.k2)) : 0.f;
+  const float largest = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(size)));
+  if (!(y > -CUDART_INF_F) || x - y > 4.f * score_error + 1e-6f * largest) return in;
+  *contended = groups_in_question(best, score_error, mine && rank < p.topk_groups, mine && rank >= p.topk_groups);
   return in & ~*contended;
 }
 
@@ -314,7 +348,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& p, float best
 // groups: the lane's keys' groups, five bits each. shared: the warp's shared memory.
 template <int V>  // keys per lane
 __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, const float (&bias)[V],
-                                            float largest_bias, const uint32_t (&groups)[(V + 5) / 6],
+                                            const uint32_t (&groups)[(V + 5) / 6],
                                             double* shared, int* expert, float* weight) {
   const int lane = threadIdx.x & 31;
   const size_t base = token * static_cast<size_t>(p.ldl);
@@ -328,7 +362,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
   }
   Token t{0.f, 1.f};
   uint32_t key[V];
-  float far = 0.f;  // the keys' error
+  float score_error = 0.f;
   if (p.scoring == kScoreSoftmax) {
     float top = x[0];
 #pragma unroll
@@ -343,7 +377,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     t.sum = warp_sum(sum);
   }
   if (p.bias != nullptr) {
-    far = keys_error(p, t, largest_bias);
+    score_error = scores_error(p, t);
     const float inv = p.scoring == kScoreSoftmax && t.sum > 0.f ? 1.f / t.sum : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -363,7 +397,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
         if (lane + 32 * i < p.E) keys[lane + 32 * i] = x[i];
       __syncwarp();
     };
-    float best;
+    Best best;
     if (p.group_regs > 0) {
       best = best_of_registers<V>(p, key);
     } else {
@@ -371,10 +405,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       best = best_of_shared(p, keys);
     }
     uint32_t contended;
-    open = choose_groups(p, best, far, &contended);
+    open = choose_groups(p, best, score_error, &contended);
     if (contended != 0) {
       share_keys();
-      open = groups64(p, base, t.top, open, contended, keys, far);
+      open = groups64(p, base, t.top, open, contended, keys, score_error);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -401,7 +435,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       if (key[i] == kMasked) key[i] -= lane + 32 * i;
     least = bound();
   }
-  if (p.bias != nullptr && least > kMasked) least = ord32(unord32(least) - 2.f * far);
+  if (p.bias != nullptr && least > kMasked)
+    least = ord32(unord32(least) - 2.f * key_error(score_error, unord32(least)));
   least = max(least, 1u);
   // gathered in the order of their indices
   volatile uint2* const list = reinterpret_cast<volatile uint2*>(shared);
@@ -440,9 +475,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
       const int other = lane < p.top_k ? max(lane - 1, 0) : p.top_k - 1;
       const uint32_t ko = __shfl_sync(kFull, k, other), eo = __shfl_sync(kFull, e, other);
       bool close = false;
-      if (lane > 0 && lane < n && k > kMasked && !(unord32(ko) - unord32(k) > 2.f * far))
+      if (lane > 0 && lane < n && k > kMasked &&
+          !(unord32(ko) - unord32(k) > key_error(score_error, unord32(ko)) + key_error(score_error, unord32(k))))
         close = load_logit(p.logits, base + eo, p.bf16) != load_logit(p.logits, base + e, p.bf16) ||
-                load_bias(p.bias, eo) != load_bias(p.bias, e);
+                bias_value(p.bias[eo]) != bias_value(p.bias[e]);
       if (__any_sync(kFull, close)) mine = order64(p, base, e, n, t.top, reinterpret_cast<volatile int*>(shared));
     }
   } else if (p.bias != nullptr) {
@@ -531,22 +567,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32, 4) route_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
   pdl_wait();
-  float bias[V], largest_bias = 0.f;
+  float bias[V];
   uint32_t groups[(V + 5) / 6] = {};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
-    bias[i] = p.bias != nullptr && e < p.E ? load_bias(p.bias, e) : 0.f;
-    if (bias[i] > -CUDART_INF_F) largest_bias = fmaxf(largest_bias, fabsf(bias[i]));
+    bias[i] = bias_value(p.bias != nullptr && e < p.E ? p.bias[e] : 0.f);
     if (e < p.E) groups[i / 6] |= div_u32(e, p.per_group) << (5 * (i % 6));
   }
-  largest_bias = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(largest_bias)));
   __syncthreads();
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   for (int t = t0 + warp; t < t1; t += kRouteWarps) {
     int e;
     float w;
-    route_token<V>(p, t, bias, largest_bias, groups, route_smem + warp * p.shared_keys, &e, &w);
+    route_token<V>(p, t, bias, groups, route_smem + warp * p.shared_keys, &e, &w);
     if (lane < p.top_k) {
       const size_t r = static_cast<size_t>(t) * p.top_k + lane;
       p.experts[r] = e;
