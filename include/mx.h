@@ -400,7 +400,8 @@ int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a,
  * ties to the lowest index; which they are is decided as in exact arithmetic on the
  * given float32 / bf16 numbers (float64 where float32 cannot tell).
  *   weights  out [T, top_k] float32: the chosen scores, divided by their sum if
- *            renormalize (0 where the sum is 0), times scale
+ *            renormalize (0 where the sum is 0 in float64: every chosen expert masked, or its
+ *            score below 1e-307), times scale
  *   experts  out [T, top_k] int32
  *   offsets  out [E + 1] int32: first row of each expert when the T * top_k (token,
  *            choice) pairs are ordered by expert, then token and choice

@@ -74,6 +74,20 @@ __device__ __forceinline__ uint32_t div_u32(uint32_t n, FastDiv f) {
   return f.shift < 0 ? n : (t + ((n - t) >> 1)) >> f.shift;
 }
 
+// Renormalized weights of scores (lane j: of logit x, -inf where it has no choice) whose sum is
+// so small that some of them may be float32 subnormals or 0: in float64; 0 where the sum is 0
+// there too. With the sum at kSmallSum or more such a score's weight is below 2^-106.
+constexpr float kSmallSum = 1.f / (1 << 20);
+__device__ __noinline__ float small_weights(const RouteArgs& p, float x, float top) {
+  double s = 0.0;
+  if (x > -CUDART_INF_F)
+    s = p.scoring == kScoreSigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x))) : exp(static_cast<double>(x) - top);
+  double sum = s;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  return sum > 0.0 ? static_cast<float>(s / sum) : 0.f;
+}
+
 // Keeps the two largest of (a1 >= a2) and (b1 >= b2) in a1, a2.
 template <typename F>
 __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
@@ -87,7 +101,8 @@ struct Token {
 };
 
 __device__ __forceinline__ float score32(const RouteArgs& p, const Token& t, float x) {
-  if (p.scoring == kScoreSigmoid) return 1.f / (1.f + expf(-x));
+  // far below 0 exp(-x) overflows, and the score is exp(x) to within exp(x) of itself
+  if (p.scoring == kScoreSigmoid) return x < -80.f ? expf(x) : 1.f / (1.f + expf(-x));
   return t.sum > 0.f ? expf(x - t.top) / t.sum : 0.f;
 }
 
@@ -491,14 +506,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, size_t token, co
     __syncwarp();
     mine = select32(p, keys);
   }
-  float w = 0.f;
+  float w = 0.f, xm = -CUDART_INF_F;
   if (lane < p.top_k) {
-    const float xm = load_logit(p.logits, base + mine, p.bf16);
+    xm = load_logit(p.logits, base + mine, p.bf16);
     w = xm > -CUDART_INF_F ? score32(p, t, xm) : 0.f;
   }
   if (p.renormalize) {
     const float sum = warp_sum(w);
-    w = sum > 0.f ? w / sum : 0.f;
+    w = sum < kSmallSum ? small_weights(p, xm, t.top) : w / sum;
   }
   *expert = mine;
   *weight = w * p.scale;
