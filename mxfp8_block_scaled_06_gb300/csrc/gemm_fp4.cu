@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     const uint64_t pol = policy_evict_normal();
     int s = 0, issuer = 0;
     uint32_t ph = 1;
-    bool ok = true;
+    bool ok = true, early = p.early_weights;
     for (int idx = first; ok && idx < total; idx += stride) {
       const Tile t = table.at(idx, p.N, rank);
       const uint8_t* const sf = p.w_scales + static_cast<size_t>(t.w_row >> 7) * units * kSfTile;
@@ -278,7 +278,12 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
         }
         __syncwarp();
         issuer = (issuer + 1) & 31;
-        if (++s == stages) s = 0, ph ^= 1u;
+        if (++s == stages) {
+          s = 0, ph ^= 1u;
+          // from here on the waits' limit counts: not while the previous kernel may still run
+          if (early) pdl_wait();
+          early = false;
+        }
       }
     }
   } else if (!kGather && warp == 2) {
