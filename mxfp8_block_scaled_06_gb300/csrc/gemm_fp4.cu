@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
       tmem_alloc_pair(smem_u32(tmem_slot), p.tmem_cols);
     else
       tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+    // only now: a dependent that shares the SM and took tensor memory this CTA still waits for
+    // would keep it, waiting in turn for this kernel to end
+    pdl_launch_dependents();
   }
-  pdl_launch_dependents();
   if (warp == 1) {
     if (p.offsets != nullptr) pdl_wait();
     // the experts' rows, clamped to the output, and the tiles before each expert
