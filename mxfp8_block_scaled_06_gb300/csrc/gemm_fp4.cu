@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
           const int r = r0 + apart * j, i = r + rank * mine_ahead;
-          ahead[j] = r < mine_ahead && i < t.rows ? __ldg(p.tokens + t.row0 + i) : -1;
+          ahead[j] = r < mine_ahead && i < t.rows ? p.tokens[t.row0 + i] : -1;
         }
       };
       find(idx, chunk);
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
         if (vec) {
 #pragma unroll
           for (int j = 0; j < kRows; ++j) {
-            const uint4 q = src[j] != nullptr && u0 < units ? __ldg(reinterpret_cast<const uint4*>(src[j] + u0 * 4))
+            const uint4 q = src[j] != nullptr && u0 < units ? *reinterpret_cast<const uint4*>(src[j] + u0 * 4)
                                                             : make_uint4(0, 0, 0, 0);
             w[0][j] = q.x;
             w[1][j] = q.y;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 #pragma unroll
           for (int j = 0; j < kRows; ++j)
             w[b][j] = src[j] != nullptr && u0 + b < units
-                          ? __ldg(reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step))
+                          ? *reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step)
                           : 0u;
       };
       int u0 = 0;

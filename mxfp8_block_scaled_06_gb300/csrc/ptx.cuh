@@ -144,6 +144,9 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// What the previous kernel wrote is read after this wait by ordinary loads: the non-coherent
+// ones (__ldg, or a const __restrict__ parameter) are for data that no kernel writes
+// while this one is resident.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // -------------------------------------------------------------- async proxy

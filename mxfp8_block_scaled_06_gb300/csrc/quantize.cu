@@ -24,7 +24,7 @@ constexpr int kWarpsPerBlock = 8;
 constexpr int kPadRows = 8;  // swizzled-scale padding rows zeroed by one warp
 
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
-    quantize_rows_kernel(const uint16_t* __restrict__ x, long ldx, int M, int K,
+    quantize_rows_kernel(const uint16_t* x, long ldx, int M, int K,
                          uint8_t* __restrict__ q, uint8_t* __restrict__ scales, int swizzled,
                          int rows_total, int groups_per_row, RopeArgs rope) {
   // Programmatic dependent launch: let the next kernel (typically a GEMM that
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
 // division) and the row's weight, rounds to bf16 (optionally stored) and
 // quantizes per 32-block as quantize_rows_kernel does.
 __global__ void __launch_bounds__(kWarpsPerBlock * 32)
-    rmsnorm_quantize_rows_kernel(const uint16_t* __restrict__ x, long ldx, int M, int K,
+    rmsnorm_quantize_rows_kernel(const uint16_t* x, long ldx, int M, int K,
                                  const uint16_t* __restrict__ gamma, float eps,
                                  uint16_t* __restrict__ y, uint8_t* __restrict__ q,
                                  uint8_t* __restrict__ scales, int swizzled, int rows_total) {

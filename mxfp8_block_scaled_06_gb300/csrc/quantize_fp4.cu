@@ -120,7 +120,7 @@ struct Unit<float> {
 // kUnits 8-element units per thread, kThreads apart: their loads are in flight together.
 template <typename T, int kUnits>
 __global__ void __launch_bounds__(kThreads)
-    quantize_rows_fp4_kernel(const T* __restrict__ x, long ldx, int M, int K, uint32_t* __restrict__ q,
+    quantize_rows_fp4_kernel(const T* x, long ldx, int M, int K, uint32_t* __restrict__ q,
                              uint8_t* __restrict__ scales, int swizzled, uint4* __restrict__ y, uint32_t units,
                              FastDiv per_row, uint32_t unit_blocks) {
   pdl_launch_dependents();

@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
       if (!ok && c == 0) atomicOr(p.status, kStatusBadInput);
       w[i] = ok && j < p.top_k ? weights[j] : 0.f;
       // a slot out of range reads nothing and adds nothing
-      v[i] = ok && j < p.top_k ? __ldg(reinterpret_cast<const uint4*>(p.y + static_cast<size_t>(s) * p.ldy) + c)
+      v[i] = ok && j < p.top_k ? reinterpret_cast<const uint4*>(p.y + static_cast<size_t>(s) * p.ldy)[c]
                                : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
