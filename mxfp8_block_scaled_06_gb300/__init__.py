@@ -6,7 +6,8 @@ stream. There is no fallback: if libmx.so is missing or the device is not a
 compute-capability 10.3 GPU, the calls raise. Since the C entry points see only
 plain pointers, each wrapper first checks every tensor's element type, size,
 layout and residency on the handle's GPU (TypeError / ValueError, nothing
-launched).
+launched). A call runs on `stream` (default: the current one); outputs that it
+allocates belong to that stream, and the order with other streams is the caller's.
 
 Names and argument order follow the C entry points: mx_create, mx_scale_bytes,
 mx_quantize_rows, mx_gemm, mx_gemm_chain, wo_a_grouped, mx_device_status; for expert
@@ -162,9 +163,21 @@ def _stream(stream):
     return s.cuda_stream
 
 
-def _empty_u8(shape, device):
+def _empty_on(stream):
+    """torch.empty, of tensors that belong to this stream: memory of the current one may still be
+    in use there by work that was queued before it was freed."""
     import torch
-    return torch.empty(shape, dtype=torch.uint8, device=device)
+
+    def empty(shape, dtype, device):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return empty
+
+
+def _empty_u8(shape, device, stream):
+    import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
+    return empty(shape, dtype=torch.uint8, device=device)
 
 
 # The C entry points take plain pointers and cannot see what they point at, so
@@ -276,8 +289,8 @@ def mx_quantize_rows(h: Handle, x, q=None, scales=None, swizzled: bool = True, s
     if q is None or scales is None:  # outputs to allocate: x must be usable first
         _resident(h, host_ok=("x",), x=x)
     dev = x.device if x.is_cuda else torch.device("cuda", h.device)  # x may be pinned host memory
-    q = _empty_u8((m, k), dev) if q is None else q
-    scales = _empty_u8(shape, dev) if scales is None else scales
+    q = _empty_u8((m, k), dev, stream) if q is None else q
+    scales = _empty_u8(shape, dev, stream) if scales is None else scales
     _resident(h, host_ok=("x",), x=x, q=q, scales=scales)
     _check(load_library().mx_quantize_rows(h.ptr, m, k, _ptr(x), x.stride(0), _ptr(q),
                                            _ptr(scales), int(swizzled), _stream(stream)),
@@ -290,12 +303,13 @@ def mx_gemm(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = None,
     """out[M, N] bf16 = dequant(a[M, K]) x dequant(w[N, K])^T (M = a's rows unless m is given);
     out may be on the handle's GPU or in pinned host memory (written directly)."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     n, k = _weight(0, w, w_scales)
     m = a.shape[0] if m is None else m
     _matrix("a", a, _codes_types(), m, k)
     _flat("a_scales", a_scales, _scale_types(), _sbytes(m, k))
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device)
+        out = empty((m, n), dtype=torch.bfloat16, device=w.device)
     _matrix("out", out, (torch.bfloat16,), m, n)
     _resident(h, host_ok=("out",), a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out)
     _check(load_library().mx_gemm(h.ptr, m, n, k, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales),
@@ -308,11 +322,12 @@ def mx_gemm_bf16(h: Handle, x, w, w_scales, out=None, m: int | None = None, pdl:
     """out[M, N] bf16 = dequant(MXFP8(x[M, K])) x dequant(w[N, K])^T, x bf16 with its
     quantization inside the GEMM kernel (row stride x.stride(0))."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     n, k = _weight(0, w, w_scales)
     m = x.shape[0] if m is None else m
     _matrix("x", x, (torch.bfloat16,), m, k, row_stride=True)
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device)
+        out = empty((m, n), dtype=torch.bfloat16, device=w.device)
     _matrix("out", out, (torch.bfloat16,), m, n)
     _resident(h, x=x, w=w, w_scales=w_scales, out=out)
     _check(load_library().mx_gemm_bf16(h.ptr, m, n, k, _ptr(x), x.stride(0), _ptr(w), _ptr(w_scales),
@@ -321,9 +336,10 @@ def mx_gemm_bf16(h: Handle, x, w, w_scales, out=None, m: int | None = None, pdl:
     return out
 
 
-def _chain_buffers(a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out):
+def _chain_buffers(a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out, stream):
     """Checks and allocations shared by the two chain entry points."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     if len(weights) != 3:
         raise ValueError("weights: three (w, w_scales) pairs are required")
     (n1, k1), (n2, _), (n3, _) = (_weight(i, w, s) for i, (w, s) in enumerate(weights))
@@ -331,13 +347,13 @@ def _chain_buffers(a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales
     dev = a1.device
     _matrix("a1", a1, _codes_types(), m, k1)
     _flat("a1_scales", a1_scales, _scale_types(), _sbytes(m, k1))
-    a2 = _empty_u8((m, g1_cols), dev) if a2 is None else _matrix("a2", a2, _codes_types(), m, g1_cols)
-    a2_scales = (_empty_u8((_sbytes(m, g1_cols),), dev) if a2_scales is None else
+    a2 = _empty_u8((m, g1_cols), dev, stream) if a2 is None else _matrix("a2", a2, _codes_types(), m, g1_cols)
+    a2_scales = (_empty_u8((_sbytes(m, g1_cols),), dev, stream) if a2_scales is None else
                  _flat("a2_scales", a2_scales, _scale_types(), _sbytes(m, g1_cols)))
-    a3 = _empty_u8((m, n2), dev) if a3 is None else _matrix("a3", a3, _codes_types(), m, n2)
-    a3_scales = (_empty_u8((_sbytes(m, n2),), dev) if a3_scales is None else
+    a3 = _empty_u8((m, n2), dev, stream) if a3 is None else _matrix("a3", a3, _codes_types(), m, n2)
+    a3_scales = (_empty_u8((_sbytes(m, n2),), dev, stream) if a3_scales is None else
                  _flat("a3_scales", a3_scales, _scale_types(), _sbytes(m, n2)))
-    out = torch.empty((m, n3), dtype=torch.bfloat16, device=dev) if out is None else out
+    out = empty((m, n3), dtype=torch.bfloat16, device=dev) if out is None else out
     _matrix("out", out, (torch.bfloat16,), m, n3)
     ws = (MxWeight * 3)(*[MxWeight(_ptr(w), _ptr(s), w.shape[0], w.shape[1]) for w, s in weights])
     return m, dev, ws, (n1, n2, n3), a2, a2_scales, a3, a3_scales, out
@@ -355,10 +371,11 @@ def mx_gemm_chain(h: Handle, a1, a1_scales, weights, g1_cols: int = 1536, out=No
     """Three projections on one stream with PDL: G1 -> MXFP8 requant of its first
     g1_cols columns -> G2 -> requant -> G3. weights = [(w, w_scales)] * 3."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     m, dev, ws, (n1, n2, n3), a2, a2_scales, a3, a3_scales, out = _chain_buffers(
-        a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out)
-    d1 = torch.empty((m, n1), dtype=torch.bfloat16, device=dev) if debug else None
-    d2 = torch.empty((m, n2), dtype=torch.bfloat16, device=dev) if debug else None
+        a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out, stream)
+    d1 = empty((m, n1), dtype=torch.bfloat16, device=dev) if debug else None
+    d2 = empty((m, n2), dtype=torch.bfloat16, device=dev) if debug else None
     _chain_resident(h, a1, a1_scales, weights, a2, a2_scales, a3, a3_scales, out)
     _check(load_library().mx_gemm_chain(h.ptr, m, _ptr(a1), _ptr(a1_scales), ws, g1_cols, _ptr(a2),
                                         _ptr(a2_scales), _ptr(a3), _ptr(a3_scales), _ptr(out),
@@ -373,13 +390,14 @@ def mx_gemm_chain_noalloc(h: Handle, a1, a1_scales, weights, g1_cols: int = 1536
     1 MiB device array (see include/mx.h). Raises MxError (MX_ERR_UNSUPPORTED)
     when the intermediates do not fit; calls that overlap on the GPU race."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     if len(weights) != 3:
         raise ValueError("weights: three (w, w_scales) pairs are required")
     (_, k1), _, (n3, _) = (_weight(i, w, s) for i, (w, s) in enumerate(weights))
     m = a1.shape[0]
     _matrix("a1", a1, _codes_types(), m, k1)
     _flat("a1_scales", a1_scales, _scale_types(), _sbytes(m, k1))
-    out = torch.empty((m, n3), dtype=torch.bfloat16, device=a1.device) if out is None else out
+    out = empty((m, n3), dtype=torch.bfloat16, device=a1.device) if out is None else out
     _matrix("out", out, (torch.bfloat16,), m, n3)
     ws = (MxWeight * 3)(*[MxWeight(_ptr(w), _ptr(s), w.shape[0], w.shape[1]) for w, s in weights])
     _resident(h, a1=a1, a1_scales=a1_scales, out=out,
@@ -396,16 +414,17 @@ def mx_rmsnorm_quantize_rows(h: Handle, x, norm_weight, eps: float, q=None, scal
     """bf16 [M, K] (row stride x.stride(0)) -> RMS-normalized with norm_weight [K] bf16 and
     eps, rounded to bf16 (returned as y when asked) and MX-quantized: (q, scales, y)."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     if x.dim() != 2:
         raise ValueError("x: a 2-D [M, K] tensor is required")
     m, k = x.shape
     _matrix("x", x, (torch.bfloat16,), m, k, row_stride=True)
     _flat("norm_weight", norm_weight, (torch.bfloat16,), k)
     sbytes = _sbytes(m, k) if swizzled else m * (k // 32)
-    q = _empty_u8((m, k), x.device) if q is None else _matrix("q", q, _codes_types(), m, k)
+    q = _empty_u8((m, k), x.device, stream) if q is None else _matrix("q", q, _codes_types(), m, k)
     shape = (sbytes,) if swizzled else (m, k // 32)
-    scales = _empty_u8(shape, x.device) if scales is None else _flat("scales", scales, _scale_types(), sbytes)
-    yt = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
+    scales = _empty_u8(shape, x.device, stream) if scales is None else _flat("scales", scales, _scale_types(), sbytes)
+    yt = empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
     _resident(h, x=x, norm_weight=norm_weight, q=q, scales=scales)
     _check(load_library().mx_rmsnorm_quantize_rows(h.ptr, m, k, _ptr(x), x.stride(0),
                                                    _ptr(norm_weight), float(eps), _ptr(yt), _ptr(q),
@@ -420,13 +439,14 @@ def mx_gemm_chain_norm(h: Handle, a1, a1_scales, weights, norm_weight, eps: floa
     """mx_gemm_chain with the RMS-norm split between G1 and G2: G1's bf16 output goes
     to out1 (qr | kv), qr is normalized and quantized for G2."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     m, dev, ws, (n1, n2, n3), a2, a2_scales, a3, a3_scales, out = _chain_buffers(
-        a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out)
+        a1, a1_scales, weights, g1_cols, a2, a2_scales, a3, a3_scales, out, stream)
     _flat("norm_weight", norm_weight, (torch.bfloat16,), g1_cols)
-    out1 = torch.empty((m, n1), dtype=torch.bfloat16, device=dev) if out1 is None else out1
+    out1 = empty((m, n1), dtype=torch.bfloat16, device=dev) if out1 is None else out1
     _matrix("out1", out1, (torch.bfloat16,), m, n1)
-    dy = torch.empty((m, g1_cols), dtype=torch.bfloat16, device=dev) if debug else None
-    d2 = torch.empty((m, n2), dtype=torch.bfloat16, device=dev) if debug else None
+    dy = empty((m, g1_cols), dtype=torch.bfloat16, device=dev) if debug else None
+    d2 = empty((m, n2), dtype=torch.bfloat16, device=dev) if debug else None
     _chain_resident(h, a1, a1_scales, weights, a2, a2_scales, a3, a3_scales, out)
     _resident(h, norm_weight=norm_weight, out1=out1)
     _check(load_library().mx_gemm_chain_norm(h.ptr, m, _ptr(a1), _ptr(a1_scales), ws, g1_cols,
@@ -474,15 +494,16 @@ def wo_a_grouped(h: Handle, x, positions, cos_sin, w, w_scales, n_groups: int,
     before requantization) with z or debug, the quantized activation with debug
     (which keeps the call on the fused kernel at every T)."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     t, kall, cols = _wo_a_inputs(x, positions, cos_sin, w, w_scales, n_groups, heads_per_group,
                                  o_lora_rank, d_nope, d_rope)
     dev = x.device
-    q = _empty_u8((t, cols), dev) if q is None else _matrix("q", q, _codes_types(), t, cols)
-    q_scales = (_empty_u8((_sbytes(t, cols),), dev) if q_scales is None else
+    q = _empty_u8((t, cols), dev, stream) if q is None else _matrix("q", q, _codes_types(), t, cols)
+    q_scales = (_empty_u8((_sbytes(t, cols),), dev, stream) if q_scales is None else
                 _flat("q_scales", q_scales, _scale_types(), _sbytes(t, cols)))
-    dz = torch.empty((t, cols), dtype=torch.bfloat16, device=dev) if debug or z else None
-    dxq = _empty_u8((t, kall), dev) if debug else None
-    dxs = _empty_u8((t, kall // 32), dev) if debug else None
+    dz = empty((t, cols), dtype=torch.bfloat16, device=dev) if debug or z else None
+    dxq = _empty_u8((t, kall), dev, stream) if debug else None
+    dxs = _empty_u8((t, kall // 32), dev, stream) if debug else None
     _wo_a_resident(h, x, positions, cos_sin, w, w_scales)
     _resident(h, q=q, q_scales=q_scales)
     _check(load_library().wo_a_grouped(h.ptr, t, _ptr(x), x.stride(0), _ptr(positions),
@@ -500,16 +521,17 @@ def wo_a_grouped_unfused(h: Handle, x, positions, cos_sin, w, w_scales, n_groups
     """wo_a_grouped in two launches (RoPE + quantize into the caller-owned xq, then a
     grouped GEMM with the requantization fused); for token counts up to 256."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     t, kall, cols = _wo_a_inputs(x, positions, cos_sin, w, w_scales, n_groups, heads_per_group,
                                  o_lora_rank, d_nope, d_rope)
     dev = x.device
-    q = _empty_u8((t, cols), dev) if q is None else _matrix("q", q, _codes_types(), t, cols)
-    q_scales = (_empty_u8((_sbytes(t, cols),), dev) if q_scales is None else
+    q = _empty_u8((t, cols), dev, stream) if q is None else _matrix("q", q, _codes_types(), t, cols)
+    q_scales = (_empty_u8((_sbytes(t, cols),), dev, stream) if q_scales is None else
                 _flat("q_scales", q_scales, _scale_types(), _sbytes(t, cols)))
-    xq = _empty_u8((t, kall), dev) if xq is None else _matrix("xq", xq, _codes_types(), t, kall)
-    xq_scales = (_empty_u8((_sbytes(t, kall),), dev) if xq_scales is None else
+    xq = _empty_u8((t, kall), dev, stream) if xq is None else _matrix("xq", xq, _codes_types(), t, kall)
+    xq_scales = (_empty_u8((_sbytes(t, kall),), dev, stream) if xq_scales is None else
                  _flat("xq_scales", xq_scales, _scale_types(), _sbytes(t, kall)))
-    zt = torch.empty((t, cols), dtype=torch.bfloat16, device=dev) if z else None
+    zt = empty((t, cols), dtype=torch.bfloat16, device=dev) if z else None
     _wo_a_resident(h, x, positions, cos_sin, w, w_scales)
     _resident(h, q=q, q_scales=q_scales, xq=xq, xq_scales=xq_scales)
     _check(load_library().wo_a_grouped_unfused(h.ptr, t, _ptr(x), x.stride(0), _ptr(positions),
@@ -576,6 +598,7 @@ def mx_quantize_rows_fp4(h: Handle, x, q=None, scales=None, swizzled: bool = Tru
     """bf16, fp16 or fp32 [M, K] (row stride x.stride(0)) -> (packed E2M1 codes uint8
     [M, K/2], scale bytes, y): y = the codes' values in bf16 [M, K] when asked, else None."""
     torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if x.dim() != 2:
         raise ValueError("x: a 2-D [M, K] tensor is required")
     m, k = x.shape
@@ -590,10 +613,10 @@ def mx_quantize_rows_fp4(h: Handle, x, q=None, scales=None, swizzled: bool = Tru
         _flat("scales", scales, _scale_types(), sbytes)
     _here(h, ("x", x), ("q", q), ("scales", scales))
     if q is None:
-        q = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+        q = empty((m, k // 2), dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty((sbytes,) if swizzled else (m, k // 32), dtype=torch.uint8, device=x.device)
-    yt = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
+        scales = empty((sbytes,) if swizzled else (m, k // 32), dtype=torch.uint8, device=x.device)
+    yt = empty((m, k), dtype=torch.bfloat16, device=x.device) if y else None
     _check(load_library().mx_quantize_rows_fp4(h.ptr, m, k, x.data_ptr(), x.stride(0), code, q.data_ptr(),
                                                scales.data_ptr(), int(swizzled), _ptr(yt), _stream_of(h, stream)),
            "mx_quantize_rows_fp4")
@@ -615,6 +638,7 @@ def mx_gemm_fp4(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = N
     [N, K/2] and swizzled scales. a: MXFP8 codes [M, K] or packed MXFP4 codes [M, K/2],
     with swizzled scales (M = a's rows unless m is given)."""
     torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if w is None or w.dim() != 2:
         raise ValueError("w: a 2-D [N, K/2] tensor is required")
     n, k = w.shape[0], 2 * w.shape[1]
@@ -627,7 +651,7 @@ def mx_gemm_fp4(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = N
         _matrix("out", out, _BF16, m, n)
     _here(h, ("a", a), ("a_scales", a_scales), ("w", w), ("w_scales", w_scales), ("out", out))
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=w.device)
+        out = empty((m, n), dtype=torch.bfloat16, device=w.device)
     _check(load_library().mx_gemm_fp4(h.ptr, m, n, k, a.data_ptr(), a_scales.data_ptr(), fp4, w.data_ptr(),
                                       w_scales.data_ptr(), out.data_ptr(), MX_FLAG_PDL if pdl else 0,
                                       _stream_of(h, stream)), "mx_gemm_fp4")
@@ -643,6 +667,7 @@ def mx_gemm_fp4_grouped(h: Handle, a, a_scales, w, w_scales, offsets, tokens=Non
     int32 [R]. gated: weight rows 2i, 2i + 1 are gate i, up i and out is [R, N/2],
     silu(gate) * up. Rows that no expert has are left as they are."""
     torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if w is None or w.dim() != 3:
         raise ValueError("w: a 3-D [E, N, K/2] tensor is required")
     e, n, k = w.shape[0], w.shape[1], 2 * w.shape[2]
@@ -663,7 +688,7 @@ def mx_gemm_fp4_grouped(h: Handle, a, a_scales, w, w_scales, offsets, tokens=Non
     _here(h, ("a", a), ("a_scales", a_scales), ("w", w), ("w_scales", w_scales), ("offsets", offsets),
           ("tokens", tokens), ("out", out))
     if out is None:
-        out = torch.empty((r, cols), dtype=torch.bfloat16, device=w.device)
+        out = empty((r, cols), dtype=torch.bfloat16, device=w.device)
     _check(load_library().mx_gemm_fp4_grouped(h.ptr, e, r, n, k, a.data_ptr(), rows, a_scales.data_ptr(), fp4,
                                               w.data_ptr(), w_scales.data_ptr(), offsets.data_ptr(), _ptr(tokens),
                                               int(gated), out.data_ptr(), _stream_of(h, stream)),
@@ -680,6 +705,7 @@ def mx_route(h: Handle, logits, top_k: int, bias=None, scoring: str = "softmax",
     tokens int32 [T * top_k] (the token of each row), slots int32 [T, top_k] (the row of
     each choice)."""
     torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if logits.dim() != 2:
         raise ValueError("logits: a 2-D [T, E] tensor is required")
     t, e = logits.shape
@@ -702,15 +728,15 @@ def mx_route(h: Handle, logits, top_k: int, bias=None, scoring: str = "softmax",
           ("tokens", tokens), ("slots", slots))
     dev, i32 = logits.device, torch.int32
     if weights is None:
-        weights = torch.empty((t, top_k), dtype=torch.float32, device=dev)
+        weights = empty((t, top_k), dtype=torch.float32, device=dev)
     if experts is None:
-        experts = torch.empty((t, top_k), dtype=i32, device=dev)
+        experts = empty((t, top_k), dtype=i32, device=dev)
     if offsets is None:
-        offsets = torch.empty((e + 1,), dtype=i32, device=dev)
+        offsets = empty((e + 1,), dtype=i32, device=dev)
     if tokens is None:
-        tokens = torch.empty((t * top_k,), dtype=i32, device=dev)
+        tokens = empty((t * top_k,), dtype=i32, device=dev)
     if slots is None:
-        slots = torch.empty((t, top_k), dtype=i32, device=dev)
+        slots = empty((t, top_k), dtype=i32, device=dev)
     _check(load_library().mx_route(h.ptr, t, e, top_k, logits.data_ptr(), logits.stride(0), code, _ptr(bias),
                                    MX_SCORE_SIGMOID if scoring == "sigmoid" else MX_SCORE_SOFTMAX, n_groups,
                                    topk_groups, int(renormalize), scale, weights.data_ptr(), experts.data_ptr(),
@@ -723,6 +749,7 @@ def mx_combine(h: Handle, y, slots, weights, residual=None, out=None, stream=Non
     """out[t] = sum over j of weights[t, j] * y[slots[t, j]] (+ residual[t]): y bf16 [R, N]
     (row stride y.stride(0)), slots int32 and weights fp32 [T, top_k], bf16 [T, N] out."""
     torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y [R, N] and slots [T, top_k]: 2-D tensors are required")
     r, n = y.shape
@@ -736,7 +763,7 @@ def mx_combine(h: Handle, y, slots, weights, residual=None, out=None, stream=Non
         _matrix("out", out, _BF16, t, n)
     _here(h, ("y", y), ("slots", slots), ("weights", weights), ("residual", residual), ("out", out))
     if out is None:
-        out = torch.empty((t, n), dtype=torch.bfloat16, device=y.device)
+        out = empty((t, n), dtype=torch.bfloat16, device=y.device)
     _check(load_library().mx_combine(h.ptr, t, k, n, y.data_ptr(), r, y.stride(0), slots.data_ptr(),
                                      weights.data_ptr(), _ptr(residual), out.data_ptr(), _stream_of(h, stream)),
            "mx_combine")
@@ -749,6 +776,7 @@ def mx_warmup(h: Handle, weights, rows, stream=None) -> list:
     pairs; returns the runs' bf16 outputs ([rows, n], all zero for finite
     weights) in run order: shapes in increasing (n, k), then rows as given."""
     import torch
+    empty = torch.empty if stream is None else _empty_on(stream)
     if not weights or not rows:
         raise ValueError("mx_warmup needs at least one weight and one row count")
     ws = (MxWeight * len(weights))(*[MxWeight(_ptr(w), _ptr(s), w.shape[0], w.shape[1])
@@ -759,7 +787,7 @@ def mx_warmup(h: Handle, weights, rows, stream=None) -> list:
     if nbytes == 0:
         raise MxError(MX_ERR_INVALID_ARG, "mx_warmup_bytes")
     dev = weights[0][0].device
-    scratch = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+    scratch = empty(nbytes + 256, dtype=torch.uint8, device=dev)
     off0 = (-scratch.data_ptr()) % 256
     buf = scratch[off0:off0 + nbytes]
     _check(lib.mx_warmup(h.ptr, ws, len(weights), rr, len(rows), _ptr(buf), nbytes, _stream(stream)),
