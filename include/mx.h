@@ -62,11 +62,20 @@ enum {
                              mx_device_status)                                 */
 };
 
-/* Flags for mx_gemm. */
+/* Flags for mx_gemm, mx_gemm_bf16 and mx_gemm_fp4. */
 #define MX_FLAG_PDL 1u /* launch with programmatic stream serialization: the
                           kernel streams its weights before waiting for the
                           previous kernel on the stream (`launch_low_latency`
-                          / module docstring of the mxfp8 page)              */
+                          / module docstring of the mxfp8 page). So w and
+                          w_scales have to be complete before any kernel that
+                          may still run on the stream: not only the previous
+                          one, as this library's kernels (the quantizers too)
+                          let the next one start while the one before them
+                          still runs. A weight quantized on the stream is safe
+                          after a synchronization, or after a kernel of another
+                          origin, launched in the ordinary way: such a kernel
+                          starts when all before it has ended. The chains and
+                          wo_a_grouped always read their weights so.         */
 
 typedef struct mx_handle mx_handle;
 
@@ -357,7 +366,8 @@ int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, in
  *                layout; both 16-byte aligned
  *   w, w_scales  MXFP4 weights [N, K] packed, scales in the 128x4 layout; both
  *                32-byte aligned
- *   flags        MX_FLAG_PDL or 0, as for mx_gemm
+ *   flags        MX_FLAG_PDL or 0, as for mx_gemm: w and w_scales complete before any kernel
+ *                still running on the stream
  * The call takes mx_gemm's kernel (K split over a cluster) where that is the faster one
  * (few rows or few columns), otherwise a kernel of whole-K tiles.
  * Constraints: 1 <= M <= 2^24, N % 128 == 0, K % 128 == 0, (N / 128) (M / 16 + 1) < 2^31,

@@ -301,7 +301,9 @@ def mx_quantize_rows(h: Handle, x, q=None, scales=None, swizzled: bool = True, s
 def mx_gemm(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = None,
             pdl: bool = False, stream=None):
     """out[M, N] bf16 = dequant(a[M, K]) x dequant(w[N, K])^T (M = a's rows unless m is given);
-    out may be on the handle's GPU or in pinned host memory (written directly)."""
+    out may be on the handle's GPU or in pinned host memory (written directly). pdl: the
+    weights are read before the kernels still running on the stream have ended, so none
+    of these may write them (MX_FLAG_PDL in include/mx.h)."""
     import torch
     empty = torch.empty if stream is None else _empty_on(stream)
     n, k = _weight(0, w, w_scales)
@@ -320,7 +322,7 @@ def mx_gemm(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = None,
 def mx_gemm_bf16(h: Handle, x, w, w_scales, out=None, m: int | None = None, pdl: bool = False,
                  stream=None):
     """out[M, N] bf16 = dequant(MXFP8(x[M, K])) x dequant(w[N, K])^T, x bf16 with its
-    quantization inside the GEMM kernel (row stride x.stride(0))."""
+    quantization inside the GEMM kernel (row stride x.stride(0)). pdl as for mx_gemm."""
     import torch
     empty = torch.empty if stream is None else _empty_on(stream)
     n, k = _weight(0, w, w_scales)
@@ -636,7 +638,8 @@ def mx_gemm_fp4(h: Handle, a, a_scales, w, w_scales, out=None, m: int | None = N
                 stream=None):
     """out[M, N] bf16 = dequant(a) x dequant(w)^T with MXFP4 weights w: packed codes uint8
     [N, K/2] and swizzled scales. a: MXFP8 codes [M, K] or packed MXFP4 codes [M, K/2],
-    with swizzled scales (M = a's rows unless m is given)."""
+    with swizzled scales (M = a's rows unless m is given). pdl as for mx_gemm: no kernel
+    still running on the stream may write w or w_scales."""
     torch = _t()
     empty = torch.empty if stream is None else _empty_on(stream)
     if w is None or w.dim() != 2:

@@ -67,3 +67,32 @@ def test_chain_on_reused_buffers(mx, t, fp4):  # noqa: F811
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(*outs))
     assert mx.mx_device_status(h) == mx.MX_OK
+
+
+@pytest.mark.parametrize("m,n,k", [(8, 16384, 4096), (100, 16384, 2048)])
+def test_weights_made_on_the_stream(mx, m, n, k):  # noqa: F811
+    """New weights for every product under PDL: safe behind an ordinary kernel, which starts when
+    all before it has ended."""
+    h = handle()
+    g = torch.Generator(device="cuda:0").manual_seed(n)
+    x, w = normal(g, m, k), [normal(g, n, k).bfloat16() for _ in range(3)]
+    q, s, _ = mx.mx_quantize_rows_fp4(h, w[0])
+    want = []
+    for v in w:
+        mx.mx_quantize_rows_fp4(h, v, q=q, scales=s)
+        a, a_s, _ = mx.mx_quantize_rows_fp4(h, x)
+        torch.cuda.synchronize()
+        want.append(mx.mx_gemm_fp4(h, a, a_s, q, s))
+    got = [torch.zeros_like(o) for o in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for v, out in zip(w, got):
+            mx.mx_quantize_rows_fp4(h, v, q=q, scales=s)
+            out.fill_(7.0)  # the ordinary kernel
+            mx.mx_quantize_rows_fp4(h, x, q=a, scales=a_s)
+            mx.mx_gemm_fp4(h, a, a_s, q, s, out=out, pdl=True)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, e) for o, e in zip(got, want))
+    assert mx.mx_device_status(h) == mx.MX_OK
