@@ -82,9 +82,12 @@ __device__ __forceinline__ bool mbar_wait_or(uint32_t bar, uint32_t parity, cons
   }
 }
 // Arrive on the barrier of another CTA of the cluster (an address from
-// map_shared_rank). The arrival follows what this thread has seen and done in its own
-// CTA's shared memory; a release at cluster scope would also wait for the thread's
-// earlier arrivals to reach the other SM, about 0.9 us each.
+// map_shared_rank), releasing at CTA scope: the memory model orders this thread's and
+// its CTA's earlier writes before what follows in the other CTA at cluster scope only. It
+// is for arrivals that carry no data across: the other CTA then starts operations which
+// this SM performs on its own shared and tensor memory, where the writes are complete
+// before the arrival is issued (seen through a local barrier, or tcgen05.wait). A release
+// at cluster scope takes a warp 0.86 us whatever its lanes have outstanding.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
