@@ -1148,12 +1148,13 @@ constexpr int kRowsMax = 48;
 // holds at once with one CTA to an SM (of 152 SMs 76 of two CTAs, 46, 36, 28, 23, 15 and 15
 // of eight) run two to an SM where both fit: a quarter more for the way, and more for the
 // exchange. One split stands for whole-K tiles (gemm_fp4.cu), which take 14 a row more, from
-// 65 rows on 1500 (MXFP4 rows 1900) more; 33 to 64 MXFP8 rows leave their ring four stages
-// instead of five: a seventh more for the way, with over 48 rows half as much again, which
-// puts the change to two splits where it was measured: with 77 to 152 weight tiles at K =
-// 1400 to 2500 for 34 and 48 rows, 2000 to 2500 for 64 (whole K / two splits, us: N = 12288,
-// 48 rows, K = 512 5.1 / 6.1, 2048 8.3 / 8.4, 4096 12.5 / 11.1; 64 rows, K = 1024 6.5 / 6.9,
-// 2560 9.8 / 9.0; N = 19456, 48 rows, K = 1536 7.3 / 8.2).
+// 65 rows on 1500 (MXFP4 rows 1900) more. 33 to 64 MXFP8 rows leave their ring four stages
+// instead of five; against over 76 weight tiles (fewer split K from short K on either way) a
+// seventh more for the way, with over 48 rows half as much again, puts the change to two
+// splits where it was measured: with 77 to 152 tiles at K = 1400 to 2500 for 34 and 48 rows,
+// 2000 to 2500 for 64 (whole K / two splits, us: N = 12288, 48 rows, K = 512 5.1 / 6.1, 2048
+// 8.3 / 8.4, 4096 12.5 / 11.1; 64 rows, K = 1024 6.5 / 6.9, 2560 9.8 / 9.0; N = 19456, 48 rows,
+// K = 1536 7.3 / 8.2).
 // Measured on GB300, us with MXFP8 rows and 2 / 3 / 4 / 6 / 8 splits: N = 1024, K = 10368
 // 11.8 / 9.1 / 7.9 / 6.7 / 6.1 at one row, 14.3 / 11.5 / 10.1 / 8.8 / 8.3 at 128; N = 2048,
 // K = 5120 7.7 / 6.6 / 5.9 / 5.1 / 5.3 (two to an SM) at one row, 8.9 / 7.8 / 7.0 / 6.6 / 7.9
@@ -1173,7 +1174,7 @@ W4Split w4_split(int M, int N, int K, const PlanEnv& env, bool a_fp4, const Fits
   const int sft = a_fp4 ? 2 : 1, chunks = (K / 128 + sft - 1) / sft;
   const long walk = (a_fp4 ? 110L : 180L) * (K / 128);
   W4Split best{std::min(M, 128), 1};
-  long least = walk + (M > 64 ? (a_fp4 ? 1900 : 1500) : 14 * M + (a_fp4 || M <= 32 ? 0 : M <= 48 ? walk / 7 : walk / 2));
+  long least = walk + (M > 64 ? (a_fp4 ? 1900 : 1500) : 14 * M + (a_fp4 || M <= 32 || N / 128 <= 76 ? 0 : M <= 48 ? walk / 7 : walk / 2));
   for (int slice : {std::min(M, 128), std::min(M, 256)}) {
     const long clusters = static_cast<long>(N / 128) * ((M + slice - 1) / slice);
     for (int s = 2; s <= std::min(slice > 128 ? 4 : 8, chunks); ++s) {
