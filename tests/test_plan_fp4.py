@@ -70,3 +70,19 @@ def test_split_of_33_to_64_rows_follows_k(m, n):
         assert mx.mx_plan_gemm_fp4(m, n, k)["splits"] == 1
     for k in (4096, 8192):
         assert mx.mx_plan_gemm_fp4(m, n, k)["splits"] > 1
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_whole_k_rings_are_long_enough(fp4):
+    """Experts' and plain products: the ring has the stages that warps which take them in turn need (the
+    stages left to others and one more: 5 of MXFP8 rows, 3 of MXFP4 where two warps load the scales),
+    and what shares an SM fits its tensor memory."""
+    for e, r, n, k in itertools.product((1, 2, 7, 64, 512), (1, 16, 63, 100, 700, 1024, 4099, 20818, 50000, 1 << 20),
+                                        (128, 256, 640, 4096), (128, 640, 4096)):
+        if e * n * k > 1 << 34:
+            continue
+        p = mx.mx_plan_gemm_fp4(r, n, k, experts=e, fp4_activations=fp4)
+        two = p["mtile"] <= 64  # CTAs to an SM
+        assert p["splits"] == 1 and p["mtile"] % 16 == 0 and p["mtile"] <= 224
+        assert p["stages"] >= p["min_stages"] >= 3 and (two or fp4 or p["min_stages"] == 5), (e, r, n, k, p)
+        assert p["smem"] <= (115712 if two else MAX_SMEM) and p["tmem_cols"] <= (256 if two else 512), (e, r, n, k, p)
