@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
     const uint64_t pol = policy_evict_normal();
     int s = 0, issuer = 0;
     uint32_t ph = 1;
-    bool ok = true, early = p.early_weights;
+    bool ok = true, early = !kGather && p.early_weights;  // gathered rows come with offsets
     for (int idx = first; ok && idx < total; idx += stride) {
       const Tile t = table.at(idx, p.N, rank);
       const uint8_t* const sf = p.w_scales + static_cast<size_t>(t.w_row >> 7) * units * kSfTile;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
         if (vec) {
 #pragma unroll
           for (int j = 0; j < kRows; ++j) {
-            const uint4 q = src[j] != nullptr && u0 < units ? *reinterpret_cast<const uint4*>(src[j] + u0 * 4)
+            const uint4 q = src[j] != nullptr && u0 < units ? ld_global(reinterpret_cast<const uint4*>(src[j] + u0 * 4))
                                                             : make_uint4(0, 0, 0, 0);
             w[0][j] = q.x;
             w[1][j] = q.y;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
 #pragma unroll
           for (int j = 0; j < kRows; ++j)
             w[b][j] = src[j] != nullptr && u0 + b < units
-                          ? *reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step)
+                          ? ld_global(reinterpret_cast<const uint32_t*>(src[j] + static_cast<size_t>(u0 + b) * step))
                           : 0u;
       };
       int u0 = 0;
