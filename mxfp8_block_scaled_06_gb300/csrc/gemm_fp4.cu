@@ -142,7 +142,12 @@ struct Table {
   }
 };
 
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+// g / (1 + exp(-g)) as g h / (1 + h), h = exp(g) (from 30 on the quotient is 1): for g below -87
+// exp(-g) would be beyond what __fdividef takes as a divisor (2^126).
+__device__ __forceinline__ float silu(float g) {
+  const float h = __expf(fminf(g, 30.f));
+  return g * __fdividef(h, 1.f + h);
+}
 
 template <bool kA4, bool kGather, int kMode>
 __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 : 1)
