@@ -17,7 +17,7 @@
  *    once: a status word, the per-tile counters of the persistent chain kernel
  *    (64 KiB), the activation scratch of wo_a_grouped's two-launch form
  *    (8.25 MiB), the block sums of squares of mx_gemm_chain_norm's
- *    three-launch form (64 KiB) and mx_route's row counts (1 MiB);
+ *    three-launch form (64 KiB) and mx_route's row counts (1.2 MiB);
  *    mx_gemm_chain_noalloc also uses a fixed
  *    array inside the library.
  *  - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
@@ -163,9 +163,9 @@ int mx_gemm(mx_handle* h, int M, int N, int K, const void* a, const void* a_scal
  * Cost: every CTA quantizes the K-range it contracts (each 32-block split
  * over up to 8 threads when the rows are few), so the N/128 weight tiles
  * repeat that work; it saves a launch, and on GB300 at N = 2048, K = 5120 it
- * is faster than mx_quantize_rows + mx_gemm from one to four rows (4.44 /
- * 4.46 / 4.81 us at 1 / 2 / 4 rows against 1.17 us + 3.85 / 3.89 / 4.03 us),
- * slower at eight (5.57 against 1.17 + 4.01 us). */
+ * is faster than mx_quantize_rows + mx_gemm from one to four rows (4.22 /
+ * 4.26 / 4.55 us at 1 / 2 / 4 rows against 1.19 us + 3.51 / 3.55 / 3.67 us),
+ * slower at eight (5.43 against 1.21 + 3.67 us). */
 int mx_gemm_bf16(mx_handle* h, int M, int N, int K, const void* x, long ldx,
                  const void* w, const void* w_scales, void* out, unsigned flags,
                  void* stream);
@@ -291,9 +291,10 @@ int wo_a_grouped(mx_handle* h, int T, const void* x, long ldx, const int64_t* po
  *   z          optional [T, G*R] bf16 (the pre-quantization output), or null.
  *   other arguments as in wo_a_grouped (H is not limited to 8 here).
  * q / q_scales equal mx_quantize_rows of bf16(z). On GB300 the fused kernel is
- * faster up to 8 tokens and this path from 10 on (T = 10: 7.85 vs 8.04 us;
- * T = 32: 9.9 vs 15.8 us; T = 128: 19.4 vs 74.7 us), so wo_a_grouped itself
- * takes this path above 8 tokens. Constraints: 1 <= T <= 256,
+ * faster up to 6 tokens (T = 1: 6.1 vs 6.5 us; T = 4: 6.3 vs 6.75), at 7 and 8 this path
+ * by 1 and 2 % (T = 8: 7.05 vs 7.2 us), and by far beyond (with an earlier GEMM
+ * T = 32: 9.9 vs 15.8 us; T = 128: 19.4 vs 74.7 us); wo_a_grouped itself takes this path,
+ * and the handle's scratch with it, above 8 tokens. Constraints: 1 <= T <= 256,
  * d_nope = 448, d_rope = 64, R % 128 == 0, else MX_ERR_UNSUPPORTED. A position
  * outside [0, max_pos) reads cache row 0 and is reported by mx_device_status,
  * as in wo_a_grouped. */
@@ -407,8 +408,8 @@ int mx_gemm_fp4_grouped(mx_handle* h, int E, int R, int N, int K, const void* a,
  * the experts form n_groups equal groups of neighbours, ranked by their largest key
  * (with a bias: the sum of their two largest), and only the first topk_groups
  * groups' experts can be chosen. The top_k largest keys are chosen, the largest first,
- * ties to the lowest index; which they are is decided as in exact arithmetic on the
- * given float32 / bf16 numbers (float64 where float32 cannot tell).
+ * ties to the lowest index; without a bias the logits are compared, with one the keys as
+ * float64 gives them for the given float32 / bf16 numbers (float32 keys where these tell).
  *   weights  out [T, top_k] float32: the chosen scores, divided by their sum if
  *            renormalize (0 where the sum is 0 in float64: every chosen expert masked, or its
  *            score below 1e-307), times scale

@@ -72,7 +72,9 @@ constexpr size_t kWoaScratchBytes = (size_t{8} << 20) + (size_t{256} << 10) + 25
 // (8.3 against 8.4 us; 19 against 75 us at 128 tokens). Re-measured with both
 // paths on the push split-K exchange: the two launches are faster from 10
 // tokens on (7.85 / 7.85 / 8.12 us against 8.04 / 8.19 / 8.96 us at 10 / 12 /
-// 16 tokens).
+// 16 tokens). With the GEMM's MMA warp on uniform registers the two launches take
+// 6.75 / 7.11 / 7.14 / 7.17 / 7.05 us at 4 to 8 tokens, the fused kernel 6.30 / 7.04 / 7.13 /
+// 7.23 / 7.22: the limit stays, as up to it no call uses the handle's scratch.
 constexpr int kWoaFusedMaxTokens = 8;
 // mx_gemm_chain_norm applies the RMS norm in G2's prologue up to this many rows
 // (measured on GB300 with N1 = 2048, qr 1536, N2 = 8192, N3 = 5120; beyond, G2's

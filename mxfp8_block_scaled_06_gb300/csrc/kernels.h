@@ -275,7 +275,7 @@ struct GemmFp4Plan {
 };
 GemmFp4Plan plan_gemm_fp4(int E, int R, int N, int K, bool a_fp4, int sm_count);
 cudaError_t set_gemm_fp4_attributes();
-// tm_w: [E N, K] weights, tm_a: the activations (box nt rows high; unused where tokens is set).
+// tm_w: [E N, K] weights, tm_a: the activations (box plan.a_rows rows high; unused where tokens is set).
 cudaError_t launch_gemm_fp4(const CUtensorMap& tm_w, const CUtensorMap& tm_a, const GemmFp4Args& args,
                             const GemmFp4Plan& plan, bool a_fp4, cudaStream_t stream);
 
