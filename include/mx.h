@@ -357,7 +357,8 @@ int mx_warmup(mx_handle* h, const mx_weight* w, int nw, const int* rows, int nro
  * round-to-nearest-even of x * 2^-e, saturating at +-6; scale byte e + 127. A zero
  * block has scale byte 0; the sign of zeros is kept. A block with an Inf or NaN has
  * scale byte 0xFF (NaN), zero codes and NaN values.
- * Constraints: M >= 1, K % 32 == 0; M * K < 2^34, else MX_ERR_UNSUPPORTED. */
+ * Constraints: M >= 1, K % 32 == 0; M * K < 2^34 and, swizzled, mx_scale_bytes(M, K) < 2^32,
+ * else MX_ERR_UNSUPPORTED. */
 int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, int x_type, void* q,
                          void* scales, int swizzled, void* y, void* stream);
 
@@ -513,7 +514,8 @@ int mx_plan_chain_push(int M, const mx_weight w[3], int norm, int sm_count, size
                        size_t smem_reserved, int modes[3]);
 
 /* Read and clear the device status word: MX_OK, or MX_ERR_TIMEOUT if a kernel
- * gave up on a bounded wait since the last call. Synchronizes the device. */
+ * gave up on a bounded wait since the last call, or MX_ERR_INVALID_ARG if one met
+ * an index outside its tensor. Synchronizes the device. */
 int mx_device_status(mx_handle* h, int* status);
 
 /* Diagnostic of the failure path. Launches one thread that waits, through the

@@ -832,7 +832,9 @@ int mx_quantize_rows_fp4(mx_handle* h, int M, int K, const void* x, long ldx, in
   if (x_type != MX_TYPE_BF16 && x_type != MX_TYPE_F16 && x_type != MX_TYPE_F32) return MX_ERR_INVALID_ARG;
   if (x == nullptr || q == nullptr || scales == nullptr) return MX_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 4) || !aligned(y, 16)) return MX_ERR_INVALID_ARG;
-  if (static_cast<long>(M) * K >= (1L << 34)) return MX_ERR_UNSUPPORTED;
+  // element and swizzled scale numbers are 32-bit (a row or a few are padded to 128 scale rows)
+  if (static_cast<long>(M) * K >= (1L << 34) || (swizzled && mx_scale_bytes(M, K) >= (size_t{1} << 32)))
+    return MX_ERR_UNSUPPORTED;
   return cuda_status(mx::launch_quantize_rows_fp4(x, ldx, x_type, M, K, q, scales, swizzled, y,
                                                   static_cast<cudaStream_t>(stream)));
 }
