@@ -26,6 +26,8 @@ import torch
 
 import mxfp8_block_scaled_06_gb300 as mx
 
+MOST_ROWS = 65536  # of one mx_quantize_rows call
+
 
 class ExpertLayer:
     """gate, up: [E, I, H]; down: [E, H, I] (bf16, fp16 or fp32 on the GPU); H % 128 == 0, I % 128 == 0."""
@@ -45,7 +47,14 @@ class ExpertLayer:
         return q.view(e, n, k // 2), s.view(e, -1)
 
     def _quantize(self, x):
-        return self.quantize_rows(self.h, x, swizzled=False)[:2]
+        rows, k = x.shape
+        if rows <= MOST_ROWS or self.quantize_rows is mx.mx_quantize_rows_fp4:
+            return self.quantize_rows(self.h, x, swizzled=False)[:2]
+        q, s = (torch.empty((rows, c), dtype=torch.uint8, device=x.device) for c in (k, k // 32))
+        for i in range(0, rows, MOST_ROWS):
+            part = slice(i, i + MOST_ROWS)
+            self.quantize_rows(self.h, x[part], q=q[part], scales=s[part], swizzled=False)
+        return q, s
 
     def __call__(self, x, residual=None):
         """x [T, H] bf16 -> residual + the experts' weighted sum, bf16."""

@@ -89,3 +89,13 @@ def test_every_call_of_the_layer(example, monkeypatch, t, fp4):  # noqa: F811
             ref = ox.combine(y, slots, w, f64(kw["residual"]))
             size = ox.combine(np.abs(y), slots, w, np.abs(f64(kw["residual"])))
             assert (np.abs(f64(out) - ref) <= 2.0**-8 * np.abs(ref) + (k + 2) * 2.0**-23 * size).all()
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_more_rows_than_one_quantizer_call_takes(example, fp4):  # noqa: F811
+    """22100 tokens to three experts each: 66300 rows of products, as the same tokens in two calls."""
+    layer = example.random_layer(handle(), 8, 128, 128, 3, fp4_activations=fp4)
+    x = torch.randn(22100, 128, generator=torch.Generator(device="cuda").manual_seed(1), device=dev()).bfloat16()
+    whole, parts = layer(x, residual=x), [layer(p, residual=p) for p in (x[:9000], x[9000:])]
+    assert example.mx.mx_device_status(handle()) == example.mx.MX_OK
+    assert torch.equal(whole, torch.cat(parts))
