@@ -386,7 +386,8 @@ int mx_gemm_fp4(mx_handle* h, int M, int N, int K, const void* a, const void* a_
  *                one expert after another
  *   offsets      [E + 1] int32 on the device, non-decreasing; values outside [0, R]
  *                are taken as the nearest of the two. Rows of out that no expert
- *                has are not written
+ *                has are not written. Offsets that fall are reported by mx_device_status
+ *                as MX_ERR_INVALID_ARG, and nothing is written
  *   tokens       [R] int32 on the device: the row of a behind each row of out; null: row
  *                r of a (a_rows >= R). A value outside [0, a_rows) reads as a zero row
  *                and is reported by mx_device_status as MX_ERR_INVALID_ARG

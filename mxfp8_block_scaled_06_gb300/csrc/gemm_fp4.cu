@@ -215,29 +215,45 @@ __global__ void __launch_bounds__(threads(kMode, kGather), kMode == kSmall ? 2 :
   }
   if (warp == 1) {
     if (p.offsets != nullptr) pdl_wait();
-    // the experts' rows, clamped to the output, and the tiles before each expert
+    // the experts' rows, clamped to the output, and the tiles before each expert; none at all
+    // where the offsets fall (experts would share rows, and the tiles pass 32 bits). The
+    // offsets of kAhead times 32 experts are loaded together.
+    constexpr int kAhead = 4;
     const int ntiles = kTwo ? p.N >> 8 : p.N >> 7;
-    int run = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, hi = p.R;
-      if (p.offsets != nullptr && e < p.E) {
-        lo = min(max(p.offsets[e], 0), p.R);
-        hi = min(max(p.offsets[e + 1], lo), p.R);
-      }
-      const int own = e < p.E ? (hi - lo + p.nt - 1) / p.nt * ntiles : 0;
-      int s = own;
+    int run = 0, rise = 0;  // the least rise of the offsets, of this lane
+    for (int e0 = 0; e0 < p.E; e0 += 32 * kAhead) {
+      int from[kAhead], to[kAhead];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(kFull, s, o);
-        if (lane >= o) s += up;
+      for (int j = 0; j < kAhead; ++j) {
+        const int e = e0 + 32 * j + lane;
+        const bool given = p.offsets != nullptr && e < p.E;
+        from[j] = given ? p.offsets[e] : 0;
+        to[j] = given ? p.offsets[e + 1] : p.R;
       }
-      if (e < p.E) {
-        cum[e] = run + s - own;
-        off[e] = lo;
-        if (e == p.E - 1) off[p.E] = hi;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (e0 + 32 * j >= p.E) break;
+        const int e = e0 + 32 * j + lane;
+        const int lo = min(max(from[j], 0), p.R), hi = min(max(to[j], 0), p.R);
+        if (e < p.E) rise = min(rise, hi - lo);
+        const int own = e < p.E ? (max(hi - lo, 0) + p.nt - 1) / p.nt * ntiles : 0;
+        int s = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(kFull, s, o);
+          if (lane >= o) s += up;
+        }
+        if (e < p.E) {
+          cum[e] = run + s - own;
+          off[e] = lo;
+          if (e == p.E - 1) off[p.E] = hi;
+        }
+        run += __shfl_sync(kFull, s, 31);
       }
-      run += __shfl_sync(kFull, s, 31);
+    }
+    if (__any_sync(kFull, rise < 0)) {
+      run = 0;
+      if (lane == 0) atomicOr(p.status, kStatusBadInput);
     }
     if (lane == 0) cum[p.E] = run;
   }
