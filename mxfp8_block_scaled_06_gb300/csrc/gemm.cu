@@ -1249,11 +1249,12 @@ GemmPlan plan_gemm(int M, int N, int K, int sm_count, const PlanEnv& env, bool f
                       (w_fmt == kFmtMx8 || tiles <= env.clusters[splits]) &&
                       Layout(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, area, sft).total() <=
                           kMaxDynamicSmem;
-    pl.reduction = !push                         ? w_fmt != kFmtMx8          ? rows <= kRowsMax ? kReduceRows : kReduceBulk
-                                                   : row_reduction(rows, splits) ? kReduceRows
-                                                                              : kReduceItems
-                   : push_mode == kPushCompact ? kReducePushCompact
-                                               : kReducePush;
+    if (push)
+      pl.reduction = push_mode == kPushCompact ? kReducePushCompact : kReducePush;
+    else if (w_fmt != kFmtMx8)
+      pl.reduction = rows <= kRowsMax ? kReduceRows : kReduceBulk;
+    else
+      pl.reduction = row_reduction(rows, splits) ? kReduceRows : kReduceItems;
     const Layout L(mtile, stages, per_cta, fused_a, xrows, norm ? K / 32 : 0, push ? area : 0u, sft);
     // CTAs that can share an SM must fit their TMEM together: ask for enough
     // shared memory that at most 512 / tmem_cols of them are resident.
