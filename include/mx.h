@@ -443,6 +443,122 @@ int mx_route(mx_handle* h, int T, int E, int top_k, const void* logits, long ldl
 int mx_combine(mx_handle* h, int T, int top_k, int N, const void* y, int R, long ldy, const int* slots,
                const float* weights, const void* residual, void* out, void* stream);
 
+/* ------------------------------------------- attention over an MXFP4 cache
+ * What stands between the projections of a decode step's attention: rotary positions, a
+ * paged cache whose rows are quantized to MXFP4 as they are written, and the attention
+ * that reads it (its output goes on to wo_a_grouped, which undoes the rotation). They
+ * run together in examples/cached_attention.py. */
+
+#define MX_ROPE_PLAIN 0
+#define MX_ROPE_LINEAR 1
+#define MX_ROPE_YARN 2
+
+/* cos_sin[p] = [magnitude cos(p f_i) | magnitude sin(p f_i)], i < d_rope / 2, for positions
+ * p < max_pos: float32 [max_pos, d_rope], 16-byte aligned, as mx_rope and wo_a_grouped
+ * read it. f_i = base^(-2 i / d_rope); with scaling
+ *   MX_ROPE_LINEAR  f_i / factor
+ *   MX_ROPE_YARN    f_i (1 - r_i) + f_i / factor r_i, r_i = clamp((i - lo) / max(hi - lo,
+ *                   0.001), 0, 1), lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)),
+ *                   d_rope - 1), c(b) = d_rope ln(original / (2 pi b)) / (2 ln base): pairs that
+ *                   turn more than beta_fast times over `original` positions stay, those
+ *                   that turn less than beta_slow times are interpolated (Peng et al., 2023)
+ * The angles are reduced to a fraction of a turn exactly, so far positions are as good as
+ * near ones; an entry is off by at most 2^-22 of the magnitude.
+ * Constraints: d_rope even, base > 1, factor >= 1, original >= 1, beta_fast >= beta_slow > 0
+ * (the last four as far as the scaling has them); d_rope <= 512, else MX_ERR_UNSUPPORTED. */
+int mx_rope_table(mx_handle* h, int max_pos, int d_rope, double base, int scaling, double factor, int original,
+                  double beta_fast, double beta_slow, float magnitude, float* cos_sin, void* stream);
+
+/* Rotates dimensions [first, first + d_rope) of every head by its token's position, and
+ * copies the others (in place, out == x with x's strides, they stay).
+ *   x, out     [T, heads, d] of x_type; strides of tokens and heads in elements
+ *   positions  [T] int64, 0 <= pos < max_pos; another reads row 0 and is reported by
+ *              mx_device_status as MX_ERR_INVALID_ARG
+ *   cos_sin    [max_pos, d_rope] float32, 16-byte aligned
+ *   interleaved  != 0: pair i is dimensions 2i and 2i + 1 of the part, else i and
+ *              i + d_rope / 2
+ *   inverse    != 0: by the negative angle (the gradient of the rotation, and with a
+ *              magnitude of 1 its inverse)
+ * a' = a cos - b sin, b' = b cos + a sin in float32 without fused multiply-adds, rounded once.
+ * The inverse of interleaved pairs is the rotation of wo_a_grouped.
+ * Constraints: d_rope even; head strides >= d; interleaved: d, first, all strides (and the
+ * addresses, in elements) even, else MX_ERR_UNSUPPORTED; T * heads < 2^31. Every multiple of 4
+ * and of 8 elements in all of them makes wider accesses. */
+int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const void* x, long ldx, long ldx_head,
+            int x_type, const int64_t* positions, const float* cos_sin, int max_pos, int interleaved, int inverse,
+            void* out, long ldo, long ldo_head, void* stream);
+
+/* A paged cache in MXFP4. A page holds page_size tokens: of each head, page_size rows of
+ * d / 2 bytes of packed E2M1 codes in k, and in k_scales page_size rows of d / 32 scale
+ * bytes (plain, element 2i in the low four bits); v and v_scales the same, or both null where
+ * the values are the keys. All four 16-byte aligned, strides between pages in bytes
+ * (multiples of 16). Slot page * page_size + place names a token.
+ * Constraints: page_size % 16 == 0, d % 32 == 0; pages * page_size < 2^31, d <= 1024,
+ * heads <= 65536, else MX_ERR_UNSUPPORTED. */
+typedef struct mx_cache {
+  void* k;        /* [pages][heads][page_size][d / 2]  */
+  void* k_scales; /* [pages][heads][page_size][d / 32] */
+  void* v;
+  void* v_scales;
+  int pages, page_size, heads, d;
+  long k_stride, k_scales_stride, v_stride, v_scales_stride;
+} mx_cache;
+
+/* Quantizes T tokens' keys and values into their slots, by mx_quantize_rows_fp4's rule.
+ *   slots     [T] int64, different from one another (a slot named twice ends with a mix of
+ *             the rows). A negative one is left out; one of pages * page_size or more is
+ *             left out and reported by mx_device_status as MX_ERR_INVALID_ARG
+ *   k, v      [T, heads, d] of x_type, strides of tokens and heads in elements (multiples
+ *             of 8), 16-byte aligned; v null where the cache has none
+ *   k_values, v_values  out [T, heads, d] bf16, the values that the codes stand for, of
+ *             every token (exact), or null
+ * Constraints: T * heads * d / 8 < 2^31, else MX_ERR_UNSUPPORTED. */
+int mx_cache_write(mx_handle* h, const mx_cache* cache, int T, const int64_t* slots, const void* k, long ldk,
+                   long ldk_head, const void* v, long ldv, long ldv_head, int x_type, void* k_values, void* v_values,
+                   void* stream);
+
+/* The values of R slots' rows: k (and v where the cache has values) out [R, heads, d] of
+ * out_type, contiguous, 16-byte aligned; exact in bf16 and float32, rounded to nearest in fp16. A row whose
+ * slot is negative is left as it is; one of pages * page_size or more too, and is reported
+ * by mx_device_status as MX_ERR_INVALID_ARG. A slot may be named twice.
+ * Constraints: as for mx_cache_write. */
+int mx_cache_read(mx_handle* h, const mx_cache* cache, int R, const int64_t* slots, int out_type, void* k, void* v,
+                  void* stream);
+
+/* Bytes of workspace that mx_attend needs for head dimension d (shared: values are the
+ * keys), whatever the lengths; 0 for a head dimension that it does not take. */
+size_t mx_attend_bytes(const mx_handle* h, int d, int shared);
+
+/* out[r] = sum over t of softmax_t(scale q[r].k[t]) v[t] over a paged cache.
+ *   B          sequences; T query tokens in all, sequence after sequence
+ *   q, out     [T, q_heads, d] of q_type (bf16 or fp16), strides of tokens and heads in
+ *              elements (multiples of 8), 16-byte aligned; query heads
+ *              j q_heads / heads .. are those of kv head j
+ *   q_offsets  [B + 1] int32: sequence b has query tokens q_offsets[b] .. q_offsets[b + 1] - 1;
+ *              null: T / B each. Query tokens that no sequence has are left as they are
+ *   table      [B, table_cols] int32, row stride ld_table: token t of sequence b is in page
+ *              table[b, t / page_size]. Only the pages behind lengths[b] tokens are read; one
+ *              outside [0, pages) counts as rows of zeros
+ *   lengths    [B] int32 cached tokens, the query tokens among them
+ *   causal     != 0: query token j of n sees tokens up to its own, lengths[b] - n + j; else all
+ *   window     > 0 (causal only): of these, the last `window`
+ *   lse        out [T, q_heads] float32, the log of the sum of exp(scale q.k), or null
+ *   workspace  mx_attend_bytes(h, d, v == null) bytes, 16-byte aligned; calls that overlap on
+ *              the GPU need one each
+ * Pages, offsets and lengths out of range (lengths above table_cols * page_size) are
+ * reported by mx_device_status as MX_ERR_INVALID_ARG; such a sequence's offsets count as
+ * no query tokens, its length as the nearest of 0 and the largest. A row that sees nothing
+ * is 0, its lse -inf. A NaN in the cache reaches the rows that see it.
+ * Scores and sums are float32; the weights are rounded to 11 bits relative to the largest
+ * contribution. The order of the sums follows from the lengths and the number of SMs: the same
+ * bits on every call.
+ * Constraints: q_heads % heads == 0; d one of 64, 128, 256, 512, T * q_heads and
+ * table_cols * page_size < 2^30, else MX_ERR_UNSUPPORTED. */
+int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
+              int q_type, const int* q_offsets, const int* table, int table_cols, long ld_table, const int* lengths,
+              float scale, int causal, int window, void* out, long ldo, long ldo_head, float* lse, void* workspace,
+              size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ plan queries
  * Host-only (no device, no handle): the launch plans the entry points make,
  * the mxfp8 page's fixed tactic per (shape, row range) as this library picks

@@ -12,7 +12,8 @@ allocates belong to that stream, and the order with other streams is the caller'
 Names and argument order follow the C entry points: mx_create, mx_scale_bytes,
 mx_quantize_rows, mx_gemm, mx_gemm_chain, wo_a_grouped, mx_device_status; for expert
 layers with MXFP4 weights mx_quantize_rows_fp4, mx_gemm_fp4, mx_route,
-mx_gemm_fp4_grouped, mx_combine.
+mx_gemm_fp4_grouped, mx_combine; for attention over a cache in MXFP4 (MxCache) mx_rope_table,
+mx_rope, mx_cache_write, mx_cache_read, mx_attend.
 """
 from __future__ import annotations
 
@@ -31,7 +32,8 @@ EXPORTS = ["mx_create", "mx_destroy", "mx_scale_bytes", "mx_quantize_rows",
            "mx_warmup_bytes", "mx_warmup", "mx_plan_gemm", "mx_plan_gemm_fp4", "mx_plan_chain_push",
            "mx_device_status",
            "mx_wait_selftest", "mx_status_string", "mx_quantize_rows_fp4", "mx_gemm_fp4", "mx_gemm_fp4_grouped",
-           "mx_route", "mx_combine"]
+           "mx_route", "mx_combine", "mx_rope_table", "mx_rope", "mx_cache_write", "mx_cache_read",
+           "mx_attend_bytes", "mx_attend"]
 
 _vp, _i, _l, _u = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_uint
 
@@ -46,6 +48,7 @@ MX_PUSH_NONE, MX_PUSH_COMPACT, MX_PUSH_FULL = range(3)
 # element types and router scorings (include/mx.h)
 MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32 = range(3)
 MX_SCORE_SOFTMAX, MX_SCORE_SIGMOID = range(2)
+MX_ROPE_PLAIN, MX_ROPE_LINEAR, MX_ROPE_YARN = range(3)
 
 
 class MxPlanInfo(ctypes.Structure):
@@ -56,6 +59,12 @@ class MxPlanInfo(ctypes.Structure):
 class MxPlanFp4Info(ctypes.Structure):
     _fields_ = [(f, _i) for f in ("splits", "rows", "mtile", "slices", "scale_tiles", "stages", "min_stages",
                                   "tmem_cols", "reduction")] + [("smem", ctypes.c_size_t)]
+
+
+class MxCacheInfo(ctypes.Structure):
+    _fields_ = ([(f, _vp) for f in ("k", "k_scales", "v", "v_scales")]
+                + [(f, _i) for f in ("pages", "page_size", "heads", "d")]
+                + [(f, _l) for f in ("k_stride", "k_scales_stride", "v_stride", "v_scales_stride")])
 
 
 class MxError(RuntimeError):
@@ -107,6 +116,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mx_route.argtypes = [_vp, _i, _i, _i, _vp, _l, _i, _vp, _i, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp,
                              _vp, _vp, _vp]
     lib.mx_combine.argtypes = [_vp, _i, _i, _i, _vp, _i, _l, _vp, _vp, _vp, _vp, _vp]
+    d = ctypes.c_double
+    cache = ctypes.POINTER(MxCacheInfo)
+    lib.mx_rope_table.argtypes = [_vp, _i, _i, d, _i, d, _i, d, d, ctypes.c_float, _vp, _vp]
+    lib.mx_rope.argtypes = [_vp, _i, _i, _i, _i, _i, _vp, _l, _l, _i, _vp, _vp, _i, _i, _i, _vp, _l, _l, _vp]
+    lib.mx_cache_write.argtypes = [_vp, cache, _i, _vp, _vp, _l, _l, _vp, _l, _l, _i, _vp, _vp, _vp]
+    lib.mx_cache_read.argtypes = [_vp, cache, _i, _vp, _i, _vp, _vp, _vp]
+    lib.mx_attend_bytes.argtypes = [_vp, _i, _i]
+    lib.mx_attend_bytes.restype = ctypes.c_size_t
+    lib.mx_attend.argtypes = [_vp, cache, _i, _i, _i, _vp, _l, _l, _i, _vp, _vp, _i, _l, _vp, ctypes.c_float, _i, _i,
+                              _vp, _l, _l, _vp, _vp, ctypes.c_size_t, _vp]
     lib.mx_device_status.argtypes = [_vp, ctypes.POINTER(_i)]
     lib.mx_wait_selftest.argtypes = [_vp, _vp]
     lib.mx_status_string.argtypes = [_i]
@@ -771,6 +790,236 @@ def mx_combine(h: Handle, y, slots, weights, residual=None, out=None, stream=Non
                                      weights.data_ptr(), _ptr(residual), out.data_ptr(), _stream_of(h, stream)),
            "mx_combine")
     return out
+
+
+class MxCache:
+    """A paged cache in MXFP4: k uint8 [pages, heads, page_size, d / 2] packed codes, k_scales uint8
+    [pages, heads, page_size, d / 32]; v and v_scales the same, or None where the values are the
+    keys. A page is contiguous; pages may be any distance apart (k.stride(0))."""
+
+    def __init__(self, k, k_scales, v=None, v_scales=None):
+        _t()
+        if (v is None) != (v_scales is None):
+            raise ValueError("v, v_scales: both or neither are required")
+        if k is None or k.dim() != 4:
+            raise ValueError("k: a 4-D [pages, heads, page_size, d / 2] tensor is required")
+        pages, heads, page_size, half = k.shape
+        d = 2 * half
+        if d % 32 or page_size % 16 or not (pages and heads and page_size and d):
+            raise ValueError(f"k: shape {tuple(k.shape)}, at least one page and head, a multiple of 16 tokens and of 32 "
+                             "dimensions are required")
+        for name, t, cols in (("k", k, half), ("k_scales", k_scales, d // 32), ("v", v, half), ("v_scales", v_scales, d // 32)):
+            if t is None and name[0] == "v":
+                continue
+            if t is None:
+                raise ValueError(f"{name}: a tensor is required")
+            if t.dtype not in (_scale_types() if name.endswith("scales") else _U8):
+                raise TypeError(f"{name}: dtype {t.dtype} not supported")
+            if tuple(t.shape) != (pages, heads, page_size, cols):
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(pages, heads, page_size, cols)}")
+            size = heads * page_size * cols
+            if (not t[0].is_contiguous() or t.data_ptr() % 16 or (pages > 1 and (t.stride(0) < size or t.stride(0) % 16))):
+                raise ValueError(f"{name}: layout {t.stride()} not supported")
+            if t.get_device() != k.get_device():
+                raise ValueError(f"{name}: on {t.device}, k is on {k.device}")
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self.pages, self.page_size, self.heads, self.d = pages, page_size, heads, d
+        stride = lambda t: 0 if t is None else t.stride(0) if pages > 1 else t[0].numel()  # noqa: E731
+        self.info = MxCacheInfo(_ptr(k), _ptr(k_scales), _ptr(v), _ptr(v_scales), pages, page_size, heads, d,
+                                stride(k), stride(k_scales), stride(v), stride(v_scales))
+
+    @staticmethod
+    def zeros(h: Handle, pages: int, page_size: int, heads: int, d: int, shared: bool = False):
+        """A new cache of zero rows on the handle's GPU."""
+        torch = _t()
+        t = lambda n: torch.zeros((pages, heads, page_size, n), dtype=torch.uint8,  # noqa: E731
+                                  device=torch.device("cuda", h.device))
+        return MxCache(t(d // 2), t(d // 32), *(() if shared else (t(d // 2), t(d // 32))))
+
+
+def _heads(name: str, t, dtypes, tokens: int, heads: int, d: int, step: int):
+    """A [tokens, heads, d] tensor whose last stride is 1 and whose other strides are multiples of step."""
+    if t is None:
+        raise ValueError(f"{name}: a tensor is required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+    st = t.stride()
+    # the stride of a dimension of one element says nothing
+    if (st[2] != 1 or (tokens > 1 and (st[0] < 0 or st[0] % step)) or (heads > 1 and (st[1] < d or st[1] % step))):
+        raise ValueError(f"{name}: layout {st} not supported")
+    return (st[0] if tokens > 1 else heads * d), (st[1] if heads > 1 else d)
+
+
+def _output(name: str, t, tokens: int, heads: int, d: int):
+    """Rows of an output lie apart."""
+    st = t.stride()
+    if tokens > 1 and st[0] < d or (tokens > 1 and heads > 1 and
+                                    max(st[0], st[1]) < min(st[0], st[1]) * ((tokens if st[0] <= st[1] else heads) - 1) + d):
+        raise ValueError(f"{name}: layout {st} not supported, rows lie over one another")
+
+
+def mx_rope_table(h: Handle, max_pos: int, d_rope: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, magnitude: float = 1.0, out=None,
+                  stream=None):
+    """float32 [max_pos, d_rope]: cosines, then sines, of every position, times magnitude. scaling: "none",
+    "linear" (all frequencies / factor) or "yarn" (those that turn seldom over `original` positions)."""
+    torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    kinds = {"none": MX_ROPE_PLAIN, "linear": MX_ROPE_LINEAR, "yarn": MX_ROPE_YARN}
+    if scaling not in kinds:
+        raise ValueError(f"scaling: {scaling!r}, expected one of {tuple(kinds)}")
+    if max_pos < 1 or d_rope < 2:
+        raise ValueError(f"max_pos, d_rope: {max_pos}, {d_rope}, at least 1 and 2 are required")
+    if out is not None:
+        _matrix("out", out, _F32, max_pos, d_rope)
+        _here(h, ("out", out))
+    else:
+        out = empty((max_pos, d_rope), dtype=torch.float32, device=torch.device("cuda", h.device))
+    _check(load_library().mx_rope_table(h.ptr, max_pos, d_rope, base, kinds[scaling], factor, original, beta_fast,
+                                        beta_slow, magnitude, out.data_ptr(), _stream_of(h, stream)), "mx_rope_table")
+    return out
+
+
+def mx_rope(h: Handle, x, positions, cos_sin, first: int | None = None, interleaved: bool = True, inverse: bool = False,
+            out=None, stream=None):
+    """x [T, heads, d] (bf16, fp16 or fp32, any strides of tokens and heads) with dimensions
+    first .. first + d_rope - 1 (default: the last) of each head rotated by its token's position, int64 [T]; cos_sin
+    [max_pos, d_rope] as from mx_rope_table. interleaved: pairs of neighbours, else of halves. inverse:
+    by the negative angle. out may be x."""
+    torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if x.dim() != 3:
+        raise ValueError("x: a 3-D [T, heads, d] tensor is required")
+    t, heads, d = x.shape
+    code = _type_code("x", x, (MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32))
+    ldx, ldxh = _heads("x", x, (x.dtype,), t, heads, d, 1)
+    _flat("positions", positions, (torch.int64,), t)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin: a 2-D [max_pos, d_rope] tensor is required")
+    max_pos, d_rope = cos_sin.shape
+    _matrix("cos_sin", cos_sin, _F32, max_pos, d_rope)
+    first = d - d_rope if first is None else first
+    if d_rope % 2 or first < 0 or first + d_rope > d:
+        raise ValueError(f"first: {first}, {d_rope} rotated dimensions do not fit in {d}")
+    if out is not None:
+        ldo, ldoh = _heads("out", out, (x.dtype,), t, heads, d, 1)
+        _output("out", out, t, heads, d)
+    _here(h, ("x", x), ("positions", positions), ("cos_sin", cos_sin), ("out", out))
+    if out is None:
+        out = empty((t, heads, d), dtype=x.dtype, device=x.device)
+        ldo, ldoh = heads * d, d
+    _check(load_library().mx_rope(h.ptr, t, heads, d, first, d_rope, x.data_ptr(), ldx, ldxh, code, positions.data_ptr(),
+                                  cos_sin.data_ptr(), max_pos, int(interleaved), int(inverse), out.data_ptr(), ldo, ldoh,
+                                  _stream_of(h, stream)), "mx_rope")
+    return out
+
+
+def mx_cache_write(h: Handle, cache: MxCache, slots, k, v=None, values: bool = False, stream=None):
+    """Quantizes k (and v) [T, heads, d], bf16, fp16 or fp32, into the cache's slots, int64 [T]: page * page_size
+    + place, different ones; negative: left out. Returns the values they are held as, bf16 [T, heads, d],
+    when asked, else None, None."""
+    torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if k.dim() != 3:
+        raise ValueError("k: a 3-D [T, heads, d] tensor is required")
+    t = k.shape[0]
+    code = _type_code("k", k, (MX_TYPE_BF16, MX_TYPE_F16, MX_TYPE_F32))
+    ldk, ldkh = _heads("k", k, (k.dtype,), t, cache.heads, cache.d, 8)
+    if (v is None) != (cache.v is None):
+        raise ValueError("v: the cache has " + ("no values apart" if cache.v is None else "values, they are required"))
+    ldv = ldvh = 0
+    if v is not None:
+        ldv, ldvh = _heads("v", v, (k.dtype,), t, cache.heads, cache.d, 8)
+    _flat("slots", slots, (torch.int64,), t)
+    _here(h, ("cache", cache.k), ("k", k), ("v", v), ("slots", slots))
+    kv = empty((t, cache.heads, cache.d), dtype=torch.bfloat16, device=k.device) if values else None
+    vv = empty((t, cache.heads, cache.d), dtype=torch.bfloat16, device=k.device) if values and v is not None else None
+    _check(load_library().mx_cache_write(h.ptr, cache.info, t, slots.data_ptr(), k.data_ptr(), ldk, ldkh, _ptr(v), ldv, ldvh,
+                                         code, _ptr(kv), _ptr(vv), _stream_of(h, stream)), "mx_cache_write")
+    return kv, vv
+
+
+def mx_cache_read(h: Handle, cache: MxCache, slots, dtype=None, k=None, v=None, stream=None):
+    """The values of the cache's rows at slots, int64 [R]: (k, v) [R, heads, d] of dtype (bf16 unless given;
+    fp16, fp32), v None where the cache has no values apart. Rows of negative slots are left as they are."""
+    torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if slots is None or slots.dim() != 1:
+        raise ValueError("slots: a 1-D tensor is required")
+    r = slots.shape[0]
+    _flat("slots", slots, (torch.int64,), r)
+    dtype = dtype or (torch.bfloat16 if k is None else k.dtype)
+    if dtype not in _TYPE_CODES:
+        raise TypeError(f"dtype: {dtype} not supported")
+    if v is not None and cache.v is None:
+        raise ValueError("v: the cache has no values apart")
+    shape = (r, cache.heads, cache.d)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _flat(name, t, (dtype,), r * cache.heads * cache.d)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _here(h, ("cache", cache.k), ("slots", slots), ("k", k), ("v", v))
+    if k is None:
+        k = empty(shape, dtype=dtype, device=slots.device)
+    if v is None and cache.v is not None:
+        v = empty(shape, dtype=dtype, device=slots.device)
+    _check(load_library().mx_cache_read(h.ptr, cache.info, r, slots.data_ptr(), _TYPE_CODES[dtype], k.data_ptr(), _ptr(v),
+                                        _stream_of(h, stream)), "mx_cache_read")
+    return k, v
+
+
+def mx_attend_bytes(h: Handle, d: int, shared: bool = False) -> int:
+    return int(load_library().mx_attend_bytes(h.ptr, d, int(shared)))
+
+
+def mx_attend(h: Handle, q, cache: MxCache, table, lengths, q_offsets=None, scale: float | None = None, causal: bool = True,
+              window: int = 0, out=None, lse: bool = False, workspace=None, stream=None):
+    """Attention of q [T, q_heads, d] (bf16 or fp16, any strides of tokens and heads) over a paged cache: table
+    int32 [B, columns] pages of each sequence (row stride table.stride(0)), lengths int32 [B] cached tokens, the
+    query tokens among them; q_offsets int32 [B + 1] first query token of each sequence (None: T / B each). scale:
+    d^-0.5 unless given. causal: a query token sees tokens up to its own, with window only the last so many.
+    Returns out [T, q_heads, d] in q's type; with lse (out, float32 [T, q_heads]). workspace: uint8 of
+    mx_attend_bytes, allocated unless given."""
+    torch = _t()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if q.dim() != 3:
+        raise ValueError("q: a 3-D [T, q_heads, d] tensor is required")
+    t, heads, d = q.shape
+    code = _type_code("q", q, (MX_TYPE_BF16, MX_TYPE_F16))
+    ldq, ldqh = _heads("q", q, (q.dtype,), t, heads, cache.d, 8)
+    if heads % cache.heads:
+        raise ValueError(f"q: {heads} heads, a multiple of the cache's {cache.heads} is required")
+    if table.dim() != 2 or table.dtype != torch.int32:
+        raise (ValueError if table.dtype == torch.int32 else TypeError)("table: a 2-D int32 [B, columns] tensor is required")
+    b, cols = table.shape
+    _matrix("table", table, _I32, b, cols, row_stride=b > 1)
+    _flat("lengths", lengths, _I32, b)
+    if q_offsets is not None:
+        _flat("q_offsets", q_offsets, _I32, b + 1)
+    elif b == 0 or t % b:
+        raise ValueError(f"q: {t} query tokens of {b} sequences, q_offsets is required")
+    if out is not None:
+        ldo, ldoh = _heads("out", out, (q.dtype,), t, heads, d, 8)
+        _output("out", out, t, heads, d)
+    bytes_ = mx_attend_bytes(h, d, cache.v is None)
+    if workspace is not None:
+        _flat("workspace", workspace, _U8, bytes_)
+    _here(h, ("q", q), ("cache", cache.k), ("table", table), ("lengths", lengths), ("q_offsets", q_offsets), ("out", out),
+          ("workspace", workspace))
+    if out is None:
+        out = empty((t, heads, d), dtype=q.dtype, device=q.device)
+        ldo, ldoh = heads * d, d
+    if workspace is None:
+        workspace = empty((max(bytes_, 16),), dtype=torch.uint8, device=q.device)
+    sums = empty((t, heads), dtype=torch.float32, device=q.device) if lse else None
+    _check(load_library().mx_attend(h.ptr, cache.info, b, t, heads, q.data_ptr(), ldq, ldqh, code, _ptr(q_offsets),
+                                    table.data_ptr(), cols, table.stride(0) if b > 1 else cols, lengths.data_ptr(),
+                                    d ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), ldo, ldoh,
+                                    _ptr(sums), workspace.data_ptr(), bytes_, _stream_of(h, stream)), "mx_attend")
+    return (out, sums) if lse else out
 
 
 def mx_warmup(h: Handle, weights, rows, stream=None) -> list:

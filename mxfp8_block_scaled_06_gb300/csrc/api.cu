@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <mutex>
@@ -53,6 +54,7 @@ struct mx_handle {
   uint8_t* d_woa;      // wo_a_grouped's two-launch activation (kWoaScratchBytes)
   float* d_ssq;        // mx_gemm_chain_norm's block sums of squares (kSsqBytes)
   int* d_route;        // mx_route's rows per (expert, chunk of tokens) (kRouteWorkspace)
+  int attend_ctas[mx::kAttendVariants];  // CTAs of mx_attend's kernels that are resident at once
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   TmapEntry tmaps[kTmapCache];
   int tmap_count;
@@ -403,6 +405,7 @@ int mx_create(mx_handle** out, int device) {
       h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
       if (mx::set_gemm_attributes() != cudaSuccess || mx::set_wo_a_attributes() != cudaSuccess ||
           mx::set_chain_attributes() != cudaSuccess || mx::set_gemm_fp4_attributes() != cudaSuccess ||
+          mx::set_attend_attributes(sms, h->attend_ctas) != cudaSuccess ||
           cudaMalloc(&h->d_status, 16) != cudaSuccess ||
           cudaMemset(h->d_status, 0, 16) != cudaSuccess ||
           cudaMalloc(&h->d_chain, mx::kChainCounters * sizeof(unsigned)) != cudaSuccess ||
@@ -1001,6 +1004,231 @@ int mx_combine(mx_handle* h, int T, int top_k, int N, const void* y, int R, long
   args.out = static_cast<__nv_bfloat16*>(out);
   args.status = h->d_status;
   return cuda_status(mx::launch_combine(args, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------ attention over an MXFP4 cache
+static_assert(MX_ROPE_PLAIN == mx::kRopePlain && MX_ROPE_LINEAR == mx::kRopeLinear && MX_ROPE_YARN == mx::kRopeYarn,
+              "mx.h rope scalings");
+
+int mx_rope_table(mx_handle* h, int max_pos, int d_rope, double base, int scaling, double factor, int original,
+                  double beta_fast, double beta_slow, float magnitude, float* cos_sin, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (max_pos < 1 || d_rope < 2 || d_rope % 2 != 0 || !(base > 1.0) || !std::isfinite(base) ||
+      !std::isfinite(magnitude))
+    return MX_ERR_INVALID_ARG;
+  if (scaling != MX_ROPE_PLAIN && scaling != MX_ROPE_LINEAR && scaling != MX_ROPE_YARN) return MX_ERR_INVALID_ARG;
+  if (scaling != MX_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor))) return MX_ERR_INVALID_ARG;
+  if (scaling == MX_ROPE_YARN && (original < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+    return MX_ERR_INVALID_ARG;
+  if (cos_sin == nullptr || !aligned(cos_sin, 16)) return MX_ERR_INVALID_ARG;
+  if (d_rope > mx::kRopeMaxDim) return MX_ERR_UNSUPPORTED;
+  const mx::RopeTable t = {max_pos, d_rope, scaling, base, factor, beta_fast, beta_slow, original, magnitude};
+  return cuda_status(mx::launch_rope_table(t, h->sm_count, cos_sin, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const void* x, long ldx, long ldx_head,
+            int x_type, const int64_t* positions, const float* cos_sin, int max_pos, int interleaved, int inverse,
+            void* out, long ldo, long ldo_head, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  if (T < 1 || heads < 1 || d < 2 || first < 0 || d_rope < 2 || d_rope % 2 != 0 || first > d - d_rope || max_pos < 1)
+    return MX_ERR_INVALID_ARG;
+  if (x_type != MX_TYPE_BF16 && x_type != MX_TYPE_F16 && x_type != MX_TYPE_F32) return MX_ERR_INVALID_ARG;
+  if (x == nullptr || positions == nullptr || cos_sin == nullptr || out == nullptr) return MX_ERR_INVALID_ARG;
+  const int size = x_type == MX_TYPE_F32 ? 4 : 2;
+  if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 8) || !aligned(cos_sin, 16))
+    return MX_ERR_INVALID_ARG;
+  if (ldx < 0 || ldx_head < d || ldo < 0 || ldo_head < d)
+    return MX_ERR_INVALID_ARG;
+  // in place, every element is where it was
+  if (x == out && (ldx != ldo || ldx_head != ldo_head)) return MX_ERR_INVALID_ARG;
+  mx::RopeRows a = {};
+  a.tokens = T;
+  a.heads = heads;
+  a.d = d;
+  a.first = first;
+  a.d_rope = d_rope;
+  a.x = x;
+  a.ldx = ldx;
+  a.ldx_head = ldx_head;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  a.out = out;
+  a.ldo = ldo;
+  a.ldo_head = ldo_head;
+  a.status = h->d_status;
+  // pairs are moved as two elements at least; chunk numbers are 32-bit
+  const int vec = mx::rope_vec(a, size);
+  if (interleaved && vec < 2) return MX_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(T) * heads >= (int64_t{1} << 31) ||
+      static_cast<int64_t>(T) * heads * (d / vec + 1) >= (int64_t{1} << 32))
+    return MX_ERR_UNSUPPORTED;
+  return cuda_status(mx::launch_rope(a, x_type, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// The checks that the three calls on a cache share.
+int validate_cache(const mx_cache* c) {
+  if (c == nullptr || c->pages < 1 || c->page_size < 16 || c->page_size % 16 != 0 || c->heads < 1 || c->d < 32 ||
+      c->d % 32 != 0)
+    return MX_ERR_INVALID_ARG;
+  if (c->k == nullptr || c->k_scales == nullptr || (c->v == nullptr) != (c->v_scales == nullptr))
+    return MX_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(c->pages) * c->page_size >= (int64_t{1} << 31) || c->d > 1024 || c->heads > 65536)
+    return MX_ERR_UNSUPPORTED;
+  const int64_t codes = static_cast<int64_t>(c->heads) * c->page_size * (c->d / 2), scales = codes / 16;
+  const void* pools[4] = {c->k, c->k_scales, c->v, c->v_scales};
+  const long strides[4] = {c->k_stride, c->k_scales_stride, c->v_stride, c->v_scales_stride};
+  for (int i = 0; i < (c->v != nullptr ? 4 : 2); ++i)
+    if (!aligned(pools[i], 16) || strides[i] % 16 != 0 || strides[i] < (i % 2 ? scales : codes))
+      return MX_ERR_INVALID_ARG;
+  return MX_OK;
+}
+
+mx::CacheRows cache_rows(const mx_handle* h, const mx_cache* c, int rows, const int64_t* slots) {
+  mx::CacheRows a = {};
+  a.rows = rows;
+  a.sides = c->v != nullptr ? 2 : 1;
+  a.heads = static_cast<uint32_t>(c->heads);
+  a.head_units = static_cast<uint32_t>(c->d / 8);
+  a.page_size = static_cast<uint32_t>(c->page_size);
+  a.slot_count = static_cast<int64_t>(c->pages) * c->page_size;
+  a.slots = slots;
+  a.side[0].codes = static_cast<uint8_t*>(c->k);
+  a.side[0].scales = static_cast<uint8_t*>(c->k_scales);
+  a.side[0].page_stride = c->k_stride;
+  a.side[0].scale_page_stride = c->k_scales_stride;
+  a.side[1].codes = static_cast<uint8_t*>(c->v);
+  a.side[1].scales = static_cast<uint8_t*>(c->v_scales);
+  a.side[1].page_stride = c->v_stride;
+  a.side[1].scale_page_stride = c->v_scales_stride;
+  a.status = h->d_status;
+  return a;
+}
+
+// 8-element unit numbers are 32-bit
+bool cache_units_fit(const mx_cache* c, int rows) {
+  return static_cast<int64_t>(rows) * c->heads * (c->d / 8) < (int64_t{1} << 31);
+}
+
+}  // namespace
+
+int mx_cache_write(mx_handle* h, const mx_cache* cache, int T, const int64_t* slots, const void* k, long ldk,
+                   long ldk_head, const void* v, long ldv, long ldv_head, int x_type, void* k_values, void* v_values,
+                   void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  rc = validate_cache(cache);
+  if (rc != MX_OK) return rc;
+  if (T < 1 || slots == nullptr || k == nullptr || (v == nullptr) != (cache->v == nullptr) ||
+      (v == nullptr && v_values != nullptr))
+    return MX_ERR_INVALID_ARG;
+  if (x_type != MX_TYPE_BF16 && x_type != MX_TYPE_F16 && x_type != MX_TYPE_F32) return MX_ERR_INVALID_ARG;
+  if (ldk < 0 || ldk % 8 != 0 || ldk_head < cache->d || ldk_head % 8 != 0) return MX_ERR_INVALID_ARG;
+  if (v != nullptr && (ldv < 0 || ldv % 8 != 0 || ldv_head < cache->d || ldv_head % 8 != 0)) return MX_ERR_INVALID_ARG;
+  if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_values, 16) || !aligned(v_values, 16))
+    return MX_ERR_INVALID_ARG;
+  if (!cache_units_fit(cache, T)) return MX_ERR_UNSUPPORTED;
+  mx::CacheRows a = cache_rows(h, cache, T, slots);
+  a.side[0].x = k;
+  a.side[0].ldx = ldk;
+  a.side[0].ldx_head = ldk_head;
+  a.side[0].y = k_values;
+  a.side[1].x = v;
+  a.side[1].ldx = ldv;
+  a.side[1].ldx_head = ldv_head;
+  a.side[1].y = v_values;
+  return cuda_status(mx::launch_cache_write(a, x_type, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_cache_read(mx_handle* h, const mx_cache* cache, int R, const int64_t* slots, int out_type, void* k, void* v,
+                  void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  rc = validate_cache(cache);
+  if (rc != MX_OK) return rc;
+  if (R < 1 || slots == nullptr || k == nullptr || (v == nullptr) != (cache->v == nullptr)) return MX_ERR_INVALID_ARG;
+  if (out_type != MX_TYPE_BF16 && out_type != MX_TYPE_F16 && out_type != MX_TYPE_F32) return MX_ERR_INVALID_ARG;
+  if (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return MX_ERR_INVALID_ARG;
+  if (!cache_units_fit(cache, R)) return MX_ERR_UNSUPPORTED;
+  mx::CacheRows a = cache_rows(h, cache, R, slots);
+  a.side[0].y = k;
+  a.side[1].y = v;
+  return cuda_status(mx::launch_cache_read(a, out_type, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_attend_bytes(const mx_handle* h, int d, int shared) {
+  if (h == nullptr) return 0;
+  const int v = mx::attend_variant(d, shared != 0);
+  return v < 0 ? 0 : mx::attend_bytes(d, h->attend_ctas[v]);
+}
+
+int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
+              int q_type, const int* q_offsets, const int* table, int table_cols, long ld_table, const int* lengths,
+              float scale, int causal, int window, void* out, long ldo, long ldo_head, float* lse, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  int rc = check_device(h);
+  if (rc != MX_OK) return rc;
+  rc = validate_cache(cache);
+  if (rc != MX_OK) return rc;
+  if (B < 1 || T < 1 || q_heads < 1 || q_heads % cache->heads != 0 || table_cols < 1 || ld_table < table_cols ||
+      !std::isfinite(scale) || window < 0 || (window > 0 && !causal) || (q_offsets == nullptr && T % B != 0))
+    return MX_ERR_INVALID_ARG;
+  if (q_type != MX_TYPE_BF16 && q_type != MX_TYPE_F16) return MX_ERR_INVALID_ARG;
+  if (q == nullptr || table == nullptr || lengths == nullptr || out == nullptr) return MX_ERR_INVALID_ARG;
+  if (ldq < 0 || ldq % 8 != 0 || ldq_head < cache->d || ldq_head % 8 != 0 || ldo < 0 || ldo % 8 != 0 ||
+      ldo_head < cache->d || ldo_head % 8 != 0)
+    return MX_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(q_offsets, 4) || !aligned(table, 4) || !aligned(lengths, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 16))
+    return MX_ERR_INVALID_ARG;
+  const bool shared = cache->v == nullptr;
+  const int variant = mx::attend_variant(cache->d, shared);
+  if (variant < 0 || static_cast<int64_t>(T) * q_heads >= (int64_t{1} << 30) ||
+      static_cast<int64_t>(table_cols) * cache->page_size >= (int64_t{1} << 30))
+    return MX_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < mx_attend_bytes(h, cache->d, shared)) return MX_ERR_INVALID_ARG;
+  mx::AttendArgs a = {};
+  a.B = B;
+  a.T = T;
+  a.q_heads = q_heads;
+  a.heads = cache->heads;
+  a.group = q_heads / cache->heads;
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq = ldq;
+  a.ldq_head = ldq_head;
+  a.q_f16 = q_type == MX_TYPE_F16;
+  a.q_offsets = q_offsets;
+  a.table = table;
+  a.ld_table = ld_table;
+  a.table_cols = table_cols;
+  a.lengths = lengths;
+  a.k = static_cast<const uint8_t*>(cache->k);
+  a.k_scales = static_cast<const uint8_t*>(cache->k_scales);
+  a.k_page = cache->k_stride;
+  a.k_scale_page = cache->k_scales_stride;
+  a.v = static_cast<const uint8_t*>(cache->v);
+  a.v_scales = static_cast<const uint8_t*>(cache->v_scales);
+  a.v_page = cache->v_stride;
+  a.v_scale_page = cache->v_scales_stride;
+  a.pages = cache->pages;
+  a.page_size = cache->page_size;
+  a.per_page = mx::fast_div(static_cast<uint32_t>(cache->page_size / 16));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  a.ldo_head = ldo_head;
+  a.lse = lse;
+  a.partial = static_cast<float*>(workspace);
+  a.status = h->d_status;
+  return cuda_status(mx::launch_attend(a, cache->d, shared, h->attend_ctas[variant], static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------ chain without allocation

@@ -329,4 +329,94 @@ struct CombineArgs {
 };
 cudaError_t launch_combine(const CombineArgs& args, cudaStream_t stream);
 
+// ------------------------------------------------------------ rotary positions
+enum RopeScaling : int { kRopePlain = 0, kRopeLinear = 1, kRopeYarn = 2 };
+constexpr int kRopeMaxDim = 512;
+struct RopeTable {
+  int max_pos, d_rope, scaling;
+  double base, factor, beta_fast, beta_slow;
+  int original;
+  float magnitude;
+};
+cudaError_t launch_rope_table(const RopeTable& t, int sm_count, float* cos_sin, cudaStream_t stream);
+
+// From this many chunks on a thread takes four heads of one.
+constexpr int64_t kRopeManyUnits = 1 << 20;
+struct RopeRows {
+  int tokens, heads, d, first, d_rope;
+  const void* x;
+  long ldx, ldx_head;
+  const int64_t* positions;
+  const float* cos_sin;  // [max_pos, d_rope]
+  int max_pos, interleaved, inverse;
+  void* out;
+  long ldo, ldo_head;
+  int* status;
+  // set by launch_rope
+  uint32_t units, chunks, turned, head_groups;
+  FastDiv per_row, per_token;
+};
+int rope_vec(const RopeRows& a, int size);
+cudaError_t launch_rope(const RopeRows& a, int x_type, cudaStream_t stream);
+
+// ------------------------------------------------------------ attention cache
+// From this many 8-element units on a thread takes four.
+constexpr uint32_t kCacheManyUnits = 1u << 19;
+struct CacheSide {
+  const void* x;  // write: [rows, heads, d], strides ldx and ldx_head elements
+  long ldx, ldx_head;
+  void* y;  // write: the values in bf16, or null; read: the output
+  uint8_t* codes;
+  uint8_t* scales;
+  long page_stride, scale_page_stride;  // bytes
+};
+struct CacheRows {
+  int rows, sides;
+  uint32_t heads, head_units;  // head_units = d / 8
+  uint32_t page_size;
+  int64_t slot_count;  // pages * page_size, below 2^31
+  const int64_t* slots;
+  CacheSide side[2];
+  int* status;
+  // set by the launchers
+  uint32_t units;
+  FastDiv per_head, per_row, per_page;
+};
+cudaError_t launch_cache_write(const CacheRows& args, int x_type, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheRows& args, int out_type, cudaStream_t stream);
+
+// ------------------------------------------------------------ attention over the cache
+struct AttendArgs {
+  int B, T, q_heads, heads, group;  // group = q_heads / heads
+  const uint16_t* q;  // bf16 or (q_f16) fp16 bits [T, q_heads, d], strides in elements
+  long ldq, ldq_head;
+  int q_f16;
+  const int* q_offsets;  // [B + 1], or null: T / B query tokens of each sequence
+  const int* table;      // [B, table_cols] pages, row stride ld_table
+  long ld_table;
+  int table_cols;
+  const int* lengths;  // [B]
+  const uint8_t* k;
+  const uint8_t* k_scales;
+  const uint8_t* v;  // keys' pools where values are shared
+  const uint8_t* v_scales;
+  long k_page, k_scale_page, v_page, v_scale_page;  // bytes between pages
+  int pages, page_size;
+  FastDiv per_page;  // by page_size / 16
+  float scale_log2;  // scale * log2(e)
+  int causal, window;
+  uint16_t* out;  // of q's type [T, q_heads, d]
+  long ldo, ldo_head;
+  float* lse;  // [T, q_heads] or null
+  float* partial;
+  int* status;
+};
+// Kernel variants of few query rows: head dims 64, 128, 256, 512, values apart or shared.
+constexpr int kAttendVariants = 8;
+constexpr int kAttendRows = 16;
+int attend_variant(int d, bool shared);  // -1: no such head dim
+cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]);
+size_t attend_bytes(int d, int ctas);
+cudaError_t launch_attend(const AttendArgs& args, int d, bool shared, int ctas, cudaStream_t stream);
+
 }  // namespace mx

@@ -13,11 +13,9 @@
 // Bound by memory: 2 (4) bytes in, 0.53 out, and 2 more for the values. Four threads
 // share a block, eight elements each: one 16-byte load (32 bytes
 // for fp32), two xor-shuffles for the block's amax, one 4-byte store of codes.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -31,91 +29,6 @@ constexpr int kThreads = 256;
 // smaller calls need the blocks. Streaming loads and stores (.cs) were slower: 62 and
 // 95 us.
 constexpr uint32_t kManyUnits = 1u << 20;
-
-// n / d for the d that (mul, shift) was made for (host: fast_div).
-__device__ __forceinline__ uint32_t div_u32(uint32_t n, FastDiv f) {
-  const uint32_t t = __umulhi(f.mul, n);
-  return f.shift < 0 ? n : (t + ((n - t) >> 1)) >> f.shift;
-}
-
-// Eight floats times f -> eight E2M1 codes, the first in the low bits.
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8], float f) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(v[0] * f), "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f),
-        "f"(v[6] * f), "f"(v[7] * f));
-  return r;
-}
-
-// The value of E2M1 code c (sign in bit 3): the magnitude's exponent and mantissa
-// bits are those of a float 2^126 times smaller, shifted into place; one exact
-// multiplication restores the exponent (and makes code 1 the subnormal 0.5).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const float m = __uint_as_float((c & 7u) << 22) * __uint_as_float(253u << 23);
-  return __uint_as_float(__float_as_uint(m) | ((c & 8u) << 28));
-}
-
-// Eight elements as loaded, their values, and the bits of the largest magnitude as a
-// float: at or above Inf's bits when any element is Inf or NaN.
-template <typename T>
-struct Unit {
-  uint4 raw;
-  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
-  // magnitudes of either 16-bit type order as unsigned numbers, NaN last: two at a time
-  __device__ __forceinline__ uint32_t amax() const {
-    constexpr uint32_t kMag = 0x7FFF7FFFu;
-    const uint32_t m = __vmaxu2(__vmaxu2(raw.x & kMag, raw.y & kMag), __vmaxu2(raw.z & kMag, raw.w & kMag));
-    return max(m & 0xFFFFu, m >> 16);
-  }
-  static __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
-    if constexpr (std::is_same<T, __half>::value)
-      return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
-    else
-      return m << 16;
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      } else {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  }
-};
-template <>
-struct Unit<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ uint32_t amax() const {
-    float v[8];
-    values(v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-    return m;
-  }
-  static __device__ __forceinline__ uint32_t amax_bits(uint32_t m) { return m; }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-};
 
 // kUnits 8-element units per thread, kThreads apart: their loads are in flight together.
 template <typename T, int kUnits>
@@ -168,19 +81,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t codes = finite ? cvt_e2m1x8(v, mx_inv_scale(s)) : 0u;
     if (!valid) continue;
     q[u] = codes;
-    if (y != nullptr) {
-      // 2^(s - 127): s = 0 is the subnormal 2^-127, 0xFF is NaN
-      const float f = s == 0   ? __uint_as_float(0x00400000u)
-                      : finite ? __uint_as_float(s << 23)
-                               : __uint_as_float(0x7FC00000u);
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = e2m1_value(codes >> (8 * e)) * f, b = e2m1_value(codes >> (8 * e + 4)) * f;
-        w[e] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);  // exact: the low halves are zero
-      }
-      y[u] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if (y != nullptr) y[u] = e2m1_values_bf16(codes, scale_value(s));
     if ((col[i] & 3) != 0) continue;
     const uint32_t blk = col[i] >> 2;
     scales[swizzled ? swz_offset(row[i], blk, cpad4) : row[i] * static_cast<size_t>(nblk) + blk] =
