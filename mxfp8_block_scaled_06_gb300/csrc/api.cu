@@ -90,6 +90,9 @@ constexpr size_t kSsqBytes = size_t{64} << 10;
 // rows of the MXFP4 products, and (token, choice) rows of the router: tile and row
 // numbers are 32-bit
 constexpr int kMaxFp4Rows = 1 << 24;
+// Query rows (query heads of a kv head x query tokens) of a sequence, on average, from which
+// mx_attend takes the kernel of many rows.
+constexpr int kAttendManyRows = 64;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -406,6 +409,7 @@ int mx_create(mx_handle** out, int device) {
       if (mx::set_gemm_attributes() != cudaSuccess || mx::set_wo_a_attributes() != cudaSuccess ||
           mx::set_chain_attributes() != cudaSuccess || mx::set_gemm_fp4_attributes() != cudaSuccess ||
           mx::set_attend_attributes(sms, h->attend_ctas) != cudaSuccess ||
+          mx::set_attend_rows_attributes() != cudaSuccess ||
           cudaMalloc(&h->d_status, 16) != cudaSuccess ||
           cudaMemset(h->d_status, 0, 16) != cudaSuccess ||
           cudaMalloc(&h->d_chain, mx::kChainCounters * sizeof(unsigned)) != cudaSuccess ||
@@ -1165,7 +1169,8 @@ int mx_cache_read(mx_handle* h, const mx_cache* cache, int R, const int64_t* slo
 size_t mx_attend_bytes(const mx_handle* h, int d, int shared) {
   if (h == nullptr) return 0;
   const int v = mx::attend_variant(d, shared != 0);
-  return v < 0 ? 0 : mx::attend_bytes(d, h->attend_ctas[v]);
+  return v < 0 ? 0
+               : std::max(mx::attend_bytes(d, h->attend_ctas[v]), mx::attend_rows_bytes(d, shared != 0, h->sm_count));
 }
 
 int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
@@ -1228,6 +1233,13 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
   a.lse = lse;
   a.partial = static_cast<float*>(workspace);
   a.status = h->d_status;
+  if (static_cast<int64_t>(T) * a.group >= static_cast<int64_t>(B) * kAttendManyRows) {
+    const mx::AttendRowsPlan plan =
+        mx::plan_attend_rows(cache->d, shared, B, T, q_offsets == nullptr, a.heads, a.group,
+                             static_cast<int64_t>(table_cols) * cache->page_size, h->sm_count);
+    if (plan.ok)
+      return cuda_status(mx::launch_attend_rows(a, cache->d, shared, plan, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(mx::launch_attend(a, cache->d, shared, h->attend_ctas[variant], static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,696 @@
+// attend_rows.cu - attention of many query rows over the MXFP4 cache: prompts, drafts, wide
+// groups of heads.
+//
+// As attend.cu, with the products on the 5th-generation tensor cores: 128 query rows x 128
+// cached tokens at a time, S = Q K^T and O += P V, with both accumulators and the
+// weights P in tensor memory. Keys and values are dequantized into shared memory as fp16, once
+// for all rows of a CTA: two tiles of 128 rows up to d = 128 (so that one's softmax runs
+// under the other's products), one at 256. A row of 64 dimensions of a token is 128
+// bytes of the 128-byte swizzle: as an operand of S it is K-major, as one of O it
+// is N-major, in the same place and layout.
+//
+// fp16 under powers of two, as in attend.cu, but of a whole tile: the codes are held as
+// code * 2^(s - S + 13), S the largest scale of the tile's keys, or of all values so far,
+// so a block is exact down to 2^-27 of that one. The weights are exp2(x - m + 7), rounded to fp16
+// (2^-11 down to 2^-21 of the largest, 2^-32 of it below), where m is a maximum of the row's scores that is
+// behind by 2^8 at most: O is only rescaled when a score goes beyond.
+//
+// What runs where: four warps to each tile of rows take S to P (a thread to a row), four
+// dequantize, one issues the products. Bound by the tensor cores, then by the
+// exponentials (half their time at d = 128).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kTokens = 128;    // of a tile
+constexpr int kRows = 128;      // of a tile of queries
+constexpr float kLag = 8.f;     // a score may be 2^8 above the row's reference
+constexpr float kTop = 7.f;     // 2^7 and 2^8: weights up to 2^15
+constexpr int kCodeBits = 13;   // 6 * 2^13 < 65504
+
+template <int D, bool kShared>
+struct Plan {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;            // of queries
+  static constexpr int kStages = D <= 128 || kShared ? 2 : 1;  // of dequantized tokens
+  static constexpr int kSides = kShared ? 1 : 2;
+  static constexpr int kBlocks = D / 32;
+  static constexpr int kThreads = kTiles * 128 + 128 + 32;
+  static constexpr int kTile = kTokens * D * 2;              // bytes of one side of a stage, or of a query tile
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffStage = kTiles * kTile;
+  static constexpr int kOffNan = kOffStage + kStages * kSides * kTile;  // [tile parity][token] blocks that are NaN
+  static constexpr int kBytes = kOffNan + 2 * kTokens + 1024;     // and the alignment of the base
+  // tensor memory: S (and P over it) of each tile, then O
+  static constexpr int kColO = kTiles * kTokens;
+  static constexpr int kCols = kColO + kTiles * D <= 256 ? 256 : 512;
+};
+
+// D[tmem] (+)= A[smem] x B[smem]^T or A[tmem] x B[smem], fp16 operands, float32 sums.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of .kind::f16: fp16 x fp16 -> float32, M = 128, N = n, A K-major, B
+// K-major or (n_major) N-major.
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t n, bool n_major) {
+  return (1u << 4) | (n_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// N-major operand in the 128-byte swizzle: rows (K) of 64 elements, eight rows of 1024 bytes
+// after one another, the next 64 elements of N `next` bytes on.
+__device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t saddr, uint32_t next) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(next >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Shared {
+  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+  uint32_t tmem;
+  int abort;
+  int b, row_block;      // of this CTA; b < 0: none
+  int top[2][4][2];      // largest scale bytes of each dequantizing warp's share: [tile parity][warp][side]
+  // of the tile, by its parity
+  float k_factor[2];     // 2^(S_k - 127 - 13)
+  int v_ref[2];          // S_v
+  int nan[2];            // the tile has NaN values
+};
+
+// (block of rows, sequence) of number `index` among all sequences' blocks, last block
+// first; by one warp.
+__device__ void find_block(const AttendArgs& a, int per_block, int index, Shared& sh) {
+  const int lane = threadIdx.x & 31;
+  auto blocks_of = [&](int b) { return b < a.B ? (seq_of(a, b).n * a.group + per_block - 1) / per_block : 0; };
+  int sum = 0;
+  for (int b = lane; b < a.B; b += 32) sum += blocks_of(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if (lane == 0) sh.b = -1;
+  __syncwarp();
+  if (index >= sum) return;
+  const int at = sum - 1 - index;
+  int base = 0;
+  for (int c = 0; c < a.B && base <= at; c += 32) {
+    const int w = blocks_of(c + lane);
+    int incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (base + incl - w <= at && at < base + incl) {
+      sh.b = c + lane;
+      sh.row_block = at - (base + incl - w);
+    }
+    base += __shfl_sync(kFull, incl, 31);
+  }
+}
+
+template <int D, bool kShared>
+__global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_kernel(const AttendArgs a, int splits) {
+  using L = Plan<D, kShared>;
+  constexpr int kTiles = L::kTiles, kStages = L::kStages, kBlocks = L::kBlocks;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  __shared__ Shared sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* smem = raw + (base - smem_u32(raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kDequant = kTiles * 4, kIssue = kDequant + 4;  // first warps of these roles
+
+  const uint32_t unit = blockIdx.x;
+  const int split = unit % splits;
+  const int head = unit / splits % a.heads;
+  const int index = unit / (splits * a.heads);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), 128);
+      mbar_init(smem_u32(&sh.v_full[i]), 128);
+      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_full[i]), 128);
+      mbar_init(smem_u32(&sh.o_done[i]), 1);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssue) tmem_alloc(smem_u32(&sh.tmem), L::kCols);
+  pdl_wait();
+  if (warp == 0) {
+    if (blockIdx.x == 0) {
+      bool bad = false;
+      for (int b = lane; b < a.B; b += 32) bad |= seq_of(a, b).bad;
+      if (bad) atomicOr(a.status, kStatusBadInput);
+    }
+    find_block(a, kTiles * kRows, index, sh);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int b = sh.b;
+  const bool work = b >= 0;
+  Seq s = {};
+  int row0 = 0, rows = 0, t_first = 0, tiles = 0;
+  if (work) {
+    s = seq_of(a, b);
+    rows = s.n * a.group;
+    row0 = sh.row_block * (kTiles * kRows);
+    // tokens that any row of the block sees
+    const int q_first = row0 / a.group, q_last = (min(row0 + kTiles * kRows, rows) - 1) / a.group;
+    const int64_t from = static_cast<int64_t>(s.len) - s.n + q_first - a.window + 1;
+    const int begin = a.window > 0 && from > 0 ? min(static_cast<int>(from), s.len) & ~15 : 0;
+    const int end = a.causal ? max(min(s.len - s.n + q_last + 1, s.len), begin) : s.len;
+    const int all = (end - begin + kTokens - 1) / kTokens;
+    const int first = static_cast<int>(static_cast<int64_t>(all) * split / splits);
+    tiles = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / splits) - first;
+    t_first = begin + first * kTokens;
+  }
+  volatile int* abort = &sh.abort;
+  auto wait = [&](uint64_t& bar, int n) {  // for the n-th completion
+    if (mbar_wait_or(smem_u32(&bar), (n - 1) & 1, abort)) return true;
+    if (*abort == 0) {
+      *abort = 1;
+      atomicOr(a.status, kStatusTimeout);
+    }
+    return false;
+  };
+  // as wait, the same for the whole warp
+  auto wait_warp = [&](uint64_t& bar, int n) { return __all_sync(kFull, wait(bar, n)) != 0; };
+
+  // ---- queries: fp16, each row's largest brought into [2^14, 2^15)
+  float row_factor = 0.f;
+  int lo = 0, hi = 0, token = 0, q_head = 0;
+  bool valid = false;
+  const int tile = warp >> 2;
+  if (work && warp < kDequant) {
+    const int r = row0 + tile * kRows + (warp & 3) * 32 + lane;
+    valid = r < rows;
+    token = r / a.group;
+    q_head = head * a.group + r - token * a.group;
+    const int pos = s.len - s.n + token;
+    token += s.q0;
+    hi = !valid ? 0 : a.causal ? min(pos + 1, s.len) : s.len;
+    lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const uint16_t* q = a.q + static_cast<size_t>(valid ? token : s.q0) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i)
+      if (valid) most = max(most, max_bits(reinterpret_cast<const uint4*>(q)[i]));
+    const int shift = query_shift(most, a.q_f16);
+    // a negative scale turns the queries' sign: the factor of the scores is not negative
+    const float f = a.scale_log2 < 0.f ? -pow2(shift) : pow2(shift);
+    row_factor = pow2(-shift) * fabsf(a.scale_log2);
+    const int m = (warp & 3) * 32 + lane;
+    const uint32_t to = base + L::kOffQ + tile * L::kTile + m * 128;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 v = valid ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
+      sts128(to + (i >> 3) * (kRows * 128) + (((i & 7) ^ (m & 7)) << 4), query_f16(v, a.q_f16, f));
+    }
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+
+  if (work && tiles > 0) {
+    if (warp < kDequant) {
+      // ================= softmax: a thread to a row
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + tile * kTokens, t_o = tmem + lanes + L::kColO + tile * D;
+      float m = -INFINITY, l = 0.f;
+      int v_ref = -1;
+      uint32_t nan_blocks = 0;
+      for (int j = 0; j < tiles; ++j) {
+        const int t0 = t_first + j * kTokens;
+        // the dequantizing warps' words are theirs to publish: through their own barrier
+        if (!wait_warp(sh.s_full[tile], j + 1) || !wait_warp(sh.k_full[j % kStages], j / kStages + 1)) break;
+        tc_fence_after();
+        const float f = row_factor * sh.k_factor[j & 1];
+        const int vr = sh.v_ref[j & 1];
+        if (sh.nan[j & 1]) {
+          for (int t = 0; t < kTokens; ++t)
+            if (t0 + t >= lo && t0 + t < hi) nan_blocks |= smem[L::kOffNan + (j & 1) * kTokens + t];
+        }
+        const bool masked = __any_sync(kFull, t0 < lo || t0 + kTokens > hi);
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kTokens; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(t_s + c, r);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int t = t0 + c + i;
+              if (t >= lo && t < hi) top = fmaxf(top, __uint_as_float(r[i]) * f);
+            }
+          } else {
+            float x[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i & 1] = fmaxf(x[i & 1], __uint_as_float(r[i]));
+            top = fmaxf(top, fmaxf(x[0], x[1]) * f);
+          }
+        }
+        // the reference: the row's maximum when one was first seen, or was exceeded by 2^8
+        float scale_o = 1.f;
+        if (top > m + kLag || m == -INFINITY) {
+          const float keep = exp2_fast(m - (top == -INFINITY ? 0.f : top));  // m = -inf: 0
+          l *= keep;
+          scale_o = keep;
+          m = top;
+        }
+        if (j > 0 && vr != v_ref) scale_o *= pow2(max(v_ref - vr, -126));
+        const bool rescale = j > 0 && __any_sync(kFull, scale_o != 1.f);
+        v_ref = vr;
+        if (rescale) {
+          if (!wait_warp(sh.o_done[tile], j)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(t_o + c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * scale_o);
+            tmem_st32(t_o + c, r);
+          }
+        }
+        const float sub = (m == -INFINITY ? 0.f : m) - kTop;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kTokens; c += 32) {
+          uint32_t r[32], p[16];
+          tmem_ld32(t_s + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float x = fmaf(__uint_as_float(r[i]), f, -sub), y = fmaf(__uint_as_float(r[i + 1]), f, -sub);
+            if (masked) {
+              const int t = t0 + c + i;
+              if (t < lo || t >= hi) x = -INFINITY;
+              if (t + 1 < lo || t + 1 >= hi) y = -INFINITY;
+            }
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            sum[0] += x;
+            sum[1] += y;
+            p[i / 2] = pack_f16(x, y);
+          }
+          // P lies over the S columns that this thread has read: 32 of them make 16 of P
+          tmem_st16(t_s + c / 2, p);
+        }
+        l += sum[0] + sum[1];
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.p_full[tile]));
+      }
+      // ---- the result
+      if (wait_warp(sh.o_done[tile], tiles)) {
+        tc_fence_after();
+        if (kShared && nan_blocks) l = NAN;
+        const bool whole = splits == 1;
+        const float to_m = pow2(max(v_ref - 127 - kCodeBits, -126));
+        const float inv = (whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f) * to_m;
+        // parts of splits: [unit][row] {m, l} and the sums
+        float* part = a.partial + static_cast<size_t>(unit) * (kTiles * kRows) * (D + 2);
+        const int pr = tile * kRows + (warp & 3) * 32 + lane;
+        uint16_t* out = a.out + static_cast<size_t>(valid ? token : 0) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(t_o + c, r);
+          tmem_ld_wait();
+          float v[32];
+          const float x = !kShared && ((nan_blocks >> (c / 32)) & 1u) ? NAN : inv;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (whole) {
+            if (valid)
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(out + c + i) = pack_out8(v + i, x, a.q_f16);
+          } else {
+            float4* to = reinterpret_cast<float4*>(part + 2 * kTiles * kRows + static_cast<size_t>(pr) * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              to[i / 4] = make_float4(v[i] * x, v[i + 1] * x, v[i + 2] * x, v[i + 3] * x);
+          }
+        }
+        if (!whole) {
+          part[pr] = m - kTop;
+          part[kTiles * kRows + pr] = l;
+        } else if (valid && a.lse != nullptr) {
+          a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (m - kTop + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    } else if (warp < kIssue) {
+      // ================= dequantization
+      const int tid = (warp - kDequant) * 32 + lane;
+      constexpr int kEach = kTokens * kBlocks / 128;  // 32-blocks of a side that a thread has
+      // its blocks are numbers tid + 128 x of the tile's [token][block]
+      const int blk = tid % kBlocks, tok = tid / kBlocks;
+      constexpr int kStep = 128 / kBlocks;  // tokens between two of them
+      uint4 code[L::kSides][kEach];
+      uint32_t scale[L::kSides][kEach];
+      bool here[kEach];
+      const int t_stop = min(t_first + tiles * kTokens, s.len);
+      auto load = [&](int j) {
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+          const int t = t_first + j * kTokens + tok + x * kStep;
+          here[x] = t < t_stop;
+          if (!here[x]) continue;
+          const uint32_t group = static_cast<uint32_t>(t) >> 4, col = div_u32(group, a.per_page);
+          const int page = a.table[static_cast<size_t>(b) * a.ld_table + col];
+          here[x] = page >= 0 && page < a.pages;
+          if (!here[x]) {
+            atomicOr(a.status, kStatusBadInput);
+            continue;
+          }
+          const size_t row = static_cast<size_t>(head) * a.page_size + (t - col * a.page_size);
+#pragma unroll
+          for (int sd = 0; sd < L::kSides; ++sd) {
+            const uint8_t* codes = (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2);
+            const uint8_t* scales = (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks;
+            code[sd][x] = *reinterpret_cast<const uint4*>(codes + blk * 16);
+            scale[sd][x] = scales[blk];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kEach; ++x)
+          if (!here[x])
+#pragma unroll
+            for (int sd = 0; sd < L::kSides; ++sd) code[sd][x] = make_uint4(0, 0, 0, 0), scale[sd][x] = 0;
+      };
+      load(0);
+      // no less than 2^-113: the factors are normal numbers
+      int v_ref = 127 + kCodeBits - 126;
+      bool ok = true;
+      for (int j = 0; j < tiles; ++j) {
+        const int st = j % kStages;
+        // the tile's largest scales, and whether it has NaN
+        int top[2] = {0, 0};
+        uint32_t nan = 0;
+#pragma unroll
+        for (int sd = 0; sd < L::kSides; ++sd)
+#pragma unroll
+          for (int x = 0; x < kEach; ++x) {
+            if (scale[sd][x] == 255u) {
+              if (sd == L::kSides - 1) nan |= 1u << x;
+            } else {
+              top[sd] = max(top[sd], static_cast<int>(scale[sd][x]));
+            }
+          }
+#pragma unroll
+        for (int sd = 0; sd < L::kSides; ++sd) top[sd] = __reduce_max_sync(kFull, top[sd]);
+        const bool any_nan = __any_sync(kFull, nan != 0);
+        if (lane == 0) {
+          sh.top[j & 1][warp - kDequant][0] = top[0];
+          sh.top[j & 1][warp - kDequant][1] = (kShared ? top[0] : top[1]) | (any_nan ? 256 : 0);
+        }
+        // every thread comes here, also after a wait that ran out: all leave together
+        if (named_barrier_or(1, 128, !ok)) break;
+        int k_top = 127 + kCodeBits - 126;
+        bool nans = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          k_top = max(k_top, sh.top[j & 1][w][0]);
+          const int v = sh.top[j & 1][w][1];
+          v_ref = max(v_ref, v & 255);
+          nans |= v >= 256;
+        }
+        if constexpr (kShared) k_top = v_ref;  // one copy serves both
+        // Stage and words are free: the scores of this stage's last tile are done, and with two stages
+        // its sums, whose weights the softmax took from tile j - 2's words. (With one stage: the scores of
+        // tile j - 1 were issued after those sums.)
+        if (j >= kStages) {
+          if (!kShared) ok = wait(sh.k_empty[st], j / kStages);
+          if (kShared || kStages > 1) ok = ok && wait(sh.v_empty[st], j / kStages);
+        }
+        if (nans) {
+          // one byte a token: which of its blocks are NaN
+          if (ok) smem[L::kOffNan + (j & 1) * kTokens + tid] = 0;
+          if (named_barrier_or(1, 128, !ok)) break;
+#pragma unroll
+          for (int x = 0; x < kEach; ++x)
+            if (nan >> x & 1u)
+              atomicOr(reinterpret_cast<unsigned*>(smem + L::kOffNan + (j & 1) * kTokens + ((tok + x * kStep) & ~3)),
+                       1u << (blk + 8 * ((tok + x * kStep) & 3)));
+        }
+        if (ok && tid == 0) {
+          sh.k_factor[j & 1] = pow2(k_top - 127 - kCodeBits);
+          sh.v_ref[j & 1] = v_ref;
+          sh.nan[j & 1] = nans;
+        }
+#pragma unroll
+        for (int sd = 0; sd < L::kSides; ++sd) {
+          const int ref = sd ? v_ref : k_top;
+          if (sd == 1 && kStages == 1 && j > 0) ok = ok && wait(sh.v_empty[st], j);
+          if (!ok) continue;
+          const uint32_t to = base + L::kOffStage + (st * L::kSides + sd) * L::kTile + (blk >> 1) * (kTokens * 128);
+#pragma unroll
+          for (int x = 0; x < kEach; ++x) {
+            const int t = tok + x * kStep;
+            const int e = static_cast<int>(scale[sd][x]) - ref + 15 + kCodeBits;  // biased exponent of fp16
+            uint32_t f = static_cast<uint32_t>(max(e, 0)) << 10;
+            // a NaN value is 0 here and comes back in its rows' results; a NaN key is NaN
+            if (scale[sd][x] == 255u) f = sd == L::kSides - 1 ? 0u : 0x7E00u;
+            f *= 0x10001u;
+            const uint32_t w[4] = {code[sd][x].x, code[sd][x].y, code[sd][x].z, code[sd][x].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[4];
+              codes_f16(w[i], r);
+              sts128(to + t * 128 + (((((blk & 1) << 2) + i) ^ (t & 7)) << 4),
+                     make_uint4(mul_f16x2(r[0], f), mul_f16x2(r[1], f), mul_f16x2(r[2], f), mul_f16x2(r[3], f)));
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(smem_u32(sd == 0 ? &sh.k_full[st] : &sh.v_full[st]));
+        }
+        if (j + 1 < tiles) load(j + 1);
+      }
+    } else if (warp == kIssue) {
+      // ================= products
+      if (elect_one()) {
+        const uint32_t id_s = idesc_f16(kTokens, false), id_o = idesc_f16(D, true);
+        bool ok = true;
+        auto sums = [&](int g, int j) {  // O_g += P_g V of tile j
+          const int st = j % kStages;
+          if (!wait(sh.p_full[g], j + 1)) return false;
+          if (!kShared && g == 0 && !wait(sh.v_full[st], j / kStages + 1)) return false;
+          tc_fence_after();
+          const uint32_t v = base + L::kOffStage + (st * L::kSides + L::kSides - 1) * L::kTile;
+#pragma unroll
+          for (int k = 0; k < kTokens / 16; ++k)
+            mma_ts(tmem + L::kColO + g * D, tmem + g * kTokens + k * 8, sdesc_n_sw128(v + k * 2048, kTokens * 128), id_o,
+                   j > 0 || k > 0);
+          tc_commit(smem_u32(&sh.o_done[g]));
+          if (g == kTiles - 1) tc_commit(smem_u32(&sh.v_empty[st]));
+          return true;
+        };
+        for (int j = 0; ok && j < tiles; ++j) {
+          const int st = j % kStages;
+          if (!wait(sh.k_full[st], j / kStages + 1)) break;
+          const uint32_t k0 = base + L::kOffStage + st * L::kSides * L::kTile;
+          for (int g = 0; ok && g < kTiles; ++g) {
+            if (j > 0) ok = sums(g, j - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t q0 = base + L::kOffQ + g * L::kTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
+              mma_ss(tmem + g * kTokens, sdesc_k_sw128(q0 + at), sdesc_k_sw128(k0 + at), id_s, k > 0);
+            }
+            tc_commit(smem_u32(&sh.s_full[g]));
+          }
+          if (ok && !kShared) tc_commit(smem_u32(&sh.k_empty[st]));
+        }
+        for (int g = 0; ok && g < kTiles; ++g) ok = sums(g, tiles - 1);
+      }
+      __syncwarp();
+    }
+  } else if (work && warp < kDequant) {
+    // no token in sight: zeros, or an empty part
+    if (splits == 1) {
+      if (valid) {
+        uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+        if (a.lse != nullptr) a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = -INFINITY;
+      }
+    } else {
+      float* part = a.partial + static_cast<size_t>(unit) * (kTiles * kRows) * (D + 2);
+      const int pr = tile * kRows + (warp & 3) * 32 + lane;
+      part[pr] = -INFINITY;
+      part[kTiles * kRows + pr] = 0.f;
+      for (int c = 0; c < D; c += 4)
+        *reinterpret_cast<float4*>(part + 2 * kTiles * kRows + static_cast<size_t>(pr) * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssue) tmem_dealloc(tmem, L::kCols);
+}
+
+// The splits of each block of rows, added up in order: a warp to a row.
+template <int D, int kRowsOfBlock>
+__global__ void __launch_bounds__(256) attend_rows_join_kernel(const AttendArgs a, int splits) {
+  __shared__ Shared sh;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % a.heads, index = blockIdx.x / a.heads;
+  if (warp == 0) find_block(a, kRowsOfBlock, index, sh);
+  __syncthreads();
+  if (sh.b < 0) return;
+  const Seq s = seq_of(a, sh.b);
+  const int rows = s.n * a.group;
+  const int i = blockIdx.y * 8 + warp, r = sh.row_block * kRowsOfBlock + i;
+  if (r >= rows) return;
+  const float* first = a.partial + static_cast<size_t>(blockIdx.x) * splits * kRowsOfBlock * (D + 2);
+  constexpr size_t kPart = static_cast<size_t>(kRowsOfBlock) * (D + 2);
+  float top = -INFINITY;
+  for (int p = 0; p < splits; ++p) top = fmaxf(top, first[p * kPart + i]);
+  float sum = 0.f, v[D / 32] = {};
+  for (int p = 0; p < splits; ++p) {
+    const float* x = first + p * kPart;
+    const float m = x[i], l = x[kRowsOfBlock + i];
+    const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - top);
+    sum += l * f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) v[c] += x[2 * kRowsOfBlock + static_cast<size_t>(i) * D + c * 32 + lane] * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int q_token = r / a.group, token = s.q0 + q_token, q_head = head * a.group + r - q_token * a.group;
+  uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) out[c * 32 + lane] = static_cast<uint16_t>(pack_out(v[c] * inv, 0.f, a.q_f16));
+  if (a.lse != nullptr && lane == 0)
+    a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, bool kShared, typename F>
+auto with_kernels(F&& f) {
+  using L = Plan<D, kShared>;
+  return f(attend_rows_kernel<D, kShared>, attend_rows_join_kernel<D, L::kTiles * kRows>, L::kBytes, L::kThreads,
+           L::kTiles * kRows);
+}
+template <typename F>
+auto with_variant(int v, F&& f) {
+  switch (v) {
+    case 0: return with_kernels<64, false>(f);
+    case 1: return with_kernels<64, true>(f);
+    case 2: return with_kernels<128, false>(f);
+    case 3: return with_kernels<128, true>(f);
+    case 4: return with_kernels<256, false>(f);
+    default: return with_kernels<256, true>(f);
+  }
+}
+
+}  // namespace
+
+cudaError_t set_attend_rows_attributes() {
+  for (int v = 0; v < kAttendRowsVariants; ++v) {
+    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int, int) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+AttendRowsPlan plan_attend_rows(int d, bool shared, int B, int T, bool uniform, int heads, int group, int64_t most_tokens,
+                                int sm_count) {
+  AttendRowsPlan p = {};
+  const int v = attend_variant(d, shared);
+  if (v < 0 || v >= kAttendRowsVariants) return p;
+  // blocks of rows: at most one beyond the full ones in each sequence
+  const int per = with_variant(v, [](auto, auto, int, int, int rows) { return rows; });
+  const int64_t most = static_cast<int64_t>(T) * group / per + std::min(B, T);
+  const int64_t blocks = uniform ? (static_cast<int64_t>(T / B) * group + per - 1) / per * B : most;
+  if (blocks * heads >= (int64_t{1} << 30)) return p;
+  p.blocks = static_cast<int>(blocks);
+  const int64_t tiles = (most_tokens + kTokens - 1) / kTokens;
+  const int64_t units = static_cast<int64_t>(p.blocks) * heads;
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count / units, tiles)));
+  p.ok = true;
+  return p;
+}
+
+// Parts of at most sm_count splits.
+size_t attend_rows_bytes(int d, bool shared, int sm_count) {
+  const int v = attend_variant(d, shared);
+  if (v < 0 || v >= kAttendRowsVariants) return 0;
+  const int per = with_variant(v, [](auto, auto, int, int, int rows) { return rows; });
+  return static_cast<size_t>(sm_count) * per * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend_rows(const AttendArgs& a, int d, bool shared, const AttendRowsPlan& p, cudaStream_t stream) {
+  return with_variant(attend_variant(d, shared), [&](auto kernel, auto join, int bytes, int threads, int rows) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<uint32_t>(p.blocks) * a.heads * p.splits);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, p.splits);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cfg.gridDim = dim3(static_cast<uint32_t>(p.blocks) * a.heads, rows / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join, a, p.splits);
+  });
+}
+
+}  // namespace mx

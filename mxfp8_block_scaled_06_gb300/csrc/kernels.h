@@ -418,5 +418,17 @@ int attend_variant(int d, bool shared);  // -1: no such head dim
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]);
 size_t attend_bytes(int d, int ctas);
 cudaError_t launch_attend(const AttendArgs& args, int d, bool shared, int ctas, cudaStream_t stream);
+// Many query rows (head dims up to 256): blocks of rows, and splits of their tokens.
+constexpr int kAttendRowsVariants = 6;
+struct AttendRowsPlan {
+  bool ok;
+  int blocks, splits;
+};
+cudaError_t set_attend_rows_attributes();
+// uniform: T / B query tokens of every sequence; most_tokens: of a sequence at most.
+AttendRowsPlan plan_attend_rows(int d, bool shared, int B, int T, bool uniform, int heads, int group, int64_t most_tokens,
+                                int sm_count);
+size_t attend_rows_bytes(int d, bool shared, int sm_count);
+cudaError_t launch_attend_rows(const AttendArgs& args, int d, bool shared, const AttendRowsPlan& plan, cudaStream_t stream);
 
 }  // namespace mx

@@ -179,6 +179,19 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const unsigned* p) {
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same, telling whether any of the threads came with v set.
+__device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t threads, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return any != 0;
+}
 
 // ------------------------------------------------------------------ cluster
 __device__ __forceinline__ void cluster_sync() {
