@@ -107,6 +107,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 struct Shared {
@@ -271,31 +286,46 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         // the dequantizing warps' words are theirs to publish: through their own barrier
         if (!wait_warp(sh.s_full[tile], j + 1) || !wait_warp(sh.k_full[j % kStages], j / kStages + 1)) break;
         tc_fence_after();
-        const float f = row_factor * sh.k_factor[j & 1];
+        // not 0, as -inf times it has to stay; scores of 2^44 at most times 2^-100 are 0 all the same
+        const float f = fmaxf(row_factor * sh.k_factor[j & 1], 0x1p-100f);
         const int vr = sh.v_ref[j & 1];
         if (sh.nan[j & 1]) {
           for (int t = 0; t < kTokens; ++t)
             if (t0 + t >= lo && t0 + t < hi) nan_blocks |= smem[L::kOffNan + (j & 1) * kTokens + t];
         }
-        const bool masked = __any_sync(kFull, t0 < lo || t0 + kTokens > hi);
-        float top = -INFINITY;
+        if (__any_sync(kFull, t0 < lo || t0 + kTokens > hi)) {
+          // what a row does not see becomes -inf; tiles at the diagonal and the ends only
+#pragma unroll 1
+          for (int c = 0; c < kTokens; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(t_s + c, r);
+            tmem_ld_wait();
+            const int from = lo - t0 - c, to = hi - t0 - c;
 #pragma unroll
-        for (int c = 0; c < kTokens; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(t_s + c, r);
-          tmem_ld_wait();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int t = t0 + c + i;
-              if (t >= lo && t < hi) top = fmaxf(top, __uint_as_float(r[i]) * f);
-            }
-          } else {
-            float x[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i & 1] = fmaxf(x[i & 1], __uint_as_float(r[i]));
-            top = fmaxf(top, fmaxf(x[0], x[1]) * f);
+            for (int i = 0; i < 32; ++i) r[i] = i >= from && i < to ? r[i] : 0xFF800000u;
+            tmem_st32(t_s + c, r);
           }
+          tmem_st_wait();
+        }
+        // (loops are not unrolled more than they have to be: twelve warps run different code, and
+        // waited for instructions: 8500 cycles a pair of tiles)
+        float top = -INFINITY;
+        {
+          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t r0[32], r1[32];
+          tmem_ld32(t_s, r0);
+#pragma unroll 1
+          for (int c = 0; c < kTokens; c += 64) {
+            tmem_ld_wait();
+            tmem_ld32(t_s + c + 32, r1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i & 3] = fmaxf(x[i & 3], __uint_as_float(r0[i]));
+            tmem_ld_wait();
+            if (c + 64 < kTokens) tmem_ld32(t_s + c + 64, r0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i & 3] = fmaxf(x[i & 3], __uint_as_float(r1[i]));
+          }
+          top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
         }
         // the reference: the row's maximum when one was first seen, or was exceeded by 2^8
         float scale_o = 1.f;
@@ -322,30 +352,35 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
           }
         }
         const float sub = (m == -INFINITY ? 0.f : m) - kTop;
-        float sum[2] = {0.f, 0.f};
+        float2 sum = make_float2(0.f, 0.f);
+        {
+          const float2 f2 = make_float2(f, f), sub2 = make_float2(-sub, -sub);
+          auto weights = [&](const uint32_t (&r)[32], int c) {
+            uint32_t p[16];
 #pragma unroll
-        for (int c = 0; c < kTokens; c += 32) {
-          uint32_t r[32], p[16];
-          tmem_ld32(t_s + c, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float x = fmaf(__uint_as_float(r[i]), f, -sub), y = fmaf(__uint_as_float(r[i + 1]), f, -sub);
-            if (masked) {
-              const int t = t0 + c + i;
-              if (t < lo || t >= hi) x = -INFINITY;
-              if (t + 1 < lo || t + 1 >= hi) y = -INFINITY;
+            for (int i = 0; i < 32; i += 2) {
+              float2 x = fma_f32x2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, sub2);
+              x.x = exp2_fast(x.x);
+              x.y = exp2_fast(x.y);
+              sum = add_f32x2(sum, x);
+              p[i / 2] = pack_f16(x.x, x.y);
             }
-            x = exp2_fast(x);
-            y = exp2_fast(y);
-            sum[0] += x;
-            sum[1] += y;
-            p[i / 2] = pack_f16(x, y);
+            // P lies over the S columns that this thread has read: 32 of them make 16 of P
+            tmem_st16(t_s + c / 2, p);
+          };
+          uint32_t r0[32], r1[32];
+          tmem_ld32(t_s, r0);
+#pragma unroll 1
+          for (int c = 0; c < kTokens; c += 64) {
+            tmem_ld_wait();
+            tmem_ld32(t_s + c + 32, r1);
+            weights(r0, c);
+            tmem_ld_wait();
+            if (c + 64 < kTokens) tmem_ld32(t_s + c + 64, r0);
+            weights(r1, c + 32);
           }
-          // P lies over the S columns that this thread has read: 32 of them make 16 of P
-          tmem_st16(t_s + c / 2, p);
         }
-        l += sum[0] + sum[1];
+        l += sum.x + sum.y;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&sh.p_full[tile]));
@@ -392,47 +427,60 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
       // ================= dequantization
       const int tid = (warp - kDequant) * 32 + lane;
       constexpr int kEach = kTokens * kBlocks / 128;  // 32-blocks of a side that a thread has
-      // its blocks are numbers tid + 128 x of the tile's [token][block]
-      const int blk = tid % kBlocks, tok = tid / kBlocks;
-      constexpr int kStep = 128 / kBlocks;  // tokens between two of them
-      uint4 code[L::kSides][kEach];
-      uint32_t scale[L::kSides][kEach];
-      bool here[kEach];
+      // eight threads have the same block of eight tokens, whose rows lie in all banks
+      const int blk = (tid >> 3) % kBlocks, tok = (tid & 7) + tid / (8 * kBlocks) * 8;
+      constexpr int kStep = 128 / kBlocks;  // tokens between two of a thread's
+      // Loads run ahead: page numbers two tiles, rows one, where two tiles of them fit in the
+      // registers; else a side's next rows are loaded when the present ones are converted.
+      constexpr bool kAhead = L::kSides * kEach <= 8;
+      struct Rows {
+        uint4 code[kEach];
+        uint32_t scale[kEach];  // 256: no token
+      };
+      const int* pages_of = a.table + static_cast<size_t>(b) * a.ld_table;
+      bool bad = false;  // a page outside the cache
+      Rows now[L::kSides], next[kAhead ? L::kSides : 1];
+      int page[kEach], place[kEach];  // the next rows', page -1: no token
       const int t_stop = min(t_first + tiles * kTokens, s.len);
-      auto load = [&](int j) {
+      auto load_pages = [&](int j) {
 #pragma unroll
         for (int x = 0; x < kEach; ++x) {
           const int t = t_first + j * kTokens + tok + x * kStep;
-          here[x] = t < t_stop;
-          if (!here[x]) continue;
-          const uint32_t group = static_cast<uint32_t>(t) >> 4, col = div_u32(group, a.per_page);
-          const int page = a.table[static_cast<size_t>(b) * a.ld_table + col];
-          here[x] = page >= 0 && page < a.pages;
-          if (!here[x]) {
-            atomicOr(a.status, kStatusBadInput);
-            continue;
-          }
-          const size_t row = static_cast<size_t>(head) * a.page_size + (t - col * a.page_size);
-#pragma unroll
-          for (int sd = 0; sd < L::kSides; ++sd) {
-            const uint8_t* codes = (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2);
-            const uint8_t* scales = (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks;
-            code[sd][x] = *reinterpret_cast<const uint4*>(codes + blk * 16);
-            scale[sd][x] = scales[blk];
-          }
+          const uint32_t col = div_u32(static_cast<uint32_t>(t) >> 4, a.per_page);
+          place[x] = t - col * a.page_size;
+          page[x] = -1;
+          if (t < t_stop) page[x] = pages_of[col];
         }
-#pragma unroll
-        for (int x = 0; x < kEach; ++x)
-          if (!here[x])
-#pragma unroll
-            for (int sd = 0; sd < L::kSides; ++sd) code[sd][x] = make_uint4(0, 0, 0, 0), scale[sd][x] = 0;
       };
-      load(0);
+      const size_t head_row = static_cast<size_t>(head) * a.page_size;
+      const uint8_t* codes_of[2] = {a.k + head_row * (D / 2) + blk * 16, a.v + head_row * (D / 2) + blk * 16};
+      const uint8_t* scales_of[2] = {a.k_scales + head_row * kBlocks + blk, a.v_scales + head_row * kBlocks + blk};
+      auto load = [&](int j, int sd, Rows& to) {
+#pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+          // what is not there is read from the first page, and not used
+          const bool here = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(a.pages);
+          bad |= !here && t_first + j * kTokens + tok + x * kStep < t_stop;
+          const int pg = here ? page[x] : 0, at = here ? place[x] : 0;
+          to.code[x] = *reinterpret_cast<const uint4*>(codes_of[sd] + pg * (sd ? a.v_page : a.k_page) + at * (D / 2));
+          const uint32_t sc = scales_of[sd][pg * (sd ? a.v_scale_page : a.k_scale_page) + at * kBlocks];
+          to.scale[x] = here ? sc : 256u;
+        }
+      };
+      load_pages(0);
+#pragma unroll
+      for (int sd = 0; sd < L::kSides; ++sd) load(0, sd, now[sd]);
+      load_pages(1);
       // no less than 2^-113: the factors are normal numbers
       int v_ref = 127 + kCodeBits - 126;
       bool ok = true;
       for (int j = 0; j < tiles; ++j) {
         const int st = j % kStages;
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int sd = 0; sd < L::kSides; ++sd) load(j + 1, sd, next[sd]);
+          load_pages(j + 2);
+        }
         // the tile's largest scales, and whether it has NaN
         int top[2] = {0, 0};
         uint32_t nan = 0;
@@ -440,11 +488,9 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         for (int sd = 0; sd < L::kSides; ++sd)
 #pragma unroll
           for (int x = 0; x < kEach; ++x) {
-            if (scale[sd][x] == 255u) {
-              if (sd == L::kSides - 1) nan |= 1u << x;
-            } else {
-              top[sd] = max(top[sd], static_cast<int>(scale[sd][x]));
-            }
+            const uint32_t sc = now[sd].scale[x];
+            if (sd == L::kSides - 1 && sc == 255u) nan |= 1u << x;
+            top[sd] = max(top[sd], sc < 255u ? static_cast<int>(sc) : 0);
           }
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) top[sd] = __reduce_max_sync(kFull, top[sd]);
@@ -496,12 +542,12 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
 #pragma unroll
           for (int x = 0; x < kEach; ++x) {
             const int t = tok + x * kStep;
-            const int e = static_cast<int>(scale[sd][x]) - ref + 15 + kCodeBits;  // biased exponent of fp16
-            uint32_t f = static_cast<uint32_t>(max(e, 0)) << 10;
+            const int e = static_cast<int>(now[sd].scale[x]) - ref + 15 + kCodeBits;  // biased exponent of fp16
+            uint32_t f = static_cast<uint32_t>(max(e, 0)) * (0x10001u << 10);
             // a NaN value is 0 here and comes back in its rows' results; a NaN key is NaN
-            if (scale[sd][x] == 255u) f = sd == L::kSides - 1 ? 0u : 0x7E00u;
-            f *= 0x10001u;
-            const uint32_t w[4] = {code[sd][x].x, code[sd][x].y, code[sd][x].z, code[sd][x].w};
+            if (now[sd].scale[x] >= 255u) f = sd == L::kSides - 1 || now[sd].scale[x] == 256u ? 0u : 0x7E007E00u;
+            const uint4 cw = now[sd].code[x];
+            const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t r[4];
@@ -512,9 +558,16 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
           }
           fence_proxy_async_smem();
           mbar_arrive(smem_u32(sd == 0 ? &sh.k_full[st] : &sh.v_full[st]));
+          if constexpr (!kAhead) load(j + 1, sd, now[sd]);
         }
-        if (j + 1 < tiles) load(j + 1);
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int sd = 0; sd < L::kSides; ++sd) now[sd] = next[sd];
+        } else {
+          load_pages(j + 2);
+        }
       }
+      if (bad) atomicOr(a.status, kStatusBadInput);
     } else if (warp == kIssue) {
       // ================= products
       if (elect_one()) {
