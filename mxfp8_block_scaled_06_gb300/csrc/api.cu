@@ -1170,7 +1170,9 @@ size_t mx_attend_bytes(const mx_handle* h, int d, int shared) {
   if (h == nullptr) return 0;
   const int v = mx::attend_variant(d, shared != 0);
   return v < 0 ? 0
-               : std::max(mx::attend_bytes(d, h->attend_ctas[v]), mx::attend_rows_bytes(d, shared != 0, h->sm_count));
+               : std::max({mx::attend_bytes(d, h->attend_ctas[v], 16),
+                           mx::attend_bytes(d, h->attend_ctas[v + mx::kAttendVariants / 2], 8),
+                           mx::attend_rows_bytes(d, shared != 0, h->sm_count)});
 }
 
 int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
@@ -1240,7 +1242,8 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
     if (plan.ok)
       return cuda_status(mx::launch_attend_rows(a, cache->d, shared, plan, static_cast<cudaStream_t>(stream)));
   }
-  return cuda_status(mx::launch_attend(a, cache->d, shared, h->attend_ctas[variant], static_cast<cudaStream_t>(stream)));
+  const int of_rows = static_cast<int64_t>(T) * a.group <= static_cast<int64_t>(B) * 8 ? variant + mx::kAttendVariants / 2 : variant;
+  return cuda_status(mx::launch_attend(a, of_rows, h->attend_ctas[of_rows], static_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------ chain without allocation

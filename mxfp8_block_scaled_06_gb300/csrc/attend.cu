@@ -2,18 +2,19 @@
 //
 //   out[r] = sum over visible t of softmax_t(scale q[r].k[t]) v[t]
 //
-// The rows of a kv head (its group of query heads, of each query token) fill the 16 rows
-// of mma.sync.m16n8k16, which reads its second operand from registers: the codes go from
-// shared memory through cvt.f16x2.e2m1x2 and one multiplication by their scale straight
-// into the products, without a stop in shared memory at 16 bits (for the 5th-generation
-// tensor cores the dequantized tile would have to be written and read there: at d = 512
-// 28 bytes of shared memory traffic for each byte of cache).
+// The rows of a kv head (its group of query heads, of each query token) are the 8 columns
+// of mma.sync.m16n8k16, once or twice, and the cache is its 16 rows: tokens for the scores, dimensions
+// for the sums. That operand comes from registers: the codes go from shared memory through
+// cvt.f16x2.e2m1x2 and one multiplication by their scale straight into the products, without a
+// stop in shared memory at 16 bits (for the 5th-generation tensor cores the dequantized
+// tile would have to be written and read there: at d = 512 28 bytes of shared memory
+// traffic for each byte of cache).
 //
 // In 16 bits. fp16 holds what is multiplied, under powers of two that keep all rounding
 // out but where it says so:
-//   keys    code * 2^(s - S + 7), s the block's scale and S the row's largest: exact down
-//           to S - 30, nothing below S - 31 (2^-31 of the row's largest block); the score
-//           takes 2^(S - 7) back in float32. Values the same.
+//   keys    code * 2^(s - S + 13), s the block's scale and S the row's largest: exact down
+//           to 2^-27 of the row's largest block, nothing below; the score takes 2^(S - 13)
+//           back in float32. Values the same.
 //   queries times the power of two that brings the row's largest into [2^14, 2^15):
 //           exact down to 2^-31 of it.
 //   weights p = exp2(x + S_v - u + 8) rounded to fp16 (11 bits, where a bf16 weight would
@@ -21,11 +22,19 @@
 //           x + S_v. So what is rounded, and below 2^-22 of the largest loses bits, is a
 //           token's contribution, not its weight. The weights' sum is of float32 exponentials.
 //
-// Tokens go by in tiles of 128, 32 to each of four warps, through a ring filled by
-// 16-byte asynchronous copies. Up to d = 128 a warp is on its own: it keeps the queries
-// and its sums in registers, and four warps' results are joined at the end. Above, a
-// warp computes the scores of its 32 tokens, hands the weights on through shared memory,
-// and sums a quarter of the dimensions over all 128.
+// The maxima m (of x) and u are only moved when a score goes beyond them by 2^24, or a
+// contribution by 2^7: then the sums are scaled anew, otherwise nothing is.
+//
+// Tokens go by in tiles of 128, 32 to each of four warps, through a ring filled by bulk
+// copies. Up to d = 128 a warp is on its own: it keeps the queries and its sums in registers,
+// and four warps' results are joined at the end. Above, a warp computes the scores of its
+// 32 tokens, hands the weights on through shared memory, and sums a quarter of the
+// dimensions over all 128, with one barrier a tile.
+//
+// Which element of a row is which column of an operand is free as long as both operands have
+// it the same, so a thread loads 16 bytes of a key row (a whole block: one scale) and 8 of
+// a value row at once. Place n of eight tokens is token n ^ (n / 2 & 1), which
+// spreads the rows that a warp reads over the banks.
 //
 // The work of all sequences is cut into equal runs of tiles, one for each resident CTA,
 // whatever the lengths; a run may end within a sequence. What a CTA has of a unit
@@ -46,8 +55,11 @@ constexpr int kWarps = 4;
 constexpr int kSub = 32;                 // tokens of a warp's part of a tile
 constexpr int kTile = kWarps * kSub;
 static_assert(kTile == kAttendTile, "tiles of the sequences' work");
-constexpr float kWeightBits = 8.f;       // weights are up to 2^8, scales up to 2^7
-constexpr float kSumBits = 15.f;
+constexpr int kScaleBits = 13;           // 6 * 2^13 < 65504
+constexpr float kWeightBits = 8.f;       // weights are up to 2^8 when u is the maximum,
+constexpr float kLagU = 7.f;             // and 2^15 before it is moved
+constexpr float kLagM = 24.f;
+constexpr float kSumBits = kScaleBits + kWeightBits;
 
 // ------------------------------------------------------------- the work
 __device__ __forceinline__ int64_t seq_work(const AttendArgs& a, const Seq& s) {
@@ -55,68 +67,74 @@ __device__ __forceinline__ int64_t seq_work(const AttendArgs& a, const Seq& s) {
 }
 
 struct Found {
-  int b;          // the sequence that holds the tile (B: none)
+  int b;          // the sequence that holds the tile
   int64_t first;  // number of its first tile
 };
 struct ScanShared {
   int64_t warp[kWarps];
-  int64_t total;
   Found found;
 };
-// Work of all sequences; every thread of the block gets it.
-__device__ int64_t total_work(const AttendArgs& a, ScanShared& sh, bool report) {
-  int64_t sum = 0;
-  bool bad = false;
-  for (int b = threadIdx.x; b < a.B; b += kThreads) {
-    const Seq s = seq_of(a, b);
-    sum += seq_work(a, s);
+// The work of kThreads sequences from c on, added up: this thread's sequence's, what is before it,
+// and all.
+template <int kRows>
+__device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh, int c, bool& bad, int64_t& before,
+                                             int64_t& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = c + threadIdx.x;
+  int64_t w = 0;
+  if (b < a.B) {
+    const Seq s = seq_of(a, b, kRows);
+    w = seq_work(a, s);
     bad |= s.bad;
   }
-  if (report && bad) atomicOr(a.status, kStatusBadInput);
+  int64_t sum = w;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) sh.warp[warp] = sum;
   __syncthreads();
-  sum = 0;
+  before = sum - w;
+  all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += sh.warp[w];
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) before += sh.warp[i];
+    all += sh.warp[i];
+  }
   __syncthreads();
-  return sum;
+  return w;
 }
-// The sequence that holds tile `index` of the work.
-__device__ Found find_work(const AttendArgs& a, ScanShared& sh, int64_t index) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) sh.found = Found{a.B, 0};
-  int64_t base = 0;
-  for (int c = 0; c < a.B && base <= index; c += kThreads) {
-    const int b = c + threadIdx.x;
-    const int64_t w = b < a.B ? seq_work(a, seq_of(a, b)) : 0;
-    int64_t sum = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += v;
+// Tiles of each CTA's run: an equal share.
+__device__ __forceinline__ int64_t run_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
+// All work, and the sequence in which the run of this CTA begins (where it has one).
+template <int kRows>
+__device__ Found find_run(const AttendArgs& a, ScanShared& sh, int64_t& total) {
+  bool bad = false;
+  int64_t before, all;
+  const int64_t w = scan_work<kRows>(a, sh, 0, bad, before, all);
+  total = all;
+  for (int c = kThreads; c < a.B; c += kThreads) {
+    int64_t x;
+    scan_work<kRows>(a, sh, c, bad, x, all);
+    total += all;
+  }
+  if (blockIdx.x == 0 && bad) atomicOr(a.status, kStatusBadInput);
+  const int64_t at = run_of(total, gridDim.x) * blockIdx.x;
+  if (before <= at && at < before + w) sh.found = Found{static_cast<int>(threadIdx.x), before};
+  if (a.B > kThreads) {
+    scan_work<kRows>(a, sh, 0, bad, before, all);
+    int64_t base = all;
+    for (int c = kThreads; c < a.B; c += kThreads, base += all) {
+      const int64_t v = scan_work<kRows>(a, sh, c, bad, before, all);
+      if (base + before <= at && at < base + before + v) sh.found = Found{c + static_cast<int>(threadIdx.x), base + before};
     }
-    if (lane == 31) sh.warp[warp] = sum;
-    __syncthreads();
-    int64_t before = base, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += sh.warp[i];
-      all += sh.warp[i];
-    }
-    if (before + sum - w <= index && index < before + sum) sh.found = Found{b, before + sum - w};
-    base += all;
-    __syncthreads();
   }
   __syncthreads();
   return sh.found;
 }
-// Tiles of each CTA's run.
-__device__ __forceinline__ int64_t run_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
 
-// A unit: 16 query rows of a kv head. Row i is query token (16 r + i) / group.
-struct Unit16 {
+// A unit: 8 or 16 query rows of a kv head, row i the query token (row0 + i) / group.
+struct AttendUnit {
   int head, row0, rows;  // rows: all of this sequence and head
   __device__ __forceinline__ bool row(const AttendArgs& a, const Seq& s, int i, int& token, int& q_head) const {
     const int r = row0 + i;
@@ -128,135 +146,250 @@ struct Unit16 {
 };
 
 // ------------------------------------------------------------- pieces
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Row t of a 16-token group lies at t * (d / 2), its 16-byte chunk c at c ^ flip(t): the
-// eight tokens {0..3, 8..11} of one chunk (scores) and the four tokens {0..3} of two
-// neighbouring chunks (sums), like those of the other halves, lie in 32 different banks.
-template <int D>
-__device__ __forceinline__ uint32_t flip(uint32_t t) {
-  const uint32_t b3 = (t >> 3) & 1u;
-  if constexpr (D == 64) return b3;
-  if constexpr (D == 128) return (t & 2u) | b3;
-  return ((t & 3u) << 1) | b3;
+// The 8 x 8 matrix of 16-bit elements that a warp holds, row lane / 4, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
+// Place n of eight tokens, and the other way round.
+__device__ __forceinline__ constexpr int place_of(int n) { return n ^ ((n >> 1) & 1); }
 
-// fp16 bits of 2^(s - top + 7) for scale byte s: 0 below 2^-24, NaN for byte 255.
+// fp16 bits of 2^(s - top + 13) for scale byte s <= top: 0 below 2^-14. NaN for byte 255.
 __device__ __forceinline__ uint32_t scale_f16(uint32_t s, int top) {
-  const int e = static_cast<int>(s) - top + 22;  // biased exponent
-  const uint32_t v = e >= 1 ? static_cast<uint32_t>(e) << 10 : e > -10 ? 1u << (9 + e) : 0u;
+  const uint32_t v = static_cast<uint32_t>(max(static_cast<int>(s) - top + 28, 0)) << 10;
   return s == 255u ? 0x7E00u : v;
 }
 
-template <int D, bool kShared>
+template <int D, bool kShared, int kRows>
 struct Layout {
   static constexpr bool kCoop = D > 128;
   static constexpr int kSides = kShared ? 1 : 2;
   static constexpr int kBlocks = D / 32;
-  static constexpr int kCodes = kSub * D / 2;       // bytes of a warp's part of a stage
+  // a row's distance: rows of whole 128 bytes are moved on by 16, so that two CTAs fit an SM (by
+  // 64, a key's loads of two rows would be free of bank conflicts)
+  static constexpr int kPitch = D <= 128 ? D / 2 : D / 2 + 16;
+  static constexpr int kCodes = kSub * kPitch;      // bytes of a warp's part of a stage
   static constexpr int kRaw = kSub * kBlocks;       // scale bytes
   static constexpr int kPart = kSides * (kCodes + kRaw);
-  static constexpr int kStages = kCoop ? 2 : 4;
+  static constexpr int kStages = kCoop ? 2 : kRows == 8 ? 3 : 4;
   static constexpr int kRing = kStages * kWarps * kPart;
-  // fp16 scales of a warp's 32 tokens, block after block: two groups of eight words
-  // {token i, token i + 8}, i in the order 0 4 1 5 2 6 3 7; 96 bytes apart, so that two
-  // neighbouring blocks' words lie in different banks
-  static constexpr int kScaleStride = 96;
-  static constexpr int kScales = kBlocks * kScaleStride;
-  static constexpr int kTokens = kSub * 8;  // {2^(S_k - 127), S_v - 127} of each token
-  static constexpr int kSide = kSides * kScales + kTokens;  // of a warp
-  static constexpr int kDump = kWarps * kAttendRows * (D + 4) * 4;
-  static constexpr int kQ = kCoop ? kAttendRows * D * 2 : 0;
-  static constexpr int kP = kCoop ? kTile / 16 * 512 : 0;
+  // Of each warp's 32 tokens: the keys' fp16 scales [token][block]; the values' [block][group of
+  // 16] in the order of the places, a pair of each half together, 80 bytes to a block, so that
+  // neighbouring blocks lie in different banks; {2^(S_k - 127), S_v - 127} [place].
+  static constexpr int kKeyScales = kSub * kBlocks * 2;
+  static constexpr int kValueStride = 80;
+  static constexpr int kValueScales = kBlocks * kValueStride;
+  static constexpr int kTokens = kSub * 8;
+  static constexpr int kBuffers = kCoop ? 2 : 1;    // of what other warps read
+  static constexpr int kSide = kKeyScales + kTokens + kBuffers * kValueScales;
+  static constexpr int kDump = kWarps * kRows * (D + 4) * 4;
+  static constexpr int kQ = kCoop ? kRows * D * 2 : 0;
+  static constexpr int kP = kCoop ? kTile / 16 * 32 * kRows : 0;
   static constexpr int kRingArea = !kCoop && kDump > kRing ? kDump : kRing;
   static constexpr int kOffSide = kRingArea;
   static constexpr int kOffQ = kOffSide + kWarps * kSide;
   static constexpr int kOffP = kOffQ + kQ;
-  static constexpr int kOffRows = kOffP + kP;                  // [warp][16] {max x, max x + S_v}, or {m, l}
-  static constexpr int kOffScale = kOffRows + kWarps * kAttendRows * 8;  // [16] row factors
-  static constexpr int kBytes = kOffScale + kAttendRows * 4;
+  static constexpr int kOffRows = kOffP + kBuffers * kP;                 // [warp][row] {max x, max x + S_v}, or {m, l}
+  static constexpr int kOffScale = kOffRows + kWarps * kRows * 8;  // [row] factors
+  static constexpr int kBytes = kOffScale + kRows * 4;
+  static constexpr int kCtas = D == 512 && !kShared ? 1 : D >= 256 ? 2 : kRows == 8 ? 4 : 3;  // of an SM, by shared memory
+};
+
+// What a unit that several runs have parts of is joined from: written by the CTA in whose
+// run the unit's first cut lies.
+struct Cut {
+  int first, last;  // CTAs; last < 0: nothing to do
+  int later;        // whether the first CTA's part is its second
+  int head, row0, rows, q0;
+  int pad;
 };
 
 // Floats of one CTA's part of a unit: the rows' maxima, sums, and weighted sums.
-template <int D>
-constexpr int kPartFloats = kAttendRows * (D + 2);
+template <int D, int kRows>
+constexpr int kPartFloats = kRows * (D + 2);
+__host__ __device__ constexpr size_t cut_bytes(int ctas) { return static_cast<size_t>(ctas) * sizeof(Cut); }
 
 // ------------------------------------------------------------- the kernel
-template <int D, bool kShared>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
-  using L = Layout<D, kShared>;
+template <int D, bool kShared, int kRows>
+__global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) attend_kernel(const AttendArgs a) {
+  using L = Layout<D, kShared, kRows>;
   constexpr bool kCoop = L::kCoop;
   constexpr int kBlocks = L::kBlocks;
   constexpr int kStages = L::kStages;
-  constexpr int kChunks = kCoop ? D / 64 / kWarps : D / 64;  // 64 dimensions each, of a warp's sums
+  constexpr int kSlices = D <= 128 ? 1 : D / 128;  // of the scores: a thread has 1, or half a, block of each
+  constexpr int kKeyWords = D == 64 ? 2 : 4;       // words of a key row's slice
+  constexpr int kWords = D == 64 || D == 256 ? 1 : 2;  // words of a value row: 8 dimensions each
+  constexpr int kN = kRows / 8;                    // tiles of rows
+  constexpr int kWide = 64 * kWords;               // dimensions of a warp's sums
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ ScanShared scan;
+  __shared__ uint64_t full[kWarps][kStages];
   const uint32_t base = smem_u32(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t side0 = base + L::kOffSide + warp * L::kSide;  // this warp's fp16 scales
-  const uint32_t tokens0 = side0 + L::kSides * L::kScales;
+  const uint32_t keys0 = base + L::kOffSide + warp * L::kSide;  // this warp's
+  const uint32_t tokens0 = keys0 + L::kKeyScales;
+  constexpr int kValues0 = L::kOffSide + L::kKeyScales + L::kTokens;  // the first warp's
   float2* rows_sh = reinterpret_cast<float2*>(smem + L::kOffRows);
   float* factor_sh = reinterpret_cast<float*>(smem + L::kOffScale);
+  // this warp's dimensions
+  const int wide0 = kCoop ? warp * kWide : 0;
 
+  pdl_launch_dependents();  // every CTA is resident: a dependent grid waits for none to start
+  if (lane < kStages) mbar_init(smem_u32(&full[warp][lane]), 1);
+  fence_mbar_init();
   pdl_wait();
-  const int64_t total = total_work(a, scan, blockIdx.x == 0);
+  int64_t total;
+  const Found found = find_run<kRows>(a, scan, total);
   const int64_t run = run_of(total, gridDim.x);
   int64_t at = run * blockIdx.x;
   const int64_t stop = min(at + run, total);
+  Cut* cuts = reinterpret_cast<Cut*>(a.partial);
+  float* parts0 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partial) + cut_bytes(gridDim.x));
   if (at >= stop) {
-    pdl_launch_dependents();
+    if (threadIdx.x == 0) cuts[blockIdx.x].last = -1;
     return;
   }
-  const Found found = find_work(a, scan, at);
   int b = found.b;
   int64_t seq_first = found.first;
-  Seq s = seq_of(a, b);
+  Seq s = seq_of(a, b, kRows);
+  uint32_t slot0 = 0;  // parts that this warp has taken through the ring
+  bool failed = false;
 
   while (at < stop) {
     while (at >= seq_first + seq_work(a, s)) {  // sequences without queries have no work
       seq_first += seq_work(a, s);
-      s = seq_of(a, ++b);
+      s = seq_of(a, ++b, kRows);
     }
     const int64_t in = at - seq_first;
     const int unit = static_cast<int>(in / s.tiles);
     const int tile0 = static_cast<int>(in - static_cast<int64_t>(unit) * s.tiles);
     const int tile1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), tile0 + (stop - at)));
     // a CTA has two parts of units at most: the one its run begins within, and a later one
-    const int part = at == run * blockIdx.x ? 0 : 1;
-    at += tile1 - tile0;
-    Unit16 un;
+    const bool begin = at == run * blockIdx.x;
+    AttendUnit un;
     un.head = unit / s.row_tiles;
-    un.row0 = (unit - un.head * s.row_tiles) * kAttendRows;
+    un.row0 = (unit - un.head * s.row_tiles) * kRows;
     un.rows = s.n * a.group;
+    if (begin && threadIdx.x == 0) {
+      Cut cut;
+      const int64_t first = at - tile0;
+      cut.first = static_cast<int>(first / run);
+      // the first cut of the unit: the run before does not begin within it
+      cut.last = tile0 > 0 && at - run <= first ? static_cast<int>((first + s.tiles - 1) / run) : -1;
+      cut.later = first != run * cut.first;
+      cut.head = un.head, cut.row0 = un.row0, cut.rows = un.rows, cut.q0 = s.q0;
+      cuts[blockIdx.x] = cut;
+    }
+    at += tile1 - tile0;
     const int t_begin = s.start + tile0 * kTile;
     const int t_end = min(s.start + tile1 * kTile, s.len);
+    const int parts = (t_end - t_begin + kTile - 1) / kTile;
 
-    // ---- queries and what each row sees
-    int lo[2], hi[2];
-    bool valid[2];
+    // ---- the ring: a warp's parts are tokens [t_begin + 32 (warp + 4 i), + 32)
+    int page_next[2];
+    const int* pages_of = a.table + static_cast<size_t>(b) * a.ld_table;
+    auto page_load = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      int token, q_head;
-      valid[r] = un.row(a, s, g + 8 * r, token, q_head);
-      const int pos = s.len - s.n + token - s.q0;
-      hi[r] = !valid[r] ? 0 : a.causal ? min(pos + 1, s.len) : s.len;
-      lo[r] = a.window > 0 ? pos - a.window + 1 : 0;
-    }
+      for (int j = 0; j < 2; ++j) {
+        const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
+        page_next[j] = -1;
+        if (t < t_end) page_next[j] = pages_of[div_u32(t >> 4, a.per_page)];
+      }
+    };
+    const size_t head_row = static_cast<size_t>(un.head) * a.page_size;
+    uint32_t live = 0;  // groups of 16 tokens that are there, two bits to a stage
+    // Rows behind the last token, and of a page outside the cache, are whatever lies there: their
+    // scales become 0, and any code is finite.
+    auto issue = [&](int i) {
+      if (i >= parts) return;
+      const uint32_t slot = (slot0 + i) % kStages;
+      const uint32_t to0 = base + (slot * kWarps + warp) * L::kPart, bar = smem_u32(&full[warp][slot]);
+      uint32_t here = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
+        if (static_cast<uint32_t>(page_next[j]) < static_cast<uint32_t>(a.pages))
+          here |= 1u << j;
+        else if (t < t_end && lane == 0)
+          atomicOr(a.status, kStatusBadInput);
+      }
+      live = (live & ~(3u << (2 * slot))) | here << (2 * slot);
+      if (lane == 0) mbar_expect_tx(bar, __popc(here) * L::kSides * 16 * (D / 2 + kBlocks));
+      __syncwarp();
+      // codes: a thread to a row where rows are padded, to a group of rows else
+      const int j = kCoop ? lane >> 4 : lane & 1;
+      const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
+      const uint32_t group = static_cast<uint32_t>(t) >> 4;
+      const int place = static_cast<int>(group - div_u32(group, a.per_page) * (a.page_size >> 4)) << 4;
+      const int64_t page = page_next[j];
+      const size_t row = head_row + place;
+      const uint64_t policy = policy_evict_first();
+      if (here >> j & 1u) {
+        if constexpr (kCoop) {
+#pragma unroll
+          for (int sd = 0; sd < L::kSides; ++sd)
+            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
+                      (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + (row + (lane & 15)) * (D / 2), D / 2, bar, policy);
+          if ((lane & 15) < L::kSides) {
+            const int sd = lane & 15;
+            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + L::kCodes + j * 16 * kBlocks,
+                      (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
+                      16 * kBlocks, bar, policy);
+          }
+        } else if (lane < 4 * L::kSides) {
+          const int sd = (lane >> 1) & (L::kSides - 1);
+          const uint32_t to = to0 + sd * (L::kCodes + L::kRaw);
+          if (lane < 2 * L::kSides)
+            bulk_load(to + j * 16 * L::kPitch, (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2), 8 * D,
+                      bar, policy);
+          else
+            bulk_load(to + L::kCodes + j * 16 * kBlocks,
+                      (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
+                      16 * kBlocks, bar, policy);
+        }
+      }
+    };
+    page_load(0);
+
+    // ---- queries and what each row sees: this thread's score columns are rows 8 n + 2 c and the next
+    int lo[kN][2], hi[kN][2], lo_most = 0, hi_least = s.len;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int token, q_head;
+        const bool valid = un.row(a, s, 8 * n + 2 * c + e, token, q_head);
+        const int pos = s.len - s.n + token - s.q0;
+        hi[n][e] = !valid ? 0 : min(a.causal ? min(pos + 1, s.len) : s.len, t_end);
+        lo[n][e] = a.window > 0 ? pos - a.window + 1 : 0;
+        // rows that are none see nothing, and nobody looks at them
+        if (valid) lo_most = max(lo_most, lo[n][e]), hi_least = min(hi_least, hi[n][e]);
+      }
     // whether a tile may hold tokens that not every row sees
     const bool masked = a.window > 0 || (a.causal && s.n > 1);
-    uint32_t qf[kCoop ? 1 : kBlocks][2][4];
-    float factor[2];
-    if constexpr (kCoop) {
-      __syncthreads();  // the previous unit's queries are read
+    uint32_t qf[kCoop ? 1 : kKeyWords][kN][4];  // [word][row 8 n + g][two dimensions]
+    float factor[kN][2];
+    fence_proxy_async_smem();  // what lay in the ring meanwhile is written over by copies
+    __syncthreads();           // the previous unit's queries are read, and its results
 #pragma unroll
-      for (int i = 0; i < kAttendRows / kWarps; ++i) {
-        const int r = warp * (kAttendRows / kWarps) + i;
+    for (int i = 0; i < kStages - 1; ++i) {
+      issue(i);
+      page_load(i + 1);
+    }
+    if constexpr (kCoop) {
+#pragma unroll
+      for (int i = 0; i < kRows / kWarps; ++i) {
+        const int r = warp * (kRows / kWarps) + i;
         int token, q_head;
         const bool ok = un.row(a, s, r, token, q_head);
         const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
@@ -267,32 +400,28 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
           v[j] = ok ? *reinterpret_cast<const uint4*>(q + (lane + 32 * j) * 8) : make_uint4(0, 0, 0, 0);
           most = max(most, max_bits(v[j]));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+        most = __reduce_max_sync(kFull, most);
         const int shift = query_shift(most, a.q_f16);
         const float f = pow2(shift);
 #pragma unroll
         for (int j = 0; j < D / 256; ++j) {
-          const int ch = lane + 32 * j;  // eight dimensions: block ch / 4, thread ch % 4 of a row's four
-          sts128(base + L::kOffQ + ((((ch >> 2) * 2 + (r >> 3)) * 32) + (r & 7) * 4 + (ch & 3)) * 16,
+          const int ch = lane + 32 * j;  // eight dimensions: slice ch / 16, thread's block ch / 4 % 4, word ch % 4
+          sts128(base + L::kOffQ + ((((ch >> 4) * 4 + (ch & 3)) * kN + (r >> 3)) * 32 + (r & 7) * 4 + ((ch >> 2) & 3)) * 16,
                  query_f16(v[j], a.q_f16, f));
         }
-        if (lane == 0) factor_sh[r] = pow2(-shift - 7) * a.scale_log2;
+        if (lane == 0) factor_sh[r] = pow2(-shift - kScaleBits) * a.scale_log2;
       }
-      __syncthreads();
-      factor[0] = factor_sh[g];
-      factor[1] = factor_sh[g + 8];
     } else {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int n = 0; n < kN; ++n) {
         int token, q_head;
-        const bool ok = un.row(a, s, g + 8 * r, token, q_head);
+        const bool ok = un.row(a, s, 8 * n + g, token, q_head);
         const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
-        uint4 v[kBlocks];
+        uint4 v[kKeyWords];
         uint32_t most = 0;
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-          v[j] = ok ? *reinterpret_cast<const uint4*>(q + 32 * j + 8 * c) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < kKeyWords; ++j) {
+          v[j] = ok ? *reinterpret_cast<const uint4*>(q + (c * kKeyWords + j) * 8) : make_uint4(0, 0, 0, 0);
           most = max(most, max_bits(v[j]));
         }
         most = max(most, __shfl_xor_sync(kFull, most, 1));
@@ -300,89 +429,51 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         const int shift = query_shift(most, a.q_f16);
         const float f = pow2(shift);
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
+        for (int j = 0; j < kKeyWords; ++j) {
           const uint4 w = query_f16(v[j], a.q_f16, f);
-          qf[j][r][0] = w.x, qf[j][r][1] = w.y, qf[j][r][2] = w.z, qf[j][r][3] = w.w;
+          qf[j][n][0] = w.x, qf[j][n][1] = w.y, qf[j][n][2] = w.z, qf[j][n][3] = w.w;
         }
-        factor[r] = pow2(-shift - 7) * a.scale_log2;
+        if (warp == 0 && c == 0) factor_sh[8 * n + g] = pow2(-shift - kScaleBits) * a.scale_log2;
       }
     }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      factor[n][0] = factor_sh[8 * n + 2 * c];
+      factor[n][1] = factor_sh[8 * n + 2 * c + 1];
+    }
 
-    // ---- the ring
-    // a warp's parts: tokens [t_begin + 32 (warp + 4 i), + 32)
-    const int parts = (t_end - t_begin + kTile - 1) / kTile;
-    int page_next[2];
-    auto page_load = [&](int i) {
+    // [rows' tile][16 dimensions: codes 2 t and 2 t + 1 of this thread's][code, row 2 c (+ 1)]
+    float acc[kN][4 * kWords][4];
+    float m[kN][2], u[kN][2], l[kN][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
-        page_next[j] = i < parts && t < t_end
-                           ? a.table[static_cast<size_t>(b) * a.ld_table + div_u32(t >> 4, a.per_page)]
-                           : -1;
-      }
-    };
-    auto issue = [&](int i) {
-      if (i < parts) {
-        const uint32_t stage = base + (i % kStages) * (kWarps * L::kPart) + warp * L::kPart;
+    for (int n = 0; n < kN; ++n) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
-          const bool here = t < t_end && page_next[j] >= 0 && page_next[j] < a.pages;
-          if (t < t_end && !here && lane == 0) atomicOr(a.status, kStatusBadInput);
-          const uint32_t place = ((t >> 4) - div_u32(t >> 4, a.per_page) * (a.page_size >> 4)) << 4;
-          const size_t row = here ? static_cast<size_t>(un.head) * a.page_size + place : 0;
-          const size_t page = here ? page_next[j] : 0;
+      for (int t = 0; t < 4 * kWords; ++t)
 #pragma unroll
-          for (int sd = 0; sd < L::kSides; ++sd) {
-            const uint8_t* codes = (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2);
-            const uint8_t* scales =
-                (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks;
-            const uint32_t to = stage + sd * (L::kCodes + L::kRaw);
+        for (int e = 0; e < 4; ++e) acc[n][t][e] = 0.f;
 #pragma unroll
-            for (int x = 0; x < kBlocks / 2; ++x) {  // 16 rows of kBlocks chunks
-              const int e = lane + 32 * x, r = e / kBlocks, ch = e % kBlocks;
-              cp_async_16(to + (16 * j + r) * (D / 2) + ((ch ^ flip<D>(r)) << 4), codes + e * 16,
-                          here && t + r < t_end ? 16u : 0u);
-            }
-            if (lane < kBlocks) cp_async_16(to + L::kCodes + j * 16 * kBlocks + lane * 16, scales + lane * 16, here ? 16u : 0u);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-
-    float acc[kChunks][8][4];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, u[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    page_load(0);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      issue(i);
-      page_load(i + 1);
+      for (int e = 0; e < 2; ++e) m[n][e] = u[n][e] = -INFINITY, l[n][e] = 0.f;
     }
 
     for (int i = 0; i < parts; ++i) {
-      cp_async_wait<kStages - 2>();
-      if constexpr (kCoop)
-        __syncthreads();
-      else
-        __syncwarp();
-      issue(i + kStages - 1);
-      page_load(i + kStages);
-      const uint32_t stage_all = base + (i % kStages) * (kWarps * L::kPart);
+      const uint32_t slot = (slot0 + i) % kStages;
+      if (!failed && !mbar_wait(smem_u32(&full[warp][slot]), ((slot0 + i) / kStages) & 1)) failed = true;
+      if constexpr (!kCoop) {
+        __syncwarp();  // the stage before is read
+        issue(i + kStages - 1);
+        page_load(i + kStages);
+      }
+      const uint32_t stage_all = base + slot * (kWarps * L::kPart);
       const uint32_t stage = stage_all + warp * L::kPart;
       const int t0 = t_begin + (warp + kWarps * i) * kSub;
+      const uint32_t values_all = base + kValues0 + (kCoop ? (i & 1) * L::kValueScales : 0);
 
       // ---- scales of token `lane`: fp16 relative to the row's largest, and that one
       bool nan_value = false;
       {
-        const bool here = t0 + lane < t_end;
+        const bool here = t0 + lane < t_end && (live >> (2 * slot + (lane >> 4)) & 1u);
+        const int col = place_of(lane & 7);  // (lane & 24) + col: the token's place
         float2 tok = make_float2(0.f, 0.f);
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) {
@@ -412,193 +503,294 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
           // a NaN among values that not every row sees must not meet the others' zero
           // weights: it is added to its own rows below
           const bool quiet = value && masked;
-          const uint32_t to = side0 + sd * L::kScales + (lane >> 4) * 32 + ((lane & 3) * 2 + ((lane >> 2) & 1)) * 4 +
-                              ((lane >> 3) & 1) * 2;
+          uint32_t f[kBlocks];
 #pragma unroll
           for (int k = 0; k < kBlocks; ++k) {
             const uint32_t x = (w[k / 4] >> (8 * (k % 4))) & 255;
-            sts16(to + k * L::kScaleStride, !here || (quiet && x == 255u) ? 0u : scale_f16(x, top));
+            f[k] = !here || (quiet && x == 255u) ? 0u : scale_f16(x, top);
           }
-          if (sd == 0) tok.x = __uint_as_float(max(static_cast<uint32_t>(top) << 23, 0x00400000u));
-          if (value) tok.y = static_cast<float>(top - 127);
+          if (sd == 0) {
+            const uint32_t to = keys0 + lane * kBlocks * 2;
+            uint32_t h[kBlocks / 2];
+#pragma unroll
+            for (int k = 0; k < kBlocks / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
+            if constexpr (kBlocks == 2)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(h[0]) : "memory");
+            else if constexpr (kBlocks == 4)
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
+            else
+#pragma unroll
+              for (int k = 0; k < kBlocks / 2; k += 4) sts128(to + k * 4, make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]));
+            tok.x = __uint_as_float(max(static_cast<uint32_t>(top) << 23, 0x00400000u));
+          }
+          if (value) {
+            const uint32_t to =
+                values_all + warp * L::kSide + (lane >> 4) * 32 + (col >> 1) * 8 + ((lane >> 3) & 1) * 4 + (col & 1) * 2;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) sts16(to + k * L::kValueStride, f[k]);
+            tok.y = static_cast<float>(top - 127);
+          }
         }
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + lane * 8), "f"(tok.x), "f"(tok.y) : "memory");
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + ((lane & 24) + col) * 8), "f"(tok.x), "f"(tok.y) : "memory");
       }
       __syncwarp();
 
       // ---- scores of this warp's tokens
-      float x[2][2][4];  // [group][n tile][row, token c + 4 n (+ 8)]
+      float x[2][kN][4];  // [group][rows' tile][token g, g + 8; row 2 c (+ 1)]
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[j][n][e] = 0.f;
-      {
-        // column n of the first (second) n tile is token n / 2 (+ 4) + 8 (n & 1)
-        const uint32_t row = (g >> 1) + 8 * (g & 1);
-        const uint32_t pick = (g & 1) ? 0x3232u : 0x1010u;
-#pragma unroll(kCoop ? 4 : kBlocks)
-        for (int k = 0; k < kBlocks; ++k) {
-          uint32_t qa[2][4];  // [kstep]
-          if constexpr (kCoop) {
-            const uint4 q0 = lds128(base + L::kOffQ + (k * 64 + lane) * 16);
-            const uint4 q1 = lds128(base + L::kOffQ + (k * 64 + 32 + lane) * 16);
-            qa[0][0] = q0.x, qa[0][1] = q1.x, qa[0][2] = q0.y, qa[0][3] = q1.y;
-            qa[1][0] = q0.z, qa[1][1] = q1.z, qa[1][2] = q0.w, qa[1][3] = q1.w;
-          } else {
+      const uint32_t key_at = stage + place_of(g) * L::kPitch + c * (kKeyWords * 4);
+      const uint32_t scale_at = keys0 + place_of(g) * kBlocks * 2 + (D == 64 ? c >> 1 : c) * 2;
+      constexpr int kAtOnce = kCoop ? 2 : 1;  // groups that share a load of the queries
+#pragma unroll 1
+      for (int k = 0; k < kSlices; ++k)
+#pragma unroll
+        for (int j0 = 0; j0 < 2; j0 += kAtOnce) {
+          uint32_t w[kAtOnce][2][kKeyWords], sc[kAtOnce][2];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              qa[h][0] = qf[k][0][2 * h], qa[h][1] = qf[k][1][2 * h];
-              qa[h][2] = qf[k][0][2 * h + 1], qa[h][3] = qf[k][1][2 * h + 1];
+              const uint32_t from = key_at + (16 * (j0 + j) + 8 * h) * L::kPitch + k * 64;
+              if constexpr (kKeyWords == 4) {
+                const uint4 v = lds128(from);
+                w[j][h][0] = v.x, w[j][h][1] = v.y, w[j][h][2] = v.z, w[j][h][3] = v.w;
+              } else {
+                const uint2 v = lds64(from);
+                w[j][h][0] = v.x, w[j][h][1] = v.y;
+              }
+              uint32_t f;
+              asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}"
+                           : "=r"(f)
+                           : "r"(scale_at + (16 * (j0 + j) + 8 * h) * kBlocks * 2 + k * 8));
+              sc[j][h] = f * 0x10001u;
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint2 sc = lds64(side0 + k * L::kScaleStride + j * 32 + (g >> 1) * 8);
+          for (int i = 0; i < kKeyWords; ++i) {
+            uint4 q[kN];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t t = row + 4 * n;
-              const uint32_t w = lds32(stage + (16 * j + t) * (D / 2) + ((k ^ flip<D>(t)) << 4) + 4 * c);
-              const uint32_t scale = __byte_perm(n ? sc.y : sc.x, 0, pick);
-              uint32_t r[4];
-              codes_f16(w, r);
+            for (int n = 0; n < kN; ++n) {
+              if constexpr (kCoop)
+                q[n] = lds128(base + L::kOffQ + (((k * 4 + i) * kN + n) * 32 + lane) * 16);
+              else
+                q[n] = make_uint4(qf[i][n][0], qf[i][n][1], qf[i][n][2], qf[i][n][3]);
+            }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) r[e] = mul_f16x2(r[e], scale);
-              mma_f16(x[j][n], qa[0], r[0], r[1]);
-              mma_f16(x[j][n], qa[1], r[2], r[3]);
+            for (int j = 0; j < kAtOnce; ++j) {
+              uint32_t r[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                codes_f16(w[j][h][i], r[h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[h][e] = mul_f16x2(r[h][e], sc[j][h]);
+              }
+#pragma unroll
+              for (int n = 0; n < kN; ++n) {
+                mma_f16(x[j0 + j][n], r[0][0], r[1][0], r[0][1], r[1][1], q[n].x, q[n].y);
+                mma_f16(x[j0 + j][n], r[0][2], r[1][2], r[0][3], r[1][3], q[n].z, q[n].w);
+              }
             }
           }
         }
-      }
 
       // ---- weights
-      float vs[2][2][2];  // S_v of the tokens
-      float mx[2] = {-INFINITY, -INFINITY}, ux[2] = {-INFINITY, -INFINITY};
+      float vs[2][2];  // S_v of tokens g and g + 8
+      float mx[kN][2], ux[kN][2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int h = 0; h < 2; ++h) {
+          const uint2 tk = lds64(tokens0 + (16 * j + 8 * h + g) * 8);
+          vs[j][h] = __uint_as_float(tk.y);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tl = 16 * j + c + 4 * n + 8 * e;
-            const uint2 tk = lds64(tokens0 + tl * 8);
-            const float kf = __uint_as_float(tk.x);
-            vs[j][n][e] = __uint_as_float(tk.y);
+          for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float& v = x[j][n][2 * r + e];
-              v = v * kf * factor[r];
-              const int t = t0 + tl;
-              if (t >= min(hi[r], t_end) || t < lo[r]) v = -INFINITY;
-              mx[r] = fmaxf(mx[r], v);
-              ux[r] = fmaxf(ux[r], v + vs[j][n][e]);
-            }
-          }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
-        ux[r] = fmaxf(ux[r], __shfl_xor_sync(kFull, ux[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
-        ux[r] = fmaxf(ux[r], __shfl_xor_sync(kFull, ux[r], 2));
-      }
-      if constexpr (kCoop) {
-        if (c == 0) {
-          rows_sh[warp * kAttendRows + g] = make_float2(mx[0], ux[0]);
-          rows_sh[warp * kAttendRows + g + 8] = make_float2(mx[1], ux[1]);
+            for (int e = 0; e < 2; ++e) x[j][n][2 * h + e] *= __uint_as_float(tk.x) * factor[n][e];
         }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 v = rows_sh[w * kAttendRows + g + 8 * r];
-            mx[r] = fmaxf(mx[r], v.x);
-            ux[r] = fmaxf(ux[r], v.y);
-          }
-      }
-      float shrink[2], mr[2], ur[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], m[r]);
-        ux[r] = fmaxf(ux[r], u[r]);
-        // a row that has seen nothing yet has no maximum to subtract
-        mr[r] = mx[r] == -INFINITY ? 0.f : mx[r];
-        ur[r] = ux[r] == -INFINITY ? 0.f : ux[r];
-        l[r] *= exp2_fast(m[r] - mr[r]);
-        shrink[r] = exp2_fast(u[r] - ur[r]);
-        m[r] = mx[r];
-        u[r] = ux[r];
-        ur[r] -= kWeightBits;
-      }
-      uint32_t p[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float v0 = x[j][n][2 * r], v1 = x[j][n][2 * r + 1];
-            l[r] += exp2_fast(v0 - mr[r]) + exp2_fast(v1 - mr[r]);
-            p[j][2 * n + r] = pack_f16(exp2_fast(v0 + vs[j][n][0] - ur[r]), exp2_fast(v1 + vs[j][n][1] - ur[r]));
-          }
-      if constexpr (kCoop) {
+      if (__any_sync(kFull, t0 < lo_most || t0 + kSub > hi_least)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          sts128(base + L::kOffP + ((warp * 2 + j) * 32 + lane) * 16, make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]));
-        __syncthreads();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = t0 + 16 * j + 8 * h + place_of(g);
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (t >= hi[n][e] || t < lo[n][e]) x[j][n][2 * h + e] = -INFINITY;
+          }
       }
-      if (__any_sync(kFull, shrink[0] != 1.f || shrink[1] != 1.f)) {
+      bool beyond = false;
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k)
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
+        for (int e = 0; e < 2; ++e) {
+          mx[n][e] = fmaxf(fmaxf(x[0][n][e], x[0][n][2 + e]), fmaxf(x[1][n][e], x[1][n][2 + e]));
+          ux[n][e] = fmaxf(fmaxf(x[0][n][e] + vs[0][0], x[0][n][2 + e] + vs[0][1]),
+                           fmaxf(x[1][n][e] + vs[1][0], x[1][n][2 + e] + vs[1][1]));
+          beyond |= mx[n][e] > m[n][e] + kLagM || ux[n][e] > u[n][e] + kLagU;
+        }
+      uint32_t p[2][kN][2];  // [group][rows' tile][tokens 2 c, 2 c + 1 of row g, of the first and the second eight]
+      float sum[kN][2];
+      auto weights = [&] {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[k][n][e] *= shrink[e >> 1];
+        for (int n = 0; n < kN; ++n) {
+          float mr[2], ur[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // a row that has seen nothing yet has no maximum to subtract
+            mr[e] = m[n][e] == -INFINITY ? 0.f : m[n][e];
+            ur[e] = (u[n][e] == -INFINITY ? 0.f : u[n][e]) - kWeightBits;
+            sum[n][e] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float w[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float v = x[j][n][2 * h + e];
+                sum[n][e] += exp2_fast(v - mr[e]);
+                w[e] = exp2_fast(v + vs[j][h] - ur[e]);
+              }
+              p[j][n][h] = transposed(pack_f16(w[0], w[1]));
+            }
+        }
+      };
+      auto hand_on = [&] {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t to = base + L::kOffP + (i & 1) * L::kP + ((warp * 2 + j) * 32 + lane) * (8 * kN);
+          if constexpr (kN == 2)
+            sts128(to, make_uint4(p[j][0][0], p[j][0][1], p[j][1][0], p[j][1][1]));
+          else
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(p[j][0][0]), "r"(p[j][0][1]) : "memory");
+        }
+      };
+      weights();
+      if constexpr (kCoop) {
+        hand_on();
+        beyond = __syncthreads_or(beyond || failed);
+      } else {
+        beyond = __any_sync(kFull, beyond);
+      }
+      if (beyond) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(kFull, mx[n][e], o));
+              ux[n][e] = fmaxf(ux[n][e], __shfl_xor_sync(kFull, ux[n][e], o));
+            }
+        if constexpr (kCoop) {
+          if (g == 0)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) rows_sh[warp * kRows + 8 * n + 2 * c + e] = make_float2(mx[n][e], ux[n][e]);
+          __syncthreads();
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w) {
+                const float2 v = rows_sh[w * kRows + 8 * n + 2 * c + e];
+                mx[n][e] = fmaxf(mx[n][e], v.x);
+                ux[n][e] = fmaxf(ux[n][e], v.y);
+              }
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[n][e] = fmaxf(mx[n][e], m[n][e]);
+            ux[n][e] = fmaxf(ux[n][e], u[n][e]);
+            l[n][e] *= exp2_fast(m[n][e] - (mx[n][e] == -INFINITY ? 0.f : mx[n][e]));
+            const float shrink = exp2_fast(u[n][e] - (ux[n][e] == -INFINITY ? 0.f : ux[n][e]));
+            m[n][e] = mx[n][e];
+            u[n][e] = ux[n][e];
+#pragma unroll
+            for (int t = 0; t < 4 * kWords; ++t) {
+              acc[n][t][e] *= shrink;
+              acc[n][t][2 + e] *= shrink;
+            }
+          }
+        weights();
+        if constexpr (kCoop) {
+          hand_on();
+          __syncthreads();
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        l[n][0] += sum[n][0];
+        l[n][1] += sum[n][1];
+      }
+      if constexpr (kCoop) {  // every warp has left the sums of the other stage
+        issue(i + 1);
+        page_load(i + 2);
       }
 
       // ---- weighted sums of the values
       constexpr int kGroups = kCoop ? kTile / 16 : 2;
 #pragma unroll(kCoop ? 2 : kGroups)
       for (int j = 0; j < kGroups; ++j) {
-        uint32_t pa[4];
+        uint32_t pb[kN][2];
         uint32_t from, sc_from;
         if constexpr (kCoop) {
-          const uint4 v = lds128(base + L::kOffP + (j * 32 + lane) * 16);
-          pa[0] = v.x, pa[1] = v.y, pa[2] = v.z, pa[3] = v.w;
-          from = stage_all + (j >> 1) * L::kPart + (j & 1) * 8 * D;
-          sc_from = base + L::kOffSide + (j >> 1) * L::kSide + (j & 1) * 32;
-        } else {
-          pa[0] = p[j][0], pa[1] = p[j][1], pa[2] = p[j][2], pa[3] = p[j][3];
-          from = stage + j * 8 * D;
-          sc_from = side0 + j * 32;
-        }
-        if constexpr (!kShared) {
-          from += L::kCodes + L::kRaw;
-          sc_from += L::kScales;
-        }
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int chunk = kCoop ? warp * kChunks + k : k;  // of 64 dimensions
-          const uint32_t ch = 2 * chunk + (g >> 2);          // the 32-block of this thread's eight
-          const uint2 sc = lds64(sc_from + ch * L::kScaleStride + c * 8);
-          uint32_t w[4];  // tokens c, c + 8, c + 4, c + 12
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t t = c + 8 * (e & 1) + 4 * (e >> 1);
-            w[e] = lds32(from + t * (D / 2) + ((ch ^ flip<D>(t)) << 4) + 4 * (g & 3));
+          const uint32_t p_at = base + L::kOffP + (i & 1) * L::kP + (j * 32 + lane) * (8 * kN);
+          if constexpr (kN == 2) {
+            const uint4 v = lds128(p_at);
+            pb[0][0] = v.x, pb[0][1] = v.y, pb[kN - 1][0] = v.z, pb[kN - 1][1] = v.w;
+          } else {
+            const uint2 v = lds64(p_at);
+            pb[0][0] = v.x, pb[0][1] = v.y;
           }
-          // a byte of one code of each of two tokens, codes 2 i and 2 i + 1
+          from = stage_all + (j >> 1) * L::kPart + (j & 1) * 16 * L::kPitch;
+          sc_from = values_all + (j >> 1) * L::kSide + (j & 1) * 32;
+        } else {
+#pragma unroll
+          for (int n = 0; n < kN; ++n) pb[n][0] = p[j][n][0], pb[n][1] = p[j][n][1];
+          from = stage + j * 16 * L::kPitch;
+          sc_from = values_all + warp * L::kSide + j * 32;
+        }
+        if constexpr (!kShared) from += L::kCodes + L::kRaw;
+        // this thread's dimensions: 8 kWords g on
+        const uint2 sc = lds64(sc_from + (wide0 / 32 + (kWords == 2 ? g >> 1 : g >> 2)) * L::kValueStride + c * 8);
+        uint32_t w[4][kWords];  // places 2 c, 2 c + 1, and 8 on
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t row_at = from + (place_of(2 * c + (e & 1)) + 8 * (e >> 1)) * L::kPitch + wide0 / 2 + g * 4 * kWords;
+          if constexpr (kWords == 2) {
+            const uint2 v = lds64(row_at);
+            w[e][0] = v.x, w[e][1] = v.y;
+          } else {
+            w[e][0] = lds32(row_at);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          // a byte of one code of each of two tokens, codes 2 t and 2 t + 1
           uint32_t ev[2][4], od[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            codes_f16((w[2 * h] & 0x0F0F0F0Fu) | ((w[2 * h + 1] << 4) & 0xF0F0F0F0u), ev[h]);
-            codes_f16(((w[2 * h] >> 4) & 0x0F0F0F0Fu) | (w[2 * h + 1] & 0xF0F0F0F0u), od[h]);
+            codes_f16((w[2 * h][k] & 0x0F0F0F0Fu) | ((w[2 * h + 1][k] << 4) & 0xF0F0F0F0u), ev[h]);
+            codes_f16(((w[2 * h][k] >> 4) & 0x0F0F0F0Fu) | (w[2 * h + 1][k] & 0xF0F0F0F0u), od[h]);
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            mma_f16(acc[k][2 * n], pa, mul_f16x2(ev[0][n], sc.x), mul_f16x2(ev[1][n], sc.y));
-            mma_f16(acc[k][2 * n + 1], pa, mul_f16x2(od[0][n], sc.x), mul_f16x2(od[1][n], sc.y));
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t a0 = mul_f16x2(ev[0][t], sc.x), a1 = mul_f16x2(od[0][t], sc.x);
+            const uint32_t a2 = mul_f16x2(ev[1][t], sc.y), a3 = mul_f16x2(od[1][t], sc.y);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) mma_f16(acc[n][4 * k + t], a0, a1, a2, a3, pb[n][0], pb[n][1]);
           }
         }
       }
@@ -615,111 +807,98 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
             bool row_nan = false;  // a shared row is a key as well: its score is NaN
             if constexpr (kShared)
               for (int k = 0; k < kBlocks; ++k) row_nan |= from[k] == 255;
+            // the block of this thread's sums
+            if (!row_nan && from[wide0 / 32 + (kWords == 2 ? g >> 1 : g >> 2)] != 255) continue;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (pos < lo[r] || pos >= hi[r]) continue;
-              if (row_nan) l[r] = NAN;
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-              for (int k = 0; k < kChunks; ++k) {
-                const int chunk = kCoop ? warp * kChunks + k : k;
-                if (!row_nan && from[2 * chunk + (c >> 1)] != 255) continue;
+              for (int e = 0; e < 2; ++e) {
+                if (pos < lo[n][e] || pos >= hi[n][e]) continue;
+                if (row_nan) l[n][e] = NAN;
 #pragma unroll
-                for (int n = 0; n < 8; ++n) acc[k][n][2 * r] = acc[k][n][2 * r + 1] = NAN;
+                for (int x = 0; x < 4 * kWords; ++x) acc[n][x][e] = acc[n][x][2 + e] = NAN;
               }
-            }
           }
         }
       }
     }
-    cp_async_wait<0>();
+    slot0 += parts;
 
     // ---- join the warps
     const bool whole = tile0 == 0 && tile1 == s.tiles;
+    // this thread has, of each of its rows, dimensions wide0 + 8 kWords g on
+    float to_m[kN][2];  // from sums relative to 2^(u + 21) to 2^m
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(kFull, l[r], 1);
-      l[r] += __shfl_xor_sync(kFull, l[r], 2);
-    }
-    float* part_out = a.partial + (static_cast<size_t>(blockIdx.x) * 2 + part) * kPartFloats<D>;
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(kFull, l[n][e], o);
+        to_m[n][e] = u[n][e] == -INFINITY ? 0.f : exp2f(u[n][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]) - kSumBits);
+      }
+    float* part_out = parts0 + (static_cast<size_t>(blockIdx.x) * 2 + (begin ? 0 : 1)) * kPartFloats<D, kRows>;
+    __syncthreads();  // all parts of the ring are read
+    if (g == 0)
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) rows_sh[warp * kRows + 8 * n + 2 * c + e] = make_float2(m[n][e], l[n][e]);
     if constexpr (kCoop) {
       __syncthreads();
-      if (c == 0) {
-        rows_sh[warp * kAttendRows + g] = make_float2(m[0], l[0]);
-        rows_sh[warp * kAttendRows + g + 8] = make_float2(m[1], l[1]);
-      }
-      __syncthreads();
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float sum = 0.f;
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += rows_sh[w * kAttendRows + g + 8 * r].y;
-        // sums relative to 2^(u + 15) -> to 2^m
-        const float f = u[r] == -INFINITY ? 0.f : exp2f(u[r] - (m[r] == -INFINITY ? 0.f : m[r]) - kSumBits);
-        int token, q_head;
-        const bool ok = un.row(a, s, g + 8 * r, token, q_head);
-        if (whole) {
-          if (!ok) continue;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * c + e;
+          float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            float v[16];
+          for (int w = 0; w < kWarps; ++w) sum += rows_sh[w * kRows + r].y;
+          int token, q_head;
+          const bool ok = un.row(a, s, r, token, q_head);
+          float v[8 * kWords];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) v[n] = acc[k][n][2 * r] * f, v[8 + n] = acc[k][n][2 * r + 1] * f;
-            uint4* to = reinterpret_cast<uint4*>(out + (warp * kChunks + k) * 64 + 16 * c);
-            to[0] = pack_out8(v, inv, a.q_f16);
-            to[1] = pack_out8(v + 8, inv, a.q_f16);
-          }
-          if (a.lse != nullptr && warp == 0 && c == 0)
-            a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (m[r] + log2f(sum)) * 0.6931471805599453f;
-        } else {
-          if (warp == 0 && c == 0) {
-            part_out[g + 8 * r] = m[r];
-            part_out[kAttendRows + g + 8 * r] = sum;
-          }
+          for (int t = 0; t < 4 * kWords; ++t) v[2 * t] = acc[n][t][e] * to_m[n][e], v[2 * t + 1] = acc[n][t][2 + e] * to_m[n][e];
+          if (whole) {
+            if (!ok) continue;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint4* to = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(token) * a.ldo +
+                                                 static_cast<size_t>(q_head) * a.ldo_head + wide0 + 8 * kWords * g);
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            float4* to = reinterpret_cast<float4*>(part_out + 2 * kAttendRows + (g + 8 * r) * D +
-                                                   (warp * kChunks + k) * 64 + 16 * c);
+            for (int t = 0; t < kWords; ++t) to[t] = pack_out8(v + 8 * t, inv, a.q_f16);
+            if (a.lse != nullptr && warp == 0 && g == 0)
+              a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (m[n][e] + log2f(sum)) * 0.6931471805599453f;
+          } else {
+            if (warp == 0 && g == 0) {
+              part_out[r] = m[n][e];
+              part_out[kRows + r] = sum;
+            }
+            float4* to = reinterpret_cast<float4*>(part_out + 2 * kRows + r * D + wide0 + 8 * kWords * g);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int n = 0; n < 8; n += 4)
-                to[h * 2 + n / 4] = make_float4(acc[k][n][2 * r + h] * f, acc[k][n + 1][2 * r + h] * f,
-                                                acc[k][n + 2][2 * r + h] * f, acc[k][n + 3][2 * r + h] * f);
+            for (int t = 0; t < 2 * kWords; ++t) to[t] = make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
           }
         }
-      }
     } else {
-      __syncthreads();  // all parts of the ring are read
-      if (c == 0) {
-        rows_sh[warp * kAttendRows + g] = make_float2(m[0], l[0]);
-        rows_sh[warp * kAttendRows + g + 8] = make_float2(m[1], l[1]);
-      }
-      float* dump = reinterpret_cast<float*>(smem) + warp * kAttendRows * (D + 4);
+      float* dump = reinterpret_cast<float*>(smem) + warp * kRows * (D + 4);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float f = u[r] == -INFINITY ? 0.f : exp2f(u[r] - (m[r] == -INFINITY ? 0.f : m[r]) - kSumBits);
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          float4* to = reinterpret_cast<float4*>(dump + (g + 8 * r) * (D + 4) + k * 64 + 16 * c);
+        for (int e = 0; e < 2; ++e) {
+          float4* to = reinterpret_cast<float4*>(dump + (8 * n + 2 * c + e) * (D + 4) + 8 * kWords * g);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int n = 0; n < 8; n += 4)
-              to[h * 2 + n / 4] = make_float4(acc[k][n][2 * r + h] * f, acc[k][n + 1][2 * r + h] * f,
-                                              acc[k][n + 2][2 * r + h] * f, acc[k][n + 3][2 * r + h] * f);
+          for (int t = 0; t < 4 * kWords; t += 2)
+            to[t / 2] = make_float4(acc[n][t][e] * to_m[n][e], acc[n][t][2 + e] * to_m[n][e], acc[n][t + 1][e] * to_m[n][e],
+                                    acc[n][t + 1][2 + e] * to_m[n][e]);
         }
-      }
       __syncthreads();
-      // eight threads to a row, eight dimensions of 64 at a time
-      const int r = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * 8;
+      // so many threads to a row, eight dimensions of each at a time
+      constexpr int kTeam = kThreads / kRows;
+      const int r = threadIdx.x / kTeam, e0 = threadIdx.x % kTeam * 8;
       float top = -INFINITY, sum = 0.f, f[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, rows_sh[w * kAttendRows + r].x);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, rows_sh[w * kRows + r].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 v = rows_sh[w * kAttendRows + r];
+        const float2 v = rows_sh[w * kRows + r];
         f[w] = v.x == -INFINITY ? (v.y != v.y ? v.y : 0.f) : exp2f(v.x - top);
         sum += v.y * f[w];
       }
@@ -727,12 +906,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
       const bool ok = un.row(a, s, r, token, q_head);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k) {
+      for (int d = e0; d < D; d += kTeam * 8) {
         float v[8] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float4* from = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                               (w * kAttendRows + r) * (D + 4) + k * 64 + e0);
+          const float4* from = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) + (w * kRows + r) * (D + 4) + d);
           const float4 y = from[0], z = from[1];
           v[0] += y.x * f[w], v[1] += y.y * f[w], v[2] += y.z * f[w], v[3] += y.w * f[w];
           v[4] += z.x * f[w], v[5] += z.y * f[w], v[6] += z.z * f[w], v[7] += z.w * f[w];
@@ -740,98 +918,106 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         if (whole) {
           if (ok)
             *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(token) * a.ldo +
-                                      static_cast<size_t>(q_head) * a.ldo_head + k * 64 + e0) =
-                pack_out8(v, inv, a.q_f16);
+                                      static_cast<size_t>(q_head) * a.ldo_head + d) = pack_out8(v, inv, a.q_f16);
         } else {
-          float4* to = reinterpret_cast<float4*>(part_out + 2 * kAttendRows + r * D + k * 64 + e0);
+          float4* to = reinterpret_cast<float4*>(part_out + 2 * kRows + r * D + d);
           to[0] = make_float4(v[0], v[1], v[2], v[3]);
           to[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
-      if ((threadIdx.x & 7) == 0) {
+      if (threadIdx.x % kTeam == 0) {
         if (!whole) {
           part_out[r] = top;
-          part_out[kAttendRows + r] = sum;
+          part_out[kRows + r] = sum;
         } else if (ok && a.lse != nullptr) {
           a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      __syncthreads();  // the dump lies in the ring
     }
   }
-  pdl_launch_dependents();
+  if (failed) atomicOr(a.status, kStatusTimeout);
 }
 
 // ------------------------------------------------------------- joining
-// Block (c, row): if the run of CTA c + 1 begins within a unit, and is the first that does,
-// the parts of that unit are added up for one row, in the order of the runs.
-template <int D>
-__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, int ctas) {
-  __shared__ ScanShared scan;
+// Block (c, y): the unit that is first cut where the run of CTA c + 1 begins, rows y, y + gridDim.y, ..;
+// its parts are added up by D / 4 threads to each share of them, in the order of the runs, and the
+// shares one after another.
+constexpr int kJoinThreads = 512;
+template <int D, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int ctas) {
+  constexpr int kEach = D / 4, kShares = kJoinThreads / kEach;
+  __shared__ float4 sums[kShares][kEach];
+  __shared__ float2 tops[kShares];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t total = total_work(a, scan, false);
-  const int64_t run = run_of(total, ctas);
-  const int64_t cut = run * (blockIdx.x + 1);
-  if (cut >= total) return;
-  const Found found = find_work(a, scan, cut);
-  const Seq s = seq_of(a, found.b);
-  const int64_t in = cut - found.first;
-  const int unit = static_cast<int>(in / s.tiles);
-  const int64_t first = found.first + static_cast<int64_t>(unit) * s.tiles;
-  if (first == cut || cut - run > first) return;
-  Unit16 un;
-  un.head = unit / s.row_tiles;
-  un.row0 = (unit - un.head * s.row_tiles) * kAttendRows;
-  un.rows = s.n * a.group;
-  const int r = blockIdx.y;
-  int token, q_head;
-  if (!un.row(a, s, r, token, q_head)) return;
-  const int c0 = static_cast<int>(first / run), c1 = static_cast<int>((first + s.tiles - 1) / run);
-  auto part = [&](int c) {
-    return a.partial + (static_cast<size_t>(c) * 2 + (c == c0 && first != run * c0 ? 1 : 0)) * kPartFloats<D>;
+  const Cut cut = reinterpret_cast<const Cut*>(a.partial)[blockIdx.x + 1];
+  if (cut.last < 0) return;
+  const float* parts0 = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.partial) + cut_bytes(ctas));
+  const int share = threadIdx.x / kEach, e = threadIdx.x % kEach;
+  const int n = cut.last - cut.first + 1, each = (n + kShares - 1) / kShares;
+  const int p0 = min(share * each, n), p1 = min(p0 + each, n);
+  auto part = [&](int p) {
+    return parts0 + (static_cast<size_t>(cut.first + p) * 2 + (p == 0 ? cut.later : 0)) * kPartFloats<D, kRows>;
   };
-  float top = -INFINITY;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, part(c)[r]);
-  float sum = 0.f, v[(D + kThreads - 1) / kThreads] = {};
-  for (int c = c0; c <= c1; ++c) {
-    const float* p = part(c);
-    const float m = p[r], l = p[kAttendRows + r];
-    const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - top);
-    sum += l * f;
-#pragma unroll
-    for (int i = 0; i < (D + kThreads - 1) / kThreads; ++i) {
-      const int d = threadIdx.x + i * kThreads;
-      if (d < D) v[i] += p[2 * kAttendRows + r * D + d] * f;
+  for (int r = blockIdx.y; r < kRows && cut.row0 + r < cut.rows; r += gridDim.y) {
+    float top = -INFINITY, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = p0; p < p1; ++p) top = fmaxf(top, part(p)[r]);
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) {
+      const float* x = part(p);
+      const float m = x[r], l = x[kRows + r];
+      const float4 y = *reinterpret_cast<const float4*>(x + 2 * kRows + r * D + 4 * e);
+      const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - top);
+      sum += l * f;
+      v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
     }
+    sums[share][e] = v;
+    if (e == 0) tops[share] = make_float2(top, sum);
+    __syncthreads();
+    if (share == 0) {
+      const int shares = (n + each - 1) / each;
+      for (int i = 1; i < shares; ++i) top = fmaxf(top, tops[i].x);
+      sum = 0.f;
+      v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < shares; ++i) {
+        const float2 t = tops[i];
+        const float4 y = sums[i][e];
+        const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2f(t.x - top);
+        sum += t.y * f;
+        v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int q_row = cut.row0 + r, q_token = q_row / a.group, token = cut.q0 + q_token;
+      const int q_head = cut.head * a.group + q_row - q_token * a.group;
+      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + 4 * e) =
+          make_uint2(pack_out(v.x * inv, v.y * inv, a.q_f16), pack_out(v.z * inv, v.w * inv, a.q_f16));
+      if (a.lse != nullptr && e == 0)
+        a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
-#pragma unroll
-  for (int i = 0; i < (D + kThreads - 1) / kThreads; ++i) {
-    const int d = threadIdx.x + i * kThreads;
-    if (d < D) out[d] = static_cast<uint16_t>(pack_out(v[i] * inv, 0.f, a.q_f16));
-  }
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// f(kernel, join kernel, shared bytes) of a variant.
+// f(kernel, join kernel, shared bytes, rows of a unit) of a variant.
 template <int D, bool kShared, typename F>
-auto with_kernels(F&& f) {
-  return f(attend_kernel<D, kShared>, attend_join_kernel<D>, Layout<D, kShared>::kBytes);
+auto with_kernels(bool few, F&& f) {
+  return few ? f(attend_kernel<D, kShared, 8>, attend_join_kernel<D, 8>, Layout<D, kShared, 8>::kBytes, 8)
+             : f(attend_kernel<D, kShared, 16>, attend_join_kernel<D, 16>, Layout<D, kShared, 16>::kBytes, 16);
 }
 template <typename F>
 auto with_variant(int v, F&& f) {
-  switch (v) {
-    case 0: return with_kernels<64, false>(f);
-    case 1: return with_kernels<64, true>(f);
-    case 2: return with_kernels<128, false>(f);
-    case 3: return with_kernels<128, true>(f);
-    case 4: return with_kernels<256, false>(f);
-    case 5: return with_kernels<256, true>(f);
-    case 6: return with_kernels<512, false>(f);
-    default: return with_kernels<512, true>(f);
+  const bool few = v >= kAttendVariants / 2;  // 8 rows
+  switch (v % (kAttendVariants / 2)) {
+    case 0: return with_kernels<64, false>(few, f);
+    case 1: return with_kernels<64, true>(few, f);
+    case 2: return with_kernels<128, false>(few, f);
+    case 3: return with_kernels<128, true>(few, f);
+    case 4: return with_kernels<256, false>(few, f);
+    case 5: return with_kernels<256, true>(few, f);
+    case 6: return with_kernels<512, false>(few, f);
+    default: return with_kernels<512, true>(few, f);
   }
 }
 
@@ -844,7 +1030,7 @@ int attend_variant(int d, bool shared) {
 
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]) {
   for (int v = 0; v < kAttendVariants; ++v) {
-    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes) {
+    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int) {
       cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       int n = 0;
       if (rc == cudaSuccess) rc = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, bytes);
@@ -856,10 +1042,12 @@ cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]) {
   return cudaSuccess;
 }
 
-size_t attend_bytes(int d, int ctas) { return static_cast<size_t>(ctas) * 2 * kAttendRows * (d + 2) * sizeof(float); }
+size_t attend_bytes(int d, int ctas, int rows) {
+  return cut_bytes(ctas) + static_cast<size_t>(ctas) * 2 * rows * (d + 2) * sizeof(float);
+}
 
-cudaError_t launch_attend(const AttendArgs& a, int d, bool shared, int ctas, cudaStream_t stream) {
-  return with_variant(attend_variant(d, shared), [&](auto kernel, auto join, int bytes) {
+cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream_t stream) {
+  return with_variant(variant, [&](auto kernel, auto join, int bytes, int rows) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -872,7 +1060,10 @@ cudaError_t launch_attend(const AttendArgs& a, int d, bool shared, int ctas, cud
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || ctas < 2) return e;
-    cfg.gridDim = dim3(ctas - 1, kAttendRows);
+    // the fewer units there are, the more parts each has, and the more blocks share its rows
+    const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(a.T) * a.group / rows) * a.heads;
+    cfg.gridDim = dim3(ctas - 1, static_cast<uint32_t>(std::min<int64_t>(rows, std::max<int64_t>(1, ctas / units))));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join, a, ctas);
   });

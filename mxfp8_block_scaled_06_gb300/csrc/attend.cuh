@@ -20,7 +20,8 @@ struct Seq {
   int row_tiles;
   bool bad;
 };
-__device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b) {
+// rows: of a unit.
+__device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b, int rows) {
   Seq s;
   int q1;
   if (a.q_offsets != nullptr) {
@@ -39,7 +40,7 @@ __device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b) {
   const int64_t first = static_cast<int64_t>(s.len) - s.n - a.window + 1;
   s.start = a.window > 0 && first > 0 ? min(static_cast<int>(first), s.len) & ~15 : 0;
   s.tiles = max((s.len - s.start + kAttendTile - 1) / kAttendTile, 1);
-  s.row_tiles = (s.n * a.group + kAttendRows - 1) / kAttendRows;
+  s.row_tiles = (s.n * a.group + rows - 1) / rows;
   return s;
 }
 // The four bytes of w, two codes each, as fp16 pairs (low code in the low half).

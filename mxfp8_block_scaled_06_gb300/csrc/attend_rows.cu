@@ -107,7 +107,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+// a * b, as a * b - 0: a product and a sum would be fused to one operation.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  const float2 c = make_float2(-0.f, -0.f);
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;"
       : "=l"(d)
@@ -140,7 +142,7 @@ struct Shared {
 // first; by one warp.
 __device__ void find_block(const AttendArgs& a, int per_block, int index, Shared& sh) {
   const int lane = threadIdx.x & 31;
-  auto blocks_of = [&](int b) { return b < a.B ? (seq_of(a, b).n * a.group + per_block - 1) / per_block : 0; };
+  auto blocks_of = [&](int b) { return b < a.B ? (seq_of(a, b, kRows).n * a.group + per_block - 1) / per_block : 0; };
   int sum = 0;
   for (int b = lane; b < a.B; b += 32) sum += blocks_of(b);
 #pragma unroll
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
   if (warp == 0) {
     if (blockIdx.x == 0) {
       bool bad = false;
-      for (int b = lane; b < a.B; b += 32) bad |= seq_of(a, b).bad;
+      for (int b = lane; b < a.B; b += 32) bad |= seq_of(a, b, kRows).bad;
       if (bad) atomicOr(a.status, kStatusBadInput);
     }
     find_block(a, kTiles * kRows, index, sh);
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
   Seq s = {};
   int row0 = 0, rows = 0, t_first = 0, tiles = 0;
   if (work) {
-    s = seq_of(a, b);
+    s = seq_of(a, b, kRows);
     rows = s.n * a.group;
     row0 = sh.row_block * (kTiles * kRows);
     // tokens that any row of the block sees
@@ -359,7 +361,10 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              float2 x = fma_f32x2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2, sub2);
+              // (the product rounded like the maximum's: fused, it would be off from that by up to half a
+              // step, which is 64 where scores reach 2^30)
+              float2 x = mul_f32x2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2);
+              x = add_f32x2(x, sub2);
               x.x = exp2_fast(x.x);
               x.y = exp2_fast(x.y);
               sum = add_f32x2(sum, x);
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const AttendArgs 
   if (warp == 0) find_block(a, kRowsOfBlock, index, sh);
   __syncthreads();
   if (sh.b < 0) return;
-  const Seq s = seq_of(a, sh.b);
+  const Seq s = seq_of(a, sh.b, kRows);
   const int rows = s.n * a.group;
   const int i = blockIdx.y * 8 + warp, r = sh.row_block * kRowsOfBlock + i;
   if (r >= rows) return;

@@ -411,13 +411,13 @@ struct AttendArgs {
   float* partial;
   int* status;
 };
-// Kernel variants of few query rows: head dims 64, 128, 256, 512, values apart or shared.
-constexpr int kAttendVariants = 8;
-constexpr int kAttendRows = 16;
-int attend_variant(int d, bool shared);  // -1: no such head dim
+// Kernel variants of few query rows: head dims 64, 128, 256, 512, values apart or shared, with units
+// of 16 rows, then the same with 8.
+constexpr int kAttendVariants = 16;
+int attend_variant(int d, bool shared);  // the one of 16 rows; -1: no such head dim
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]);
-size_t attend_bytes(int d, int ctas);
-cudaError_t launch_attend(const AttendArgs& args, int d, bool shared, int ctas, cudaStream_t stream);
+size_t attend_bytes(int d, int ctas, int rows);
+cudaError_t launch_attend(const AttendArgs& args, int variant, int ctas, cudaStream_t stream);
 // Many query rows (head dims up to 256): blocks of rows, and splits of their tokens.
 constexpr int kAttendRowsVariants = 6;
 struct AttendRowsPlan {

@@ -1,4 +1,5 @@
 """mx_attend of many query rows (prompts, drafts, wide groups) against the definition in 64 bits."""
+import numpy as np
 import pytest
 import torch
 
@@ -146,3 +147,17 @@ def test_wrong_pages_and_offsets_are_reported(mx):  # noqa: F811
     for offsets in ([0, 100, 191], [0, 150, 90], [-1, 100, 190]):
         mx.mx_attend(c.h, c.q, c.cache, c.table, c.len_t, q_offsets=torch.tensor(offsets, dtype=torch.int32, device=dev()))
         assert mx.mx_device_status(c.h) == mx.MX_ERR_INVALID_ARG
+
+
+def test_scores_of_any_size(mx):  # noqa: F811
+    """Scores of 2^40 in steps of 2^18: a weight is 1 or 0, and the largest score's own has to be 1."""
+    c = Case(mx, [140], [140], 2, 1, 64, False, seed=12, q_size=2.0**20, k_size=2.0**20)
+    out = c.run(causal=False)
+    k, v, q = c.rows("k", 0)[:, 0], c.rows("v", 0)[:, 0], c.q.double().cpu().numpy()
+    for j in range(2):
+        x = q[:, j] @ k.T
+        top = np.sort(x, 1)
+        sure = top[:, -1] - top[:, -2] > 2.0**24 * 64  # beyond any rounding of the scores
+        assert sure.sum() > 100
+        want = torch.from_numpy(v[x.argmax(1)]).bfloat16()
+        assert torch.equal(out[:, j].cpu()[torch.from_numpy(sure)], want[torch.from_numpy(sure)])
