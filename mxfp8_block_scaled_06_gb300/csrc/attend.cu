@@ -204,10 +204,9 @@ struct Layout {
   static constexpr int kCtas = D == 512 && !kShared ? 1 : D >= 256 ? 2 : kRows == 8 ? 4 : 3;  // of an SM, by shared memory
 };
 
-// What a unit that several runs have parts of is joined from: written by the CTA in whose
-// run the unit's first cut lies.
+// A cut of a unit: written by the CTA whose run begins there.
 struct Cut {
-  int first, last;  // CTAs; last < 0: nothing to do
+  int first, last;  // the CTAs that have parts of it; last < 0: the run does not begin within a unit
   int later;        // whether the first CTA's part is its second
   int head, row0, rows, q0;
   int pad;
@@ -284,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       Cut cut;
       const int64_t first = at - tile0;
       cut.first = static_cast<int>(first / run);
-      // the first cut of the unit: the run before does not begin within it
-      cut.last = tile0 > 0 && at - run <= first ? static_cast<int>((first + s.tiles - 1) / run) : -1;
+      cut.last = tile0 > 0 ? static_cast<int>((first + s.tiles - 1) / run) : -1;
       cut.later = first != run * cut.first;
       cut.head = un.head, cut.row0 = un.row0, cut.rows = un.rows, cut.q0 = s.q0;
       cuts[blockIdx.x] = cut;
@@ -939,64 +937,86 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
 }
 
 // ------------------------------------------------------------- joining
-// Block (c, y): the unit that is first cut where the run of CTA c + 1 begins, rows y, y + gridDim.y, ..;
-// its parts are added up by D / 4 threads to each share of them, in the order of the runs, and the
-// shares one after another.
-constexpr int kJoinThreads = 512;
+// Block c is that of the cut where the run of CTA c + 1 begins. A unit of n parts has n - 1 cuts, whose
+// blocks share its rows' pieces of 128 dimensions (64 at d = 64). A warp adds up a piece of
+// some parts in the order of the runs; where there are many, 2 to 8 warps share a piece.
+constexpr int kJoinThreads = 256;
 template <int D, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int ctas) {
-  constexpr int kEach = D / 4, kShares = kJoinThreads / kEach;
-  __shared__ float4 sums[kShares][kEach];
-  __shared__ float2 tops[kShares];
+  constexpr int kPiece = D < 128 ? D : 128, kVec = kPiece / 32;  // floats of a thread
+  constexpr int kPieces = kRows * D / kPiece, kWarpsHere = kJoinThreads / 32;
+  __shared__ float sums[kWarpsHere][kPiece];
+  __shared__ float2 tops[kWarpsHere];
   pdl_launch_dependents();
   pdl_wait();
   const Cut cut = reinterpret_cast<const Cut*>(a.partial)[blockIdx.x + 1];
   if (cut.last < 0) return;
   const float* parts0 = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.partial) + cut_bytes(ctas));
-  const int share = threadIdx.x / kEach, e = threadIdx.x % kEach;
-  const int n = cut.last - cut.first + 1, each = (n + kShares - 1) / kShares;
-  const int p0 = min(share * each, n), p1 = min(p0 + each, n);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = cut.last - cut.first + 1, blocks = n - 1, block = static_cast<int>(blockIdx.x) - cut.first;
+  const int team = n > 64 ? 8 : n > 32 ? 4 : n > 16 ? 2 : 1;  // warps to a piece
+  const int at_once = kWarpsHere / team, share = warp % team;
+  const int each = (n + team - 1) / team, p0 = min(share * each, n), p1 = min(p0 + each, n);
   auto part = [&](int p) {
     return parts0 + (static_cast<size_t>(cut.first + p) * 2 + (p == 0 ? cut.later : 0)) * kPartFloats<D, kRows>;
   };
-  for (int r = blockIdx.y; r < kRows && cut.row0 + r < cut.rows; r += gridDim.y) {
-    float top = -INFINITY, sum = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = p0; p < p1; ++p) top = fmaxf(top, part(p)[r]);
+  for (int x0 = block * at_once; x0 < kPieces; x0 += blocks * at_once) {
+    const int piece = x0 + warp / team, r = piece / (D / kPiece), d = piece % (D / kPiece) * kPiece + lane * kVec;
+    const bool here = piece < kPieces && cut.row0 + r < cut.rows;
+    float top = -INFINITY, sum = 0.f, v[kVec] = {};
+    if (here) {
 #pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-      const float* x = part(p);
-      const float m = x[r], l = x[kRows + r];
-      const float4 y = *reinterpret_cast<const float4*>(x + 2 * kRows + r * D + 4 * e);
-      const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - top);
-      sum += l * f;
-      v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
-    }
-    sums[share][e] = v;
-    if (e == 0) tops[share] = make_float2(top, sum);
-    __syncthreads();
-    if (share == 0) {
-      const int shares = (n + each - 1) / each;
-      for (int i = 1; i < shares; ++i) top = fmaxf(top, tops[i].x);
-      sum = 0.f;
-      v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < shares; ++i) {
-        const float2 t = tops[i];
-        const float4 y = sums[i][e];
-        const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2f(t.x - top);
-        sum += t.y * f;
-        v.x += y.x * f, v.y += y.y * f, v.z += y.z * f, v.w += y.w * f;
+      for (int p = p0; p < p1; ++p) {
+        const float* from = part(p);
+        const float m = from[r], l = from[kRows + r];
+        float y[kVec];
+        if constexpr (kVec == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(from + 2 * kRows + r * D + d);
+          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(from + 2 * kRows + r * D + d);
+          y[0] = z.x, y[1] = z.y;
+        }
+        const float most = fmaxf(top, m);
+        // a row that saw nothing yet, or here, adds nothing, or the NaN that it saw
+        const float keep = top == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(top - most);
+        const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - most);
+        sum = sum * keep + l * f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = v[e] * keep + y[e] * f;
+        top = most;
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int q_row = cut.row0 + r, q_token = q_row / a.group, token = cut.q0 + q_token;
-      const int q_head = cut.head * a.group + q_row - q_token * a.group;
-      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + 4 * e) =
-          make_uint2(pack_out(v.x * inv, v.y * inv, a.q_f16), pack_out(v.z * inv, v.w * inv, a.q_f16));
-      if (a.lse != nullptr && e == 0)
-        a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
     }
-    __syncthreads();
+    if (team > 1) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
+      if (lane == 0) tops[warp] = make_float2(top, sum);
+      __syncthreads();
+      if (share == 0) {
+        for (int i = 1; i < team; ++i) {
+          const float2 t = tops[warp + i];
+          const float most = fmaxf(top, t.x);
+          const float keep = top == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(top - most);
+          const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2f(t.x - most);
+          sum = sum * keep + t.y * f;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) v[e] = v[e] * keep + sums[warp + i][lane * kVec + e] * f;
+          top = most;
+        }
+      }
+      __syncthreads();
+    }
+    if (!here || share != 0) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int q_row = cut.row0 + r, q_token = q_row / a.group, token = cut.q0 + q_token;
+    const int q_head = cut.head * a.group + q_row - q_token * a.group;
+    uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + d;
+    if constexpr (kVec == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_out(v[0] * inv, v[1] * inv, a.q_f16), pack_out(v[2] * inv, v[3] * inv, a.q_f16));
+    else
+      *reinterpret_cast<uint32_t*>(out) = pack_out(v[0] * inv, v[1] * inv, a.q_f16);
+    if (a.lse != nullptr && d == 0)
+      a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -1048,6 +1068,10 @@ size_t attend_bytes(int d, int ctas, int rows) {
 
 cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream_t stream) {
   return with_variant(variant, [&](auto kernel, auto join, int bytes, int rows) {
+    // no more CTAs than tiles: every sequence has at most a block of rows more than its share
+    const int64_t tiles = (static_cast<int64_t>(a.table_cols) * a.page_size + 15 + kTile - 1) / kTile;
+    const int64_t units = (static_cast<int64_t>(a.T) * a.group / rows + std::min(a.B, a.T)) * a.heads;
+    ctas = static_cast<int>(std::min<int64_t>(ctas, std::max<int64_t>(1, tiles) * units));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -1060,9 +1084,7 @@ cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e != cudaSuccess || ctas < 2) return e;
-    // the fewer units there are, the more parts each has, and the more blocks share its rows
-    const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(a.T) * a.group / rows) * a.heads;
-    cfg.gridDim = dim3(ctas - 1, static_cast<uint32_t>(std::min<int64_t>(rows, std::max<int64_t>(1, ctas / units))));
+    cfg.gridDim = dim3(ctas - 1);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join, a, ctas);
