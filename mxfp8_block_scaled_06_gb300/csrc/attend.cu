@@ -25,10 +25,10 @@
 // The maxima m (of x) and u are only moved when a score goes beyond them by 2^24, or a
 // contribution by 2^7: then the sums are scaled anew, otherwise nothing is.
 //
-// Tokens go by in tiles of 128, 32 to each of four warps, through a ring filled by bulk
-// copies. Up to d = 128 a warp is on its own: it keeps the queries and its sums in registers,
-// and four warps' results are joined at the end. Above, a warp computes the scores of its
-// 32 tokens, hands the weights on through shared memory, and sums a quarter of the
+// Tokens go by in tiles of 128, an equal part to each of four warps (eight at d = 512), through a
+// ring filled by bulk copies. Up to d = 128 a warp is on its own: it keeps the queries and its
+// sums in registers, and four warps' results are joined at the end. Above, a warp computes the
+// scores of its tokens, hands the weights on through shared memory, and sums its share of the
 // dimensions over all 128, with one barrier a tile.
 //
 // Which element of a row is which column of an operand is free as long as both operands have
@@ -50,11 +50,7 @@
 namespace mx {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
-constexpr int kSub = 32;                 // tokens of a warp's part of a tile
-constexpr int kTile = kWarps * kSub;
-static_assert(kTile == kAttendTile, "tiles of the sequences' work");
+constexpr int kTile = kAttendTile;
 constexpr int kScaleBits = 13;           // 6 * 2^13 < 65504
 constexpr float kWeightBits = 8.f;       // weights are up to 2^8 when u is the maximum,
 constexpr float kLagU = 7.f;             // and 2^15 before it is moved
@@ -71,12 +67,12 @@ struct Found {
   int64_t first;  // number of its first tile
 };
 struct ScanShared {
-  int64_t warp[kWarps];
+  int64_t warp[8];
   Found found;
 };
-// The work of kThreads sequences from c on, added up: this thread's sequence's, what is before it,
+// The work of as many sequences as threads from c on, added up: this thread's sequence's, what is before it,
 // and all.
-template <int kRows>
+template <int kRows, int kWarps>
 __device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh, int c, bool& bad, int64_t& before,
                                              int64_t& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = c + threadIdx.x;
@@ -107,25 +103,26 @@ __device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh
 // Tiles of each CTA's run: an equal share.
 __device__ __forceinline__ int64_t run_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
 // All work, and the sequence in which the run of this CTA begins (where it has one).
-template <int kRows>
+template <int kRows, int kWarps>
 __device__ Found find_run(const AttendArgs& a, ScanShared& sh, int64_t& total) {
+  constexpr int kThreads = 32 * kWarps;
   bool bad = false;
   int64_t before, all;
-  const int64_t w = scan_work<kRows>(a, sh, 0, bad, before, all);
+  const int64_t w = scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
   total = all;
   for (int c = kThreads; c < a.B; c += kThreads) {
     int64_t x;
-    scan_work<kRows>(a, sh, c, bad, x, all);
+    scan_work<kRows, kWarps>(a, sh, c, bad, x, all);
     total += all;
   }
   if (blockIdx.x == 0 && bad) atomicOr(a.status, kStatusBadInput);
   const int64_t at = run_of(total, gridDim.x) * blockIdx.x;
   if (before <= at && at < before + w) sh.found = Found{static_cast<int>(threadIdx.x), before};
   if (a.B > kThreads) {
-    scan_work<kRows>(a, sh, 0, bad, before, all);
+    scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
     int64_t base = all;
     for (int c = kThreads; c < a.B; c += kThreads, base += all) {
-      const int64_t v = scan_work<kRows>(a, sh, c, bad, before, all);
+      const int64_t v = scan_work<kRows, kWarps>(a, sh, c, bad, before, all);
       if (base + before <= at && at < base + before + v) sh.found = Found{c + static_cast<int>(threadIdx.x), base + before};
     }
   }
@@ -172,6 +169,9 @@ __device__ __forceinline__ uint32_t scale_f16(uint32_t s, int top) {
 template <int D, bool kShared, int kRows>
 struct Layout {
   static constexpr bool kCoop = D > 128;
+  static constexpr int kWarps = D == 512 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kSub = kTile / kWarps;       // tokens of a warp's part of a tile
   static constexpr int kSides = kShared ? 1 : 2;
   static constexpr int kBlocks = D / 32;
   // a row's distance: rows of whole 128 bytes are moved on by 16, so that two CTAs fit an SM (by
@@ -182,11 +182,11 @@ struct Layout {
   static constexpr int kPart = kSides * (kCodes + kRaw);
   static constexpr int kStages = kCoop ? 2 : kRows == 8 ? 3 : 4;
   static constexpr int kRing = kStages * kWarps * kPart;
-  // Of each warp's 32 tokens: the keys' fp16 scales [token][block]; the values' [block][group of
-  // 16] in the order of the places, a pair of each half together, 80 bytes to a block, so that
+  // Of each warp's tokens: the keys' fp16 scales [token][block]; the values' [block][group of
+  // 16] in the order of the places, a pair of each half together, and some bytes more to a block, so that
   // neighbouring blocks lie in different banks; {2^(S_k - 127), S_v - 127} [place].
   static constexpr int kKeyScales = kSub * kBlocks * 2;
-  static constexpr int kValueStride = 80;
+  static constexpr int kValueStride = 2 * kSub + (kSub == 16 ? 8 : 16);
   static constexpr int kValueScales = kBlocks * kValueStride;
   static constexpr int kTokens = kSub * 8;
   static constexpr int kBuffers = kCoop ? 2 : 1;    // of what other warps read
@@ -201,7 +201,7 @@ struct Layout {
   static constexpr int kOffRows = kOffP + kBuffers * kP;                 // [warp][row] {max x, max x + S_v}, or {m, l}
   static constexpr int kOffScale = kOffRows + kWarps * kRows * 8;  // [row] factors
   static constexpr int kBytes = kOffScale + kRows * 4;
-  static constexpr int kCtas = D == 512 && !kShared ? 1 : D >= 256 ? 2 : kRows == 8 ? 4 : 3;  // of an SM, by shared memory
+  static constexpr int kCtas = D == 512 && !kShared ? 1 : D >= 256 ? 2 : kRows == 8 ? 4 : D == 128 ? 2 : 3;  // of an SM, by shared memory
 };
 
 // A cut of a unit: written by the CTA whose run begins there.
@@ -219,14 +219,15 @@ __host__ __device__ constexpr size_t cut_bytes(int ctas) { return static_cast<si
 
 // ------------------------------------------------------------- the kernel
 template <int D, bool kShared, int kRows>
-__global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D, kShared, kRows>::kCtas) attend_kernel(const AttendArgs a) {
   using L = Layout<D, kShared, kRows>;
   constexpr bool kCoop = L::kCoop;
   constexpr int kBlocks = L::kBlocks;
   constexpr int kStages = L::kStages;
+  constexpr int kWarps = L::kWarps, kSub = L::kSub, kOwn = kSub / 16;  // groups of 16 tokens of a warp
   constexpr int kSlices = D <= 128 ? 1 : D / 128;  // of the scores: a thread has 1, or half a, block of each
   constexpr int kKeyWords = D == 64 ? 2 : 4;       // words of a key row's slice
-  constexpr int kWords = D == 64 || D == 256 ? 1 : 2;  // words of a value row: 8 dimensions each
+  constexpr int kWords = D == 128 ? 2 : 1;  // words of a value row: 8 dimensions each
   constexpr int kN = kRows / 8;                    // tiles of rows
   constexpr int kWide = 64 * kWords;               // dimensions of a warp's sums
   extern __shared__ __align__(128) uint8_t smem[];
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
   fence_mbar_init();
   pdl_wait();
   int64_t total;
-  const Found found = find_run<kRows>(a, scan, total);
+  const Found found = find_run<kRows, kWarps>(a, scan, total);
   const int64_t run = run_of(total, gridDim.x);
   int64_t at = run * blockIdx.x;
   const int64_t stop = min(at + run, total);
@@ -293,12 +294,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
     const int t_end = min(s.start + tile1 * kTile, s.len);
     const int parts = (t_end - t_begin + kTile - 1) / kTile;
 
-    // ---- the ring: a warp's parts are tokens [t_begin + 32 (warp + 4 i), + 32)
-    int page_next[2];
+    // ---- the ring: a warp's part i is tokens [t_begin + kSub (warp + kWarps i), + kSub)
+    int page_next[kOwn];
     const int* pages_of = a.table + static_cast<size_t>(b) * a.ld_table;
     auto page_load = [&](int i) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kOwn; ++j) {
         const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
         page_next[j] = -1;
         if (t < t_end) page_next[j] = pages_of[div_u32(t >> 4, a.per_page)];
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       const uint32_t to0 = base + (slot * kWarps + warp) * L::kPart, bar = smem_u32(&full[warp][slot]);
       uint32_t here = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kOwn; ++j) {
         const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
         if (static_cast<uint32_t>(page_next[j]) < static_cast<uint32_t>(a.pages))
           here |= 1u << j;
@@ -325,21 +326,23 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       if (lane == 0) mbar_expect_tx(bar, __popc(here) * L::kSides * 16 * (D / 2 + kBlocks));
       __syncwarp();
       // codes: a thread to a row where rows are padded, to a group of rows else
-      const int j = kCoop ? lane >> 4 : lane & 1;
+      const int j = (kCoop ? lane >> 4 : lane) & (kOwn - 1);
       const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
       const uint32_t group = static_cast<uint32_t>(t) >> 4;
       const int place = static_cast<int>(group - div_u32(group, a.per_page) * (a.page_size >> 4)) << 4;
-      const int64_t page = page_next[j];
+      const int64_t page = kOwn == 1 ? page_next[0] : j ? page_next[kOwn - 1] : page_next[0];
       const size_t row = head_row + place;
       const uint64_t policy = policy_evict_first();
       if (here >> j & 1u) {
         if constexpr (kCoop) {
+          if (lane < kSub)
 #pragma unroll
-          for (int sd = 0; sd < L::kSides; ++sd)
-            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
+            for (int sd = 0; sd < L::kSides; ++sd)
+              bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
                       (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + (row + (lane & 15)) * (D / 2), D / 2, bar, policy);
-          if ((lane & 15) < L::kSides) {
-            const int sd = lane & 15;
+          // the scales by threads that have no row, or by the first of each group
+          const int sd = kOwn == 1 ? lane - 16 : lane & 15;
+          if (sd >= 0 && sd < L::kSides) {
             bulk_load(to0 + sd * (L::kCodes + L::kRaw) + L::kCodes + j * 16 * kBlocks,
                       (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
                       16 * kBlocks, bar, policy);
@@ -467,87 +470,89 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       const int t0 = t_begin + (warp + kWarps * i) * kSub;
       const uint32_t values_all = base + kValues0 + (kCoop ? (i & 1) * L::kValueScales : 0);
 
-      // ---- scales of token `lane`: fp16 relative to the row's largest, and that one
+      // ---- scales: fp16 relative to the row's largest, and that one. A thread has a token's, or where
+      // there are 16 tokens half of one's
+      constexpr int kMine = kBlocks * kSub / 32;
+      const int token = lane & (kSub - 1), first = kOwn == 1 ? (lane >> 4) * kMine : 0;
       bool nan_value = false;
       {
-        const bool here = t0 + lane < t_end && (live >> (2 * slot + (lane >> 4)) & 1u);
-        const int col = place_of(lane & 7);  // (lane & 24) + col: the token's place
+        const bool here = t0 + token < t_end && (live >> (2 * slot + (token >> 4)) & 1u);
+        const int col = place_of(token & 7);  // (token & 24) + col: the token's place
         float2 tok = make_float2(0.f, 0.f);
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) {
-          uint32_t w[(kBlocks + 3) / 4];
-          const uint32_t from = stage + sd * (L::kCodes + L::kRaw) + L::kCodes + lane * kBlocks;
-          if constexpr (kBlocks == 2) {
+          uint32_t w[(kMine + 3) / 4];
+          const uint32_t from = stage + sd * (L::kCodes + L::kRaw) + L::kCodes + token * kBlocks + first;
+          if constexpr (kMine == 2) {
             asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(w[0]) : "r"(from));
-          } else if constexpr (kBlocks == 4) {
+          } else if constexpr (kMine == 4) {
             w[0] = lds32(from);
-          } else if constexpr (kBlocks == 8) {
+          } else {
             const uint2 v = lds64(from);
             w[0] = v.x, w[1] = v.y;
-          } else {
-            const uint4 v = lds128(from);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
           }
           int top = 0;
           bool nan = false;
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
+          for (int k = 0; k < kMine; ++k) {
             const int x = (w[k / 4] >> (8 * (k % 4))) & 255;
             nan |= x == 255;
             top = max(top, x == 255 ? 0 : x);
           }
+          if constexpr (kOwn == 1) top = max(top, __shfl_xor_sync(kFull, top, 16));
           const bool value = sd == 1 || kShared;
           if (value) nan_value = nan && here;
           // a NaN among values that not every row sees must not meet the others' zero
           // weights: it is added to its own rows below
           const bool quiet = value && masked;
-          uint32_t f[kBlocks];
+          uint32_t f[kMine];
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
+          for (int k = 0; k < kMine; ++k) {
             const uint32_t x = (w[k / 4] >> (8 * (k % 4))) & 255;
             f[k] = !here || (quiet && x == 255u) ? 0u : scale_f16(x, top);
           }
           if (sd == 0) {
-            const uint32_t to = keys0 + lane * kBlocks * 2;
-            uint32_t h[kBlocks / 2];
+            const uint32_t to = keys0 + (token * kBlocks + first) * 2;
+            uint32_t h[kMine / 2];
 #pragma unroll
-            for (int k = 0; k < kBlocks / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
-            if constexpr (kBlocks == 2)
+            for (int k = 0; k < kMine / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
+            if constexpr (kMine == 2)
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(h[0]) : "memory");
-            else if constexpr (kBlocks == 4)
+            else if constexpr (kMine == 4)
               asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
             else
-#pragma unroll
-              for (int k = 0; k < kBlocks / 2; k += 4) sts128(to + k * 4, make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]));
+              sts128(to, make_uint4(h[0], h[1], h[2], h[3]));
             tok.x = __uint_as_float(max(static_cast<uint32_t>(top) << 23, 0x00400000u));
           }
           if (value) {
-            const uint32_t to =
-                values_all + warp * L::kSide + (lane >> 4) * 32 + (col >> 1) * 8 + ((lane >> 3) & 1) * 4 + (col & 1) * 2;
+            const uint32_t to = values_all + warp * L::kSide + first * L::kValueStride + (token >> 4) * 32 + (col >> 1) * 8 +
+                                ((token >> 3) & 1) * 4 + (col & 1) * 2;
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) sts16(to + k * L::kValueStride, f[k]);
+            for (int k = 0; k < kMine; ++k) sts16(to + k * L::kValueStride, f[k]);
             tok.y = static_cast<float>(top - 127);
           }
         }
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + ((lane & 24) + col) * 8), "f"(tok.x), "f"(tok.y) : "memory");
+        if (lane < kSub)
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + ((token & 24) + col) * 8), "f"(tok.x), "f"(tok.y)
+                       : "memory");
       }
       __syncwarp();
 
       // ---- scores of this warp's tokens
-      float x[2][kN][4];  // [group][rows' tile][token g, g + 8; row 2 c (+ 1)]
+      float x[kOwn][kN][4];  // [group][rows' tile][token g, g + 8; row 2 c (+ 1)]
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < kOwn; ++j)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[j][n][e] = 0.f;
       const uint32_t key_at = stage + place_of(g) * L::kPitch + c * (kKeyWords * 4);
       const uint32_t scale_at = keys0 + place_of(g) * kBlocks * 2 + (D == 64 ? c >> 1 : c) * 2;
-      constexpr int kAtOnce = kCoop ? 2 : 1;  // groups that share a load of the queries
+      constexpr int kAtOnce = kCoop ? kOwn : 1;  // groups that share a load of the queries
 #pragma unroll 1
       for (int k = 0; k < kSlices; ++k)
 #pragma unroll
-        for (int j0 = 0; j0 < 2; j0 += kAtOnce) {
+        for (int j0 = 0; j0 < kOwn; j0 += kAtOnce) {
           uint32_t w[kAtOnce][2][kKeyWords], sc[kAtOnce][2];
 #pragma unroll
           for (int j = 0; j < kAtOnce; ++j)
@@ -596,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
         }
 
       // ---- weights
-      float vs[2][2];  // S_v of tokens g and g + 8
+      float vs[kOwn][2];  // S_v of tokens g and g + 8
       float mx[kN][2], ux[kN][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < kOwn; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint2 tk = lds64(tokens0 + (16 * j + 8 * h + g) * 8);
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
         }
       if (__any_sync(kFull, t0 < lo_most || t0 + kSub > hi_least)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kOwn; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int t = t0 + 16 * j + 8 * h + place_of(g);
@@ -627,12 +632,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[n][e] = fmaxf(fmaxf(x[0][n][e], x[0][n][2 + e]), fmaxf(x[1][n][e], x[1][n][2 + e]));
-          ux[n][e] = fmaxf(fmaxf(x[0][n][e] + vs[0][0], x[0][n][2 + e] + vs[0][1]),
-                           fmaxf(x[1][n][e] + vs[1][0], x[1][n][2 + e] + vs[1][1]));
+          mx[n][e] = ux[n][e] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            mx[n][e] = fmaxf(mx[n][e], fmaxf(x[j][n][e], x[j][n][2 + e]));
+            ux[n][e] = fmaxf(ux[n][e], fmaxf(x[j][n][e] + vs[j][0], x[j][n][2 + e] + vs[j][1]));
+          }
           beyond |= mx[n][e] > m[n][e] + kLagM || ux[n][e] > u[n][e] + kLagU;
         }
-      uint32_t p[2][kN][2];  // [group][rows' tile][tokens 2 c, 2 c + 1 of row g, of the first and the second eight]
+      uint32_t p[kOwn][kN][2];  // [group][rows' tile][tokens 2 c, 2 c + 1 of row g, of the first and the second eight]
       float sum[kN][2];
       auto weights = [&] {
 #pragma unroll
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
             sum[n][e] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < kOwn; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float w[2];
@@ -662,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       };
       auto hand_on = [&] {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t to = base + L::kOffP + (i & 1) * L::kP + ((warp * 2 + j) * 32 + lane) * (8 * kN);
+        for (int j = 0; j < kOwn; ++j) {
+          const uint32_t to = base + L::kOffP + (i & 1) * L::kP + ((warp * kOwn + j) * 32 + lane) * (8 * kN);
           if constexpr (kN == 2)
             sts128(to, make_uint4(p[j][0][0], p[j][0][1], p[j][1][0], p[j][1][1]));
           else
@@ -738,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
       }
 
       // ---- weighted sums of the values
-      constexpr int kGroups = kCoop ? kTile / 16 : 2;
+      constexpr int kGroups = kCoop ? kTile / 16 : kOwn;
 #pragma unroll(kCoop ? 2 : kGroups)
       for (int j = 0; j < kGroups; ++j) {
         uint32_t pb[kN][2];
@@ -752,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
             const uint2 v = lds64(p_at);
             pb[0][0] = v.x, pb[0][1] = v.y;
           }
-          from = stage_all + (j >> 1) * L::kPart + (j & 1) * 16 * L::kPitch;
-          sc_from = values_all + (j >> 1) * L::kSide + (j & 1) * 32;
+          from = stage_all + j / kOwn * L::kPart + j % kOwn * 16 * L::kPitch;
+          sc_from = values_all + j / kOwn * L::kSide + j % kOwn * 32;
         } else {
 #pragma unroll
           for (int n = 0; n < kN; ++n) pb[n][0] = p[j][n][0], pb[n][1] = p[j][n][1];
@@ -798,8 +806,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
         if constexpr (kCoop) any = __syncthreads_or(any);
         if (any) {
           for (int t = 0; t < (kCoop ? kTile : kSub); ++t) {
-            const uint8_t* from = smem + ((kCoop ? stage_all + (t >> 5) * L::kPart : stage) - base) +
-                                  (kShared ? 0 : L::kCodes + L::kRaw) + L::kCodes + (t & 31) * kBlocks;
+            const uint8_t* from = smem + ((kCoop ? stage_all + t / kSub * L::kPart : stage) - base) +
+                                  (kShared ? 0 : L::kCodes + L::kRaw) + L::kCodes + t % kSub * kBlocks;
             const int pos = kCoop ? t_begin + i * kTile + t : t0 + t;
             if (pos >= t_end) break;
             bool row_nan = false;  // a shared row is a key as well: its score is NaN
@@ -889,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, kShared, kRows>::kCtas) at
         }
       __syncthreads();
       // so many threads to a row, eight dimensions of each at a time
-      constexpr int kTeam = kThreads / kRows;
+      constexpr int kTeam = L::kThreads / kRows;
       const int r = threadIdx.x / kTeam, e0 = threadIdx.x % kTeam * 8;
       float top = -INFINITY, sum = 0.f, f[kWarps];
 #pragma unroll
@@ -1020,11 +1028,13 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   }
 }
 
-// f(kernel, join kernel, shared bytes, rows of a unit) of a variant.
+// f(kernel, join kernel, shared bytes, threads, rows of a unit) of a variant.
 template <int D, bool kShared, typename F>
 auto with_kernels(bool few, F&& f) {
-  return few ? f(attend_kernel<D, kShared, 8>, attend_join_kernel<D, 8>, Layout<D, kShared, 8>::kBytes, 8)
-             : f(attend_kernel<D, kShared, 16>, attend_join_kernel<D, 16>, Layout<D, kShared, 16>::kBytes, 16);
+  return few ? f(attend_kernel<D, kShared, 8>, attend_join_kernel<D, 8>, Layout<D, kShared, 8>::kBytes,
+                 Layout<D, kShared, 8>::kThreads, 8)
+             : f(attend_kernel<D, kShared, 16>, attend_join_kernel<D, 16>, Layout<D, kShared, 16>::kBytes,
+                 Layout<D, kShared, 16>::kThreads, 16);
 }
 template <typename F>
 auto with_variant(int v, F&& f) {
@@ -1050,10 +1060,10 @@ int attend_variant(int d, bool shared) {
 
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]) {
   for (int v = 0; v < kAttendVariants; ++v) {
-    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int) {
+    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int threads, int) {
       cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       int n = 0;
-      if (rc == cudaSuccess) rc = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, bytes);
+      if (rc == cudaSuccess) rc = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, bytes);
       ctas[v] = n * sm_count;
       return rc == cudaSuccess && n < 1 ? cudaErrorInvalidConfiguration : rc;
     });
@@ -1067,14 +1077,14 @@ size_t attend_bytes(int d, int ctas, int rows) {
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream_t stream) {
-  return with_variant(variant, [&](auto kernel, auto join, int bytes, int rows) {
+  return with_variant(variant, [&](auto kernel, auto join, int bytes, int threads, int rows) {
     // no more CTAs than tiles: every sequence has at most a block of rows more than its share
     const int64_t tiles = (static_cast<int64_t>(a.table_cols) * a.page_size + 15 + kTile - 1) / kTile;
     const int64_t units = (static_cast<int64_t>(a.T) * a.group / rows + std::min(a.B, a.T)) * a.heads;
     ctas = static_cast<int>(std::min<int64_t>(ctas, std::max<int64_t>(1, tiles) * units));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
