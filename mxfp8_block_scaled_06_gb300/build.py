@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libmx.so")
 TIMELINE_LIB = os.path.join(HERE, "libmx_timeline.so")
 TIMELINE_BUILD = os.path.join(HERE, "_build_timeline")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "wo_a.cu", "chain.cu", "quantize_fp4.cu",
-           "gemm_fp4.cu", "route.cu", "rope.cu", "cache.cu", "attend.cu", "attend_rows.cu"]
+           "gemm_fp4.cu", "route.cu", "rope.cu", "cache.cu", "attend.cu", "attend_rows.cu",
+           "attend_latent.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -93,6 +93,8 @@ constexpr int kMaxFp4Rows = 1 << 24;
 // Query rows (query heads of a kv head x query tokens) of a sequence, on average, from which
 // mx_attend takes the kernel of many rows.
 constexpr int kAttendManyRows = 64;
+// Latents of 512 dimensions: more than so many rows go to their own kernel.
+constexpr int kAttendLatentRows = 8;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -410,6 +412,7 @@ int mx_create(mx_handle** out, int device) {
           mx::set_chain_attributes() != cudaSuccess || mx::set_gemm_fp4_attributes() != cudaSuccess ||
           mx::set_attend_attributes(sms, h->attend_ctas) != cudaSuccess ||
           mx::set_attend_rows_attributes() != cudaSuccess ||
+          mx::set_attend_latent_attributes() != cudaSuccess ||
           cudaMalloc(&h->d_status, 16) != cudaSuccess ||
           cudaMemset(h->d_status, 0, 16) != cudaSuccess ||
           cudaMalloc(&h->d_chain, mx::kChainCounters * sizeof(unsigned)) != cudaSuccess ||
@@ -1172,7 +1175,8 @@ size_t mx_attend_bytes(const mx_handle* h, int d, int shared) {
   return v < 0 ? 0
                : std::max({mx::attend_bytes(d, h->attend_ctas[v], 16),
                            mx::attend_bytes(d, h->attend_ctas[v + mx::kAttendVariants / 2], 8),
-                           mx::attend_rows_bytes(d, shared != 0, h->sm_count)});
+                           mx::attend_rows_bytes(d, shared != 0, h->sm_count),
+                           d == 512 && shared ? mx::attend_latent_bytes(h->sm_count) : 0});
 }
 
 int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
@@ -1241,6 +1245,11 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
                              static_cast<int64_t>(table_cols) * cache->page_size, h->sm_count);
     if (plan.ok)
       return cuda_status(mx::launch_attend_rows(a, cache->d, shared, plan, static_cast<cudaStream_t>(stream)));
+  }
+  if (cache->d == 512 && shared && T * static_cast<int64_t>(a.group) > static_cast<int64_t>(B) * kAttendLatentRows) {
+    const int64_t rows = static_cast<int64_t>(T) * a.group;
+    return cuda_status(mx::launch_attend_latent(a, rows <= 16ll * B ? 16 : rows <= 32ll * B ? 32 : 64, h->sm_count,
+                                                static_cast<cudaStream_t>(stream)));
   }
   const int of_rows = static_cast<int64_t>(T) * a.group <= static_cast<int64_t>(B) * 8 ? variant + mx::kAttendVariants / 2 : variant;
   return cuda_status(mx::launch_attend(a, of_rows, h->attend_ctas[of_rows], static_cast<cudaStream_t>(stream)));

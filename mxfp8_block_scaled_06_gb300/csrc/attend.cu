@@ -57,91 +57,6 @@ constexpr float kLagU = 7.f;             // and 2^15 before it is moved
 constexpr float kLagM = 24.f;
 constexpr float kSumBits = kScaleBits + kWeightBits;
 
-// ------------------------------------------------------------- the work
-__device__ __forceinline__ int64_t seq_work(const AttendArgs& a, const Seq& s) {
-  return static_cast<int64_t>(s.tiles) * s.row_tiles * a.heads;
-}
-
-struct Found {
-  int b;          // the sequence that holds the tile
-  int64_t first;  // number of its first tile
-};
-struct ScanShared {
-  int64_t warp[8];
-  Found found;
-};
-// The work of as many sequences as threads from c on, added up: this thread's sequence's, what is before it,
-// and all.
-template <int kRows, int kWarps>
-__device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh, int c, bool& bad, int64_t& before,
-                                             int64_t& all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = c + threadIdx.x;
-  int64_t w = 0;
-  if (b < a.B) {
-    const Seq s = seq_of(a, b, kRows);
-    w = seq_work(a, s);
-    bad |= s.bad;
-  }
-  int64_t sum = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(kFull, sum, o);
-    if (lane >= o) sum += v;
-  }
-  if (lane == 31) sh.warp[warp] = sum;
-  __syncthreads();
-  before = sum - w;
-  all = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += sh.warp[i];
-    all += sh.warp[i];
-  }
-  __syncthreads();
-  return w;
-}
-// Tiles of each CTA's run: an equal share.
-__device__ __forceinline__ int64_t run_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
-// All work, and the sequence in which the run of this CTA begins (where it has one).
-template <int kRows, int kWarps>
-__device__ Found find_run(const AttendArgs& a, ScanShared& sh, int64_t& total) {
-  constexpr int kThreads = 32 * kWarps;
-  bool bad = false;
-  int64_t before, all;
-  const int64_t w = scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
-  total = all;
-  for (int c = kThreads; c < a.B; c += kThreads) {
-    int64_t x;
-    scan_work<kRows, kWarps>(a, sh, c, bad, x, all);
-    total += all;
-  }
-  if (blockIdx.x == 0 && bad) atomicOr(a.status, kStatusBadInput);
-  const int64_t at = run_of(total, gridDim.x) * blockIdx.x;
-  if (before <= at && at < before + w) sh.found = Found{static_cast<int>(threadIdx.x), before};
-  if (a.B > kThreads) {
-    scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
-    int64_t base = all;
-    for (int c = kThreads; c < a.B; c += kThreads, base += all) {
-      const int64_t v = scan_work<kRows, kWarps>(a, sh, c, bad, before, all);
-      if (base + before <= at && at < base + before + v) sh.found = Found{c + static_cast<int>(threadIdx.x), base + before};
-    }
-  }
-  __syncthreads();
-  return sh.found;
-}
-
-// A unit: 8 or 16 query rows of a kv head, row i the query token (row0 + i) / group.
-struct AttendUnit {
-  int head, row0, rows;  // rows: all of this sequence and head
-  __device__ __forceinline__ bool row(const AttendArgs& a, const Seq& s, int i, int& token, int& q_head) const {
-    const int r = row0 + i;
-    token = r / a.group;
-    q_head = head * a.group + r - token * a.group;
-    token += s.q0;
-    return r < rows;
-  }
-};
-
 // ------------------------------------------------------------- pieces
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -203,19 +118,6 @@ struct Layout {
   static constexpr int kBytes = kOffScale + kRows * 4;
   static constexpr int kCtas = D == 512 && !kShared ? 1 : D >= 256 ? 2 : kRows == 8 ? 4 : D == 128 ? 2 : 3;  // of an SM, by shared memory
 };
-
-// A cut of a unit: written by the CTA whose run begins there.
-struct Cut {
-  int first, last;  // the CTAs that have parts of it; last < 0: the run does not begin within a unit
-  int later;        // whether the first CTA's part is its second
-  int head, row0, rows, q0;
-  int pad;
-};
-
-// Floats of one CTA's part of a unit: the rows' maxima, sums, and weighted sums.
-template <int D, int kRows>
-constexpr int kPartFloats = kRows * (D + 2);
-__host__ __device__ constexpr size_t cut_bytes(int ctas) { return static_cast<size_t>(ctas) * sizeof(Cut); }
 
 // ------------------------------------------------------------- the kernel
 template <int D, bool kShared, int kRows>
@@ -944,90 +846,6 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
   if (failed) atomicOr(a.status, kStatusTimeout);
 }
 
-// ------------------------------------------------------------- joining
-// Block c is that of the cut where the run of CTA c + 1 begins. A unit of n parts has n - 1 cuts, whose
-// blocks share its rows' pieces of 128 dimensions (64 at d = 64). A warp adds up a piece of
-// some parts in the order of the runs; where there are many, 2 to 8 warps share a piece.
-constexpr int kJoinThreads = 256;
-template <int D, int kRows>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int ctas) {
-  constexpr int kPiece = D < 128 ? D : 128, kVec = kPiece / 32;  // floats of a thread
-  constexpr int kPieces = kRows * D / kPiece, kWarpsHere = kJoinThreads / 32;
-  __shared__ float sums[kWarpsHere][kPiece];
-  __shared__ float2 tops[kWarpsHere];
-  pdl_launch_dependents();
-  pdl_wait();
-  const Cut cut = reinterpret_cast<const Cut*>(a.partial)[blockIdx.x + 1];
-  if (cut.last < 0) return;
-  const float* parts0 = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.partial) + cut_bytes(ctas));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = cut.last - cut.first + 1, blocks = n - 1, block = static_cast<int>(blockIdx.x) - cut.first;
-  const int team = n > 64 ? 8 : n > 32 ? 4 : n > 16 ? 2 : 1;  // warps to a piece
-  const int at_once = kWarpsHere / team, share = warp % team;
-  const int each = (n + team - 1) / team, p0 = min(share * each, n), p1 = min(p0 + each, n);
-  auto part = [&](int p) {
-    return parts0 + (static_cast<size_t>(cut.first + p) * 2 + (p == 0 ? cut.later : 0)) * kPartFloats<D, kRows>;
-  };
-  for (int x0 = block * at_once; x0 < kPieces; x0 += blocks * at_once) {
-    const int piece = x0 + warp / team, r = piece / (D / kPiece), d = piece % (D / kPiece) * kPiece + lane * kVec;
-    const bool here = piece < kPieces && cut.row0 + r < cut.rows;
-    float top = -INFINITY, sum = 0.f, v[kVec] = {};
-    if (here) {
-#pragma unroll 8
-      for (int p = p0; p < p1; ++p) {
-        const float* from = part(p);
-        const float m = from[r], l = from[kRows + r];
-        float y[kVec];
-        if constexpr (kVec == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(from + 2 * kRows + r * D + d);
-          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(from + 2 * kRows + r * D + d);
-          y[0] = z.x, y[1] = z.y;
-        }
-        const float most = fmaxf(top, m);
-        // a row that saw nothing yet, or here, adds nothing, or the NaN that it saw
-        const float keep = top == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(top - most);
-        const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - most);
-        sum = sum * keep + l * f;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = v[e] * keep + y[e] * f;
-        top = most;
-      }
-    }
-    if (team > 1) {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) sums[warp][lane * kVec + e] = v[e];
-      if (lane == 0) tops[warp] = make_float2(top, sum);
-      __syncthreads();
-      if (share == 0) {
-        for (int i = 1; i < team; ++i) {
-          const float2 t = tops[warp + i];
-          const float most = fmaxf(top, t.x);
-          const float keep = top == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(top - most);
-          const float f = t.x == -INFINITY ? (t.y != t.y ? t.y : 0.f) : exp2f(t.x - most);
-          sum = sum * keep + t.y * f;
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) v[e] = v[e] * keep + sums[warp + i][lane * kVec + e] * f;
-          top = most;
-        }
-      }
-      __syncthreads();
-    }
-    if (!here || share != 0) continue;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int q_row = cut.row0 + r, q_token = q_row / a.group, token = cut.q0 + q_token;
-    const int q_head = cut.head * a.group + q_row - q_token * a.group;
-    uint16_t* out = a.out + static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + d;
-    if constexpr (kVec == 4)
-      *reinterpret_cast<uint2*>(out) = make_uint2(pack_out(v[0] * inv, v[1] * inv, a.q_f16), pack_out(v[2] * inv, v[3] * inv, a.q_f16));
-    else
-      *reinterpret_cast<uint32_t*>(out) = pack_out(v[0] * inv, v[1] * inv, a.q_f16);
-    if (a.lse != nullptr && d == 0)
-      a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (top + log2f(sum)) * 0.6931471805599453f;
-  }
-}
-
 // f(kernel, join kernel, shared bytes, threads, rows of a unit) of a variant.
 template <int D, bool kShared, typename F>
 auto with_kernels(bool few, F&& f) {
@@ -1078,26 +896,10 @@ size_t attend_bytes(int d, int ctas, int rows) {
 
 cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream_t stream) {
   return with_variant(variant, [&](auto kernel, auto join, int bytes, int threads, int rows) {
-    // no more CTAs than tiles: every sequence has at most a block of rows more than its share
-    const int64_t tiles = (static_cast<int64_t>(a.table_cols) * a.page_size + 15 + kTile - 1) / kTile;
-    const int64_t units = (static_cast<int64_t>(a.T) * a.group / rows + std::min(a.B, a.T)) * a.heads;
-    ctas = static_cast<int>(std::min<int64_t>(ctas, std::max<int64_t>(1, tiles) * units));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    ctas = attend_ctas(a, rows, ctas);
+    const cudaError_t e = launch_overlapping(kernel, dim3(ctas), threads, bytes, stream, a);
     if (e != cudaSuccess || ctas < 2) return e;
-    cfg.gridDim = dim3(ctas - 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join, a, ctas);
+    return launch_overlapping(join, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
   });
 }
 

@@ -1,0 +1,549 @@
+// attend_latent.cu - attention over latents of 512 dimensions in the MXFP4 cache, which are keys and
+// values in one: decode steps of many heads, drafts, prompts.
+//
+// On the 5th-generation tensor cores with the cache as the products' rows: for 128 tokens
+//   S^T[token, row] = sum_d latent[token, d] Q[row, d]    (128 x R x 512)
+//   O^T[d, row]    += sum_t latent[t, d] P[t, row]        (4 times 128 x R x 128)
+// R = 16, 32 or 64 query rows. The latents are dequantized once, to fp16 in shared memory, [8 chunks of 64
+// dimensions][128 tokens][128 bytes in the 128-byte swizzle], and read from there by both: K-major
+// for the scores, M-major for the sums. fp16 under powers of two as in attend_rows.cu: the codes
+// relative to the largest scale so far, weights 2^7 above a reference that a score may exceed by 2^8.
+//
+// Bound by shared memory: a token's 1024 bytes are written once and read twice there, 24 cycles of
+// an SM, whatever R is (the cache's 272 bytes take 12 from HBM). The fp16 tile fills it, so
+// there is one, and its chunks change hands singly: while the sums of tile j go from one 128
+// dimensions to the next, the chunks behind them are written for tile j + 1, and its scores
+// follow these.
+//
+// Four warps have a token to a thread and turn S to P (rows' references and sums in shared memory),
+// eight dequantize, one issues the products; one CTA to an SM, its run of tiles as in attend.cu.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kD = 512;
+constexpr int kTokens = 128;
+static_assert(kTokens == kAttendTile, "tiles of the sequences' work");
+constexpr int kBlocks = kD / 32, kChunks = kD / 64;
+constexpr int kSoftmax = 4, kDequant = 8, kWarpsAll = kSoftmax + kDequant + 1, kThreads = 32 * kWarpsAll;
+constexpr float kLag = 8.f, kTop = 7.f;
+constexpr int kCodeBits = 13;  // 6 * 2^13 < 65504
+
+template <int kRows>
+struct Plan {
+  static constexpr int kTile = kTokens * kD * 2;
+  static constexpr int kOffQ = kTile;                       // [chunk][row][128 bytes]
+  static constexpr int kOffP = kOffQ + kRows * kD * 2;      // [token][128 bytes], the first 2 R of them
+  static constexpr int kBytes = kOffP + kTokens * 128 + 1024;
+  static constexpr int kColO = kRows;                       // S^T, then O^T of each 128 dimensions
+  static constexpr int kCols = 5 * kRows <= 128 ? 128 : 5 * kRows <= 256 ? 256 : 512;
+};
+
+template <int kRows>
+struct Shared {
+  uint64_t chunk_full[kChunks], sums_done[4], s_full, p_full, q_full;
+  uint32_t tmem;
+  int abort;
+  ScanShared scan;
+  int top[2][kDequant];      // largest scale bytes, + 256: with NaN
+  int ref[2];                // of the tile, by its parity
+  uint8_t nan[2][kTokens];   // tokens with a NaN
+  int any_nan[2];
+  // of the rows, the softmax's own
+  float factor[kRows], m[kRows], keep[kRows];
+  int lo[kRows], hi[kRows];
+  float part[kSoftmax][kRows];
+};
+
+// The segments of this CTA's run, one after another, the same for every role.
+template <int kRows>
+struct Walk {
+  int64_t at, stop, run, seq_first;
+  int b;
+  Seq s;
+  AttendUnit un;
+  int tile0, tile1;   // of the unit
+  int t_begin, t_end; // tokens of these tiles that any row of the unit sees, from a tile's first
+  int tiles;          // of 128 tokens to take
+  bool begin;
+  __device__ __forceinline__ void start(const AttendArgs& a, const Found& f, int64_t total) {
+    run = run_of(total, gridDim.x);
+    at = run * blockIdx.x;
+    stop = min(at + run, total);
+    if (at >= stop) return;
+    b = f.b;
+    seq_first = f.first;
+    s = seq_of(a, b, kRows);
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
+    if (at >= stop) return false;
+    while (at >= seq_first + seq_work(a, s)) {
+      seq_first += seq_work(a, s);
+      s = seq_of(a, ++b, kRows);
+    }
+    const int64_t in = at - seq_first;
+    const int unit = static_cast<int>(in / s.tiles);
+    tile0 = static_cast<int>(in - static_cast<int64_t>(unit) * s.tiles);
+    tile1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), tile0 + (stop - at)));
+    begin = at == run * blockIdx.x;
+    at += tile1 - tile0;
+    un.head = unit / s.row_tiles;
+    // blocks of a prompt from both its ends in turn: the first see few tokens, and a run gets both kinds
+    const int r = unit - un.head * s.row_tiles;
+    un.row0 = ((r & 1) ? s.row_tiles - 1 - (r >> 1) : r >> 1) * kRows;
+    un.rows = s.n * a.group;
+    // what the block's rows see
+    const int q_first = un.row0 / a.group, q_last = (min(un.row0 + kRows, un.rows) - 1) / a.group;
+    const int pos0 = s.len - s.n + q_first, pos1 = s.len - s.n + q_last;
+    const int from = a.window > 0 ? max(pos0 - a.window + 1, s.start) : s.start;
+    const int to = a.causal ? min(pos1 + 1, s.len) : s.len;
+    t_begin = s.start + tile0 * kTokens;
+    t_end = min(s.start + tile1 * kTokens, s.len);
+    t_end = min(t_end, to);
+    if (from > t_begin) t_begin += (from - t_begin) / kTokens * kTokens;
+    tiles = max((t_end - t_begin + kTokens - 1) / kTokens, 0);
+    return true;
+  }
+};
+
+template <int kRows>
+__global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const AttendArgs a) {
+  using L = Plan<kRows>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  __shared__ Shared<kRows> sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kIssue = kSoftmax + kDequant;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&sh.chunk_full[i]), 32 * kDequant);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.sums_done[i]), 1);
+    mbar_init(smem_u32(&sh.s_full), 1);
+    mbar_init(smem_u32(&sh.p_full), 32 * kSoftmax);
+    mbar_init(smem_u32(&sh.q_full), 32 * kSoftmax);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssue) tmem_alloc(smem_u32(&sh.tmem), L::kCols);
+  pdl_wait();
+  int64_t total;
+  const Found found = find_run<kRows, kWarpsAll>(a, sh.scan, total);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();  // after the tensor memory is here: a dependent CTA may take what is left
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort = &sh.abort;
+  auto wait = [&](uint64_t& bar, uint32_t n) {  // for the n-th completion
+    if (mbar_wait_or(smem_u32(&bar), (n - 1) & 1, abort)) return true;
+    if (*abort == 0) {
+      *abort = 1;
+      atomicOr(a.status, kStatusTimeout);
+    }
+    return false;
+  };
+  auto wait_warp = [&](uint64_t& bar, uint32_t n) { return __all_sync(kFull, wait(bar, n)) != 0; };
+  Walk<kRows> w;
+  w.start(a, found, total);
+  Cut* cuts = reinterpret_cast<Cut*>(a.partial);
+  if (threadIdx.x == 0 && w.at >= w.stop) cuts[blockIdx.x].last = -1;
+  float* parts0 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partial) + cut_bytes(gridDim.x));
+  uint32_t done = 0;  // tiles taken
+
+  if (warp < kSoftmax) {
+    // ================= queries, weights, results: a thread to a token, or to a dimension of the sums
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int tid = threadIdx.x;
+    bool ok = true;
+    while (ok && w.next(a)) {
+      if (w.begin && tid == 0) {
+        Cut cut;
+        const int64_t at = w.run * blockIdx.x, first = at - w.tile0;
+        cut.first = static_cast<int>(first / w.run);
+        cut.last = w.tile0 > 0 ? static_cast<int>((first + w.s.tiles - 1) / w.run) : -1;
+        cut.later = first != w.run * cut.first;
+        cut.head = w.un.head, cut.row0 = w.un.row0, cut.rows = w.un.rows, cut.q0 = w.s.q0;
+        cuts[blockIdx.x] = cut;
+      }
+      // ---- queries to fp16, a warp to a row at a time: each row's largest into [2^14, 2^15)
+      for (int r = warp; r < kRows; r += kSoftmax) {
+        int token, q_head;
+        const bool valid = w.un.row(a, w.s, r, token, q_head);
+        const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
+        uint4 v[2];
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[j] = valid ? *reinterpret_cast<const uint4*>(q + (lane + 32 * j) * 8) : make_uint4(0, 0, 0, 0);
+          most = max(most, max_bits(v[j]));
+        }
+        most = __reduce_max_sync(kFull, most);
+        const int shift = query_shift(most, a.q_f16);
+        const float f = a.scale_log2 < 0.f ? -pow2(shift) : pow2(shift);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int ch = lane + 32 * j;
+          sts128(base + L::kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                 query_f16(v[j], a.q_f16, f));
+        }
+        if (lane == 0) {
+          const int pos = w.s.len - w.s.n + token - w.s.q0;
+          sh.factor[r] = pow2(-shift) * fabsf(a.scale_log2);
+          sh.m[r] = -INFINITY;
+          sh.hi[r] = !valid ? 0 : a.causal ? min(pos + 1, w.s.len) : w.s.len;
+          sh.lo[r] = a.window > 0 ? pos - a.window + 1 : 0;
+        }
+      }
+      fence_proxy_async_smem();
+      if (w.tiles > 0) mbar_arrive(smem_u32(&sh.q_full));
+      named_barrier_sync(1, 32 * kSoftmax);
+      int hi_least = w.s.len, lo_most = 0;
+      for (int r = 0; r < kRows; ++r)
+        if (w.un.row0 + r < w.un.rows) hi_least = min(hi_least, sh.hi[r]), lo_most = max(lo_most, sh.lo[r]);
+
+      float l[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) l[r] = 0.f;
+      int ref = 0;
+      for (int j = 0; j < w.tiles; ++j) {
+        const uint32_t n = done + j + 1;
+        // the dequantizing warps' words are published through the last chunk's barrier
+        ok = ok && wait_warp(sh.s_full, n) && wait_warp(sh.chunk_full[kChunks - 1], n);
+        tc_fence_after();
+        const int par = (n - 1) & 1;
+        const int new_ref = sh.ref[par];
+        const float kf = pow2(new_ref - 127 - kCodeBits);
+        const bool nan = sh.any_nan[par] != 0 && sh.nan[par][tid] != 0;
+        const int t0 = w.t_begin + j * kTokens, t = t0 + tid;
+        const bool masked = t0 < lo_most || t0 + kTokens > hi_least;
+        // scores of 16 rows of this token
+        auto scores = [&](int r0, float (&x)[16]) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16_nowait(tmem + lanes + r0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            x[i] = __uint_as_float(v[i]) * (kf * sh.factor[r0 + i]);
+            if (masked || nan) {
+              if (nan) x[i] = NAN;
+              if (t >= sh.hi[r0 + i] || t < sh.lo[r0 + i]) x[i] = -INFINITY;
+            }
+          }
+        };
+        bool beyond = j > 0 && new_ref != ref;
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRows; r0 += 16) {
+          float x[16];
+          scores(r0, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) beyond |= x[i] > sh.m[r0 + i] + kLag;
+        }
+        // a wait that ran out makes all four warps leave together
+        const int votes = named_barrier_or(1, 32 * kSoftmax, beyond || !ok);
+        if (*abort != 0) ok = false;
+        if (votes) {
+          // the rows' references become their maxima
+#pragma unroll 1
+          for (int r0 = 0; r0 < kRows; r0 += 16) {
+            float x[16];
+            scores(r0, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) x[i] = fmaxf(x[i], __shfl_xor_sync(kFull, x[i], o));
+              if (lane == 0) sh.part[warp][r0 + i] = x[i];
+            }
+          }
+          named_barrier_sync(1, 32 * kSoftmax);
+          if (tid < kRows) {
+            float top = sh.m[tid];
+#pragma unroll
+            for (int i = 0; i < kSoftmax; ++i) top = fmaxf(top, sh.part[i][tid]);
+            sh.keep[tid] = exp2_fast(sh.m[tid] - (top == -INFINITY ? 0.f : top));  // m = -inf: 0
+            sh.m[tid] = top;
+          }
+          named_barrier_sync(1, 32 * kSoftmax);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) l[r] *= sh.keep[r];
+          if (j > 0) {  // the sums of the tiles before are done: this tile's scores were issued behind them
+            const float by = pow2(max(ref - new_ref, -126));
+#pragma unroll 1
+            for (int c = 0; c < 4 * kRows; c += 16) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16_nowait(tmem + lanes + L::kColO + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * (by * sh.keep[c % kRows + i]));
+              tmem_st16(tmem + lanes + L::kColO + c, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        ref = new_ref;
+#pragma unroll
+        for (int r0 = 0; r0 < kRows; r0 += 16) {
+          float x[16];
+          scores(r0, x);
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float m = sh.m[r0 + i + e];
+              y[e] = exp2_fast(x[i + e] - (m == -INFINITY ? 0.f : m) + kTop);
+              l[r0 + i + e] += y[e];
+            }
+            p[i / 2] = pack_f16(y[0], y[1]);
+          }
+          const uint32_t to = base + L::kOffP + tid * 128;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            sts128(to + (((r0 / 8 + i) ^ (tid & 7)) << 4), make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.p_full));
+      }
+      done += w.tiles;
+      // ---- results
+      if (w.tiles > 0) ok = ok && wait_warp(sh.sums_done[3], done);
+      tc_fence_after();
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+        if (lane == 0) sh.part[warp][r] = v;
+      }
+      named_barrier_sync(1, 32 * kSoftmax);
+      const bool whole = w.tile0 == 0 && w.tile1 == w.s.tiles;
+      float* part = parts0 + (static_cast<size_t>(blockIdx.x) * 2 + (w.begin ? 0 : 1)) * kPartFloats<kD, kRows>;
+      const float to_m = w.tiles > 0 ? pow2(max(ref - 127 - kCodeBits, -126)) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 4 * kRows; c += 16) {
+        uint32_t v[16];
+        if (w.tiles > 0) {
+          tmem_ld_32x32b_x16_nowait(tmem + lanes + L::kColO + c, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0u;
+        }
+        const int d = c / kRows * 128 + tid;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = c % kRows + i;
+          if (w.un.row0 + r >= w.un.rows) break;
+          const float sum = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
+          const float y = __uint_as_float(v[i]) * to_m;
+          if (whole) {
+            int token, q_head;
+            w.un.row(a, w.s, r, token, q_head);
+            a.out[static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + d] =
+                static_cast<uint16_t>(pack_out(sum == 0.f ? 0.f : y / sum, 0.f, a.q_f16));
+          } else {
+            part[2 * kRows + r * kD + d] = y;
+          }
+        }
+      }
+      if (tid < kRows && w.un.row0 + tid < w.un.rows) {
+        const float sum = sh.part[0][tid] + sh.part[1][tid] + sh.part[2][tid] + sh.part[3][tid];
+        if (!whole) {
+          part[tid] = sh.m[tid] - kTop;
+          part[kRows + tid] = sum;
+        } else if (a.lse != nullptr) {
+          int token, q_head;
+          w.un.row(a, w.s, tid, token, q_head);
+          a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (sh.m[tid] - kTop + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();
+      ok = !named_barrier_or(1, 32 * kSoftmax, !ok);  // the rows' words are read; all go on, or none
+    }
+  } else if (warp < kIssue) {
+    // ================= dequantization: a thread has one half of every 64 dimensions of a token
+    const int tid = threadIdx.x - 32 * kSoftmax;
+    const int tok = (tid & 7) + 8 * (tid >> 4), half = (tid >> 3) & 1;
+    bool ok = true, bad = false, leave = false;
+    while (!leave && w.next(a)) {
+      const int* pages_of = a.table + static_cast<size_t>(w.b) * a.ld_table;
+      const size_t head_row = static_cast<size_t>(w.un.head) * a.page_size;
+      const uint8_t* codes_of = a.k + head_row * (kD / 2) + half * 16;
+      const uint8_t* scales_of = a.k_scales + head_row * kBlocks;
+      int page, place;
+      auto load_page = [&](int j) {
+        const int t = w.t_begin + j * kTokens + tok;
+        const uint32_t col = div_u32(static_cast<uint32_t>(t) >> 4, a.per_page);
+        place = t - col * a.page_size;
+        page = -1;
+        if (t < w.t_end) page = pages_of[col];
+      };
+      uint4 code[kChunks], next[kChunks], scale, next_scale;
+      bool here, next_here;
+      auto load = [&](int j, uint4 (&to)[kChunks], uint4& sc, bool& is) {
+        // what is not there is read from the first page, and not used
+        is = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+        bad |= !is && w.t_begin + j * kTokens + tok < w.t_end;
+        const int64_t pg = is ? page : 0, at = is ? place : 0;
+        sc = *reinterpret_cast<const uint4*>(scales_of + pg * a.k_scale_page + at * kBlocks);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+          to[k] = *reinterpret_cast<const uint4*>(codes_of + pg * a.k_page + at * (kD / 2) + k * 32);
+      };
+      // no less than 2^-113: the factors are normal numbers
+      int ref = 127 + kCodeBits - 126;
+      if (w.tiles > 0) {
+        load_page(0);
+        load(0, code, scale, here);
+        load_page(1);
+      }
+      for (int j = 0; j < w.tiles; ++j) {
+        const uint32_t n = done + j + 1;
+        const int par = (n - 1) & 1;
+        if (j + 1 < w.tiles) {
+          load(j + 1, next, next_scale, next_here);
+          load_page(j + 2);
+        }
+        const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
+        int top = 0;
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+          const int x = (sw[k / 4] >> (8 * (k % 4))) & 255;
+          nan |= x == 255;
+          top = max(top, x == 255 ? 0 : x);
+        }
+        nan = nan && here;
+        top = here ? top : 0;
+        top = __reduce_max_sync(kFull, top);
+        const bool any = __any_sync(kFull, nan);
+        if (lane == 0) sh.top[par][warp - kSoftmax] = top | (any ? 256 : 0);
+        // every thread comes here, also after a wait that ran out: all leave together
+        leave = named_barrier_or(2, 32 * kDequant, !ok);
+        if (leave) break;
+        bool nans = false;
+#pragma unroll
+        for (int i = 0; i < kDequant; ++i) {
+          const int x = sh.top[par][i];
+          ref = max(ref, x & 255);
+          nans |= x >= 256;
+        }
+        // the words of tile n - 2 are read: its weights went into sums that the first chunk's wait
+        // for tile n - 1 has shown to be done
+        if (half == 0) sh.nan[par][tok] = nan;
+        if (tid == 0) sh.ref[par] = ref, sh.any_nan[par] = nans;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          // the chunk is free when the sums of its dimensions over the tile before are done
+          if (k % 2 == 0 && n > 1) ok = ok && wait(sh.sums_done[k / 2], n - 1);
+          const uint32_t s8 = (sw[k / 2] >> (16 * (k & 1) + 8 * half)) & 255u;
+          uint32_t f = static_cast<uint32_t>(max(static_cast<int>(s8) - ref + 15 + kCodeBits, 0)) * (0x10001u << 10);
+          // a NaN is 0 here: its token's weights are NaN where they are seen
+          if (!here || s8 == 255u) f = 0u;
+          const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+          const uint32_t to = base + k * (kTokens * 128) + tok * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t r[4];
+            codes_f16(cw[i], r);
+            if (ok)
+              sts128(to + (((half * 4 + i) ^ (tok & 7)) << 4),
+                     make_uint4(mul_f16x2(r[0], f), mul_f16x2(r[1], f), mul_f16x2(r[2], f), mul_f16x2(r[3], f)));
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(smem_u32(&sh.chunk_full[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) code[k] = next[k];
+        scale = next_scale;
+        here = next_here;
+      }
+      done += w.tiles;
+    }
+    if (bad) atomicOr(a.status, kStatusBadInput);
+  } else {
+    // ================= products
+    const bool leader = elect_one();
+    bool ok = true;
+    uint32_t units = 0;
+    while (ok && w.next(a)) {
+      if (w.tiles == 0) continue;
+      ++units;
+      if (leader) {
+        const uint32_t id_s = idesc_f16(kRows, false), id_o = idesc_f16(kRows, true, true);
+        ok = wait(sh.q_full, units);
+        for (int j = 0; ok && j < w.tiles; ++j) {
+          const uint32_t n = done + j + 1;
+          for (int k = 0; ok && k < kChunks; ++k) {
+            ok = wait(sh.chunk_full[k], n);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_ss(tmem, sdesc_k_sw128(base + k * (kTokens * 128) + i * 32),
+                     sdesc_k_sw128(base + L::kOffQ + k * (kRows * 128) + i * 32), id_s, k > 0 || i > 0);
+          }
+          if (!ok) break;
+          tc_commit(smem_u32(&sh.s_full));
+          ok = wait(sh.p_full, n);
+          if (!ok) break;
+          tc_fence_after();
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int i = 0; i < kTokens / 16; ++i)
+              mma_ss(tmem + L::kColO + m * kRows, sdesc_n_sw128(base + 2 * m * (kTokens * 128) + i * 2048, kTokens * 128),
+                     sdesc_n_sw128(base + L::kOffP + i * 2048, 0), id_o, j > 0 || i > 0);
+            tc_commit(smem_u32(&sh.sums_done[m]));
+          }
+        }
+      }
+      ok = __all_sync(kFull, ok) != 0;
+      done += w.tiles;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssue) tmem_dealloc(tmem, L::kCols);
+}
+
+template <typename F>
+auto with_rows(int rows, F&& f) {
+  if (rows == 16) return f(attend_latent_kernel<16>, attend_join_kernel<kD, 16>, Plan<16>::kBytes);
+  if (rows == 32) return f(attend_latent_kernel<32>, attend_join_kernel<kD, 32>, Plan<32>::kBytes);
+  return f(attend_latent_kernel<64>, attend_join_kernel<kD, 64>, Plan<64>::kBytes);
+}
+
+}  // namespace
+
+cudaError_t set_attend_latent_attributes() {
+  for (int rows = 16; rows <= 64; rows *= 2) {
+    const cudaError_t e = with_rows(rows, [](auto kernel, auto, int bytes) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+size_t attend_latent_bytes(int sm_count) {
+  return cut_bytes(sm_count) + static_cast<size_t>(sm_count) * 2 * 64 * (kD + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend_latent(const AttendArgs& a, int rows, int sm_count, cudaStream_t stream) {
+  return with_rows(rows, [&](auto kernel, auto join, int bytes) {
+    const int ctas = attend_ctas(a, rows, sm_count);
+    const cudaError_t e = launch_overlapping(kernel, dim3(ctas), kThreads, bytes, stream, a);
+    if (e != cudaSuccess || ctas < 2) return e;
+    return launch_overlapping(join, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
+  });
+}
+
+}  // namespace mx

@@ -51,72 +51,6 @@ struct Plan {
   static constexpr int kCols = kColO + kTiles * D <= 256 ? 256 : 512;
 };
 
-// D[tmem] (+)= A[smem] x B[smem]^T or A[tmem] x B[smem], fp16 operands, float32 sums.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor of .kind::f16: fp16 x fp16 -> float32, M = 128, N = n, A K-major, B
-// K-major or (n_major) N-major.
-__device__ __forceinline__ uint32_t idesc_f16(uint32_t n, bool n_major) {
-  return (1u << 4) | (n_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-// N-major operand in the 128-byte swizzle: rows (K) of 64 elements, eight rows of 1024 bytes
-// after one another, the next 64 elements of N `next` bytes on.
-__device__ __forceinline__ uint64_t sdesc_n_sw128(uint32_t saddr, uint32_t next) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(next >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-// a * b, as a * b - 0: a product and a sum would be fused to one operation.
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-  const float2 c = make_float2(-0.f, -0.f);
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
-        "l"(*reinterpret_cast<const uint64_t*>(&c)));
-  return *reinterpret_cast<const float2*>(&d);
-}
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -124,8 +58,6 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&d);
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 struct Shared {
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
@@ -356,14 +288,15 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         const float sub = (m == -INFINITY ? 0.f : m) - kTop;
         float2 sum = make_float2(0.f, 0.f);
         {
-          const float2 f2 = make_float2(f, f), sub2 = make_float2(-sub, -sub);
+          const float2 sub2 = make_float2(-sub, -sub);
           auto weights = [&](const uint32_t (&r)[32], int c) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              // (the product rounded like the maximum's: fused, it would be off from that by up to half a
-              // step, which is 64 where scores reach 2^30)
-              float2 x = mul_f32x2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2);
+              // (the products rounded like the maximum's: fused with the subtraction they would be off from
+              // it by up to half a step, which is 64 where scores reach 2^30. Two separate operations
+              // on pairs come out fused, too)
+              float2 x = make_float2(__fmul_rn(__uint_as_float(r[i]), f), __fmul_rn(__uint_as_float(r[i + 1]), f));
               x = add_f32x2(x, sub2);
               x.x = exp2_fast(x.x);
               x.y = exp2_fast(x.y);
@@ -732,22 +665,10 @@ size_t attend_rows_bytes(int d, bool shared, int sm_count) {
 
 cudaError_t launch_attend_rows(const AttendArgs& a, int d, bool shared, const AttendRowsPlan& p, cudaStream_t stream) {
   return with_variant(attend_variant(d, shared), [&](auto kernel, auto join, int bytes, int threads, int rows) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<uint32_t>(p.blocks) * a.heads * p.splits);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, p.splits);
+    const uint32_t blocks = static_cast<uint32_t>(p.blocks) * a.heads;
+    const cudaError_t e = launch_overlapping(kernel, dim3(blocks * p.splits), threads, bytes, stream, a, p.splits);
     if (e != cudaSuccess || p.splits == 1) return e;
-    cfg.gridDim = dim3(static_cast<uint32_t>(p.blocks) * a.heads, rows / 8);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join, a, p.splits);
+    return launch_overlapping(join, dim3(blocks, rows / 8), 256, 0, stream, a, p.splits);
   });
 }
 
