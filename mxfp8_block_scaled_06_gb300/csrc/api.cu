@@ -94,7 +94,7 @@ constexpr int kMaxFp4Rows = 1 << 24;
 // mx_attend takes the kernel of many rows.
 constexpr int kAttendManyRows = 64;
 // Latents of 512 dimensions: more than so many rows go to their own kernel.
-constexpr int kAttendLatentRows = 8;
+constexpr int kAttendLatentRows = 16;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =

@@ -25,8 +25,7 @@
 // The maxima m (of x) and u are only moved when a score goes beyond them by 2^24, or a
 // contribution by 2^7: then the sums are scaled anew, otherwise nothing is.
 //
-// Tokens go by in tiles of 128, an equal part to each of four warps (eight at d = 512), through a
-// ring filled by bulk copies. Up to d = 128 a warp is on its own: it keeps the queries and its
+// Tokens go by in tiles of 128, an equal part to each of four warps, through a ring filled by bulk copies. Up to d = 128 a warp is on its own: it keeps the queries and its
 // sums in registers, and four warps' results are joined at the end. Above, a warp computes the
 // scores of its tokens, hands the weights on through shared memory, and sums its share of the
 // dimensions over all 128, with one barrier a tile.
@@ -84,9 +83,10 @@ __device__ __forceinline__ uint32_t scale_f16(uint32_t s, int top) {
 template <int D, bool kShared, int kRows>
 struct Layout {
   static constexpr bool kCoop = D > 128;
-  static constexpr int kWarps = D == 512 ? 8 : 4;
+  static constexpr int kWarps = 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kSub = kTile / kWarps;       // tokens of a warp's part of a tile
+  static constexpr int kSub = kTile / kWarps;       // tokens of a warp's part of a tile: a thread to each
+  static_assert(kSub == 32, "scales");
   static constexpr int kSides = kShared ? 1 : 2;
   static constexpr int kBlocks = D / 32;
   // a row's distance: rows of whole 128 bytes are moved on by 16, so that two CTAs fit an SM (by
@@ -98,10 +98,10 @@ struct Layout {
   static constexpr int kStages = kCoop ? 2 : kRows == 8 ? 3 : 4;
   static constexpr int kRing = kStages * kWarps * kPart;
   // Of each warp's tokens: the keys' fp16 scales [token][block]; the values' [block][group of
-  // 16] in the order of the places, a pair of each half together, and some bytes more to a block, so that
+  // 16] in the order of the places, a pair of each half together, and 16 bytes more to a block, so that
   // neighbouring blocks lie in different banks; {2^(S_k - 127), S_v - 127} [place].
   static constexpr int kKeyScales = kSub * kBlocks * 2;
-  static constexpr int kValueStride = 2 * kSub + (kSub == 16 ? 8 : 16);
+  static constexpr int kValueStride = 2 * kSub + 16;
   static constexpr int kValueScales = kBlocks * kValueStride;
   static constexpr int kTokens = kSub * 8;
   static constexpr int kBuffers = kCoop ? 2 : 1;    // of what other warps read
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
   constexpr int kWarps = L::kWarps, kSub = L::kSub, kOwn = kSub / 16;  // groups of 16 tokens of a warp
   constexpr int kSlices = D <= 128 ? 1 : D / 128;  // of the scores: a thread has 1, or half a, block of each
   constexpr int kKeyWords = D == 64 ? 2 : 4;       // words of a key row's slice
-  constexpr int kWords = D == 128 ? 2 : 1;  // words of a value row: 8 dimensions each
+  constexpr int kWords = D == 64 || D == 256 ? 1 : 2;  // words of a value row: 8 dimensions each
   constexpr int kN = kRows / 8;                    // tiles of rows
   constexpr int kWide = 64 * kWords;               // dimensions of a warp's sums
   extern __shared__ __align__(128) uint8_t smem[];
@@ -228,23 +228,21 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
       if (lane == 0) mbar_expect_tx(bar, __popc(here) * L::kSides * 16 * (D / 2 + kBlocks));
       __syncwarp();
       // codes: a thread to a row where rows are padded, to a group of rows else
-      const int j = (kCoop ? lane >> 4 : lane) & (kOwn - 1);
+      const int j = kCoop ? lane >> 4 : lane & 1;
       const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
       const uint32_t group = static_cast<uint32_t>(t) >> 4;
       const int place = static_cast<int>(group - div_u32(group, a.per_page) * (a.page_size >> 4)) << 4;
-      const int64_t page = kOwn == 1 ? page_next[0] : j ? page_next[kOwn - 1] : page_next[0];
+      const int64_t page = j ? page_next[1] : page_next[0];
       const size_t row = head_row + place;
       const uint64_t policy = policy_evict_first();
       if (here >> j & 1u) {
         if constexpr (kCoop) {
-          if (lane < kSub)
 #pragma unroll
-            for (int sd = 0; sd < L::kSides; ++sd)
-              bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
+          for (int sd = 0; sd < L::kSides; ++sd)
+            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
                       (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + (row + (lane & 15)) * (D / 2), D / 2, bar, policy);
-          // the scales by threads that have no row, or by the first of each group
-          const int sd = kOwn == 1 ? lane - 16 : lane & 15;
-          if (sd >= 0 && sd < L::kSides) {
+          const int sd = lane & 15;  // the scales by the first threads of each group
+          if (sd < L::kSides) {
             bulk_load(to0 + sd * (L::kCodes + L::kRaw) + L::kCodes + j * 16 * kBlocks,
                       (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
                       16 * kBlocks, bar, policy);
@@ -372,10 +370,8 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
       const int t0 = t_begin + (warp + kWarps * i) * kSub;
       const uint32_t values_all = base + kValues0 + (kCoop ? (i & 1) * L::kValueScales : 0);
 
-      // ---- scales: fp16 relative to the row's largest, and that one. A thread has a token's, or where
-      // there are 16 tokens half of one's
-      constexpr int kMine = kBlocks * kSub / 32;
-      const int token = lane & (kSub - 1), first = kOwn == 1 ? (lane >> 4) * kMine : 0;
+      // ---- scales of token `lane`: fp16 relative to the row's largest, and that one
+      const int token = lane;
       bool nan_value = false;
       {
         const bool here = t0 + token < t_end && (live >> (2 * slot + (token >> 4)) & 1u);
@@ -383,59 +379,61 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
         float2 tok = make_float2(0.f, 0.f);
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) {
-          uint32_t w[(kMine + 3) / 4];
-          const uint32_t from = stage + sd * (L::kCodes + L::kRaw) + L::kCodes + token * kBlocks + first;
-          if constexpr (kMine == 2) {
+          uint32_t w[(kBlocks + 3) / 4];
+          const uint32_t from = stage + sd * (L::kCodes + L::kRaw) + L::kCodes + token * kBlocks;
+          if constexpr (kBlocks == 2) {
             asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(w[0]) : "r"(from));
-          } else if constexpr (kMine == 4) {
+          } else if constexpr (kBlocks == 4) {
             w[0] = lds32(from);
-          } else {
+          } else if constexpr (kBlocks == 8) {
             const uint2 v = lds64(from);
             w[0] = v.x, w[1] = v.y;
+          } else {
+            const uint4 v = lds128(from);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
           }
           int top = 0;
           bool nan = false;
 #pragma unroll
-          for (int k = 0; k < kMine; ++k) {
+          for (int k = 0; k < kBlocks; ++k) {
             const int x = (w[k / 4] >> (8 * (k % 4))) & 255;
             nan |= x == 255;
             top = max(top, x == 255 ? 0 : x);
           }
-          if constexpr (kOwn == 1) top = max(top, __shfl_xor_sync(kFull, top, 16));
           const bool value = sd == 1 || kShared;
           if (value) nan_value = nan && here;
           // a NaN among values that not every row sees must not meet the others' zero
           // weights: it is added to its own rows below
           const bool quiet = value && masked;
-          uint32_t f[kMine];
+          uint32_t f[kBlocks];
 #pragma unroll
-          for (int k = 0; k < kMine; ++k) {
+          for (int k = 0; k < kBlocks; ++k) {
             const uint32_t x = (w[k / 4] >> (8 * (k % 4))) & 255;
             f[k] = !here || (quiet && x == 255u) ? 0u : scale_f16(x, top);
           }
           if (sd == 0) {
-            const uint32_t to = keys0 + (token * kBlocks + first) * 2;
-            uint32_t h[kMine / 2];
+            const uint32_t to = keys0 + token * kBlocks * 2;
+            uint32_t h[kBlocks / 2];
 #pragma unroll
-            for (int k = 0; k < kMine / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
-            if constexpr (kMine == 2)
+            for (int k = 0; k < kBlocks / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
+            if constexpr (kBlocks == 2)
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(h[0]) : "memory");
-            else if constexpr (kMine == 4)
+            else if constexpr (kBlocks == 4)
               asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
             else
-              sts128(to, make_uint4(h[0], h[1], h[2], h[3]));
+#pragma unroll
+              for (int k = 0; k < kBlocks / 2; k += 4) sts128(to + k * 4, make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]));
             tok.x = __uint_as_float(max(static_cast<uint32_t>(top) << 23, 0x00400000u));
           }
           if (value) {
-            const uint32_t to = values_all + warp * L::kSide + first * L::kValueStride + (token >> 4) * 32 + (col >> 1) * 8 +
+            const uint32_t to = values_all + warp * L::kSide + (token >> 4) * 32 + (col >> 1) * 8 +
                                 ((token >> 3) & 1) * 4 + (col & 1) * 2;
 #pragma unroll
-            for (int k = 0; k < kMine; ++k) sts16(to + k * L::kValueStride, f[k]);
+            for (int k = 0; k < kBlocks; ++k) sts16(to + k * L::kValueStride, f[k]);
             tok.y = static_cast<float>(top - 127);
           }
         }
-        if (lane < kSub)
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + ((token & 24) + col) * 8), "f"(tok.x), "f"(tok.y)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(tokens0 + ((token & 24) + col) * 8), "f"(tok.x), "f"(tok.y)
                        : "memory");
       }
       __syncwarp();

@@ -70,6 +70,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Waits for loaded values before later loads are issued: a wait that came after those would be for
+// them as well (of six counters, loads of one kind share one), a whole memory latency.
+__device__ __forceinline__ void arrived(uint32_t v) { asm volatile("" ::"r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t folded(uint4 v) { return (v.x ^ v.y) ^ (v.z ^ v.w); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ uint32_t lds32(uint32_t p) {
   uint32_t v;

@@ -47,7 +47,7 @@ struct Plan {
 
 template <int kRows>
 struct Shared {
-  uint64_t chunk_full[kChunks], sums_done[4], s_full, p_full, q_full;
+  uint64_t pair_full[4], sums_done[4], s_full, p_full, q_full;
   uint32_t tmem;
   int abort;
   ScanShared scan;
@@ -56,7 +56,7 @@ struct Shared {
   uint8_t nan[2][kTokens];   // tokens with a NaN
   int any_nan[2];
   // of the rows, the softmax's own
-  float factor[kRows], m[kRows], keep[kRows];
+  alignas(16) float factor[kRows], m[kRows], keep[kRows];
   int lo[kRows], hi[kRows];
   float part[kSoftmax][kRows];
 };
@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
   constexpr int kIssue = kSoftmax + kDequant;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&sh.chunk_full[i]), 32 * kDequant);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.pair_full[i]), kDequant);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.sums_done[i]), 1);
     mbar_init(smem_u32(&sh.s_full), 1);
-    mbar_init(smem_u32(&sh.p_full), 32 * kSoftmax);
-    mbar_init(smem_u32(&sh.q_full), 32 * kSoftmax);
+    mbar_init(smem_u32(&sh.p_full), kSoftmax);
+    mbar_init(smem_u32(&sh.q_full), kSoftmax);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -147,6 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       atomicOr(a.status, kStatusTimeout);
     }
     return false;
+  };
+  auto arrive_warp = [&](uint64_t& bar) {  // once for the warp (32 arrivals on a barrier go one by one)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
   auto wait_warp = [&](uint64_t& bar, uint32_t n) { return __all_sync(kFull, wait(bar, n)) != 0; };
   Walk<kRows> w;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         }
       }
       fence_proxy_async_smem();
-      if (w.tiles > 0) mbar_arrive(smem_u32(&sh.q_full));
+      if (w.tiles > 0) arrive_warp(sh.q_full);
       named_barrier_sync(1, 32 * kSoftmax);
       int hi_least = w.s.len, lo_most = 0;
       for (int r = 0; r < kRows; ++r)
@@ -214,50 +218,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       for (int j = 0; j < w.tiles; ++j) {
         const uint32_t n = done + j + 1;
         // the dequantizing warps' words are published through the last chunk's barrier
-        ok = ok && wait_warp(sh.s_full, n) && wait_warp(sh.chunk_full[kChunks - 1], n);
+        ok = ok && wait_warp(sh.s_full, n) && wait_warp(sh.pair_full[3], n);
         tc_fence_after();
         const int par = (n - 1) & 1;
         const int new_ref = sh.ref[par];
         const float kf = pow2(new_ref - 127 - kCodeBits);
         const bool nan = sh.any_nan[par] != 0 && sh.nan[par][tid] != 0;
         const int t0 = w.t_begin + j * kTokens, t = t0 + tid;
-        const bool masked = t0 < lo_most || t0 + kTokens > hi_least;
+        // tokens that not every row sees, or NaN
+        const bool special = t0 < lo_most || t0 + kTokens > hi_least || sh.any_nan[par] != 0;
         // scores of 16 rows of this token
         auto scores = [&](int r0, float (&x)[16]) {
           uint32_t v[16];
           tmem_ld_32x32b_x16_nowait(tmem + lanes + r0, v);
+          float f[16];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&f[i]) = *reinterpret_cast<const float4*>(&sh.factor[r0 + i]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = __uint_as_float(v[i]) * (kf * sh.factor[r0 + i]);
-            if (masked || nan) {
+          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]) * (kf * f[i]);
+          if (special) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
               if (nan) x[i] = NAN;
               if (t >= sh.hi[r0 + i] || t < sh.lo[r0 + i]) x[i] = -INFINITY;
             }
           }
         };
         bool beyond = j > 0 && new_ref != ref;
+        float x[16];
 #pragma unroll 1
         for (int r0 = 0; r0 < kRows; r0 += 16) {
-          float x[16];
           scores(r0, x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) beyond |= x[i] > sh.m[r0 + i] + kLag;
+          for (int i = 0; i < 16; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r0 + i]);
+            beyond |= x[i] > m.x + kLag || x[i + 1] > m.y + kLag || x[i + 2] > m.z + kLag || x[i + 3] > m.w + kLag;
+          }
         }
         // a wait that ran out makes all four warps leave together
-        const int votes = named_barrier_or(1, 32 * kSoftmax, beyond || !ok);
+        const bool votes = named_barrier_or(1, 32 * kSoftmax, beyond || !ok);
         if (*abort != 0) ok = false;
         if (votes) {
           // the rows' references become their maxima
 #pragma unroll 1
           for (int r0 = 0; r0 < kRows; r0 += 16) {
-            float x[16];
-            scores(r0, x);
+            if constexpr (kRows > 16) scores(r0, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
+              float y = x[i];
 #pragma unroll
-              for (int o = 16; o > 0; o >>= 1) x[i] = fmaxf(x[i], __shfl_xor_sync(kFull, x[i], o));
-              if (lane == 0) sh.part[warp][r0 + i] = x[i];
+              for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
+              if (lane == 0) sh.part[warp][r0 + i] = y;
             }
           }
           named_barrier_sync(1, 32 * kSoftmax);
@@ -288,19 +300,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         ref = new_ref;
 #pragma unroll
         for (int r0 = 0; r0 < kRows; r0 += 16) {
-          float x[16];
-          scores(r0, x);
+          if constexpr (kRows > 16) scores(r0, x);
           uint32_t p[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float y[2];
+          for (int i = 0; i < 16; i += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(&sh.m[r0 + i]);
+            const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+            float y[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float m = sh.m[r0 + i + e];
-              y[e] = exp2_fast(x[i + e] - (m == -INFINITY ? 0.f : m) + kTop);
+            for (int e = 0; e < 4; ++e) {
+              y[e] = exp2_fast(x[i + e] - (m[e] == -INFINITY ? 0.f : m[e]) + kTop);
               l[r0 + i + e] += y[e];
             }
             p[i / 2] = pack_f16(y[0], y[1]);
+            p[i / 2 + 1] = pack_f16(y[2], y[3]);
           }
           const uint32_t to = base + L::kOffP + tid * 128;
 #pragma unroll
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sh.p_full));
+        arrive_warp(sh.p_full);
       }
       done += w.tiles;
       // ---- results
@@ -382,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         const int t = w.t_begin + j * kTokens + tok;
         const uint32_t col = div_u32(static_cast<uint32_t>(t) >> 4, a.per_page);
         place = t - col * a.page_size;
-        page = -1;
-        if (t < w.t_end) page = pages_of[col];
+        const int pg = pages_of[t < w.t_end ? col : 0];
+        page = t < w.t_end ? pg : -1;
       };
       uint4 code[kChunks], next[kChunks], scale, next_scale;
       bool here, next_here;
@@ -399,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       };
       // no less than 2^-113: the factors are normal numbers
       int ref = 127 + kCodeBits - 126;
-      if (w.tiles > 0) {
+      {
         load_page(0);
         load(0, code, scale, here);
         load_page(1);
@@ -407,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       for (int j = 0; j < w.tiles; ++j) {
         const uint32_t n = done + j + 1;
         const int par = (n - 1) & 1;
-        if (j + 1 < w.tiles) {
-          load(j + 1, next, next_scale, next_here);
-          load_page(j + 2);
-        }
+        uint32_t all = folded(scale) ^ static_cast<uint32_t>(page);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) all ^= code[k].x;
+        arrived(all);
         const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
         int top = 0;
         bool nan = false;
@@ -428,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         // every thread comes here, also after a wait that ran out: all leave together
         leave = named_barrier_or(2, 32 * kDequant, !ok);
         if (leave) break;
+        load(j + 1, next, next_scale, next_here);
+        load_page(j + 2);
         bool nans = false;
 #pragma unroll
         for (int i = 0; i < kDequant; ++i) {
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
           // the chunk is free when the sums of its dimensions over the tile before are done
-          if (k % 2 == 0 && n > 1) ok = ok && wait(sh.sums_done[k / 2], n - 1);
+          if (k % 2 == 0 && n > 1) ok = ok && wait_warp(sh.sums_done[k / 2], n - 1);
           const uint32_t s8 = (sw[k / 2] >> (16 * (k & 1) + 8 * half)) & 255u;
           uint32_t f = static_cast<uint32_t>(max(static_cast<int>(s8) - ref + 15 + kCodeBits, 0)) * (0x10001u << 10);
           // a NaN is 0 here: its token's weights are NaN where they are seen
@@ -457,8 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
               sts128(to + (((half * 4 + i) ^ (tok & 7)) << 4),
                      make_uint4(mul_f16x2(r[0], f), mul_f16x2(r[1], f), mul_f16x2(r[2], f), mul_f16x2(r[3], f)));
           }
-          fence_proxy_async_smem();
-          mbar_arrive(smem_u32(&sh.chunk_full[k]));
+          if (k % 2 == 1) {
+            fence_proxy_async_smem();
+            arrive_warp(sh.pair_full[k / 2]);
+          }
         }
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) code[k] = next[k];
@@ -469,42 +486,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     }
     if (bad) atomicOr(a.status, kStatusBadInput);
   } else {
-    // ================= products
-    const bool leader = elect_one();
+    // ================= products: the warp goes along, one lane issues
     bool ok = true;
     uint32_t units = 0;
+    const uint32_t id_s = idesc_f16(kRows, false), id_o = idesc_f16(kRows, true, true);
+    const uint32_t d0 = __shfl_sync(kFull, tmem, 0);
+    const uint32_t k_lo = sw128_lo(base), q_lo = sw128_lo(base + L::kOffQ), v_lo = sw128_lo(base, kTokens * 128),
+                   p_lo = sw128_lo(base + L::kOffP);
     while (ok && w.next(a)) {
       if (w.tiles == 0) continue;
       ++units;
-      if (leader) {
-        const uint32_t id_s = idesc_f16(kRows, false), id_o = idesc_f16(kRows, true, true);
-        ok = wait(sh.q_full, units);
-        for (int j = 0; ok && j < w.tiles; ++j) {
-          const uint32_t n = done + j + 1;
-          for (int k = 0; ok && k < kChunks; ++k) {
-            ok = wait(sh.chunk_full[k], n);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_ss(tmem, sdesc_k_sw128(base + k * (kTokens * 128) + i * 32),
-                     sdesc_k_sw128(base + L::kOffQ + k * (kRows * 128) + i * 32), id_s, k > 0 || i > 0);
-          }
-          if (!ok) break;
-          tc_commit(smem_u32(&sh.s_full));
-          ok = wait(sh.p_full, n);
+      ok = wait_warp(sh.q_full, units);
+      for (int j = 0; ok && j < w.tiles; ++j) {
+        const uint32_t n = done + j + 1;
+#pragma unroll 1
+        for (int k = 0; ok && k < kChunks; k += 2) {
+          ok = wait_warp(sh.pair_full[k / 2], n);
           if (!ok) break;
           tc_fence_after();
-          for (int m = 0; m < 4; ++m) {
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              mma_ss(d0, k_lo + (k + i / 4) * (kTokens * 8) + i % 4 * 2, kSw128Hi,
+                     q_lo + (k + i / 4) * (kRows * 8) + i % 4 * 2, kSw128Hi, id_s, k > 0 || i > 0);
+            if (k == kChunks - 2) tc_commit(smem_u32(&sh.s_full));
+          }
+          __syncwarp();
+        }
+        ok = ok && wait_warp(sh.p_full, n);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < kTokens / 16; ++i)
-              mma_ss(tmem + L::kColO + m * kRows, sdesc_n_sw128(base + 2 * m * (kTokens * 128) + i * 2048, kTokens * 128),
-                     sdesc_n_sw128(base + L::kOffP + i * 2048, 0), id_o, j > 0 || i > 0);
+              mma_ss(d0 + L::kColO + m * kRows, v_lo + 2 * m * (kTokens * 8) + i * 128, kSw128Hi, p_lo + i * 128, kSw128Hi,
+                     id_o, j > 0 || i > 0);
             tc_commit(smem_u32(&sh.sums_done[m]));
           }
+          __syncwarp();
         }
       }
-      ok = __all_sync(kFull, ok) != 0;
       done += w.tiles;
     }
   }

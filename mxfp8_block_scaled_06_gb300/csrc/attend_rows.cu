@@ -118,12 +118,12 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.k_full[i]), 128);
-      mbar_init(smem_u32(&sh.v_full[i]), 128);
+      mbar_init(smem_u32(&sh.k_full[i]), 4);
+      mbar_init(smem_u32(&sh.v_full[i]), 4);
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_full[i]), 128);
+      mbar_init(smem_u32(&sh.p_full[i]), 4);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
     sh.abort = 0;
@@ -169,6 +169,10 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
       atomicOr(a.status, kStatusTimeout);
     }
     return false;
+  };
+  auto arrive_warp = [&](uint64_t& bar) {  // once for the warp (32 arrivals on a barrier go one by one)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
   // as wait, the same for the whole warp
   auto wait_warp = [&](uint64_t& bar, int n) { return __all_sync(kFull, wait(bar, n)) != 0; };
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         l += sum.x + sum.y;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sh.p_full[tile]));
+        arrive_warp(sh.p_full[tile]);
       }
       // ---- the result
       if (wait_warp(sh.o_done[tile], tiles)) {
@@ -364,72 +368,85 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
     } else if (warp < kIssue) {
       // ================= dequantization
       const int tid = (warp - kDequant) * 32 + lane;
-      constexpr int kEach = kTokens * kBlocks / 128;  // 32-blocks of a side that a thread has
-      // eight threads have the same block of eight tokens, whose rows lie in all banks
-      const int blk = (tid >> 3) % kBlocks, tok = (tid & 7) + tid / (8 * kBlocks) * 8;
-      constexpr int kStep = 128 / kBlocks;  // tokens between two of a thread's
-      // Loads run ahead: page numbers two tiles, rows one, where two tiles of them fit in the
+      // A thread has a token: one page, 16 kBlocks neighbouring bytes of each side. (A share of every
+      // row to each thread, loads of whole lines, took four times the instructions for addresses and
+      // 1300 of the 3800 cycles of a tile.) Eight neighbours store 16 bytes of eight rows: all banks.
+      const int tok = tid;
+      // Loads run ahead: the page number two tiles, rows one, where two tiles of them fit in the
       // registers; else a side's next rows are loaded when the present ones are converted.
-      constexpr bool kAhead = L::kSides * kEach <= 8;
+      constexpr bool kAhead = L::kSides * kBlocks <= 8;
       struct Rows {
-        uint4 code[kEach];
-        uint32_t scale[kEach];  // 256: no token
+        uint4 code[kBlocks];
+        uint32_t scale[(kBlocks + 3) / 4];
       };
       const int* pages_of = a.table + static_cast<size_t>(b) * a.ld_table;
       bool bad = false;  // a page outside the cache
       Rows now[L::kSides], next[kAhead ? L::kSides : 1];
-      int page[kEach], place[kEach];  // the next rows', page -1: no token
+      bool here, next_here;  // whether there is a token
+      int page, place;       // the next row's
       const int t_stop = min(t_first + tiles * kTokens, s.len);
-      auto load_pages = [&](int j) {
-#pragma unroll
-        for (int x = 0; x < kEach; ++x) {
-          const int t = t_first + j * kTokens + tok + x * kStep;
-          const uint32_t col = div_u32(static_cast<uint32_t>(t) >> 4, a.per_page);
-          place[x] = t - col * a.page_size;
-          page[x] = -1;
-          if (t < t_stop) page[x] = pages_of[col];
-        }
+      auto load_page = [&](int j) {
+        const int t = t_first + j * kTokens + tok;
+        const uint32_t col = div_u32(static_cast<uint32_t>(t) >> 4, a.per_page);
+        place = t - col * a.page_size;
+        const int pg = pages_of[t < t_stop ? col : 0];
+        page = t < t_stop ? pg : -1;
       };
       const size_t head_row = static_cast<size_t>(head) * a.page_size;
-      const uint8_t* codes_of[2] = {a.k + head_row * (D / 2) + blk * 16, a.v + head_row * (D / 2) + blk * 16};
-      const uint8_t* scales_of[2] = {a.k_scales + head_row * kBlocks + blk, a.v_scales + head_row * kBlocks + blk};
-      auto load = [&](int j, int sd, Rows& to) {
+      const uint8_t* codes_of[2] = {a.k + head_row * (D / 2), a.v + head_row * (D / 2)};
+      const uint8_t* scales_of[2] = {a.k_scales + head_row * kBlocks, a.v_scales + head_row * kBlocks};
+      auto load = [&](int j, int sd, Rows& to, bool& is) {
+        // what is not there is read from the first page, and not used
+        is = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+        bad |= !is && t_first + j * kTokens + tok < t_stop;
+        const int64_t pg = is ? page : 0;
+        const int at = is ? place : 0;
+        const uint8_t* codes = codes_of[sd] + pg * (sd ? a.v_page : a.k_page) + at * (D / 2);
+        const uint8_t* scales = scales_of[sd] + pg * (sd ? a.v_scale_page : a.k_scale_page) + at * kBlocks;
+        if constexpr (kBlocks == 2) {
+          to.scale[0] = *reinterpret_cast<const uint16_t*>(scales);
+        } else {
 #pragma unroll
-        for (int x = 0; x < kEach; ++x) {
-          // what is not there is read from the first page, and not used
-          const bool here = static_cast<uint32_t>(page[x]) < static_cast<uint32_t>(a.pages);
-          bad |= !here && t_first + j * kTokens + tok + x * kStep < t_stop;
-          const int pg = here ? page[x] : 0, at = here ? place[x] : 0;
-          to.code[x] = *reinterpret_cast<const uint4*>(codes_of[sd] + pg * (sd ? a.v_page : a.k_page) + at * (D / 2));
-          const uint32_t sc = scales_of[sd][pg * (sd ? a.v_scale_page : a.k_scale_page) + at * kBlocks];
-          to.scale[x] = here ? sc : 256u;
+          for (int x = 0; x < kBlocks / 4; ++x) to.scale[x] = reinterpret_cast<const uint32_t*>(scales)[x];
         }
-      };
-      load_pages(0);
 #pragma unroll
-      for (int sd = 0; sd < L::kSides; ++sd) load(0, sd, now[sd]);
-      load_pages(1);
+        for (int x = 0; x < kBlocks; ++x) to.code[x] = reinterpret_cast<const uint4*>(codes)[x];
+      };
+      load_page(0);
+#pragma unroll
+      for (int sd = 0; sd < L::kSides; ++sd) load(0, sd, now[sd], here);
+      load_page(1);
       // no less than 2^-113: the factors are normal numbers
       int v_ref = 127 + kCodeBits - 126;
       bool ok = true;
       for (int j = 0; j < tiles; ++j) {
         const int st = j % kStages;
         if constexpr (kAhead) {
+          uint32_t all = static_cast<uint32_t>(page);
 #pragma unroll
-          for (int sd = 0; sd < L::kSides; ++sd) load(j + 1, sd, next[sd]);
-          load_pages(j + 2);
+          for (int sd = 0; sd < L::kSides; ++sd) {
+            all ^= now[sd].scale[0];
+#pragma unroll
+            for (int x = 0; x < kBlocks; ++x) all ^= now[sd].code[x].x;
+          }
+          arrived(all);
+#pragma unroll
+          for (int sd = 0; sd < L::kSides; ++sd) load(j + 1, sd, next[sd], next_here);
+          load_page(j + 2);
         }
-        // the tile's largest scales, and whether it has NaN
+        // the tile's largest scales, and which of the values' blocks are NaN
         int top[2] = {0, 0};
         uint32_t nan = 0;
 #pragma unroll
-        for (int sd = 0; sd < L::kSides; ++sd)
+        for (int sd = 0; sd < L::kSides; ++sd) {
 #pragma unroll
-          for (int x = 0; x < kEach; ++x) {
-            const uint32_t sc = now[sd].scale[x];
-            if (sd == L::kSides - 1 && sc == 255u) nan |= 1u << x;
-            top[sd] = max(top[sd], sc < 255u ? static_cast<int>(sc) : 0);
+          for (int x = 0; x < kBlocks; ++x) {
+            const int sc = (now[sd].scale[x / 4] >> (8 * (x % 4))) & 255;
+            if (sd == L::kSides - 1 && sc == 255) nan |= 1u << x;
+            top[sd] = max(top[sd], sc < 255 ? sc : 0);
           }
+          if (!here) top[sd] = 0, nan = 0;
+        }
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) top[sd] = __reduce_max_sync(kFull, top[sd]);
         const bool any_nan = __any_sync(kFull, nan != 0);
@@ -453,18 +470,12 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         // its sums, whose weights the softmax took from tile j - 2's words. (With one stage: the scores of
         // tile j - 1 were issued after those sums.)
         if (j >= kStages) {
-          if (!kShared) ok = wait(sh.k_empty[st], j / kStages);
-          if (kShared || kStages > 1) ok = ok && wait(sh.v_empty[st], j / kStages);
+          if (!kShared) ok = wait_warp(sh.k_empty[st], j / kStages);
+          if (kShared || kStages > 1) ok = ok && wait_warp(sh.v_empty[st], j / kStages);
         }
         if (nans) {
-          // one byte a token: which of its blocks are NaN
-          if (ok) smem[L::kOffNan + (j & 1) * kTokens + tid] = 0;
-          if (named_barrier_or(1, 128, !ok)) break;
-#pragma unroll
-          for (int x = 0; x < kEach; ++x)
-            if (nan >> x & 1u)
-              atomicOr(reinterpret_cast<unsigned*>(smem + L::kOffNan + (j & 1) * kTokens + ((tok + x * kStep) & ~3)),
-                       1u << (blk + 8 * ((tok + x * kStep) & 3)));
+          // one byte a token
+          if (ok) smem[L::kOffNan + (j & 1) * kTokens + tid] = static_cast<uint8_t>(nan);
         }
         if (ok && tid == 0) {
           sh.k_factor[j & 1] = pow2(k_top - 127 - kCodeBits);
@@ -474,78 +485,84 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
 #pragma unroll
         for (int sd = 0; sd < L::kSides; ++sd) {
           const int ref = sd ? v_ref : k_top;
-          if (sd == 1 && kStages == 1 && j > 0) ok = ok && wait(sh.v_empty[st], j);
+          if (sd == 1 && kStages == 1 && j > 0) ok = ok && wait_warp(sh.v_empty[st], j);
           if (!ok) continue;
-          const uint32_t to = base + L::kOffStage + (st * L::kSides + sd) * L::kTile + (blk >> 1) * (kTokens * 128);
+          const uint32_t to = base + L::kOffStage + (st * L::kSides + sd) * L::kTile + tok * 128;
 #pragma unroll
-          for (int x = 0; x < kEach; ++x) {
-            const int t = tok + x * kStep;
-            const int e = static_cast<int>(now[sd].scale[x]) - ref + 15 + kCodeBits;  // biased exponent of fp16
-            uint32_t f = static_cast<uint32_t>(max(e, 0)) * (0x10001u << 10);
+          for (int x = 0; x < kBlocks; ++x) {
+            const uint32_t sc = (now[sd].scale[x / 4] >> (8 * (x % 4))) & 255u;
+            // biased exponent of fp16
+            uint32_t f = static_cast<uint32_t>(max(static_cast<int>(sc) - ref + 15 + kCodeBits, 0)) * (0x10001u << 10);
             // a NaN value is 0 here and comes back in its rows' results; a NaN key is NaN
-            if (now[sd].scale[x] >= 255u) f = sd == L::kSides - 1 || now[sd].scale[x] == 256u ? 0u : 0x7E007E00u;
+            if (sc == 255u) f = sd == L::kSides - 1 ? 0u : 0x7E007E00u;
+            if (!here) f = 0u;
             const uint4 cw = now[sd].code[x];
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t r[4];
               codes_f16(w[i], r);
-              sts128(to + t * 128 + (((((blk & 1) << 2) + i) ^ (t & 7)) << 4),
+              sts128(to + (x >> 1) * (kTokens * 128) + (((((x & 1) << 2) + i) ^ (tok & 7)) << 4),
                      make_uint4(mul_f16x2(r[0], f), mul_f16x2(r[1], f), mul_f16x2(r[2], f), mul_f16x2(r[3], f)));
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(smem_u32(sd == 0 ? &sh.k_full[st] : &sh.v_full[st]));
-          if constexpr (!kAhead) load(j + 1, sd, now[sd]);
+          arrive_warp(sd == 0 ? sh.k_full[st] : sh.v_full[st]);
+          if constexpr (!kAhead) load(j + 1, sd, now[sd], next_here);
         }
         if constexpr (kAhead) {
 #pragma unroll
           for (int sd = 0; sd < L::kSides; ++sd) now[sd] = next[sd];
         } else {
-          load_pages(j + 2);
+          load_page(j + 2);
         }
+        here = next_here;
       }
       if (bad) atomicOr(a.status, kStatusBadInput);
     } else if (warp == kIssue) {
-      // ================= products
-      if (elect_one()) {
-        const uint32_t id_s = idesc_f16(kTokens, false), id_o = idesc_f16(D, true);
-        bool ok = true;
-        auto sums = [&](int g, int j) {  // O_g += P_g V of tile j
-          const int st = j % kStages;
-          if (!wait(sh.p_full[g], j + 1)) return false;
-          if (!kShared && g == 0 && !wait(sh.v_full[st], j / kStages + 1)) return false;
-          tc_fence_after();
-          const uint32_t v = base + L::kOffStage + (st * L::kSides + L::kSides - 1) * L::kTile;
+      // ================= products: the warp goes along, one lane issues
+      const uint32_t id_s = idesc_f16(kTokens, false), id_o = idesc_f16(D, true);
+      const uint32_t d0 = __shfl_sync(kFull, tmem, 0);
+      constexpr uint32_t kSide16 = L::kTile / 16;
+      const uint32_t q_lo = sw128_lo(base + L::kOffQ), k_lo = sw128_lo(base + L::kOffStage),
+                     v_lo = sw128_lo(base + L::kOffStage, kTokens * 128) + (L::kSides - 1) * kSide16;
+      bool ok = true;
+      auto sums = [&](int g, int j) {  // O_g += P_g V of tile j
+        const int st = j % kStages;
+        if (!wait_warp(sh.p_full[g], j + 1)) return false;
+        if (!kShared && g == 0 && !wait_warp(sh.v_full[st], j / kStages + 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v = v_lo + st * (L::kSides * kSide16);
 #pragma unroll
           for (int k = 0; k < kTokens / 16; ++k)
-            mma_ts(tmem + L::kColO + g * D, tmem + g * kTokens + k * 8, sdesc_n_sw128(v + k * 2048, kTokens * 128), id_o,
-                   j > 0 || k > 0);
+            mma_ts(d0 + L::kColO + g * D, d0 + g * kTokens + k * 8, v + k * 128, kSw128Hi, id_o, j > 0 || k > 0);
           tc_commit(smem_u32(&sh.o_done[g]));
           if (g == kTiles - 1) tc_commit(smem_u32(&sh.v_empty[st]));
-          return true;
-        };
-        for (int j = 0; ok && j < tiles; ++j) {
-          const int st = j % kStages;
-          if (!wait(sh.k_full[st], j / kStages + 1)) break;
-          const uint32_t k0 = base + L::kOffStage + st * L::kSides * L::kTile;
-          for (int g = 0; ok && g < kTiles; ++g) {
-            if (j > 0) ok = sums(g, j - 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t q0 = base + L::kOffQ + g * L::kTile;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
-              mma_ss(tmem + g * kTokens, sdesc_k_sw128(q0 + at), sdesc_k_sw128(k0 + at), id_s, k > 0);
-            }
-            tc_commit(smem_u32(&sh.s_full[g]));
-          }
-          if (ok && !kShared) tc_commit(smem_u32(&sh.k_empty[st]));
         }
-        for (int g = 0; ok && g < kTiles; ++g) ok = sums(g, tiles - 1);
+        __syncwarp();
+        return true;
+      };
+      for (int j = 0; ok && j < tiles; ++j) {
+        const int st = j % kStages;
+        if (!wait_warp(sh.k_full[st], j / kStages + 1)) break;
+        for (int g = 0; ok && g < kTiles; ++g) {
+          if (j > 0) ok = sums(g, j - 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t q0 = q_lo + g * kSide16, k0 = k_lo + st * (L::kSides * kSide16);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(d0 + g * kTokens, q0 + (k >> 2) * 1024 + (k & 3) * 2, kSw128Hi, k0 + (k >> 2) * 1024 + (k & 3) * 2,
+                     kSw128Hi, id_s, k > 0);
+            tc_commit(smem_u32(&sh.s_full[g]));
+            if (!kShared && g == kTiles - 1) tc_commit(smem_u32(&sh.k_empty[st]));
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
+      for (int g = 0; ok && g < kTiles; ++g) ok = sums(g, tiles - 1);
     }
   } else if (work && warp < kDequant) {
     // no token in sight: zeros, or an empty part
