@@ -58,8 +58,17 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&d);
 }
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+
 struct Shared {
-  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2][2], o_done[2];
   uint32_t tmem;
   int abort;
   int b, row_block;      // of this CTA; b < 0: none
@@ -123,7 +132,8 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
       mbar_init(smem_u32(&sh.k_empty[i]), 1);
       mbar_init(smem_u32(&sh.v_empty[i]), 1);
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.p_full[i][0]), 4);
+      mbar_init(smem_u32(&sh.p_full[i][1]), 4);
       mbar_init(smem_u32(&sh.o_done[i]), 1);
     }
     sh.abort = 0;
@@ -292,16 +302,16 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         const float sub = (m == -INFINITY ? 0.f : m) - kTop;
         float2 sum = make_float2(0.f, 0.f);
         {
-          const float2 sub2 = make_float2(-sub, -sub);
-          auto weights = [&](const uint32_t (&r)[32], int c) {
+          const float2 f2 = make_float2(f, f), sub2 = make_float2(-sub, -sub);
+          auto weights = [&](auto exact, const uint32_t (&r)[32], int c) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              // (the products rounded like the maximum's: fused with the subtraction they would be off from
-              // it by up to half a step, which is 64 where scores reach 2^30. Two separate operations
-              // on pairs come out fused, too)
-              float2 x = make_float2(__fmul_rn(__uint_as_float(r[i]), f), __fmul_rn(__uint_as_float(r[i + 1]), f));
-              x = add_f32x2(x, sub2);
+              float2 x = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+              if constexpr (decltype(exact)::value)
+                x = add_f32x2(make_float2(__fmul_rn(x.x, f), __fmul_rn(x.y, f)), sub2);
+              else
+                x = fma_f32x2(x, f2, sub2);
               x.x = exp2_fast(x.x);
               x.y = exp2_fast(x.y);
               sum = add_f32x2(sum, x);
@@ -310,22 +320,32 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
             // P lies over the S columns that this thread has read: 32 of them make 16 of P
             tmem_st16(t_s + c / 2, p);
           };
-          uint32_t r0[32], r1[32];
-          tmem_ld32(t_s, r0);
+          auto all = [&](auto exact) {
+            uint32_t r0[32], r1[32];
+            tmem_ld32(t_s, r0);
 #pragma unroll 1
-          for (int c = 0; c < kTokens; c += 64) {
-            tmem_ld_wait();
-            tmem_ld32(t_s + c + 32, r1);
-            weights(r0, c);
-            tmem_ld_wait();
-            if (c + 64 < kTokens) tmem_ld32(t_s + c + 64, r0);
-            weights(r1, c + 32);
-          }
+            for (int c = 0; c < kTokens; c += 64) {
+              tmem_ld_wait();
+              tmem_ld32(t_s + c + 32, r1);
+              weights(exact, r0, c);
+              tmem_ld_wait();
+              if (c + 64 < kTokens) tmem_ld32(t_s + c + 64, r0);
+              weights(exact, r1, c + 32);
+              // the sums over the first half of the tokens begin
+              tmem_st_wait();
+              tc_fence_before();
+              arrive_warp(sh.p_full[tile][c / 64]);
+            }
+          };
+          // Fused, a product is not rounded as the maximum's was. Its difference from that is off by up
+          // to half a step of it, the same for a whole row: a quarter at 2^22, but 64 at 2^30, where a
+          // weight would not be finite.
+          if (__any_sync(kFull, fabsf(sub) > 0x1p22f))
+            all(std::true_type{});
+          else
+            all(std::false_type{});
         }
         l += sum.x + sum.y;
-        tmem_st_wait();
-        tc_fence_before();
-        arrive_warp(sh.p_full[tile]);
       }
       // ---- the result
       if (wait_warp(sh.o_done[tile], tiles)) {
@@ -529,18 +549,23 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
       bool ok = true;
       auto sums = [&](int g, int j) {  // O_g += P_g V of tile j
         const int st = j % kStages;
-        if (!wait_warp(sh.p_full[g], j + 1)) return false;
-        if (!kShared && g == 0 && !wait_warp(sh.v_full[st], j / kStages + 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t v = v_lo + st * (L::kSides * kSide16);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_warp(sh.p_full[g][half], j + 1)) return false;
+          if (!kShared && g == 0 && half == 0 && !wait_warp(sh.v_full[st], j / kStages + 1)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t v = v_lo + st * (L::kSides * kSide16) + half * 512;
 #pragma unroll
-          for (int k = 0; k < kTokens / 16; ++k)
-            mma_ts(d0 + L::kColO + g * D, d0 + g * kTokens + k * 8, v + k * 128, kSw128Hi, id_o, j > 0 || k > 0);
-          tc_commit(smem_u32(&sh.o_done[g]));
-          if (g == kTiles - 1) tc_commit(smem_u32(&sh.v_empty[st]));
+            for (int k = 0; k < kTokens / 32; ++k)
+              mma_ts(d0 + L::kColO + g * D, d0 + g * kTokens + half * 32 + k * 8, v + k * 128, kSw128Hi, id_o,
+                     j > 0 || half > 0 || k > 0);
+            if (half == 1) {
+              tc_commit(smem_u32(&sh.o_done[g]));
+              if (g == kTiles - 1) tc_commit(smem_u32(&sh.v_empty[st]));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         return true;
       };
       for (int j = 0; ok && j < tiles; ++j) {
