@@ -89,9 +89,9 @@ struct Layout {
   static_assert(kSub == 32, "scales");
   static constexpr int kSides = kShared ? 1 : 2;
   static constexpr int kBlocks = D / 32;
-  // a row's distance: rows of whole 128 bytes are moved on by 16, so that two CTAs fit an SM (by
-  // 64, a key's loads of two rows would be free of bank conflicts)
-  static constexpr int kPitch = D <= 128 ? D / 2 : D / 2 + 16;
+  // (rows of whole 128 bytes that were copied one by one, 16 bytes further each, had fewer bank
+  // conflicts, and arrived at 3.7 TB/s at most)
+  static constexpr int kPitch = D / 2;
   static constexpr int kCodes = kSub * kPitch;      // bytes of a warp's part of a stage
   static constexpr int kRaw = kSub * kBlocks;       // scale bytes
   static constexpr int kPart = kSides * (kCodes + kRaw);
@@ -227,37 +227,25 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
       live = (live & ~(3u << (2 * slot))) | here << (2 * slot);
       if (lane == 0) mbar_expect_tx(bar, __popc(here) * L::kSides * 16 * (D / 2 + kBlocks));
       __syncwarp();
-      // codes: a thread to a row where rows are padded, to a group of rows else
-      const int j = kCoop ? lane >> 4 : lane & 1;
-      const int t = t_begin + (warp + kWarps * i) * kSub + 16 * j;
-      const uint32_t group = static_cast<uint32_t>(t) >> 4;
-      const int place = static_cast<int>(group - div_u32(group, a.per_page) * (a.page_size >> 4)) << 4;
-      const int64_t page = j ? page_next[1] : page_next[0];
-      const size_t row = head_row + place;
-      const uint64_t policy = policy_evict_first();
-      if (here >> j & 1u) {
-        if constexpr (kCoop) {
-#pragma unroll
-          for (int sd = 0; sd < L::kSides; ++sd)
-            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + lane * L::kPitch,
-                      (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + (row + (lane & 15)) * (D / 2), D / 2, bar, policy);
-          const int sd = lane & 15;  // the scales by the first threads of each group
-          if (sd < L::kSides) {
-            bulk_load(to0 + sd * (L::kCodes + L::kRaw) + L::kCodes + j * 16 * kBlocks,
-                      (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
-                      16 * kBlocks, bar, policy);
-          }
-        } else if (lane < 4 * L::kSides) {
-          const int sd = (lane >> 1) & (L::kSides - 1);
-          const uint32_t to = to0 + sd * (L::kCodes + L::kRaw);
-          if (lane < 2 * L::kSides)
-            bulk_load(to + j * 16 * L::kPitch, (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2), 8 * D,
-                      bar, policy);
-          else
-            bulk_load(to + L::kCodes + j * 16 * kBlocks,
-                      (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
-                      16 * kBlocks, bar, policy);
-        }
+      // a thread to each run of neighbouring rows: codes and scales of each side, of both groups at once
+      // where they lie in one page (a copy takes about 20 cycles whatever its size)
+      const int t = t_begin + (warp + kWarps * i) * kSub;
+      const uint32_t group = static_cast<uint32_t>(t) >> 4, col = div_u32(group, a.per_page);
+      const bool together = here == 3u && div_u32(group + 1, a.per_page) == col;
+      const int j = lane & 1, sd = (lane >> 1) & (L::kSides - 1);
+      if (lane < 4 * L::kSides && (here >> j & 1u) && !(together && j == 1)) {
+        const uint32_t of_page = j == 0 ? col : div_u32(group + 1, a.per_page);
+        const size_t row = head_row + ((group + j - of_page * (a.page_size >> 4)) << 4);
+        const int64_t page = j ? page_next[1] : page_next[0];
+        const uint32_t to = to0 + sd * (L::kCodes + L::kRaw), rows = together ? 32u : 16u;
+        const uint64_t policy = policy_evict_first();
+        if (lane < 2 * L::kSides)
+          bulk_load(to + j * 16 * L::kPitch, (sd ? a.v + page * a.v_page : a.k + page * a.k_page) + row * (D / 2),
+                    rows * (D / 2), bar, policy);
+        else
+          bulk_load(to + L::kCodes + j * 16 * kBlocks,
+                    (sd ? a.v_scales + page * a.v_scale_page : a.k_scales + page * a.k_scale_page) + row * kBlocks,
+                    rows * kBlocks, bar, policy);
       }
     };
     page_load(0);
