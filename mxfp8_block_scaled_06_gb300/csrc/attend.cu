@@ -97,7 +97,7 @@ struct Layout {
   static constexpr int kPart = kSides * (kCodes + kRaw);
   static constexpr int kStages = kCoop ? 2 : kRows == 8 ? 3 : 4;
   static constexpr int kRing = kStages * kWarps * kPart;
-  // Of each warp's tokens: the keys' fp16 scales [token][block]; the values' [block][group of
+  // Of each warp's tokens: the keys' fp16 scales [token][block, in the order 0 2 1 3]; the values' [block][group of
   // 16] in the order of the places, a pair of each half together, and 16 bytes more to a block, so that
   // neighbouring blocks lie in different banks; {2^(S_k - 127), S_v - 127} [place].
   static constexpr int kKeyScales = kSub * kBlocks * 2;
@@ -380,44 +380,74 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
             const uint4 v = lds128(from);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
           }
-          int top = 0;
-          bool nan = false;
+          // Two bytes at a time, 16 bits to each: blocks 4 k and 4 k + 2 in one word, 4 k + 1 and
+          // 4 k + 3 in the next; 255 (NaN) goes by apart.
+          constexpr int kPairs = kBlocks / 2;
+          uint32_t f[kPairs];
+          uint32_t nan = 0;
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
-            const int x = (w[k / 4] >> (8 * (k % 4))) & 255;
-            nan |= x == 255;
-            top = max(top, x == 255 ? 0 : x);
-          }
+          for (int k = 0; k < (kBlocks + 3) / 4; ++k) nan |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & w[k] & 0x80808080u;
           const bool value = sd == 1 || kShared;
-          if (value) nan_value = nan && here;
-          // a NaN among values that not every row sees must not meet the others' zero
-          // weights: it is added to its own rows below
-          const bool quiet = value && masked;
-          uint32_t f[kBlocks];
+          int top = 0;
+          if (__any_sync(kFull, nan != 0)) {
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
-            const uint32_t x = (w[k / 4] >> (8 * (k % 4))) & 255;
-            f[k] = !here || (quiet && x == 255u) ? 0u : scale_f16(x, top);
+            for (int k = 0; k < kBlocks; ++k) {
+              const int x = (w[k / 4] >> (8 * (k % 4))) & 255;
+              top = max(top, x == 255 ? 0 : x);
+            }
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) f[k] = 0;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+              const uint32_t x = (w[k / 4] >> (8 * (k % 4))) & 255;
+              // a NaN among values that not every row sees must not meet the others' zero
+              // weights: it is added to its own rows below
+              const uint32_t v = value && masked && x == 255u ? 0u : scale_f16(x, top);
+              f[kBlocks == 2 ? 0 : k / 4 * 2 + k % 2] |= v << (kBlocks == 2 ? 16 * k : k % 4 / 2 * 16);
+            }
+            if (value) nan_value = nan != 0 && here;
+          } else {
+            if constexpr (kBlocks == 2) {
+              f[0] = (w[0] & 255u) | (w[0] & 0xFF00u) << 8;
+            } else {
+#pragma unroll
+              for (int k = 0; k < kBlocks / 4; ++k) {
+                f[2 * k] = w[k] & 0x00FF00FFu;
+                f[2 * k + 1] = (w[k] >> 8) & 0x00FF00FFu;
+              }
+            }
+            uint32_t most = f[0];
+#pragma unroll
+            for (int k = 1; k < kPairs; ++k) most = __vmaxu2(most, f[k]);
+            top = static_cast<int>(max(most & 0xFFFFu, most >> 16));
+            // 2^(s - top + 13) in fp16, 0 below 2^-14: exponent 28 less the distance
+            const uint32_t top2 = static_cast<uint32_t>(top) * 0x10001u;
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) f[k] = (0x001C001Cu - __vminu2(top2 - f[k], 0x001C001Cu)) << 10;
           }
+          if (!here)
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k) f[k] = 0u;
           if (sd == 0) {
             const uint32_t to = keys0 + token * kBlocks * 2;
-            uint32_t h[kBlocks / 2];
-#pragma unroll
-            for (int k = 0; k < kBlocks / 2; ++k) h[k] = f[2 * k] | f[2 * k + 1] << 16;
             if constexpr (kBlocks == 2)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(h[0]) : "memory");
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(f[0]) : "memory");
             else if constexpr (kBlocks == 4)
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(h[0]), "r"(h[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(f[0]), "r"(f[1]) : "memory");
             else
 #pragma unroll
-              for (int k = 0; k < kBlocks / 2; k += 4) sts128(to + k * 4, make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]));
+              for (int k = 0; k < kPairs; k += 4) sts128(to + k * 4, make_uint4(f[k], f[k + 1], f[k + 2], f[k + 3]));
             tok.x = __uint_as_float(max(static_cast<uint32_t>(top) << 23, 0x00400000u));
           }
           if (value) {
-            const uint32_t to = values_all + warp * L::kSide + (token >> 4) * 32 + (col >> 1) * 8 +
-                                ((token >> 3) & 1) * 4 + (col & 1) * 2;
+            const uint32_t to =
+                values_all + warp * L::kSide + (token >> 4) * 32 + (col >> 1) * 8 + ((token >> 3) & 1) * 4 + (col & 1) * 2;
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) sts16(to + k * L::kValueStride, f[k]);
+            for (int k = 0; k < kPairs; ++k) {
+              const int low = kBlocks == 2 ? 0 : k / 2 * 4 + k % 2;
+              sts16(to + low * L::kValueStride, f[k]);
+              sts16(to + (kBlocks == 2 ? 1 : low + 2) * L::kValueStride, f[k] >> 16);
+            }
             tok.y = static_cast<float>(top - 127);
           }
         }
@@ -435,7 +465,8 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[j][n][e] = 0.f;
       const uint32_t key_at = stage + place_of(g) * L::kPitch + c * (kKeyWords * 4);
-      const uint32_t scale_at = keys0 + place_of(g) * kBlocks * 2 + (D == 64 ? c >> 1 : c) * 2;
+      // (blocks 0 2 1 3 of each four)
+      const uint32_t scale_at = keys0 + place_of(g) * kBlocks * 2 + (D == 64 ? c >> 1 : (c & 1) * 2 + (c >> 1)) * 2;
       constexpr int kAtOnce = kCoop ? kOwn : 1;  // groups that share a load of the queries
 #pragma unroll 1
       for (int k = 0; k < kSlices; ++k)
