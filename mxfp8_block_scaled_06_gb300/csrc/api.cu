@@ -93,8 +93,17 @@ constexpr int kMaxFp4Rows = 1 << 24;
 // Query rows (query heads of a kv head x query tokens) of a sequence, on average, from which
 // mx_attend takes the kernel of many rows.
 constexpr int kAttendManyRows = 64;
-// Latents of 512 dimensions: more than so many rows go to their own kernel.
-constexpr int kAttendLatentRows = 16;
+// It takes about the same time whatever the rows of a sequence are up to 128 (48 sequences of up to 4096 tokens, d 128,
+// 133 us), where the other's grows with them: 113 us at 48 rows, 146 at 64, 212 at 96 (d 64: 79, 99,
+// 140 against 116; d 256: 159, 206, 301 against 154). 4 such sequences: 27 and 34 us at 64, 37 and 32 at 128.
+// Latents of 512 dimensions go to their own kernel from so many rows of a sequence on, where there is
+// work for 16 tiles of 64 rows and 128 tokens or more on each SM: it reads the cache for four times as many rows
+// at once, and takes 20 us longer to begin and to end. Few rows against it, 16 heads, us: 48 sequences of
+// up to 8192 tokens 141 / 145 at 64 rows, 266 / 234 at 128, 1000 / 793 at 512, 15780 / 9201 at 8192;
+// 2 of them 78 / 80 at 512, 136 / 118 at 1024, 919 / 594 at 8192; 8 of up to 1024 tokens 95 / 175 at 1024
+// (7 tiles), 573 / 417 at 8192 (54).
+constexpr int kAttendLatentRows = 128;
+constexpr int64_t kAttendLatentWork = int64_t{16} * 64 * 128;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =
@@ -1246,10 +1255,11 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
     if (plan.ok)
       return cuda_status(mx::launch_attend_rows(a, cache->d, shared, plan, static_cast<cudaStream_t>(stream)));
   }
-  if (cache->d == 512 && shared && T * static_cast<int64_t>(a.group) > static_cast<int64_t>(B) * kAttendLatentRows) {
-    const int64_t rows = static_cast<int64_t>(T) * a.group;
-    return cuda_status(mx::launch_attend_latent(a, rows <= 16ll * B ? 16 : rows <= 32ll * B ? 32 : 64, h->sm_count,
-                                                static_cast<cudaStream_t>(stream)));
+  // rows x tokens of the work, where every sequence is as long as the table has room for
+  if (cache->d == 512 && shared && static_cast<int64_t>(T) * a.group >= static_cast<int64_t>(B) * kAttendLatentRows &&
+      static_cast<int64_t>(T) * a.group * (static_cast<int64_t>(table_cols) * cache->page_size) >=
+          static_cast<int64_t>(h->sm_count) * kAttendLatentWork) {
+    return cuda_status(mx::launch_attend_latent(a, h->sm_count, static_cast<cudaStream_t>(stream)));
   }
   const int of_rows = static_cast<int64_t>(T) * a.group <= static_cast<int64_t>(B) * 8 ? variant + mx::kAttendVariants / 2 : variant;
   return cuda_status(mx::launch_attend(a, of_rows, h->attend_ctas[of_rows], static_cast<cudaStream_t>(stream)));

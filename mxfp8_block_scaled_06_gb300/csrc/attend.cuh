@@ -233,7 +233,7 @@ __host__ __device__ constexpr size_t cut_bytes(int ctas) { return static_cast<si
 // Block c is that of the cut where the run of CTA c + 1 begins. A unit of n parts has n - 1 cuts, whose
 // blocks share its rows' pieces of 128 dimensions (64 at d = 64). A warp adds up a piece of
 // some parts in the order of the runs; where there are many, 2 to 8 warps share a piece.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kAtOnce = 4;
 template <int D, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int ctas) {
   constexpr int kPiece = D < 128 ? D : 128, kVec = kPiece / 32;  // floats of a thread
@@ -258,25 +258,38 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     const bool here = piece < kPieces && cut.row0 + r < cut.rows;
     float top = -INFINITY, sum = 0.f, v[kVec] = {};
     if (here) {
-#pragma unroll 8
-      for (int p = p0; p < p1; ++p) {
-        const float* from = part(p);
-        const float m = from[r], l = from[kRows + r];
-        float y[kVec];
-        if constexpr (kVec == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(from + 2 * kRows + r * D + d);
-          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(from + 2 * kRows + r * D + d);
-          y[0] = z.x, y[1] = z.y;
+#pragma unroll 1
+      for (int p = p0; p < p1; p += kAtOnce) {
+        // all loads first; behind the last part, that one again, which is not used
+        float m[kAtOnce], l[kAtOnce], y[kAtOnce][kVec];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float* from = part(min(p + i, p1 - 1));
+          m[i] = from[r], l[i] = from[kRows + r];
+          if constexpr (kVec == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(from + 2 * kRows + r * D + d);
+            y[i][0] = z.x, y[i][1] = z.y, y[i][2] = z.z, y[i][3] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(from + 2 * kRows + r * D + d);
+            y[i][0] = z.x, y[i][1] = z.y;
+          }
         }
-        const float most = fmaxf(top, m);
+        float most = top;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) most = fmaxf(most, m[i]);
         // a row that saw nothing yet, or here, adds nothing, or the NaN that it saw
         const float keep = top == -INFINITY ? (sum != sum ? sum : 0.f) : exp2f(top - most);
-        const float f = m == -INFINITY ? (l != l ? l : 0.f) : exp2f(m - most);
-        sum = sum * keep + l * f;
+        sum *= keep;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = v[e] * keep + y[e] * f;
+        for (int e = 0; e < kVec; ++e) v[e] *= keep;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (p + i >= p1) break;
+          const float f = m[i] == -INFINITY ? (l[i] != l[i] ? l[i] : 0.f) : exp2f(m[i] - most);
+          sum += l[i] * f;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) v[e] += y[i][e] * f;
+        }
         top = most;
       }
     }

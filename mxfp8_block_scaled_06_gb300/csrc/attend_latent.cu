@@ -1,19 +1,21 @@
 // attend_latent.cu - attention over latents of 512 dimensions in the MXFP4 cache, which are keys and
-// values in one: decode steps of many heads, drafts, prompts.
+// values in one: prompts, and drafts of many tokens.
 //
 // On the 5th-generation tensor cores with the cache as the products' rows: for 128 tokens
-//   S^T[token, row] = sum_d latent[token, d] Q[row, d]    (128 x R x 512)
-//   O^T[d, row]    += sum_t latent[t, d] P[t, row]        (4 times 128 x R x 128)
-// R = 16, 32 or 64 query rows. The latents are dequantized once, to fp16 in shared memory, [8 chunks of 64
+//   S^T[token, row] = sum_d latent[token, d] Q[row, d]    (128 x 64 x 512)
+//   O^T[d, row]    += sum_t latent[t, d] P[t, row]        (4 times 128 x 64 x 128)
+// for 64 query rows. The latents are dequantized once, to fp16 in shared memory, [8 chunks of 64
 // dimensions][128 tokens][128 bytes in the 128-byte swizzle], and read from there by both: K-major
 // for the scores, M-major for the sums. fp16 under powers of two as in attend_rows.cu: the codes
 // relative to the largest scale so far, weights 2^7 above a reference that a score may exceed by 2^8.
 //
-// Bound by shared memory: a token's 1024 bytes are written once and read twice there, 24 cycles of
-// an SM, whatever R is (the cache's 272 bytes take 12 from HBM). The fp16 tile fills it, so
-// there is one, and its chunks change hands singly: while the sums of tile j go from one 128
-// dimensions to the next, the chunks behind them are written for tile j + 1, and its scores
-// follow these.
+// The fp16 tile fills the shared memory, so there is one, and its chunks change hands singly: while the sums
+// of tile j go from one 128 dimensions to the next, the chunks behind them are written for tile
+// j + 1, and its scores follow these. What bounds it is that chain: a tile takes 6900 cycles, of which 3400 are
+// the 64 products (53 cycles each, shared memory's rate; 68 for 128 rows, which it has no room for),
+// 1000 to 1800 the weights between them, the rest the last chunk's way to the scores. Two prompts of up to
+// 6000 tokens and 16 heads: 945 us, 375 TFLOP/s, against 1609 us with 16 rows at a time (attend.cu).
+// A run's first tile begins 18000 cycles after its launch and its results take 6000.
 //
 // Four warps have a token to a thread and turn S to P (rows' references and sums in shared memory),
 // eight dequantize, one issues the products; one CTA to an SM, its run of tiles as in attend.cu.
@@ -30,22 +32,18 @@ namespace {
 constexpr int kD = 512;
 constexpr int kTokens = 128;
 static_assert(kTokens == kAttendTile, "tiles of the sequences' work");
+constexpr int kRows = 64;  // of queries
 constexpr int kBlocks = kD / 32, kChunks = kD / 64;
 constexpr int kSoftmax = 4, kDequant = 8, kWarpsAll = kSoftmax + kDequant + 1, kThreads = 32 * kWarpsAll;
 constexpr float kLag = 8.f, kTop = 7.f;
 constexpr int kCodeBits = 13;  // 6 * 2^13 < 65504
 
-template <int kRows>
-struct Plan {
-  static constexpr int kTile = kTokens * kD * 2;
-  static constexpr int kOffQ = kTile;                       // [chunk][row][128 bytes]
-  static constexpr int kOffP = kOffQ + kRows * kD * 2;      // [token][128 bytes], the first 2 R of them
-  static constexpr int kBytes = kOffP + kTokens * 128 + 1024;
-  static constexpr int kColO = kRows;                       // S^T, then O^T of each 128 dimensions
-  static constexpr int kCols = 5 * kRows <= 128 ? 128 : 5 * kRows <= 256 ? 256 : 512;
-};
+constexpr int kOffQ = kTokens * kD * 2;                 // [chunk][row][128 bytes]
+constexpr int kOffP = kOffQ + kRows * kD * 2;           // [token][128 bytes]
+constexpr int kBytes = kOffP + kTokens * 128 + 1024;
+constexpr int kColO = kRows;                            // S^T, then O^T of each 128 dimensions
+constexpr int kCols = 512;                              // 5 * kRows of them, and a power of two
 
-template <int kRows>
 struct Shared {
   uint64_t pair_full[4], sums_done[4], s_full, p_full, q_full;
   uint32_t tmem;
@@ -59,10 +57,26 @@ struct Shared {
   alignas(16) float factor[kRows], m[kRows], keep[kRows];
   int lo[kRows], hi[kRows];
   float part[kSoftmax][kRows];
+  size_t to[kRows];  // places of the rows' results
 };
 
+// Over the warp's lanes, of 16 values in each: lane i has f of them all for value i / 2. 16 shuffles,
+// where one value after the other takes 80.
+template <typename F>
+__device__ __forceinline__ float reduce16(const float (&x)[16], int lane, F f) {
+  float a[8], b[4], c[2];
+  const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4, h2 = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = f(h16 ? x[i + 8] : x[i], __shfl_xor_sync(kFull, h16 ? x[i] : x[i + 8], 16));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = f(h8 ? a[i + 4] : a[i], __shfl_xor_sync(kFull, h8 ? a[i] : a[i + 4], 8));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) c[i] = f(h4 ? b[i + 2] : b[i], __shfl_xor_sync(kFull, h4 ? b[i] : b[i + 2], 4));
+  const float y = f(h2 ? c[1] : c[0], __shfl_xor_sync(kFull, h2 ? c[0] : c[1], 2));
+  return f(y, __shfl_xor_sync(kFull, y, 1));
+}
+
 // The segments of this CTA's run, one after another, the same for every role.
-template <int kRows>
 struct Walk {
   int64_t at, stop, run, seq_first;
   int b;
@@ -71,6 +85,7 @@ struct Walk {
   int tile0, tile1;   // of the unit
   int t_begin, t_end; // tokens of these tiles that any row of the unit sees, from a tile's first
   int tiles;          // of 128 tokens to take
+  int hi_least, lo_most;  // tokens from lo_most to hi_least are seen by all rows
   bool begin;
   __device__ __forceinline__ void start(const AttendArgs& a, const Found& f, int64_t total) {
     run = run_of(total, gridDim.x);
@@ -108,15 +123,15 @@ struct Walk {
     t_end = min(t_end, to);
     if (from > t_begin) t_begin += (from - t_begin) / kTokens * kTokens;
     tiles = max((t_end - t_begin + kTokens - 1) / kTokens, 0);
+    hi_least = a.causal ? min(pos0 + 1, s.len) : s.len;
+    lo_most = a.window > 0 ? pos1 - a.window + 1 : 0;
     return true;
   }
 };
 
-template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const AttendArgs a) {
-  using L = Plan<kRows>;
   extern __shared__ __align__(1024) uint8_t raw[];
-  __shared__ Shared<kRows> sh;
+  __shared__ Shared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kIssue = kSoftmax + kDequant;
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kIssue) tmem_alloc(smem_u32(&sh.tmem), L::kCols);
+  if (warp == kIssue) tmem_alloc(smem_u32(&sh.tmem), kCols);
   pdl_wait();
   int64_t total;
   const Found found = find_run<kRows, kWarpsAll>(a, sh.scan, total);
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
   auto wait_warp = [&](uint64_t& bar, uint32_t n) { return __all_sync(kFull, wait(bar, n)) != 0; };
-  Walk<kRows> w;
+  Walk w;
   w.start(a, found, total);
   Cut* cuts = reinterpret_cast<Cut*>(a.partial);
   if (threadIdx.x == 0 && w.at >= w.stop) cuts[blockIdx.x].last = -1;
@@ -176,41 +191,45 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         cuts[blockIdx.x] = cut;
       }
       // ---- queries to fp16, a warp to a row at a time: each row's largest into [2^14, 2^15)
-      for (int r = warp; r < kRows; r += kSoftmax) {
-        int token, q_head;
-        const bool valid = w.un.row(a, w.s, r, token, q_head);
-        const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
-        uint4 v[2];
-        uint32_t most = 0;
+      // (four rows' loads at a time)
+#pragma unroll 1
+      for (int r0 = warp; r0 < kRows; r0 += 4 * kSoftmax) {
+        uint4 v[4][2];
+        int pos[4];
+        bool there[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          v[j] = valid ? *reinterpret_cast<const uint4*>(q + (lane + 32 * j) * 8) : make_uint4(0, 0, 0, 0);
-          most = max(most, max_bits(v[j]));
-        }
-        most = __reduce_max_sync(kFull, most);
-        const int shift = query_shift(most, a.q_f16);
-        const float f = a.scale_log2 < 0.f ? -pow2(shift) : pow2(shift);
+        for (int i = 0; i < 4; ++i) {
+          int token, q_head;
+          const bool valid = w.un.row(a, w.s, r0 + i * kSoftmax, token, q_head);
+          const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int ch = lane + 32 * j;
-          sts128(base + L::kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                 query_f16(v[j], a.q_f16, f));
+          for (int j = 0; j < 2; ++j)
+            v[i][j] = valid ? *reinterpret_cast<const uint4*>(q + (lane + 32 * j) * 8) : make_uint4(0, 0, 0, 0);
+          pos[i] = w.s.len - w.s.n + token - w.s.q0;
+          there[i] = valid;
         }
-        if (lane == 0) {
-          const int pos = w.s.len - w.s.n + token - w.s.q0;
-          sh.factor[r] = pow2(-shift) * fabsf(a.scale_log2);
-          sh.m[r] = -INFINITY;
-          sh.hi[r] = !valid ? 0 : a.causal ? min(pos + 1, w.s.len) : w.s.len;
-          sh.lo[r] = a.window > 0 ? pos - a.window + 1 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i * kSoftmax;
+          const int shift = query_shift(__reduce_max_sync(kFull, max(max_bits(v[i][0]), max_bits(v[i][1]))), a.q_f16);
+          const float f = a.scale_log2 < 0.f ? -pow2(shift) : pow2(shift);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int ch = lane + 32 * j;
+            sts128(base + kOffQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   query_f16(v[i][j], a.q_f16, f));
+          }
+          if (lane == 0) {
+            sh.factor[r] = pow2(-shift) * fabsf(a.scale_log2);
+            sh.m[r] = -INFINITY;
+            sh.hi[r] = !there[i] ? 0 : a.causal ? min(pos[i] + 1, w.s.len) : w.s.len;
+            sh.lo[r] = a.window > 0 ? pos[i] - a.window + 1 : 0;
+          }
         }
       }
       fence_proxy_async_smem();
       if (w.tiles > 0) arrive_warp(sh.q_full);
       named_barrier_sync(1, 32 * kSoftmax);
-      int hi_least = w.s.len, lo_most = 0;
-      for (int r = 0; r < kRows; ++r)
-        if (w.un.row0 + r < w.un.rows) hi_least = min(hi_least, sh.hi[r]), lo_most = max(lo_most, sh.lo[r]);
-
       float l[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) l[r] = 0.f;
@@ -226,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         const bool nan = sh.any_nan[par] != 0 && sh.nan[par][tid] != 0;
         const int t0 = w.t_begin + j * kTokens, t = t0 + tid;
         // tokens that not every row sees, or NaN
-        const bool special = t0 < lo_most || t0 + kTokens > hi_least || sh.any_nan[par] != 0;
+        const bool special = t0 < w.lo_most || t0 + kTokens > w.hi_least || sh.any_nan[par] != 0;
         // scores of 16 rows of this token
         auto scores = [&](int r0, float (&x)[16]) {
           uint32_t v[16];
@@ -263,14 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
           // the rows' references become their maxima
 #pragma unroll 1
           for (int r0 = 0; r0 < kRows; r0 += 16) {
-            if constexpr (kRows > 16) scores(r0, x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float y = x[i];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(kFull, y, o));
-              if (lane == 0) sh.part[warp][r0 + i] = y;
-            }
+            scores(r0, x);
+            const float y = reduce16(x, lane, [](float p, float q) { return fmaxf(p, q); });
+            if ((lane & 1) == 0) sh.part[warp][r0 + lane / 2] = y;
           }
           named_barrier_sync(1, 32 * kSoftmax);
           if (tid < kRows) {
@@ -288,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
 #pragma unroll 1
             for (int c = 0; c < 4 * kRows; c += 16) {
               uint32_t v[16];
-              tmem_ld_32x32b_x16_nowait(tmem + lanes + L::kColO + c, v);
+              tmem_ld_32x32b_x16_nowait(tmem + lanes + kColO + c, v);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * (by * sh.keep[c % kRows + i]));
-              tmem_st16(tmem + lanes + L::kColO + c, v);
+              tmem_st16(tmem + lanes + kColO + c, v);
             }
             tmem_st_wait();
           }
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
         ref = new_ref;
 #pragma unroll
         for (int r0 = 0; r0 < kRows; r0 += 16) {
-          if constexpr (kRows > 16) scores(r0, x);
+          scores(r0, x);
           uint32_t p[8];
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
@@ -315,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
             p[i / 2] = pack_f16(y[0], y[1]);
             p[i / 2 + 1] = pack_f16(y[2], y[3]);
           }
-          const uint32_t to = base + L::kOffP + tid * 128;
+          const uint32_t to = base + kOffP + tid * 128;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             sts128(to + (((r0 / 8 + i) ^ (tid & 7)) << 4), make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
@@ -329,53 +343,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       if (w.tiles > 0) ok = ok && wait_warp(sh.sums_done[3], done);
       tc_fence_after();
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float v = l[r];
+      for (int r0 = 0; r0 < kRows; r0 += 16) {
+        float x[16];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-        if (lane == 0) sh.part[warp][r] = v;
+        for (int i = 0; i < 16; ++i) x[i] = l[r0 + i];
+        const float y = reduce16(x, lane, [](float p, float q) { return p + q; });
+        if ((lane & 1) == 0) sh.part[warp][r0 + lane / 2] = y;
       }
       named_barrier_sync(1, 32 * kSoftmax);
       const bool whole = w.tile0 == 0 && w.tile1 == w.s.tiles;
       float* part = parts0 + (static_cast<size_t>(blockIdx.x) * 2 + (w.begin ? 0 : 1)) * kPartFloats<kD, kRows>;
+      if (tid < kRows) {
+        int token, q_head;
+        const bool valid = w.un.row(a, w.s, tid, token, q_head);
+        const float sum = sh.part[0][tid] + sh.part[1][tid] + sh.part[2][tid] + sh.part[3][tid];
+        sh.keep[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        sh.to[tid] = static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+        if (valid && !whole) {
+          part[tid] = sh.m[tid] - kTop;
+          part[kRows + tid] = sum;
+        } else if (valid && a.lse != nullptr) {
+          a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (sh.m[tid] - kTop + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+      named_barrier_sync(1, 32 * kSoftmax);
       const float to_m = w.tiles > 0 ? pow2(max(ref - 127 - kCodeBits, -126)) : 0.f;
 #pragma unroll 1
       for (int c = 0; c < 4 * kRows; c += 16) {
         uint32_t v[16];
         if (w.tiles > 0) {
-          tmem_ld_32x32b_x16_nowait(tmem + lanes + L::kColO + c, v);
+          tmem_ld_32x32b_x16_nowait(tmem + lanes + kColO + c, v);
           tmem_ld_wait();
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0u;
         }
-        const int d = c / kRows * 128 + tid;
+        const int d = c / kRows * 128 + tid, r0 = c % kRows, rows = w.un.rows - w.un.row0 - r0;
+        if (!whole) {
+          float* to = part + 2 * kRows + r0 * kD + d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < rows) to[i * kD] = __uint_as_float(v[i]) * to_m;
+          continue;
+        }
+        // the places and factors before the first store, which might be to them for all that is known
+        size_t to[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int r = c % kRows + i;
-          if (w.un.row0 + r >= w.un.rows) break;
-          const float sum = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
-          const float y = __uint_as_float(v[i]) * to_m;
-          if (whole) {
-            int token, q_head;
-            w.un.row(a, w.s, r, token, q_head);
-            a.out[static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head + d] =
-                static_cast<uint16_t>(pack_out(sum == 0.f ? 0.f : y / sum, 0.f, a.q_f16));
-          } else {
-            part[2 * kRows + r * kD + d] = y;
-          }
+          to[i] = sh.to[r0 + i];
+          v[i] = pack_out(__uint_as_float(v[i]) * sh.keep[r0 + i] * to_m, 0.f, a.q_f16);
         }
-      }
-      if (tid < kRows && w.un.row0 + tid < w.un.rows) {
-        const float sum = sh.part[0][tid] + sh.part[1][tid] + sh.part[2][tid] + sh.part[3][tid];
-        if (!whole) {
-          part[tid] = sh.m[tid] - kTop;
-          part[kRows + tid] = sum;
-        } else if (a.lse != nullptr) {
-          int token, q_head;
-          w.un.row(a, w.s, tid, token, q_head);
-          a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (sh.m[tid] - kTop + log2f(sum)) * 0.6931471805599453f;
-        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < rows) a.out[to[i] + d] = static_cast<uint16_t>(v[i]);
       }
       tc_fence_before();
       ok = !named_barrier_or(1, 32 * kSoftmax, !ok);  // the rows' words are read; all go on, or none
@@ -491,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     uint32_t units = 0;
     const uint32_t id_s = idesc_f16(kRows, false), id_o = idesc_f16(kRows, true, true);
     const uint32_t d0 = __shfl_sync(kFull, tmem, 0);
-    const uint32_t k_lo = sw128_lo(base), q_lo = sw128_lo(base + L::kOffQ), v_lo = sw128_lo(base, kTokens * 128),
-                   p_lo = sw128_lo(base + L::kOffP);
+    const uint32_t k_lo = sw128_lo(base), q_lo = sw128_lo(base + kOffQ), v_lo = sw128_lo(base, kTokens * 128),
+                   p_lo = sw128_lo(base + kOffP);
     while (ok && w.next(a)) {
       if (w.tiles == 0) continue;
       ++units;
@@ -521,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
           if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < kTokens / 16; ++i)
-              mma_ss(d0 + L::kColO + m * kRows, v_lo + 2 * m * (kTokens * 8) + i * 128, kSw128Hi, p_lo + i * 128, kSw128Hi,
+              mma_ss(d0 + kColO + m * kRows, v_lo + 2 * m * (kTokens * 8) + i * 128, kSw128Hi, p_lo + i * 128, kSw128Hi,
                      id_o, j > 0 || i > 0);
             tc_commit(smem_u32(&sh.sums_done[m]));
           }
@@ -534,39 +554,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssue) tmem_dealloc(tmem, L::kCols);
-}
-
-template <typename F>
-auto with_rows(int rows, F&& f) {
-  if (rows == 16) return f(attend_latent_kernel<16>, attend_join_kernel<kD, 16>, Plan<16>::kBytes);
-  if (rows == 32) return f(attend_latent_kernel<32>, attend_join_kernel<kD, 32>, Plan<32>::kBytes);
-  return f(attend_latent_kernel<64>, attend_join_kernel<kD, 64>, Plan<64>::kBytes);
+  if (warp == kIssue) tmem_dealloc(tmem, kCols);
 }
 
 }  // namespace
 
 cudaError_t set_attend_latent_attributes() {
-  for (int rows = 16; rows <= 64; rows *= 2) {
-    const cudaError_t e = with_rows(rows, [](auto kernel, auto, int bytes) {
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    });
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return cudaFuncSetAttribute(attend_latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
 }
 
 size_t attend_latent_bytes(int sm_count) {
-  return cut_bytes(sm_count) + static_cast<size_t>(sm_count) * 2 * 64 * (kD + 2) * sizeof(float);
+  return cut_bytes(sm_count) + static_cast<size_t>(sm_count) * 2 * kPartFloats<kD, kRows> * sizeof(float);
 }
 
-cudaError_t launch_attend_latent(const AttendArgs& a, int rows, int sm_count, cudaStream_t stream) {
-  return with_rows(rows, [&](auto kernel, auto join, int bytes) {
-    const int ctas = attend_ctas(a, rows, sm_count);
-    const cudaError_t e = launch_overlapping(kernel, dim3(ctas), kThreads, bytes, stream, a);
-    if (e != cudaSuccess || ctas < 2) return e;
-    return launch_overlapping(join, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
-  });
+cudaError_t launch_attend_latent(const AttendArgs& a, int sm_count, cudaStream_t stream) {
+  const int ctas = attend_ctas(a, kRows, sm_count);
+  const cudaError_t e = launch_overlapping(attend_latent_kernel, dim3(ctas), kThreads, kBytes, stream, a);
+  if (e != cudaSuccess || ctas < 2) return e;
+  return launch_overlapping(attend_join_kernel<kD, kRows>, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
 }
 
 }  // namespace mx

@@ -418,10 +418,10 @@ int attend_variant(int d, bool shared);  // the one of 16 rows; -1: no such head
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]);
 size_t attend_bytes(int d, int ctas, int rows);
 cudaError_t launch_attend(const AttendArgs& args, int variant, int ctas, cudaStream_t stream);
-// Latents of 512 dimensions that are keys and values in one, in units of 16, 32 or 64 rows.
+// Latents of 512 dimensions that are keys and values in one, in units of 64 rows.
 cudaError_t set_attend_latent_attributes();
 size_t attend_latent_bytes(int sm_count);
-cudaError_t launch_attend_latent(const AttendArgs& args, int rows, int sm_count, cudaStream_t stream);
+cudaError_t launch_attend_latent(const AttendArgs& args, int sm_count, cudaStream_t stream);
 // Many query rows (head dims up to 256): blocks of rows, and splits of their tokens.
 constexpr int kAttendRowsVariants = 6;
 struct AttendRowsPlan {

@@ -1,4 +1,4 @@
-"""mx_attend over latents of 512 dimensions (keys and values in one) in units of 16, 32 and 64 rows."""
+"""mx_attend over latents of 512 dimensions (keys and values in one), many rows and room for long sequences."""
 import pytest
 import torch
 
@@ -10,14 +10,21 @@ pytestmark = pytest.mark.gpu
 
 
 def case(mx, lengths, counts, group=16, heads=1, **kw):  # noqa: F811
-    return Case(mx, lengths, counts, group, heads, 512, True, **kw)
+    """The sequences, and behind them one with so many queries that 128 rows or more come to each, in a wide table."""
+    more = max(0, -(-128 * (len(lengths) + 1) // group) - sum(counts)) if sum(counts) * group < 128 * len(lengths) else 0
+    c = Case(mx, lengths + [90] * (more > 0), counts + [more] * (more > 0), group, heads, 512, True, **kw)
+    cols = 160 * 16 * 64 * 128 // (len(c.q) * group * c.page) + 1
+    wide = torch.full((len(c.table), max(cols, c.table.shape[1])), -1, dtype=torch.int32, device=dev())
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    return c
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("group,heads", [(16, 1), (9, 2), (20, 1), (48, 1)])
-def test_single_tokens(mx, group, heads, dtype):  # noqa: F811
+def test_equal_queries(mx, group, heads, dtype):  # noqa: F811
     lengths = [1, 16, 17, 127, 128, 129, 255, 300, 513]
-    c = case(mx, lengths, [1] * len(lengths), group, heads, dtype=dtype, page=48)
+    c = case(mx, lengths, [-(-128 // group)] * len(lengths), group, heads, dtype=dtype, page=48)
     out, lse = c.run(lse=True, q_offsets=None)
     c.check(out, lse)
 
@@ -75,7 +82,7 @@ def test_nan_reaches_the_rows_that_see_it(mx, window, tokens):  # noqa: F811
         want |= (pos >= t) & ((pos < t + window) if window else True)
     assert want.any() and not want.all()
     assert torch.equal(torch.isnan(out[:120]).all(2).all(1), want) and torch.equal(torch.isnan(lse[:120]).all(1), want)
-    assert not torch.isnan(out[:120][~want]).any() and not torch.isnan(out[120:]).any()
+    assert not torch.isnan(out[:120][~want]).any() and not torch.isnan(out[120:140]).any()
 
 
 def test_nan_and_infinite_queries_stay_in_their_rows(mx):  # noqa: F811
@@ -84,7 +91,7 @@ def test_nan_and_infinite_queries_stay_in_their_rows(mx):  # noqa: F811
     c.q[0, 1, 7] = float("nan")
     c.q[4, 3, 9] = float("inf")
     out = c.run()
-    bad = torch.zeros(5, 16, dtype=torch.bool, device=dev())
+    bad = torch.zeros(len(c.q), 16, dtype=torch.bool, device=dev())
     bad[0, 1] = bad[4, 3] = True
     assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
 
