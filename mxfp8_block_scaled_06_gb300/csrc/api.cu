@@ -1111,7 +1111,7 @@ mx::CacheRows cache_rows(const mx_handle* h, const mx_cache* c, int rows, const 
   a.rows = rows;
   a.sides = c->v != nullptr ? 2 : 1;
   a.heads = static_cast<uint32_t>(c->heads);
-  a.head_units = static_cast<uint32_t>(c->d / 8);
+  a.head_units = static_cast<uint32_t>(c->d / 16);
   a.page_size = static_cast<uint32_t>(c->page_size);
   a.slot_count = static_cast<int64_t>(c->pages) * c->page_size;
   a.slots = slots;

@@ -45,17 +45,6 @@ __device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b, int rows) {
   s.row_tiles = (s.n * a.group + rows - 1) / rows;
   return s;
 }
-// The four bytes of w, two codes each, as fp16 pairs (low code in the low half).
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

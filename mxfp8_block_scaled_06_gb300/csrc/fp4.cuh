@@ -32,14 +32,6 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8], float f) {
   return r;
 }
 
-// The value of E2M1 code c (sign in bit 3): the magnitude's exponent and mantissa
-// bits are those of a float 2^126 times smaller, shifted into place; one exact
-// multiplication restores the exponent (and makes code 1 the subnormal 0.5).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const float m = __uint_as_float((c & 7u) << 22) * __uint_as_float(253u << 23);
-  return __uint_as_float(__float_as_uint(m) | ((c & 8u) << 28));
-}
-
 // Eight elements as loaded, their values, and the bits of the largest magnitude as a
 // float: at or above Inf's bits when any element is Inf or NaN.
 template <typename T>
@@ -102,14 +94,31 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
          : s < 255u ? __uint_as_float(s << 23)
                     : __uint_as_float(0x7FC00000u);
 }
-// Eight codes times f in bf16, exact where f is a scale (one mantissa bit).
+// The four bytes of w, two codes each, as fp16 pairs (low code in the low half).
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes times f in bf16, exact where f is a scale (one mantissa bit). Exponent and upper
+// mantissa bits of an fp16 code are those of a bf16 number 2^112 times smaller.
 __device__ __forceinline__ uint4 e2m1_values_bf16(uint32_t codes, float f) {
+  const uint32_t f2 = (__float_as_uint(f) >> 16) * 0x10001u;
   uint32_t w[4];
+  codes_f16(codes, w);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float a = e2m1_value(codes >> (8 * e)) * f, b = e2m1_value(codes >> (8 * e + 4)) * f;
-    w[e] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);  // exact: the low halves are zero
-  }
+  for (int e = 0; e < 4; ++e)
+    w[e] = mul_bf16x2(mul_bf16x2((w[e] >> 3 & 0x0FFF0FFFu) | (w[e] & 0x80008000u), 0x77807780u), f2);  // 2^112
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -360,7 +360,8 @@ int rope_vec(const RopeRows& a, int size);
 cudaError_t launch_rope(const RopeRows& a, int x_type, cudaStream_t stream);
 
 // ------------------------------------------------------------ attention cache
-// From this many 8-element units on a thread takes four.
+// From this many 16-element units on a thread takes two (8 heads of 128, read, one against two: 4096 rows 5.0 us
+// both, 16381 rows 14.0 and 13.3, 32749 rows 32.5 and 30.4; four: 5.6, 12.9, 28.5 and 7.9 instead of 7.2 at 8192).
 constexpr uint32_t kCacheManyUnits = 1u << 19;
 struct CacheSide {
   const void* x;  // write: [rows, heads, d], strides ldx and ldx_head elements
@@ -372,7 +373,7 @@ struct CacheSide {
 };
 struct CacheRows {
   int rows, sides;
-  uint32_t heads, head_units;  // head_units = d / 8
+  uint32_t heads, head_units;  // head_units = d / 16
   uint32_t page_size;
   int64_t slot_count;  // pages * page_size, below 2^31
   const int64_t* slots;

@@ -72,8 +72,8 @@ def test_write_and_read(mx, t, heads, d, page, shared, dtype):  # noqa: F811
 
 
 def test_many_rows(mx):  # noqa: F811
-    """Enough rows that a thread takes four units, the last ones short of it."""
-    h, t, heads, d, page = handle(), 8191, 4, 128, 64
+    """Enough rows that a thread takes two units, the last ones short of it."""
+    h, t, heads, d, page = handle(), 8209, 8, 128, 64
     c = mx.MxCache.zeros(h, 131, page, heads, d)
     slots = torch.randperm(131 * page, device=dev())[:t]
     k, v = normal(1, t, heads, d).bfloat16(), normal(2, t, heads, d).bfloat16()
@@ -81,6 +81,22 @@ def test_many_rows(mx):  # noqa: F811
     for x, y, back in zip((k, v), (kv, vv), mx.mx_cache_read(h, c, slots)):
         q, s, want = mx.mx_quantize_rows_fp4(h, x.reshape(t * heads, d), swizzled=False, y=True)
         assert torch.equal(y.view(-1), want.view(-1)) and torch.equal(back.view(-1), want.view(-1))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_rows_that_begin_within_32_bytes(mx, dtype):  # noqa: F811
+    h, t, heads, d, page = handle(), 37, 3, 96, 16
+    c = mx.MxCache.zeros(h, 4, page, heads, d)
+    slots = torch.randperm(4 * page, device=dev())[:t]
+    k, v = (torch.empty(t * (heads * (d + 8) + 8) + 8, device=dev(), dtype=dtype)[8:].as_strided((t, heads, d), (heads * (d + 8) + 8, d + 8, 1))
+            .copy_(normal(i, t, heads, d)) for i in (1, 2))
+    outs = [torch.zeros(t * heads * d + 8, device=dev(), dtype=dtype)[(4 if dtype is torch.float32 else 8):][:t * heads * d].view(t, heads, d) for _ in range(2)]
+    assert all(x.data_ptr() % 32 == 16 for x in outs)
+    values = mx.mx_cache_write(h, c, slots, k, v, values=True)
+    mx.mx_cache_read(h, c, slots, dtype=dtype, k=outs[0], v=outs[1])
+    for x, y, back in zip((k, v), values, outs):
+        want = mx.mx_quantize_rows_fp4(h, x.reshape(t * heads, d), swizzled=False, y=True)[2].view(t, heads, d)
+        assert torch.equal(y, want) and torch.equal(back, want.to(dtype))
 
 
 def test_special_blocks(mx):  # noqa: F811
