@@ -1241,7 +1241,7 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
   a.per_page = mx::fast_div(static_cast<uint32_t>(cache->page_size / 16));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = std::min(window, 1 << 30);  // no longer than any sequence, and positions less it are 32-bit
   a.out = static_cast<uint16_t*>(out);
   a.ldo = ldo;
   a.ldo_head = ldo_head;

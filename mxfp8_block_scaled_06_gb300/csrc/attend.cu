@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
   fence_mbar_init();
   pdl_wait();
   int64_t total;
-  const Found found = find_run<kRows, kWarps>(a, scan, total);
+  const Found found = find_run<kRows, kWarps>(a, scan, seq_work, total);
   const int64_t run = run_of(total, gridDim.x);
   int64_t at = run * blockIdx.x;
   const int64_t stop = min(at + run, total);
@@ -866,9 +866,9 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 // f(kernel, join kernel, shared bytes, threads, rows of a unit) of a variant.
 template <int D, bool kShared, typename F>
 auto with_kernels(bool few, F&& f) {
-  return few ? f(attend_kernel<D, kShared, 8>, attend_join_kernel<D, 8>, Layout<D, kShared, 8>::kBytes,
+  return few ? f(attend_kernel<D, kShared, 8>, launch_join<D, 8>, Layout<D, kShared, 8>::kBytes,
                  Layout<D, kShared, 8>::kThreads, 8)
-             : f(attend_kernel<D, kShared, 16>, attend_join_kernel<D, 16>, Layout<D, kShared, 16>::kBytes,
+             : f(attend_kernel<D, kShared, 16>, launch_join<D, 16>, Layout<D, kShared, 16>::kBytes,
                  Layout<D, kShared, 16>::kThreads, 16);
 }
 template <typename F>
@@ -916,7 +916,7 @@ cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream
     ctas = attend_ctas(a, rows, ctas);
     const cudaError_t e = launch_overlapping(kernel, dim3(ctas), threads, bytes, stream, a);
     if (e != cudaSuccess || ctas < 2) return e;
-    return launch_overlapping(join, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
+    return join(a, ctas, stream);
   });
 }
 

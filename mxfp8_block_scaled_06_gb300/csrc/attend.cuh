@@ -135,14 +135,14 @@ struct ScanShared {
 };
 // The work of as many sequences as threads from c on, added up: this thread's sequence's, what is before it,
 // and all.
-template <int kRows, int kWarps>
-__device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh, int c, bool& bad, int64_t& before,
-                                             int64_t& all) {
+template <int kRows, int kWarps, typename Work>
+__device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh, int c, Work work, bool& bad,
+                                             int64_t& before, int64_t& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = c + threadIdx.x;
   int64_t w = 0;
   if (b < a.B) {
     const Seq s = seq_of(a, b, kRows);
-    w = seq_work(a, s);
+    w = work(a, s);
     bad |= s.bad;
   }
   int64_t sum = w;
@@ -166,26 +166,26 @@ __device__ __forceinline__ int64_t scan_work(const AttendArgs& a, ScanShared& sh
 // Tiles of each CTA's run: an equal share.
 __device__ __forceinline__ int64_t run_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
 // All work, and the sequence in which the run of this CTA begins (where it has one).
-template <int kRows, int kWarps>
-__device__ __forceinline__ Found find_run(const AttendArgs& a, ScanShared& sh, int64_t& total) {
+template <int kRows, int kWarps, typename Work>
+__device__ __forceinline__ Found find_run(const AttendArgs& a, ScanShared& sh, Work work, int64_t& total) {
   constexpr int kThreads = 32 * kWarps;
   bool bad = false;
   int64_t before, all;
-  const int64_t w = scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
+  const int64_t w = scan_work<kRows, kWarps>(a, sh, 0, work, bad, before, all);
   total = all;
   for (int c = kThreads; c < a.B; c += kThreads) {
     int64_t x;
-    scan_work<kRows, kWarps>(a, sh, c, bad, x, all);
+    scan_work<kRows, kWarps>(a, sh, c, work, bad, x, all);
     total += all;
   }
   if (blockIdx.x == 0 && bad) atomicOr(a.status, kStatusBadInput);
   const int64_t at = run_of(total, gridDim.x) * blockIdx.x;
   if (before <= at && at < before + w) sh.found = Found{static_cast<int>(threadIdx.x), before};
   if (a.B > kThreads) {
-    scan_work<kRows, kWarps>(a, sh, 0, bad, before, all);
+    scan_work<kRows, kWarps>(a, sh, 0, work, bad, before, all);
     int64_t base = all;
     for (int c = kThreads; c < a.B; c += kThreads, base += all) {
-      const int64_t v = scan_work<kRows, kWarps>(a, sh, c, bad, before, all);
+      const int64_t v = scan_work<kRows, kWarps>(a, sh, c, work, bad, before, all);
       if (base + before <= at && at < base + before + v) sh.found = Found{c + static_cast<int>(threadIdx.x), base + before};
     }
   }
@@ -220,9 +220,11 @@ __host__ __device__ constexpr size_t cut_bytes(int ctas) { return static_cast<si
 
 // ------------------------------------------------------------- joining
 // Block c is that of the cut where the run of CTA c + 1 begins. A unit of n parts has n - 1 cuts, whose
-// blocks share its rows' pieces of 128 dimensions (64 at d = 64). A warp adds up a piece of
+// blocks (one each, or one for 32 pieces) share its rows' pieces of 128 dimensions (64 at d = 64). A warp adds up a piece of
 // some parts in the order of the runs; where there are many, 2 to 8 warps share a piece.
 constexpr int kJoinThreads = 256, kAtOnce = 4;
+template <int D, int kRows>
+constexpr int kJoinBlocks = kRows * D / (D < 128 ? D : 128) > 32 ? kRows * D / (D < 128 ? D : 128) / 32 : 1;  // of a cut
 template <int D, int kRows>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int ctas) {
   constexpr int kPiece = D < 128 ? D : 128, kVec = kPiece / 32;  // floats of a thread
@@ -235,7 +237,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
   if (cut.last < 0) return;
   const float* parts0 = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.partial) + cut_bytes(ctas));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = cut.last - cut.first + 1, blocks = n - 1, block = static_cast<int>(blockIdx.x) - cut.first;
+  const int n = cut.last - cut.first + 1, blocks = (n - 1) * gridDim.y;
+  const int block = (static_cast<int>(blockIdx.x) - cut.first) * gridDim.y + blockIdx.y;
   const int team = n > 64 ? 8 : n > 32 ? 4 : n > 16 ? 2 : 1;  // warps to a piece
   const int at_once = kWarpsHere / team, share = warp % team;
   const int each = (n + team - 1) / team, p0 = min(share * each, n), p1 = min(p0 + each, n);
@@ -336,6 +339,12 @@ cudaError_t launch_overlapping(Kernel kernel, dim3 grid, int threads, int bytes,
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int kRows>
+cudaError_t launch_join(const AttendArgs& a, int ctas, cudaStream_t stream) {
+  return launch_overlapping(attend_join_kernel<D, kRows>, dim3(ctas - 1, kJoinBlocks<D, kRows>), kJoinThreads, 0, stream, a,
+                            ctas);
 }
 
 }  // namespace mx

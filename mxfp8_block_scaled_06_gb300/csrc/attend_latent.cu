@@ -44,17 +44,155 @@ constexpr int kBytes = kOffP + kTokens * 128 + 1024;
 constexpr int kColO = kRows;                            // S^T, then O^T of each 128 dimensions
 constexpr int kCols = 512;                              // 5 * kRows of them, and a power of two
 
+// ------------------------------------------------------------- runs of what rows see
+// Blocks of kRows rows whose first and last tokens differ: block r of R has the tiles of 128 tokens that any
+// of its rows sees, one at least. Blocks r and R - 1 - r stand together, as causal ones have about the same number of
+// tiles between them: places for so many, the most that two have; the last of them may be empty.
+struct Span {
+  int begin, end;  // tokens
+  int tiles;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const Seq& s, int r) {
+  const int rows = s.n * a.group;
+  const int pos0 = s.len - s.n + r * kRows / a.group, pos1 = s.len - s.n + (min((r + 1) * kRows, rows) - 1) / a.group;
+  const int64_t from = static_cast<int64_t>(pos0) - a.window + 1;
+  Span p;
+  p.begin = a.window > 0 && from > 0 ? min(static_cast<int>(from), s.len) & ~15 : 0;
+  p.end = a.causal ? max(min(pos1 + 1, s.len), p.begin) : s.len;
+  p.tiles = max((p.end - p.begin + kAttendTile - 1) / kAttendTile, 1);
+  return p;
+}
+__device__ __forceinline__ int64_t pair_tiles(const AttendArgs& a, const Seq& s) {
+  // the last block ends last; with a window, none is longer than that and its rows' tokens
+  int64_t most = 2 * static_cast<int64_t>((s.len + kAttendTile - 1) / kAttendTile);
+  if (a.causal && s.n <= s.len) {
+    // the two ends are (r + 1) kRows / group and (R - r) kRows / group tokens behind the cached ones, at most
+    const int64_t ends = 2 * (static_cast<int64_t>(s.len) - s.n) + (static_cast<int64_t>(s.row_tiles) + 1) * kRows / a.group + 2;
+    most = min(most, (ends + 2 * (kAttendTile - 1)) / kAttendTile);
+  }
+  if (a.window > 0)
+    most = min(most, 2 * ((static_cast<int64_t>(a.window) + kRows / a.group + 16 + kAttendTile) / kAttendTile));
+  return max(most, int64_t{2});
+}
+__device__ __forceinline__ int64_t head_tiles(const AttendArgs& a, const Seq& s) {
+  return s.row_tiles / 2 * pair_tiles(a, s) +
+         (s.row_tiles & 1 ? span_of(a, s, s.row_tiles / 2).tiles : 0);
+}
+
+// Where a warp is in its CTA's run of parts of blocks: in shared memory, a copy for each warp, as it would take
+// registers from the roles' loops.
+struct Walk {
+  int64_t at, stop, run;
+  int64_t pair_first, block_first;  // numbers of the first tiles
+  int b, head, pair, second;        // block `pair` from the front, or (second) from the back
+  Seq s;
+};
+// A part of a block.
+struct Part {
+  AttendUnit un;
+  int b, q0, n, len;      // of its sequence
+  bool whole;             // all of the block
+  bool begin;             // the run begins with it
+  int t_begin, t_end;     // tokens
+  int tiles;              // to take, of 128 tokens
+  int hi_least, lo_most;  // tokens from lo_most to hi_least are seen by all rows
+  __device__ __forceinline__ bool row(const AttendArgs& a, int i, int& token, int& q_head) const {
+    const int r = un.row0 + i;
+    token = r / a.group;
+    q_head = un.head * a.group + r - token * a.group;
+    token += q0;
+    return r < un.rows;
+  }
+};
+__device__ __forceinline__ void walk_start(const AttendArgs& a, const Found& f, int64_t total, Walk& walk) {
+  Walk w = {};
+  w.run = run_of(total, gridDim.x);
+  w.at = w.run * blockIdx.x;
+  w.stop = min(w.at + w.run, total);
+  if (w.at < w.stop) {
+    w.b = f.b;
+    w.s = seq_of(a, f.b, kRows);
+    const int64_t in = w.at - f.first, of_head = head_tiles(a, w.s), of_pair = pair_tiles(a, w.s);
+    w.head = static_cast<int>(in / of_head);
+    const int64_t in_head = in - w.head * of_head;
+    w.pair = static_cast<int>(min(in_head / of_pair, static_cast<int64_t>(w.s.row_tiles / 2)));
+    w.pair_first = w.block_first = f.first + w.head * of_head + w.pair * of_pair;
+  }
+  if ((threadIdx.x & 31) == 0) walk = w;
+  __syncwarp();
+}
+// The next part, the same for all warps (code that the roles share). note: writes the CTA's cut where the run begins within a block.
+__device__ __noinline__ bool walk_next(const AttendArgs& a, Walk& walk, Part& p, Cut* note = nullptr) {
+  Walk w = walk;
+  bool found = false;
+  while (w.at < w.stop) {
+    const int half = w.s.row_tiles / 2;
+    const int r = w.second ? w.s.row_tiles - 1 - w.pair : w.pair;
+    const Span span = span_of(a, w.s, r);
+    const int64_t off = w.at - w.block_first;
+    if (off < span.tiles) {
+      const int tile0 = static_cast<int>(off), take = static_cast<int>(min(span.tiles - off, w.stop - w.at));
+      const int rows = w.s.n * a.group;
+      p.un = AttendUnit{w.head, r * kRows, rows};
+      p.b = w.b, p.q0 = w.s.q0, p.n = w.s.n, p.len = w.s.len;
+      p.whole = take == span.tiles;
+      p.begin = w.at == w.run * blockIdx.x;
+      p.t_begin = min(span.begin + tile0 * kAttendTile, span.end);
+      p.t_end = min(span.begin + (tile0 + take) * kAttendTile, span.end);
+      p.tiles = (p.t_end - p.t_begin + kAttendTile - 1) / kAttendTile;
+      const int pos0 = w.s.len - w.s.n + r * kRows / a.group;
+      const int pos1 = w.s.len - w.s.n + (min((r + 1) * kRows, rows) - 1) / a.group;
+      p.hi_least = a.causal ? min(pos0 + 1, w.s.len) : w.s.len;
+      p.lo_most = a.window > 0 ? pos1 - a.window + 1 : 0;
+      if (note != nullptr && p.begin && tile0 > 0) {
+        // others have parts of this block too
+        Cut c;
+        c.first = static_cast<int>(w.block_first / w.run);
+        c.last = static_cast<int>((w.block_first + span.tiles - 1) / w.run);
+        c.later = w.block_first != w.run * c.first;
+        c.head = w.head, c.row0 = r * kRows, c.rows = rows, c.q0 = w.s.q0;
+        *note = c;
+      }
+      w.at += take;
+      found = true;
+      break;
+    }
+    if (!w.second && w.pair < half) {
+      w.second = 1;
+      w.block_first += span.tiles;
+      continue;
+    }
+    w.pair_first += w.pair < half ? pair_tiles(a, w.s) : span.tiles;
+    w.block_first = w.pair_first;
+    w.at = max(w.at, w.pair_first);  // places behind the second block are empty
+    w.second = 0;
+    if (w.at >= w.stop) break;
+    if (++w.pair < half + (w.s.row_tiles & 1)) continue;
+    w.pair = 0;
+    if (++w.head < a.heads) continue;
+    w.head = 0;
+    do w.s = seq_of(a, ++w.b, kRows);
+    while (w.s.row_tiles == 0);  // there is one with queries: the run goes on
+  }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) walk = w;
+  __syncwarp();
+  return found;
+}
+
 struct Shared {
   uint64_t pair_full[4], sums_done[4], s_full, p_full, q_full;
   uint32_t tmem;
   int abort;
   ScanShared scan;
+  Walk walk[kWarpsAll];
   int top[2][kDequant];      // largest scale bytes, + 256: with NaN
   int ref[2];                // of the tile, by its parity
   uint8_t nan[2][kTokens];   // tokens with a NaN
   int any_nan[2];
   // of the rows, the softmax's own
-  alignas(16) float factor[kRows], m[kRows], keep[kRows];
+  // (sub, lim: what is subtracted from a score, and which one moves the reference)
+  alignas(16) float factor[kRows], m[kRows], sub[kRows], lim[kRows], keep[kRows];
   int lo[kRows], hi[kRows];
   float part[kSoftmax][kRows];
   size_t to[kRows];  // places of the rows' results
@@ -76,59 +214,6 @@ __device__ __forceinline__ float reduce16(const float (&x)[16], int lane, F f) {
   return f(y, __shfl_xor_sync(kFull, y, 1));
 }
 
-// The segments of this CTA's run, one after another, the same for every role.
-struct Walk {
-  int64_t at, stop, run, seq_first;
-  int b;
-  Seq s;
-  AttendUnit un;
-  int tile0, tile1;   // of the unit
-  int t_begin, t_end; // tokens of these tiles that any row of the unit sees, from a tile's first
-  int tiles;          // of 128 tokens to take
-  int hi_least, lo_most;  // tokens from lo_most to hi_least are seen by all rows
-  bool begin;
-  __device__ __forceinline__ void start(const AttendArgs& a, const Found& f, int64_t total) {
-    run = run_of(total, gridDim.x);
-    at = run * blockIdx.x;
-    stop = min(at + run, total);
-    if (at >= stop) return;
-    b = f.b;
-    seq_first = f.first;
-    s = seq_of(a, b, kRows);
-  }
-  __device__ __forceinline__ bool next(const AttendArgs& a) {
-    if (at >= stop) return false;
-    while (at >= seq_first + seq_work(a, s)) {
-      seq_first += seq_work(a, s);
-      s = seq_of(a, ++b, kRows);
-    }
-    const int64_t in = at - seq_first;
-    const int unit = static_cast<int>(in / s.tiles);
-    tile0 = static_cast<int>(in - static_cast<int64_t>(unit) * s.tiles);
-    tile1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), tile0 + (stop - at)));
-    begin = at == run * blockIdx.x;
-    at += tile1 - tile0;
-    un.head = unit / s.row_tiles;
-    // blocks of a prompt from both its ends in turn: the first see few tokens, and a run gets both kinds
-    const int r = unit - un.head * s.row_tiles;
-    un.row0 = ((r & 1) ? s.row_tiles - 1 - (r >> 1) : r >> 1) * kRows;
-    un.rows = s.n * a.group;
-    // what the block's rows see
-    const int q_first = un.row0 / a.group, q_last = (min(un.row0 + kRows, un.rows) - 1) / a.group;
-    const int pos0 = s.len - s.n + q_first, pos1 = s.len - s.n + q_last;
-    const int from = a.window > 0 ? max(pos0 - a.window + 1, s.start) : s.start;
-    const int to = a.causal ? min(pos1 + 1, s.len) : s.len;
-    t_begin = s.start + tile0 * kTokens;
-    t_end = min(s.start + tile1 * kTokens, s.len);
-    t_end = min(t_end, to);
-    if (from > t_begin) t_begin += (from - t_begin) / kTokens * kTokens;
-    tiles = max((t_end - t_begin + kTokens - 1) / kTokens, 0);
-    hi_least = a.causal ? min(pos0 + 1, s.len) : s.len;
-    lo_most = a.window > 0 ? pos1 - a.window + 1 : 0;
-    return true;
-  }
-};
-
 __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ Shared sh;
@@ -148,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
   if (warp == kIssue) tmem_alloc(smem_u32(&sh.tmem), kCols);
   pdl_wait();
   int64_t total;
-  const Found found = find_run<kRows, kWarpsAll>(a, sh.scan, total);
+  auto work = [](const AttendArgs& a, const Seq& s) { return a.heads * head_tiles(a, s); };
+  const Found found = find_run<kRows, kWarpsAll>(a, sh.scan, work, total);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -168,10 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     if (lane == 0) mbar_arrive(smem_u32(&bar));
   };
   auto wait_warp = [&](uint64_t& bar, uint32_t n) { return __all_sync(kFull, wait(bar, n)) != 0; };
-  Walk w;
-  w.start(a, found, total);
+  Walk& walk = sh.walk[warp];
+  walk_start(a, found, total, walk);
+  Part next;
   Cut* cuts = reinterpret_cast<Cut*>(a.partial);
-  if (threadIdx.x == 0 && w.at >= w.stop) cuts[blockIdx.x].last = -1;
+  if (threadIdx.x == 0) cuts[blockIdx.x].last = -1;
   float* parts0 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partial) + cut_bytes(gridDim.x));
   uint32_t done = 0;  // tiles taken
 
@@ -180,16 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int tid = threadIdx.x;
     bool ok = true;
-    while (ok && w.next(a)) {
-      if (w.begin && tid == 0) {
-        Cut cut;
-        const int64_t at = w.run * blockIdx.x, first = at - w.tile0;
-        cut.first = static_cast<int>(first / w.run);
-        cut.last = w.tile0 > 0 ? static_cast<int>((first + w.s.tiles - 1) / w.run) : -1;
-        cut.later = first != w.run * cut.first;
-        cut.head = w.un.head, cut.row0 = w.un.row0, cut.rows = w.un.rows, cut.q0 = w.s.q0;
-        cuts[blockIdx.x] = cut;
-      }
+    while (ok && walk_next(a, walk, next, tid == 0 ? cuts + blockIdx.x : nullptr)) {
+      const Part w = next;
       // ---- queries to fp16, a warp to a row at a time: each row's largest into [2^14, 2^15)
       // (four rows' loads at a time)
 #pragma unroll 1
@@ -200,12 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           int token, q_head;
-          const bool valid = w.un.row(a, w.s, r0 + i * kSoftmax, token, q_head);
+          const bool valid = w.row(a, r0 + i * kSoftmax, token, q_head);
           const uint16_t* q = a.q + static_cast<size_t>(token) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             v[i][j] = valid ? *reinterpret_cast<const uint4*>(q + (lane + 32 * j) * 8) : make_uint4(0, 0, 0, 0);
-          pos[i] = w.s.len - w.s.n + token - w.s.q0;
+          pos[i] = w.len - w.n + token - w.q0;
           there[i] = valid;
         }
 #pragma unroll
@@ -221,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
           }
           if (lane == 0) {
             sh.factor[r] = pow2(-shift) * fabsf(a.scale_log2);
-            sh.m[r] = -INFINITY;
-            sh.hi[r] = !there[i] ? 0 : a.causal ? min(pos[i] + 1, w.s.len) : w.s.len;
+            sh.m[r] = sh.lim[r] = -INFINITY;
+            sh.sub[r] = -kTop;
+            sh.hi[r] = !there[i] ? 0 : a.causal ? min(pos[i] + 1, w.len) : w.len;
             sh.lo[r] = a.window > 0 ? pos[i] - a.window + 1 : 0;
           }
         }
@@ -230,9 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       fence_proxy_async_smem();
       if (w.tiles > 0) arrive_warp(sh.q_full);
       named_barrier_sync(1, 32 * kSoftmax);
-      float l[kRows];
+      float l[kRows / 16];  // of row 16 g + lane / 2, this warp's tokens
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) l[r] = 0.f;
+      for (int g = 0; g < kRows / 16; ++g) l[g] = 0.f;
       int ref = 0;
       for (int j = 0; j < w.tiles; ++j) {
         const uint32_t n = done + j + 1;
@@ -264,17 +344,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
             }
           }
         };
-        bool beyond = j > 0 && new_ref != ref;
-        float x[16];
+        // The weights, by the references as they are, and whether one has to move. (Loops are rolled: with a
+        // thread's 64 rows in a row, the warps waited for instructions, and took 5300 cycles instead of
+        // 3700.)
+        float sum[kRows / 16];
+        auto weights = [&] {
+          bool beyond = false;
+          float x[16];
 #pragma unroll 1
-        for (int r0 = 0; r0 < kRows; r0 += 16) {
-          scores(r0, x);
+          for (int g = 0; g < kRows / 16; ++g) {
+            scores(16 * g, x);
+            uint32_t p[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r0 + i]);
-            beyond |= x[i] > m.x + kLag || x[i + 1] > m.y + kLag || x[i + 2] > m.z + kLag || x[i + 3] > m.w + kLag;
+            for (int i = 0; i < 16; i += 4) {
+              const float4 sub4 = *reinterpret_cast<const float4*>(&sh.sub[16 * g + i]);
+              const float4 lim4 = *reinterpret_cast<const float4*>(&sh.lim[16 * g + i]);
+              const float sub[4] = {sub4.x, sub4.y, sub4.z, sub4.w}, lim[4] = {lim4.x, lim4.y, lim4.z, lim4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                beyond |= x[i + e] > lim[e];
+                x[i + e] = exp2_fast(x[i + e] - sub[e]);
+              }
+              p[i / 2] = pack_f16(x[i], x[i + 1]);
+              p[i / 2 + 1] = pack_f16(x[i + 2], x[i + 3]);
+            }
+            const uint32_t to = base + kOffP + tid * 128;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              sts128(to + (((2 * g + i) ^ (tid & 7)) << 4), make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
+            const float y = reduce16(x, lane, [](float p, float q) { return p + q; });
+#pragma unroll
+            for (int k = 0; k < kRows / 16; ++k) sum[k] = g == k ? y : sum[k];
           }
-        }
+          return beyond;
+        };
+        const bool beyond = weights() || (j > 0 && new_ref != ref);
         // a wait that ran out makes all four warps leave together
         const bool votes = named_barrier_or(1, 32 * kSoftmax, beyond || !ok);
         if (*abort != 0) ok = false;
@@ -282,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
           // the rows' references become their maxima
 #pragma unroll 1
           for (int r0 = 0; r0 < kRows; r0 += 16) {
+            float x[16];
             scores(r0, x);
             const float y = reduce16(x, lane, [](float p, float q) { return fmaxf(p, q); });
             if ((lane & 1) == 0) sh.part[warp][r0 + lane / 2] = y;
@@ -293,10 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
             for (int i = 0; i < kSoftmax; ++i) top = fmaxf(top, sh.part[i][tid]);
             sh.keep[tid] = exp2_fast(sh.m[tid] - (top == -INFINITY ? 0.f : top));  // m = -inf: 0
             sh.m[tid] = top;
+            sh.sub[tid] = (top == -INFINITY ? 0.f : top) - kTop;
+            sh.lim[tid] = top + kLag;
           }
           named_barrier_sync(1, 32 * kSoftmax);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) l[r] *= sh.keep[r];
+          for (int g = 0; g < kRows / 16; ++g) l[g] *= sh.keep[16 * g + lane / 2];
           if (j > 0) {  // the sums of the tiles before are done: this tile's scores were issued behind them
             const float by = pow2(max(ref - new_ref, -126));
 #pragma unroll 1
@@ -311,29 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
             tmem_st_wait();
           }
         }
+        if (votes) weights();
         ref = new_ref;
 #pragma unroll
-        for (int r0 = 0; r0 < kRows; r0 += 16) {
-          scores(r0, x);
-          uint32_t p[8];
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 m4 = *reinterpret_cast<const float4*>(&sh.m[r0 + i]);
-            const float m[4] = {m4.x, m4.y, m4.z, m4.w};
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[e] = exp2_fast(x[i + e] - (m[e] == -INFINITY ? 0.f : m[e]) + kTop);
-              l[r0 + i + e] += y[e];
-            }
-            p[i / 2] = pack_f16(y[0], y[1]);
-            p[i / 2 + 1] = pack_f16(y[2], y[3]);
-          }
-          const uint32_t to = base + kOffP + tid * 128;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            sts128(to + (((r0 / 8 + i) ^ (tid & 7)) << 4), make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
-        }
+        for (int g = 0; g < kRows / 16; ++g) l[g] += sum[g];
         fence_proxy_async_smem();
         tc_fence_before();
         arrive_warp(sh.p_full);
@@ -342,20 +430,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
       // ---- results
       if (w.tiles > 0) ok = ok && wait_warp(sh.sums_done[3], done);
       tc_fence_after();
+      if ((lane & 1) == 0)
 #pragma unroll
-      for (int r0 = 0; r0 < kRows; r0 += 16) {
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = l[r0 + i];
-        const float y = reduce16(x, lane, [](float p, float q) { return p + q; });
-        if ((lane & 1) == 0) sh.part[warp][r0 + lane / 2] = y;
-      }
+        for (int g = 0; g < kRows / 16; ++g) sh.part[warp][16 * g + lane / 2] = l[g];
       named_barrier_sync(1, 32 * kSoftmax);
-      const bool whole = w.tile0 == 0 && w.tile1 == w.s.tiles;
+      const bool whole = w.whole;
       float* part = parts0 + (static_cast<size_t>(blockIdx.x) * 2 + (w.begin ? 0 : 1)) * kPartFloats<kD, kRows>;
       if (tid < kRows) {
         int token, q_head;
-        const bool valid = w.un.row(a, w.s, tid, token, q_head);
+        const bool valid = w.row(a, tid, token, q_head);
         const float sum = sh.part[0][tid] + sh.part[1][tid] + sh.part[2][tid] + sh.part[3][tid];
         sh.keep[tid] = sum == 0.f ? 0.f : 1.f / sum;
         sh.to[tid] = static_cast<size_t>(token) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
@@ -405,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     const int tid = threadIdx.x - 32 * kSoftmax;
     const int tok = (tid & 7) + 8 * (tid >> 4), half = (tid >> 3) & 1;
     bool ok = true, bad = false, leave = false;
-    while (!leave && w.next(a)) {
+    while (!leave && walk_next(a, walk, next)) {
+      const Part w = next;
       const int* pages_of = a.table + static_cast<size_t>(w.b) * a.ld_table;
       const size_t head_row = static_cast<size_t>(w.un.head) * a.page_size;
       const uint8_t* codes_of = a.k + head_row * (kD / 2) + half * 16;
@@ -513,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
     const uint32_t d0 = __shfl_sync(kFull, tmem, 0);
     const uint32_t k_lo = sw128_lo(base), q_lo = sw128_lo(base + kOffQ), v_lo = sw128_lo(base, kTokens * 128),
                    p_lo = sw128_lo(base + kOffP);
-    while (ok && w.next(a)) {
+    while (ok && walk_next(a, walk, next)) {
+      const Part w = next;
       if (w.tiles == 0) continue;
       ++units;
       ok = wait_warp(sh.q_full, units);
@@ -571,7 +656,7 @@ cudaError_t launch_attend_latent(const AttendArgs& a, int sm_count, cudaStream_t
   const int ctas = attend_ctas(a, kRows, sm_count);
   const cudaError_t e = launch_overlapping(attend_latent_kernel, dim3(ctas), kThreads, kBytes, stream, a);
   if (e != cudaSuccess || ctas < 2) return e;
-  return launch_overlapping(attend_join_kernel<kD, kRows>, dim3(ctas - 1), kJoinThreads, 0, stream, a, ctas);
+  return launch_join<kD, kRows>(a, ctas, stream);
 }
 
 }  // namespace mx

@@ -17,7 +17,13 @@
 //
 // What runs where: four warps to each tile of rows take S to P (a thread to a row), four
 // dequantize, one issues the products. Bound by the tensor cores, then by the
-// exponentials (half their time at d = 128).
+// exponentials (half their time at d = 128). A pair of 128 x 128 tiles takes 1.82 us at d = 128, 1.58 at 64, 2.91
+// (one of 256 dimensions) at 256, where the products alone are 1.15; a block of rows costs 12 us besides (launch, queries,
+// first tiles, results). Three prompts (518 GFLOP) 494 us, 1049 TFLOP/s.
+//
+// A CTA to a block of rows, in splits of its tokens where the blocks are fewer than the SMs. (CTAs that
+// stay, with equal runs of tiles, waste nothing on a last wave, 13 % of those prompts' time. But
+// every role then carries its place in the run, a tile took 7 % longer, and 561 us were left.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -192,6 +198,10 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
   int lo = 0, hi = 0, token = 0, q_head = 0;
   bool valid = false;
   const int tile = warp >> 2;
+  constexpr int kLanes = D / 8, kEach = 32 / kLanes;
+  // 16 bytes of one of this warp's rows, in the queries' place
+  const uint32_t rows0 = base + L::kOffQ + tile * L::kTile + (warp & 3) * (32 * 128);
+  auto rows_at = [&](int r, int i) { return rows0 + (i >> 3) * (kRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4); };
   if (work && warp < kDequant) {
     const int r = row0 + tile * kRows + (warp & 3) * 32 + lane;
     valid = r < rows;
@@ -201,22 +211,26 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
     token += s.q0;
     hi = !valid ? 0 : a.causal ? min(pos + 1, s.len) : s.len;
     lo = a.window > 0 ? pos - a.window + 1 : 0;
-    const uint16_t* q = a.q + static_cast<size_t>(valid ? token : s.q0) * a.ldq + static_cast<size_t>(q_head) * a.ldq_head;
+    // Rows come by whole lines, kLanes lanes to each (loaded by a thread to each row of its own, twice, they took
+    // 10000 cycles, and the results 5700).
+    const int64_t q_at = valid ? static_cast<int64_t>(token) * a.ldq + static_cast<int64_t>(q_head) * a.ldq_head : -1;
+#pragma unroll 2
+    for (int i = 0; i < kLanes; ++i) {
+      const int r = i * kEach + lane / kLanes;
+      const int64_t from = __shfl_sync(kFull, q_at, r);
+      cp_async_16(rows_at(r, lane % kLanes), a.q + max(from, int64_t{0}) + lane % kLanes * 8, from >= 0 ? 16 : 0);
+    }
+    cp_async_wait_all();
+    __syncwarp();
     uint32_t most = 0;
 #pragma unroll 4
-    for (int i = 0; i < D / 8; ++i)
-      if (valid) most = max(most, max_bits(reinterpret_cast<const uint4*>(q)[i]));
+    for (int i = 0; i < kLanes; ++i) most = max(most, max_bits(lds128(rows_at(lane, i))));
     const int shift = query_shift(most, a.q_f16);
     // a negative scale turns the queries' sign: the factor of the scores is not negative
     const float f = a.scale_log2 < 0.f ? -pow2(shift) : pow2(shift);
     row_factor = pow2(-shift) * fabsf(a.scale_log2);
-    const int m = (warp & 3) * 32 + lane;
-    const uint32_t to = base + L::kOffQ + tile * L::kTile + m * 128;
 #pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 v = valid ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
-      sts128(to + (i >> 3) * (kRows * 128) + (((i & 7) ^ (m & 7)) << 4), query_f16(v, a.q_f16, f));
-    }
+    for (int i = 0; i < kLanes; ++i) sts128(rows_at(lane, i), query_f16(lds128(rows_at(lane, i)), a.q_f16, f));
     fence_proxy_async_smem();
   }
   __syncthreads();
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         // parts of splits: [unit][row] {m, l} and the sums
         float* part = a.partial + static_cast<size_t>(unit) * (kTiles * kRows) * (D + 2);
         const int pr = tile * kRows + (warp & 3) * 32 + lane;
-        uint16_t* out = a.out + static_cast<size_t>(valid ? token : 0) * a.ldo + static_cast<size_t>(q_head) * a.ldo_head;
+        const int64_t out_at = valid ? static_cast<int64_t>(token) * a.ldo + static_cast<int64_t>(q_head) * a.ldo_head : -1;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t r[32];
@@ -367,10 +381,9 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
           const float x = !kShared && ((nan_blocks >> (c / 32)) & 1u) ? NAN : inv;
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (whole) {
-            if (valid)
+          if (whole) {  // the products with the queries are done
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(out + c + i) = pack_out8(v + i, x, a.q_f16);
+            for (int i = 0; i < 4; ++i) sts128(rows_at(lane, c / 8 + i), pack_out8(v + 8 * i, x, a.q_f16));
           } else {
             float4* to = reinterpret_cast<float4*>(part + 2 * kTiles * kRows + static_cast<size_t>(pr) * D + c);
 #pragma unroll
@@ -381,8 +394,17 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
         if (!whole) {
           part[pr] = m - kTop;
           part[kTiles * kRows + pr] = l;
-        } else if (valid && a.lse != nullptr) {
-          a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (m - kTop + log2f(l)) * 0.6931471805599453f;
+        } else {
+          if (valid && a.lse != nullptr)
+            a.lse[static_cast<size_t>(token) * a.q_heads + q_head] = (m - kTop + log2f(l)) * 0.6931471805599453f;
+          __syncwarp();
+#pragma unroll 2
+          for (int i = 0; i < kLanes; ++i) {
+            const int r = i * kEach + lane / kLanes;
+            const int64_t to = __shfl_sync(kFull, out_at, r);
+            const uint4 y = lds128(rows_at(r, lane % kLanes));
+            if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + lane % kLanes * 8) = y;
+          }
         }
       }
     } else if (warp < kIssue) {
