@@ -97,13 +97,12 @@ constexpr int kAttendManyRows = 64;
 // 133 us), where the other's grows with them: 113 us at 48 rows, 146 at 64, 212 at 96 (d 64: 79, 99,
 // 140 against 116; d 256: 159, 206, 301 against 154). 4 such sequences: 27 and 34 us at 64, 37 and 32 at 128.
 // Latents of 512 dimensions go to their own kernel from so many rows of a sequence on, where there is
-// work for 16 tiles of 64 rows and 128 tokens or more on each SM: it reads the cache for four times as many rows
-// at once, and takes 20 us longer to begin and to end. Few rows against it, 16 heads, us: 48 sequences of
-// up to 8192 tokens 141 / 145 at 64 rows, 266 / 234 at 128, 1000 / 793 at 512, 15780 / 9201 at 8192;
-// 2 of them 78 / 80 at 512, 136 / 118 at 1024, 919 / 594 at 8192; 8 of up to 1024 tokens 95 / 175 at 1024
-// (7 tiles), 573 / 417 at 8192 (54).
-constexpr int kAttendLatentRows = 128;
-constexpr int64_t kAttendLatentWork = int64_t{16} * 64 * 128;
+// work for 3 tiles of 64 rows and 128 tokens or more on each SM: it reads the cache for four times as many rows
+// at once, and takes longer to begin and to end. Few rows against it, 16 heads, us: 48 sequences of
+// up to 8192 tokens 74 / 81 at 32 rows, 105 / 84 at 48, 136 / 87 at 64, 942 / 469 at 512; 2 of them 28 / 37 at 128
+// (1.7 tiles), 46 / 38 at 256 (3.4), 73 / 51 at 512; 8 of up to 1024 tokens 36 / 39 at 256 (1.7), 50 / 45 at 512 (3.4).
+constexpr int kAttendLatentRows = 40;
+constexpr int64_t kAttendLatentWork = int64_t{3} * 64 * 128;
 #ifdef MX_TIMELINE
 constexpr int kTimelineLaunches = 256;
 constexpr size_t kTimelineBytes =

@@ -124,6 +124,7 @@ template <int D, bool kShared, int kRows>
 __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D, kShared, kRows>::kCtas) attend_kernel(const AttendArgs a) {
   using L = Layout<D, kShared, kRows>;
   constexpr bool kCoop = L::kCoop;
+  constexpr int kExtra = kUnitExtra<D>;
   constexpr int kBlocks = L::kBlocks;
   constexpr int kStages = L::kStages;
   constexpr int kWarps = L::kWarps, kSub = L::kSub, kOwn = kSub / 16;  // groups of 16 tokens of a warp
@@ -151,16 +152,14 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
   fence_mbar_init();
   pdl_wait();
   int64_t total;
-  const Found found = find_run<kRows, kWarps>(a, scan, seq_work, total);
+  const Found found = find_run<kRows, kWarps>(a, scan, seq_work<D>, total);
   const int64_t run = run_of(total, gridDim.x);
   int64_t at = run * blockIdx.x;
   const int64_t stop = min(at + run, total);
   Cut* cuts = reinterpret_cast<Cut*>(a.partial);
   float* parts0 = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partial) + cut_bytes(gridDim.x));
-  if (at >= stop) {
-    if (threadIdx.x == 0) cuts[blockIdx.x].last = -1;
-    return;
-  }
+  if (threadIdx.x == 0) cuts[blockIdx.x].last = -1;  // until the run is seen to begin within a unit
+  if (at >= stop) return;
   int b = found.b;
   int64_t seq_first = found.first;
   Seq s = seq_of(a, b, kRows);
@@ -168,13 +167,16 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
   bool failed = false;
 
   while (at < stop) {
-    while (at >= seq_first + seq_work(a, s)) {  // sequences without queries have no work
-      seq_first += seq_work(a, s);
+    while (at >= seq_first + seq_work<D>(a, s)) {  // sequences without queries have no work
+      seq_first += seq_work<D>(a, s);
       s = seq_of(a, ++b, kRows);
     }
     const int64_t in = at - seq_first;
-    const int unit = static_cast<int>(in / s.tiles);
-    const int tile0 = static_cast<int>(in - static_cast<int64_t>(unit) * s.tiles);
+    const int unit = static_cast<int>(in / (s.tiles + kExtra));
+    const int place = static_cast<int>(in - static_cast<int64_t>(unit) * (s.tiles + kExtra));
+    const int tile0 = max(place - kExtra, 0);
+    at += max(kExtra - place, 0);
+    if (at >= stop) break;
     const int tile1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), tile0 + (stop - at)));
     // a CTA has two parts of units at most: the one its run begins within, and a later one
     const bool begin = at == run * blockIdx.x;
@@ -182,11 +184,11 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
     un.head = unit / s.row_tiles;
     un.row0 = (unit - un.head * s.row_tiles) * kRows;
     un.rows = s.n * a.group;
-    if (begin && threadIdx.x == 0) {
+    if (begin && tile0 > 0 && threadIdx.x == 0) {
       Cut cut;
       const int64_t first = at - tile0;
       cut.first = static_cast<int>(first / run);
-      cut.last = tile0 > 0 ? static_cast<int>((first + s.tiles - 1) / run) : -1;
+      cut.last = static_cast<int>((first + s.tiles - 1) / run);
       cut.later = first != run * cut.first;
       cut.head = un.head, cut.row0 = un.row0, cut.rows = un.rows, cut.q0 = s.q0;
       cuts[blockIdx.x] = cut;
@@ -867,9 +869,9 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 template <int D, bool kShared, typename F>
 auto with_kernels(bool few, F&& f) {
   return few ? f(attend_kernel<D, kShared, 8>, launch_join<D, 8>, Layout<D, kShared, 8>::kBytes,
-                 Layout<D, kShared, 8>::kThreads, 8)
+                 Layout<D, kShared, 8>::kThreads, 8, kUnitExtra<D>)
              : f(attend_kernel<D, kShared, 16>, launch_join<D, 16>, Layout<D, kShared, 16>::kBytes,
-                 Layout<D, kShared, 16>::kThreads, 16);
+                 Layout<D, kShared, 16>::kThreads, 16, kUnitExtra<D>);
 }
 template <typename F>
 auto with_variant(int v, F&& f) {
@@ -895,7 +897,7 @@ int attend_variant(int d, bool shared) {
 
 cudaError_t set_attend_attributes(int sm_count, int (&ctas)[kAttendVariants]) {
   for (int v = 0; v < kAttendVariants; ++v) {
-    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int threads, int) {
+    const cudaError_t e = with_variant(v, [&](auto kernel, auto, int bytes, int threads, int, int) {
       cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       int n = 0;
       if (rc == cudaSuccess) rc = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, bytes);
@@ -912,8 +914,8 @@ size_t attend_bytes(int d, int ctas, int rows) {
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int variant, int ctas, cudaStream_t stream) {
-  return with_variant(variant, [&](auto kernel, auto join, int bytes, int threads, int rows) {
-    ctas = attend_ctas(a, rows, ctas);
+  return with_variant(variant, [&](auto kernel, auto join, int bytes, int threads, int rows, int extra) {
+    ctas = attend_ctas(a, rows, extra, ctas);
     const cudaError_t e = launch_overlapping(kernel, dim3(ctas), threads, bytes, stream, a);
     if (e != cudaSuccess || ctas < 2) return e;
     return join(a, ctas, stream);
