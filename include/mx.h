@@ -549,9 +549,11 @@ size_t mx_attend_bytes(const mx_handle* h, int d, int shared);
  * reported by mx_device_status as MX_ERR_INVALID_ARG; such a sequence's offsets count as
  * no query tokens, its length as the nearest of 0 and the largest. A row that sees nothing
  * is 0, its lse -inf. A NaN in the cache reaches the rows that see it.
- * Scores and sums are float32; the weights are rounded to 11 bits relative to the largest
- * contribution. The order of the sums follows from the lengths and the number of SMs: the same
- * bits on every call.
+ * Scores and sums are float32. The weights are rounded to 11 bits, those below 2^-21 of the row's
+ * largest to 2^-32 of it. A block of 32 whose scale is below 2^-27 of the largest of its token's
+ * keys or values (with many query rows: of the tokens before it, too) counts as zeros. The
+ * order of the sums follows from the shapes, the lengths and the number of SMs: the same bits on
+ * every call.
  * Constraints: q_heads % heads == 0; d one of 64, 128, 256, 512, T * q_heads and
  * table_cols * page_size < 2^30, else MX_ERR_UNSUPPORTED. */
 int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, const void* q, long ldq, long ldq_head,
