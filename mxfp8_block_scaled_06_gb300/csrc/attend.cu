@@ -17,12 +17,13 @@
 //           back in float32. Values the same.
 //   queries times the power of two that brings the row's largest into [2^14, 2^15):
 //           exact down to 2^-31 of it.
-//   weights p = exp2(x + S_v - u + 8) rounded to fp16 (11 bits, where a bf16 weight would
-//           have 8): x the score, S_v the value row's scale, u the running maximum of
-//           x + S_v. So what is rounded, and below 2^-22 of the largest loses bits, is a
+//   weights p = exp2(x - m + S_v - u + 8) rounded to fp16 (11 bits, where a bf16 weight would
+//           have 8): x the score, m the running maximum, S_v the value row's scale, u the running
+//           maximum of x - m + S_v (of the difference, which is exact near 0: S_v would be lost in a large
+//           score). So what is rounded, and below 2^-22 of the largest loses bits, is a
 //           token's contribution, not its weight. The weights' sum is of float32 exponentials.
 //
-// The maxima m (of x) and u are only moved when a score goes beyond them by 2^24, or a
+// m and u are only moved when a score goes beyond by 2^24, or a
 // contribution by 2^7: then the sums are scaled anew, otherwise nothing is.
 //
 // Tokens go by in tiles of 128, an equal part to each of four warps, through a ring filled by bulk copies. Up to d = 128 a warp is on its own: it keeps the queries and its
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 #pragma unroll
           for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) x[j][n][2 * h + e] *= __uint_as_float(tk.x) * factor[n][e];
+            for (int e = 0; e < 2; ++e) x[j][n][2 * h + e] = __fmul_rn(x[j][n][2 * h + e], __uint_as_float(tk.x) * factor[n][e]);  // (never fused)
         }
       if (__any_sync(kFull, t0 < lo_most || t0 + kSub > hi_least)) {
 #pragma unroll
@@ -554,10 +555,11 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[n][e] = ux[n][e] = -INFINITY;
+          const float mr = m[n][e] == -INFINITY ? 0.f : m[n][e];
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
             mx[n][e] = fmaxf(mx[n][e], fmaxf(x[j][n][e], x[j][n][2 + e]));
-            ux[n][e] = fmaxf(ux[n][e], fmaxf(x[j][n][e] + vs[j][0], x[j][n][2 + e] + vs[j][1]));
+            ux[n][e] = fmaxf(ux[n][e], fmaxf(x[j][n][e] - mr + vs[j][0], x[j][n][2 + e] - mr + vs[j][1]));
           }
           beyond |= mx[n][e] > m[n][e] + kLagM || ux[n][e] > u[n][e] + kLagU;
         }
@@ -581,9 +583,9 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
               float w[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float v = x[j][n][2 * h + e];
-                sum[n][e] += exp2_fast(v - mr[e]);
-                w[e] = exp2_fast(v + vs[j][h] - ur[e]);
+                const float v = x[j][n][2 * h + e] - mr[e];
+                sum[n][e] += exp2_fast(v);
+                w[e] = exp2_fast(v + (vs[j][h] - ur[e]));
               }
               p[j][n][h] = transposed(pack_f16(w[0], w[1]));
             }
@@ -607,42 +609,52 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
         beyond = __any_sync(kFull, beyond);
       }
       if (beyond) {
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(kFull, mx[n][e], o));
-              ux[n][e] = fmaxf(ux[n][e], __shfl_xor_sync(kFull, ux[n][e], o));
-            }
-        if constexpr (kCoop) {
-          if (g == 0)
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) rows_sh[warp * kRows + 8 * n + 2 * c + e] = make_float2(mx[n][e], ux[n][e]);
-          __syncthreads();
+        // all warps' largest of v, each row's in [0] or [1] of rows_sh
+        auto largest = [&](float (&v)[kN][2], int word) {
 #pragma unroll
           for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int w = 0; w < kWarps; ++w) {
-                const float2 v = rows_sh[w * kRows + 8 * n + 2 * c + e];
-                mx[n][e] = fmaxf(mx[n][e], v.x);
-                ux[n][e] = fmaxf(ux[n][e], v.y);
-              }
-        }
+              for (int o = 4; o < 32; o <<= 1) v[n][e] = fmaxf(v[n][e], __shfl_xor_sync(kFull, v[n][e], o));
+          if constexpr (kCoop) {
+            float* words = reinterpret_cast<float*>(rows_sh) + word;
+            if (g == 0)
+#pragma unroll
+              for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) words[2 * (warp * kRows + 8 * n + 2 * c + e)] = v[n][e];
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v[n][e] = fmaxf(v[n][e], words[2 * (w * kRows + 8 * n + 2 * c + e)]);
+          }
+        };
+        largest(mx, 0);
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             mx[n][e] = fmaxf(mx[n][e], m[n][e]);
-            ux[n][e] = fmaxf(ux[n][e], u[n][e]);
-            l[n][e] *= exp2_fast(m[n][e] - (mx[n][e] == -INFINITY ? 0.f : mx[n][e]));
-            const float shrink = exp2_fast(u[n][e] - (ux[n][e] == -INFINITY ? 0.f : ux[n][e]));
+            const float mr = mx[n][e] == -INFINITY ? 0.f : mx[n][e];
+            l[n][e] *= exp2_fast(m[n][e] - mr);
+            u[n][e] += (m[n][e] == -INFINITY ? 0.f : m[n][e]) - mr;
             m[n][e] = mx[n][e];
+            ux[n][e] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+              ux[n][e] = fmaxf(ux[n][e], fmaxf(x[j][n][e] - mr + vs[j][0], x[j][n][2 + e] - mr + vs[j][1]));
+          }
+        largest(ux, 1);
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            ux[n][e] = fmaxf(ux[n][e], u[n][e]);
+            const float shrink = exp2_fast(u[n][e] - (ux[n][e] == -INFINITY ? 0.f : ux[n][e]));
             u[n][e] = ux[n][e];
 #pragma unroll
             for (int t = 0; t < 4 * kWords; ++t) {
@@ -754,14 +766,14 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
     // ---- join the warps
     const bool whole = tile0 == 0 && tile1 == s.tiles;
     // this thread has, of each of its rows, dimensions wide0 + 8 kWords g on
-    float to_m[kN][2];  // from sums relative to 2^(u + 21) to 2^m
+    float to_m[kN][2];  // from sums relative to 2^(m + u + 21) to 2^m
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(kFull, l[n][e], o);
-        to_m[n][e] = u[n][e] == -INFINITY ? 0.f : exp2f(u[n][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]) - kSumBits);
+        to_m[n][e] = u[n][e] == -INFINITY ? 0.f : exp2f(u[n][e] - kSumBits);
       }
     float* part_out = parts0 + (static_cast<size_t>(blockIdx.x) * 2 + (begin ? 0 : 1)) * kPartFloats<D, kRows>;
     __syncthreads();  // all parts of the ring are read

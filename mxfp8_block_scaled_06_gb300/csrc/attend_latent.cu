@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_latent_kernel(const Attend
           for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&f[i]) = *reinterpret_cast<const float4*>(&sh.factor[r0 + i]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]) * (kf * f[i]);
+          for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__uint_as_float(v[i]), kf * f[i]);  // (never fused)
           if (special) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
