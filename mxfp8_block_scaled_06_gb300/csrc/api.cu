@@ -1260,6 +1260,8 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
           static_cast<int64_t>(h->sm_count) * kAttendLatentWork) {
     return cuda_status(mx::launch_attend_latent(a, h->sm_count, static_cast<cudaStream_t>(stream)));
   }
+  // One tile of 8 rows or two (8 rows of 61 sequences of up to 8192 tokens, 8 heads of 128: 94 us and 139; 48 of
+  // up to 8192 latents 37 and 46; one sequence 14.7 and 15.3).
   const int of_rows = static_cast<int64_t>(T) * a.group <= static_cast<int64_t>(B) * 8 ? variant + mx::kAttendVariants / 2 : variant;
   return cuda_status(mx::launch_attend(a, of_rows, h->attend_ctas[of_rows], static_cast<cudaStream_t>(stream)));
 }

@@ -340,8 +340,10 @@ struct RopeTable {
 };
 cudaError_t launch_rope_table(const RopeTable& t, int sm_count, float* cos_sin, cudaStream_t stream);
 
-// From this many chunks on a thread takes four heads of one.
-constexpr int64_t kRopeManyUnits = 1 << 20;
+// From this many chunks on a thread takes four heads of one, where there are four. (32 heads of 128, one head against
+// four: 64 tokens 2.3 and 2.9 us, 256 2.7 and 3.2, 512 3.5 and 3.4, 4096 9.5 and 8.2, 16381 46.9 and 43.7; 4096
+// tokens of one head of 512 3.1 and 3.9.)
+constexpr int64_t kRopeManyUnits = 1 << 17;
 struct RopeRows {
   int tokens, heads, d, first, d_rope;
   const void* x;
