@@ -990,6 +990,8 @@ def mx_attend(h: Handle, q, cache: MxCache, table, lengths, q_offsets=None, scal
     t, heads, d = q.shape
     code = _type_code("q", q, (MX_TYPE_BF16, MX_TYPE_F16))
     ldq, ldqh = _heads("q", q, (q.dtype,), t, heads, cache.d, 8)
+    if not -2**31 <= window < 2**31:
+        raise ValueError(f"window: {window}, at most 2^31 - 1 tokens are possible")
     if heads % cache.heads:
         raise ValueError(f"q: {heads} heads, a multiple of the cache's {cache.heads} is required")
     if table.dim() != 2 or table.dtype != torch.int32:

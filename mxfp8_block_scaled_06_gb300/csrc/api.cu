@@ -1196,7 +1196,7 @@ int mx_attend(mx_handle* h, const mx_cache* cache, int B, int T, int q_heads, co
   rc = validate_cache(cache);
   if (rc != MX_OK) return rc;
   if (B < 1 || T < 1 || q_heads < 1 || q_heads % cache->heads != 0 || table_cols < 1 || ld_table < table_cols ||
-      !std::isfinite(scale) || window < 0 || (window > 0 && !causal) || (q_offsets == nullptr && T % B != 0))
+      !std::isfinite(scale * 1.4426950408889634f) || window < 0 || (window > 0 && !causal) || (q_offsets == nullptr && T % B != 0))
     return MX_ERR_INVALID_ARG;
   if (q_type != MX_TYPE_BF16 && q_type != MX_TYPE_F16) return MX_ERR_INVALID_ARG;
   if (q == nullptr || table == nullptr || lengths == nullptr || out == nullptr) return MX_ERR_INVALID_ARG;

@@ -66,7 +66,8 @@ CASES = [
     (attend, dict(out=bf16(6, 8, 64)), ValueError), (attend, dict(out=torch.zeros(6, 8, 128).half()), TypeError),
     (attend, dict(out=bf16(1, 8, 128).expand(6, 8, 128)), ValueError),
     (attend, dict(out=bf16(6, 1, 128).expand(6, 8, 128)), ValueError),
-    (attend, dict(workspace=f32(1 << 20)), TypeError),
+    (attend, dict(workspace=f32(1 << 20)), TypeError), (attend, dict(window=2**32), ValueError),
+    (attend, dict(window=-2**32), ValueError),
 ]
 
 

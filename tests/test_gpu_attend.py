@@ -280,7 +280,8 @@ def test_a_workspace_given(mx):  # noqa: F811
         c.run(workspace=room[:need - 16])
 
 
-@pytest.mark.parametrize("kw", [dict(window=-1), dict(window=5, causal=False), dict(scale=float("nan"))])
+@pytest.mark.parametrize("kw", [dict(window=-1), dict(window=5, causal=False), dict(scale=float("nan")),
+                                dict(scale=3e38)])
 def test_calls_that_are_refused(mx, kw):  # noqa: F811
     c = Case(mx, [30], [1], 4, 2, 128, False)
     with pytest.raises(mx.MxError) as e:
