@@ -17,7 +17,7 @@
 //
 // What runs where: four warps to each tile of rows take S to P (a thread to a row), four
 // dequantize, one issues the products. Bound by the tensor cores, then by the
-// exponentials (half their time at d = 128). A pair of 128 x 128 tiles takes 1.82 us at d = 128, 1.58 at 64, 2.91
+// exponentials (half their time at d = 128). A pair of 128 x 128 tiles takes 1.82 us at d = 128, 1.58 at 64, 2.75
 // (one of 256 dimensions) at 256, where the products alone are 1.15; a block of rows costs 12 us besides (launch, queries,
 // first tiles, results). Three prompts (518 GFLOP) 494 us, 1049 TFLOP/s.
 //
@@ -549,6 +549,9 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
             }
           }
           fence_proxy_async_smem();
+          // One stage: these keys may be there before the softmax has looked at the barrier for the tile before, and
+          // it would take this phase for that one. Its first weights come after that look, and before these scores.
+          if (kStages == 1 && sd == 0 && j > 0) ok = ok && wait_warp(sh.p_full[0][0], j);
           arrive_warp(sd == 0 ? sh.k_full[st] : sh.v_full[st]);
           if constexpr (!kAhead) load(j + 1, sd, now[sd], next_here);
         }
@@ -592,9 +595,12 @@ __global__ void __launch_bounds__(Plan<D, kShared>::kThreads, 1) attend_rows_ker
       };
       for (int j = 0; ok && j < tiles; ++j) {
         const int st = j % kStages;
-        if (!wait_warp(sh.k_full[st], j / kStages + 1)) break;
+        // (one stage: the keys come after the first weights of the tile before, its sums need not wait for them)
+        static_assert(kStages > 1 || kTiles == 1, "one wait for a tile's keys");
+        if (kStages > 1 && !wait_warp(sh.k_full[st], j / kStages + 1)) break;
         for (int g = 0; ok && g < kTiles; ++g) {
           if (j > 0) ok = sums(g, j - 1);
+          if (kStages == 1) ok = ok && wait_warp(sh.k_full[st], j + 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
