@@ -1,4 +1,4 @@
-// attend.cuh - what the two kernels of the attention over the MXFP4 cache share.
+// attend.cuh - what the three kernels of the attention over the MXFP4 cache share.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
