@@ -433,9 +433,13 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) f[k] = (0x001C001Cu - __vminu2(top2 - f[k], 0x001C001Cu)) << 10;
           }
-          if (!here)
+          // The bytes of a token that is not there are an earlier stage's: with a page outside the cache it is
+          // a row of zeros, whose scale may not raise a reference.
+          if (!here) {
+            top = 0;
 #pragma unroll
             for (int k = 0; k < kPairs; ++k) f[k] = 0u;
+          }
           if (sd == 0) {
             const uint32_t to = keys0 + token * kBlocks * 2;
             if constexpr (kBlocks == 2)
@@ -748,6 +752,9 @@ __global__ void __launch_bounds__(Layout<D, kShared, kRows>::kThreads, Layout<D,
                                   (kShared ? 0 : L::kCodes + L::kRaw) + L::kCodes + t % kSub * kBlocks;
             const int pos = kCoop ? t_begin + i * kTile + t : t0 + t;
             if (pos >= t_end) break;
+            // (of a page outside the cache nothing was copied)
+            if (static_cast<uint32_t>(pages_of[div_u32(static_cast<uint32_t>(pos) >> 4, a.per_page)]) >= static_cast<uint32_t>(a.pages))
+              continue;
             bool row_nan = false;  // a shared row is a key as well: its score is NaN
             if constexpr (kShared)
               for (int k = 0; k < kBlocks; ++k) row_nan |= from[k] == 255;
