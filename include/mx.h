@@ -481,6 +481,8 @@ int mx_rope_table(mx_handle* h, int max_pos, int d_rope, double base, int scalin
  *              magnitude of 1 its inverse)
  * a' = a cos - b sin, b' = b cos + a sin in float32 without fused multiply-adds, rounded once.
  * The inverse of interleaved pairs is the rotation of wo_a_grouped.
+ * out is x, or has no element in common with it (refused as MX_ERR_INVALID_ARG where the strides are the
+ * same; with others it is the caller's to see to).
  * Constraints: d_rope even; head strides >= d; interleaved: d, first, all strides (and the
  * addresses, in elements) even, else MX_ERR_UNSUPPORTED; T * heads < 2^31. Every multiple of 4
  * and of 8 elements in all of them makes wider accesses. */

@@ -887,7 +887,7 @@ def mx_rope(h: Handle, x, positions, cos_sin, first: int | None = None, interlea
     """x [T, heads, d] (bf16, fp16 or fp32, any strides of tokens and heads) with dimensions
     first .. first + d_rope - 1 (default: the last) of each head rotated by its token's position, int64 [T]; cos_sin
     [max_pos, d_rope] as from mx_rope_table. interleaved: pairs of neighbours, else of halves. inverse:
-    by the negative angle. out may be x."""
+    by the negative angle. out may be x, or memory that has nothing in common with it."""
     torch = _t()
     empty = torch.empty if stream is None else _empty_on(stream)
     if x.dim() != 3:

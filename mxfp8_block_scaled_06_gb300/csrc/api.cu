@@ -1042,6 +1042,22 @@ int mx_rope_table(mx_handle* h, int max_pos, int d_rope, double base, int scalin
   return cuda_status(mx::launch_rope_table(t, h->sm_count, cos_sin, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// Whether two blocks of [m][n] rows of d elements, `apart` elements from one another and of the same strides, have
+// elements in common: rows that differ by i and j places, all i of the axis with fewer.
+bool rows_meet(int64_t apart, int64_t m, int64_t n, int64_t d, int64_t ld_m, int64_t ld_n) {
+  if (m > n) return rows_meet(apart, n, m, d, ld_n, ld_m);
+  if (std::abs(apart) >= (m - 1) * ld_m + (n - 1) * ld_n + d) return false;
+  for (int64_t i = 1 - m; i < m; ++i) {
+    const int64_t rest = std::abs(apart - i * ld_m), j = ld_n > 0 ? std::min(rest / ld_n, n - 1) : 0;
+    if (rest - j * ld_n < d || (ld_n > 0 && j + 1 < n && (j + 1) * ld_n - rest < d)) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
 int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const void* x, long ldx, long ldx_head,
             int x_type, const int64_t* positions, const float* cos_sin, int max_pos, int interleaved, int inverse,
             void* out, long ldo, long ldo_head, void* stream) {
@@ -1058,6 +1074,10 @@ int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const 
     return MX_ERR_INVALID_ARG;
   // in place, every element is where it was
   if (x == out && (ldx != ldo || ldx_head != ldo_head)) return MX_ERR_INVALID_ARG;
+  // beside x, no element is read where another is written
+  if (x != out && (T == 1 || ldx == ldo) && (heads == 1 || ldx_head == ldo_head) &&
+      rows_meet((reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(x)) / size, T, heads, d, ldx, ldx_head))
+    return MX_ERR_INVALID_ARG;
   mx::RopeRows a = {};
   a.tokens = T;
   a.heads = heads;
