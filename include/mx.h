@@ -484,8 +484,9 @@ int mx_rope_table(mx_handle* h, int max_pos, int d_rope, double base, int scalin
  * out is x, or has no element in common with it (refused as MX_ERR_INVALID_ARG where the strides are the
  * same; with others it is the caller's to see to).
  * Constraints: d_rope even; head strides >= d; interleaved: d, first, all strides (and the
- * addresses, in elements) even, else MX_ERR_UNSUPPORTED; T * heads < 2^31. Every multiple of 4
- * and of 8 elements in all of them makes wider accesses. */
+ * addresses, in elements) even, else MX_ERR_UNSUPPORTED. Accesses are of w elements, the largest power of
+ * two of up to 16 bytes that divides all of them and d_rope (halves: d_rope / 2); T * heads < 2^31 and
+ * T * heads * (d / w + 1) < 2^32 - 256, else MX_ERR_UNSUPPORTED. */
 int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const void* x, long ldx, long ldx_head,
             int x_type, const int64_t* positions, const float* cos_sin, int max_pos, int interleaved, int inverse,
             void* out, long ldo, long ldo_head, void* stream);

@@ -1096,11 +1096,11 @@ int mx_rope(mx_handle* h, int T, int heads, int d, int first, int d_rope, const 
   a.ldo = ldo;
   a.ldo_head = ldo_head;
   a.status = h->d_status;
-  // pairs are moved as two elements at least; chunk numbers are 32-bit
+  // pairs are moved as two elements at least; chunk numbers are 32-bit, those of a last block's idle threads too
   const int vec = mx::rope_vec(a, size);
   if (interleaved && vec < 2) return MX_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(T) * heads >= (int64_t{1} << 31) ||
-      static_cast<int64_t>(T) * heads * (d / vec + 1) >= (int64_t{1} << 32))
+      static_cast<int64_t>(T) * heads * (d / vec + 1) >= (int64_t{1} << 32) - 256)
     return MX_ERR_UNSUPPORTED;
   return cuda_status(mx::launch_rope(a, x_type, static_cast<cudaStream_t>(stream)));
 }
@@ -1146,7 +1146,7 @@ mx::CacheRows cache_rows(const mx_handle* h, const mx_cache* c, int rows, const 
   return a;
 }
 
-// 8-element unit numbers are 32-bit
+// numbers of 16-element units are 32-bit, those of a last block's idle threads too
 bool cache_units_fit(const mx_cache* c, int rows) {
   return static_cast<int64_t>(rows) * c->heads * (c->d / 8) < (int64_t{1} << 31);
 }
