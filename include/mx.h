@@ -554,11 +554,11 @@ size_t mx_attend_bytes(const mx_handle* h, int d, int shared);
  * is 0, its lse -inf. A NaN in the cache reaches the rows that see it.
  * Scores and sums are float32. The weights are rounded to 11 bits, those below 2^-21 of the row's
  * largest to 2^-32 of it. A block of 32 whose scale is below 2^-27 of the largest of its token's
- * keys or values counts as zeros. Where query rows are many (64 and more of a kv head in a sequence, on
- * average; 40 over latents of 512 dimensions) it is the largest of the keys of up to 128 tokens that are
- * taken together, and of the values (of all, where they are the keys) of these and of tokens taken before them:
- * whether a row sees these tokens or not. The order of the sums follows from the shapes, the lengths and the
- * number of SMs: the same bits on every call.
+ * keys or values counts as zeros. Where query rows are many (of a kv head in a sequence, on average,
+ * 64 and more at d <= 256, 40 over latents of 512) it is the largest of the keys of up to 128 tokens that are taken
+ * together, and of the values (of all, where they are the keys) of these and of tokens taken before them:
+ * whether a row sees these tokens or not. The order of the sums follows from the shapes, whether
+ * offsets are given, the lengths and the number of SMs: the same bits on every call.
  * Which kernel runs, and into how many parts the tokens are split, follows from the shapes alone, as lengths and
  * offsets are on the device. Sequences count with the average of the rows, and each is taken to be as long as
  * the table is wide: one that is much wider than the sequences are long costs time.
