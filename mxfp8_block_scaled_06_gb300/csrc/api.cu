@@ -95,7 +95,8 @@ constexpr int kMaxFp4Rows = 1 << 24;
 constexpr int kAttendManyRows = 64;
 // It takes about the same time whatever the rows of a sequence are up to 128 (48 sequences of up to 4096 tokens, d 128,
 // 133 us), where the other's grows with them: 113 us at 48 rows, 146 at 64, 212 at 96 (d 64: 79, 99,
-// 140 against 116; d 256: 159, 206, 301 against 154). 4 such sequences: 27 and 34 us at 64, 37 and 32 at 128.
+// 140 against 116; d 256: 159, 206, 301 against 154). 4 such sequences: 27 and 34 us at 64, 37 and 32 at 128. (One number for
+// all: at d = 64, and for few sequences, it is a little low, at d = 256 high.)
 // Latents of 512 dimensions go to their own kernel from so many rows of a sequence on, where there is
 // work for 3 tiles of 64 rows and 128 tokens or more on each SM: it reads the cache for four times as many rows
 // at once, and takes longer to begin and to end. Few rows against it, 16 heads, us: 48 sequences of

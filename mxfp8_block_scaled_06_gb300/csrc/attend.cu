@@ -41,9 +41,11 @@
 // (sequence, kv head, 8 or 16 rows) that is not all its own goes to a workspace, from which a
 // second kernel adds it up in the order of the tokens.
 //
-// Bound by issue: conversion, scale and products of 256 codes take 6.8 cycles of an SM, whose share of HBM brings
-// that many in 6.2. 61 sequences of up to 16384 tokens, 32 heads on 8 of 128: 160 us, 3.5 TB/s (loads alone 117,
-// all but the loads 143); 48 of up to 32768 latents, 16 heads: 123 us, 1.9 TB/s.
+// Conversion, scale and products of 256 codes take 6.8 cycles of an SM where nothing else runs, and its share of HBM
+// brings that many in 6.2. 61 sequences of up to 16384 tokens, 32 heads on 8 of 128: 160 to 168 us, 3.5 TB/s (loads
+// alone 117, all but the loads 143, conversions and products at that rate 98: the chain from one to the next is
+// not filled by 16 warps, which issue 2.4 instructions a cycle of 4); 48 of up to 32768 latents, 16 heads: 123 to 132 us,
+// 1.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
