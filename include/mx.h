@@ -550,8 +550,8 @@ size_t mx_attend_bytes(const mx_handle* h, int d, int shared);
  *              the GPU need one each
  * Pages, offsets and lengths out of range (lengths above table_cols * page_size) are
  * reported by mx_device_status as MX_ERR_INVALID_ARG; such a sequence's offsets count as
- * no query tokens, its length as the nearest of 0 and the largest. A row that sees nothing
- * is 0, its lse -inf. A NaN in the cache reaches the rows that see it.
+ * no query tokens, its length as the nearest of 0 and the largest. (Offsets that fall leave query tokens that two
+ * other sequences name: the results of such a call say nothing.) A row that sees nothing is 0, its lse -inf. A NaN in the cache reaches the rows that see it.
  * Scores and sums are float32. The weights are rounded to 11 bits, those below 2^-21 of the row's
  * largest to 2^-32 of it. A block of 32 whose scale is below 2^-27 of the largest of its token's
  * keys or values counts as zeros. Where query rows are many (of a kv head in a sequence, on average,
